@@ -1,0 +1,223 @@
+// Entry points of the attention half of the block (see include/moetree.h): argument checks, the
+// attention workspace's layout, and the launches.
+#include <algorithm>
+#include <cmath>
+
+#include "attn.cuh"
+#include "cache.cuh"
+
+namespace moe {
+namespace attn {
+
+static size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// Partial results: slots 0 and 1 of every CTA, for whichever kernel runs.
+WsLayout ws_layout(int dh, long long rows_per_seq) {
+    const size_t simt = (size_t)kMaxCtas * std::min<long long>(kSimtRows, rows_per_seq);
+    WsLayout w{};
+    w.rec = kHeadBytes;
+    w.ml = align256(w.rec + (size_t)kMaxCtas * 8 * sizeof(int));
+    w.o = align256(w.ml + simt * 2 * 2 * sizeof(float));
+    w.total = align256(w.o + simt * 2 * dh * sizeof(float));
+    return w;
+}
+
+}  // namespace attn
+
+namespace {
+
+bool cache_ok(const moe_cache_desc *C) {
+    if (!C || C->H_kv < 1 || C->H < C->H_kv || C->H % C->H_kv || C->H > 65536) return false;
+    if (C->dh < 8 || C->dh % 8 || C->dh > 256) return false;
+    if (C->dtype != MOE_DTYPE_F32 && C->dtype != MOE_DTYPE_BF16) return false;
+    if (C->page_size < 1 || C->n_pages < 1 || C->max_pages < 1) return false;
+    if ((long long)C->page_size * C->max_pages > (1ll << 30)) return false;
+    for (long long st : {C->stride_page, C->stride_tok, C->stride_head})
+        if (st < C->dh || st % 8 || st > (1ll << 36)) return false;
+    if (C->window < 0 || C->sink_tokens < 0) return false;
+    return C->scale > 0.f && std::isfinite(C->scale);
+}
+
+// Rows of a ragged or uniform block. N nodes of G heads each must fit an int.
+bool block_ok(const moe_cache_desc *C, int B, int N, int R, const int *row_start) {
+    if (B < 0 || N < 0 || R < 0) return false;
+    if ((long long)N * (C->H / C->H_kv) > (1ll << 30)) return false;
+    return row_start ? true : (long long)B * N == R;
+}
+
+bool rows_ok(const void *p, long long ld, int width) {
+    return p && aligned16(p) && ld >= width && ld % 8 == 0;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+size_t moe_attention_workspace_bytes(const moe_cache_desc *C, int B, int N) {
+    if (!cache_ok(C) || B < 1 || N < 1) return 0;
+    if ((long long)N * (C->H / C->H_kv) > (1ll << 30)) return 0;
+    return attn::ws_layout(C->dh, (long long)N * (C->H / C->H_kv)).total;
+}
+
+moe_status moe_tree_attention(const moe_cache_desc *C, const void *q, long long ldq,
+                              const void *k_pages, const void *v_pages, const int *page_table,
+                              const int *cache_len, const int *row_start, const int *parent,
+                              const float *sink_logit, int B, int N, int R, void *out, float *lse,
+                              void *workspace, moe_stream_t stream) {
+    if (!cache_ok(C) || !block_ok(C, B, N, R, row_start)) return MOE_ERR_ARG;
+    if (B == 0 || N == 0 || R == 0) return MOE_OK;
+    if (!rows_ok(q, ldq, C->H * C->dh) || !k_pages || !v_pages || !page_table || !cache_len ||
+        !out || !workspace)
+        return MOE_ERR_ARG;
+    if (!aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out) ||
+        ((uintptr_t)workspace & 255u))
+        return MOE_ERR_ARG;
+    attn::Args a{};
+    a.G = C->H / C->H_kv;
+    // (sequence, block of rows) pairs are counted in an int
+    if ((long long)B * (((long long)N * a.G + attn::kSimtRows - 1) / attn::kSimtRows) > (1 << 30))
+        return MOE_ERR_UNSUPPORTED;
+    const attn::WsLayout w = attn::ws_layout(C->dh, (long long)N * a.G);
+    a.q = q;
+    a.ldq = ldq;
+    a.k = k_pages;
+    a.v = v_pages;
+    a.table = page_table;
+    a.cache_len = cache_len;
+    a.row_start = row_start;
+    a.parent = parent;
+    a.sink = sink_logit;
+    a.out = out;
+    a.lse = lse;
+    a.flags = at<int>(workspace, 0);
+    a.rec = at<int>(workspace, w.rec);
+    a.part_ml = at<float>(workspace, w.ml);
+    a.part_o = at<float>(workspace, w.o);
+    a.B = B;
+    a.N = N;
+    a.R = R;
+    a.H = C->H;
+    a.Hkv = C->H_kv;
+    a.dh = C->dh;
+    a.page = C->page_size;
+    a.n_pages = C->n_pages;
+    a.max_pages = C->max_pages;
+    a.cap = C->page_size * C->max_pages;
+    a.st_page = C->stride_page;
+    a.st_tok = C->stride_tok;
+    a.st_head = C->stride_head;
+    a.window = C->window;
+    a.sinks = C->sink_tokens;
+    a.scale = C->scale;
+    return cuda_status(attn::launch_simt(a, C->dtype, (cudaStream_t)stream));
+}
+
+moe_status moe_kv_append(const moe_cache_desc *C, const moe_rope_params *P, const void *q,
+                         long long ldq, const void *k, long long ldk, const void *v, long long ldv,
+                         void *k_pages, void *v_pages, const int *page_table,
+                         const int *cache_len, const int *row_start, const int *depth, int B,
+                         int N, int R, void *q_out, void *workspace, moe_stream_t stream) {
+    if (!cache_ok(C) || !P || !block_ok(C, B, N, R, row_start)) return MOE_ERR_ARG;
+    if (P->inv_freq && (P->rot_dim < 4 || P->rot_dim % 4 || P->rot_dim > C->dh ||
+                        !std::isfinite(P->rope_scale)))
+        return MOE_ERR_ARG;
+    if (!(P->eps >= 0.f) || !std::isfinite(P->eps)) return MOE_ERR_ARG;
+    if (B == 0 || N == 0 || R == 0) return MOE_OK;
+    if (!q != !q_out || (q && (!rows_ok(q, ldq, C->H * C->dh) || !aligned16(q_out))))
+        return MOE_ERR_ARG;
+    if (q && q == q_out && ldq != (long long)C->H * C->dh) return MOE_ERR_ARG;
+    if (!rows_ok(k, ldk, C->H_kv * C->dh) || !rows_ok(v, ldv, C->H_kv * C->dh) || !k_pages ||
+        !v_pages || !aligned16(k_pages) || !aligned16(v_pages) || !page_table || !cache_len)
+        return MOE_ERR_ARG;
+    if (!aligned16(P->q_weight) || !aligned16(P->k_weight) || ((uintptr_t)workspace & 255u))
+        return MOE_ERR_ARG;
+    cache::AppendArgs a{};
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.wq = P->q_weight;
+    a.wk = P->k_weight;
+    a.ldq = ldq;
+    a.ldk = ldk;
+    a.ldv = ldv;
+    a.kp = k_pages;
+    a.vp = v_pages;
+    a.q_out = q_out;
+    a.table = page_table;
+    a.cache_len = cache_len;
+    a.row_start = row_start;
+    a.depth = depth;
+    a.inv_freq = P->inv_freq;
+    a.eps = P->eps;
+    a.rope_scale = P->rope_scale;
+    a.rot = P->inv_freq ? P->rot_dim : 0;
+    a.flags = (int *)workspace;
+    a.B = B;
+    a.N = N;
+    a.R = R;
+    a.H = C->H;
+    a.Hkv = C->H_kv;
+    a.dh = C->dh;
+    a.page = C->page_size;
+    a.n_pages = C->n_pages;
+    a.max_pages = C->max_pages;
+    a.cap = C->page_size * C->max_pages;
+    a.st_page = C->stride_page;
+    a.st_tok = C->stride_tok;
+    a.st_head = C->stride_head;
+    return cuda_status(cache::launch_append(a, C->dtype, (cudaStream_t)stream));
+}
+
+moe_status moe_kv_commit(const moe_cache_desc *C, void *k_pages, void *v_pages,
+                         const int *page_table, const int *cache_len, const int *path,
+                         const int *n_accept, int B, int P, int *new_len, void *workspace,
+                         moe_stream_t stream) {
+    if (!cache_ok(C) || B < 0 || P < 0) return MOE_ERR_ARG;
+    if (B == 0) return MOE_OK;
+    if (!k_pages || !v_pages || !aligned16(k_pages) || !aligned16(v_pages) || !page_table ||
+        !cache_len || (P > 0 && !path) || !n_accept || !new_len || ((uintptr_t)workspace & 255u))
+        return MOE_ERR_ARG;
+    const long long e = (long long)elem_size(C->dtype);
+    cache::CommitArgs a{};
+    a.kp = k_pages;
+    a.vp = v_pages;
+    a.table = page_table;
+    a.cache_len = cache_len;
+    a.path = path;
+    a.n_accept = n_accept;
+    a.new_len = new_len;
+    a.flags = (int *)workspace;
+    a.B = B;
+    a.P = P;
+    a.Hkv = C->H_kv;
+    a.page = C->page_size;
+    a.n_pages = C->n_pages;
+    a.max_pages = C->max_pages;
+    a.cap = C->page_size * C->max_pages;
+    a.row_bytes = (int)(C->dh * e);
+    a.st_page = C->stride_page * e;
+    a.st_tok = C->stride_tok * e;
+    a.st_head = C->stride_head * e;
+    return cuda_status(cache::launch_commit(a, (cudaStream_t)stream));
+}
+
+moe_status moe_block_norm(const moe_layer_desc *L, const void *x, const void *branch,
+                          const void *w_post, const void *gate, int gate_rows, float scale,
+                          const void *w_pre, float eps, int R, void *h, void *hn,
+                          moe_stream_t stream) {
+    if (!desc_ok(L) || R < 0 || !(eps >= 0.f) || !std::isfinite(eps) || !std::isfinite(scale))
+        return MOE_ERR_ARG;
+    if (gate && gate_rows < 1) return MOE_ERR_ARG;
+    if (R == 0) return MOE_OK;
+    if (!x || (branch && !h) || (!h && !hn)) return MOE_ERR_ARG;
+    if ((h && h == hn) || (!branch && (w_post || gate))) return MOE_ERR_ARG;
+    for (const void *p : {x, branch, w_post, gate, w_pre, (const void *)h, (const void *)hn})
+        if (!aligned16(p)) return MOE_ERR_ARG;
+    return cuda_status(launch_block_norm(*L, x, branch, w_post, gate, gate_rows, scale, w_pre, eps,
+                                         R, h, hn, (cudaStream_t)stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,325 @@
+// Shared parts of the paged-attention kernels: arguments, the visibility rule, the division
+// of the work over the CTAs of one launch, and the layout of the partial results.
+//
+// Sequence b has cache_len[b] committed tokens in cache slots 0 .. len - 1 (slot = position)
+// and n new nodes in slots len .. len + n - 1. The query heads of one key/value head share
+// its keys, so the rows of a work item are (node, head in group) pairs: row q of a sequence
+// and key/value head h is node q / G, query head h G + q % G.
+//
+// The work of a launch is a list of items, one per (sequence, block of rows, key/value head),
+// each a number of key tiles. All tiles of all items, in this order, are divided into equal
+// ranges, one per CTA, whatever items they belong to: lengths that differ between the
+// sequences of a batch, causal chunks and single long sequences all keep every SM busy to the
+// end. An item inside one range is finished by its CTA; an item that a range boundary cuts
+// leaves unnormalised partial results (O, running maximum, sum) that attn_combine merges.
+// The lengths live in device memory, so every CTA finds its range by itself (attn_plan) and
+// the launch has the same shape whatever they are (it can be captured into a graph).
+#pragma once
+
+#include "common.cuh"
+
+namespace moe {
+namespace attn {
+
+constexpr int kMaxCtas = 640;         // CTAs of an attention launch at most
+constexpr size_t kHeadBytes = 4096;   // head of the workspace: the check word (zeroed by the caller)
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Bits of the check word, beside those of the layer calls.
+enum : int { FLAG_BAD_PAGE = 4, FLAG_BAD_SEQUENCE = 8 };
+
+struct Args {
+    const void *q;
+    long long ldq;
+    const void *k, *v;
+    const int *table, *cache_len, *row_start, *parent;
+    const float *sink;
+    void *out;
+    float *lse;
+    int *flags;      // check word
+    int *rec;        // [kMaxCtas][8]: the item a CTA's range begins inside (see attn_combine)
+    float *part_o;   // [CTAs][2][prows][dh]
+    float *part_ml;  // [CTAs][2][prows][2]
+    int B, N, R, H, Hkv, G, dh;
+    int page, n_pages, max_pages, cap;  // cap: cache slots of a sequence (max_pages * page)
+    long long st_page, st_tok, st_head;
+    int window, sinks;
+    float scale;
+    int rows;        // rows of an item (of the launched kernel)
+    int prows;       // rows of a partial result: min(rows, N G)
+    int qblocks;     // blocks of `rows` rows that N nodes take
+    int min_tiles;   // tiles of a CTA's range at least
+};
+
+struct Seq {
+    int len, n, row0;  // committed tokens, new nodes, first row of q
+    int L;             // cache slots in use: len + n, at most cap
+};
+
+// Sizes that contradict one another are cut to what the buffers hold.
+__device__ __forceinline__ Seq sequence(const Args &a, int b, int *bad = nullptr) {
+    Seq s;
+    int n, r0;
+    if (a.row_start) {
+        r0 = a.row_start[b];
+        n = a.row_start[b + 1] - r0;
+        if (r0 < 0 || n < 0 || n > a.N || r0 > a.R - n) {
+            if (bad) *bad = 1;
+            n = r0 < 0 ? 0 : min(min(n, a.N), a.R - r0);
+            if (n < 0) n = 0;
+        }
+    } else {
+        r0 = b * a.N;
+        n = a.N;
+    }
+    int len = a.cache_len[b];
+    if (len < 0 || len > a.cap - n) {
+        if (bad) *bad = 1;
+        len = max(0, min(len, a.cap));
+    }
+    s.len = len;
+    s.n = n;
+    s.row0 = r0;
+    s.L = min(len + n, a.cap);
+    return s;
+}
+
+// The key tiles of rows [q0, q1) (q1 > q0) of a sequence: ns tiles from slot 0 (first tokens that
+// stay visible), then the tiles from w0 on; nt in all.
+struct Tiles {
+    int ns, w0, nt;
+    __device__ __forceinline__ int at(int t) const { return t < ns ? t : w0 + (t - ns); }
+};
+template <int BN>
+__device__ __forceinline__ Tiles tiles_of(const Args &a, const Seq &s, int q0, int q1) {
+    const int i0 = q0 / a.G, i1 = (q1 - 1) / a.G;
+    const int kend = a.parent ? s.L : min(s.L, s.len + i1 + 1);
+    Tiles t;
+    t.ns = t.w0 = 0;
+    const int all = (kend + BN - 1) / BN;
+    if (a.window > 0) {
+        // the oldest slot a window can reach (tree nodes may all be at the root's depth)
+        const int lo = max(0, s.len + (a.parent ? 0 : i0) - a.window + 1);
+        t.w0 = min(lo / BN, all);
+        t.ns = min((int)(((long long)a.sinks + BN - 1) / BN), t.w0);
+    }
+    t.nt = t.ns + all - t.w0;
+    return t;
+}
+
+template <int BN>
+__device__ __forceinline__ int entry_tiles(const Args &a, int e, int *bad = nullptr) {
+    const int b = e / a.qblocks, q0 = (e - b * a.qblocks) * a.rows;
+    const Seq s = sequence(a, b, bad);
+    const int rows = s.n * a.G;
+    if (q0 >= rows) return 0;
+    return tiles_of<BN>(a, s, q0, min(rows, q0 + a.rows)).nt;
+}
+
+// A CTA's range of tiles: `left` tiles from tile t of the item (entry e, key/value head h),
+// where entry e = sequence * qblocks + block of rows.
+struct Range {
+    long long quota;
+    int e, h, t;
+    long long left;
+};
+
+// Finds the CTA's range (block-wide; every thread gets it). scratch: 34 long longs of shared
+// memory. Each thread sums a run of entries, a block scan places the runs, and the thread
+// whose run holds the range's first tile looks it up.
+template <int BN, int kThreads>
+__device__ __forceinline__ Range attn_plan(const Args &a, int cta, int n_ctas, long long *scratch) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int kWarps = kThreads / 32;
+    static_assert(kWarps <= 28, "scratch holds a sum per warp and the result");
+    const int E = a.B * a.qblocks;
+    const int per = (E + kThreads - 1) / kThreads;
+    const int e0 = min(E, tid * per), e1 = min(E, e0 + per);
+    long long sum = 0;
+    int bad = 0;
+    for (int e = e0; e < e1; ++e) sum += (long long)a.Hkv * entry_tiles<BN>(a, e, &bad);
+    if (bad) atomicOr(a.flags, FLAG_BAD_SEQUENCE);
+    long long inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+    }
+    if (lane == 31) scratch[warp] = inc;
+    __syncthreads();
+    long long before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += scratch[w];
+        total += scratch[w];
+    }
+    Range r;
+    r.quota = max((long long)a.min_tiles, (total + n_ctas - 1) / n_ctas);
+    const long long start = r.quota * cta;
+    r.left = max(0ll, min(r.quota, total - start));
+    long long at = before + inc - sum;  // first tile of this thread's run
+    int *found = reinterpret_cast<int *>(scratch + 28);
+    if (r.left > 0 && start >= at && start < at + sum) {
+        for (int e = e0; e < e1; ++e) {
+            const int nt = entry_tiles<BN>(a, e);
+            const long long w = (long long)a.Hkv * nt;
+            if (start < at + w) {
+                const long long off = start - at;
+                found[0] = e;
+                found[1] = (int)(off / nt);
+                found[2] = (int)(off % nt);
+                break;
+            }
+            at += w;
+        }
+    }
+    __syncthreads();
+    r.e = found[0];
+    r.h = found[1];
+    r.t = found[2];
+    return r;
+}
+
+// One piece of an item: its tiles t .. t + count - 1 of nt.
+struct Segment {
+    Seq s;
+    Tiles tl;
+    int b, h, q0, rows;  // rows [q0, q0 + rows) of the sequence
+    int t, count;
+    bool whole;
+};
+
+// The next segment of a range; r.left > 0. Moves the range past it.
+template <int BN>
+__device__ __forceinline__ Segment next_segment(const Args &a, Range &r) {
+    Segment g;
+    for (;;) {
+        g.b = r.e / a.qblocks;
+        g.q0 = (r.e - g.b * a.qblocks) * a.rows;
+        g.s = sequence(a, g.b);
+        g.rows = min(a.rows, g.s.n * a.G - g.q0);
+        if (g.rows > 0) {
+            g.tl = tiles_of<BN>(a, g.s, g.q0, g.q0 + g.rows);
+            if (g.tl.nt > 0) break;
+        }
+        ++r.e;
+        r.h = r.t = 0;
+    }
+    g.h = r.h;
+    g.t = r.t;
+    g.count = (int)min((long long)(g.tl.nt - r.t), r.left);
+    g.whole = g.t == 0 && g.count == g.tl.nt;
+    r.left -= g.count;
+    r.t = 0;
+    if (g.t + g.count == g.tl.nt && ++r.h == a.Hkv) {
+        r.h = 0;
+        ++r.e;
+    }
+    return g;
+}
+
+// A cut item leaves its partial result in slot 0 of a CTA whose range begins inside it and in
+// slot 1 of the CTA whose range holds its first tile.
+__device__ __forceinline__ size_t part_row(const Args &a, int cta, const Segment &g, int row) {
+    return ((size_t)cta * 2 + (g.t == 0 ? 1 : 0)) * a.prows + row;
+}
+
+// Record for attn_combine: the item in which this CTA's range begins, if not at its start.
+template <int BN>
+__device__ __forceinline__ void write_record(const Args &a, int cta, const Range &r) {
+    int *rec = a.rec + cta * 8;
+    const bool inside = r.left > 0 && r.t > 0;
+    rec[0] = inside ? r.e : -1;
+    if (!inside) return;
+    rec[1] = r.h;
+    rec[2] = r.t;
+    rec[3] = entry_tiles<BN>(a, r.e);
+    reinterpret_cast<long long *>(rec)[2] = r.quota;
+}
+
+// Bits of visible slots among [k0, k0 + 32) for the query node `node`, at position pos.
+// Chains: slots up to the node's own, in the window or among the first tokens. Trees: the
+// committed slots and the node's ancestors, found by walking up its parents (each step goes to
+// a lower node: a parent outside [0, node) is the top).
+__device__ __forceinline__ uint32_t range_bits(int lo, int hi, int k0) {  // slots [lo, hi)
+    const int x0 = max(lo - k0, 0), x1 = min(hi - k0, 32);
+    if (x1 <= x0) return 0u;
+    return (x1 == 32 ? 0xffffffffu : (1u << x1) - 1u) & ~((1u << x0) - 1u);
+}
+template <int WORDS>
+__device__ __forceinline__ void visible_bits(const Args &a, const Seq &s, int node, int pos, int k0,
+                                             uint32_t (&bits)[WORDS]) {
+    const int hi = a.parent ? min(s.len, s.L) : min(pos + 1, s.L);
+    const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+#pragma unroll
+    for (int w = 0; w < WORDS; ++w) {
+        const int kw = k0 + 32 * w;
+        bits[w] = range_bits(lo, hi, kw);
+        if (a.window > 0) bits[w] |= range_bits(0, min(a.sinks, hi), kw);
+    }
+    if (a.parent && k0 + 32 * WORDS > s.len) {
+        int p = pos;
+        for (int m = node; m >= 0 && s.len + m >= k0; --p) {
+            const int j = s.len + m - k0;
+            const bool in = a.window <= 0 || pos - p < a.window || p < a.sinks;
+            if (in && j < 32 * WORDS && s.len + m < s.L) {
+#pragma unroll
+                for (int w = 0; w < WORDS; ++w)
+                    if ((j >> 5) == w) bits[w] |= 1u << (j & 31);
+            }
+            const int up = a.parent[s.row0 + m];
+            m = up < m ? up : -1;
+        }
+    }
+}
+
+// A node's position: its depth in the tree is only needed (and only walked) for a window.
+__device__ __forceinline__ int node_position(const Args &a, const Seq &s, int node) {
+    if (!a.parent) return s.len + node;
+    int d = 0;
+    if (a.window > 0) {
+        for (int m = node;; ++d) {
+            const int up = a.parent[s.row0 + m];
+            if (up < 0 || up >= m) break;
+            m = up;
+        }
+    }
+    return s.len + d;
+}
+
+// Factor that normalises an accumulated O, and the log of the denominator, from the running
+// maximum m (base-2 logits) and sum l, with the head's sink logit (natural log units).
+__device__ __forceinline__ float finish(float m, float l, const float *sink, int head, float *lse) {
+    float mm = l > 0.f ? m : -INFINITY;
+    float den = l;
+    float f = 1.f;
+    if (sink) {
+        const float s2 = sink[head] * kLog2e;
+        const float top = fmaxf(mm, s2);
+        if (top > -INFINITY) {
+            f = l > 0.f ? exp2f(mm - top) : 0.f;
+            den = l * f + exp2f(s2 - top);
+            mm = top;
+        }
+    }
+    *lse = den > 0.f ? (mm + log2f(den)) * 0.6931471805599453f : (den == den ? -INFINITY : den);
+    return den == 0.f ? 0.f : f / den;
+}
+
+template <typename T> __device__ __forceinline__ T from_float(float v);
+template <> __device__ __forceinline__ float from_float<float>(float v) { return v; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) {
+    return __float2bfloat16_rn(v);
+}
+
+cudaError_t launch_simt(Args a, int dtype, cudaStream_t s);
+cudaError_t launch_combine(const Args &a, int dtype, int n_ctas, cudaStream_t s);
+constexpr int kSimtRows = 32;  // rows of an item
+
+struct WsLayout {
+    size_t rec, ml, o, total;
+};
+WsLayout ws_layout(int dh, long long rows_per_seq);  // rows_per_seq = N G
+
+}  // namespace attn
+}  // namespace moe

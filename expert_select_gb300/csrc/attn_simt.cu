@@ -1,0 +1,344 @@
+// Paged attention on the CUDA cores, for every type and head size: fp32, and bf16 head sizes
+// that the tensor-core kernel does not take. Also the merge of cut items.
+//
+//   out[n, h] = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q.k_j - max)  over visible slots j
+//
+// computed in one pass over the keys with a running maximum and sum. An item is 32 rows
+// (node, head in group) of one key/value head; a CTA of 128 threads takes a tile of 32 keys at a
+// time: K and V rows go through the page table into shared memory as fp32, each thread forms 4
+// rows x 2 keys of the scores, 16 lanes share a row's maximum and sum, and each thread
+// accumulates 4 rows x dh / 16 columns of O in registers.
+#include <algorithm>
+
+#include "attn.cuh"
+
+namespace moe {
+namespace attn {
+namespace {
+
+constexpr int kBN = 32;
+constexpr int kThr = 128;
+
+// NC: 64-column chunks of the head size (dh <= 64 NC).
+template <int NC> constexpr int simt_smem() {
+    // Q and K rows padded by 4 floats (the 8 lanes of a 16-byte phase read different banks)
+    return (32 * (64 * NC + 4) * 2 + 32 * 64 * NC + 32 * 36) * 4;
+}
+
+template <typename T>
+__device__ __forceinline__ void load_row(float *dst, const T *src, int col, bool ok) {
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (ok) Vec8<T>::load(src + col, v);
+    *reinterpret_cast<float4 *>(dst + col) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4 *>(dst + col + 4) = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+template <typename T, int NC>
+__global__ void __launch_bounds__(kThr) attn_simt_kernel(const Args a) {
+    extern __shared__ float sm[];
+    __shared__ long long scratch[34];
+    constexpr int D = 64 * NC, LD = D + 4;
+    float *sQ = sm, *sK = sQ + 32 * LD, *sV = sK + 32 * LD, *sP = sV + 32 * D;  // sP [key][36]
+    const int tid = threadIdx.x, tr = tid >> 4, tk = tid & 15;
+    pdl_wait();
+    Range r = attn_plan<kBN, kThr>(a, blockIdx.x, gridDim.x, scratch);
+    if (tid == 0) write_record<kBN>(a, blockIdx.x, r);
+    const T *q = (const T *)a.q, *kp = (const T *)a.k, *vp = (const T *)a.v;
+    while (r.left > 0) {
+        const Segment g = next_segment<kBN>(a, r);
+        __syncthreads();
+        // query rows, scaled so that scores are base-2 logits
+        for (int i = tid; i < 32 * (D / 8); i += kThr) {
+            const int row = i / (D / 8), col = (i % (D / 8)) * 8;
+            const int qr = g.q0 + row;
+            const bool ok = row < g.rows && col < a.dh;
+            const int node = qr / a.G;
+            const T *src = q + (size_t)(g.s.row0 + (ok ? node : 0)) * a.ldq +
+                           (size_t)(g.h * a.G + (ok ? qr - node * a.G : 0)) * a.dh;
+            load_row<T>(sQ + row * LD, src, col, ok);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) sQ[row * LD + col + c] *= a.scale * kLog2e;
+        }
+        float m[4], l[4], acc[4][NC][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            m[i] = -INFINITY;
+            l[i] = 0.f;
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) acc[i][c][x] = 0.f;
+        }
+        // the half-warp's four rows: lanes 0-3 of it look up their visible bits
+        const int vrow = tr * 4 + (tk & 3);
+        const bool vok = vrow < g.rows;
+        const int vnode = (g.q0 + (vok ? vrow : 0)) / a.G;
+        const int vpos = node_position(a, g.s, vnode);
+        for (int t = g.t; t < g.t + g.count; ++t) {
+            const int k0 = g.tl.at(t) * kBN;
+            __syncthreads();
+            int bad = 0;
+            for (int i = tid; i < 32 * (D / 8); i += kThr) {
+                const int key = i / (D / 8), col = (i % (D / 8)) * 8;
+                const int j = k0 + key;
+                bool ok = j < g.s.L && col < a.dh;
+                size_t off = 0;
+                if (ok) {
+                    const int pi = j / a.page, pg = a.table[(size_t)g.b * a.max_pages + pi];
+                    if (pg < 0 || pg >= a.n_pages) {
+                        ok = false;
+                        bad = 1;
+                    } else {
+                        off = (size_t)pg * a.st_page + (size_t)(j - pi * a.page) * a.st_tok +
+                              (size_t)g.h * a.st_head;
+                    }
+                }
+                load_row<T>(sK + key * LD, kp + off, col, ok);
+                load_row<T>(sV + key * D, vp + off, col, ok);
+            }
+            if (bad) atomicOr(a.flags, FLAG_BAD_PAGE);
+            // slots of a page outside the pool are not visible
+            uint32_t pages_ok = 0xffffffffu;
+            {
+                const int j = k0 + (tid & 31);
+                bool ok = true;
+                if (j < g.s.L) {
+                    const int pg = a.table[(size_t)g.b * a.max_pages + j / a.page];
+                    ok = pg >= 0 && pg < a.n_pages;
+                }
+                pages_ok = __ballot_sync(0xffffffffu, ok);
+            }
+            uint32_t bits[1] = {0u};
+            if (vok) visible_bits<1>(a, g.s, vnode, vpos, k0, bits);
+            bits[0] &= pages_ok;
+            __syncthreads();
+            float s[4][2];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[i][0] = s[i][1] = 0.f;
+#pragma unroll 4
+            for (int c = 0; c < D; c += 4) {
+                const float4 ka = *reinterpret_cast<const float4 *>(sK + tk * LD + c);
+                const float4 kb = *reinterpret_cast<const float4 *>(sK + (tk + 16) * LD + c);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float4 qv = *reinterpret_cast<const float4 *>(sQ + (tr * 4 + i) * LD + c);
+                    s[i][0] += qv.x * ka.x + qv.y * ka.y + qv.z * ka.z + qv.w * ka.w;
+                    s[i][1] += qv.x * kb.x + qv.y * kb.y + qv.z * kb.z + qv.w * kb.w;
+                }
+            }
+            float p[4][2];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t vb = __shfl_sync(0xffffffffu, bits[0], (tid & 16) + i);
+                const bool on0 = (vb >> tk) & 1u, on1 = (vb >> (tk + 16)) & 1u;
+                const float s0 = on0 ? s[i][0] : -INFINITY, s1 = on1 ? s[i][1] : -INFINITY;
+                float mx = fmaxf(s0, s1);
+#pragma unroll
+                for (int o = 8; o >= 1; o >>= 1)
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                const float mn = fmaxf(m[i], mx);
+                const float base = mn == -INFINITY ? 0.f : mn;
+                const float f = exp2f(m[i] - base);
+                p[i][0] = on0 ? exp2f(s0 - base) : 0.f;
+                p[i][1] = on1 ? exp2f(s1 - base) : 0.f;
+                float sum = p[i][0] + p[i][1];
+#pragma unroll
+                for (int o = 8; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                l[i] = l[i] * f + sum;
+                m[i] = mn;
+                if (f != 1.f) {
+#pragma unroll
+                    for (int c = 0; c < NC; ++c)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) acc[i][c][x] *= f;
+                }
+            }
+            // P goes to the 16 lanes of its rows (one warp) through shared memory, key-major
+            *reinterpret_cast<float4 *>(sP + tk * 36 + tr * 4) =
+                make_float4(p[0][0], p[1][0], p[2][0], p[3][0]);
+            *reinterpret_cast<float4 *>(sP + (tk + 16) * 36 + tr * 4) =
+                make_float4(p[0][1], p[1][1], p[2][1], p[3][1]);
+            __syncwarp();
+#pragma unroll 2
+            for (int key = 0; key < kBN; ++key) {
+                const float4 pv = *reinterpret_cast<const float4 *>(sP + key * 36 + tr * 4);
+                const float pr[4] = {pv.x, pv.y, pv.z, pv.w};
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    const float4 v =
+                        *reinterpret_cast<const float4 *>(sV + key * D + c * 64 + tk * 4);
+                    // a slot that the row does not see (p = 0) takes no part, whatever it holds
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (pr[i] != 0.f) {
+                            acc[i][c][0] += pr[i] * v.x;
+                            acc[i][c][1] += pr[i] * v.y;
+                            acc[i][c][2] += pr[i] * v.z;
+                            acc[i][c][3] += pr[i] * v.w;
+                        }
+                }
+            }
+            __syncwarp();
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = tr * 4 + i;
+            if (row >= g.rows) continue;
+            if (g.whole) {
+                const int qr = g.q0 + row, node = qr / a.G, head = g.h * a.G + (qr - node * a.G);
+                const size_t orow = (size_t)(g.s.row0 + node) * a.H + head;
+                float lse;
+                const float f = finish(m[i], l[i], a.sink, head, &lse);
+                T *o = (T *)a.out + orow * a.dh;
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    const int col = c * 64 + tk * 4;
+                    if (col < a.dh) {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) o[col + x] = from_float<T>(acc[i][c][x] * f);
+                    }
+                }
+                if (a.lse && tk == 0) a.lse[orow] = lse;
+            } else {
+                const size_t pr = part_row(a, blockIdx.x, g, row);
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    const int col = c * 64 + tk * 4;
+                    if (col < a.dh)
+                        *reinterpret_cast<float4 *>(a.part_o + pr * a.dh + col) =
+                            make_float4(acc[i][c][0], acc[i][c][1], acc[i][c][2], acc[i][c][3]);
+                }
+                if (tk == 0) {
+                    a.part_ml[pr * 2] = m[i];
+                    a.part_ml[pr * 2 + 1] = l[i];
+                }
+            }
+        }
+    }
+}
+
+// Merges a cut item: block (c, y) looks at the item inside which CTA c's range begins. The
+// item's first tiles are in slot 1 of the CTA before, the rest in slot 0 of CTAs c, c + 1, ...;
+// the block of the first such c does the item's rows 8 y .. 8 y + 7, a warp per row, the parts in
+// CTA order: sum_i 2^(m_i - M) O_i over sum_i 2^(m_i - M) l_i, M the largest m_i. Lane i reads part
+// i's maximum and sum; the parts' O rows are read 4 columns a lane.
+template <typename T>
+__global__ void __launch_bounds__(256) attn_combine_kernel(const Args a, int n_ctas) {
+    pdl_wait();
+    const int c = blockIdx.x;
+    const int *rec = a.rec + c * 8;
+    const int e = rec[0];
+    if (c == 0 || e < 0) return;
+    const int h = rec[1], t0 = rec[2], nt = rec[3];
+    const long long quota = reinterpret_cast<const long long *>(rec)[2];
+    if (t0 > quota) return;  // an earlier CTA's range begins inside the item too
+    const int lane = threadIdx.x & 31;
+    const int b = e / a.qblocks, q0 = (e - b * a.qblocks) * a.rows;
+    const Seq s = sequence(a, b);
+    const int row = blockIdx.y * 8 + (threadIdx.x >> 5);
+    if (row >= min(a.rows, s.n * a.G - q0)) return;
+    // parts: CTA c - 1 (t0 tiles), then as many as the remaining tiles take
+    const int parts = 1 + (int)((nt - t0 + quota - 1) / quota);
+    float M = -INFINITY;
+    for (int i = lane; i < parts; i += 32) {
+        const size_t pr = ((size_t)(c - 1 + i) * 2 + (i == 0)) * a.prows + row;
+        if (a.part_ml[pr * 2 + 1] > 0.f || a.part_ml[pr * 2 + 1] != a.part_ml[pr * 2 + 1])
+            M = fmaxf(M, a.part_ml[pr * 2]);
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float base = M == -INFINITY ? 0.f : M;
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};  // columns 4 lane + 128 c (dh <= 256)
+    float l = 0.f;
+    for (int i0 = 0; i0 < parts; i0 += 32) {
+        float w = 0.f;
+        if (i0 + lane < parts) {
+            const int i = i0 + lane;
+            const size_t pr = ((size_t)(c - 1 + i) * 2 + (i == 0)) * a.prows + row;
+            const float li = a.part_ml[pr * 2 + 1];
+            w = li == 0.f ? 0.f : exp2f(a.part_ml[pr * 2] - base);
+            l += w * li;
+        }
+        const int ni = min(32, parts - i0);
+#pragma unroll 4
+        for (int i = 0; i < ni; ++i) {
+            const float wi = __shfl_sync(0xffffffffu, w, i);
+            const size_t pr = ((size_t)(c - 1 + i0 + i) * 2 + (i0 + i == 0)) * a.prows + row;
+#pragma unroll
+            for (int cc = 0; cc < 2; ++cc) {
+                const int col = cc * 128 + lane * 4;
+                if (col < a.dh && wi != 0.f) {
+                    const float4 v = *reinterpret_cast<const float4 *>(a.part_o + pr * a.dh + col);
+                    acc[cc * 4] += wi * v.x;
+                    acc[cc * 4 + 1] += wi * v.y;
+                    acc[cc * 4 + 2] += wi * v.z;
+                    acc[cc * 4 + 3] += wi * v.w;
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    const int qr = q0 + row, node = qr / a.G, head = h * a.G + (qr - node * a.G);
+    const size_t orow = (size_t)(s.row0 + node) * a.H + head;
+    float lse;
+    const float f = finish(base, l, a.sink, head, &lse);
+    T *out = (T *)a.out + orow * a.dh;
+#pragma unroll
+    for (int cc = 0; cc < 2; ++cc) {
+        const int col = cc * 128 + lane * 4;
+        if (col < a.dh) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) out[col + x] = from_float<T>(acc[cc * 4 + x] * f);
+        }
+    }
+    if (a.lse && lane == 0) a.lse[orow] = lse;
+}
+
+template <typename T, int NC>
+cudaError_t launch_nc(const Args &a, int nsm, int *ctas, cudaStream_t s) {
+    constexpr int smem = simt_smem<NC>();
+    const cudaError_t err = cudaFuncSetAttribute(
+        attn_simt_kernel<T, NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (err != cudaSuccess) return err;
+    // CTAs per SM that shared memory (228 KB, 1 KB of it per CTA) allows, at most four
+    *ctas = std::min(kMaxCtas, nsm * std::max(1, std::min(4, (228 * 1024) / (smem + 2048))));
+    return launch_pdl(attn_simt_kernel<T, NC>, dim3(*ctas), dim3(kThr), smem, s, a);
+}
+
+template <typename T> cudaError_t launch_t(const Args &a, int nsm, int *ctas, cudaStream_t s) {
+    switch ((a.dh + 63) / 64) {
+        case 1: return launch_nc<T, 1>(a, nsm, ctas, s);
+        case 2: return launch_nc<T, 2>(a, nsm, ctas, s);
+        case 3: return launch_nc<T, 3>(a, nsm, ctas, s);
+        default: return launch_nc<T, 4>(a, nsm, ctas, s);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_combine(const Args &a, int dtype, int n_ctas, cudaStream_t s) {
+    const dim3 grid(n_ctas, (a.prows + 7) / 8);
+    if (dtype == MOE_DTYPE_BF16)
+        return launch_pdl(attn_combine_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, a, n_ctas);
+    return launch_pdl(attn_combine_kernel<float>, grid, dim3(256), 0, s, a, n_ctas);
+}
+
+cudaError_t launch_simt(Args a, int dtype, cudaStream_t s) {
+    int dev = 0, nsm = 0, ctas = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err == cudaSuccess)
+        err = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
+    if (err != cudaSuccess) return err;
+    a.rows = kSimtRows;
+    a.qblocks = (int)(((long long)a.N * a.G + kSimtRows - 1) / kSimtRows);
+    a.prows = (int)std::min<long long>(a.rows, (long long)a.N * a.G);
+    a.min_tiles = 4;
+    err = dtype == MOE_DTYPE_BF16 ? launch_t<__nv_bfloat16>(a, nsm, &ctas, s)
+                                  : launch_t<float>(a, nsm, &ctas, s);
+    if (err != cudaSuccess) return err;
+    return launch_combine(a, dtype, ctas, s);
+}
+
+}  // namespace attn
+}  // namespace moe

@@ -153,6 +153,10 @@ cudaError_t launch_publish(int E, const int *slot_host, const uint8_t *res_host,
 constexpr double kNormEps = 1e-6;
 cudaError_t launch_rmsnorm(const moe_layer_desc &L, const void *x, int R, void *xn,
                            cudaStream_t s);
+cudaError_t launch_block_norm(const moe_layer_desc &L, const void *x, const void *branch,
+                              const void *w_post, const void *gate, int gate_rows, float scale,
+                              const void *w_pre, float eps, int R, void *h, void *hn,
+                              cudaStream_t s);
 
 // ---- host helpers shared by the entry points (api.cu, offload.cu) ----
 // Timing events of the offloaded layer's upload waits, kept in the residency table.

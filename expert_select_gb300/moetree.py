@@ -34,7 +34,8 @@ EXPORTS = (
     "moe_residency_query", "moe_residency_plan", "moe_residency_publish", "moe_expert_upload",
     "moe_event_wait", "moe_tree_forward_noalloc", "moe_offload_forward", "moe_draft_select",
     "moe_tree_route", "moe_tree_block_stats", "moe_noalloc_check", "moe_offload_upload_wait",
-    "moe_rms_norm",
+    "moe_rms_norm", "moe_attention_workspace_bytes", "moe_tree_attention", "moe_kv_append",
+    "moe_kv_commit", "moe_block_norm",
 )
 
 
@@ -81,6 +82,19 @@ class RunOpts(C.Structure):
                 ("ffn_max_ctas", C.c_int)]
 
 
+class CacheDesc(C.Structure):
+    _fields_ = [("H", C.c_int), ("H_kv", C.c_int), ("dh", C.c_int), ("dtype", C.c_int),
+                ("page_size", C.c_int), ("n_pages", C.c_int), ("max_pages", C.c_int),
+                ("stride_page", C.c_longlong), ("stride_tok", C.c_longlong),
+                ("stride_head", C.c_longlong), ("window", C.c_int), ("sink_tokens", C.c_int),
+                ("scale", C.c_float)]
+
+
+class RopeParams(C.Structure):
+    _fields_ = [("q_weight", C.c_void_p), ("k_weight", C.c_void_p), ("eps", C.c_float),
+                ("inv_freq", C.c_void_p), ("rot_dim", C.c_int), ("rope_scale", C.c_float)]
+
+
 _lib = None
 
 
@@ -118,6 +132,13 @@ def lib() -> C.CDLL:
             "moe_tree_block_stats": ([P, I, I, P, P, P, P, P], I),
             "moe_noalloc_check": ([P, P], I),
             "moe_offload_upload_wait": ([P, I, C.c_double, P, P], I),
+            "moe_attention_workspace_bytes": ([P, I, I], S),
+            "moe_tree_attention": ([P, P, C.c_longlong, P, P, P, P, P, P, P, I, I, I, P, P, P, P],
+                                   I),
+            "moe_kv_append": ([P, P, P, C.c_longlong, P, C.c_longlong, P, C.c_longlong, P, P, P, P,
+                               P, P, I, I, I, P, P, P], I),
+            "moe_kv_commit": ([P, P, P, P, P, P, P, I, I, P, P, P], I),
+            "moe_block_norm": ([P, P, P, P, P, I, C.c_float, P, C.c_float, I, P, P, P], I),
         }
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
@@ -373,6 +394,181 @@ def moe_draft_select(L, parent, depth, logp, footprint, lam: float, gamma: int, 
         C.byref(L), parent.shape[0], _ptr(parent), _ptr(depth), _ptr(logp), _ptr(footprint),
         float(lam), gamma, _ptr(x), _ptr(selected), _ptr(sel_parent), _ptr(sel_depth),
         _ptr(x_sel), _ptr(n_union), _stream(stream)))
+
+
+# ------------------------------------------------------------- attention half of the block
+
+_CODE = {torch.float32: MOE_DTYPE_F32, torch.bfloat16: MOE_DTYPE_BF16}
+
+
+def _expect(fn: str, name: str, t: Optional[torch.Tensor], dtype=None, shape=None, device=None,
+            dense=True):
+    """Refuses a tensor that the entry point would read or write wrongly: another type, shape,
+    device or layout than its pointer is taken for."""
+    if t is None:
+        return
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{fn}: {name} is {t.dtype}, expected {dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{fn}: {name} is on {t.device}, expected {device}")
+    if dense and not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} must be contiguous")
+
+
+def _rows(fn: str, name: str, t: torch.Tensor, dtype, shape, device) -> int:
+    """A [rows, heads, dh] tensor whose rows may be a part of wider ones; its row stride."""
+    _expect(fn, name, t, dtype, shape, device, dense=False)
+    if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2])):
+        raise ValueError(f"{fn}: the heads of {name}'s rows must lie side by side")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * t.shape[2])
+
+
+class _on:
+    """Makes a tensor's device the current one for a call, and gives the stream to use."""
+
+    def __init__(self, t: torch.Tensor, stream):
+        self.index, self.stream = t.device.index, stream
+
+    def __enter__(self):
+        self.before = torch.cuda.current_device()
+        if self.before != self.index:
+            torch.cuda.set_device(self.index)
+        return _stream(self.stream)
+
+    def __exit__(self, *exc):
+        if self.before != self.index:
+            torch.cuda.set_device(self.before)
+        return False
+
+
+def cache_desc(pages: torch.Tensor, H: int, max_pages: int, window: int = 0, sink_tokens: int = 0,
+               scale: Optional[float] = None) -> CacheDesc:
+    """The cache of one layer whose K pool is `pages`, [n_pages, page_size, H_kv, dh] or a view
+    with those dimensions (a head-major pool is one, permuted); the V pool has the same shape
+    and strides. H: query heads; max_pages: entries of a page-table row; window, sink_tokens:
+    see moe_cache_desc; scale: of q.k, 1 / sqrt(dh) if not given."""
+    n, page, h_kv, dh = pages.shape
+    if pages.dtype not in _CODE:
+        raise ValueError(f"cache_desc: pages are {pages.dtype}, expected float32 or bfloat16")
+    if dh > 1 and pages.stride(3) != 1:
+        raise ValueError("cache_desc: a head's elements must lie side by side")
+    st = [pages.stride(i) if pages.shape[i] > 1 else max(pages.stride(i), dh) for i in range(3)]
+    st = [v if pages.shape[i] > 1 else (v + 7) // 8 * 8 for i, v in enumerate(st)]
+    return CacheDesc(H, h_kv, dh, _CODE[pages.dtype], page, n, max_pages, *st, window, sink_tokens,
+                     dh ** -0.5 if scale is None else scale)
+
+
+def _expect_pools(fn, C_, k_pages, v_pages, page_table, cache_len, B, row_start, R):
+    dev = k_pages.device
+    dt = torch.bfloat16 if C_.dtype == MOE_DTYPE_BF16 else torch.float32
+    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        _expect(fn, name, t, dt, (C_.n_pages, C_.page_size, C_.H_kv, C_.dh), dev, dense=False)
+        want = (C_.stride_page, C_.stride_tok, C_.stride_head, 1)
+        if any(t.shape[i] > 1 and t.stride(i) != want[i] for i in range(4)):
+            raise ValueError(f"{fn}: {name} has other strides than the cache description")
+    _expect(fn, "page_table", page_table, torch.int32, (B, C_.max_pages), dev)
+    _expect(fn, "cache_len", cache_len, torch.int32, (B,), dev)
+    _expect(fn, "row_start", row_start, torch.int32, (B + 1,), dev)
+    return dev, dt
+
+
+def moe_attention_workspace_bytes(C_: CacheDesc, B: int, N: int) -> int:
+    return int(lib().moe_attention_workspace_bytes(C.byref(C_), B, N))
+
+
+def attention_workspace(C_: CacheDesc, B: int, N: int, device="cuda") -> torch.Tensor:
+    """A device byte buffer of moe_attention_workspace_bytes whose head is zeroed."""
+    n = moe_attention_workspace_bytes(C_, B, N)
+    if n == 0:
+        raise MoeError("moe_attention_workspace_bytes", MOE_ERR_ARG)
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    ws[:4096].zero_()
+    return ws
+
+
+def moe_tree_attention(C_, q, k_pages, v_pages, page_table, cache_len, B, N, out, ws, parent=None,
+                       row_start=None, sink_logit=None, lse=None, stream=None):
+    """Attention of a block's nodes over the paged cache (see include/moetree.h). q, out
+    [R, H, dh]; pools as given to cache_desc."""
+    fn, R = "moe_tree_attention", q.shape[0]
+    dev, dt = _expect_pools(fn, C_, k_pages, v_pages, page_table, cache_len, B, row_start, R)
+    ldq = _rows(fn, "q", q, dt, (R, C_.H, C_.dh), dev)
+    _expect(fn, "out", out, dt, (R, C_.H, C_.dh), dev)
+    _expect(fn, "parent", parent, torch.int32, (R,), dev)
+    _expect(fn, "sink_logit", sink_logit, torch.float32, (C_.H,), dev)
+    _expect(fn, "lse", lse, torch.float32, (R, C_.H), dev)
+    _expect(fn, "workspace", ws, torch.uint8, None, dev)
+    if ws.numel() < moe_attention_workspace_bytes(C_, max(B, 1), max(N, 1)):
+        raise ValueError(f"{fn}: the workspace is smaller than attention_workspace(C, {B}, {N})")
+    with _on(q, stream) as s:
+        return _check(fn, lib().moe_tree_attention(
+            C.byref(C_), _ptr(q), ldq, _ptr(k_pages), _ptr(v_pages), _ptr(page_table),
+            _ptr(cache_len), _ptr(row_start), _ptr(parent), _ptr(sink_logit), B, N, R, _ptr(out),
+            _ptr(lse), _ptr(ws), s))
+
+
+def moe_kv_append(C_, q, k, v, k_pages, v_pages, page_table, cache_len, B, N, q_out, ws=None,
+                  depth=None, row_start=None, inv_freq=None, rope_scale=1.0, q_weight=None,
+                  k_weight=None, eps=1e-6, stream=None):
+    """Writes a block's k and v to the cache and rotates its q (see include/moetree.h). q, k, v
+    [R, heads, dh] may be parts of one projection's rows; q and q_out may both be None."""
+    fn, R = "moe_kv_append", k.shape[0]
+    dev, dt = _expect_pools(fn, C_, k_pages, v_pages, page_table, cache_len, B, row_start, R)
+    ldq = _rows(fn, "q", q, dt, (R, C_.H, C_.dh), dev) if q is not None else 0
+    ldk = _rows(fn, "k", k, dt, (R, C_.H_kv, C_.dh), dev)
+    ldv = _rows(fn, "v", v, dt, (R, C_.H_kv, C_.dh), dev)
+    _expect(fn, "q_out", q_out, dt, (R, C_.H, C_.dh), dev)
+    _expect(fn, "depth", depth, torch.int32, (R,), dev)
+    _expect(fn, "inv_freq", inv_freq, torch.float32, None, dev)
+    _expect(fn, "q_weight", q_weight, dt, (C_.dh,), dev)
+    _expect(fn, "k_weight", k_weight, dt, (C_.dh,), dev)
+    _expect(fn, "workspace", ws, torch.uint8, None, dev)
+    P = RopeParams(q_weight.data_ptr() if q_weight is not None else None,
+                   k_weight.data_ptr() if k_weight is not None else None, eps,
+                   inv_freq.data_ptr() if inv_freq is not None else None,
+                   2 * inv_freq.numel() if inv_freq is not None else 0, rope_scale)
+    with _on(k, stream) as s:
+        return _check(fn, lib().moe_kv_append(
+            C.byref(C_), C.byref(P), _ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(k_pages),
+            _ptr(v_pages), _ptr(page_table), _ptr(cache_len), _ptr(row_start), _ptr(depth), B, N,
+            R, _ptr(q_out), _ptr(ws), s))
+
+
+def moe_kv_commit(C_, k_pages, v_pages, page_table, cache_len, path, n_accept, new_len, ws=None,
+                  stream=None):
+    """Moves each sequence's accepted path to the front of its block (see include/moetree.h).
+    path [B, P], n_accept [B], new_len [B] (may be cache_len), all int32 on the device."""
+    fn = "moe_kv_commit"
+    B, P = path.shape
+    dev, _ = _expect_pools(fn, C_, k_pages, v_pages, page_table, cache_len, B, None, 0)
+    _expect(fn, "path", path, torch.int32, None, dev)
+    _expect(fn, "n_accept", n_accept, torch.int32, (B,), dev)
+    _expect(fn, "new_len", new_len, torch.int32, (B,), dev)
+    _expect(fn, "workspace", ws, torch.uint8, None, dev)
+    with _on(k_pages, stream) as s:
+        return _check(fn, lib().moe_kv_commit(
+            C.byref(C_), _ptr(k_pages), _ptr(v_pages), _ptr(page_table), _ptr(cache_len),
+            _ptr(path), _ptr(n_accept), B, P, _ptr(new_len), _ptr(ws), s))
+
+
+def moe_block_norm(L, x, branch=None, h=None, hn=None, w_post=None, gate=None, gate_rows=0,
+                   scale=1.0, w_pre=None, eps=1e-6, stream=None):
+    """The norms and the residual between the halves of a block (see include/moetree.h):
+    h = x + scale * gate * norm(branch), hn = norm(h), both [R, d]."""
+    fn, (R, d) = "moe_block_norm", x.shape
+    dev, dt = x.device, torch.bfloat16 if L.dtype == MOE_DTYPE_BF16 else torch.float32
+    if gate is not None and gate_rows < 1:
+        raise ValueError(f"{fn}: gate_rows is {gate_rows}, expected the rows that share a gate row")
+    for name, t, shape in (("x", x, (R, L.d)), ("branch", branch, (R, d)), ("h", h, (R, d)),
+                           ("hn", hn, (R, d)), ("w_post", w_post, (d,)), ("w_pre", w_pre, (d,)),
+                           ("gate", gate, (-(-R // max(1, gate_rows)), d))):
+        _expect(fn, name, t, dt, shape, dev)
+    with _on(x, stream) as s:
+        return _check(fn, lib().moe_block_norm(
+            C.byref(L), _ptr(x), _ptr(branch), _ptr(w_post), _ptr(gate), gate_rows, scale,
+            _ptr(w_pre), eps, R, _ptr(h), _ptr(hn), s))
 
 
 def moe_event_wait(event, timeout_s: float) -> None:

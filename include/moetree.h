@@ -17,6 +17,8 @@
  *   - "Fewer experts, faster decoding: cost-aware speculative decoding for MoE"
  *     (EcoSpec), section 1 and Fig. 2-3, with the scoring rule of the blog above:
  *     a cost-aware choice of which drafted nodes to verify (moe_draft_select).
+ *   - the attention half of the block for the same nodes: a paged cache, tree attention
+ *     over it, the commit of the accepted path, and the norms between the halves.
  *
  * Conventions shared by every entry point:
  *   - All tensors are plain pointers, row-major, densely packed. "device" means
@@ -333,7 +335,8 @@ moe_status moe_draft_select(const moe_layer_desc *L, int C, const int *parent, c
 
 /* Reads and clears the kernel-side check word of a workspace. Waits for `stream`.
  * *flags = 0 when no kernel reported a problem since the last call; bit 0 = an
- * expert id outside [0, E) was skipped; bit 1 = a bounded device wait gave up. */
+ * expert id outside [0, E) was skipped; bit 1 = a bounded device wait gave up; bits 2 and 3
+ * are those of the attention calls. */
 moe_status moe_workspace_check(void *workspace, int *flags, moe_stream_t stream);
 
 /* ---------------------------------------------------------------- offload ----
@@ -420,6 +423,131 @@ moe_status moe_offload_upload_wait(moe_residency *table, int layer, double timeo
 /* Host poll of cudaEventQuery(ev) for at most timeout_s seconds. MOE_ERR_TIMEOUT if
  * the event has not completed by then. */
 moe_status moe_event_wait(moe_event_t ev, double timeout_s);
+
+/* ------------------------------------------------------------ attention ----
+ * The attention half of a decoder block for the same verification block ("MoE and
+ * speculative decoding" blog: per round the engine keeps KV pages, a tree mask and the
+ * rollback of what was not accepted): the block's nodes are written to a paged cache of
+ * keys and values (moe_kv_append), attend over it (moe_tree_attention), and after
+ * verification the accepted path moves to the front of the block (moe_kv_commit).
+ *
+ * Sequence b holds cache_len[b] committed tokens in cache slots 0 .. len - 1 (slot j is the
+ * token at position j) and the n nodes of its block in slots len .. len + n - 1, node m in
+ * slot len + m. Slot j lies in page page_table[b][j / page_size] of the pool, at token
+ * j % page_size. The nodes are a draft tree (`parent`), or, with parent == NULL, a chain:
+ * a chunk of a prompt, or (n = 1) the single next token. */
+
+/* A layer's cache and heads. Query head i reads key/value head i / (H / H_kv). K and V pools
+ * have the same strides, in elements: page p, token t, head h starts at
+ * p * stride_page + t * stride_tok + h * stride_head, and its dh elements are contiguous.
+ * With window > 0 a query at position i sees the positions i - window + 1 .. i and the first
+ * `sink_tokens` positions; with 0 it sees all. Limits: H a multiple of H_kv, dh a multiple of 8
+ * and at most 256, strides multiples of 8 and at least dh, max_pages * page_size <= 2^30,
+ * scale > 0. bf16 heads of dh <= 128 run on the tensor cores, fp32 and larger heads on the
+ * CUDA cores. */
+typedef struct {
+    int H, H_kv, dh;
+    int dtype;      /* moe_dtype of q, k, v, the pools and the output */
+    int page_size;  /* tokens of a page */
+    int n_pages;    /* pages of the pool */
+    int max_pages;  /* entries of a page-table row */
+    long long stride_page, stride_tok, stride_head;
+    int window;
+    int sink_tokens;
+    float scale;    /* of q.k before the softmax, 1 / sqrt(dh) as a rule */
+} moe_cache_desc;
+
+/* Bytes of workspace of moe_tree_attention for up to B sequences of up to N nodes each; 0 for a
+ * bad descriptor. Unlike the layer's workspace, its first 4096 bytes must be zero before the
+ * first call that gets it (they hold the check word, to which calls only add bits until
+ * moe_workspace_check reads and clears it); the rest is scratch. Two calls that overlap in time
+ * must use different workspaces, captured graphs that may run at the same time too. */
+size_t moe_attention_workspace_bytes(const moe_cache_desc *C, int B, int N);
+
+/* Attention of the block's nodes over the cache: for row r = node n of sequence b and head h
+ *   out[r, h] = sum_j p_j v_j,  p_j = exp(scale q[r, h].k_j) / Z,  Z = sum_j exp(scale q.k_j)
+ * over the slots j that the node sees: the committed ones, itself and its ancestors (chain:
+ * itself and the nodes before it), inside the window if there is one. A row that sees nothing
+ * gives zeros. A slot that no row sees takes no part, whatever it holds (infinities, NaN).
+ *   q           [R, H, dh] device, rows ldq elements apart (ldq a multiple of 8, >= H dh).
+ *   k_pages, v_pages  the pools; the block's own k and v must be in them (moe_kv_append).
+ *   page_table  [B, max_pages] device int32; entries past a sequence's last slot are not read.
+ *   cache_len   [B] device int32, committed tokens.
+ *   row_start   [B + 1] device int32: sequence b has rows row_start[b] .. row_start[b+1] - 1, at
+ *               most N of them (none is fine); rows past row_start[B] are left as they are.
+ *               NULL: N rows for each, R = B N.
+ *   parent      [R] device int32: parent[r] is the node index (within the sequence, lower than
+ *               the node's own) of row r's parent; anything else makes it a root. NULL: chains.
+ *   sink_logit  [H] device fp32 or NULL: Z also counts exp(sink_logit[h]) (GPT-OSS's sinks).
+ *   out         [R, H, dh] device, dense; lse [R, H] device fp32 or NULL: log Z (-inf where
+ *               nothing is seen).
+ * Pointers to q, pools and out are 16-byte aligned, workspace 256-byte. Scores, softmax
+ * statistics and sums are fp32; the tensor-core kernel rounds the unnormalised p to bf16 for
+ * its second product. Lengths and tables are only read on the device, so a captured graph may
+ * be replayed with other ones. Device-side checks (moe_workspace_check): bit 2 = a page outside
+ * the pool (its slots are not seen), bit 3 = lengths or row ranges that do not fit the page
+ * table, N or R (cut to what fits). */
+moe_status moe_tree_attention(const moe_cache_desc *C, const void *q, long long ldq,
+                              const void *k_pages, const void *v_pages, const int *page_table,
+                              const int *cache_len, const int *row_start, const int *parent,
+                              const float *sink_logit, int B, int N, int R, void *out, float *lse,
+                              void *workspace, moe_stream_t stream);
+
+/* What moe_kv_append does to the projected rows before it writes them. q_weight, k_weight [dh]
+ * (layer dtype, device, or NULL): RMS norm of each head's q and k, x / sqrt(mean x^2 + eps) w.
+ * inv_freq [rot_dim / 2] (device fp32, or NULL: no rotation): elements i and i + rot_dim / 2 of
+ * a head, i < rot_dim / 2, turn by the angle position * inv_freq[i] (the product is formed in
+ * fp64, so far positions keep their angle), and are multiplied by rope_scale; elements from
+ * rot_dim on stay. rot_dim is a multiple of 4, at most dh. */
+typedef struct {
+    const void *q_weight, *k_weight;
+    float eps;
+    const float *inv_freq;
+    int rot_dim;
+    float rope_scale;
+} moe_rope_params;
+
+/* Writes the block's new keys and values to the cache and rotates its queries: row r = node n of
+ * sequence b goes to slot cache_len[b] + n, at position cache_len[b] + depth[r] (depth NULL:
+ * n).
+ *   q [R, H, dh], k, v [R, H_kv, dh] device, rows ldq, ldk, ldv elements apart (each may be
+ *   part of one projection's output); q_out [R, H, dh] device, dense; it may be q itself where
+ *   ldq = H dh. q and q_out may both be NULL (only the cache is written).
+ *   workspace: only its check word is used (bits as for moe_tree_attention; rows whose slot has
+ *   no valid page are not written to the cache); may be NULL.
+ * Other arguments as moe_tree_attention. */
+moe_status moe_kv_append(const moe_cache_desc *C, const moe_rope_params *P, const void *q,
+                         long long ldq, const void *k, long long ldk, const void *v, long long ldv,
+                         void *k_pages, void *v_pages, const int *page_table,
+                         const int *cache_len, const int *row_start, const int *depth, int B,
+                         int N, int R, void *q_out, void *workspace, moe_stream_t stream);
+
+/* Commits a verified tree's accepted path: for each sequence the keys and values of node
+ * path[b][j] move to slot cache_len[b] + j, j < n_accept[b], and
+ * new_len[b] = cache_len[b] + n_accept[b].
+ *   path [B, P] device int32: ascending node indexes from the root down (rows of moe_draft_select's
+ *   order, parents first); n_accept [B] device int32, 0 .. P; new_len [B] device int32, may be
+ *   cache_len itself. A path that is not ascending, or leaves the page table or the pool, ends
+ *   before its first bad node (bit 2 or 3 of the check word; workspace may be NULL). */
+moe_status moe_kv_commit(const moe_cache_desc *C, void *k_pages, void *v_pages,
+                         const int *page_table, const int *cache_len, const int *path,
+                         const int *n_accept, int B, int P, int *new_len, void *workspace,
+                         moe_stream_t stream);
+
+/* The norms and the residual between the two halves of a block in one pass:
+ *   u  = branch, or with w_post: w_post (.) branch / sqrt(mean branch^2 + eps)
+ *   h  = x + scale gate (.) u                      (the residual stream after the branch)
+ *   hn = w_pre (.) h / sqrt(mean h^2 + eps)        (the next half's input; w_pre NULL: ones)
+ * Sums in fp32 (rows whose squares leave fp32's range are scaled first); hn is formed from h
+ * before its rounding; each output is rounded once.
+ *   x, branch, h, hn [R, d] device, layer dtype; h may be x or branch; hn may be NULL, or
+ *   branch, or x where h is not x. branch NULL: h = x (h may be NULL then).
+ *   gate [ceil(R / gate_rows), d] or NULL: rows r share gate row r / gate_rows (gate_rows = R: one
+ *   row for all). w_post, w_pre [d]. eps >= 0. All 16-byte aligned. */
+moe_status moe_block_norm(const moe_layer_desc *L, const void *x, const void *branch,
+                          const void *w_post, const void *gate, int gate_rows, float scale,
+                          const void *w_pre, float eps, int R, void *h, void *hn,
+                          moe_stream_t stream);
 
 #ifdef __cplusplus
 }
