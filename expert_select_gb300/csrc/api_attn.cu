@@ -13,12 +13,14 @@ static size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Partial results: slots 0 and 1 of every CTA, for whichever kernel runs.
 WsLayout ws_layout(int dh, long long rows_per_seq) {
-    const size_t simt = (size_t)kMaxCtas * std::min<long long>(kSimtRows, rows_per_seq);
+    const size_t rows =
+        std::max((size_t)kMaxCtas * std::min<long long>(kSimtRows, rows_per_seq),
+                 (size_t)kTcMaxCtas * std::min<long long>(kTcRows, rows_per_seq));
     WsLayout w{};
     w.rec = kHeadBytes;
     w.ml = align256(w.rec + (size_t)kMaxCtas * 8 * sizeof(int));
-    w.o = align256(w.ml + simt * 2 * 2 * sizeof(float));
-    w.total = align256(w.o + simt * 2 * dh * sizeof(float));
+    w.o = align256(w.ml + rows * 2 * 2 * sizeof(float));
+    w.total = align256(w.o + rows * 2 * dh * sizeof(float));
     return w;
 }
 
@@ -112,7 +114,9 @@ moe_status moe_tree_attention(const moe_cache_desc *C, const void *q, long long 
     a.window = C->window;
     a.sinks = C->sink_tokens;
     a.scale = C->scale;
-    return cuda_status(attn::launch_simt(a, C->dtype, (cudaStream_t)stream));
+    return cuda_status(attn::tc_supported(a, C->dtype)
+                           ? attn::launch_tc(a, (cudaStream_t)stream)
+                           : attn::launch_simt(a, C->dtype, (cudaStream_t)stream));
 }
 
 moe_status moe_kv_append(const moe_cache_desc *C, const moe_rope_params *P, const void *q,

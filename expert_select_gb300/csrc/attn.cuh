@@ -314,7 +314,10 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(f
 
 cudaError_t launch_simt(Args a, int dtype, cudaStream_t s);
 cudaError_t launch_combine(const Args &a, int dtype, int n_ctas, cudaStream_t s);
-constexpr int kSimtRows = 32;  // rows of an item
+cudaError_t launch_tc(Args a, cudaStream_t s);
+bool tc_supported(const Args &a, int dtype);
+// rows of an item, and CTAs of the tensor-core kernel at most (one per SM)
+constexpr int kSimtRows = 32, kTcRows = 256, kTcMaxCtas = 160;
 
 struct WsLayout {
     size_t rec, ml, o, total;
