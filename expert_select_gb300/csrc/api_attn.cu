@@ -114,9 +114,11 @@ moe_status moe_tree_attention(const moe_cache_desc *C, const void *q, long long 
     a.window = C->window;
     a.sinks = C->sink_tokens;
     a.scale = C->scale;
-    return cuda_status(attn::tc_supported(a, C->dtype)
-                           ? attn::launch_tc(a, (cudaStream_t)stream)
-                           : attn::launch_simt(a, C->dtype, (cudaStream_t)stream));
+    cudaStream_t s = (cudaStream_t)stream;
+    if (!attn::tc_supported(a, C->dtype)) return cuda_status(attn::launch_simt(a, C->dtype, s));
+    // an item of at most 16 rows is bound by reading the cache, whatever multiplies
+    return cuda_status((long long)N * a.G <= attn::kFewRows ? attn::launch_few(a, s)
+                                                            : attn::launch_tc(a, s));
 }
 
 moe_status moe_kv_append(const moe_cache_desc *C, const moe_rope_params *P, const void *q,

@@ -287,6 +287,39 @@ __device__ __forceinline__ int node_position(const Args &a, const Seq &s, int no
     return s.len + d;
 }
 
+// May a row of nodes i0 .. i1 not see some of the BN slots from k0? (Never false wrongly.)
+template <int BN>
+__device__ __forceinline__ bool tile_masked(const Args &a, const Seq &s, int i0, int i1, int k0) {
+    const int first_hidden = a.parent ? min(s.len, s.L) : min(s.len + i0 + 1, s.L);
+    if (k0 + BN > first_hidden) return true;
+    if (a.window <= 0) return false;
+    const int max_pos = s.len + (a.parent ? s.n - 1 : i1);
+    return k0 < max_pos - a.window + 1 && k0 + BN > a.sinks;
+}
+
+// The page of slot j, or -1 if the table's entry is outside the pool.
+__device__ __forceinline__ int page_of(const Args &a, int b, int j) {
+    const int pg = a.table[(size_t)b * a.max_pages + j / a.page];
+    return pg >= 0 && pg < a.n_pages ? pg : -1;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&t);
+}
+
+// The tensor-core kernels raise a row's running maximum only when it grows by more than this
+// (log2): until then the unnormalised p is at most 2^8, which bf16 and the fp32 sums hold as well
+// as values up to 1, and O needs no rescaling. The maximum a row ends with is a scale factor that
+// the division by the sum takes out again.
+constexpr float kRaise = 8.f;
+
 // Factor that normalises an accumulated O, and the log of the denominator, from the running
 // maximum m (base-2 logits) and sum l, with the head's sink logit (natural log units).
 __device__ __forceinline__ float finish(float m, float l, const float *sink, int head, float *lse) {
@@ -315,9 +348,10 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(f
 cudaError_t launch_simt(Args a, int dtype, cudaStream_t s);
 cudaError_t launch_combine(const Args &a, int dtype, int n_ctas, cudaStream_t s);
 cudaError_t launch_tc(Args a, cudaStream_t s);
+cudaError_t launch_few(Args a, cudaStream_t s);
 bool tc_supported(const Args &a, int dtype);
 // rows of an item, and CTAs of the tensor-core kernel at most (one per SM)
-constexpr int kSimtRows = 32, kTcRows = 256, kTcMaxCtas = 160;
+constexpr int kSimtRows = 32, kTcRows = 256, kTcMaxCtas = 160, kFewRows = 16;
 
 struct WsLayout {
     size_t rec, ml, o, total;

@@ -219,11 +219,14 @@ __global__ void __launch_bounds__(kThr) attn_simt_kernel(const Args a) {
 
 // Merges a cut item: block (c, y) looks at the item inside which CTA c's range begins. The
 // item's first tiles are in slot 1 of the CTA before, the rest in slot 0 of CTAs c, c + 1, ...;
-// the block of the first such c does the item's rows 8 y .. 8 y + 7, a warp per row, the parts in
-// CTA order: sum_i 2^(m_i - M) O_i over sum_i 2^(m_i - M) l_i, M the largest m_i. Lane i reads part
-// i's maximum and sum; the parts' O rows are read 4 columns a lane.
-template <typename T>
-__global__ void __launch_bounds__(256) attn_combine_kernel(const Args a, int n_ctas) {
+// the block of the first such c merges the item's rows:
+//   sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i,  M the largest m_i.
+// WPR warps share a row (8 / WPR rows per block), warp w taking the parts w, w + WPR, ... in
+// order: a single long sequence leaves a few rows in many parts, whose reads must not queue up
+// behind one another; large items have many rows in few parts. Sums run in a fixed order.
+template <typename T, int WPR>
+__global__ void __launch_bounds__(256) attn_combine_kernel(const Args a) {
+    __shared__ float s_o[WPR > 1 ? 8 : 1][256], s_ml[8][2];
     pdl_wait();
     const int c = blockIdx.x;
     const int *rec = a.rec + c * 8;
@@ -232,43 +235,36 @@ __global__ void __launch_bounds__(256) attn_combine_kernel(const Args a, int n_c
     const int h = rec[1], t0 = rec[2], nt = rec[3];
     const long long quota = reinterpret_cast<const long long *>(rec)[2];
     if (t0 > quota) return;  // an earlier CTA's range begins inside the item too
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = warp % WPR;
     const int b = e / a.qblocks, q0 = (e - b * a.qblocks) * a.rows;
     const Seq s = sequence(a, b);
-    const int row = blockIdx.y * 8 + (threadIdx.x >> 5);
-    if (row >= min(a.rows, s.n * a.G - q0)) return;
+    const int row = blockIdx.y * (8 / WPR) + warp / WPR;
+    const bool live = row < min(a.rows, s.n * a.G - q0);
+    if (WPR == 1 && !live) return;
     // parts: CTA c - 1 (t0 tiles), then as many as the remaining tiles take
-    const int parts = 1 + (int)((nt - t0 + quota - 1) / quota);
+    const int parts = live ? 1 + (int)((nt - t0 + quota - 1) / quota) : 0;
+    auto part = [&](int i) { return ((size_t)(c - 1 + i) * 2 + (i == 0)) * a.prows + row; };
     float M = -INFINITY;
     for (int i = lane; i < parts; i += 32) {
-        const size_t pr = ((size_t)(c - 1 + i) * 2 + (i == 0)) * a.prows + row;
-        if (a.part_ml[pr * 2 + 1] > 0.f || a.part_ml[pr * 2 + 1] != a.part_ml[pr * 2 + 1])
-            M = fmaxf(M, a.part_ml[pr * 2]);
+        const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + part(i) * 2);
+        if (ml.y != 0.f) M = fmaxf(M, ml.x);
     }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     const float base = M == -INFINITY ? 0.f : M;
     float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};  // columns 4 lane + 128 c (dh <= 256)
     float l = 0.f;
-    for (int i0 = 0; i0 < parts; i0 += 32) {
-        float w = 0.f;
-        if (i0 + lane < parts) {
-            const int i = i0 + lane;
-            const size_t pr = ((size_t)(c - 1 + i) * 2 + (i == 0)) * a.prows + row;
-            const float li = a.part_ml[pr * 2 + 1];
-            w = li == 0.f ? 0.f : exp2f(a.part_ml[pr * 2] - base);
-            l += w * li;
-        }
-        const int ni = min(32, parts - i0);
 #pragma unroll 4
-        for (int i = 0; i < ni; ++i) {
-            const float wi = __shfl_sync(0xffffffffu, w, i);
-            const size_t pr = ((size_t)(c - 1 + i0 + i) * 2 + (i0 + i == 0)) * a.prows + row;
+    for (int i = w; i < parts; i += WPR) {
+        const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + part(i) * 2);
+        const float wi = ml.y == 0.f ? 0.f : exp2f(ml.x - base);
+        l += wi * ml.y;
 #pragma unroll
-            for (int cc = 0; cc < 2; ++cc) {
-                const int col = cc * 128 + lane * 4;
-                if (col < a.dh && wi != 0.f) {
-                    const float4 v = *reinterpret_cast<const float4 *>(a.part_o + pr * a.dh + col);
+        for (int cc = 0; cc < 2; ++cc) {
+            const int col = cc * 128 + lane * 4;
+            if (col < a.dh) {
+                const float4 v = *reinterpret_cast<const float4 *>(a.part_o + part(i) * a.dh + col);
+                if (wi != 0.f) {
                     acc[cc * 4] += wi * v.x;
                     acc[cc * 4 + 1] += wi * v.y;
                     acc[cc * 4 + 2] += wi * v.z;
@@ -277,8 +273,28 @@ __global__ void __launch_bounds__(256) attn_combine_kernel(const Args a, int n_c
             }
         }
     }
+    if constexpr (WPR > 1) {
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        for (int cc = 0; cc < 2; ++cc)
+            *reinterpret_cast<float4 *>(&s_o[warp][cc * 128 + lane * 4]) =
+                make_float4(acc[cc * 4], acc[cc * 4 + 1], acc[cc * 4 + 2], acc[cc * 4 + 3]);
+        if (lane == 0) s_ml[warp][0] = l;
+        __syncthreads();
+        if (w != 0 || !live) return;
+#pragma unroll 1
+        for (int x = 1; x < WPR; ++x) {
+            l += s_ml[warp + x][0];
+#pragma unroll
+            for (int cc = 0; cc < 2; ++cc) {
+                const float4 v =
+                    *reinterpret_cast<const float4 *>(&s_o[warp + x][cc * 128 + lane * 4]);
+                acc[cc * 4] += v.x;
+                acc[cc * 4 + 1] += v.y;
+                acc[cc * 4 + 2] += v.z;
+                acc[cc * 4 + 3] += v.w;
+            }
+        }
+    }
     const int qr = q0 + row, node = qr / a.G, head = h * a.G + (qr - node * a.G);
     const size_t orow = (size_t)(s.row0 + node) * a.H + head;
     float lse;
@@ -293,6 +309,13 @@ __global__ void __launch_bounds__(256) attn_combine_kernel(const Args a, int n_c
         }
     }
     if (a.lse && lane == 0) a.lse[orow] = lse;
+}
+
+template <typename T> cudaError_t combine_t(const Args &a, int n_ctas, cudaStream_t s) {
+    if (a.prows <= kFewRows)
+        return launch_pdl(attn_combine_kernel<T, 8>, dim3(n_ctas, a.prows), dim3(256), 0, s, a);
+    return launch_pdl(attn_combine_kernel<T, 1>, dim3(n_ctas, (a.prows + 7) / 8), dim3(256), 0, s,
+                      a);
 }
 
 template <typename T, int NC>
@@ -318,10 +341,8 @@ template <typename T> cudaError_t launch_t(const Args &a, int nsm, int *ctas, cu
 }  // namespace
 
 cudaError_t launch_combine(const Args &a, int dtype, int n_ctas, cudaStream_t s) {
-    const dim3 grid(n_ctas, (a.prows + 7) / 8);
-    if (dtype == MOE_DTYPE_BF16)
-        return launch_pdl(attn_combine_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, a, n_ctas);
-    return launch_pdl(attn_combine_kernel<float>, grid, dim3(256), 0, s, a, n_ctas);
+    return dtype == MOE_DTYPE_BF16 ? combine_t<__nv_bfloat16>(a, n_ctas, s)
+                                   : combine_t<float>(a, n_ctas, s);
 }
 
 cudaError_t launch_simt(Args a, int dtype, cudaStream_t s) {

@@ -22,11 +22,6 @@
 // 1. The second product reads P from tensor memory and V from shared memory as it was loaded
 // (MN-major), so P never passes through shared memory.
 //
-// The running maximum is only raised when a row's maximum grows by more than 2^8: until then P
-// is at most 2^8, which bf16 and the fp32 sums hold as well as values up to 1, and O needs no
-// rescaling. The maximum a row ends with is only a scale factor, the result does not depend on
-// it (up to rounding).
-//
 // A masked score is -inf, so its P is 0; but 0 x V is NaN where V is infinite or NaN. In tiles
 // that hold masked slots (the last ones, and a window's first) warp 2 therefore clears the rows of
 // V past the sequence's end and the non-finite elements of the others before the second product;
@@ -49,7 +44,6 @@ constexpr int kThreads = 384;
 constexpr int kVq = 8;           // V-ready barriers in rotation: more than V tiles in the ring
 constexpr int kMaxStages = 6;
 constexpr int kCtlBytes = 2048;
-constexpr float kRaise = 8.f;    // log2 growth of a row's maximum that is tolerated
 
 struct Params {
     Args a;
@@ -73,32 +67,6 @@ static_assert(sizeof(Ctl) <= kCtlBytes, "control block");
 __device__ __forceinline__ void softmax_bar() {  // the 256 threads of warps 4-11
     __syncwarp();
     asm volatile("bar.sync 1, 256;" ::: "memory");
-}
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&t);
-}
-
-// May a row of nodes i0 .. i1 not see some slot of the tile at k0? (Never false wrongly.)
-__device__ __forceinline__ bool tile_masked(const Args &a, const Seq &s, int i0, int i1, int k0) {
-    const int first_hidden = a.parent ? min(s.len, s.L) : min(s.len + i0 + 1, s.L);
-    if (k0 + kBN > first_hidden) return true;
-    if (a.window <= 0) return false;
-    const int max_pos = s.len + (a.parent ? s.n - 1 : i1);
-    return k0 < max_pos - a.window + 1 && k0 + kBN > a.sinks;
-}
-
-// The page of slot j, or -1 if the table's entry is outside the pool.
-__device__ __forceinline__ int page_of(const Args &a, int b, int j) {
-    const int pg = a.table[(size_t)b * a.max_pages + j / a.page];
-    return pg >= 0 && pg < a.n_pages ? pg : -1;
 }
 
 // Positions of K and V tiles of a segment of n tiles in the ring's order: LA K tiles first, then
@@ -330,7 +298,7 @@ attn_tc_kernel(const __grid_constant__ Params p) {
                                 mbar_wait(bar(c.full[st]), ring.parity(rp), &c.abort, a.flags));
                 if (!ok) break;
                 const int k0 = g.tl.at(g.t + t) * kBN;
-                if (c.bad_page || tile_masked(a, g.s, i0, i1, k0)) {
+                if (c.bad_page || tile_masked<kBN>(a, g.s, i0, i1, k0)) {
                     // rows that no query of the item sees are cleared whole: with one node all
                     // that it does not see, else what lies past the end or has no page
                     uint32_t bits[4];
@@ -438,7 +406,7 @@ attn_tc_kernel(const __grid_constant__ Params p) {
                 if (active && !__any_sync(0xffffffffu, dead)) {
                     uint32_t s[128];
                     tmem_ld128(tS, s);
-                    if (tile_masked(a, g.s, i0, i1, k0) || c.bad_page) {
+                    if (tile_masked<kBN>(a, g.s, i0, i1, k0) || c.bad_page) {
                         uint32_t bits[4];
                         visible_bits<4>(a, g.s, node, pos, k0, bits);
                         if (c.bad_page) {
