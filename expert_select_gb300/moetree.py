@@ -399,48 +399,62 @@ def moe_draft_select(L, parent, depth, logp, footprint, lam: float, gamma: int, 
 # ------------------------------------------------------------- attention half of the block
 
 _CODE = {torch.float32: MOE_DTYPE_F32, torch.bfloat16: MOE_DTYPE_BF16}
+_TORCH = {v: k for k, v in _CODE.items()}
 
 
-def _expect(fn: str, name: str, t: Optional[torch.Tensor], dtype=None, shape=None, device=None,
-            dense=True):
-    """Refuses a tensor that the entry point would read or write wrongly: another type, shape,
-    device or layout than its pointer is taken for."""
-    if t is None:
-        return
-    if dtype is not None and t.dtype != dtype:
+def _refuse(fn: str, name: str, t: torch.Tensor, dtype, shape, index, dense=True):
+    """Says why a tensor is not what its pointer would be taken for."""
+    if t.dtype != dtype:
         raise ValueError(f"{fn}: {name} is {t.dtype}, expected {dtype}")
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{fn}: {name} is on {t.device}, expected {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{fn}: {name} is on {t.device}, the first tensor on device {index}")
     if dense and not t.is_contiguous():
         raise ValueError(f"{fn}: {name} must be contiguous")
 
 
-def _rows(fn: str, name: str, t: torch.Tensor, dtype, shape, device) -> int:
+def _dense(fn, name, t, dtype, shape, index):
+    """Refuses a tensor (None passes) of another type, shape, device or layout. One expression, as
+    it runs for every argument of every call."""
+    if t is not None and not (t.dtype is dtype and t.shape == shape and t.get_device() == index and
+                              t.is_contiguous()):
+        _refuse(fn, name, t, dtype, shape, index)
+
+
+def _rows(fn, name, t, dtype, shape, index) -> int:
     """A [rows, heads, dh] tensor whose rows may be a part of wider ones; its row stride."""
-    _expect(fn, name, t, dtype, shape, device, dense=False)
-    if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2])):
+    if not (t.dtype is dtype and t.shape == shape and t.get_device() == index):
+        _refuse(fn, name, t, dtype, shape, index, dense=False)
+    ld, head, one = t.stride()
+    n, heads, dh = shape
+    if n == 0:
+        return heads * dh
+    if one != 1 or (heads > 1 and head != dh):
         raise ValueError(f"{fn}: the heads of {name}'s rows must lie side by side")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * t.shape[2])
+    return ld if n > 1 else max(ld, heads * dh)
 
 
-class _on:
-    """Makes a tensor's device the current one for a call, and gives the stream to use."""
+def _at(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
 
-    def __init__(self, t: torch.Tensor, stream):
-        self.index, self.stream = t.device.index, stream
 
-    def __enter__(self):
-        self.before = torch.cuda.current_device()
-        if self.before != self.index:
-            torch.cuda.set_device(self.index)
-        return _stream(self.stream)
-
-    def __exit__(self, *exc):
-        if self.before != self.index:
-            torch.cuda.set_device(self.before)
-        return False
+def _run(fn: str, index: int, stream, *args) -> int:
+    """Calls entry point `fn` on device `index`, on `stream` or the device's current one."""
+    if index < 0:
+        raise ValueError(f"{fn}: the tensors must be on a CUDA device")
+    before = torch._C._cuda_getDevice()
+    if before != index:
+        torch.cuda.set_device(index)
+    try:
+        s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+        st = getattr(lib(), fn)(*args, s)
+    finally:
+        if before != index:
+            torch.cuda.set_device(before)
+    if st != MOE_OK:
+        raise MoeError(fn, st)
+    return st
 
 
 def cache_desc(pages: torch.Tensor, H: int, max_pages: int, window: int = 0, sink_tokens: int = 0,
@@ -460,18 +474,28 @@ def cache_desc(pages: torch.Tensor, H: int, max_pages: int, window: int = 0, sin
                      dh ** -0.5 if scale is None else scale)
 
 
-def _expect_pools(fn, C_, k_pages, v_pages, page_table, cache_len, B, row_start, R):
-    dev = k_pages.device
-    dt = torch.bfloat16 if C_.dtype == MOE_DTYPE_BF16 else torch.float32
+def _pools(fn, C_, k_pages, v_pages, page_table, cache_len, B, row_start):
+    """Checks the cache's tensors against its description; the device index and type."""
+    index, dt = k_pages.get_device(), _TORCH[C_.dtype]
+    shape = (C_.n_pages, C_.page_size, C_.H_kv, C_.dh)
+    st = (C_.stride_page, C_.stride_tok, C_.stride_head, 1)
     for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        _expect(fn, name, t, dt, (C_.n_pages, C_.page_size, C_.H_kv, C_.dh), dev, dense=False)
-        want = (C_.stride_page, C_.stride_tok, C_.stride_head, 1)
-        if any(t.shape[i] > 1 and t.stride(i) != want[i] for i in range(4)):
+        if not (t.dtype is dt and t.shape == shape and t.get_device() == index):
+            _refuse(fn, name, t, dt, shape, index, dense=False)
+        if t.stride() != st and any(n > 1 and x != y for n, x, y in zip(shape, t.stride(), st)):
             raise ValueError(f"{fn}: {name} has other strides than the cache description")
-    _expect(fn, "page_table", page_table, torch.int32, (B, C_.max_pages), dev)
-    _expect(fn, "cache_len", cache_len, torch.int32, (B,), dev)
-    _expect(fn, "row_start", row_start, torch.int32, (B + 1,), dev)
-    return dev, dt
+    _dense(fn, "page_table", page_table, torch.int32, (B, C_.max_pages), index)
+    _dense(fn, "cache_len", cache_len, torch.int32, (B,), index)
+    if row_start is not None:
+        _dense(fn, "row_start", row_start, torch.int32, (B + 1,), index)
+    return index, dt
+
+
+def _scratch(fn, ws, index, need):
+    if ws is not None and not (ws.dtype is torch.uint8 and ws.get_device() == index and
+                               ws.is_contiguous() and ws.numel() >= need):
+        _refuse(fn, "workspace", ws, torch.uint8, None, index)
+        raise ValueError(f"{fn}: the workspace has {ws.numel()} bytes, expected {need} or more")
 
 
 def moe_attention_workspace_bytes(C_: CacheDesc, B: int, N: int) -> int:
@@ -492,21 +516,20 @@ def moe_tree_attention(C_, q, k_pages, v_pages, page_table, cache_len, B, N, out
                        row_start=None, sink_logit=None, lse=None, stream=None):
     """Attention of a block's nodes over the paged cache (see include/moetree.h). q, out
     [R, H, dh]; pools as given to cache_desc."""
-    fn, R = "moe_tree_attention", q.shape[0]
-    dev, dt = _expect_pools(fn, C_, k_pages, v_pages, page_table, cache_len, B, row_start, R)
-    ldq = _rows(fn, "q", q, dt, (R, C_.H, C_.dh), dev)
-    _expect(fn, "out", out, dt, (R, C_.H, C_.dh), dev)
-    _expect(fn, "parent", parent, torch.int32, (R,), dev)
-    _expect(fn, "sink_logit", sink_logit, torch.float32, (C_.H,), dev)
-    _expect(fn, "lse", lse, torch.float32, (R, C_.H), dev)
-    _expect(fn, "workspace", ws, torch.uint8, None, dev)
-    if ws.numel() < moe_attention_workspace_bytes(C_, max(B, 1), max(N, 1)):
-        raise ValueError(f"{fn}: the workspace is smaller than attention_workspace(C, {B}, {N})")
-    with _on(q, stream) as s:
-        return _check(fn, lib().moe_tree_attention(
-            C.byref(C_), _ptr(q), ldq, _ptr(k_pages), _ptr(v_pages), _ptr(page_table),
-            _ptr(cache_len), _ptr(row_start), _ptr(parent), _ptr(sink_logit), B, N, R, _ptr(out),
-            _ptr(lse), _ptr(ws), s))
+    fn, R, H = "moe_tree_attention", q.shape[0], C_.H
+    index, dt = _pools(fn, C_, k_pages, v_pages, page_table, cache_len, B, row_start)
+    shape = (R, H, C_.dh)
+    ldq = _rows(fn, "q", q, dt, shape, index)
+    _dense(fn, "out", out, dt, shape, index)
+    _dense(fn, "parent", parent, torch.int32, (R,), index)
+    _dense(fn, "sink_logit", sink_logit, torch.float32, (H,), index)
+    _dense(fn, "lse", lse, torch.float32, (R, H), index)
+    desc = C.byref(C_)
+    if B > 0 and N > 0:
+        _scratch(fn, ws, index, lib().moe_attention_workspace_bytes(desc, B, N))
+    return _run(fn, index, stream, desc, q.data_ptr(), ldq, k_pages.data_ptr(),
+                v_pages.data_ptr(), page_table.data_ptr(), cache_len.data_ptr(), _at(row_start),
+                _at(parent), _at(sink_logit), B, N, R, out.data_ptr(), _at(lse), ws.data_ptr())
 
 
 def moe_kv_append(C_, q, k, v, k_pages, v_pages, page_table, cache_len, B, N, q_out, ws=None,
@@ -514,26 +537,26 @@ def moe_kv_append(C_, q, k, v, k_pages, v_pages, page_table, cache_len, B, N, q_
                   k_weight=None, eps=1e-6, stream=None):
     """Writes a block's k and v to the cache and rotates its q (see include/moetree.h). q, k, v
     [R, heads, dh] may be parts of one projection's rows; q and q_out may both be None."""
-    fn, R = "moe_kv_append", k.shape[0]
-    dev, dt = _expect_pools(fn, C_, k_pages, v_pages, page_table, cache_len, B, row_start, R)
-    ldq = _rows(fn, "q", q, dt, (R, C_.H, C_.dh), dev) if q is not None else 0
-    ldk = _rows(fn, "k", k, dt, (R, C_.H_kv, C_.dh), dev)
-    ldv = _rows(fn, "v", v, dt, (R, C_.H_kv, C_.dh), dev)
-    _expect(fn, "q_out", q_out, dt, (R, C_.H, C_.dh), dev)
-    _expect(fn, "depth", depth, torch.int32, (R,), dev)
-    _expect(fn, "inv_freq", inv_freq, torch.float32, None, dev)
-    _expect(fn, "q_weight", q_weight, dt, (C_.dh,), dev)
-    _expect(fn, "k_weight", k_weight, dt, (C_.dh,), dev)
-    _expect(fn, "workspace", ws, torch.uint8, None, dev)
-    P = RopeParams(q_weight.data_ptr() if q_weight is not None else None,
-                   k_weight.data_ptr() if k_weight is not None else None, eps,
-                   inv_freq.data_ptr() if inv_freq is not None else None,
-                   2 * inv_freq.numel() if inv_freq is not None else 0, rope_scale)
-    with _on(k, stream) as s:
-        return _check(fn, lib().moe_kv_append(
-            C.byref(C_), C.byref(P), _ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(k_pages),
-            _ptr(v_pages), _ptr(page_table), _ptr(cache_len), _ptr(row_start), _ptr(depth), B, N,
-            R, _ptr(q_out), _ptr(ws), s))
+    fn, R, dh = "moe_kv_append", k.shape[0], C_.dh
+    index, dt = _pools(fn, C_, k_pages, v_pages, page_table, cache_len, B, row_start)
+    ldq = 0
+    if q is not None:
+        ldq = _rows(fn, "q", q, dt, (R, C_.H, dh), index)
+        _dense(fn, "q_out", q_out, dt, (R, C_.H, dh), index)
+    kv = (R, C_.H_kv, dh)
+    ldk, ldv = _rows(fn, "k", k, dt, kv, index), _rows(fn, "v", v, dt, kv, index)
+    _dense(fn, "depth", depth, torch.int32, (R,), index)
+    rot = 0
+    if inv_freq is not None:
+        rot = 2 * inv_freq.numel()
+        _dense(fn, "inv_freq", inv_freq, torch.float32, inv_freq.shape, index)
+    _dense(fn, "q_weight", q_weight, dt, (dh,), index)
+    _dense(fn, "k_weight", k_weight, dt, (dh,), index)
+    _scratch(fn, ws, index, 4096)
+    P = RopeParams(_at(q_weight), _at(k_weight), eps, _at(inv_freq), rot, rope_scale)
+    return _run(fn, index, stream, C.byref(C_), C.byref(P), _at(q), ldq, k.data_ptr(), ldk,
+                v.data_ptr(), ldv, k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
+                cache_len.data_ptr(), _at(row_start), _at(depth), B, N, R, _at(q_out), _at(ws))
 
 
 def moe_kv_commit(C_, k_pages, v_pages, page_table, cache_len, path, n_accept, new_len, ws=None,
@@ -542,33 +565,35 @@ def moe_kv_commit(C_, k_pages, v_pages, page_table, cache_len, path, n_accept, n
     path [B, P], n_accept [B], new_len [B] (may be cache_len), all int32 on the device."""
     fn = "moe_kv_commit"
     B, P = path.shape
-    dev, _ = _expect_pools(fn, C_, k_pages, v_pages, page_table, cache_len, B, None, 0)
-    _expect(fn, "path", path, torch.int32, None, dev)
-    _expect(fn, "n_accept", n_accept, torch.int32, (B,), dev)
-    _expect(fn, "new_len", new_len, torch.int32, (B,), dev)
-    _expect(fn, "workspace", ws, torch.uint8, None, dev)
-    with _on(k_pages, stream) as s:
-        return _check(fn, lib().moe_kv_commit(
-            C.byref(C_), _ptr(k_pages), _ptr(v_pages), _ptr(page_table), _ptr(cache_len),
-            _ptr(path), _ptr(n_accept), B, P, _ptr(new_len), _ptr(ws), s))
+    index, _ = _pools(fn, C_, k_pages, v_pages, page_table, cache_len, B, None)
+    _dense(fn, "path", path, torch.int32, (B, P), index)
+    _dense(fn, "n_accept", n_accept, torch.int32, (B,), index)
+    _dense(fn, "new_len", new_len, torch.int32, (B,), index)
+    _scratch(fn, ws, index, 4096)
+    return _run(fn, index, stream, C.byref(C_), k_pages.data_ptr(), v_pages.data_ptr(),
+                page_table.data_ptr(), cache_len.data_ptr(), path.data_ptr(), n_accept.data_ptr(),
+                B, P, new_len.data_ptr(), _at(ws))
 
 
 def moe_block_norm(L, x, branch=None, h=None, hn=None, w_post=None, gate=None, gate_rows=0,
                    scale=1.0, w_pre=None, eps=1e-6, stream=None):
     """The norms and the residual between the halves of a block (see include/moetree.h):
     h = x + scale * gate * norm(branch), hn = norm(h), both [R, d]."""
-    fn, (R, d) = "moe_block_norm", x.shape
-    dev, dt = x.device, torch.bfloat16 if L.dtype == MOE_DTYPE_BF16 else torch.float32
-    if gate is not None and gate_rows < 1:
-        raise ValueError(f"{fn}: gate_rows is {gate_rows}, expected the rows that share a gate row")
-    for name, t, shape in (("x", x, (R, L.d)), ("branch", branch, (R, d)), ("h", h, (R, d)),
-                           ("hn", hn, (R, d)), ("w_post", w_post, (d,)), ("w_pre", w_pre, (d,)),
-                           ("gate", gate, (-(-R // max(1, gate_rows)), d))):
-        _expect(fn, name, t, dt, shape, dev)
-    with _on(x, stream) as s:
-        return _check(fn, lib().moe_block_norm(
-            C.byref(L), _ptr(x), _ptr(branch), _ptr(w_post), _ptr(gate), gate_rows, scale,
-            _ptr(w_pre), eps, R, _ptr(h), _ptr(hn), s))
+    fn, d, dt, index = "moe_block_norm", L.d, _TORCH[L.dtype], x.get_device()
+    R = x.shape[0]
+    shape = (R, d)
+    _dense(fn, "x", x, dt, shape, index)
+    _dense(fn, "branch", branch, dt, shape, index)
+    _dense(fn, "h", h, dt, shape, index)
+    _dense(fn, "hn", hn, dt, shape, index)
+    _dense(fn, "w_post", w_post, dt, (d,), index)
+    _dense(fn, "w_pre", w_pre, dt, (d,), index)
+    if gate is not None:
+        if gate_rows < 1:
+            raise ValueError(f"{fn}: gate_rows is {gate_rows}, expected the rows of a gate row")
+        _dense(fn, "gate", gate, dt, (-(-R // gate_rows), d), index)
+    return _run(fn, index, stream, C.byref(L), x.data_ptr(), _at(branch), _at(w_post), _at(gate),
+                gate_rows, scale, _at(w_pre), eps, R, _at(h), _at(hn))
 
 
 def moe_event_wait(event, timeout_s: float) -> None:
