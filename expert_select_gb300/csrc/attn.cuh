@@ -48,7 +48,7 @@ struct Args {
     int rows;        // rows of an item (of the launched kernel)
     int prows;       // rows of a partial result: min(rows, N G)
     int qblocks;     // blocks of `rows` rows that N nodes take
-    int min_tiles;   // tiles of a CTA's range at least
+    int min_units;   // units of work of a CTA's range at least (two or more)
 };
 
 struct Seq {
@@ -107,27 +107,36 @@ __device__ __forceinline__ Tiles tiles_of(const Args &a, const Seq &s, int q0, i
     return t;
 }
 
-template <int BN>
-__device__ __forceinline__ int entry_tiles(const Args &a, int e, int *bad = nullptr) {
+// Tiles of an entry's items, and the weight of one: a tile of 256 rows is twice the work of one of
+// 128 (HEAVY: rows from which a tile counts two).
+template <int BN, int HEAVY>
+__device__ __forceinline__ int entry_tiles(const Args &a, int e, int *w, int *bad = nullptr) {
     const int b = e / a.qblocks, q0 = (e - b * a.qblocks) * a.rows;
     const Seq s = sequence(a, b, bad);
     const int rows = s.n * a.G;
+    *w = 1;
     if (q0 >= rows) return 0;
-    return tiles_of<BN>(a, s, q0, min(rows, q0 + a.rows)).nt;
+    const int q1 = min(rows, q0 + a.rows);
+    if (q1 - q0 >= HEAVY) *w = 2;
+    return tiles_of<BN>(a, s, q0, q1).nt;
 }
 
-// A CTA's range of tiles: `left` tiles from tile t of the item (entry e, key/value head h),
-// where entry e = sequence * qblocks + block of rows.
+// A CTA's range of work, from `off` units into the item (entry e, key/value head h), where entry
+// e = sequence * qblocks + block of rows. Tile t of an item of weight w is the units w t ..
+// w t + w - 1; it belongs to one CTA: a boundary at
+// unit u of the item lies before tile floor(u / w), for the range that ends there and for the one
+// that begins.
 struct Range {
-    long long quota;
-    int e, h, t;
-    long long left;
+    long long quota;  // units of a range
+    int e, h;
+    long long off;    // the range's first unit within the item
+    long long left;   // units from there to the range's end
 };
 
 // Finds the CTA's range (block-wide; every thread gets it). scratch: 34 long longs of shared
 // memory. Each thread sums a run of entries, a block scan places the runs, and the thread
-// whose run holds the range's first tile looks it up.
-template <int BN, int kThreads>
+// whose run holds the range's first unit looks it up.
+template <int BN, int HEAVY, int kThreads>
 __device__ __forceinline__ Range attn_plan(const Args &a, int cta, int n_ctas, long long *scratch) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int kWarps = kThreads / 32;
@@ -136,8 +145,11 @@ __device__ __forceinline__ Range attn_plan(const Args &a, int cta, int n_ctas, l
     const int per = (E + kThreads - 1) / kThreads;
     const int e0 = min(E, tid * per), e1 = min(E, e0 + per);
     long long sum = 0;
-    int bad = 0;
-    for (int e = e0; e < e1; ++e) sum += (long long)a.Hkv * entry_tiles<BN>(a, e, &bad);
+    int bad = 0, w;
+    for (int e = e0; e < e1; ++e) {
+        const int nt = entry_tiles<BN, HEAVY>(a, e, &w, &bad);
+        sum += (long long)a.Hkv * nt * w;
+    }
     if (bad) atomicOr(a.flags, FLAG_BAD_SEQUENCE);
     long long inc = sum;
 #pragma unroll
@@ -149,34 +161,34 @@ __device__ __forceinline__ Range attn_plan(const Args &a, int cta, int n_ctas, l
     __syncthreads();
     long long before = 0, total = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += scratch[w];
-        total += scratch[w];
+    for (int i = 0; i < kWarps; ++i) {
+        if (i < warp) before += scratch[i];
+        total += scratch[i];
     }
     Range r;
-    r.quota = max((long long)a.min_tiles, (total + n_ctas - 1) / n_ctas);
+    r.quota = max((long long)a.min_units, (total + n_ctas - 1) / n_ctas);
     const long long start = r.quota * cta;
     r.left = max(0ll, min(r.quota, total - start));
-    long long at = before + inc - sum;  // first tile of this thread's run
+    long long at = before + inc - sum;  // first unit of this thread's run
     int *found = reinterpret_cast<int *>(scratch + 28);
     if (r.left > 0 && start >= at && start < at + sum) {
         for (int e = e0; e < e1; ++e) {
-            const int nt = entry_tiles<BN>(a, e);
-            const long long w = (long long)a.Hkv * nt;
-            if (start < at + w) {
+            const int nt = entry_tiles<BN, HEAVY>(a, e, &w);
+            const long long item = (long long)nt * w, all = a.Hkv * item;
+            if (start < at + all) {
                 const long long off = start - at;
                 found[0] = e;
-                found[1] = (int)(off / nt);
-                found[2] = (int)(off % nt);
+                found[1] = (int)(off / item);
+                scratch[30] = off % item;
                 break;
             }
-            at += w;
+            at += all;
         }
     }
     __syncthreads();
     r.e = found[0];
     r.h = found[1];
-    r.t = found[2];
+    r.off = scratch[30];
     return r;
 }
 
@@ -189,33 +201,37 @@ struct Segment {
     bool whole;
 };
 
-// The next segment of a range; r.left > 0. Moves the range past it.
-template <int BN>
-__device__ __forceinline__ Segment next_segment(const Args &a, Range &r) {
-    Segment g;
-    for (;;) {
+// The next segment of a range (false: none is left). Moves the range past it.
+template <int BN, int HEAVY>
+__device__ __forceinline__ bool next_segment(const Args &a, Range &r, Segment &g) {
+    while (r.left > 0) {
         g.b = r.e / a.qblocks;
         g.q0 = (r.e - g.b * a.qblocks) * a.rows;
         g.s = sequence(a, g.b);
         g.rows = min(a.rows, g.s.n * a.G - g.q0);
-        if (g.rows > 0) {
-            g.tl = tiles_of<BN>(a, g.s, g.q0, g.q0 + g.rows);
-            if (g.tl.nt > 0) break;
+        g.tl.nt = 0;
+        if (g.rows > 0) g.tl = tiles_of<BN>(a, g.s, g.q0, g.q0 + g.rows);
+        if (g.tl.nt == 0) {
+            ++r.e;
+            r.h = 0;
+            r.off = 0;
+            continue;
         }
-        ++r.e;
-        r.h = r.t = 0;
+        const int sh = g.rows >= HEAVY ? 1 : 0;  // log2 of the weight
+        const long long item = (long long)g.tl.nt << sh, end = min(item, r.off + r.left);
+        g.h = r.h;
+        g.t = (int)(r.off >> sh);
+        g.count = (int)(end >> sh) - g.t;
+        g.whole = g.t == 0 && g.count == g.tl.nt;
+        r.left -= end - r.off;
+        r.off = 0;
+        if (end == item && ++r.h == a.Hkv) {
+            r.h = 0;
+            ++r.e;
+        }
+        if (g.count > 0) return true;
     }
-    g.h = r.h;
-    g.t = r.t;
-    g.count = (int)min((long long)(g.tl.nt - r.t), r.left);
-    g.whole = g.t == 0 && g.count == g.tl.nt;
-    r.left -= g.count;
-    r.t = 0;
-    if (g.t + g.count == g.tl.nt && ++r.h == a.Hkv) {
-        r.h = 0;
-        ++r.e;
-    }
-    return g;
+    return false;
 }
 
 // A cut item leaves its partial result in slot 0 of a CTA whose range begins inside it and in
@@ -225,16 +241,21 @@ __device__ __forceinline__ size_t part_row(const Args &a, int cta, const Segment
 }
 
 // Record for attn_combine: the item in which this CTA's range begins, if not at its start.
-template <int BN>
+template <int BN, int HEAVY>
 __device__ __forceinline__ void write_record(const Args &a, int cta, const Range &r) {
     int *rec = a.rec + cta * 8;
-    const bool inside = r.left > 0 && r.t > 0;
-    rec[0] = inside ? r.e : -1;
-    if (!inside) return;
+    if (r.left <= 0 || r.off == 0) {
+        rec[0] = -1;
+        return;
+    }
+    int w;
+    const int nt = entry_tiles<BN, HEAVY>(a, r.e, &w);
+    rec[0] = r.off >= w ? r.e : -1;
     rec[1] = r.h;
-    rec[2] = r.t;
-    rec[3] = entry_tiles<BN>(a, r.e);
+    rec[2] = nt;
+    rec[3] = w;
     reinterpret_cast<long long *>(rec)[2] = r.quota;
+    reinterpret_cast<long long *>(rec)[3] = r.off;
 }
 
 // Bits of visible slots among [k0, k0 + 32) for the query node `node`, at position pos.

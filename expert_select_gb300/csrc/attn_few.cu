@@ -22,6 +22,7 @@ namespace {
 constexpr int kBN = 64;     // slots of a tile
 constexpr int kWarps = 4;   // 16 slots each
 constexpr int kThr = 32 * kWarps;
+constexpr int kLight = kFewRows + 1;  // every tile has weight one
 
 template <int DC> struct Shape {
     static constexpr int kRow = DC * 128;           // bytes of a row in shared memory
@@ -66,14 +67,12 @@ struct Cursor {
     __device__ __forceinline__ void start(const Args &a, const Range &range) {
         r = range;
         t = 0;
-        on = r.left > 0;
-        if (on) g = next_segment<kBN>(a, r);
+        on = next_segment<kBN, kLight>(a, r, g);
     }
     __device__ __forceinline__ void step(const Args &a) {
         if (++t < g.count) return;
         t = 0;
-        on = r.left > 0;
-        if (on) g = next_segment<kBN>(a, r);
+        on = next_segment<kBN, kLight>(a, r, g);
     }
 };
 
@@ -86,8 +85,8 @@ __global__ void __launch_bounds__(kThr, 2) attn_few_kernel(const Args a) {
     __shared__ float s_ml[kWarps][2][16];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_wait();
-    const Range range = attn_plan<kBN, kThr>(a, blockIdx.x, gridDim.x, scratch);
-    if (threadIdx.x == 0) write_record<kBN>(a, blockIdx.x, range);
+    const Range range = attn_plan<kBN, kLight, kThr>(a, blockIdx.x, gridDim.x, scratch);
+    if (threadIdx.x == 0) write_record<kBN, kLight>(a, blockIdx.x, range);
     const uint32_t ring = tc::smem_u32(smem) + warp * S::kRing;
     uint8_t *gring = smem + warp * S::kRing;
     float *xch = reinterpret_cast<float *>(smem + kWarps * S::kRing);
@@ -435,7 +434,7 @@ cudaError_t launch_few(Args a, cudaStream_t s) {
     a.rows = kFewRows;
     a.qblocks = (int)(((long long)a.N * a.G + kFewRows - 1) / kFewRows);
     a.prows = (int)std::min<long long>(a.rows, (long long)a.N * a.G);
-    a.min_tiles = 2;
+    a.min_units = 2;
     err = a.dh <= 64 ? launch_dc<1>(a, ctas, s) : launch_dc<2>(a, ctas, s);
     if (err != cudaSuccess) return err;
     return launch_combine(a, MOE_DTYPE_BF16, ctas, s);

@@ -18,6 +18,7 @@ namespace {
 
 constexpr int kBN = 32;
 constexpr int kThr = 128;
+constexpr int kLight = kSimtRows + 1;  // every tile has weight one
 
 // NC: 64-column chunks of the head size (dh <= 64 NC).
 template <int NC> constexpr int simt_smem() {
@@ -41,11 +42,11 @@ __global__ void __launch_bounds__(kThr) attn_simt_kernel(const Args a) {
     float *sQ = sm, *sK = sQ + 32 * LD, *sV = sK + 32 * LD, *sP = sV + 32 * D;  // sP [key][36]
     const int tid = threadIdx.x, tr = tid >> 4, tk = tid & 15;
     pdl_wait();
-    Range r = attn_plan<kBN, kThr>(a, blockIdx.x, gridDim.x, scratch);
-    if (tid == 0) write_record<kBN>(a, blockIdx.x, r);
+    Range r = attn_plan<kBN, kLight, kThr>(a, blockIdx.x, gridDim.x, scratch);
+    if (tid == 0) write_record<kBN, kLight>(a, blockIdx.x, r);
     const T *q = (const T *)a.q, *kp = (const T *)a.k, *vp = (const T *)a.v;
-    while (r.left > 0) {
-        const Segment g = next_segment<kBN>(a, r);
+    Segment g;
+    while (next_segment<kBN, kLight>(a, r, g)) {
         __syncthreads();
         // query rows, scaled so that scores are base-2 logits
         for (int i = tid; i < 32 * (D / 8); i += kThr) {
@@ -232,17 +233,19 @@ __global__ void __launch_bounds__(256) attn_combine_kernel(const Args a) {
     const int *rec = a.rec + c * 8;
     const int e = rec[0];
     if (c == 0 || e < 0) return;
-    const int h = rec[1], t0 = rec[2], nt = rec[3];
+    const int h = rec[1];
+    const long long w_tile = rec[3], units = rec[2] * w_tile;
     const long long quota = reinterpret_cast<const long long *>(rec)[2];
-    if (t0 > quota) return;  // an earlier CTA's range begins inside the item too
+    const long long off = reinterpret_cast<const long long *>(rec)[3];
+    if (off - quota >= w_tile) return;  // an earlier CTA's range begins inside the item too
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = warp % WPR;
     const int b = e / a.qblocks, q0 = (e - b * a.qblocks) * a.rows;
     const Seq s = sequence(a, b);
     const int row = blockIdx.y * (8 / WPR) + warp / WPR;
     const bool live = row < min(a.rows, s.n * a.G - q0);
     if (WPR == 1 && !live) return;
-    // parts: CTA c - 1 (t0 tiles), then as many as the remaining tiles take
-    const int parts = live ? 1 + (int)((nt - t0 + quota - 1) / quota) : 0;
+    // parts: CTA c - 1, then as many as the units from off on take
+    const int parts = live ? 1 + (int)((units - off + quota - 1) / quota) : 0;
     auto part = [&](int i) { return ((size_t)(c - 1 + i) * 2 + (i == 0)) * a.prows + row; };
     float M = -INFINITY;
     for (int i = lane; i < parts; i += 32) {
@@ -354,7 +357,7 @@ cudaError_t launch_simt(Args a, int dtype, cudaStream_t s) {
     a.rows = kSimtRows;
     a.qblocks = (int)(((long long)a.N * a.G + kSimtRows - 1) / kSimtRows);
     a.prows = (int)std::min<long long>(a.rows, (long long)a.N * a.G);
-    a.min_tiles = 4;
+    a.min_units = 4;
     err = dtype == MOE_DTYPE_BF16 ? launch_t<__nv_bfloat16>(a, nsm, &ctas, s)
                                   : launch_t<float>(a, nsm, &ctas, s);
     if (err != cudaSuccess) return err;

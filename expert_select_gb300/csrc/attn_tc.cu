@@ -11,9 +11,9 @@
 // the tensor cores work for one, the CUDA cores exponentiate the other.
 //
 // One CTA per SM, 384 threads:
-//   warp 0       TMA producer: key tiles of 128 slots, K and V alternating, through a ring of
-//                stages; a tile is gathered as boxes of gcd(page size, 128) slots, a lane per box,
-//                each looking its page up
+//   warps 0, 3   TMA producers of K and of V: tiles of 128 slots, each through a ring of stages;
+//                a tile is gathered as boxes of gcd(page size, 128) slots, their pages looked up
+//                a tile ahead (with 16-slot pages one warp spent 1.7 us on a tile's 16 copies)
 //   warp 1       TMEM allocator and MMA issuer (one lane)
 //   warp 2       looks after V: clears what no row may see (see below)
 //   warps 4-7, 8-11  softmax of slot 0 and slot 1: a thread per row, its 128 scores in registers
@@ -28,6 +28,8 @@
 // rows that do see such an element get it back at the end (a slow path that only runs then).
 //
 // Every wait is bounded: after 2 s it sets the check bit and the CTA drains and leaves.
+#include <limits.h>
+
 #include <algorithm>
 
 #include "attn.cuh"
@@ -41,20 +43,19 @@ using namespace tc;
 
 constexpr int kBN = 128;
 constexpr int kThreads = 384;
-constexpr int kVq = 8;           // V-ready barriers in rotation: more than V tiles in the ring
-constexpr int kMaxStages = 6;
+constexpr int kHeavy = 129;      // rows from which an item has two tiles
+constexpr int kMaxStages = 4;    // of K and of V each
 constexpr int kCtlBytes = 2048;
 
 struct Params {
     Args a;
     CUtensorMap kmap, vmap;
-    int box;     // slots of a TMA box: gcd(page size, 128)
-    int stages;
+    int box;  // slots of a TMA box: gcd(page size, 128)
 };
 
 struct Ctl {  // control block in shared memory; barriers first
-    uint64_t full[kMaxStages], empty[kMaxStages], vready[kVq], s_full[2], p_full[2], o_done[2],
-        q_full, done;
+    uint64_t kfull[kMaxStages], kempty[kMaxStages], vfull[kMaxStages], vempty[kMaxStages],
+        vready[kMaxStages], s_full[2], p_half[2], p_full[2], o_done[2], q_full, done;
     long long scratch[34];
     uint32_t tmem;
     volatile int abort;
@@ -69,17 +70,70 @@ __device__ __forceinline__ void softmax_bar() {  // the 256 threads of warps 4-1
     asm volatile("bar.sync 1, 256;" ::: "memory");
 }
 
-// Positions of K and V tiles of a segment of n tiles in the ring's order: LA K tiles first, then
-// V(t), K(t + LA) in turn.
-__device__ __forceinline__ int k_pos(int t, int la) { return t < la ? t : 2 * t - la + 1; }
-__device__ __forceinline__ int v_pos(int t, int la, int n) { return t + min(t + la, n); }
+// Pairs of fp32 values, two to an instruction.
+__device__ __forceinline__ void pack2(uint64_t &d, float lo, float hi) {
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(x), "l"(y), "l"(z));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+    return d;
+}
 
-struct Ring {
-    uint32_t base;  // ring position of the segment's first tile
-    int stages;
-    __device__ __forceinline__ int stage(uint32_t pos) const { return (int)(pos % stages); }
-    __device__ __forceinline__ uint32_t parity(uint32_t pos) const { return (pos / stages) & 1u; }
+// Position of a tile in the ring of K (or V) stages: counts up over the CTA's segments.
+template <int NS> struct Slot {
+    static __device__ __forceinline__ int stage(uint32_t pos) { return (int)(pos % NS); }
+    static __device__ __forceinline__ uint32_t parity(uint32_t pos) { return (pos / NS) & 1u; }
 };
+
+// Adds the non-finite elements of V that a row sees to its O (slow; only where a masked tile held
+// some, which took no part in the products).
+__device__ __forceinline__ void give_back(const Args &a, const Segment &g, int node, int pos, int n,
+                                       int chunks, uint32_t tO) {
+    for (int x = 0; x < chunks; ++x) {
+        uint32_t o[32];
+        tmem_ld32(tO + x * 32u, o);
+        for (int t = 0; t < n; ++t) {
+            const int k0 = g.tl.at(g.t + t) * kBN;
+            uint32_t bits[4];
+            visible_bits<4>(a, g.s, node, pos, k0, bits);
+#pragma unroll 1
+            for (int j = 0; j < kBN; ++j) {
+                const uint32_t wb = j < 64 ? (j < 32 ? bits[0] : bits[1])
+                                           : (j < 96 ? bits[2] : bits[3]);
+                if (!((wb >> (j & 31)) & 1u)) continue;
+                const int pg = page_of(a, g.b, k0 + j);
+                if (pg < 0) continue;
+                const __nv_bfloat16 *vr = (const __nv_bfloat16 *)a.v + (size_t)pg * a.st_page +
+                                          (size_t)((k0 + j) % a.page) * a.st_tok +
+                                          (size_t)g.h * a.st_head;
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (x * 32 + i < a.dh) {
+                        const float e = __bfloat162float(vr[x * 32 + i]);
+                        const float v = __uint_as_float(o[i]);
+                        if (!isfinite(e)) o[i] = __float_as_uint(isfinite(v) ? e : v + e);
+                    }
+            }
+        }
+        __syncwarp();
+        tmem_st32(tO + x * 32u, o);
+        tmem_wait_st();
+    }
+}
+
+// Stages of K and of V each that fit beside the query tiles.
+template <int DC> constexpr int stages() {
+    return std::min(kMaxStages, ((227 * 1024 - 1024 - kCtlBytes) / (DC * 16384) - 2) / 2);
+}
 
 template <int DC>  // 64-column chunks of the head size
 __global__ void __launch_bounds__(kThreads, 1)
@@ -90,24 +144,29 @@ attn_tc_kernel(const __grid_constant__ Params p) {
     uint8_t *gbase = smem_raw + (base - raw);
     Ctl &c = *reinterpret_cast<Ctl *>(gbase);
     constexpr uint32_t kTile = DC * 16384u;  // 128 rows x 64 DC bf16
-    const uint32_t sQ = base + kCtlBytes, sRing = sQ + 2 * kTile;
-    uint8_t *gQ = gbase + kCtlBytes, *gRing = gQ + 2 * kTile;
+    constexpr int NS = stages<DC>();
+    using Ring = Slot<NS>;
+    const uint32_t sQ = base + kCtlBytes, sK = sQ + 2 * kTile, sV = sK + NS * kTile;
+    uint8_t *gQ = gbase + kCtlBytes, *gV = gQ + (2 + NS) * kTile;
     const Args &a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     auto bar = [&](uint64_t &b) { return smem_u32(&b); };
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kMaxStages; ++s) {
-            mbar_init(bar(c.full[s]), 1);
-            mbar_init(bar(c.empty[s]), 1);
+            mbar_init(bar(c.kfull[s]), 1);
+            mbar_init(bar(c.kempty[s]), 1);
+            mbar_init(bar(c.vfull[s]), 1);
+            mbar_init(bar(c.vempty[s]), 1);
+            mbar_init(bar(c.vready[s]), 1);
         }
-        for (int i = 0; i < kVq; ++i) mbar_init(bar(c.vready[i]), 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(c.s_full[i]), 1);
-            mbar_init(bar(c.p_full[i]), 128);
+            mbar_init(bar(c.p_half[i]), 4);  // a lane of each warp
+            mbar_init(bar(c.p_full[i]), 4);
             mbar_init(bar(c.o_done[i]), 1);
         }
-        mbar_init(bar(c.q_full), 256);
+        mbar_init(bar(c.q_full), 8);
         mbar_init(bar(c.done), 1);
         c.abort = c.bad_page = c.bad_v = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -126,176 +185,195 @@ attn_tc_kernel(const __grid_constant__ Params p) {
     tc_fence_after();
     pdl_wait();
     const uint32_t tmem = c.tmem;
-    Range r = attn_plan<kBN, kThreads>(a, blockIdx.x, gridDim.x, c.scratch);
-    if (threadIdx.x == 96) write_record<kBN>(a, blockIdx.x, r);
-    Ring ring{0, p.stages};
+    Range r = attn_plan<kBN, kHeavy, kThreads>(a, blockIdx.x, gridDim.x, c.scratch);
+    if (threadIdx.x == 64) write_record<kBN, kHeavy>(a, blockIdx.x, r);
 
     uint32_t issued = 0, last_par = 0;  // producer: stages with a load issued, parity of the last
     bool mma_issued = false;
 
-    if (warp == 0) {
-        // ------------------------------------------------------------- producer
+    if (warp == 0 || warp == 3) {
+        // -------------------------------------- producers: warp 0 of K, warp 3 of V
+        const bool is_k = warp == 0;
+        const CUtensorMap *map = is_k ? &p.kmap : &p.vmap;
+        uint64_t *full = is_k ? c.kfull : c.vfull, *empty = is_k ? c.kempty : c.vempty;
+        uint32_t rp = 0;
         bool ok = true;
-        while (ok && r.left > 0) {
-            const Segment g = next_segment<kBN>(a, r);
-            const int la = g.rows > 128 ? 1 : 2, n = g.count;
-            for (int pos = 0, kt = 0, vt = 0; ok && pos < 2 * n; ++pos) {
-                const bool is_k = kt < n && kt < vt + la;
-                const int t = is_k ? kt++ : vt++;
+        Segment g;
+        while (ok && next_segment<kBN, kHeavy>(a, r, g)) {
+            const int n = __shfl_sync(0xffffffffu, g.count, 0);
+            int pg[4], next[4];  // pages of the tile's boxes (at most 128), lane by lane
+            auto look_up = [&](int t, int (&out)[4]) {
                 const int k0 = g.tl.at(g.t + t) * kBN;
-                const uint32_t rp = ring.base + pos;
-                const int st = ring.stage(rp);
-                const int boxes = (min(kBN, g.s.L - k0) + p.box - 1) / p.box;
-                int pg[4], good = 0;  // kBN / box <= 128 boxes, lane by lane
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int bx = lane + 32 * i;
-                    pg[i] = bx < boxes ? page_of(a, g.b, k0 + bx * p.box) : -1;
-                    good += __popc(__ballot_sync(0xffffffffu, pg[i] >= 0));
+                    const int j = k0 + (lane + 32 * i) * p.box;
+                    out[i] = lane + 32 * i < kBN / p.box && j < g.s.L
+                                 ? a.table[(size_t)g.b * a.max_pages + j / a.page]
+                                 : INT_MIN;
                 }
-                if (good < boxes && lane == 0) {
-                    c.bad_page = 1;
-                    __threadfence_block();
-                    atomicOr(a.flags, FLAG_BAD_PAGE);
+            };
+            look_up(0, next);
+            for (int t = 0; ok && t < n; ++t, ++rp) {
+                const int k0 = __shfl_sync(0xffffffffu, g.tl.at(g.t + t) * kBN, 0);
+                const int st = Ring::stage(rp);
+                int good = 0, bad = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    pg[i] = next[i];
+                    const bool in = pg[i] >= 0 && pg[i] < a.n_pages;
+                    good += __popc(__ballot_sync(0xffffffffu, in));
+                    bad |= !in && pg[i] != INT_MIN;
+                    if (!in) pg[i] = -1;
                 }
-                ok = mbar_wait(bar(c.empty[st]), ring.parity(rp) ^ 1u, &c.abort, a.flags);
-                ok = __all_sync(0xffffffffu, ok);
+                if (t + 1 < n) look_up(t + 1, next);  // in flight while this tile is copied
+                if (__any_sync(0xffffffffu, bad)) {
+                    if (lane == 0) {
+                        c.bad_page = 1;
+                        __threadfence_block();
+                        atomicOr(a.flags, FLAG_BAD_PAGE);
+                    }
+                    __syncwarp();
+                }
+                ok = __all_sync(0xffffffffu,
+                                mbar_wait(bar(empty[st]), Ring::parity(rp) ^ 1u, &c.abort, a.flags));
                 if (!ok) break;
-                const uint32_t fb = bar(c.full[st]);
+                const uint32_t fb = bar(full[st]);
                 if (lane == 0) mbar_expect_tx(fb, (uint32_t)good * p.box * 128u * DC);
                 __syncwarp();
-                const CUtensorMap *map = is_k ? &p.kmap : &p.vmap;
-                const uint32_t dst = sRing + (uint32_t)st * kTile;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (pg[i] >= 0) {
-                        const int j = k0 + (lane + 32 * i) * p.box;
+                const uint32_t dst = (is_k ? sK : sV) + (uint32_t)st * kTile;
+                const int boxes = (min(kBN, g.s.L - k0) + p.box - 1) / p.box;
+                int in_page = k0 % a.page;
+                for (int x = 0; x < boxes; ++x) {
+                    const int lo = x & 31, hi = x >> 5;
+                    const int mine = hi == 0 ? pg[0] : (hi == 1 ? pg[1] : (hi == 2 ? pg[2] : pg[3]));
+                    const int page = __shfl_sync(0xffffffffu, mine, lo);
+                    if (page >= 0) {
 #pragma unroll
                         for (int h = 0; h < DC; ++h)
-                            tma_load_4d(dst + h * 16384u + (uint32_t)(lane + 32 * i) * p.box * 128u,
-                                        map, h * 64, j % a.page, g.h, pg[i], fb);
+                            tma_load_4d_elect(dst + h * 16384u + (uint32_t)x * p.box * 128u, map,
+                                              h * 64, in_page, g.h, page, fb);
                     }
+                    in_page += p.box;
+                    if (in_page >= a.page) in_page = 0;
+                }
                 issued |= 1u << st;
-                last_par = (last_par & ~(1u << st)) | (ring.parity(rp) << st);
-                __syncwarp();
+                last_par = (last_par & ~(1u << st)) | (Ring::parity(rp) << st);
             }
-            ring.base += 2 * n;
         }
+        __syncwarp();
     } else if (warp == 1) {
         // ----------------------------------------------------------- MMA issuer
-        if (lane == 0) {
-            const uint32_t id_s = idesc_bf16(128, 128), id_o = idesc_bf16(128, 64 * DC) | kIdescBMn;
-            uint32_t pcount[2] = {0, 0}, vcount = 0, seg = 0;
-            bool ok = true;
-            auto wait = [&](uint64_t &b, uint32_t par) {
-                if (ok) ok = mbar_wait(bar(b), par, &c.abort, a.flags);
-                tc_fence_after();
-                return ok;
+        const uint32_t id_s = idesc_bf16(128, 128), id_o = idesc_bf16(128, 64 * DC) | kIdescBMn;
+        uint32_t pcount[2] = {0, 0}, kpos = 0, vpos = 0, seg = 0;  // kpos, vpos: of the segment's
+        bool ok = true;
+        auto wait = [&](uint64_t &b, uint32_t par) {
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(b), par, &c.abort, a.flags));
+            tc_fence_after();
+            return ok;
+        };
+        Segment g;
+        while (ok && next_segment<kBN, kHeavy>(a, r, g)) {
+            const bool two = __shfl_sync(0xffffffffu, g.rows, 0) > 128;
+            const int n = __shfl_sync(0xffffffffu, g.count, 0);
+            auto score = [&](int slot, int t) {  // S of a slot from K tile t
+                const uint32_t k = sw128_lo(sK + (uint32_t)Ring::stage(kpos + t) * kTile, 16);
+                const uint32_t q = sw128_lo(sQ + (two ? (uint32_t)slot * kTile : 0u), 16);
+#pragma unroll
+                for (int x = 0; x < 4 * DC; ++x) {
+                    const uint32_t off = ((x >> 2) * 16384u + (x & 3) * 32u) >> 4;
+                    mma_ss_elect(tmem + slot * 128u, q + off, k + off, id_s, x != 0);
+                }
+                mma_issued = true;
+                commit_elect(bar(c.s_full[slot]));
             };
-            while (ok && r.left > 0) {
-                const Segment g = next_segment<kBN>(a, r);
-                const bool two = g.rows > 128;
-                const int la = two ? 1 : 2, n = g.count;
-                auto score = [&](int slot, int t) {  // S of a slot from K tile t
-                    const uint32_t k = sRing + (uint32_t)ring.stage(ring.base + k_pos(t, la)) * kTile;
-                    const uint32_t q = sQ + (two ? (uint32_t)slot * kTile : 0u);
+            auto wait_k = [&](int t) {
+                return wait(c.kfull[Ring::stage(kpos + t)], Ring::parity(kpos + t));
+            };
+            auto free_k = [&](int t) {
+                commit_elect(bar(c.kempty[Ring::stage(kpos + t)]));
+            };
+            // O += P V tile t, the first 64 keys while the others are still exponentiated
+            auto output = [&](int slot, int t, bool first) {
+                const uint32_t v = sw128_lo(sV + (uint32_t)Ring::stage(vpos + t) * kTile, 16384);
+                const uint32_t par = pcount[slot]++ & 1u;
+                if (!wait(c.p_half[slot], par)) return false;
 #pragma unroll
-                    for (int x = 0; x < 4 * DC; ++x) {
-                        const uint32_t off = (x >> 2) * 16384u + (x & 3) * 32u;
-                        mma_bf16(tmem + slot * 128u, sw128_desc(q + off), sw128_desc(k + off), id_s,
-                                 x != 0);
-                    }
-                    mma_issued = true;
-                    mma_commit(bar(c.s_full[slot]));
-                };
-                auto wait_k = [&](int t) {
-                    const uint32_t rp = ring.base + k_pos(t, la);
-                    return wait(c.full[ring.stage(rp)], ring.parity(rp));
-                };
-                auto free_k = [&](int t) {
-                    mma_commit(bar(c.empty[ring.stage(ring.base + k_pos(t, la))]));
-                };
-                auto output = [&](int slot, int t, bool first) {  // O += P V tile t
-                    const uint32_t v =
-                        sRing + (uint32_t)ring.stage(ring.base + v_pos(t, la, n)) * kTile;
+                for (int x = 0; x < 4; ++x)
+                    mma_ts_elect(tmem + 256u + slot * 128u, tmem + slot * 128u + x * 8u,
+                                 v + x * (2048u >> 4), id_o, !first || x != 0);
+                if (!wait(c.p_full[slot], par)) return false;
 #pragma unroll
-                    for (int x = 0; x < 8; ++x)
-                        mma_bf16_ts(tmem + 256u + slot * 128u, tmem + slot * 128u + x * 8u,
-                                    sw128_mn_desc(v + x * 2048u, 16384u), id_o, !first || x != 0);
-                };
-                auto wait_p = [&](int slot) { return wait(c.p_full[slot], pcount[slot]++ & 1u); };
-                auto wait_v = [&]() {
-                    const bool w = wait(c.vready[vcount % kVq], (vcount / kVq) & 1u);
-                    ++vcount;
-                    return w;
-                };
-                auto free_v = [&](int t) {
-                    mma_commit(bar(c.empty[ring.stage(ring.base + v_pos(t, la, n))]));
-                };
-                if (!wait(c.q_full, seg++ & 1u)) break;
-                if (two) {
-                    if (!wait_k(0)) break;
-                    score(0, 0);
-                    score(1, 0);
-                    free_k(0);
-                    for (int t = 0; ok && t < n; ++t) {
-                        const bool more = t + 1 < n;
-                        if (!wait_v() || !wait_p(0)) break;
-                        output(0, t, t == 0);
-                        if (more) {
-                            if (!wait_k(t + 1)) break;
-                            score(0, t + 1);
-                        } else {
-                            mma_commit(bar(c.o_done[0]));
-                        }
-                        if (!wait_p(1)) break;
-                        output(1, t, t == 0);
-                        free_v(t);
-                        if (more) {
-                            score(1, t + 1);
-                            free_k(t + 1);
-                        } else {
-                            mma_commit(bar(c.o_done[1]));
-                        }
+                for (int x = 4; x < 8; ++x)
+                    mma_ts_elect(tmem + 256u + slot * 128u, tmem + slot * 128u + x * 8u,
+                                 v + x * (2048u >> 4), id_o, 1u);
+                return true;
+            };
+            auto wait_v = [&](int t) {
+                return wait(c.vready[Ring::stage(vpos + t)], Ring::parity(vpos + t));
+            };
+            auto free_v = [&](int t) {
+                commit_elect(bar(c.vempty[Ring::stage(vpos + t)]));
+            };
+            if (!wait(c.q_full, seg++ & 1u)) break;
+            if (two) {
+                if (!wait_k(0)) break;
+                score(0, 0);
+                score(1, 0);
+                free_k(0);
+                for (int t = 0; ok && t < n; ++t) {
+                    const bool more = t + 1 < n;
+                    if (!wait_v(t) || !output(0, t, t == 0)) break;
+                    if (more) {
+                        if (!wait_k(t + 1)) break;
+                        score(0, t + 1);
+                    } else {
+                        commit_elect(bar(c.o_done[0]));
                     }
-                } else {
-                    for (int t = 0; t < min(n, 2); ++t) {
-                        if (!wait_k(t)) break;
-                        score(t, t);
-                        free_k(t);
-                    }
-                    for (int t = 0; ok && t < n; ++t) {
-                        const int slot = t & 1;
-                        if (!wait_v() || !wait_p(slot)) break;
-                        output(slot, t, t < 2);
-                        free_v(t);
-                        if (t + 2 < n) {
-                            if (!wait_k(t + 2)) break;
-                            score(slot, t + 2);
-                            free_k(t + 2);
-                        } else {
-                            mma_commit(bar(c.o_done[slot]));
-                        }
+                    if (!output(1, t, t == 0)) break;
+                    free_v(t);
+                    if (more) {
+                        score(1, t + 1);
+                        free_k(t + 1);
+                    } else {
+                        commit_elect(bar(c.o_done[1]));
                     }
                 }
-                ring.base += 2 * n;
+            } else {
+                for (int t = 0; t < min(n, 2); ++t) {
+                    if (!wait_k(t)) break;
+                    score(t, t);
+                    free_k(t);
+                }
+                for (int t = 0; ok && t < n; ++t) {
+                    const int slot = t & 1;
+                    if (!wait_v(t) || !output(slot, t, t < 2)) break;
+                    free_v(t);
+                    if (t + 2 < n) {
+                        if (!wait_k(t + 2)) break;
+                        score(slot, t + 2);
+                        free_k(t + 2);
+                    } else {
+                        commit_elect(bar(c.o_done[slot]));
+                    }
+                }
             }
+            kpos += n;
+            vpos += n;
         }
         __syncwarp();
     } else if (warp == 2) {
         // -------------------------------------------------------- keeper of V
-        uint32_t vcount = 0;
+        uint32_t rp = 0;
         bool ok = true;
-        while (ok && r.left > 0) {
-            const Segment g = next_segment<kBN>(a, r);
-            const int la = g.rows > 128 ? 1 : 2, n = g.count;
+        Segment g;
+        while (ok && next_segment<kBN, kHeavy>(a, r, g)) {
+            const int n = g.count;
             const int i0 = g.q0 / a.G, i1 = (g.q0 + g.rows - 1) / a.G;
             const int pos = i0 == i1 ? node_position(a, g.s, i0) : 0;
-            for (int t = 0; ok && t < n; ++t) {
-                const uint32_t rp = ring.base + v_pos(t, la, n);
-                const int st = ring.stage(rp);
-                ok = __all_sync(0xffffffffu,
-                                mbar_wait(bar(c.full[st]), ring.parity(rp), &c.abort, a.flags));
+            for (int t = 0; ok && t < n; ++t, ++rp) {
+                const int st = Ring::stage(rp);
+                ok = __all_sync(0xffffffffu, mbar_wait(bar(c.vfull[st]), Ring::parity(rp), &c.abort,
+                                                       a.flags));
                 if (!ok) break;
                 const int k0 = g.tl.at(g.t + t) * kBN;
                 if (c.bad_page || tile_masked<kBN>(a, g.s, i0, i1, k0)) {
@@ -308,7 +386,7 @@ attn_tc_kernel(const __grid_constant__ Params p) {
 #pragma unroll
                         for (int w = 0; w < 4; ++w) bits[w] = range_bits(0, g.s.L, k0 + 32 * w);
                     }
-                    uint8_t *tile = gRing + (size_t)st * kTile;
+                    uint8_t *tile = gV + (size_t)st * kTile;
 #pragma unroll 1
                     for (int w = 0; w < 4; ++w) {
                         const int row = 32 * w + lane;
@@ -347,10 +425,8 @@ attn_tc_kernel(const __grid_constant__ Params p) {
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                 }
-                if (lane == 0) mbar_arrive(bar(c.vready[vcount % kVq]));
-                ++vcount;
+                if (lane == 0) mbar_arrive(bar(c.vready[st]));
             }
-            ring.base += 2 * n;
         }
     } else if (warp >= 4) {
         // -------------------------------------------------------------- softmax
@@ -363,29 +439,42 @@ attn_tc_kernel(const __grid_constant__ Params p) {
         const uint32_t tS = tmem + slot * 128u + lanes, tO = tmem + 256u + slot * 128u + lanes;
         uint32_t scount = 0, ocount = 0;
         bool dead = false;
-        while (r.left > 0) {
-            const Segment g = next_segment<kBN>(a, r);
+        Segment g;
+        while (next_segment<kBN, kHeavy>(a, r, g)) {
             const bool two = g.rows > 128;
             const int n = g.count;
             softmax_bar();  // the last segment's tiles and exchange buffer are done with
             {
-                const int rows = two ? 256 : 128;
-                const __nv_bfloat16 *q = (const __nv_bfloat16 *)a.q;
-                for (int i = tid; i < rows * 8 * DC; i += 256) {
-                    const int row = i / (8 * DC), ch = i % (8 * DC);
-                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                    if (row < g.rows && ch * 8 < a.dh) {
-                        const int qr = g.q0 + row, node = qr / a.G;
-                        v = __ldg(reinterpret_cast<const uint4 *>(
-                            q + (size_t)(g.s.row0 + node) * a.ldq +
-                            (size_t)(g.h * a.G + qr - node * a.G) * a.dh + ch * 8));
+                // 8 DC pieces of 16 B a row; a thread keeps its piece and takes every
+                // (256 / (8 DC))th row, up to sixteen rows' loads in flight at a time
+                constexpr int kStep = 256 / (8 * DC);
+                const int rows = two ? 256 : 128, ch = tid % (8 * DC), first = tid / (8 * DC);
+                const __nv_bfloat16 *q = (const __nv_bfloat16 *)a.q + (size_t)g.s.row0 * a.ldq +
+                                         (size_t)g.h * a.G * a.dh + ch * 8;
+                for (int y = first; y < rows; y += 16 * kStep) {
+                    uint4 v[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int row = y + i * kStep;
+                        v[i] = make_uint4(0u, 0u, 0u, 0u);
+                        if (row < g.rows && ch * 8 < a.dh) {
+                            const int qr = g.q0 + row, node = qr / a.G;
+                            v[i] = __ldg(reinterpret_cast<const uint4 *>(
+                                q + (size_t)node * a.ldq + (size_t)(qr - node * a.G) * a.dh));
+                        }
                     }
-                    const int rr = row & 127;
-                    *reinterpret_cast<uint4 *>(gQ + (row >> 7) * kTile + (ch >> 3) * 16384 +
-                                               rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)) = v;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int row = y + i * kStep, rr = row & 127;
+                        if (row < rows)
+                            *reinterpret_cast<uint4 *>(gQ + (row >> 7) * kTile + (ch >> 3) * 16384 +
+                                                       rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)) =
+                                v[i];
+                    }
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                mbar_arrive(bar(c.q_full));
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(c.q_full));
             }
             const int row = two ? slot * 128 + trow : trow;  // row of the item
             const bool active = row - lane < g.rows;         // the warp has rows
@@ -405,7 +494,8 @@ attn_tc_kernel(const __grid_constant__ Params p) {
                 tc_fence_after();
                 if (active && !__any_sync(0xffffffffu, dead)) {
                     uint32_t s[128];
-                    tmem_ld128(tS, s);
+                    tmem_ld64(tS, s);
+                    tmem_ld64(tS + 64u, s + 64);
                     if (tile_masked<kBN>(a, g.s, i0, i1, k0) || c.bad_page) {
                         uint32_t bits[4];
                         visible_bits<4>(a, g.s, node, pos, k0, bits);
@@ -424,9 +514,14 @@ attn_tc_kernel(const __grid_constant__ Params p) {
                     }
                     float mx[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(s[i]);
+                    for (int i = 0; i < 4; ++i)
+                        mx[i] = fmaxf(__uint_as_float(s[i]), __uint_as_float(s[i + 4]));
 #pragma unroll
-                    for (int i = 4; i < 128; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i]));
+                    for (int i = 8; i < 128; i += 8)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)  // three-operand maxima
+                            mx[x] = fmaxf(fmaxf(mx[x], __uint_as_float(s[i + x])),
+                                          __uint_as_float(s[i + x + 4]));
                     const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                     const bool raise = (top - m) * cs > kRaise;  // m = -inf: yes, unless top is too
                     if (__any_sync(0xffffffffu, raise)) {
@@ -444,30 +539,46 @@ attn_tc_kernel(const __grid_constant__ Params p) {
                                     o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
                                 tmem_st32(tO + x * 32u, o);
                             }
-                            tmem_wait_st();
                         }
                     }
-                    const float sub = m == -INFINITY ? 0.f : m * cs;
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    const float sub = m == -INFINITY ? 0.f : -m * cs;
+                    uint64_t cs2, sub2, sum[2] = {0ull, 0ull};
+                    pack2(cs2, cs, cs);
+                    pack2(sub2, sub, sub);
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         uint32_t pk[32];
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
-                            const int j = x * 64 + 2 * i;
-                            const float p0 = ex2(fmaf(__uint_as_float(s[j]), cs, -sub));
-                            const float p1 = ex2(fmaf(__uint_as_float(s[j + 1]), cs, -sub));
-                            sum[(2 * i) & 3] += p0;
-                            sum[(2 * i + 1) & 3] += p1;
+                            uint64_t t2;
+                            float p0, p1;
+                            pack2(t2, __uint_as_float(s[x * 64 + 2 * i]),
+                                  __uint_as_float(s[x * 64 + 2 * i + 1]));
+                            t2 = fma2(t2, cs2, sub2);
+                            unpack2(t2, p0, p1);
+                            p0 = ex2(p0);
+                            p1 = ex2(p1);
+                            pack2(t2, p0, p1);
+                            sum[i & 1] = add2(sum[i & 1], t2);
                             pk[i] = pack_bf16(p0, p1);
                         }
                         tmem_st32(tS + x * 32u, pk);
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(x ? c.p_full[slot] : c.p_half[slot]));
                     }
-                    tmem_wait_st();
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    float s0, s1;
+                    unpack2(add2(sum[0], sum[1]), s0, s1);
+                    l += s0 + s1;
+                } else {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(bar(c.p_half[slot]));
+                        mbar_arrive(bar(c.p_full[slot]));
+                    }
                 }
-                tc_fence_before();
-                mbar_arrive(bar(c.p_full[slot]));
             }
             if (tiles > 0) {
                 if (!mbar_wait(bar(c.o_done[slot]), ocount & 1u, &c.abort, a.flags)) dead = true;
@@ -515,72 +626,65 @@ attn_tc_kernel(const __grid_constant__ Params p) {
             const size_t orow = (size_t)(g.s.row0 + node) * a.H + head;
             float fin = 1.f;
             const bool mine = row < g.rows;
-            const size_t prow = g.whole ? 0 : part_row(a, blockIdx.x, g, rr);
             if (g.whole) {
                 float lse;
                 fin = finish(m2, l, a.sink, head, &lse);
                 if (mine && a.lse) a.lse[orow] = lse;
             } else if (mine) {
-                a.part_ml[prow * 2] = m2;
-                a.part_ml[prow * 2 + 1] = l;
+                *reinterpret_cast<float2 *>(a.part_ml + part_row(a, blockIdx.x, g, row) * 2) =
+                    make_float2(m2, l);
             }
-            const bool fix = c.bad_v != 0;
+            if (c.bad_v) {
+                give_back(a, g, node, pos, n, 2 * DC, tO);
+                f0 = fmaxf(f0, 1e-37f);  // what was given back must not vanish in the merge
+            }
+            const int first = row - lane, left = min(32, g.rows - first);
+            // a row's columns are in one thread: turn the warp's 32 x 32 blocks around in shared
+            // memory (the query tile of this slot, or the exchange words that this warp has just
+            // read), so that each store covers whole sectors of few rows
 #pragma unroll 1
             for (int x = 0; x < 2 * DC; ++x) {
                 uint32_t o[32];
                 tmem_ld32(tO + x * 32u, o);
-                float v[32];
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(o[i]);
                 if (merge) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        v[i] = v[i] * f0 + xch[(x * 32 + i) * 128 + trow] * f1;
+                        o[i] = __float_as_uint(__uint_as_float(o[i]) * f0 +
+                                               xch[(x * 32 + i) * 128 + trow] * f1);
                 }
-                if (fix) {
-                    // give back the non-finite elements of V that this row sees
-                    for (int t = 0; t < n; ++t) {
-                        const int k0 = g.tl.at(g.t + t) * kBN;
-                        uint32_t bits[4];
-                        visible_bits<4>(a, g.s, node, pos, k0, bits);
-#pragma unroll 1
-                        for (int j = 0; j < kBN; ++j) {
-                            const uint32_t wb = j < 64 ? (j < 32 ? bits[0] : bits[1])
-                                                       : (j < 96 ? bits[2] : bits[3]);
-                            if (!((wb >> (j & 31)) & 1u)) continue;
-                            const int pg = page_of(a, g.b, k0 + j);
-                            if (pg < 0) continue;
-                            const __nv_bfloat16 *vr =
-                                (const __nv_bfloat16 *)a.v + (size_t)pg * a.st_page +
-                                (size_t)((k0 + j) % a.page) * a.st_tok + (size_t)g.h * a.st_head;
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (x * 32 + i < a.dh) {
-                                    const float e = __bfloat162float(vr[x * 32 + i]);
-                                    if (!isfinite(e) && isfinite(v[i])) v[i] = e;
-                                    else if (!isfinite(e)) v[i] += e;
-                                }
-                        }
-                    }
-                }
-                if (!mine) continue;
+                uint32_t *turn = reinterpret_cast<uint32_t *>(
+                                     gQ + (two ? slot * kTile : (merge ? x * 16384u : 0u))) +
+                                 quad * 32;
+                __syncwarp();
                 if (g.whole) {
-                    __nv_bfloat16 *out = (__nv_bfloat16 *)a.out + orow * a.dh + x * 32;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (x * 32 + i * 8 < a.dh)
-                            *reinterpret_cast<uint4 *>(out + i * 8) = make_uint4(
-                                pack_bf16(v[i * 8] * fin, v[i * 8 + 1] * fin),
-                                pack_bf16(v[i * 8 + 2] * fin, v[i * 8 + 3] * fin),
-                                pack_bf16(v[i * 8 + 4] * fin, v[i * 8 + 5] * fin),
-                                pack_bf16(v[i * 8 + 6] * fin, v[i * 8 + 7] * fin));
+                    for (int i = 0; i < 16; ++i)
+                        turn[i * 128 + (lane ^ i)] = pack_bf16(__uint_as_float(o[2 * i]) * fin,
+                                                               __uint_as_float(o[2 * i + 1]) * fin);
+                    __syncwarp();
+                    const int i = lane & 15, hf = lane & 16;
+#pragma unroll
+                    for (int y = 0; y < 16; ++y) o[y] = turn[i * 128 + ((y | hf) ^ i)];
+                    const bool col = x * 32 + 2 * i < a.dh;
+#pragma unroll
+                    for (int y = 0; y < 16; ++y) {
+                        const long long at = __shfl_sync(0xffffffffu, (long long)orow, y | hf);
+                        if ((y | hf) < left && col)
+                            reinterpret_cast<uint32_t *>((__nv_bfloat16 *)a.out + at * a.dh +
+                                                         x * 32)[i] = o[y];
+                    }
                 } else {
-                    float *out = a.part_o + prow * a.dh + x * 32;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (x * 32 + i * 4 < a.dh)
-                            *reinterpret_cast<float4 *>(out + i * 4) =
-                                make_float4(v[i * 4], v[i * 4 + 1], v[i * 4 + 2], v[i * 4 + 3]);
+                    for (int i = 0; i < 32; ++i) turn[i * 128 + (lane ^ i)] = o[i];
+                    __syncwarp();
+#pragma unroll
+                    for (int y = 0; y < 32; ++y) o[y] = turn[lane * 128 + (y ^ lane)];
+                    float *dst =
+                        a.part_o + part_row(a, blockIdx.x, g, first) * a.dh + x * 32 + lane;
+                    const bool col = x * 32 + lane < a.dh;
+#pragma unroll
+                    for (int y = 0; y < 32; ++y)
+                        if (y < left && col) dst[(size_t)y * a.dh] = __uint_as_float(o[y]);
                 }
             }
             tc_fence_before();
@@ -589,12 +693,13 @@ attn_tc_kernel(const __grid_constant__ Params p) {
 
     // ---- nothing may be in flight when the CTA frees its tensor memory and leaves ----
     __syncthreads();
-    if (warp == 0 && lane == 0)
-        for (int s = 0; s < p.stages; ++s)
+    if ((warp == 0 || warp == 3) && lane == 0)
+        for (int s = 0; s < NS; ++s)
             if (issued & (1u << s))
-                mbar_wait(bar(c.full[s]), (last_par >> s) & 1u, nullptr, a.flags);
-    if (warp == 1 && lane == 0 && mma_issued) {
-        mma_commit(bar(c.done));
+                mbar_wait(bar(warp == 0 ? c.kfull[s] : c.vfull[s]), (last_par >> s) & 1u, nullptr,
+                          a.flags);
+    if (warp == 1 && mma_issued) {
+        commit_elect(bar(c.done));
         mbar_wait(bar(c.done), 0, nullptr, a.flags);
     }
     __syncwarp();
@@ -621,10 +726,7 @@ bool encode_pool(CUtensorMap *m, const void *base, const Args &a, int box) {
 }
 
 template <int DC> cudaError_t launch_dc(Params &p, int ctas, cudaStream_t s) {
-    constexpr int kTile = DC * 16384;
-    constexpr int budget = 227 * 1024 - 1024 - kCtlBytes;  // less the alignment slack
-    p.stages = std::min(kMaxStages, budget / kTile - 2);
-    const int smem = 1024 + kCtlBytes + (p.stages + 2) * kTile;
+    constexpr int smem = 1024 + kCtlBytes + (2 * stages<DC>() + 2) * DC * 16384;
     const cudaError_t err = cudaFuncSetAttribute(
         attn_tc_kernel<DC>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess) return err;
@@ -652,7 +754,7 @@ cudaError_t launch_tc(Args a, cudaStream_t s) {
     a.rows = kTcRows;
     a.qblocks = (int)(((long long)a.N * a.G + kTcRows - 1) / kTcRows);
     a.prows = (int)std::min<long long>(a.rows, (long long)a.N * a.G);
-    a.min_tiles = 2;
+    a.min_units = 4;
     Params p{};
     p.a = a;
     p.box = 1;
