@@ -11,15 +11,17 @@
 // the tensor cores work for one, the CUDA cores exponentiate the other.
 //
 // One CTA per SM, 384 threads:
-//   warps 0, 3   TMA producers of K and of V: tiles of 128 slots, each through a ring of stages;
-//                a tile is gathered as boxes of gcd(page size, 128) slots, their pages looked up
+//   warps 0, 3   TMA producers of K and of V: tiles of 64 slots, each through a ring of stages;
+//                a tile is gathered as boxes of gcd(page size, 64) slots, their pages looked up
 //                a tile ahead (with 16-slot pages one warp spent 1.7 us on a tile's 16 copies)
 //   warp 1       TMEM allocator and MMA issuer (one lane)
 //   warp 2       looks after V: clears what no row may see (see below)
-//   warps 4-7, 8-11  softmax of slot 0 and slot 1: a thread per row, its 128 scores in registers
+//   warps 4-7, 8-11  softmax of slot 0 and slot 1: a thread per row, its 64 scores in registers
 //
-// TMEM (512 columns): S of slots 0 and 1 (128 each; P overwrites S's first 64), O of slots 0 and
-// 1. The second product reads P from tensor memory and V from shared memory as it was loaded
+// TMEM (512 columns): two buffers of S for each of slots 0 and 1 (64 columns each; P overwrites the
+// first 32 of its S), O of slots 0 and 1 (128 each). With two buffers S of the next tile is there
+// when a softmax warp is done with one: with one buffer of 128 keys each slot's chain S, softmax,
+// P V took 2.1 us a tile, twice the tensor cores' time. The second product reads P from tensor memory and V from shared memory as it was loaded
 // (MN-major), so P never passes through shared memory.
 //
 // A masked score is -inf, so its P is 0; but 0 x V is NaN where V is infinite or NaN. In tiles
@@ -41,21 +43,25 @@ namespace {
 
 using namespace tc;
 
-constexpr int kBN = 128;
+constexpr int kBN = 64;
 constexpr int kThreads = 384;
 constexpr int kHeavy = 129;      // rows from which an item has two tiles
-constexpr int kMaxStages = 4;    // of K and of V each
+constexpr int kMaxStages = 8;    // of K and of V each
 constexpr int kCtlBytes = 2048;
 
 struct Params {
     Args a;
     CUtensorMap kmap, vmap;
-    int box;  // slots of a TMA box: gcd(page size, 128)
+    int box;  // slots of a TMA box: gcd(page size, 64)
 };
 
-struct Ctl {  // control block in shared memory; barriers first
+// Control block in shared memory. A parity tells only neighbouring phases of a barrier apart, so
+// whoever waits must know the phase before to be over. K and V stages have barriers of their own
+// and one producer each for that, and the two S buffers too: S of tile u + 2 comes after P V of
+// tile u, so P V of tile u - 1 (the other buffer) may be outstanding when S of tile u is there.
+struct Ctl {
     uint64_t kfull[kMaxStages], kempty[kMaxStages], vfull[kMaxStages], vempty[kMaxStages],
-        vready[kMaxStages], s_full[2], p_half[2], p_full[2], o_done[2], q_full, done;
+        vready[kMaxStages], s_full[2][2], p_full[2][2], pv_done[2][2], q_full, done;
     long long scratch[34];
     uint32_t tmem;
     volatile int abort;
@@ -103,12 +109,11 @@ __device__ __forceinline__ void give_back(const Args &a, const Segment &g, int n
         tmem_ld32(tO + x * 32u, o);
         for (int t = 0; t < n; ++t) {
             const int k0 = g.tl.at(g.t + t) * kBN;
-            uint32_t bits[4];
-            visible_bits<4>(a, g.s, node, pos, k0, bits);
+            uint32_t bits[2];
+            visible_bits<2>(a, g.s, node, pos, k0, bits);
 #pragma unroll 1
             for (int j = 0; j < kBN; ++j) {
-                const uint32_t wb = j < 64 ? (j < 32 ? bits[0] : bits[1])
-                                           : (j < 96 ? bits[2] : bits[3]);
+                const uint32_t wb = j < 32 ? bits[0] : bits[1];
                 if (!((wb >> (j & 31)) & 1u)) continue;
                 const int pg = page_of(a, g.b, k0 + j);
                 if (pg < 0) continue;
@@ -132,7 +137,7 @@ __device__ __forceinline__ void give_back(const Args &a, const Segment &g, int n
 
 // Stages of K and of V each that fit beside the query tiles.
 template <int DC> constexpr int stages() {
-    return std::min(kMaxStages, ((227 * 1024 - 1024 - kCtlBytes) / (DC * 16384) - 2) / 2);
+    return std::min(kMaxStages, (227 * 1024 - 1024 - kCtlBytes - 2 * DC * 16384) / (2 * DC * 8192));
 }
 
 template <int DC>  // 64-column chunks of the head size
@@ -143,11 +148,12 @@ attn_tc_kernel(const __grid_constant__ Params p) {
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t *gbase = smem_raw + (base - raw);
     Ctl &c = *reinterpret_cast<Ctl *>(gbase);
-    constexpr uint32_t kTile = DC * 16384u;  // 128 rows x 64 DC bf16
+    constexpr uint32_t kTile = DC * 16384u;  // 128 query rows x 64 DC bf16
+    constexpr uint32_t kKv = DC * 8192u;     // 64 slots x 64 DC bf16
     constexpr int NS = stages<DC>();
     using Ring = Slot<NS>;
-    const uint32_t sQ = base + kCtlBytes, sK = sQ + 2 * kTile, sV = sK + NS * kTile;
-    uint8_t *gQ = gbase + kCtlBytes, *gV = gQ + (2 + NS) * kTile;
+    const uint32_t sQ = base + kCtlBytes, sK = sQ + 2 * kTile, sV = sK + NS * kKv;
+    uint8_t *gQ = gbase + kCtlBytes, *gV = gQ + 2 * kTile + NS * kKv;
     const Args &a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     auto bar = [&](uint64_t &b) { return smem_u32(&b); };
@@ -161,10 +167,11 @@ attn_tc_kernel(const __grid_constant__ Params p) {
             mbar_init(bar(c.vready[s]), 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(c.s_full[i]), 1);
-            mbar_init(bar(c.p_half[i]), 4);  // a lane of each warp
-            mbar_init(bar(c.p_full[i]), 4);
-            mbar_init(bar(c.o_done[i]), 1);
+            for (int x = 0; x < 2; ++x) {
+                mbar_init(bar(c.s_full[i][x]), 1);
+                mbar_init(bar(c.p_full[i][x]), 4);  // a lane of each warp
+                mbar_init(bar(c.pv_done[i][x]), 1);
+            }
         }
         mbar_init(bar(c.q_full), 8);
         mbar_init(bar(c.done), 1);
@@ -201,11 +208,11 @@ attn_tc_kernel(const __grid_constant__ Params p) {
         Segment g;
         while (ok && next_segment<kBN, kHeavy>(a, r, g)) {
             const int n = __shfl_sync(0xffffffffu, g.count, 0);
-            int pg[4], next[4];  // pages of the tile's boxes (at most 128), lane by lane
-            auto look_up = [&](int t, int (&out)[4]) {
+            int pg[2], next[2];  // pages of the tile's boxes (at most 64), lane by lane
+            auto look_up = [&](int t, int (&out)[2]) {
                 const int k0 = g.tl.at(g.t + t) * kBN;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < 2; ++i) {
                     const int j = k0 + (lane + 32 * i) * p.box;
                     out[i] = lane + 32 * i < kBN / p.box && j < g.s.L
                                  ? a.table[(size_t)g.b * a.max_pages + j / a.page]
@@ -218,7 +225,7 @@ attn_tc_kernel(const __grid_constant__ Params p) {
                 const int st = Ring::stage(rp);
                 int good = 0, bad = 0;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < 2; ++i) {
                     pg[i] = next[i];
                     const bool in = pg[i] >= 0 && pg[i] < a.n_pages;
                     good += __popc(__ballot_sync(0xffffffffu, in));
@@ -240,17 +247,15 @@ attn_tc_kernel(const __grid_constant__ Params p) {
                 const uint32_t fb = bar(full[st]);
                 if (lane == 0) mbar_expect_tx(fb, (uint32_t)good * p.box * 128u * DC);
                 __syncwarp();
-                const uint32_t dst = (is_k ? sK : sV) + (uint32_t)st * kTile;
+                const uint32_t dst = (is_k ? sK : sV) + (uint32_t)st * kKv;
                 const int boxes = (min(kBN, g.s.L - k0) + p.box - 1) / p.box;
                 int in_page = k0 % a.page;
                 for (int x = 0; x < boxes; ++x) {
-                    const int lo = x & 31, hi = x >> 5;
-                    const int mine = hi == 0 ? pg[0] : (hi == 1 ? pg[1] : (hi == 2 ? pg[2] : pg[3]));
-                    const int page = __shfl_sync(0xffffffffu, mine, lo);
+                    const int page = __shfl_sync(0xffffffffu, x < 32 ? pg[0] : pg[1], x & 31);
                     if (page >= 0) {
 #pragma unroll
                         for (int h = 0; h < DC; ++h)
-                            tma_load_4d_elect(dst + h * 16384u + (uint32_t)x * p.box * 128u, map,
+                            tma_load_4d_elect(dst + h * 8192u + (uint32_t)x * p.box * 128u, map,
                                               h * 64, in_page, g.h, page, fb);
                     }
                     in_page += p.box;
@@ -263,8 +268,9 @@ attn_tc_kernel(const __grid_constant__ Params p) {
         __syncwarp();
     } else if (warp == 1) {
         // ----------------------------------------------------------- MMA issuer
-        const uint32_t id_s = idesc_bf16(128, 128), id_o = idesc_bf16(128, 64 * DC) | kIdescBMn;
-        uint32_t pcount[2] = {0, 0}, kpos = 0, vpos = 0, seg = 0;  // kpos, vpos: of the segment's
+        const uint32_t id_s = idesc_bf16(128, kBN), id_o = idesc_bf16(128, 64 * DC) | kIdescBMn;
+        uint32_t kpos = 0, vpos = 0, seg = 0;  // ring positions of the segment's first K, V
+        uint32_t done[2] = {0, 0};             // tiles of each slot before the segment
         bool ok = true;
         auto wait = [&](uint64_t &b, uint32_t par) {
             if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(b), par, &c.abort, a.flags));
@@ -275,87 +281,81 @@ attn_tc_kernel(const __grid_constant__ Params p) {
         while (ok && next_segment<kBN, kHeavy>(a, r, g)) {
             const bool two = __shfl_sync(0xffffffffu, g.rows, 0) > 128;
             const int n = __shfl_sync(0xffffffffu, g.count, 0);
-            auto score = [&](int slot, int t) {  // S of a slot from K tile t
-                const uint32_t k = sw128_lo(sK + (uint32_t)Ring::stage(kpos + t) * kTile, 16);
+            // u: the slot's tile count; its S buffer is u & 1, the buffer's use u >> 1
+            auto score = [&](int slot, uint32_t u, int t) {  // S of a slot from K tile t
+                const uint32_t k = sw128_lo(sK + (uint32_t)Ring::stage(kpos + t) * kKv, 16);
                 const uint32_t q = sw128_lo(sQ + (two ? (uint32_t)slot * kTile : 0u), 16);
+                const uint32_t d = tmem + slot * 128u + (u & 1u) * 64u;
 #pragma unroll
-                for (int x = 0; x < 4 * DC; ++x) {
-                    const uint32_t off = ((x >> 2) * 16384u + (x & 3) * 32u) >> 4;
-                    mma_ss_elect(tmem + slot * 128u, q + off, k + off, id_s, x != 0);
-                }
+                for (int x = 0; x < 4 * DC; ++x)
+                    mma_ss_elect(d, q + (((x >> 2) * 16384u + (x & 3) * 32u) >> 4),
+                                 k + (((x >> 2) * 8192u + (x & 3) * 32u) >> 4), id_s, x != 0);
                 mma_issued = true;
-                commit_elect(bar(c.s_full[slot]));
+                commit_elect(bar(c.s_full[slot][u & 1u]));
             };
             auto wait_k = [&](int t) {
                 return wait(c.kfull[Ring::stage(kpos + t)], Ring::parity(kpos + t));
             };
-            auto free_k = [&](int t) {
-                commit_elect(bar(c.kempty[Ring::stage(kpos + t)]));
-            };
-            // O += P V tile t, the first 64 keys while the others are still exponentiated
-            auto output = [&](int slot, int t, bool first) {
-                const uint32_t v = sw128_lo(sV + (uint32_t)Ring::stage(vpos + t) * kTile, 16384);
-                const uint32_t par = pcount[slot]++ & 1u;
-                if (!wait(c.p_half[slot], par)) return false;
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    mma_ts_elect(tmem + 256u + slot * 128u, tmem + slot * 128u + x * 8u,
-                                 v + x * (2048u >> 4), id_o, !first || x != 0);
-                if (!wait(c.p_full[slot], par)) return false;
-#pragma unroll
-                for (int x = 4; x < 8; ++x)
-                    mma_ts_elect(tmem + 256u + slot * 128u, tmem + slot * 128u + x * 8u,
-                                 v + x * (2048u >> 4), id_o, 1u);
-                return true;
-            };
+            auto free_k = [&](int t) { commit_elect(bar(c.kempty[Ring::stage(kpos + t)])); };
             auto wait_v = [&](int t) {
                 return wait(c.vready[Ring::stage(vpos + t)], Ring::parity(vpos + t));
             };
-            auto free_v = [&](int t) {
-                commit_elect(bar(c.vempty[Ring::stage(vpos + t)]));
+            auto free_v = [&](int t) { commit_elect(bar(c.vempty[Ring::stage(vpos + t)])); };
+            auto output = [&](int slot, uint32_t u, int t, bool first) {  // O += P V tile t
+                if (!wait(c.p_full[slot][u & 1u], (u >> 1) & 1u)) return false;
+                const uint32_t v = sw128_lo(sV + (uint32_t)Ring::stage(vpos + t) * kKv, 8192);
+                const uint32_t pt = tmem + slot * 128u + (u & 1u) * 64u;
+#pragma unroll
+                for (int x = 0; x < kBN / 16; ++x)
+                    mma_ts_elect(tmem + 256u + slot * 128u, pt + x * 8u, v + x * (2048u >> 4), id_o,
+                                 !first || x != 0);
+                commit_elect(bar(c.pv_done[slot][u & 1u]));
+                return true;
             };
             if (!wait(c.q_full, seg++ & 1u)) break;
             if (two) {
-                if (!wait_k(0)) break;
-                score(0, 0);
-                score(1, 0);
-                free_k(0);
+                // both slots take every tile; S runs two tiles ahead of P V
+                for (int t = 0; ok && t < min(n, 2); ++t) {
+                    if (!wait_k(t)) break;
+                    score(0, done[0] + t, t);
+                    score(1, done[1] + t, t);
+                    free_k(t);
+                }
                 for (int t = 0; ok && t < n; ++t) {
-                    const bool more = t + 1 < n;
-                    if (!wait_v(t) || !output(0, t, t == 0)) break;
+                    const bool more = t + 2 < n;
+                    if (!wait_v(t) || !output(0, done[0] + t, t, t == 0)) break;
                     if (more) {
-                        if (!wait_k(t + 1)) break;
-                        score(0, t + 1);
-                    } else {
-                        commit_elect(bar(c.o_done[0]));
+                        if (!wait_k(t + 2)) break;
+                        score(0, done[0] + t + 2, t + 2);
                     }
-                    if (!output(1, t, t == 0)) break;
+                    if (!output(1, done[1] + t, t, t == 0)) break;
                     free_v(t);
                     if (more) {
-                        score(1, t + 1);
-                        free_k(t + 1);
-                    } else {
-                        commit_elect(bar(c.o_done[1]));
+                        score(1, done[1] + t + 2, t + 2);
+                        free_k(t + 2);
                     }
                 }
+                done[0] += n;
+                done[1] += n;
             } else {
-                for (int t = 0; t < min(n, 2); ++t) {
+                // the slots take tiles in turn: S runs four tiles ahead
+                for (int t = 0; ok && t < min(n, 4); ++t) {
                     if (!wait_k(t)) break;
-                    score(t, t);
+                    score(t & 1, done[t & 1] + (t >> 1), t);
                     free_k(t);
                 }
                 for (int t = 0; ok && t < n; ++t) {
                     const int slot = t & 1;
-                    if (!wait_v(t) || !output(slot, t, t < 2)) break;
+                    if (!wait_v(t) || !output(slot, done[slot] + (t >> 1), t, t < 2)) break;
                     free_v(t);
-                    if (t + 2 < n) {
-                        if (!wait_k(t + 2)) break;
-                        score(slot, t + 2);
-                        free_k(t + 2);
-                    } else {
-                        commit_elect(bar(c.o_done[slot]));
+                    if (t + 4 < n) {
+                        if (!wait_k(t + 4)) break;
+                        score(slot, done[slot] + (t >> 1) + 2, t + 4);
+                        free_k(t + 4);
                     }
                 }
+                done[0] += (n + 1) / 2;
+                done[1] += n / 2;
             }
             kpos += n;
             vpos += n;
@@ -379,16 +379,16 @@ attn_tc_kernel(const __grid_constant__ Params p) {
                 if (c.bad_page || tile_masked<kBN>(a, g.s, i0, i1, k0)) {
                     // rows that no query of the item sees are cleared whole: with one node all
                     // that it does not see, else what lies past the end or has no page
-                    uint32_t bits[4];
+                    uint32_t bits[2];
                     if (i0 == i1) {
-                        visible_bits<4>(a, g.s, i0, pos, k0, bits);
+                        visible_bits<2>(a, g.s, i0, pos, k0, bits);
                     } else {
 #pragma unroll
-                        for (int w = 0; w < 4; ++w) bits[w] = range_bits(0, g.s.L, k0 + 32 * w);
+                        for (int w = 0; w < 2; ++w) bits[w] = range_bits(0, g.s.L, k0 + 32 * w);
                     }
-                    uint8_t *tile = gV + (size_t)st * kTile;
+                    uint8_t *tile = gV + (size_t)st * kKv;
 #pragma unroll 1
-                    for (int w = 0; w < 4; ++w) {
+                    for (int w = 0; w < 2; ++w) {
                         const int row = 32 * w + lane;
                         bool keep = (bits[w] >> lane) & 1u;
                         if (keep && c.bad_page) keep = page_of(a, g.b, k0 + row) >= 0;
@@ -397,7 +397,7 @@ attn_tc_kernel(const __grid_constant__ Params p) {
                         for (int h = 0; h < DC; ++h)
 #pragma unroll
                             for (int x = 0; x < 8; ++x) {
-                                uint4 *q = reinterpret_cast<uint4 *>(tile + h * 16384 + row * 128 +
+                                uint4 *q = reinterpret_cast<uint4 *>(tile + h * 8192 + row * 128 +
                                                                      ((x ^ (row & 7)) << 4));
                                 uint4 v = make_uint4(0u, 0u, 0u, 0u);
                                 if (keep) {
@@ -436,8 +436,8 @@ attn_tc_kernel(const __grid_constant__ Params p) {
         const int trow = quad * 32 + lane;  // row of the slot's tile
         const int tid = threadIdx.x - 128;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-        const uint32_t tS = tmem + slot * 128u + lanes, tO = tmem + 256u + slot * 128u + lanes;
-        uint32_t scount = 0, ocount = 0;
+        const uint32_t tO = tmem + 256u + slot * 128u + lanes;
+        uint32_t u = 0;  // tiles of the slot so far
         bool dead = false;
         Segment g;
         while (next_segment<kBN, kHeavy>(a, r, g)) {
@@ -487,27 +487,27 @@ attn_tc_kernel(const __grid_constant__ Params p) {
             const float cs = a.scale * kLog2e;
             float m = -INFINITY, l = 0.f;
             int tiles = 0;
-            for (int t = two ? 0 : slot; t < n; t += two ? 1 : 2, ++tiles) {
+            for (int t = two ? 0 : slot; t < n; t += two ? 1 : 2, ++tiles, ++u) {
                 const int k0 = g.tl.at(g.t + t) * kBN;
-                if (!mbar_wait(bar(c.s_full[slot]), scount & 1u, &c.abort, a.flags)) dead = true;
-                ++scount;
+                const uint32_t tS = tmem + slot * 128u + (u & 1u) * 64u + lanes;
+                if (!mbar_wait(bar(c.s_full[slot][u & 1u]), (u >> 1) & 1u, &c.abort, a.flags))
+                    dead = true;
                 tc_fence_after();
                 if (active && !__any_sync(0xffffffffu, dead)) {
-                    uint32_t s[128];
+                    uint32_t s[kBN];
                     tmem_ld64(tS, s);
-                    tmem_ld64(tS + 64u, s + 64);
                     if (tile_masked<kBN>(a, g.s, i0, i1, k0) || c.bad_page) {
-                        uint32_t bits[4];
-                        visible_bits<4>(a, g.s, node, pos, k0, bits);
+                        uint32_t bits[2];
+                        visible_bits<2>(a, g.s, node, pos, k0, bits);
                         if (c.bad_page) {
 #pragma unroll
-                            for (int w = 0; w < 4; ++w)
+                            for (int w = 0; w < 2; ++w)
                                 for (int x = 0; x < 32; ++x)
                                     if (((bits[w] >> x) & 1u) && page_of(a, g.b, k0 + 32 * w + x) < 0)
                                         bits[w] &= ~(1u << x);
                         }
 #pragma unroll
-                        for (int w = 0; w < 4; ++w)
+                        for (int w = 0; w < 2; ++w)
 #pragma unroll
                             for (int x = 0; x < 32; ++x)
                                 if (!((bits[w] >> x) & 1u)) s[32 * w + x] = 0xff800000u;  // -inf
@@ -517,7 +517,7 @@ attn_tc_kernel(const __grid_constant__ Params p) {
                     for (int i = 0; i < 4; ++i)
                         mx[i] = fmaxf(__uint_as_float(s[i]), __uint_as_float(s[i + 4]));
 #pragma unroll
-                    for (int i = 8; i < 128; i += 8)
+                    for (int i = 8; i < kBN; i += 8)
 #pragma unroll
                         for (int x = 0; x < 4; ++x)  // three-operand maxima
                             mx[x] = fmaxf(fmaxf(mx[x], __uint_as_float(s[i + x])),
@@ -530,6 +530,12 @@ attn_tc_kernel(const __grid_constant__ Params p) {
                         m = mn;
                         l *= f;
                         if (tiles > 0) {
+                            // S runs ahead: the last tile's product may still be adding to O
+                            if (!mbar_wait(bar(c.pv_done[slot][(u - 1) & 1u]), ((u - 1) >> 1) & 1u,
+                                           &c.abort, a.flags))
+                                dead = true;
+                            __syncwarp();
+                            tc_fence_after();
 #pragma unroll 1
                             for (int x = 0; x < 2 * DC; ++x) {
                                 uint32_t o[32];
@@ -545,46 +551,34 @@ attn_tc_kernel(const __grid_constant__ Params p) {
                     uint64_t cs2, sub2, sum[2] = {0ull, 0ull};
                     pack2(cs2, cs, cs);
                     pack2(sub2, sub, sub);
+                    uint32_t pk[32];
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        uint32_t pk[32];
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            uint64_t t2;
-                            float p0, p1;
-                            pack2(t2, __uint_as_float(s[x * 64 + 2 * i]),
-                                  __uint_as_float(s[x * 64 + 2 * i + 1]));
-                            t2 = fma2(t2, cs2, sub2);
-                            unpack2(t2, p0, p1);
-                            p0 = ex2(p0);
-                            p1 = ex2(p1);
-                            pack2(t2, p0, p1);
-                            sum[i & 1] = add2(sum[i & 1], t2);
-                            pk[i] = pack_bf16(p0, p1);
-                        }
-                        tmem_st32(tS + x * 32u, pk);
-                        tmem_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(bar(x ? c.p_full[slot] : c.p_half[slot]));
+                    for (int i = 0; i < 32; ++i) {
+                        uint64_t t2;
+                        float p0, p1;
+                        pack2(t2, __uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
+                        t2 = fma2(t2, cs2, sub2);
+                        unpack2(t2, p0, p1);
+                        p0 = ex2(p0);
+                        p1 = ex2(p1);
+                        pack2(t2, p0, p1);
+                        sum[i & 1] = add2(sum[i & 1], t2);
+                        pk[i] = pack_bf16(p0, p1);
                     }
+                    tmem_st32(tS, pk);
+                    tmem_wait_st();
                     float s0, s1;
                     unpack2(add2(sum[0], sum[1]), s0, s1);
                     l += s0 + s1;
-                } else {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(bar(c.p_half[slot]));
-                        mbar_arrive(bar(c.p_full[slot]));
-                    }
                 }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(c.p_full[slot][u & 1u]));
             }
-            if (tiles > 0) {
-                if (!mbar_wait(bar(c.o_done[slot]), ocount & 1u, &c.abort, a.flags)) dead = true;
-                ++ocount;
-                tc_fence_after();
-            }
+            if (tiles > 0 && !mbar_wait(bar(c.pv_done[slot][(u - 1) & 1u]), ((u - 1) >> 1) & 1u,
+                                        &c.abort, a.flags))
+                dead = true;
+            tc_fence_after();
             const bool live = !__any_sync(0xffffffffu, dead);
             // one tile: slot 1 hands its part over through the query tiles' shared memory (column
             // by column, a thread per row)
@@ -726,7 +720,7 @@ bool encode_pool(CUtensorMap *m, const void *base, const Args &a, int box) {
 }
 
 template <int DC> cudaError_t launch_dc(Params &p, int ctas, cudaStream_t s) {
-    constexpr int smem = 1024 + kCtlBytes + (2 * stages<DC>() + 2) * DC * 16384;
+    constexpr int smem = 1024 + kCtlBytes + (stages<DC>() + 2) * DC * 16384;
     const cudaError_t err = cudaFuncSetAttribute(
         attn_tc_kernel<DC>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess) return err;
