@@ -166,7 +166,11 @@ __device__ __forceinline__ Range attn_plan(const Args &a, int cta, int n_ctas, l
         total += scratch[i];
     }
     Range r;
-    r.quota = max((long long)a.min_units, (total + n_ctas - 1) / n_ctas);
+    // (64-bit divisions take hundreds of cycles: only where the numbers need them)
+    const bool small = total < (1ll << 30);
+    r.quota = max((long long)a.min_units,
+                  small ? (long long)(((unsigned)total + n_ctas - 1) / (unsigned)n_ctas)
+                        : (total + n_ctas - 1) / n_ctas);
     const long long start = r.quota * cta;
     r.left = max(0ll, min(r.quota, total - start));
     long long at = before + inc - sum;  // first unit of this thread's run
@@ -178,8 +182,9 @@ __device__ __forceinline__ Range attn_plan(const Args &a, int cta, int n_ctas, l
             if (start < at + all) {
                 const long long off = start - at;
                 found[0] = e;
-                found[1] = (int)(off / item);
-                scratch[30] = off % item;
+                const long long h = small ? (long long)((unsigned)off / (unsigned)item) : off / item;
+                found[1] = (int)h;
+                scratch[30] = off - h * item;
                 break;
             }
             at += all;

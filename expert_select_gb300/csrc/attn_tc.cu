@@ -208,32 +208,30 @@ attn_tc_kernel(const __grid_constant__ Params p) {
         Segment g;
         while (ok && next_segment<kBN, kHeavy>(a, r, g)) {
             const int n = __shfl_sync(0xffffffffu, g.count, 0);
-            int pg[2], next[2];  // pages of the tile's boxes (at most 64), lane by lane
-            auto look_up = [&](int t, int (&out)[2]) {
-                const int k0 = g.tl.at(g.t + t) * kBN;
+            // Pages of 64 boxes (one tile of single-slot boxes, 64 tiles of 64-slot ones), two a
+            // lane; the next 64 boxes' are on their way while these are used.
+            const int per_tile = kBN / p.box, in_use = (g.s.L + p.box - 1) / p.box;  // boxes
+            int first = -1, in_page = 0;  // box of pg[0] of lane 0; slot in its page of the next box
+            int pg[2], next[2];
+            uint32_t good[2], there[2];
+            auto look_up = [&](int from, int (&out)[2]) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const int j = k0 + (lane + 32 * i) * p.box;
-                    out[i] = lane + 32 * i < kBN / p.box && j < g.s.L
-                                 ? a.table[(size_t)g.b * a.max_pages + j / a.page]
-                                 : INT_MIN;
+                    const int bx = from + lane + 32 * i;
+                    out[i] = bx < in_use ? a.table[(size_t)g.b * a.max_pages + bx * p.box / a.page]
+                                         : -1;
                 }
             };
-            look_up(0, next);
-            for (int t = 0; ok && t < n; ++t, ++rp) {
-                const int k0 = __shfl_sync(0xffffffffu, g.tl.at(g.t + t) * kBN, 0);
-                const int st = Ring::stage(rp);
-                int good = 0, bad = 0;
+            auto take = [&](int from) {  // makes `next` current and looks further ahead
+                first = from;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     pg[i] = next[i];
-                    const bool in = pg[i] >= 0 && pg[i] < a.n_pages;
-                    good += __popc(__ballot_sync(0xffffffffu, in));
-                    bad |= !in && pg[i] != INT_MIN;
-                    if (!in) pg[i] = -1;
+                    good[i] = __ballot_sync(0xffffffffu, pg[i] >= 0 && pg[i] < a.n_pages);
+                    there[i] = __ballot_sync(0xffffffffu, from + lane + 32 * i < in_use);
                 }
-                if (t + 1 < n) look_up(t + 1, next);  // in flight while this tile is copied
-                if (__any_sync(0xffffffffu, bad)) {
+                look_up(from + 64, next);
+                if (good[0] != there[0] || good[1] != there[1]) {
                     if (lane == 0) {
                         c.bad_page = 1;
                         __threadfence_block();
@@ -241,23 +239,39 @@ attn_tc_kernel(const __grid_constant__ Params p) {
                     }
                     __syncwarp();
                 }
-                ok = __all_sync(0xffffffffu,
-                                mbar_wait(bar(empty[st]), Ring::parity(rp) ^ 1u, &c.abort, a.flags));
+            };
+            int box0 = -1;
+            for (int t = 0; ok && t < n; ++t, ++rp) {
+                const int bx = g.tl.at(g.t + t) * per_tile;
+                const int st = Ring::stage(rp);
+                if (bx != box0 || t == 0) in_page = bx * p.box % a.page;  // the tiles' first, or a jump
+                box0 = bx + per_tile;
+                if (t == 0 || bx < first || bx >= first + 128) {
+                    look_up(bx, next);
+                    take(bx);
+                } else if (bx >= first + 64) {
+                    take(first + 64);
+                }
+                const uint64_t ok64 = (((uint64_t)good[1] << 32) | good[0]) >> (bx - first);
+                const uint64_t mask = per_tile == 64 ? ~0ull : (1ull << per_tile) - 1ull;
+                const uint64_t todo = ok64 & mask;
+                ok = mbar_wait(bar(empty[st]), Ring::parity(rp) ^ 1u, &c.abort, a.flags);
+                ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 const uint32_t fb = bar(full[st]);
-                if (lane == 0) mbar_expect_tx(fb, (uint32_t)good * p.box * 128u * DC);
+                if (lane == 0) mbar_expect_tx(fb, (uint32_t)__popcll(todo) * p.box * 128u * DC);
                 __syncwarp();
-                const uint32_t dst = (is_k ? sK : sV) + (uint32_t)st * kKv;
-                const int boxes = (min(kBN, g.s.L - k0) + p.box - 1) / p.box;
-                int in_page = k0 % a.page;
+                uint32_t dst = (is_k ? sK : sV) + (uint32_t)st * kKv;
+                const int boxes = min(per_tile, in_use - bx);
                 for (int x = 0; x < boxes; ++x) {
-                    const int page = __shfl_sync(0xffffffffu, x < 32 ? pg[0] : pg[1], x & 31);
-                    if (page >= 0) {
+                    const int i = bx - first + x;
+                    const int page = __shfl_sync(0xffffffffu, i < 32 ? pg[0] : pg[1], i & 31);
+                    if ((todo >> x) & 1ull) {
 #pragma unroll
                         for (int h = 0; h < DC; ++h)
-                            tma_load_4d_elect(dst + h * 8192u + (uint32_t)x * p.box * 128u, map,
-                                              h * 64, in_page, g.h, page, fb);
+                            tma_load_4d_elect(dst + h * 8192u, map, h * 64, in_page, g.h, page, fb);
                     }
+                    dst += p.box * 128u;
                     in_page += p.box;
                     if (in_page >= a.page) in_page = 0;
                 }
@@ -451,16 +465,21 @@ attn_tc_kernel(const __grid_constant__ Params p) {
                 const int rows = two ? 256 : 128, ch = tid % (8 * DC), first = tid / (8 * DC);
                 const __nv_bfloat16 *q = (const __nv_bfloat16 *)a.q + (size_t)g.s.row0 * a.ldq +
                                          (size_t)g.h * a.G * a.dh + ch * 8;
+                const int dn = kStep / a.G, dg = kStep - dn * a.G;  // a step in nodes and heads
+                int node = (g.q0 + first) / a.G, hd = g.q0 + first - node * a.G;
                 for (int y = first; y < rows; y += 16 * kStep) {
                     uint4 v[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        const int row = y + i * kStep;
                         v[i] = make_uint4(0u, 0u, 0u, 0u);
-                        if (row < g.rows && ch * 8 < a.dh) {
-                            const int qr = g.q0 + row, node = qr / a.G;
+                        if (y + i * kStep < g.rows && ch * 8 < a.dh)
                             v[i] = __ldg(reinterpret_cast<const uint4 *>(
-                                q + (size_t)node * a.ldq + (size_t)(qr - node * a.G) * a.dh));
+                                q + (size_t)node * a.ldq + (size_t)hd * a.dh));
+                        node += dn;
+                        hd += dg;
+                        if (hd >= a.G) {
+                            hd -= a.G;
+                            ++node;
                         }
                     }
 #pragma unroll
@@ -580,8 +599,8 @@ attn_tc_kernel(const __grid_constant__ Params p) {
                 dead = true;
             tc_fence_after();
             const bool live = !__any_sync(0xffffffffu, dead);
-            // one tile: slot 1 hands its part over through the query tiles' shared memory (column
-            // by column, a thread per row)
+            // one tile: slot 1 hands its part over through the query tiles' shared memory, a block
+            // of 32 columns x 32 rows per warp
             float *xch = reinterpret_cast<float *>(gQ);
             const bool merge = !two && n > 1;
             if (merge) {
@@ -596,7 +615,7 @@ attn_tc_kernel(const __grid_constant__ Params p) {
                             tmem_ld32(tO + x * 32u, o);
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
-                                xch[(x * 32 + i) * 128 + trow] = __uint_as_float(o[i]);
+                                xch[(x * 4 + quad) * 1024 + i * 32 + lane] = __uint_as_float(o[i]);
                         }
                     }
                 }
@@ -633,9 +652,10 @@ attn_tc_kernel(const __grid_constant__ Params p) {
                 f0 = fmaxf(f0, 1e-37f);  // what was given back must not vanish in the merge
             }
             const int first = row - lane, left = min(32, g.rows - first);
-            // a row's columns are in one thread: turn the warp's 32 x 32 blocks around in shared
-            // memory (the query tile of this slot, or the exchange words that this warp has just
-            // read), so that each store covers whole sectors of few rows
+            // a row's columns are in one thread: turn the warp's blocks of 32 rows x 32 columns around
+            // in 4 KB of shared memory (of this slot's query tile, or the exchange block that this
+            // warp has just read), in swizzled 16-byte pieces, so that a store covers whole rows
+            float *part = a.part_o + part_row(a, blockIdx.x, g, first) * a.dh;
 #pragma unroll 1
             for (int x = 0; x < 2 * DC; ++x) {
                 uint32_t o[32];
@@ -644,41 +664,52 @@ attn_tc_kernel(const __grid_constant__ Params p) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
                         o[i] = __float_as_uint(__uint_as_float(o[i]) * f0 +
-                                               xch[(x * 32 + i) * 128 + trow] * f1);
+                                               xch[(x * 4 + quad) * 1024 + i * 32 + lane] * f1);
                 }
-                uint32_t *turn = reinterpret_cast<uint32_t *>(
-                                     gQ + (two ? slot * kTile : (merge ? x * 16384u : 0u))) +
-                                 quad * 32;
+                uint8_t *turn =
+                    gQ + (two ? slot * kTile + quad * 4096u : (x * 4 + quad) * 4096u);
                 __syncwarp();
                 if (g.whole) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        turn[i * 128 + (lane ^ i)] = pack_bf16(__uint_as_float(o[2 * i]) * fin,
-                                                               __uint_as_float(o[2 * i + 1]) * fin);
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            w[y] = pack_bf16(__uint_as_float(o[8 * i + 2 * y]) * fin,
+                                             __uint_as_float(o[8 * i + 2 * y + 1]) * fin);
+                        *reinterpret_cast<uint4 *>(turn + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
+                            make_uint4(w[0], w[1], w[2], w[3]);
+                    }
                     __syncwarp();
-                    const int i = lane & 15, hf = lane & 16;
+                    const int piece = lane & 3;
+                    const bool col = x * 32 + piece * 8 < a.dh;
 #pragma unroll
-                    for (int y = 0; y < 16; ++y) o[y] = turn[i * 128 + ((y | hf) ^ i)];
-                    const bool col = x * 32 + 2 * i < a.dh;
-#pragma unroll
-                    for (int y = 0; y < 16; ++y) {
-                        const long long at = __shfl_sync(0xffffffffu, (long long)orow, y | hf);
-                        if ((y | hf) < left && col)
-                            reinterpret_cast<uint32_t *>((__nv_bfloat16 *)a.out + at * a.dh +
-                                                         x * 32)[i] = o[y];
+                    for (int y = 0; y < 4; ++y) {
+                        const int ry = y * 8 + (lane >> 2);
+                        const uint4 w = *reinterpret_cast<const uint4 *>(
+                            turn + ry * 64 + ((piece ^ ((ry >> 1) & 3)) << 4));
+                        const long long at = __shfl_sync(0xffffffffu, (long long)orow, ry);
+                        if (ry < left && col)
+                            *reinterpret_cast<uint4 *>((__nv_bfloat16 *)a.out + at * a.dh + x * 32 +
+                                                       piece * 8) = w;
                     }
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) turn[i * 128 + (lane ^ i)] = o[i];
+                    for (int i = 0; i < 8; ++i)
+                        *reinterpret_cast<uint4 *>(turn + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+                            make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                     __syncwarp();
+                    const int piece = lane & 7;
+                    const bool col = x * 32 + piece * 4 < a.dh;
 #pragma unroll
-                    for (int y = 0; y < 32; ++y) o[y] = turn[lane * 128 + (y ^ lane)];
-                    float *dst =
-                        a.part_o + part_row(a, blockIdx.x, g, first) * a.dh + x * 32 + lane;
-                    const bool col = x * 32 + lane < a.dh;
-#pragma unroll
-                    for (int y = 0; y < 32; ++y)
-                        if (y < left && col) dst[(size_t)y * a.dh] = __uint_as_float(o[y]);
+                    for (int y = 0; y < 8; ++y) {
+                        const int ry = y * 4 + (lane >> 3);
+                        const uint4 w = *reinterpret_cast<const uint4 *>(
+                            turn + ry * 128 + ((piece ^ (ry & 7)) << 4));
+                        if (ry < left && col)
+                            *reinterpret_cast<uint4 *>(part + (size_t)ry * a.dh + x * 32 +
+                                                       piece * 4) = w;
+                    }
                 }
             }
             tc_fence_before();
