@@ -283,96 +283,116 @@ attn_tc_kernel(const __grid_constant__ Params p) {
     } else if (warp == 1) {
         // ----------------------------------------------------------- MMA issuer
         const uint32_t id_s = idesc_bf16(128, kBN), id_o = idesc_bf16(128, 64 * DC) | kIdescBMn;
-        uint32_t kpos = 0, vpos = 0, seg = 0;  // ring positions of the segment's first K, V
-        uint32_t done[2] = {0, 0};             // tiles of each slot before the segment
+        // The issuing warp's own instructions are what bounds a tile's time (1280 cycles of tensor
+        // work took 2000 with a vote and two divisions by the ring's length per wait): stages and
+        // parities are counted, and the waits' verdicts are looked at once a tile.
+        uint32_t kst = 0, kph = 0, vst = 0, vph = 0, seg = 0;
+        uint32_t done[2] = {0, 0};  // tiles of each slot before the segment
         bool ok = true;
         auto wait = [&](uint64_t &b, uint32_t par) {
-            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(b), par, &c.abort, a.flags));
-            tc_fence_after();
-            return ok;
+            ok &= mbar_wait(bar(b), par, &c.abort, a.flags);
         };
+        auto all_ok = [&]() { return __all_sync(0xffffffffu, ok) != 0; };
+        const uint32_t q_lo = sw128_lo(sQ, 16), k_lo = sw128_lo(sK, 16), v_lo = sw128_lo(sV, 8192);
         Segment g;
-        while (ok && next_segment<kBN, kHeavy>(a, r, g)) {
+        while (all_ok() && next_segment<kBN, kHeavy>(a, r, g)) {
             const bool two = __shfl_sync(0xffffffffu, g.rows, 0) > 128;
             const int n = __shfl_sync(0xffffffffu, g.count, 0);
             // u: the slot's tile count; its S buffer is u & 1, the buffer's use u >> 1
-            auto score = [&](int slot, uint32_t u, int t) {  // S of a slot from K tile t
-                const uint32_t k = sw128_lo(sK + (uint32_t)Ring::stage(kpos + t) * kKv, 16);
-                const uint32_t q = sw128_lo(sQ + (two ? (uint32_t)slot * kTile : 0u), 16);
+            auto score = [&](int slot, uint32_t u) {  // S of a slot from the current K stage
+                const uint32_t k = k_lo + kst * (kKv >> 4);
+                const uint32_t q = q_lo + (two ? (uint32_t)slot * (kTile >> 4) : 0u);
                 const uint32_t d = tmem + slot * 128u + (u & 1u) * 64u;
 #pragma unroll
                 for (int x = 0; x < 4 * DC; ++x)
                     mma_ss_elect(d, q + (((x >> 2) * 16384u + (x & 3) * 32u) >> 4),
                                  k + (((x >> 2) * 8192u + (x & 3) * 32u) >> 4), id_s, x != 0);
-                mma_issued = true;
                 commit_elect(bar(c.s_full[slot][u & 1u]));
             };
-            auto wait_k = [&](int t) {
-                return wait(c.kfull[Ring::stage(kpos + t)], Ring::parity(kpos + t));
+            auto wait_k = [&]() {
+                wait(c.kfull[kst], kph);
+                __syncwarp();
+                tc_fence_after();
             };
-            auto free_k = [&](int t) { commit_elect(bar(c.kempty[Ring::stage(kpos + t)])); };
-            auto wait_v = [&](int t) {
-                return wait(c.vready[Ring::stage(vpos + t)], Ring::parity(vpos + t));
+            auto free_k = [&]() {
+                commit_elect(bar(c.kempty[kst]));
+                if (++kst == NS) {
+                    kst = 0;
+                    kph ^= 1u;
+                }
             };
-            auto free_v = [&](int t) { commit_elect(bar(c.vempty[Ring::stage(vpos + t)])); };
-            auto output = [&](int slot, uint32_t u, int t, bool first) {  // O += P V tile t
-                if (!wait(c.p_full[slot][u & 1u], (u >> 1) & 1u)) return false;
-                const uint32_t v = sw128_lo(sV + (uint32_t)Ring::stage(vpos + t) * kKv, 8192);
+            auto wait_v = [&]() { wait(c.vready[vst], vph); };
+            auto free_v = [&]() {
+                commit_elect(bar(c.vempty[vst]));
+                if (++vst == NS) {
+                    vst = 0;
+                    vph ^= 1u;
+                }
+            };
+            auto output = [&](int slot, uint32_t u, bool first) {  // O += P V, current V stage
+                wait(c.p_full[slot][u & 1u], (u >> 1) & 1u);
+                __syncwarp();
+                tc_fence_after();
+                const uint32_t v = v_lo + vst * (kKv >> 4);
                 const uint32_t pt = tmem + slot * 128u + (u & 1u) * 64u;
 #pragma unroll
                 for (int x = 0; x < kBN / 16; ++x)
                     mma_ts_elect(tmem + 256u + slot * 128u, pt + x * 8u, v + x * (2048u >> 4), id_o,
                                  !first || x != 0);
                 commit_elect(bar(c.pv_done[slot][u & 1u]));
-                return true;
             };
-            if (!wait(c.q_full, seg++ & 1u)) break;
+            wait(c.q_full, seg++ & 1u);
+            __syncwarp();
+            tc_fence_after();
+            mma_issued = true;
             if (two) {
                 // both slots take every tile; S runs two tiles ahead of P V
-                for (int t = 0; ok && t < min(n, 2); ++t) {
-                    if (!wait_k(t)) break;
-                    score(0, done[0] + t, t);
-                    score(1, done[1] + t, t);
-                    free_k(t);
+                for (int t = 0; t < min(n, 2); ++t) {
+                    wait_k();
+                    score(0, done[0] + t);
+                    score(1, done[1] + t);
+                    free_k();
                 }
-                for (int t = 0; ok && t < n; ++t) {
+                for (int t = 0; t < n; ++t) {
                     const bool more = t + 2 < n;
-                    if (!wait_v(t) || !output(0, done[0] + t, t, t == 0)) break;
+                    wait_v();
+                    output(0, done[0] + t, t == 0);
                     if (more) {
-                        if (!wait_k(t + 2)) break;
-                        score(0, done[0] + t + 2, t + 2);
+                        wait_k();
+                        score(0, done[0] + t + 2);
                     }
-                    if (!output(1, done[1] + t, t, t == 0)) break;
-                    free_v(t);
+                    output(1, done[1] + t, t == 0);
+                    free_v();
                     if (more) {
-                        score(1, done[1] + t + 2, t + 2);
-                        free_k(t + 2);
+                        score(1, done[1] + t + 2);
+                        free_k();
                     }
+                    if (!all_ok()) break;
                 }
                 done[0] += n;
                 done[1] += n;
             } else {
                 // the slots take tiles in turn: S runs four tiles ahead
-                for (int t = 0; ok && t < min(n, 4); ++t) {
-                    if (!wait_k(t)) break;
-                    score(t & 1, done[t & 1] + (t >> 1), t);
-                    free_k(t);
+                for (int t = 0; t < min(n, 4); ++t) {
+                    wait_k();
+                    score(t & 1, done[t & 1] + (t >> 1));
+                    free_k();
                 }
-                for (int t = 0; ok && t < n; ++t) {
+                for (int t = 0; t < n; ++t) {
                     const int slot = t & 1;
-                    if (!wait_v(t) || !output(slot, done[slot] + (t >> 1), t, t < 2)) break;
-                    free_v(t);
+                    wait_v();
+                    output(slot, done[slot] + (t >> 1), t < 2);
+                    free_v();
                     if (t + 4 < n) {
-                        if (!wait_k(t + 4)) break;
-                        score(slot, done[slot] + (t >> 1) + 2, t + 4);
-                        free_k(t + 4);
+                        wait_k();
+                        score(slot, done[slot] + (t >> 1) + 2);
+                        free_k();
                     }
+                    if (!all_ok()) break;
                 }
                 done[0] += (n + 1) / 2;
                 done[1] += n / 2;
             }
-            kpos += n;
-            vpos += n;
         }
         __syncwarp();
     } else if (warp == 2) {
