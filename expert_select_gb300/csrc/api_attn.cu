@@ -127,7 +127,7 @@ moe_status moe_kv_append(const moe_cache_desc *C, const moe_rope_params *P, cons
                          const int *cache_len, const int *row_start, const int *depth, int B,
                          int N, int R, void *q_out, void *workspace, moe_stream_t stream) {
     if (!cache_ok(C) || !P || !block_ok(C, B, N, R, row_start)) return MOE_ERR_ARG;
-    if (P->inv_freq && (P->rot_dim < 4 || P->rot_dim % 4 || P->rot_dim > C->dh ||
+    if (P->inv_freq && (P->rot_dim < 8 || P->rot_dim % 8 || P->rot_dim > C->dh ||
                         !std::isfinite(P->rope_scale)))
         return MOE_ERR_ARG;
     if (!(P->eps >= 0.f) || !std::isfinite(P->eps)) return MOE_ERR_ARG;

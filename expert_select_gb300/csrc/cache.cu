@@ -11,43 +11,111 @@ namespace {
 
 constexpr int kThr = 128;
 
-// Two consecutive elements at p as fp32, and back.
-__device__ __forceinline__ float2 load2(const __nv_bfloat16 *p) {
-    const uint32_t u = *reinterpret_cast<const uint32_t *>(p);
-    return make_float2(bf16_lo(u), bf16_hi(u));
-}
-__device__ __forceinline__ float2 load2(const float *p) {
-    return *reinterpret_cast<const float2 *>(p);
-}
-__device__ __forceinline__ void store2(__nv_bfloat16 *p, float2 v) {
-    *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(v.x, v.y);
-}
-__device__ __forceinline__ void store2(float *p, float2 v) { *reinterpret_cast<float2 *>(p) = v; }
+// W elements in a row, as they lie in memory and as fp32.
+template <typename T, int W> struct Run;
+template <int W> struct Run<__nv_bfloat16, W> {
+    uint32_t r[W / 2];
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
+        if constexpr (W == 8) {
+            const uint4 u = *reinterpret_cast<const uint4 *>(p);
+            r[0] = u.x; r[1] = u.y; r[2] = u.z; r[3] = u.w;
+        } else {
+            const uint2 u = *reinterpret_cast<const uint2 *>(p);
+            r[0] = u.x; r[1] = u.y;
+        }
+    }
+    __device__ __forceinline__ void get(float v[W]) const {
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i) {
+            v[2 * i] = bf16_lo(r[i]);
+            v[2 * i + 1] = bf16_hi(r[i]);
+        }
+    }
+    __device__ __forceinline__ static void store(__nv_bfloat16 *p, const float v[W]) {
+        uint32_t w[W / 2];
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i) w[i] = attn::pack_bf16(v[2 * i], v[2 * i + 1]);
+        if constexpr (W == 8)
+            *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        else
+            *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+    }
+};
+template <int W> struct Run<float, W> {
+    float r[W];
+    __device__ __forceinline__ void load(const float *p) {
+#pragma unroll
+        for (int i = 0; i < W / 4; ++i) {
+            const float4 u = *reinterpret_cast<const float4 *>(p + 4 * i);
+            r[4 * i] = u.x; r[4 * i + 1] = u.y; r[4 * i + 2] = u.z; r[4 * i + 3] = u.w;
+        }
+    }
+    __device__ __forceinline__ void get(float v[W]) const {
+#pragma unroll
+        for (int i = 0; i < W; ++i) v[i] = r[i];
+    }
+    __device__ __forceinline__ static void store(float *p, const float v[W]) {
+#pragma unroll
+        for (int i = 0; i < W / 4; ++i)
+            *reinterpret_cast<float4 *>(p + 4 * i) =
+                make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    }
+};
 
-// A CTA per row. The row's angles are formed once (pos * inv_freq in fp64, reduced to a
-// fraction of a turn there: at position 10^6 an fp32 product would be off by up to 0.06 rad),
-// then LPH lanes take a head at a time: unit u of a head is the elements (2u, 2u + 1) and their
-// rotary partners rot / 2 further on (behind rot: two pairs that only pass through).
-template <typename T, int LPH, int UPL>
+// Fraction of a turn (within half a turn of 0) that pos * freq radians leave. 1 / (2 pi) is taken
+// as the sum of two fp32 values and the product with pos, cut into parts below 2^15 and 2^16 that
+// are exact in fp32, with its rounding error: at position 10^6 a plain fp32 product would be off
+// by up to 0.06 rad, this is within 10^-9 turns.
+__device__ __forceinline__ float turns(int pos, float freq) {
+    constexpr double kInv = 0.15915494309189533577;  // 1 / (2 pi)
+    constexpr float hi = (float)kInv, lo = (float)(kInv - (double)hi);
+    const float c = freq * hi, ce = fmaf(freq, hi, -c) + freq * lo;
+    const float big = (float)(pos & ~0xffff), small = (float)(pos & 0xffff);
+    const float b = big * c, s = small * c;
+    const float be = fmaf(big, c, -b) + big * ce, se = fmaf(small, c, -s) + small * ce;
+    float t = (b - rintf(b)) + be;
+    t += (s - rintf(s)) + se;
+    return t - rintf(t);
+}
+
+// A CTA per row. The row's angles are formed once; LPH lanes take a head at a time, a lane
+// W elements and their rotary partners rot / 2 further on (behind rot: two runs that only pass
+// through). The next heads' elements are on their way while a pass is computed.
+template <typename T, int W, int LPH>
 __global__ void __launch_bounds__(kThr) append_kernel(const AppendArgs a) {
     __shared__ float2 cs[128];  // cos, sin of the rot / 2 <= 128 angles
-    __shared__ int s_seq[2];
     pdl_wait();
     const int r = blockIdx.x, tid = threadIdx.x;
-    // the row's sequence and node
+    const int sub = tid & (LPH - 1), first = tid / LPH;
+    const int half = a.inv_freq ? a.rot / 2 : 0, rot = 2 * half;
+    const bool on = sub * 2 * W < a.dh, turned = sub * W < half;
+    const int ca = turned ? sub * W : rot + (sub * W - half);
+    const int cb = ca + (turned ? half : (a.dh - rot) / 2);
+    const int q_heads = a.q ? a.H : 0, heads = q_heads + 2 * a.Hkv;
+    Run<T, W> x, y;
+    auto fetch = [&](int i) {
+        if (i >= heads || !on) return;
+        const T *src;
+        if (i < q_heads)
+            src = (const T *)a.q + (size_t)r * a.ldq + (size_t)i * a.dh;
+        else if (i < q_heads + a.Hkv)
+            src = (const T *)a.k + (size_t)r * a.ldk + (size_t)(i - q_heads) * a.dh;
+        else
+            src = (const T *)a.v + (size_t)r * a.ldv + (size_t)(i - q_heads - a.Hkv) * a.dh;
+        x.load(src + ca);
+        y.load(src + cb);
+    };
+    fetch(first);
+    // the row's sequence and node; every thread looks them up (the loads are shared)
     int b, n0, n;
     if (a.row_start) {
-        if (tid == 0) {
-            // the last sequence that starts at or before r (row_start ascends)
-            int lo = 0, hi = a.B - 1;
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (a.row_start[mid] <= r) lo = mid; else hi = mid - 1;
-            }
-            s_seq[0] = lo;
+        // the last sequence that starts at or before r (row_start ascends)
+        int lo = 0, hi = a.B - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (a.row_start[mid] <= r) lo = mid; else hi = mid - 1;
         }
-        __syncthreads();
-        b = s_seq[0];
+        b = lo;
         n0 = a.row_start[b];
         n = a.row_start[b + 1] - n0;
     } else {
@@ -56,97 +124,81 @@ __global__ void __launch_bounds__(kThr) append_kernel(const AppendArgs a) {
         n = a.N;
     }
     const int node = r - n0;
-    const int len = a.cache_len[b];
     if (node < 0 || node >= n || node >= a.N) {  // not a row of any sequence
         if (tid == 0 && a.flags && r < a.row_start[a.B]) atomicOr(a.flags, FLAG_BAD_SEQUENCE);
         return;
     }
-    const long long pos = (long long)len + (a.depth ? a.depth[r] : node);
-    const long long slot = (long long)len + node;
-    bool write = true;
+    const int len = a.cache_len[b];
+    const int pos = len + (a.depth ? a.depth[r] : node);
+    bool write = len >= 0 && len < a.cap - node;
     size_t dst = 0;
-    if (len < 0 || slot >= a.cap) {
-        write = false;
+    if (!write) {
         if (tid == 0 && a.flags) atomicOr(a.flags, FLAG_BAD_SEQUENCE);
     } else {
-        const int pi = (int)slot / a.page, pg = a.table[(size_t)b * a.max_pages + pi];
+        const int slot = len + node, pi = slot / a.page;
+        const int pg = a.table[(size_t)b * a.max_pages + pi];
         if (pg < 0 || pg >= a.n_pages) {
             write = false;
             if (tid == 0 && a.flags) atomicOr(a.flags, FLAG_BAD_PAGE);
         } else {
-            dst = (size_t)pg * a.st_page + (size_t)((int)slot - pi * a.page) * a.st_tok;
+            dst = (size_t)pg * a.st_page + (size_t)(slot - pi * a.page) * a.st_tok;
         }
     }
-    const int half = a.inv_freq ? a.rot / 2 : 0;
     for (int i = tid; i < half; i += kThr) {
-        double t = (double)pos * (double)a.inv_freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
-        t -= rint(t);
         float s, c;
-        sincospif(2.f * (float)t, &s, &c);
+        sincospif(2.f * turns(pos, a.inv_freq[i]), &s, &c);
         cs[i] = make_float2(c * a.rope_scale, s * a.rope_scale);
     }
     __syncthreads();
 
-    const int sub = tid & (LPH - 1), first = tid / LPH;
-    const int units = a.dh / 4, rot = 2 * half;
-    const int q_heads = a.q ? a.H : 0;
-    for (int i = first; i < q_heads + 2 * a.Hkv; i += kThr / LPH) {
+    for (int i = first; i < heads; i += kThr / LPH) {
         const bool is_q = i < q_heads, is_v = i >= q_heads + a.Hkv;
         const int h = is_q ? i : (is_v ? i - q_heads - a.Hkv : i - q_heads);
-        const T *src = is_q ? (const T *)a.q + (size_t)r * a.ldq
-                            : (is_v ? (const T *)a.v + (size_t)r * a.ldv
-                                    : (const T *)a.k + (size_t)r * a.ldk);
-        src += (size_t)h * a.dh;
-        float2 x[UPL], y[UPL];
-        int ca[UPL], cb[UPL];
-        float ss = 0.f;
-#pragma unroll
-        for (int j = 0; j < UPL; ++j) {
-            const int u = sub + j * LPH;
-            if (u < units) {
-                const int w = u - half / 2;
-                ca[j] = w < 0 ? 2 * u : rot + 2 * w;
-                cb[j] = ca[j] + (w < 0 ? half : (a.dh - rot) / 2);
-                x[j] = load2(src + ca[j]);
-                y[j] = load2(src + cb[j]);
-                ss += x[j].x * x[j].x + x[j].y * x[j].y + y[j].x * y[j].x + y[j].y * y[j].y;
-            }
-        }
+        float vx[W], vy[W];
+        x.get(vx);
+        y.get(vy);
+        fetch(i + kThr / LPH);
         const T *w = is_v ? nullptr : (const T *)(is_q ? a.wq : a.wk);
-        float f = 1.f;
         if (w) {
-            // the lanes of a head run together; the other half of the warp may be elsewhere
-            const uint32_t group = LPH == 32 ? 0xffffffffu : 0xffffu << (tid & 16);
+            float ss = 0.f;
+            if (on) {
+#pragma unroll
+                for (int j = 0; j < W; ++j) ss = fmaf(vx[j], vx[j], fmaf(vy[j], vy[j], ss));
+            }
+            // the lanes of a head run together; the others of the warp may be elsewhere
+            const uint32_t group =
+                LPH == 32 ? 0xffffffffu : ((1u << LPH) - 1u) << (tid & 31 & ~(LPH - 1));
 #pragma unroll
             for (int o = LPH / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(group, ss, o, LPH);
-            f = 1.f / sqrtf(ss / (float)a.dh + a.eps);
+            const float f = 1.f / sqrtf(ss / (float)a.dh + a.eps);
+            if (on) {
+                Run<T, W> wx, wy;
+                float fx[W], fy[W];
+                wx.load(w + ca);
+                wy.load(w + cb);
+                wx.get(fx);
+                wy.get(fy);
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    vx[j] *= f * fx[j];
+                    vy[j] *= f * fy[j];
+                }
+            }
+        }
+        if (!on || (!is_q && !write)) continue;
+        if (turned && !is_v) {
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+                const float2 z = cs[ca + j];
+                const float p = vx[j], q = vy[j];
+                vx[j] = p * z.x - q * z.y;
+                vy[j] = q * z.x + p * z.y;
+            }
         }
         T *out = is_q ? (T *)a.q_out + ((size_t)r * a.H + h) * a.dh
                       : (T *)(is_v ? a.vp : a.kp) + dst + (size_t)h * a.st_head;
-        if (!is_q && !write) continue;
-#pragma unroll
-        for (int j = 0; j < UPL; ++j) {
-            const int u = sub + j * LPH;
-            if (u < units) {
-                if (w) {
-                    const float2 wx = load2(w + ca[j]), wy = load2(w + cb[j]);
-                    x[j].x *= f * wx.x;
-                    x[j].y *= f * wx.y;
-                    y[j].x *= f * wy.x;
-                    y[j].y *= f * wy.y;
-                }
-                if (!is_v && u < half / 2) {
-                    const float2 c0 = cs[2 * u], c1 = cs[2 * u + 1];
-                    const float2 p = x[j], q = y[j];
-                    x[j].x = p.x * c0.x - q.x * c0.y;
-                    y[j].x = q.x * c0.x + p.x * c0.y;
-                    x[j].y = p.y * c1.x - q.y * c1.y;
-                    y[j].y = q.y * c1.x + p.y * c1.y;
-                }
-                store2(out + ca[j], x[j]);
-                store2(out + cb[j], y[j]);
-            }
-        }
+        Run<T, W>::store(out + ca, vx);
+        Run<T, W>::store(out + cb, vy);
     }
 }
 
@@ -214,10 +266,15 @@ __global__ void __launch_bounds__(256) commit_kernel(const CommitArgs a) {
 }
 
 template <typename T> cudaError_t append_t(const AppendArgs &a, cudaStream_t s) {
-    // 16 lanes hold a head of up to 64 elements, 32 lanes one of up to 128 (or 256)
-    auto *k = a.dh <= 64    ? append_kernel<T, 16, 1>
-              : a.dh <= 128 ? append_kernel<T, 32, 1>
-                            : append_kernel<T, 32, 2>;
+    // 8 elements and their partners to a lane where both halves of a head, and what lies behind the
+    // rotated part, are multiples of 8 elements; else 4
+    const bool wide = a.dh % 16 == 0 && a.rot % 16 == 0;
+    auto *k = wide ? (a.dh <= 64    ? append_kernel<T, 8, 4>
+                      : a.dh <= 128 ? append_kernel<T, 8, 8>
+                                    : append_kernel<T, 8, 16>)
+                   : (a.dh <= 64    ? append_kernel<T, 4, 8>
+                      : a.dh <= 128 ? append_kernel<T, 4, 16>
+                                    : append_kernel<T, 4, 32>);
     return launch_pdl(k, dim3(a.R), dim3(kThr), 0, s, a);
 }
 

@@ -88,7 +88,7 @@ def test_append_and_commit_arguments_are_refused():
     for kw in (dict(P=None), dict(q=nul), dict(q_out=nul), dict(q=odd), dict(ldq=4088),
                dict(q=f, q_out=f, ldq=5120), dict(k=nul), dict(ldk=504), dict(v=odd),
                dict(ldv=516), dict(kp=nul), dict(vp=odd), dict(table=nul), dict(lens=nul),
-               dict(ws=odd), dict(R=2), dict(P=rope(rot_dim=0)), dict(P=rope(rot_dim=6)),
+               dict(ws=odd), dict(R=2), dict(P=rope(rot_dim=0)), dict(P=rope(rot_dim=6)), dict(P=rope(rot_dim=12)),
                dict(P=rope(rot_dim=132)), dict(P=rope(rope_scale=float("inf"))),
                dict(P=rope(eps=-1.0)), dict(P=rope(eps=float("nan"))),
                dict(P=rope(q_weight=0x100008)), dict(P=rope(k_weight=0x100002))):
