@@ -49,6 +49,7 @@ struct Args {
     int prows;       // rows of a partial result: min(rows, N G)
     int qblocks;     // blocks of `rows` rows that N nodes take
     int min_units;   // units of work of a CTA's range at least (two or more)
+    int whole;       // units up to which an item is not cut
 };
 
 struct Seq {
@@ -134,13 +135,15 @@ struct Range {
 };
 
 // Finds the CTA's range (block-wide; every thread gets it). scratch: 34 long longs of shared
-// memory. Each thread sums a run of entries, a block scan places the runs, and the thread
-// whose run holds the range's first unit looks it up.
+// memory. Each thread sums a run of entries, a block scan places the runs, and the threads whose
+// runs hold the range's two boundaries look them up. A boundary inside an item of at most
+// a.whole units moves to the item's start: a piece costs a CTA about as much as that many units
+// (query rows, merge, and a partial result that the combine has to read), whatever its length.
 template <int BN, int HEAVY, int kThreads>
 __device__ __forceinline__ Range attn_plan(const Args &a, int cta, int n_ctas, long long *scratch) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int kWarps = kThreads / 32;
-    static_assert(kWarps <= 28, "scratch holds a sum per warp and the result");
+    static_assert(kWarps <= 24, "scratch holds a sum per warp and the result");
     const int E = a.B * a.qblocks;
     const int per = (E + kThreads - 1) / kThreads;
     const int e0 = min(E, tid * per), e1 = min(E, e0 + per);
@@ -171,29 +174,45 @@ __device__ __forceinline__ Range attn_plan(const Args &a, int cta, int n_ctas, l
     r.quota = max((long long)a.min_units,
                   small ? (long long)(((unsigned)total + n_ctas - 1) / (unsigned)n_ctas)
                         : (total + n_ctas - 1) / n_ctas);
-    const long long start = r.quota * cta;
-    r.left = max(0ll, min(r.quota, total - start));
-    long long at = before + inc - sum;  // first unit of this thread's run
-    int *found = reinterpret_cast<int *>(scratch + 28);
-    if (r.left > 0 && start >= at && start < at + sum) {
+    const long long start = r.quota * cta, end = start + r.quota;
+    const long long run = before + inc - sum;  // first unit of this thread's run
+    // scratch[24 ..]: start's item and offset in it, and how far the end boundary moved back
+    int *found = reinterpret_cast<int *>(scratch + 24);
+#pragma unroll 1
+    for (int which = 0; which < 2; ++which) {
+        const long long u = which ? end : start;
+        if (u >= total || u < run || u >= run + sum) continue;
+        long long at = run;
         for (int e = e0; e < e1; ++e) {
             const int nt = entry_tiles<BN, HEAVY>(a, e, &w);
             const long long item = (long long)nt * w, all = a.Hkv * item;
-            if (start < at + all) {
-                const long long off = start - at;
-                found[0] = e;
+            if (u < at + all) {
+                const long long off = u - at;
                 const long long h = small ? (long long)((unsigned)off / (unsigned)item) : off / item;
-                found[1] = (int)h;
-                scratch[30] = off - h * item;
+                const long long in = off - h * item;
+                if (which) {
+                    scratch[27] = item <= a.whole ? in : 0;
+                } else {
+                    found[0] = e;
+                    found[1] = (int)h;
+                    scratch[25] = item <= a.whole ? 0 : in;
+                    scratch[26] = item <= a.whole ? in : 0;
+                }
                 break;
             }
             at += all;
         }
     }
     __syncthreads();
-    r.e = found[0];
-    r.h = found[1];
-    r.off = scratch[30];
+    r.left = 0;
+    r.e = r.h = 0;
+    r.off = 0;
+    if (start < total) {
+        r.e = found[0];
+        r.h = found[1];
+        r.off = scratch[25];
+        r.left = (end < total ? end - scratch[27] : total) - (start - scratch[26]);
+    }
     return r;
 }
 
@@ -201,6 +220,7 @@ __device__ __forceinline__ Range attn_plan(const Args &a, int cta, int n_ctas, l
 struct Segment {
     Seq s;
     Tiles tl;
+    int e = -1;          // entry: the fields up to rows belong to it
     int b, h, q0, rows;  // rows [q0, q0 + rows) of the sequence
     int t, count;
     bool whole;
@@ -210,12 +230,15 @@ struct Segment {
 template <int BN, int HEAVY>
 __device__ __forceinline__ bool next_segment(const Args &a, Range &r, Segment &g) {
     while (r.left > 0) {
-        g.b = r.e / a.qblocks;
-        g.q0 = (r.e - g.b * a.qblocks) * a.rows;
-        g.s = sequence(a, g.b);
-        g.rows = min(a.rows, g.s.n * a.G - g.q0);
-        g.tl.nt = 0;
-        if (g.rows > 0) g.tl = tiles_of<BN>(a, g.s, g.q0, g.q0 + g.rows);
+        if (g.e != r.e) {  // (the next key/value head of an entry has the same rows and tiles)
+            g.e = r.e;
+            g.b = r.e / a.qblocks;
+            g.q0 = (r.e - g.b * a.qblocks) * a.rows;
+            g.s = sequence(a, g.b);
+            g.rows = min(a.rows, g.s.n * a.G - g.q0);
+            g.tl.nt = 0;
+            if (g.rows > 0) g.tl = tiles_of<BN>(a, g.s, g.q0, g.q0 + g.rows);
+        }
         if (g.tl.nt == 0) {
             ++r.e;
             r.h = 0;

@@ -10,6 +10,8 @@
 // keeps its own running maximum, sum and O for its share of the keys (m16n8k16 products: S has
 // two 8-key tiles, whose exponentials in registers are already the A operand of P V). The four
 // warps' parts are merged when the CTA's piece of the item ends.
+#include <limits.h>
+
 #include <algorithm>
 
 #include "attn.cuh"
@@ -27,7 +29,8 @@ constexpr int kLight = kFewRows + 1;  // every tile has weight one
 template <int DC> struct Shape {
     static constexpr int kRow = DC * 128;           // bytes of a row in shared memory
     static constexpr int kHalf = 16 * kRow;         // K (or V) of a stage
-    static constexpr int kStages = DC == 1 ? 6 : 3;
+    static constexpr int kCtas = DC == 1 ? 3 : 2;   // per SM
+    static constexpr int kStages = 3;
     static constexpr int kRing = kStages * 2 * kHalf;
     static constexpr int kXch = 2 * 16 * DC * 64 * 4;  // two warps' O
     static constexpr int kSmem = kWarps * kRing + kXch;
@@ -77,7 +80,7 @@ struct Cursor {
 };
 
 template <int DC>
-__global__ void __launch_bounds__(kThr, 2) attn_few_kernel(const Args a) {
+__global__ void __launch_bounds__(kThr, Shape<DC>::kCtas) attn_few_kernel(const Args a) {
     using S = Shape<DC>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ long long scratch[34];
@@ -96,22 +99,26 @@ __global__ void __launch_bounds__(kThr, 2) attn_few_kernel(const Args a) {
     ld.start(a, range);
     cp.start(a, range);
     int lstage = 0;
+    // the page of the lane's row in the tile that is copied next, looked up a tile ahead
+    // (INT_MIN: the row is past the sequence's end)
+    int page = INT_MIN, slot = 0;
+    auto look_up = [&]() {
+        page = INT_MIN;
+        if (!ld.on) return;
+        slot = ld.g.tl.at(ld.g.t + ld.t) * kBN + warp * 16 + (lane & 15);
+        if (slot < ld.g.s.L) page = a.table[(size_t)ld.g.b * a.max_pages + slot / a.page];
+    };
+    look_up();
     auto issue = [&]() {  // copies the warp's 16 slots of the next tile, if there is one
         if (ld.on) {
-            const Segment &g = ld.g;
-            const int j = g.tl.at(g.t + ld.t) * kBN + warp * 16 + (lane & 15);
-            long long off = 0;
-            bool ok = j < g.s.L;
-            if (ok) {
-                const int pg = page_of(a, g.b, j);
-                if (pg < 0) {
-                    atomicOr(a.flags, FLAG_BAD_PAGE);
-                    ok = false;
-                } else {
-                    off = (long long)pg * a.st_page + (long long)(j % a.page) * a.st_tok +
-                          (long long)g.h * a.st_head;
-                }
-            }
+            const bool ok = page >= 0 && page < a.n_pages;
+            if (!ok && page != INT_MIN) atomicOr(a.flags, FLAG_BAD_PAGE);
+            const long long off =
+                ok ? (long long)page * a.st_page + (long long)(slot % a.page) * a.st_tok +
+                         (long long)ld.g.h * a.st_head
+                   : 0ll;
+            ld.step(a);
+            look_up();
             const uint32_t have = __ballot_sync(0xffffffffu, ok) & 0xffffu;
             if (lane == 0) s_pages[warp][lstage] = have;
             const uint32_t dst = ring + lstage * 2 * S::kHalf;
@@ -124,7 +131,6 @@ __global__ void __launch_bounds__(kThr, 2) attn_few_kernel(const Args a) {
                 cp16(at, kp + (there ? o : 0), there);
                 cp16(at + S::kHalf, vp + (there ? o : 0), there);
             }
-            ld.step(a);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
         lstage = lstage + 1 == S::kStages ? 0 : lstage + 1;
@@ -414,28 +420,26 @@ __global__ void __launch_bounds__(kThr, 2) attn_few_kernel(const Args a) {
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-template <int DC> cudaError_t launch_dc(const Args &a, int ctas, cudaStream_t s) {
+template <int DC> cudaError_t launch_dc(const Args &a, int nsm, int *ctas, cudaStream_t s) {
+    *ctas = std::min(kMaxCtas, Shape<DC>::kCtas * nsm);
     constexpr int smem = Shape<DC>::kSmem;
-    const cudaError_t err = cudaFuncSetAttribute(
-        attn_few_kernel<DC>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t err = allow_smem(attn_few_kernel<DC>, smem);
     if (err != cudaSuccess) return err;
-    return launch_pdl(attn_few_kernel<DC>, dim3(ctas), dim3(kThr), smem, s, a);
+    return launch_pdl(attn_few_kernel<DC>, dim3(*ctas), dim3(kThr), smem, s, a);
 }
 
 }  // namespace
 
 cudaError_t launch_few(Args a, cudaStream_t s) {
-    int dev = 0, nsm = 0;
-    cudaError_t err = cudaGetDevice(&dev);
-    if (err == cudaSuccess)
-        err = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
-    if (err != cudaSuccess) return err;
-    const int ctas = std::min(kMaxCtas, 2 * nsm);
+    const int nsm = device_sms();
+    if (nsm <= 0) return cudaErrorInvalidDevice;
+    int ctas = 0;
     a.rows = kFewRows;
     a.qblocks = (int)(((long long)a.N * a.G + kFewRows - 1) / kFewRows);
     a.prows = (int)std::min<long long>(a.rows, (long long)a.N * a.G);
     a.min_units = 2;
-    err = a.dh <= 64 ? launch_dc<1>(a, ctas, s) : launch_dc<2>(a, ctas, s);
+    a.whole = 8;
+    cudaError_t err = a.dh <= 64 ? launch_dc<1>(a, nsm, &ctas, s) : launch_dc<2>(a, nsm, &ctas, s);
     if (err != cudaSuccess) return err;
     return launch_combine(a, MOE_DTYPE_BF16, ctas, s);
 }

@@ -324,8 +324,7 @@ template <typename T> cudaError_t combine_t(const Args &a, int n_ctas, cudaStrea
 template <typename T, int NC>
 cudaError_t launch_nc(const Args &a, int nsm, int *ctas, cudaStream_t s) {
     constexpr int smem = simt_smem<NC>();
-    const cudaError_t err = cudaFuncSetAttribute(
-        attn_simt_kernel<T, NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t err = allow_smem(attn_simt_kernel<T, NC>, smem);
     if (err != cudaSuccess) return err;
     // CTAs per SM that shared memory (228 KB, 1 KB of it per CTA) allows, at most four
     *ctas = std::min(kMaxCtas, nsm * std::max(1, std::min(4, (228 * 1024) / (smem + 2048))));
@@ -349,16 +348,15 @@ cudaError_t launch_combine(const Args &a, int dtype, int n_ctas, cudaStream_t s)
 }
 
 cudaError_t launch_simt(Args a, int dtype, cudaStream_t s) {
-    int dev = 0, nsm = 0, ctas = 0;
-    cudaError_t err = cudaGetDevice(&dev);
-    if (err == cudaSuccess)
-        err = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
-    if (err != cudaSuccess) return err;
+    const int nsm = device_sms();
+    if (nsm <= 0) return cudaErrorInvalidDevice;
+    int ctas = 0;
     a.rows = kSimtRows;
     a.qblocks = (int)(((long long)a.N * a.G + kSimtRows - 1) / kSimtRows);
     a.prows = (int)std::min<long long>(a.rows, (long long)a.N * a.G);
     a.min_units = 4;
-    err = dtype == MOE_DTYPE_BF16 ? launch_t<__nv_bfloat16>(a, nsm, &ctas, s)
+    a.whole = 6;
+    cudaError_t err = dtype == MOE_DTYPE_BF16 ? launch_t<__nv_bfloat16>(a, nsm, &ctas, s)
                                   : launch_t<float>(a, nsm, &ctas, s);
     if (err != cudaSuccess) return err;
     return launch_combine(a, dtype, ctas, s);

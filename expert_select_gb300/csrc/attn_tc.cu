@@ -76,24 +76,6 @@ __device__ __forceinline__ void softmax_bar() {  // the 256 threads of warps 4-1
     asm volatile("bar.sync 1, 256;" ::: "memory");
 }
 
-// Pairs of fp32 values, two to an instruction.
-__device__ __forceinline__ void pack2(uint64_t &d, float lo, float hi) {
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float &lo, float &hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(x), "l"(y), "l"(z));
-    return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
-    return d;
-}
-
 // Position of a tile in the ring of K (or V) stages: counts up over the CTA's segments.
 template <int NS> struct Slot {
     static __device__ __forceinline__ int stage(uint32_t pos) { return (int)(pos % NS); }
@@ -587,28 +569,22 @@ attn_tc_kernel(const __grid_constant__ Params p) {
                         }
                     }
                     const float sub = m == -INFINITY ? 0.f : -m * cs;
-                    uint64_t cs2, sub2, sum[2] = {0ull, 0ull};
-                    pack2(cs2, cs, cs);
-                    pack2(sub2, sub, sub);
+                    const uint64_t cs2 = pack2(cs, cs), sub2 = pack2(sub, sub);
+                    uint64_t sum[2] = {0ull, 0ull};
                     uint32_t pk[32];
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
-                        uint64_t t2;
-                        float p0, p1;
-                        pack2(t2, __uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
-                        t2 = fma2(t2, cs2, sub2);
-                        unpack2(t2, p0, p1);
-                        p0 = ex2(p0);
-                        p1 = ex2(p1);
-                        pack2(t2, p0, p1);
-                        sum[i & 1] = add2(sum[i & 1], t2);
+                        const float2 e = unpack2(fma2(
+                            pack2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), cs2,
+                            sub2));
+                        const float p0 = ex2(e.x), p1 = ex2(e.y);
+                        sum[i & 1] = add2(sum[i & 1], pack2(p0, p1));
                         pk[i] = pack_bf16(p0, p1);
                     }
                     tmem_st32(tS, pk);
                     tmem_wait_st();
-                    float s0, s1;
-                    unpack2(add2(sum[0], sum[1]), s0, s1);
-                    l += s0 + s1;
+                    const float2 st = unpack2(add2(sum[0], sum[1]));
+                    l += st.x + st.y;
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -772,8 +748,7 @@ bool encode_pool(CUtensorMap *m, const void *base, const Args &a, int box) {
 
 template <int DC> cudaError_t launch_dc(Params &p, int ctas, cudaStream_t s) {
     constexpr int smem = 1024 + kCtlBytes + (stages<DC>() + 2) * DC * 16384;
-    const cudaError_t err = cudaFuncSetAttribute(
-        attn_tc_kernel<DC>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t err = allow_smem(attn_tc_kernel<DC>, smem);
     if (err != cudaSuccess) return err;
     return launch_pdl(attn_tc_kernel<DC>, dim3(ctas), dim3(kThreads), smem, s, p);
 }
@@ -781,32 +756,25 @@ template <int DC> cudaError_t launch_dc(Params &p, int ctas, cudaStream_t s) {
 }  // namespace
 
 bool tc_supported(const Args &a, int dtype) {
-    if (dtype != MOE_DTYPE_BF16 || a.dh > 128) return false;
-    int dev = 0, major = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return false;
-    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess)
-        return false;
-    return major >= 10 && encode_fn() != nullptr;
+    return dtype == MOE_DTYPE_BF16 && a.dh <= 128 && encode_fn() != nullptr;
 }
 
 cudaError_t launch_tc(Args a, cudaStream_t s) {
-    int dev = 0, nsm = 0;
-    cudaError_t err = cudaGetDevice(&dev);
-    if (err == cudaSuccess)
-        err = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
-    if (err != cudaSuccess) return err;
+    const int nsm = device_sms();
+    if (nsm <= 0) return cudaErrorInvalidDevice;
     const int ctas = std::min(nsm, kTcMaxCtas);
     a.rows = kTcRows;
     a.qblocks = (int)(((long long)a.N * a.G + kTcRows - 1) / kTcRows);
     a.prows = (int)std::min<long long>(a.rows, (long long)a.N * a.G);
     a.min_units = 4;
+    a.whole = 8;
     Params p{};
     p.a = a;
     p.box = 1;
     while (p.box < kBN && a.page % (2 * p.box) == 0) p.box *= 2;
     if (!encode_pool(&p.kmap, a.k, a, p.box) || !encode_pool(&p.vmap, a.v, a, p.box))
         return cudaErrorInvalidValue;
-    err = a.dh <= 64 ? launch_dc<1>(p, ctas, s) : launch_dc<2>(p, ctas, s);
+    cudaError_t err = a.dh <= 64 ? launch_dc<1>(p, ctas, s) : launch_dc<2>(p, ctas, s);
     if (err != cudaSuccess) return err;
     return launch_combine(a, MOE_DTYPE_BF16, ctas, s);
 }

@@ -83,7 +83,7 @@ __device__ __forceinline__ float turns(int pos, float freq) {
 // through). The next heads' elements are on their way while a pass is computed.
 template <typename T, int W, int LPH>
 __global__ void __launch_bounds__(kThr) append_kernel(const AppendArgs a) {
-    __shared__ float2 cs[128];  // cos, sin of the rot / 2 <= 128 angles
+    __shared__ __align__(16) float s_cos[128], s_sin[128];  // of the rot / 2 <= 128 angles
     pdl_wait();
     const int r = blockIdx.x, tid = threadIdx.x;
     const int sub = tid & (LPH - 1), first = tid / LPH;
@@ -147,7 +147,8 @@ __global__ void __launch_bounds__(kThr) append_kernel(const AppendArgs a) {
     for (int i = tid; i < half; i += kThr) {
         float s, c;
         sincospif(2.f * turns(pos, a.inv_freq[i]), &s, &c);
-        cs[i] = make_float2(c * a.rope_scale, s * a.rope_scale);
+        s_cos[i] = c * a.rope_scale;
+        s_sin[i] = s * a.rope_scale;
     }
     __syncthreads();
 
@@ -188,11 +189,16 @@ __global__ void __launch_bounds__(kThr) append_kernel(const AppendArgs a) {
         if (!on || (!is_q && !write)) continue;
         if (turned && !is_v) {
 #pragma unroll
-            for (int j = 0; j < W; ++j) {
-                const float2 z = cs[ca + j];
-                const float p = vx[j], q = vy[j];
-                vx[j] = p * z.x - q * z.y;
-                vy[j] = q * z.x + p * z.y;
+            for (int j = 0; j < W; j += 4) {
+                const float4 c4 = *reinterpret_cast<const float4 *>(s_cos + ca + j);
+                const float4 s4 = *reinterpret_cast<const float4 *>(s_sin + ca + j);
+                const float cz[4] = {c4.x, c4.y, c4.z, c4.w}, sz[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    const float p = vx[j + z], q = vy[j + z];
+                    vx[j + z] = p * cz[z] - q * sz[z];
+                    vy[j + z] = q * cz[z] + p * sz[z];
+                }
             }
         }
         T *out = is_q ? (T *)a.q_out + ((size_t)r * a.H + h) * a.dh

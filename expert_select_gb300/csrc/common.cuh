@@ -6,6 +6,7 @@
 #include <stdint.h>
 #include <stddef.h>
 
+#include <atomic>
 #include <utility>
 
 #include "moetree.h"
@@ -218,11 +219,75 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
+// SMs of the current device (0 on error), asked for once per device.
+inline int device_sms(int *device = nullptr) {
+    constexpr int kMaxDevices = 64;
+    static std::atomic<int> sms[kMaxDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+    if (device) *device = dev;
+    int n = sms[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+        sms[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
+// Lets a kernel use `bytes` of dynamic shared memory, once per kernel and device.
+template <typename... KArgs> inline cudaError_t allow_smem(void (*kernel)(KArgs...), int bytes) {
+    constexpr int kSlots = 64;
+    static std::atomic<void *> seen[kSlots][64];  // kernels of this signature, per device
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    int at = 0;
+    for (; dev < 64 && at < kSlots; ++at) {
+        void *p = seen[at][dev].load(std::memory_order_acquire);
+        if (p == (void *)kernel) return cudaSuccess;
+        if (!p) break;
+    }
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    // (two threads may set the attribute at once: it is the same value)
+    if (err == cudaSuccess && dev < 64 && at < kSlots) {
+        void *none = nullptr;
+        seen[at][dev].compare_exchange_strong(none, (void *)kernel, std::memory_order_release);
+    }
+    return err;
+}
+
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // ---- device helpers ----
 __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+
+// Pairs of fp32 values in a 64-bit register, two to an instruction.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(x), "l"(y), "l"(z));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+    return d;
+}
 
 // Loads 8 consecutive elements starting at element `i` of a row as fp32.
 // bf16: one 16-byte load; fp32: two 16-byte loads. `p` must be 16-byte aligned at i.

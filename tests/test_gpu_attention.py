@@ -622,6 +622,8 @@ def _norm_ref(x, o, w_post, gate, gate_rows, scale, w_pre, eps):
 
 NORMS = [(1, 8, True, 0, 1.0, True), (65, 2048, True, 0, 1.0, True),
          (37, 264, False, 37, 0.5, True), (300, 2880, True, 7, -2.0, False),
+         (1300, 2880, True, 700, 0.5, True), (2000, 136, True, 0, 1.0, True),
+         (1217, 4096, False, 1217, 1.5, False), (1500, 1032, True, 3, 1.0, True),
          (33, 6144, True, 1, 0.25, True), (5, 4104, False, 0, 1.0, False)]
 
 
@@ -658,8 +660,10 @@ def test_block_norm_matches_64_bits(dtype, R, d, post, gate_rows, scale, pre):
 
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
 @pytest.mark.parametrize("eps", [1e-6, 0.0])
-def test_block_norm_rows_at_the_ends_of_the_range(dtype, eps):
-    """Rows whose squares overflow or vanish in fp32, zero rows and a single large element."""
+@pytest.mark.parametrize("times", [1, 200])
+def test_block_norm_rows_at_the_ends_of_the_range(dtype, eps, times):
+    """Rows whose squares overflow or vanish in fp32, zero rows and a single large element; few
+    rows and many (another kernel)."""
     d = 512
     L = M.layer_desc(d, 8, 1, 64, dtype)
     g = torch.Generator().manual_seed(3)
@@ -672,7 +676,7 @@ def test_block_norm_rows_at_the_ends_of_the_range(dtype, eps):
     x[5] *= 1e-18
     x[6, :] = 1e-20
     x[6, 3] = 1e25
-    x = x.to(dtype)
+    x = x.to(dtype).repeat(times, 1)
     hn, h2 = torch.empty_like(x, device=DEV), torch.empty_like(x, device=DEV)
     ones = torch.ones(d, dtype=dtype, device=DEV)
     M.moe_block_norm(L, x.to(DEV), None, None, hn, eps=eps)
