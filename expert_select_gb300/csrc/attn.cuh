@@ -48,7 +48,7 @@ struct Args {
     int rows;        // rows of an item (of the launched kernel)
     int prows;       // rows of a partial result: min(rows, N G)
     int qblocks;     // blocks of `rows` rows that N nodes take
-    int min_units;   // units of work of a CTA's range at least (two or more)
+    int min_units;   // units of work of a CTA's range at least (a tile's weight or more)
     int whole;       // units up to which an item is not cut
 };
 
@@ -108,17 +108,18 @@ __device__ __forceinline__ Tiles tiles_of(const Args &a, const Seq &s, int q0, i
     return t;
 }
 
-// Tiles of an entry's items, and the weight of one: a tile of 256 rows is twice the work of one of
-// 128 (HEAVY: rows from which a tile counts two).
+// Tiles of an entry's items, and the weight of one. HEAVY: rows from which a tile costs the
+// tensor-core kernel 4 units of work instead of 3 (1.0 us for two 128-row tiles, which share the
+// copies of K and V, against 0.75 us for one); 0: every tile is one unit.
 template <int BN, int HEAVY>
 __device__ __forceinline__ int entry_tiles(const Args &a, int e, int *w, int *bad = nullptr) {
     const int b = e / a.qblocks, q0 = (e - b * a.qblocks) * a.rows;
     const Seq s = sequence(a, b, bad);
     const int rows = s.n * a.G;
-    *w = 1;
+    *w = HEAVY ? 3 : 1;
     if (q0 >= rows) return 0;
     const int q1 = min(rows, q0 + a.rows);
-    if (q1 - q0 >= HEAVY) *w = 2;
+    if (HEAVY && q1 - q0 >= HEAVY) *w = 4;
     return tiles_of<BN>(a, s, q0, q1).nt;
 }
 
@@ -148,9 +149,9 @@ __device__ __forceinline__ Range attn_plan(const Args &a, int cta, int n_ctas, l
     const int per = (E + kThreads - 1) / kThreads;
     const int e0 = min(E, tid * per), e1 = min(E, e0 + per);
     long long sum = 0;
-    int bad = 0, w;
+    int bad = 0, w = 1, nt = 0;
     for (int e = e0; e < e1; ++e) {
-        const int nt = entry_tiles<BN, HEAVY>(a, e, &w, &bad);
+        nt = entry_tiles<BN, HEAVY>(a, e, &w, &bad);
         sum += (long long)a.Hkv * nt * w;
     }
     if (bad) atomicOr(a.flags, FLAG_BAD_SEQUENCE);
@@ -184,7 +185,7 @@ __device__ __forceinline__ Range attn_plan(const Args &a, int cta, int n_ctas, l
         if (u >= total || u < run || u >= run + sum) continue;
         long long at = run;
         for (int e = e0; e < e1; ++e) {
-            const int nt = entry_tiles<BN, HEAVY>(a, e, &w);
+            if (per > 1) nt = entry_tiles<BN, HEAVY>(a, e, &w);
             const long long item = (long long)nt * w, all = a.Hkv * item;
             if (u < at + all) {
                 const long long off = u - at;
@@ -245,11 +246,15 @@ __device__ __forceinline__ bool next_segment(const Args &a, Range &r, Segment &g
             r.off = 0;
             continue;
         }
-        const int sh = g.rows >= HEAVY ? 1 : 0;  // log2 of the weight
-        const long long item = (long long)g.tl.nt << sh, end = min(item, r.off + r.left);
+        const bool heavy = HEAVY && g.rows >= HEAVY;
+        const long long item = (long long)g.tl.nt * (HEAVY ? (heavy ? 4 : 3) : 1);
+        const long long end = min(item, r.off + r.left);
+        auto tile = [&](long long u) {  // tiles below unit u of an item (items have < 2^31 units)
+            return HEAVY ? (int)(heavy ? (unsigned)u / 4u : (unsigned)u / 3u) : (int)u;
+        };
         g.h = r.h;
-        g.t = (int)(r.off >> sh);
-        g.count = (int)(end >> sh) - g.t;
+        g.t = tile(r.off);
+        g.count = tile(end) - g.t;
         g.whole = g.t == 0 && g.count == g.tl.nt;
         r.left -= end - r.off;
         r.off = 0;

@@ -24,7 +24,7 @@ namespace {
 constexpr int kBN = 64;     // slots of a tile
 constexpr int kWarps = 4;   // 16 slots each
 constexpr int kThr = 32 * kWarps;
-constexpr int kLight = kFewRows + 1;  // every tile has weight one
+constexpr int kLight = 0;  // every tile is one unit of work
 
 template <int DC> struct Shape {
     static constexpr int kRow = DC * 128;           // bytes of a row in shared memory

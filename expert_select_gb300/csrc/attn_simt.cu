@@ -18,7 +18,7 @@ namespace {
 
 constexpr int kBN = 32;
 constexpr int kThr = 128;
-constexpr int kLight = kSimtRows + 1;  // every tile has weight one
+constexpr int kLight = 0;  // every tile is one unit of work
 
 // NC: 64-column chunks of the head size (dh <= 64 NC).
 template <int NC> constexpr int simt_smem() {

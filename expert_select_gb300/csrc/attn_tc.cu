@@ -766,8 +766,8 @@ cudaError_t launch_tc(Args a, cudaStream_t s) {
     a.rows = kTcRows;
     a.qblocks = (int)(((long long)a.N * a.G + kTcRows - 1) / kTcRows);
     a.prows = (int)std::min<long long>(a.rows, (long long)a.N * a.G);
-    a.min_units = 4;
-    a.whole = 8;
+    a.min_units = 32;
+    a.whole = 16;
     Params p{};
     p.a = a;
     p.box = 1;
