@@ -18,7 +18,7 @@ WsLayout ws_layout(int dh, long long rows_per_seq) {
                  (size_t)kTcMaxCtas * std::min<long long>(kTcRows, rows_per_seq));
     WsLayout w{};
     w.rec = kHeadBytes;
-    w.ml = align256(w.rec + (size_t)kMaxCtas * 8 * sizeof(int));
+    w.ml = align256(w.rec + (size_t)kMaxCtas * 4 * sizeof(int));
     w.o = align256(w.ml + rows * 2 * 2 * sizeof(float));
     w.total = align256(w.o + rows * 2 * dh * sizeof(float));
     return w;

@@ -37,7 +37,7 @@ struct Args {
     void *out;
     float *lse;
     int *flags;      // check word
-    int *rec;        // [kMaxCtas][8]: the item a CTA's range begins inside (see attn_combine)
+    int *rec;        // [kMaxCtas][4]: items that were cut (see attn_combine)
     float *part_o;   // [CTAs][2][prows][dh]
     float *part_ml;  // [CTAs][2][prows][2]
     int B, N, R, H, Hkv, G, dh;
@@ -125,26 +125,54 @@ __device__ __forceinline__ int entry_tiles(const Args &a, int e, int *w, int *ba
 
 // A CTA's range of work, from `off` units into the item (entry e, key/value head h), where entry
 // e = sequence * qblocks + block of rows. Tile t of an item of weight w is the units w t ..
-// w t + w - 1; it belongs to one CTA: a boundary at
-// unit u of the item lies before tile floor(u / w), for the range that ends there and for the one
-// that begins.
+// w t + w - 1; it belongs to one CTA: a boundary at unit u of the item lies before tile
+// floor(u / w), for the range that ends there and for the one that begins.
 struct Range {
-    long long quota;  // units of a range
     int e, h;
-    long long off;    // the range's first unit within the item
-    long long left;   // units from there to the range's end
+    long long off;   // the range's first unit within the item
+    long long left;  // units from there to the range's end
+    int parts;       // if the item's second part begins this range: the parts of the item; else 0
 };
 
+// Block-wide exclusive sum of `v` (and the total), over kWarps warps; scratch: kWarps long longs.
+template <int kWarps>
+__device__ __forceinline__ long long block_scan(long long v, long long *scratch, long long *total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += u;
+    }
+    if (lane == 31) scratch[warp] = inc;
+    __syncthreads();
+    long long before = 0, all = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+        if (i < warp) before += scratch[i];
+        all += scratch[i];
+    }
+    *total = all;
+    return before + inc - v;
+}
+
 // Finds the CTA's range (block-wide; every thread gets it). scratch: 34 long longs of shared
-// memory. Each thread sums a run of entries, a block scan places the runs, and the threads whose
-// runs hold the range's two boundaries look them up. A boundary inside an item of at most
-// a.whole units moves to the item's start: a piece costs a CTA about as much as that many units
-// (query rows, merge, and a partial result that the combine has to read), whatever its length.
+// memory. Each thread sums a run of entries and a block scan places the runs; the threads whose
+// runs hold the range's boundaries look them up.
+//
+// A piece of an item costs a CTA several tiles' time besides its tiles (query rows, the pipeline's
+// start and end, the output, and a partial result that the combine has to read). Two rules keep
+// pieces few:
+//  - where every item can have round(item / quota) CTAs of its own, it gets them, in equal parts,
+//    and a CTA has one piece (a few long items: one tree of 65 nodes over 4k tokens took 31 us so
+//    and 38 us with ranges that cross items);
+//  - else, ranges of equal length, but a boundary inside an item of at most a.whole units moves to
+//    the item's start.
 template <int BN, int HEAVY, int kThreads>
 __device__ __forceinline__ Range attn_plan(const Args &a, int cta, int n_ctas, long long *scratch) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x;
     constexpr int kWarps = kThreads / 32;
-    static_assert(kWarps <= 24, "scratch holds a sum per warp and the result");
+    static_assert(kWarps <= 12, "scratch holds two sums per warp and the result");
     const int E = a.B * a.qblocks;
     const int per = (E + kThreads - 1) / kThreads;
     const int e0 = min(E, tid * per), e1 = min(E, e0 + per);
@@ -155,30 +183,38 @@ __device__ __forceinline__ Range attn_plan(const Args &a, int cta, int n_ctas, l
         sum += (long long)a.Hkv * nt * w;
     }
     if (bad) atomicOr(a.flags, FLAG_BAD_SEQUENCE);
-    long long inc = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += v;
-    }
-    if (lane == 31) scratch[warp] = inc;
-    __syncthreads();
-    long long before = 0, total = 0;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-        if (i < warp) before += scratch[i];
-        total += scratch[i];
-    }
-    Range r;
+    int *found = reinterpret_cast<int *>(scratch + 24);
+    if (tid == 0) found[8] = 0;
+    long long total;
+    const long long run = block_scan<kWarps>(sum, scratch, &total);  // the run's first unit
     // (64-bit divisions take hundreds of cycles: only where the numbers need them)
     const bool small = total < (1ll << 30);
-    r.quota = max((long long)a.min_units,
-                  small ? (long long)(((unsigned)total + n_ctas - 1) / (unsigned)n_ctas)
-                        : (total + n_ctas - 1) / n_ctas);
-    const long long start = r.quota * cta, end = start + r.quota;
-    const long long run = before + inc - sum;  // first unit of this thread's run
-    // scratch[24 ..]: start's item and offset in it, and how far the end boundary moved back
-    int *found = reinterpret_cast<int *>(scratch + 24);
+    const long long quota =
+        max((long long)a.min_units, small ? (long long)(((unsigned)total + n_ctas - 1) / (unsigned)n_ctas)
+                                          : (total + n_ctas - 1) / n_ctas);
+    // scratch[24 ..]: the item, the offset in it, how far the two boundaries moved back, parts
+    if (per == 1 && small) {
+        const unsigned item = (unsigned)nt * w;
+        const int k = min(max(1, (int)((item + quota / 2) / (unsigned)quota)), nt);  // CTAs per item
+        long long ctas;
+        const long long first = block_scan<kWarps>((long long)a.Hkv * k, scratch + 12, &ctas);
+        if (ctas <= n_ctas) {
+            if (cta >= first && cta < first + (long long)a.Hkv * k) {
+                const int local = cta - (int)first, h = local / k, j = local - h * k;
+                const int t0 = (int)((long long)nt * j / k), t1 = (int)((long long)nt * (j + 1) / k);
+                found[0] = tid;
+                found[1] = h;
+                scratch[25] = (long long)t0 * w;
+                scratch[26] = (long long)(t1 - t0) * w;
+                found[8] = j == 1 ? k : 0;
+            }
+            __syncthreads();
+            Range r{0, 0, 0, 0, 0};
+            if (cta < ctas) r = {found[0], found[1], scratch[25], scratch[26], found[8]};
+            return r;
+        }
+    }
+    const long long start = quota * cta, end = start + quota;
 #pragma unroll 1
     for (int which = 0; which < 2; ++which) {
         const long long u = which ? end : start;
@@ -198,6 +234,9 @@ __device__ __forceinline__ Range attn_plan(const Args &a, int cta, int n_ctas, l
                     found[1] = (int)h;
                     scratch[25] = item <= a.whole ? 0 : in;
                     scratch[26] = item <= a.whole ? in : 0;
+                    // the first boundary inside an item that leaves tiles before it
+                    if (item > a.whole && in >= w && in - quota < w)
+                        found[8] = 1 + (int)((item - in + quota - 1) / quota);
                 }
                 break;
             }
@@ -205,15 +244,10 @@ __device__ __forceinline__ Range attn_plan(const Args &a, int cta, int n_ctas, l
         }
     }
     __syncthreads();
-    r.left = 0;
-    r.e = r.h = 0;
-    r.off = 0;
-    if (start < total) {
-        r.e = found[0];
-        r.h = found[1];
-        r.off = scratch[25];
-        r.left = (end < total ? end - scratch[27] : total) - (start - scratch[26]);
-    }
+    Range r{0, 0, 0, 0, 0};
+    if (start < total)
+        r = {found[0], found[1], scratch[25],
+             (end < total ? end - scratch[27] : total) - (start - scratch[26]), found[8]};
     return r;
 }
 
@@ -273,22 +307,12 @@ __device__ __forceinline__ size_t part_row(const Args &a, int cta, const Segment
     return ((size_t)cta * 2 + (g.t == 0 ? 1 : 0)) * a.prows + row;
 }
 
-// Record for attn_combine: the item in which this CTA's range begins, if not at its start.
-template <int BN, int HEAVY>
+// Record for attn_combine: the item whose second part begins this CTA's range, and its parts.
 __device__ __forceinline__ void write_record(const Args &a, int cta, const Range &r) {
-    int *rec = a.rec + cta * 8;
-    if (r.left <= 0 || r.off == 0) {
-        rec[0] = -1;
-        return;
-    }
-    int w;
-    const int nt = entry_tiles<BN, HEAVY>(a, r.e, &w);
-    rec[0] = r.off >= w ? r.e : -1;
+    int *rec = a.rec + cta * 4;
+    rec[0] = r.e;
     rec[1] = r.h;
-    rec[2] = nt;
-    rec[3] = w;
-    reinterpret_cast<long long *>(rec)[2] = r.quota;
-    reinterpret_cast<long long *>(rec)[3] = r.off;
+    rec[2] = r.left > 0 ? r.parts : 0;
 }
 
 // Bits of visible slots among [k0, k0 + 32) for the query node `node`, at position pos.

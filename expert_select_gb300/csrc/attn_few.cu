@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kThr, Shape<DC>::kCtas) attn_few_kernel(const 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_wait();
     const Range range = attn_plan<kBN, kLight, kThr>(a, blockIdx.x, gridDim.x, scratch);
-    if (threadIdx.x == 0) write_record<kBN, kLight>(a, blockIdx.x, range);
+    if (threadIdx.x == 0) write_record(a, blockIdx.x, range);
     const uint32_t ring = tc::smem_u32(smem) + warp * S::kRing;
     uint8_t *gring = smem + warp * S::kRing;
     float *xch = reinterpret_cast<float *>(smem + kWarps * S::kRing);

@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(kThr) attn_simt_kernel(const Args a) {
     const int tid = threadIdx.x, tr = tid >> 4, tk = tid & 15;
     pdl_wait();
     Range r = attn_plan<kBN, kLight, kThr>(a, blockIdx.x, gridDim.x, scratch);
-    if (tid == 0) write_record<kBN, kLight>(a, blockIdx.x, r);
+    if (tid == 0) write_record(a, blockIdx.x, r);
     const T *q = (const T *)a.q, *kp = (const T *)a.k, *vp = (const T *)a.v;
     Segment g;
     while (next_segment<kBN, kLight>(a, r, g)) {
@@ -218,9 +218,9 @@ __global__ void __launch_bounds__(kThr) attn_simt_kernel(const Args a) {
     }
 }
 
-// Merges a cut item: block (c, y) looks at the item inside which CTA c's range begins. The
-// item's first tiles are in slot 1 of the CTA before, the rest in slot 0 of CTAs c, c + 1, ...;
-// the block of the first such c merges the item's rows:
+// Merges a cut item: block (c, y) looks at CTA c's record, of the item whose second part begins
+// CTA c's range. The item's first part is in slot 1 of CTA c - 1, the others in slot 0 of CTAs
+// c, c + 1, ...:
 //   sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i,  M the largest m_i.
 // WPR warps share a row (8 / WPR rows per block), warp w taking the parts w, w + WPR, ... in
 // order: a single long sequence leaves a few rows in many parts, whose reads must not queue up
@@ -230,22 +230,16 @@ __global__ void __launch_bounds__(256) attn_combine_kernel(const Args a) {
     __shared__ float s_o[WPR > 1 ? 8 : 1][256], s_ml[8][2];
     pdl_wait();
     const int c = blockIdx.x;
-    const int *rec = a.rec + c * 8;
-    const int e = rec[0];
-    if (c == 0 || e < 0) return;
-    const int h = rec[1];
-    const long long w_tile = rec[3], units = rec[2] * w_tile;
-    const long long quota = reinterpret_cast<const long long *>(rec)[2];
-    const long long off = reinterpret_cast<const long long *>(rec)[3];
-    if (off - quota >= w_tile) return;  // an earlier CTA's range begins inside the item too
+    const int4 rec = *reinterpret_cast<const int4 *>(a.rec + c * 4);
+    if (rec.z == 0) return;
+    const int e = rec.x, h = rec.y;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = warp % WPR;
     const int b = e / a.qblocks, q0 = (e - b * a.qblocks) * a.rows;
     const Seq s = sequence(a, b);
     const int row = blockIdx.y * (8 / WPR) + warp / WPR;
     const bool live = row < min(a.rows, s.n * a.G - q0);
     if (WPR == 1 && !live) return;
-    // parts: CTA c - 1, then as many as the units from off on take
-    const int parts = live ? 1 + (int)((units - off + quota - 1) / quota) : 0;
+    const int parts = live ? rec.z : 0;
     auto part = [&](int i) { return ((size_t)(c - 1 + i) * 2 + (i == 0)) * a.prows + row; };
     float M = -INFINITY;
     for (int i = lane; i < parts; i += 32) {
@@ -354,7 +348,7 @@ cudaError_t launch_simt(Args a, int dtype, cudaStream_t s) {
     a.rows = kSimtRows;
     a.qblocks = (int)(((long long)a.N * a.G + kSimtRows - 1) / kSimtRows);
     a.prows = (int)std::min<long long>(a.rows, (long long)a.N * a.G);
-    a.min_units = 4;
+    a.min_units = 2;
     a.whole = 6;
     cudaError_t err = dtype == MOE_DTYPE_BF16 ? launch_t<__nv_bfloat16>(a, nsm, &ctas, s)
                                   : launch_t<float>(a, nsm, &ctas, s);

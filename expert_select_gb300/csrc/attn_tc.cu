@@ -175,7 +175,7 @@ attn_tc_kernel(const __grid_constant__ Params p) {
     pdl_wait();
     const uint32_t tmem = c.tmem;
     Range r = attn_plan<kBN, kHeavy, kThreads>(a, blockIdx.x, gridDim.x, c.scratch);
-    if (threadIdx.x == 64) write_record<kBN, kHeavy>(a, blockIdx.x, r);
+    if (threadIdx.x == 64) write_record(a, blockIdx.x, r);
 
     uint32_t issued = 0, last_par = 0;  // producer: stages with a load issued, parity of the last
     bool mma_issued = false;
@@ -766,7 +766,7 @@ cudaError_t launch_tc(Args a, cudaStream_t s) {
     a.rows = kTcRows;
     a.qblocks = (int)(((long long)a.N * a.G + kTcRows - 1) / kTcRows);
     a.prows = (int)std::min<long long>(a.rows, (long long)a.N * a.G);
-    a.min_units = 32;
+    a.min_units = 24;
     a.whole = 16;
     Params p{};
     p.a = a;
