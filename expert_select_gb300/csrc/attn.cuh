@@ -172,7 +172,7 @@ template <int BN, int HEAVY, int kThreads>
 __device__ __forceinline__ Range attn_plan(const Args &a, int cta, int n_ctas, long long *scratch) {
     const int tid = threadIdx.x;
     constexpr int kWarps = kThreads / 32;
-    static_assert(kWarps <= 12, "scratch holds two sums per warp and the result");
+    static_assert(2 * kWarps <= 28, "scratch holds two sums per warp and the result");
     const int E = a.B * a.qblocks;
     const int per = (E + kThreads - 1) / kThreads;
     const int e0 = min(E, tid * per), e1 = min(E, e0 + per);
@@ -183,7 +183,7 @@ __device__ __forceinline__ Range attn_plan(const Args &a, int cta, int n_ctas, l
         sum += (long long)a.Hkv * nt * w;
     }
     if (bad) atomicOr(a.flags, FLAG_BAD_SEQUENCE);
-    int *found = reinterpret_cast<int *>(scratch + 24);
+    int *found = reinterpret_cast<int *>(scratch + 28);
     if (tid == 0) found[8] = 0;
     long long total;
     const long long run = block_scan<kWarps>(sum, scratch, &total);  // the run's first unit
@@ -192,25 +192,25 @@ __device__ __forceinline__ Range attn_plan(const Args &a, int cta, int n_ctas, l
     const long long quota =
         max((long long)a.min_units, small ? (long long)(((unsigned)total + n_ctas - 1) / (unsigned)n_ctas)
                                           : (total + n_ctas - 1) / n_ctas);
-    // scratch[24 ..]: the item, the offset in it, how far the two boundaries moved back, parts
+    // scratch[28 ..]: the item, the offset in it, how far the two boundaries moved back, parts
     if (per == 1 && small) {
         const unsigned item = (unsigned)nt * w;
         const int k = min(max(1, (int)((item + quota / 2) / (unsigned)quota)), nt);  // CTAs per item
         long long ctas;
-        const long long first = block_scan<kWarps>((long long)a.Hkv * k, scratch + 12, &ctas);
+        const long long first = block_scan<kWarps>((long long)a.Hkv * k, scratch + 14, &ctas);
         if (ctas <= n_ctas) {
             if (cta >= first && cta < first + (long long)a.Hkv * k) {
                 const int local = cta - (int)first, h = local / k, j = local - h * k;
                 const int t0 = (int)((long long)nt * j / k), t1 = (int)((long long)nt * (j + 1) / k);
                 found[0] = tid;
                 found[1] = h;
-                scratch[25] = (long long)t0 * w;
-                scratch[26] = (long long)(t1 - t0) * w;
+                scratch[29] = (long long)t0 * w;
+                scratch[30] = (long long)(t1 - t0) * w;
                 found[8] = j == 1 ? k : 0;
             }
             __syncthreads();
             Range r{0, 0, 0, 0, 0};
-            if (cta < ctas) r = {found[0], found[1], scratch[25], scratch[26], found[8]};
+            if (cta < ctas) r = {found[0], found[1], scratch[29], scratch[30], found[8]};
             return r;
         }
     }
@@ -228,12 +228,12 @@ __device__ __forceinline__ Range attn_plan(const Args &a, int cta, int n_ctas, l
                 const long long h = small ? (long long)((unsigned)off / (unsigned)item) : off / item;
                 const long long in = off - h * item;
                 if (which) {
-                    scratch[27] = item <= a.whole ? in : 0;
+                    scratch[31] = item <= a.whole ? in : 0;
                 } else {
                     found[0] = e;
                     found[1] = (int)h;
-                    scratch[25] = item <= a.whole ? 0 : in;
-                    scratch[26] = item <= a.whole ? in : 0;
+                    scratch[29] = item <= a.whole ? 0 : in;
+                    scratch[30] = item <= a.whole ? in : 0;
                     // the first boundary inside an item that leaves tiles before it
                     if (item > a.whole && in >= w && in - quota < w)
                         found[8] = 1 + (int)((item - in + quota - 1) / quota);
@@ -246,8 +246,8 @@ __device__ __forceinline__ Range attn_plan(const Args &a, int cta, int n_ctas, l
     __syncthreads();
     Range r{0, 0, 0, 0, 0};
     if (start < total)
-        r = {found[0], found[1], scratch[25],
-             (end < total ? end - scratch[27] : total) - (start - scratch[26]), found[8]};
+        r = {found[0], found[1], scratch[29],
+             (end < total ? end - scratch[31] : total) - (start - scratch[30]), found[8]};
     return r;
 }
 

@@ -10,11 +10,11 @@
 // merged at the end ("one tile"). Either way two independent score tiles are in flight: while
 // the tensor cores work for one, the CUDA cores exponentiate the other.
 //
-// One CTA per SM, 384 threads:
+// One CTA per SM, 416 threads:
 //   warps 0, 3   TMA producers of K and of V: tiles of 64 slots, each through a ring of stages;
 //                a tile is gathered as boxes of gcd(page size, 64) slots, their pages looked up
 //                a tile ahead (with 16-slot pages one warp spent 1.7 us on a tile's 16 copies)
-//   warp 1       TMEM allocator and MMA issuer (one lane)
+//   warps 1, 12  MMA issuers of slots 0 and 1 (warp 1 also allocates TMEM)
 //   warp 2       looks after V: clears what no row may see (see below)
 //   warps 4-7, 8-11  softmax of slot 0 and slot 1: a thread per row, its 64 scores in registers
 //
@@ -44,7 +44,7 @@ namespace {
 using namespace tc;
 
 constexpr int kBN = 64;
-constexpr int kThreads = 384;
+constexpr int kThreads = 416;
 constexpr int kHeavy = 129;      // rows from which an item has two tiles
 constexpr int kMaxStages = 8;    // of K and of V each
 constexpr int kCtlBytes = 2048;
@@ -61,7 +61,7 @@ struct Params {
 // tile u, so P V of tile u - 1 (the other buffer) may be outstanding when S of tile u is there.
 struct Ctl {
     uint64_t kfull[kMaxStages], kempty[kMaxStages], vfull[kMaxStages], vempty[kMaxStages],
-        vready[kMaxStages], s_full[2][2], p_full[2][2], pv_done[2][2], q_full, done;
+        vready[kMaxStages], s_full[2][2], p_full[2][2], pv_done[2][2], q_full, done[2];
     long long scratch[34];
     uint32_t tmem;
     volatile int abort;
@@ -143,9 +143,9 @@ attn_tc_kernel(const __grid_constant__ Params p) {
     if (threadIdx.x == 0) {
         for (int s = 0; s < kMaxStages; ++s) {
             mbar_init(bar(c.kfull[s]), 1);
-            mbar_init(bar(c.kempty[s]), 1);
+            mbar_init(bar(c.kempty[s]), 2);
             mbar_init(bar(c.vfull[s]), 1);
-            mbar_init(bar(c.vempty[s]), 1);
+            mbar_init(bar(c.vempty[s]), 2);
             mbar_init(bar(c.vready[s]), 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -156,7 +156,8 @@ attn_tc_kernel(const __grid_constant__ Params p) {
             }
         }
         mbar_init(bar(c.q_full), 8);
-        mbar_init(bar(c.done), 1);
+        mbar_init(bar(c.done[0]), 1);
+        mbar_init(bar(c.done[1]), 1);
         c.abort = c.bad_page = c.bad_v = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         prefetch_map(&p.kmap);
@@ -262,32 +263,35 @@ attn_tc_kernel(const __grid_constant__ Params p) {
             }
         }
         __syncwarp();
-    } else if (warp == 1) {
+    } else if (warp == 1 || warp == 12) {
         // ----------------------------------------------------------- MMA issuer
         const uint32_t id_s = idesc_bf16(128, kBN), id_o = idesc_bf16(128, 64 * DC) | kIdescBMn;
-        // The issuing warp's own instructions are what bounds a tile's time (1280 cycles of tensor
-        // work took 2000 with a vote and two divisions by the ring's length per wait): stages and
-        // parities are counted, and the waits' verdicts are looked at once a tile.
+        // A slot's products are issued by a warp of its own: what bounds a tile's time is this
+        // warp's chain of waits and issues, not the products. (One warp for both slots took 2060
+        // cycles for a pair of tiles of which the tensor cores were busy 1280; votes and divisions
+        // by the ring's length at every wait had made it 2400.) So stages and parities are
+        // counted, and the waits' verdicts are looked at once a tile.
+        const int slot = warp == 1 ? 0 : 1;
         uint32_t kst = 0, kph = 0, vst = 0, vph = 0, seg = 0;
-        uint32_t done[2] = {0, 0};  // tiles of each slot before the segment
+        uint32_t u0 = 0;  // tiles of the slot before the segment
         bool ok = true;
         auto wait = [&](uint64_t &b, uint32_t par) {
             ok &= mbar_wait(bar(b), par, &c.abort, a.flags);
         };
         auto all_ok = [&]() { return __all_sync(0xffffffffu, ok) != 0; };
-        const uint32_t q_lo = sw128_lo(sQ, 16), k_lo = sw128_lo(sK, 16), v_lo = sw128_lo(sV, 8192);
+        const uint32_t k_lo = sw128_lo(sK, 16), v_lo = sw128_lo(sV, 8192);
+        const uint32_t tS = tmem + slot * 128u, tO = tmem + 256u + slot * 128u;
         Segment g;
         while (all_ok() && next_segment<kBN, kHeavy>(a, r, g)) {
             const bool two = __shfl_sync(0xffffffffu, g.rows, 0) > 128;
             const int n = __shfl_sync(0xffffffffu, g.count, 0);
+            const uint32_t q_lo = sw128_lo(sQ + (two ? (uint32_t)slot * kTile : 0u), 16);
             // u: the slot's tile count; its S buffer is u & 1, the buffer's use u >> 1
-            auto score = [&](int slot, uint32_t u) {  // S of a slot from the current K stage
-                const uint32_t k = k_lo + kst * (kKv >> 4);
-                const uint32_t q = q_lo + (two ? (uint32_t)slot * (kTile >> 4) : 0u);
-                const uint32_t d = tmem + slot * 128u + (u & 1u) * 64u;
+            auto score = [&](uint32_t u) {  // S from the current K stage
+                const uint32_t k = k_lo + kst * (kKv >> 4), d = tS + (u & 1u) * 64u;
 #pragma unroll
                 for (int x = 0; x < 4 * DC; ++x)
-                    mma_ss_elect(d, q + (((x >> 2) * 16384u + (x & 3) * 32u) >> 4),
+                    mma_ss_elect(d, q_lo + (((x >> 2) * 16384u + (x & 3) * 32u) >> 4),
                                  k + (((x >> 2) * 8192u + (x & 3) * 32u) >> 4), id_s, x != 0);
                 commit_elect(bar(c.s_full[slot][u & 1u]));
             };
@@ -296,85 +300,65 @@ attn_tc_kernel(const __grid_constant__ Params p) {
                 __syncwarp();
                 tc_fence_after();
             };
-            auto free_k = [&]() {
-                commit_elect(bar(c.kempty[kst]));
+            // A stage is free when both issuing warps have passed it; a tile that is not this slot's
+            // is passed at once (after its copy has landed: an arrival must not count for an
+            // earlier use of the stage).
+            auto free_k = [&](bool mine) {
+                if (mine)
+                    commit_elect(bar(c.kempty[kst]));
+                else if (lane == 0)
+                    mbar_arrive(bar(c.kempty[kst]));
                 if (++kst == NS) {
                     kst = 0;
                     kph ^= 1u;
                 }
             };
-            auto wait_v = [&]() { wait(c.vready[vst], vph); };
-            auto free_v = [&]() {
-                commit_elect(bar(c.vempty[vst]));
+            auto free_v = [&](bool mine) {
+                if (mine)
+                    commit_elect(bar(c.vempty[vst]));
+                else if (lane == 0)
+                    mbar_arrive(bar(c.vempty[vst]));
                 if (++vst == NS) {
                     vst = 0;
                     vph ^= 1u;
                 }
             };
-            auto output = [&](int slot, uint32_t u, bool first) {  // O += P V, current V stage
+            auto output = [&](uint32_t u, bool first) {  // O += P V, current V stage
                 wait(c.p_full[slot][u & 1u], (u >> 1) & 1u);
                 __syncwarp();
                 tc_fence_after();
-                const uint32_t v = v_lo + vst * (kKv >> 4);
-                const uint32_t pt = tmem + slot * 128u + (u & 1u) * 64u;
+                const uint32_t v = v_lo + vst * (kKv >> 4), pt = tS + (u & 1u) * 64u;
 #pragma unroll
                 for (int x = 0; x < kBN / 16; ++x)
-                    mma_ts_elect(tmem + 256u + slot * 128u, pt + x * 8u, v + x * (2048u >> 4), id_o,
-                                 !first || x != 0);
+                    mma_ts_elect(tO, pt + x * 8u, v + x * (2048u >> 4), id_o, !first || x != 0);
                 commit_elect(bar(c.pv_done[slot][u & 1u]));
             };
             wait(c.q_full, seg++ & 1u);
             __syncwarp();
             tc_fence_after();
             mma_issued = true;
-            if (two) {
-                // both slots take every tile; S runs two tiles ahead of P V
-                for (int t = 0; t < min(n, 2); ++t) {
-                    wait_k();
-                    score(0, done[0] + t);
-                    score(1, done[1] + t);
-                    free_k();
-                }
-                for (int t = 0; t < n; ++t) {
-                    const bool more = t + 2 < n;
-                    wait_v();
-                    output(0, done[0] + t, t == 0);
-                    if (more) {
-                        wait_k();
-                        score(0, done[0] + t + 2);
-                    }
-                    output(1, done[1] + t, t == 0);
-                    free_v();
-                    if (more) {
-                        score(1, done[1] + t + 2);
-                        free_k();
-                    }
-                    if (!all_ok()) break;
-                }
-                done[0] += n;
-                done[1] += n;
-            } else {
-                // the slots take tiles in turn: S runs four tiles ahead
-                for (int t = 0; t < min(n, 4); ++t) {
-                    wait_k();
-                    score(t & 1, done[t & 1] + (t >> 1));
-                    free_k();
-                }
-                for (int t = 0; t < n; ++t) {
-                    const int slot = t & 1;
-                    wait_v();
-                    output(slot, done[slot] + (t >> 1), t < 2);
-                    free_v();
-                    if (t + 4 < n) {
-                        wait_k();
-                        score(slot, done[slot] + (t >> 1) + 2);
-                        free_k();
-                    }
-                    if (!all_ok()) break;
-                }
-                done[0] += (n + 1) / 2;
-                done[1] += n / 2;
+            // with two row tiles each slot takes every key tile, else the slots take them in turn;
+            // S runs two of the slot's tiles ahead of P V
+            const int ahead = two ? 2 : 4, sh = two ? 0 : 1;
+            auto mine = [&](int t) { return two || (t & 1) == slot; };
+            for (int t = 0; t < min(n, ahead); ++t) {
+                wait_k();
+                if (mine(t)) score(u0 + (t >> sh));
+                free_k(mine(t));
             }
+            for (int t = 0; t < n; ++t) {
+                wait(c.vready[vst], vph);
+                if (mine(t)) output(u0 + (t >> sh), t <= sh);
+                __syncwarp();
+                free_v(mine(t));
+                if (t + ahead < n) {
+                    wait_k();
+                    if (mine(t)) score(u0 + (t >> sh) + 2);
+                    free_k(mine(t));
+                }
+                if (!all_ok()) break;
+            }
+            u0 += two ? n : (n + 1 - slot) / 2;
         }
         __syncwarp();
     } else if (warp == 2) {
@@ -444,7 +428,7 @@ attn_tc_kernel(const __grid_constant__ Params p) {
                 if (lane == 0) mbar_arrive(bar(c.vready[st]));
             }
         }
-    } else if (warp >= 4) {
+    } else {
         // -------------------------------------------------------------- softmax
         // A failed wait leaves `dead` set: the thread then runs through its loops without
         // computing or storing, so that the barriers stay matched.
@@ -719,9 +703,10 @@ attn_tc_kernel(const __grid_constant__ Params p) {
             if (issued & (1u << s))
                 mbar_wait(bar(warp == 0 ? c.kfull[s] : c.vfull[s]), (last_par >> s) & 1u, nullptr,
                           a.flags);
-    if (warp == 1 && mma_issued) {
-        commit_elect(bar(c.done));
-        mbar_wait(bar(c.done), 0, nullptr, a.flags);
+    if ((warp == 1 || warp == 12) && mma_issued) {
+        uint64_t &d = c.done[warp == 1 ? 0 : 1];
+        commit_elect(bar(d));
+        mbar_wait(bar(d), 0, nullptr, a.flags);
     }
     __syncwarp();
     tc_fence_before();
