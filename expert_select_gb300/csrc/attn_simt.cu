@@ -218,101 +218,165 @@ __global__ void __launch_bounds__(kThr) attn_simt_kernel(const Args a) {
     }
 }
 
-// Merges a cut item: block (c, y) looks at CTA c's record, of the item whose second part begins
-// CTA c's range. The item's first part is in slot 1 of CTA c - 1, the others in slot 0 of CTAs
-// c, c + 1, ...:
+// Merges the cut items. Record c is of the item whose second part begins CTA c's range (if any):
+// its first part is in slot 1 of CTA c - 1, the others in slot 0 of CTAs c, c + 1, ...:
 //   sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i,  M the largest m_i.
-// WPR warps share a row (8 / WPR rows per block), warp w taking the parts w, w + WPR, ... in
-// order: a single long sequence leaves a few rows in many parts, whose reads must not queue up
-// behind one another; large items have many rows in few parts. Sums run in a fixed order.
-template <typename T, int WPR>
-__global__ void __launch_bounds__(256) attn_combine_kernel(const Args a) {
-    __shared__ float s_o[WPR > 1 ? 8 : 1][256], s_ml[8][2];
-    pdl_wait();
-    const int c = blockIdx.x;
-    const int4 rec = *reinterpret_cast<const int4 *>(a.rec + c * 4);
-    if (rec.z == 0) return;
-    const int e = rec.x, h = rec.y;
+// Every block lists the records in use (a block per possible record and row group would be
+// thousands that find nothing to do) and takes every gridDim.x-th group of rows of all items. WPR
+// warps share a row (8 / WPR rows per group), warp w taking the parts w, w + WPR, ...: a single
+// long sequence leaves a few rows in many parts, whose reads must not queue up behind one another;
+// large items have many rows in few parts. Sums run in a fixed order.
+template <typename T, int WPR, int NC>  // NC: 128-column chunks of the head size
+__global__ void __launch_bounds__(256) attn_combine_kernel(const Args a, int n_ctas) {
+    __shared__ float s_o[WPR > 1 ? 8 : 1][128 * NC], s_ml[8][2];
+    constexpr int kAt = NC == 1 ? 10 : 5;  // parts whose loads are in flight together
+    __shared__ int s_list[kMaxCtas], s_count[8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = warp % WPR;
-    const int b = e / a.qblocks, q0 = (e - b * a.qblocks) * a.rows;
-    const Seq s = sequence(a, b);
-    const int row = blockIdx.y * (8 / WPR) + warp / WPR;
-    const bool live = row < min(a.rows, s.n * a.G - q0);
-    if (WPR == 1 && !live) return;
-    const int parts = live ? rec.z : 0;
-    auto part = [&](int i) { return ((size_t)(c - 1 + i) * 2 + (i == 0)) * a.prows + row; };
-    float M = -INFINITY;
-    for (int i = lane; i < parts; i += 32) {
-        const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + part(i) * 2);
-        if (ml.y != 0.f) M = fmaxf(M, ml.x);
+    pdl_wait();
+    int n_items = 0;
+    for (int c0 = 0; c0 < n_ctas; c0 += 256) {
+        const int c = c0 + threadIdx.x;
+        const bool used = c < n_ctas && a.rec[c * 4 + 2] != 0;
+        const uint32_t mask = __ballot_sync(0xffffffffu, used);
+        if (lane == 0) s_count[warp] = __popc(mask);
+        __syncthreads();
+        int at = n_items;
+        for (int x = 0; x < 8; ++x) {
+            if (x == warp && used) s_list[at + __popc(mask & ((1u << lane) - 1u))] = c;
+            at += s_count[x];
+        }
+        n_items = at;
+        __syncthreads();
     }
+    const int groups = (a.prows + 8 / WPR - 1) / (8 / WPR);
+    for (int work = blockIdx.x; work < n_items * groups; work += gridDim.x) {
+        const int c = s_list[work / groups];
+        const int4 rec = *reinterpret_cast<const int4 *>(a.rec + c * 4);
+        const int e = rec.x, h = rec.y;
+        const int b = e / a.qblocks, q0 = (e - b * a.qblocks) * a.rows;
+        const Seq s = sequence(a, b);
+        const int row = (work % groups) * (8 / WPR) + warp / WPR;
+        const bool live = row < min(a.rows, s.n * a.G - q0);
+        if (WPR == 1 && !live) continue;
+        const int parts = live ? rec.z : 0;
+        auto part = [&](int i) { return ((size_t)(c - 1 + i) * 2 + (i == 0)) * a.prows + row; };
+        float acc[NC][4];  // columns 4 lane + 128 c
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    const float base = M == -INFINITY ? 0.f : M;
-    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};  // columns 4 lane + 128 c (dh <= 256)
-    float l = 0.f;
-#pragma unroll 4
-    for (int i = w; i < parts; i += WPR) {
-        const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + part(i) * 2);
-        const float wi = ml.y == 0.f ? 0.f : exp2f(ml.x - base);
-        l += wi * ml.y;
+        for (int x = 0; x < NC; ++x) acc[x][0] = acc[x][1] = acc[x][2] = acc[x][3] = 0.f;
+        float base = -INFINITY, l = 0.f;
+        for (int i0 = w; i0 < parts; i0 += WPR * kAt) {
+            float2 ml[kAt];
+            float4 v[kAt][NC];
 #pragma unroll
-        for (int cc = 0; cc < 2; ++cc) {
-            const int col = cc * 128 + lane * 4;
-            if (col < a.dh) {
-                const float4 v = *reinterpret_cast<const float4 *>(a.part_o + part(i) * a.dh + col);
-                if (wi != 0.f) {
-                    acc[cc * 4] += wi * v.x;
-                    acc[cc * 4 + 1] += wi * v.y;
-                    acc[cc * 4 + 2] += wi * v.z;
-                    acc[cc * 4 + 3] += wi * v.w;
+            for (int y = 0; y < kAt; ++y) {
+                const int i = i0 + y * WPR;
+                ml[y] = make_float2(-INFINITY, 0.f);
+                if (i < parts) {
+                    ml[y] = *reinterpret_cast<const float2 *>(a.part_ml + part(i) * 2);
+#pragma unroll
+                    for (int x = 0; x < NC; ++x) {
+                        const int col = x * 128 + lane * 4;
+                        v[y][x] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (col < a.dh)
+                            v[y][x] = *reinterpret_cast<const float4 *>(a.part_o + part(i) * a.dh + col);
+                    }
+                }
+            }
+            float top = base;
+#pragma unroll
+            for (int y = 0; y < kAt; ++y)
+                if (ml[y].y != 0.f) top = fmaxf(top, ml[y].x);  // (a part that saw nothing has sum 0)
+            const float f = base == -INFINITY ? 0.f : exp2f(base - top);
+            base = top;
+            l *= f;
+#pragma unroll
+            for (int x = 0; x < NC; ++x)
+#pragma unroll
+                for (int z = 0; z < 4; ++z) acc[x][z] *= f;
+            const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll
+            for (int y = 0; y < kAt; ++y) {
+                const float wy = ml[y].y == 0.f ? 0.f : exp2f(ml[y].x - ref);
+                if (wy == 0.f) continue;
+                l += wy * ml[y].y;
+#pragma unroll
+                for (int x = 0; x < NC; ++x) {
+                    acc[x][0] += wy * v[y][x].x;
+                    acc[x][1] += wy * v[y][x].y;
+                    acc[x][2] += wy * v[y][x].z;
+                    acc[x][3] += wy * v[y][x].w;
                 }
             }
         }
-    }
-    if constexpr (WPR > 1) {
+        if constexpr (WPR > 1) {
 #pragma unroll
-        for (int cc = 0; cc < 2; ++cc)
-            *reinterpret_cast<float4 *>(&s_o[warp][cc * 128 + lane * 4]) =
-                make_float4(acc[cc * 4], acc[cc * 4 + 1], acc[cc * 4 + 2], acc[cc * 4 + 3]);
-        if (lane == 0) s_ml[warp][0] = l;
-        __syncthreads();
-        if (w != 0 || !live) return;
-#pragma unroll 1
-        for (int x = 1; x < WPR; ++x) {
-            l += s_ml[warp + x][0];
+            for (int x = 0; x < NC; ++x)
+                *reinterpret_cast<float4 *>(&s_o[warp][x * 128 + lane * 4]) =
+                    make_float4(acc[x][0], acc[x][1], acc[x][2], acc[x][3]);
+            if (lane == 0) {
+                s_ml[warp][0] = base;
+                s_ml[warp][1] = l;
+            }
+            __syncthreads();
+            if (w == 0 && live) {
+                float top = base;
 #pragma unroll
-            for (int cc = 0; cc < 2; ++cc) {
-                const float4 v =
-                    *reinterpret_cast<const float4 *>(&s_o[warp + x][cc * 128 + lane * 4]);
-                acc[cc * 4] += v.x;
-                acc[cc * 4 + 1] += v.y;
-                acc[cc * 4 + 2] += v.z;
-                acc[cc * 4 + 3] += v.w;
+                for (int x = 1; x < WPR; ++x)
+                    if (s_ml[warp + x][1] != 0.f) top = fmaxf(top, s_ml[warp + x][0]);
+                const float ref = top == -INFINITY ? 0.f : top;
+                const float f = base == -INFINITY ? 0.f : exp2f(base - ref);
+                l *= f;
+#pragma unroll
+                for (int x = 0; x < NC; ++x)
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) acc[x][z] *= f;
+#pragma unroll
+                for (int y = 1; y < WPR; ++y) {
+                    const float ly = s_ml[warp + y][1];
+                    const float wy = ly == 0.f ? 0.f : exp2f(s_ml[warp + y][0] - ref);
+                    if (wy == 0.f) continue;
+                    l += wy * ly;
+#pragma unroll
+                    for (int x = 0; x < NC; ++x) {
+                        const float4 v =
+                            *reinterpret_cast<const float4 *>(&s_o[warp + y][x * 128 + lane * 4]);
+                        acc[x][0] += wy * v.x;
+                        acc[x][1] += wy * v.y;
+                        acc[x][2] += wy * v.z;
+                        acc[x][3] += wy * v.w;
+                    }
+            }
+            base = top;
             }
         }
-    }
-    const int qr = q0 + row, node = qr / a.G, head = h * a.G + (qr - node * a.G);
-    const size_t orow = (size_t)(s.row0 + node) * a.H + head;
-    float lse;
-    const float f = finish(base, l, a.sink, head, &lse);
-    T *out = (T *)a.out + orow * a.dh;
+        if (w == 0 && live) {
+            const int qr = q0 + row, node = qr / a.G, head = h * a.G + (qr - node * a.G);
+            const size_t orow = (size_t)(s.row0 + node) * a.H + head;
+            float lse;
+            const float f = finish(base, l, a.sink, head, &lse);
+            T *out = (T *)a.out + orow * a.dh;
 #pragma unroll
-    for (int cc = 0; cc < 2; ++cc) {
-        const int col = cc * 128 + lane * 4;
-        if (col < a.dh) {
+            for (int x = 0; x < NC; ++x) {
+                const int col = x * 128 + lane * 4;
+                if (col < a.dh) {
 #pragma unroll
-            for (int x = 0; x < 4; ++x) out[col + x] = from_float<T>(acc[cc * 4 + x] * f);
+                    for (int z = 0; z < 4; ++z) out[col + z] = from_float<T>(acc[x][z] * f);
+                }
         }
+        if (a.lse && lane == 0) a.lse[orow] = lse;
+        }
+        if (WPR > 1) __syncthreads();  // the next group writes s_o again
     }
-    if (a.lse && lane == 0) a.lse[orow] = lse;
 }
 
-template <typename T> cudaError_t combine_t(const Args &a, int n_ctas, cudaStream_t s) {
+template <typename T, int NC> cudaError_t combine_nc(const Args &a, int n_ctas, cudaStream_t s) {
+    const int sms = device_sms();
     if (a.prows <= kFewRows)
-        return launch_pdl(attn_combine_kernel<T, 8>, dim3(n_ctas, a.prows), dim3(256), 0, s, a);
-    return launch_pdl(attn_combine_kernel<T, 1>, dim3(n_ctas, (a.prows + 7) / 8), dim3(256), 0, s,
-                      a);
+        return launch_pdl(attn_combine_kernel<T, 8, NC>, dim3(2 * sms), dim3(256), 0, s, a, n_ctas);
+    return launch_pdl(attn_combine_kernel<T, 1, NC>, dim3(4 * sms), dim3(256), 0, s, a, n_ctas);
+}
+template <typename T> cudaError_t combine_t(const Args &a, int n_ctas, cudaStream_t s) {
+    return a.dh <= 128 ? combine_nc<T, 1>(a, n_ctas, s) : combine_nc<T, 2>(a, n_ctas, s);
 }
 
 template <typename T, int NC>
