@@ -444,7 +444,7 @@ moe_status moe_event_wait(moe_event_t ev, double timeout_s);
  * `sink_tokens` positions; with 0 it sees all. Limits: H a multiple of H_kv, dh a multiple of 8
  * and at most 256, strides multiples of 8 and at least dh, max_pages * page_size <= 2^30,
  * scale > 0. bf16 heads of dh <= 128 run on the tensor cores, fp32 and larger heads on the
- * CUDA cores. */
+ * CUDA cores; any page size. */
 typedef struct {
     int H, H_kv, dh;
     int dtype;      /* moe_dtype of q, k, v, the pools and the output */
@@ -484,9 +484,9 @@ size_t moe_attention_workspace_bytes(const moe_cache_desc *C, int B, int N);
  * Pointers to q, pools and out are 16-byte aligned, workspace 256-byte. Scores, softmax
  * statistics and sums are fp32; the tensor-core kernel rounds the unnormalised p to bf16 for
  * its second product. Lengths and tables are only read on the device, so a captured graph may
- * be replayed with other ones. Device-side checks (moe_workspace_check): bit 2 = a page outside
- * the pool (its slots are not seen), bit 3 = lengths or row ranges that do not fit the page
- * table, N or R (cut to what fits). */
+ * be replayed with other ones. Device-side checks (moe_workspace_check): bit 1 = a bounded wait
+ * gave up (the output is not valid), bit 2 = a page outside the pool (its slots are not seen),
+ * bit 3 = lengths or row ranges that do not fit the page table, N or R (cut to what fits). */
 moe_status moe_tree_attention(const moe_cache_desc *C, const void *q, long long ldq,
                               const void *k_pages, const void *v_pages, const int *page_table,
                               const int *cache_len, const int *row_start, const int *parent,

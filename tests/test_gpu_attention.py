@@ -349,11 +349,13 @@ def test_attention_repeats_bit_for_bit():
         assert torch.equal(blk.out, first) and torch.equal(blk.lse, lse)
 
 
-def test_attention_in_a_graph_follows_new_lengths_and_tables():
+@pytest.mark.parametrize("dtype,dh,kind,ns", [(BF, 128, "chain", (1, 1)), (BF, 64, "tree", (33, 33)),
+                                             (BF, 128, "chain", (140, 140)),
+                                             (F32, 64, "tree", (9, 9))])
+def test_attention_in_a_graph_follows_new_lengths_and_tables(dtype, dh, kind, ns):
     """A captured call is replayed after the lengths, the table and q have changed, on another
     stream than the capture's."""
-    small = Block(8, lens=(50, 20), ns=(1, 1), dh=128, H=16, Hkv=2, page=8)
-    big = Block(9, lens=(2000, 700), ns=(1, 1), dh=128, H=16, Hkv=2, page=8).upload()
+    big = Block(9, dtype, lens=(2000, 700), ns=ns, kind=kind, dh=dh, H=16, Hkv=2, page=8).upload()
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):
@@ -382,7 +384,36 @@ def test_attention_in_a_graph_follows_new_lengths_and_tables():
         g.replay()
     torch.cuda.current_stream().wait_stream(side)
     big.check()
-    del small
+
+
+def test_attention_on_two_streams_at_once():
+    """Calls that overlap in time, each with its own workspace, on streams given explicitly."""
+    blocks = [Block(60 + i, **c).upload() for i, c in enumerate([
+        dict(lens=(6000, 9000), ns=(65, 65), kind="tree", dh=128, H=16, Hkv=2),
+        dict(lens=(12000,), ns=(300,), dh=64, H=8, Hkv=2),
+        dict(lens=(20000, 3), ns=(1, 1), dh=128, H=16, Hkv=2)])]
+    streams = [torch.cuda.Stream() for _ in blocks]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for b, s in zip(blocks, streams):
+            M.moe_tree_attention(b.C, b.qd, b.kd, b.vd, b.tabled, b.lend, b.B, b.N, b.out, b.ws,
+                                 parent=b.parentd, row_start=b.startd, lse=b.lse, stream=s)
+    for b in blocks:
+        b.check()
+
+
+@pytest.mark.parametrize("N", [1, 2, 16, 17, 65])
+def test_single_rows_do_not_depend_on_the_kernel(N):
+    """The same query node as the last of a chain of N: the kernels for few and for many rows give
+    the same output up to the roundings of one of them each."""
+    blk = Block(70, lens=(700,), ns=(N,), dh=128, H=8, Hkv=1).upload().attend().check()
+    last = Block(70, lens=(700,), ns=(N,), dh=128, H=8, Hkv=1).upload()
+    one = torch.empty(1, 8, 128, dtype=BF, device=DEV)
+    M.moe_tree_attention(last.C, last.qd[N - 1:], last.kd, last.vd, last.tabled,
+                         last.lend + (N - 1), 1, 1, one, last.ws)
+    _, _, tol = blk.reference()
+    diff = (one.double().cpu()[0] - blk.out.double().cpu()[N - 1]).abs()
+    assert (diff <= 2 * tol[N - 1]).all()
 
 
 def test_one_workspace_serves_blocks_of_any_shape():
