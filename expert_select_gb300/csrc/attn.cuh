@@ -49,6 +49,7 @@ struct Args {
     int prows;       // rows of a partial result: min(rows, N G)
     int qblocks;     // blocks of `rows` rows that N nodes take
     int min_units;   // units of work of a CTA's range at least (a tile's weight or more)
+    int fixed;       // units that an item costs beside its tiles
     int whole;       // units up to which an item is not cut
 };
 
@@ -124,9 +125,10 @@ __device__ __forceinline__ int entry_tiles(const Args &a, int e, int *w, int *ba
 }
 
 // A CTA's range of work, from `off` units into the item (entry e, key/value head h), where entry
-// e = sequence * qblocks + block of rows. Tile t of an item of weight w is the units w t ..
-// w t + w - 1; it belongs to one CTA: a boundary at unit u of the item lies before tile
-// floor(u / w), for the range that ends there and for the one that begins.
+// e = sequence * qblocks + block of rows. An item of nt tiles of weight w has a.fixed + nt w units:
+// the first a.fixed are what it costs beside its tiles (see attn_plan), then w for each tile. A
+// tile belongs to one CTA: a boundary at unit u of the item lies before tile
+// floor((u - a.fixed) / w), for the range that ends there and for the one that begins.
 struct Range {
     int e, h;
     long long off;   // the range's first unit within the item
@@ -160,9 +162,10 @@ __device__ __forceinline__ long long block_scan(long long v, long long *scratch,
 // memory. Each thread sums a run of entries and a block scan places the runs; the threads whose
 // runs hold the range's boundaries look them up.
 //
-// A piece of an item costs a CTA several tiles' time besides its tiles (query rows, the pipeline's
-// start and end, the output, and a partial result that the combine has to read). Two rules keep
-// pieces few:
+// A piece of an item costs a CTA several tiles' time beside its tiles (query rows, the pipeline's
+// start and end, the output, and a partial result that the combine has to read). So an item counts
+// a.fixed units beside its tiles (64 trees over contexts of 0.2-8k tokens: without, the CTAs with
+// the short sequences took 1.3 times the mean), and two rules keep pieces few:
 //  - where every item can have round(item / quota) CTAs of its own, it gets them, in equal parts,
 //    and a CTA has one piece (a few long items: one tree of 65 nodes over 4k tokens took 31 us so
 //    and 38 us with ranges that cross items);
@@ -180,7 +183,7 @@ __device__ __forceinline__ Range attn_plan(const Args &a, int cta, int n_ctas, l
     int bad = 0, w = 1, nt = 0;
     for (int e = e0; e < e1; ++e) {
         nt = entry_tiles<BN, HEAVY>(a, e, &w, &bad);
-        sum += (long long)a.Hkv * nt * w;
+        sum += nt > 0 ? a.Hkv * ((long long)nt * w + a.fixed) : 0;
     }
     if (bad) atomicOr(a.flags, FLAG_BAD_SEQUENCE);
     int *found = reinterpret_cast<int *>(scratch + 28);
@@ -194,7 +197,7 @@ __device__ __forceinline__ Range attn_plan(const Args &a, int cta, int n_ctas, l
                                           : (total + n_ctas - 1) / n_ctas);
     // scratch[28 ..]: the item, the offset in it, how far the two boundaries moved back, parts
     if (per == 1 && small) {
-        const unsigned item = (unsigned)nt * w;
+        const unsigned item = (unsigned)nt * w + a.fixed;
         const int k = min(max(1, (int)((item + quota / 2) / (unsigned)quota)), nt);  // CTAs per item
         long long ctas;
         const long long first = block_scan<kWarps>((long long)a.Hkv * k, scratch + 14, &ctas);
@@ -204,8 +207,9 @@ __device__ __forceinline__ Range attn_plan(const Args &a, int cta, int n_ctas, l
                 const int t0 = (int)((long long)nt * j / k), t1 = (int)((long long)nt * (j + 1) / k);
                 found[0] = tid;
                 found[1] = h;
-                scratch[29] = (long long)t0 * w;
-                scratch[30] = (long long)(t1 - t0) * w;
+                const long long u0 = t0 > 0 ? a.fixed + (long long)t0 * w : 0;
+                scratch[29] = u0;
+                scratch[30] = a.fixed + (long long)t1 * w - u0;
                 found[8] = j == 1 ? k : 0;
             }
             __syncthreads();
@@ -222,7 +226,7 @@ __device__ __forceinline__ Range attn_plan(const Args &a, int cta, int n_ctas, l
         long long at = run;
         for (int e = e0; e < e1; ++e) {
             if (per > 1) nt = entry_tiles<BN, HEAVY>(a, e, &w);
-            const long long item = (long long)nt * w, all = a.Hkv * item;
+            const long long item = (long long)nt * w + a.fixed, all = nt > 0 ? a.Hkv * item : 0;
             if (u < at + all) {
                 const long long off = u - at;
                 const long long h = small ? (long long)((unsigned)off / (unsigned)item) : off / item;
@@ -235,7 +239,8 @@ __device__ __forceinline__ Range attn_plan(const Args &a, int cta, int n_ctas, l
                     scratch[29] = item <= a.whole ? 0 : in;
                     scratch[30] = item <= a.whole ? in : 0;
                     // the first boundary inside an item that leaves tiles before it
-                    if (item > a.whole && in >= w && in - quota < w)
+                    const int one = a.fixed + w;
+                    if (item > a.whole && in >= one && in - quota < one)
                         found[8] = 1 + (int)((item - in + quota - 1) / quota);
                 }
                 break;
@@ -281,10 +286,11 @@ __device__ __forceinline__ bool next_segment(const Args &a, Range &r, Segment &g
             continue;
         }
         const bool heavy = HEAVY && g.rows >= HEAVY;
-        const long long item = (long long)g.tl.nt * (HEAVY ? (heavy ? 4 : 3) : 1);
+        const long long item = (long long)g.tl.nt * (HEAVY ? (heavy ? 4 : 3) : 1) + a.fixed;
         const long long end = min(item, r.off + r.left);
-        auto tile = [&](long long u) {  // tiles below unit u of an item (items have < 2^31 units)
-            return HEAVY ? (int)(heavy ? (unsigned)u / 4u : (unsigned)u / 3u) : (int)u;
+        auto tile = [&](long long unit) {  // tiles before a unit (items have < 2^32 units)
+            const unsigned u = (unsigned)max(0ll, unit - a.fixed);
+            return HEAVY ? (int)(heavy ? u / 4u : u / 3u) : (int)u;
         };
         g.h = r.h;
         g.t = tile(r.off);

@@ -438,7 +438,8 @@ cudaError_t launch_few(Args a, cudaStream_t s) {
     a.qblocks = (int)(((long long)a.N * a.G + kFewRows - 1) / kFewRows);
     a.prows = (int)std::min<long long>(a.rows, (long long)a.N * a.G);
     a.min_units = 2;
-    a.whole = 8;
+    a.fixed = 2;
+    a.whole = 10;
     cudaError_t err = a.dh <= 64 ? launch_dc<1>(a, nsm, &ctas, s) : launch_dc<2>(a, nsm, &ctas, s);
     if (err != cudaSuccess) return err;
     return launch_combine(a, MOE_DTYPE_BF16, ctas, s);

@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(256) attn_combine_kernel(const Args a, int n_c
 #pragma unroll
             for (int y = 0; y < kAt; ++y) {
                 const float wy = ml[y].y == 0.f ? 0.f : exp2f(ml[y].x - ref);
-                if (wy == 0.f) continue;
+                if (wy == 0.f && ml[y].y == ml[y].y) continue;  // (a NaN sum goes through)
                 l += wy * ml[y].y;
 #pragma unroll
                 for (int x = 0; x < NC; ++x) {
@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(256) attn_combine_kernel(const Args a, int n_c
                 for (int y = 1; y < WPR; ++y) {
                     const float ly = s_ml[warp + y][1];
                     const float wy = ly == 0.f ? 0.f : exp2f(s_ml[warp + y][0] - ref);
-                    if (wy == 0.f) continue;
+                    if (wy == 0.f && ly == ly) continue;
                     l += wy * ly;
 #pragma unroll
                     for (int x = 0; x < NC; ++x) {
@@ -413,7 +413,8 @@ cudaError_t launch_simt(Args a, int dtype, cudaStream_t s) {
     a.qblocks = (int)(((long long)a.N * a.G + kSimtRows - 1) / kSimtRows);
     a.prows = (int)std::min<long long>(a.rows, (long long)a.N * a.G);
     a.min_units = 2;
-    a.whole = 6;
+    a.fixed = 2;
+    a.whole = 8;
     cudaError_t err = dtype == MOE_DTYPE_BF16 ? launch_t<__nv_bfloat16>(a, nsm, &ctas, s)
                                   : launch_t<float>(a, nsm, &ctas, s);
     if (err != cudaSuccess) return err;

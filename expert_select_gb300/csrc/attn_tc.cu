@@ -777,7 +777,8 @@ cudaError_t launch_tc(Args a, cudaStream_t s) {
     a.qblocks = (int)(((long long)a.N * a.G + kTcRows - 1) / kTcRows);
     a.prows = (int)std::min<long long>(a.rows, (long long)a.N * a.G);
     a.min_units = 24;
-    a.whole = 16;
+    a.fixed = 48;
+    a.whole = 64;
     Params p{};
     p.a = a;
     p.box = 1;

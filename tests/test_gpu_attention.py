@@ -248,7 +248,8 @@ def test_attention_matches_64_bits(case, dtype):
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
 @pytest.mark.parametrize("kind,dh,ns", [("tree", 128, (70, 33)), ("chain", 64, (70, 33)),
                                         ("tree", 136, (70, 33)), ("tree", 128, (4, 3)),
-                                        ("chain", 64, (3, 4))])
+                                        ("chain", 64, (3, 4)), ("chain", 256, (2, 3)),
+                                        ("chain", 128, (1, 1))])
 def test_masked_infinities_and_nan_take_no_part(dtype, kind, dh, ns):
     """A node's keys and values hold NaN and infinities: rows that do not see it are what they
     would be without it, rows that do see it are not finite."""
@@ -276,6 +277,18 @@ def test_masked_infinities_and_nan_take_no_part(dtype, kind, dh, ns):
             assert (hit[:, G:, 0::2] == -math.inf).all() and (hit[:, G:, 1::2] == math.inf).all()
         else:
             assert torch.isnan(hit).all()
+
+
+@pytest.mark.parametrize("dtype,dh", [(BF, 128), (BF, 256), (F32, 64)])
+def test_a_part_of_only_nan_scores_is_not_lost(dtype, dh):
+    """A long item is cut between CTAs; the part that holds the last slots sees one key, of NaN:
+    its running maximum never rises, and its sum is NaN."""
+    for ln in (4096, 8192, 12352):  # whole tiles of committed slots before the node's own
+        blk = Block(12, dtype, lens=(ln,), ns=(1,), dh=dh, H=4, Hkv=1, page=64).upload()
+        blk.attend().check()
+        blk.kd[int(blk.table[0, ln // 64]), ln % 64] = float("nan")
+        blk.attend()
+        assert torch.isnan(blk.out).all()
 
 
 def test_nothing_visible_gives_zeros():
