@@ -481,6 +481,7 @@ APPEND = [
     dict(lens=(60,), ns=(7,), rot=256, norm=True, dh=256, H=3, Hkv=1, page=7, layout="hnd"),
     dict(lens=(60,), ns=(7,), rot=104, norm=True, dh=136, H=3, Hkv=1, scale=1.3),
     dict(lens=(60,), ns=(7,), rot=24, norm=True, dh=40, H=3, Hkv=3, scale=0.7),
+    dict(lens=(9, 0, 40), ns=(1400, 0, 1301), rot=64, norm=True, pad_rows=3, H=4, Hkv=1),
     dict(lens=(70000, 131071), ns=(3, 3), rot=96, norm=False, dh=128, H=4, Hkv=1, page=256),
 ]
 
