@@ -439,19 +439,23 @@ def _at(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
+_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else None
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_entry = {}  # entry points by name, looked up once
+
+
 def _run(fn: str, index: int, stream, *args) -> int:
     """Calls entry point `fn` on device `index`, on `stream` or the device's current one."""
+    call = _entry.get(fn)
+    if call is None:
+        call = _entry[fn] = getattr(lib(), fn)
     if index < 0:
         raise ValueError(f"{fn}: the tensors must be on a CUDA device")
-    before = torch._C._cuda_getDevice()
-    if before != index:
-        torch.cuda.set_device(index)
-    try:
-        s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
-        st = getattr(lib(), fn)(*args, s)
-    finally:
-        if before != index:
-            torch.cuda.set_device(before)
+    if _device() == index:
+        st = call(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
+    else:
+        with torch.cuda.device(index):
+            st = call(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
     if st != MOE_OK:
         raise MoeError(fn, st)
     return st
@@ -479,15 +483,19 @@ def _pools(fn, C_, k_pages, v_pages, page_table, cache_len, B, row_start):
     index, dt = k_pages.get_device(), _TORCH[C_.dtype]
     shape = (C_.n_pages, C_.page_size, C_.H_kv, C_.dh)
     st = (C_.stride_page, C_.stride_tok, C_.stride_head, 1)
-    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        if not (t.dtype is dt and t.shape == shape and t.get_device() == index):
+    if not (k_pages.dtype is dt and k_pages.shape == shape and k_pages.stride() == st and
+            v_pages.dtype is dt and v_pages.shape == shape and v_pages.stride() == st and
+            v_pages.get_device() == index):
+        for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
             _refuse(fn, name, t, dt, shape, index, dense=False)
-        if t.stride() != st and any(n > 1 and x != y for n, x, y in zip(shape, t.stride(), st)):
-            raise ValueError(f"{fn}: {name} has other strides than the cache description")
-    _dense(fn, "page_table", page_table, torch.int32, (B, C_.max_pages), index)
-    _dense(fn, "cache_len", cache_len, torch.int32, (B,), index)
+            # (a dimension of one element has no stride to speak of)
+            if any(n > 1 and x != y for n, x, y in zip(shape, t.stride(), st)):
+                raise ValueError(f"{fn}: {name} has other strides than the cache description")
+    i32 = torch.int32
+    _dense(fn, "page_table", page_table, i32, (B, C_.max_pages), index)
+    _dense(fn, "cache_len", cache_len, i32, (B,), index)
     if row_start is not None:
-        _dense(fn, "row_start", row_start, torch.int32, (B + 1,), index)
+        _dense(fn, "row_start", row_start, i32, (B + 1,), index)
     return index, dt
 
 
@@ -521,12 +529,16 @@ def moe_tree_attention(C_, q, k_pages, v_pages, page_table, cache_len, B, N, out
     shape = (R, H, C_.dh)
     ldq = _rows(fn, "q", q, dt, shape, index)
     _dense(fn, "out", out, dt, shape, index)
-    _dense(fn, "parent", parent, torch.int32, (R,), index)
-    _dense(fn, "sink_logit", sink_logit, torch.float32, (H,), index)
-    _dense(fn, "lse", lse, torch.float32, (R, H), index)
+    if parent is not None:
+        _dense(fn, "parent", parent, torch.int32, (R,), index)
+    if sink_logit is not None:
+        _dense(fn, "sink_logit", sink_logit, torch.float32, (H,), index)
+    if lse is not None:
+        _dense(fn, "lse", lse, torch.float32, (R, H), index)
     desc = C.byref(C_)
     if B > 0 and N > 0:
-        _scratch(fn, ws, index, lib().moe_attention_workspace_bytes(desc, B, N))
+        _scratch(fn, ws, index, _lib.moe_attention_workspace_bytes(desc, B, N) if _lib else
+                 moe_attention_workspace_bytes(C_, B, N))
     return _run(fn, index, stream, desc, q.data_ptr(), ldq, k_pages.data_ptr(),
                 v_pages.data_ptr(), page_table.data_ptr(), cache_len.data_ptr(), _at(row_start),
                 _at(parent), _at(sink_logit), B, N, R, out.data_ptr(), _at(lse), ws.data_ptr())
@@ -545,13 +557,16 @@ def moe_kv_append(C_, q, k, v, k_pages, v_pages, page_table, cache_len, B, N, q_
         _dense(fn, "q_out", q_out, dt, (R, C_.H, dh), index)
     kv = (R, C_.H_kv, dh)
     ldk, ldv = _rows(fn, "k", k, dt, kv, index), _rows(fn, "v", v, dt, kv, index)
-    _dense(fn, "depth", depth, torch.int32, (R,), index)
+    if depth is not None:
+        _dense(fn, "depth", depth, torch.int32, (R,), index)
     rot = 0
     if inv_freq is not None:
         rot = 2 * inv_freq.numel()
         _dense(fn, "inv_freq", inv_freq, torch.float32, inv_freq.shape, index)
-    _dense(fn, "q_weight", q_weight, dt, (dh,), index)
-    _dense(fn, "k_weight", k_weight, dt, (dh,), index)
+    if q_weight is not None:
+        _dense(fn, "q_weight", q_weight, dt, (dh,), index)
+    if k_weight is not None:
+        _dense(fn, "k_weight", k_weight, dt, (dh,), index)
     _scratch(fn, ws, index, 4096)
     P = RopeParams(_at(q_weight), _at(k_weight), eps, _at(inv_freq), rot, rope_scale)
     return _run(fn, index, stream, C.byref(C_), C.byref(P), _at(q), ldq, k.data_ptr(), ldk,
