@@ -280,7 +280,9 @@ __device__ __forceinline__ bool next_segment(const Args &a, Range &r, Segment &g
             if (g.rows > 0) g.tl = tiles_of<BN>(a, g.s, g.q0, g.q0 + g.rows);
         }
         if (g.tl.nt == 0) {
-            ++r.e;
+            // (past a sequence's rows all of its blocks are empty: in a batch of prompt chunks and
+            // single tokens most sequences have one block of many)
+            r.e = g.rows <= 0 ? (g.b + 1) * a.qblocks : r.e + 1;
             r.h = 0;
             r.off = 0;
             continue;

@@ -293,7 +293,7 @@ attn_tc_kernel(const __grid_constant__ Params p) {
         const uint32_t id_s = idesc_bf16(128, kBN), id_o = idesc_bf16(128, 64 * DC) | kIdescBMn;
         // A slot's products are issued by a warp of its own: what bounds a tile's time is this
         // warp's chain of waits and issues, not the products. (One warp for both slots took 2060
-        // cycles for a pair of tiles of which the tensor cores were busy 1280; votes and divisions
+        // cycles for a pair of tiles of which the tensor cores were busy 1090; votes and divisions
         // by the ring's length at every wait had made it 2400.) So stages and parities are
         // counted, and the waits' verdicts are looked at once a tile.
         const int slot = warp == 1 ? 0 : 1;

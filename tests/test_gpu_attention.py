@@ -245,6 +245,25 @@ def test_attention_matches_64_bits(case, dtype):
     Block(len(str(case)), dtype, **case).upload().attend().check()
 
 
+@pytest.mark.parametrize("dtype,n", [(BF, 1), (BF, 5), (F32, 2)])
+def test_more_sequences_than_a_block_has_threads(dtype, n):
+    r = np.random.default_rng(n)
+    lens = tuple(int(v) for v in np.where(r.random(520) < 0.9, r.integers(0, 60, 520),
+                                          r.integers(60, 900, 520)))
+    Block(80 + n, dtype, lens=lens, ns=(n,) * 520, H=4, Hkv=1, page=8).upload().attend().check()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+def test_chunks_and_single_tokens_in_one_block(dtype):
+    """A batch of a few prompt chunks among many single tokens and empty sequences."""
+    r = np.random.default_rng(5)
+    ns = [1] * 60
+    ns[7], ns[31], ns[32], ns[59] = 300, 0, 77, 130
+    lens = tuple(int(v) for v in r.integers(0, 400, 60))
+    Block(90, dtype, lens=lens, ns=tuple(ns), H=8, Hkv=2, page=16, pad_rows=2).upload().attend() \
+        .check()
+
+
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
 @pytest.mark.parametrize("kind,dh,ns", [("tree", 128, (70, 33)), ("chain", 64, (70, 33)),
                                         ("tree", 136, (70, 33)), ("tree", 128, (4, 3)),
