@@ -82,6 +82,11 @@ moe_status moe_tree_attention(const moe_cache_desc *C, const void *q, long long 
     // (sequence, block of rows) pairs are counted in an int
     if ((long long)B * (((long long)N * a.G + attn::kSimtRows - 1) / attn::kSimtRows) > (1 << 30))
         return MOE_ERR_UNSUPPORTED;
+    // one CTA may still read q where another has written its rows
+    const size_t elt = C->dtype == MOE_DTYPE_F32 ? 4 : 2, row = (size_t)C->H * C->dh;
+    const uintptr_t q0 = (uintptr_t)q, o0 = (uintptr_t)out;
+    if (o0 < q0 + ((size_t)(R - 1) * ldq + row) * elt && q0 < o0 + (size_t)R * row * elt)
+        return MOE_ERR_ARG;
     const attn::WsLayout w = attn::ws_layout(C->dh, (long long)N * a.G);
     a.q = q;
     a.ldq = ldq;

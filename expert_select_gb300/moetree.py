@@ -537,11 +537,13 @@ def moe_tree_attention(C_, q, k_pages, v_pages, page_table, cache_len, B, N, out
         _dense(fn, "lse", lse, torch.float32, (R, H), index)
     desc = C.byref(C_)
     if B > 0 and N > 0:
+        if ws is None:
+            raise ValueError(f"{fn}: it needs a workspace")
         _scratch(fn, ws, index, _lib.moe_attention_workspace_bytes(desc, B, N) if _lib else
                  moe_attention_workspace_bytes(C_, B, N))
     return _run(fn, index, stream, desc, q.data_ptr(), ldq, k_pages.data_ptr(),
                 v_pages.data_ptr(), page_table.data_ptr(), cache_len.data_ptr(), _at(row_start),
-                _at(parent), _at(sink_logit), B, N, R, out.data_ptr(), _at(lse), ws.data_ptr())
+                _at(parent), _at(sink_logit), B, N, R, out.data_ptr(), _at(lse), _at(ws))
 
 
 def moe_kv_append(C_, q, k, v, k_pages, v_pages, page_table, cache_len, B, N, q_out, ws=None,

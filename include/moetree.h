@@ -479,8 +479,8 @@ size_t moe_attention_workspace_bytes(const moe_cache_desc *C, int B, int N);
  *   parent      [R] device int32: parent[r] is the node index (within the sequence, lower than
  *               the node's own) of row r's parent; anything else makes it a root. NULL: chains.
  *   sink_logit  [H] device fp32 or NULL: Z also counts exp(sink_logit[h]) (GPT-OSS's sinks).
- *   out         [R, H, dh] device, dense; lse [R, H] device fp32 or NULL: log Z (-inf where
- *               nothing is seen).
+ *   out         [R, H, dh] device, dense, must not overlap q (refused) or any other input;
+ *               lse [R, H] device fp32 or NULL: log Z (-inf where nothing is seen).
  * Pointers to q, pools and out are 16-byte aligned, workspace 256-byte. Scores, softmax
  * statistics and sums are fp32; the tensor-core kernel rounds the unnormalised p to bf16 for
  * its second product. Lengths and tables are only read on the device, so a captured graph may

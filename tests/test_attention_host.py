@@ -69,6 +69,12 @@ def test_attention_arguments_are_refused():
                                   nul) == M.MOE_ERR_ARG
     # more (sequence, block of rows) pairs than are counted
     assert call(B_=1 << 25, N=1 << 12, R=8, start=f) == M.MOE_ERR_UNSUPPORTED
+    # an output over its queries: the same rows, the last one's end, a wider row's gap
+    base = 0x100000
+    for kw in (dict(), dict(R=2, N=2, out=C.c_void_p(base + 8192 + 8176)),
+               dict(R=2, N=2, ldq=3 * 4096, out=C.c_void_p(base + 8192)),
+               dict(q=C.c_void_p(base + 8176))):
+        assert call(**kw) == M.MOE_ERR_ARG, kw
     # nothing to do is fine
     assert call(B_=0, N=5, R=0, q=nul) == M.MOE_OK
     assert call(B_=3, N=0, R=0, q=nul) == M.MOE_OK
@@ -153,6 +159,7 @@ def test_cache_desc_reads_strides_of_both_layouts():
     ("parent", torch.zeros(3, dtype=torch.int64)), ("parent", torch.zeros(2, dtype=torch.int32)),
     ("logit", torch.zeros(4)), ("lse", torch.zeros(3, 4)), ("ws", torch.zeros(64,
                                                                               dtype=torch.uint8)),
+    ("ws", None),
 ])
 def test_binding_refuses_wrong_tensors(name, value):
     t = dict(q=torch.zeros(3, 32, 128, dtype=torch.bfloat16), v=_host_pool(),
