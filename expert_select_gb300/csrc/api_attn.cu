@@ -47,6 +47,23 @@ bool block_ok(const moe_cache_desc *C, int B, int N, int R, const int *row_start
     return row_start ? true : (long long)B * N == R;
 }
 
+// Whether the kernel for few rows takes a bf16 block. With up to 16 rows for a key/value head the
+// work is reading the cache: on 1-64 sequences of 4k-60k slots it takes 12-166 us where the
+// tcgen05 kernel takes 18-167 (1.0 to 1.7 times as long; 24 rows of 64 sequences: 108 against 72).
+// With more rows it reads the cache once for every 16, but starts and ends sooner: up to 32 such
+// blocks in all and 2^17 slots between them it is 1.03 to 1.6 times as fast (8 nodes of 8 heads,
+// 4 key/value heads of 128: 2003 slots 14.5 against 20.7 us, 8003 slots 20.2 against 23.1, 16003
+// slots 28.5 against 27.0; 4 sequences of 1003 slots, 64 blocks, 21.7 against 20.7). The lengths
+// are not known here: the page table's capacity stands for them.
+bool few_rows(const attn::Args &a) {
+    const long long rows = (long long)a.N * a.G;
+    if (rows <= attn::kFewRows) return true;
+    const long long blocks = (long long)a.B * a.Hkv * ((rows + attn::kFewRows - 1) / attn::kFewRows);
+    long long slots = a.cap;
+    if (a.window > 0) slots = std::min(slots, (long long)a.window + a.sinks + a.N);
+    return blocks <= 32 && blocks * slots <= 1 << 17;
+}
+
 bool rows_ok(const void *p, long long ld, int width) {
     return p && aligned16(p) && ld >= width && ld % 8 == 0;
 }
@@ -121,9 +138,7 @@ moe_status moe_tree_attention(const moe_cache_desc *C, const void *q, long long 
     a.scale = C->scale;
     cudaStream_t s = (cudaStream_t)stream;
     if (!attn::tc_supported(a, C->dtype)) return cuda_status(attn::launch_simt(a, C->dtype, s));
-    // an item of at most 16 rows is bound by reading the cache, whatever multiplies
-    return cuda_status((long long)N * a.G <= attn::kFewRows ? attn::launch_few(a, s)
-                                                            : attn::launch_tc(a, s));
+    return cuda_status(few_rows(a) ? attn::launch_few(a, s) : attn::launch_tc(a, s));
 }
 
 moe_status moe_kv_append(const moe_cache_desc *C, const moe_rope_params *P, const void *q,

