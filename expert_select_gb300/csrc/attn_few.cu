@@ -106,13 +106,15 @@ __global__ void __launch_bounds__(kThr, Shape<DC>::kCtas) attn_few_kernel(const 
     cp.start(a, range);
     int lstage = 0;
     // the page of the lane's row in the tile that is copied next, looked up a tile ahead
-    // (INT_MIN: the row is past the sequence's end)
+    // (INT_MIN: the slot is past the sequence's end, or older than every row's window and not one
+    // of the first tokens: node positions are s.len or later)
     int page = INT_MIN, slot = 0;
     auto look_up = [&]() {
         page = INT_MIN;
         if (!ld.on) return;
         slot = ld.g.tl.at(ld.g.t + ld.t) * kBN + warp * 16 + (lane & 15);
-        if (slot < ld.g.s.L) page = a.table[(size_t)ld.g.b * a.max_pages + slot / a.page];
+        const bool old = a.window > 0 && slot >= a.sinks && slot <= ld.g.s.len - a.window;
+        if (slot < ld.g.s.L && !old) page = a.table[(size_t)ld.g.b * a.max_pages + slot / a.page];
     };
     look_up();
     auto issue = [&]() {  // copies the warp's 16 slots of the next tile, if there is one
@@ -128,14 +130,16 @@ __global__ void __launch_bounds__(kThr, Shape<DC>::kCtas) attn_few_kernel(const 
             const uint32_t have = __ballot_sync(0xffffffffu, ok) & 0xffffu;
             if (lane == 0) s_pages[warp][lstage] = have;
             const uint32_t dst = ring + lstage * 2 * S::kHalf;
+            if (have) {
 #pragma unroll
-            for (int i = 0; i < 4 * DC; ++i) {
-                const int idx = lane + 32 * i, row = idx / (8 * DC), ch = idx % (8 * DC);
-                const long long o = __shfl_sync(0xffffffffu, off, row) + ch * 8;
-                const bool there = ((have >> row) & 1u) && ch * 8 < a.dh;
-                const uint32_t at = dst + row * S::kRow + ((ch ^ (row & 7)) << 4);
-                cp16(at, kp + (there ? o : 0), there);
-                cp16(at + S::kHalf, vp + (there ? o : 0), there);
+                for (int i = 0; i < 4 * DC; ++i) {
+                    const int idx = lane + 32 * i, row = idx / (8 * DC), ch = idx % (8 * DC);
+                    const long long o = __shfl_sync(0xffffffffu, off, row) + ch * 8;
+                    const bool there = ((have >> row) & 1u) && ch * 8 < a.dh;
+                    const uint32_t at = dst + row * S::kRow + ((ch ^ (row & 7)) << 4);
+                    cp16(at, kp + (there ? o : 0), there);
+                    cp16(at + S::kHalf, vp + (there ? o : 0), there);
+                }
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -180,143 +184,150 @@ __global__ void __launch_bounds__(kThr, Shape<DC>::kCtas) attn_few_kernel(const 
         issue();
         asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 1) : "memory");
         __syncwarp();
-        const uint32_t sk = ring + stage * 2 * S::kHalf, sv = sk + S::kHalf;
-        const int k0 = g.tl.at(g.t + cp.t) * kBN + warp * 16;
-        // ---- S = Q K^T, two tiles of 8 keys
-        float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-        {
-            const int key = (lane & 7) + ((lane >> 4) << 3);  // matrices: keys 0-7 twice, 8-15 twice
-#pragma unroll
-            for (int k = 0; k < 4 * DC; ++k) {
-                uint32_t b[4];
-                const int ch = 2 * k + ((lane >> 3) & 1);
-                ldsm(sk + key * S::kRow + ((ch ^ (key & 7)) << 4), b);
-                mma16(s[0], q[k], b[0], b[1]);
-                mma16(s[1], q[k], b[2], b[3]);
-            }
-        }
+        // a piece of 16 slots without one to read (3 of 4 in a tile of a few first tokens) is done
         const uint32_t have = s_pages[warp][stage];
-        uint32_t vis[2] = {0xffffu, 0xffffu}, back = 0u;  // back: keys whose V is fixed up below
-        if (have != 0xffffu || tile_masked<16>(a, g.s, i0, i1, k0)) {
-            uint32_t some = 0u, all = 0xffffu;
+        if (have) {
+            const uint32_t sk = ring + stage * 2 * S::kHalf, sv = sk + S::kHalf;
+            const int k0 = g.tl.at(g.t + cp.t) * kBN + warp * 16;
+            // ---- S = Q K^T, two tiles of 8 keys
+            float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+            {
+                // matrices: keys 0-7 twice, 8-15 twice
+                const int key = (lane & 7) + ((lane >> 4) << 3);
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                uint32_t bits[1];
-                visible_bits<1>(a, g.s, node[x], pos[x], k0, bits);
-                vis[x] = bits[0] & have;
-                if (r0 + 8 * x < g.rows) {
-                    some |= vis[x];
-                    all &= vis[x];
+                for (int k = 0; k < 4 * DC; ++k) {
+                    uint32_t b[4];
+                    const int ch = 2 * k + ((lane >> 3) & 1);
+                    ldsm(sk + key * S::kRow + ((ch ^ (key & 7)) << 4), b);
+                    mma16(s[0], q[k], b[0], b[1]);
+                    mma16(s[1], q[k], b[2], b[3]);
                 }
             }
-            some = __reduce_or_sync(0xffffffffu, some);
-            all = __reduce_and_sync(0xffffffffu, all);
-            // 0 x V is NaN where V is not finite: clear the rows that no query sees and the
-            // non-finite elements of those that only some see (added back below)
-#pragma unroll 1
-            for (int i = 0; i < 4 * DC; ++i) {
-                const int idx = lane + 32 * i, row = idx / (8 * DC), ch = idx % (8 * DC);
-                if ((all >> row) & 1u) continue;
-                uint4 *at = reinterpret_cast<uint4 *>(gring + stage * 2 * S::kHalf + S::kHalf +
-                                                      row * S::kRow + ((ch ^ (row & 7)) << 4));
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if ((some >> row) & 1u) {
-                    v = *at;
-                    uint32_t *e = reinterpret_cast<uint32_t *>(&v);
-                    bool bad = false;
+            // back: keys whose V is fixed up below
+            uint32_t vis[2] = {0xffffu, 0xffffu}, back = 0u;
+            if (have != 0xffffu || tile_masked<16>(a, g.s, i0, i1, k0)) {
+                uint32_t some = 0u, all = 0xffffu;
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        if ((e[w] & 0x7f80u) == 0x7f80u) {
-                            e[w] &= 0xffff0000u;
-                            bad = true;
-                        }
-                        if ((e[w] & 0x7f800000u) == 0x7f800000u) {
-                            e[w] &= 0xffffu;
-                            bad = true;
-                        }
+                for (int x = 0; x < 2; ++x) {
+                    uint32_t bits[1];
+                    visible_bits<1>(a, g.s, node[x], pos[x], k0, bits);
+                    vis[x] = bits[0] & have;
+                    if (r0 + 8 * x < g.rows) {
+                        some |= vis[x];
+                        all &= vis[x];
                     }
-                    if (!bad) continue;
-                    back |= 1u << row;
                 }
-                *at = v;
-            }
-            back = __reduce_or_sync(0xffffffffu, back);
-            __syncwarp();
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    if (!((vis[x >> 1] >> (n * 8 + cq + (x & 1))) & 1u)) s[n][x] = -INFINITY;
-        }
-        // ---- running maximum; P
-        float top[2], f[2] = {1.f, 1.f};
-        bool raise = false;
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            float t = fmaxf(fmaxf(s[0][2 * x], s[0][2 * x + 1]), fmaxf(s[1][2 * x], s[1][2 * x + 1]));
-            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
-            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-            top[x] = t;
-            raise |= (t - m[x]) * cs > kRaise;
-        }
-        if (__any_sync(0xffffffffu, raise)) {
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const float mn = fmaxf(m[x], top[x]);
-                f[x] = m[x] == -INFINITY ? 0.f : ex2((m[x] - mn) * cs);
-                m[x] = mn;
-                l[x] *= f[x];
-            }
-#pragma unroll
-            for (int n = 0; n < 8 * DC; ++n) {
-                o[n][0] *= f[0];
-                o[n][1] *= f[0];
-                o[n][2] *= f[1];
-                o[n][3] *= f[1];
-            }
-        }
-        const float sub[2] = {m[0] == -INFINITY ? 0.f : m[0] * cs,
-                              m[1] == -INFINITY ? 0.f : m[1] * cs};
-        uint32_t p[4];
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const float p0 = ex2(fmaf(s[n][2 * x], cs, -sub[x]));
-                const float p1 = ex2(fmaf(s[n][2 * x + 1], cs, -sub[x]));
-                l[x] += p0 + p1;
-                p[2 * n + x] = pack_bf16(p0, p1);
-            }
-        }
-        // ---- O += P V
-        {
-            const int key = (lane & 7) + (((lane >> 3) & 1) << 3);  // keys 0-7, 8-15 of a column tile
-#pragma unroll
-            for (int n = 0; n < 4 * DC; ++n) {
-                uint32_t b[4];
-                const int ch = 2 * n + (lane >> 4);
-                ldsm_t(sv + key * S::kRow + ((ch ^ (key & 7)) << 4), b);
-                mma16(o[2 * n], p, b[0], b[1]);
-                mma16(o[2 * n + 1], p, b[2], b[3]);
-            }
-        }
-        if (back) {
+                some = __reduce_or_sync(0xffffffffu, some);
+                all = __reduce_and_sync(0xffffffffu, all);
+                // 0 x V is NaN where V is not finite: clear the rows that no query sees and the
+                // non-finite elements of those that only some see (added back below)
 #pragma unroll 1
-            for (int k = 0; k < 16; ++k) {
-                if (!((back >> k) & 1u)) continue;
-                const __nv_bfloat16 *v = vp + (long long)page_of(a, g.b, k0 + k) * a.st_page +
-                                         (long long)((k0 + k) % a.page) * a.st_tok +
-                                         (long long)g.h * a.st_head;
+                for (int i = 0; i < 4 * DC; ++i) {
+                    const int idx = lane + 32 * i, row = idx / (8 * DC), ch = idx % (8 * DC);
+                    if ((all >> row) & 1u) continue;
+                    uint4 *at = reinterpret_cast<uint4 *>(gring + stage * 2 * S::kHalf + S::kHalf +
+                                                          row * S::kRow + ((ch ^ (row & 7)) << 4));
+                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                    if ((some >> row) & 1u) {
+                        v = *at;
+                        uint32_t *e = reinterpret_cast<uint32_t *>(&v);
+                        bool bad = false;
 #pragma unroll
-                for (int n = 0; n < 8 * DC; ++n)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const int col = n * 8 + cq + (x & 1);
-                        if (col < a.dh && ((vis[x >> 1] >> k) & 1u)) {
-                            const float e = __bfloat162float(v[col]);
-                            if (!isfinite(e)) o[n][x] += e;
+                        for (int w = 0; w < 4; ++w) {
+                            if ((e[w] & 0x7f80u) == 0x7f80u) {
+                                e[w] &= 0xffff0000u;
+                                bad = true;
+                            }
+                            if ((e[w] & 0x7f800000u) == 0x7f800000u) {
+                                e[w] &= 0xffffu;
+                                bad = true;
+                            }
                         }
+                        if (!bad) continue;
+                        back |= 1u << row;
                     }
+                    *at = v;
+                }
+                back = __reduce_or_sync(0xffffffffu, back);
+                __syncwarp();
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        if (!((vis[x >> 1] >> (n * 8 + cq + (x & 1))) & 1u)) s[n][x] = -INFINITY;
+            }
+            // ---- running maximum; P
+            float top[2], f[2] = {1.f, 1.f};
+            bool raise = false;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                float t = fmaxf(fmaxf(s[0][2 * x], s[0][2 * x + 1]),
+                                fmaxf(s[1][2 * x], s[1][2 * x + 1]));
+                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+                top[x] = t;
+                raise |= (t - m[x]) * cs > kRaise;
+            }
+            if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float mn = fmaxf(m[x], top[x]);
+                    f[x] = m[x] == -INFINITY ? 0.f : ex2((m[x] - mn) * cs);
+                    m[x] = mn;
+                    l[x] *= f[x];
+                }
+#pragma unroll
+                for (int n = 0; n < 8 * DC; ++n) {
+                    o[n][0] *= f[0];
+                    o[n][1] *= f[0];
+                    o[n][2] *= f[1];
+                    o[n][3] *= f[1];
+                }
+            }
+            const float sub[2] = {m[0] == -INFINITY ? 0.f : m[0] * cs,
+                                  m[1] == -INFINITY ? 0.f : m[1] * cs};
+            uint32_t p[4];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float p0 = ex2(fmaf(s[n][2 * x], cs, -sub[x]));
+                    const float p1 = ex2(fmaf(s[n][2 * x + 1], cs, -sub[x]));
+                    l[x] += p0 + p1;
+                    p[2 * n + x] = pack_bf16(p0, p1);
+                }
+            }
+            // ---- O += P V
+            {
+                // keys 0-7, 8-15 of a column tile
+                const int key = (lane & 7) + (((lane >> 3) & 1) << 3);
+#pragma unroll
+                for (int n = 0; n < 4 * DC; ++n) {
+                    uint32_t b[4];
+                    const int ch = 2 * n + (lane >> 4);
+                    ldsm_t(sv + key * S::kRow + ((ch ^ (key & 7)) << 4), b);
+                    mma16(o[2 * n], p, b[0], b[1]);
+                    mma16(o[2 * n + 1], p, b[2], b[3]);
+                }
+            }
+            if (back) {
+#pragma unroll 1
+                for (int k = 0; k < 16; ++k) {
+                    if (!((back >> k) & 1u)) continue;
+                    const __nv_bfloat16 *v = vp + (long long)page_of(a, g.b, k0 + k) * a.st_page +
+                                             (long long)((k0 + k) % a.page) * a.st_tok +
+                                             (long long)g.h * a.st_head;
+#pragma unroll
+                    for (int n = 0; n < 8 * DC; ++n)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const int col = n * 8 + cq + (x & 1);
+                            if (col < a.dh && ((vis[x >> 1] >> k) & 1u)) {
+                                const float e = __bfloat162float(v[col]);
+                                if (!isfinite(e)) o[n][x] += e;
+                            }
+                        }
+                }
             }
         }
         __syncwarp();
@@ -333,7 +344,7 @@ __global__ void __launch_bounds__(kThr, Shape<DC>::kCtas) attn_few_kernel(const 
                 }
             }
             __syncthreads();
-            float mt[2], lt[2];
+            float mt[2], lt[2], f[2];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const int row = r0 + 8 * x;
