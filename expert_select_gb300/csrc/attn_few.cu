@@ -13,7 +13,7 @@
 //
 // Measured: one token over 131k slots (4 key/value heads of 128, bf16, 268 MB) 51 us with the
 // combine (5.2 TB/s over the whole call; 39.5 us at the copy bandwidth); 128 tokens with a window
-// of 128 slots (1024 items of four tiles) 29 us. Against the tcgen05 kernel, 8 rows of 4
+// of 128 slots (1024 items of 3-4 tiles) 28 us. Against the tcgen05 kernel, 8 rows of 4
 // key/value heads of 128: one token over 60001 slots 31.8 us to 39.9, 64 of them over up to 4003
 // slots 64.0 to 73.5. TMA boxes of 16 slots instead of cp.async were no faster (131k slots: 53 us).
 #include <limits.h>
