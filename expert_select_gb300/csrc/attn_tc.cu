@@ -26,11 +26,11 @@
 // passes through shared memory.
 //
 // Measured (32 query and 4 key/value heads of 128, bf16): two chunks of 4096 tokens over 28k cached
-// ones 3.3 ms, 1.2 PFLOP/s; there a tile pair takes 1750 cycles, of which the tensor cores are busy
-// 1090, and the SM clock falls from 2.0 to 1.66 GHz under the load (power). 64 trees of 65 nodes
-// over 0.2-8k tokens 0.50 ms: 65 nodes of 8 heads are 520 rows, three items that each read the
-// sequence's K and V (1.6 GB from HBM for 0.55 GB of cache), and a piece of an item costs about
-// 10 us beside its tiles (query rows, the pipeline's start and end, the output).
+// ones 3.3 ms, 1.2 PFLOP/s; there a tile pair takes 1750 cycles, where its products need 1090 at
+// the nominal rate, and the SM clock falls from 2.0 to 1.66 GHz under the load (power). 64 trees of
+// 65 nodes over 0.2-8k tokens 0.42 ms: 65 nodes of 8 heads are 520 rows, three items that each read
+// the sequence's K and V (1.6 GB from HBM for 0.55 GB of cache), and a piece of an item costs
+// about 10 us beside its tiles (query rows, the pipeline's start and end, the output).
 //
 // A masked score is -inf, so its P is 0; but 0 x V is NaN where V is infinite or NaN. In tiles
 // that hold masked slots (the last ones, and a window's first) warp 2 therefore clears the rows of
@@ -293,8 +293,8 @@ attn_tc_kernel(const __grid_constant__ Params p) {
         const uint32_t id_s = idesc_bf16(128, kBN), id_o = idesc_bf16(128, 64 * DC) | kIdescBMn;
         // A slot's products are issued by a warp of its own: what bounds a tile's time is this
         // warp's chain of waits and issues, not the products. (One warp for both slots took 2060
-        // cycles for a pair of tiles of which the tensor cores were busy 1090; votes and divisions
-        // by the ring's length at every wait had made it 2400.) So stages and parities are
+        // cycles for a pair of tiles whose products need 1090 at the nominal rate; votes and
+        // divisions by the ring's length at every wait had made it 2400.) So stages and parities are
         // counted, and the waits' verdicts are looked at once a tile.
         const int slot = warp == 1 ? 0 : 1;
         uint32_t kst = 0, kph = 0, vst = 0, vph = 0, seg = 0;

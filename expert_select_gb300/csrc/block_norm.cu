@@ -461,7 +461,7 @@ cudaError_t launch_t(int d, const void *x, const void *branch, const void *w_pos
     };
     const int vecs = d / 8;
     // A warp per row where there are several rows for each of the SM's warps, room for their rings,
-    // and gate rows that many rows share: 8192 x 2880 bf16 takes 41 us so (4.6 TB/s) and 57 us with
+    // and gate rows that many rows share: 8192 x 2880 bf16 takes 42 us so (4.5 TB/s) and 57 us with
     // 384 threads a row, whose two block reductions are a chain of 2000 cycles; a few rows are done
     // sooner with up to 512 threads each (65 x 2048: 2.5 us).
     const size_t row_smem = (size_t)d * (8 + 4 * kRowWarps * sizeof(T));
