@@ -67,9 +67,14 @@ struct Params {
 // whoever waits must know the phase before to be over. K and V stages have barriers of their own
 // and one producer each for that, and the two S buffers too: S of tile u + 2 comes after P V of
 // tile u, so P V of tile u - 1 (the other buffer) may be outstanding when S of tile u is there.
+// And each slot has a query barrier of its own, used only in pieces where the slot has tiles: the
+// next such piece's rows are loaded after the slot's products of this one. (A barrier that both
+// slots waited for in every piece could be two phases on before the issuing warp of a slot without
+// tiles looked at it: in pieces of one key tile and at most 128 rows nothing else waits for that
+// warp until the stages of K or V run out.)
 struct Ctl {
     uint64_t kfull[kMaxStages], kempty[kMaxStages], vfull[kMaxStages], vempty[kMaxStages],
-        vready[kMaxStages], s_full[2][2], p_full[2][2], pv_done[2][2], q_full, done[2];
+        vready[kMaxStages], s_full[2][2], p_full[2][2], pv_done[2][2], q_full[2], done[2];
     long long scratch[34];
     uint32_t tmem;
     volatile int abort;
@@ -162,10 +167,9 @@ attn_tc_kernel(const __grid_constant__ Params p) {
                 mbar_init(bar(c.p_full[i][x]), 4);  // a lane of each warp
                 mbar_init(bar(c.pv_done[i][x]), 1);
             }
+            mbar_init(bar(c.q_full[i]), 8);  // a lane of each softmax warp
+            mbar_init(bar(c.done[i]), 1);
         }
-        mbar_init(bar(c.q_full), 8);
-        mbar_init(bar(c.done[0]), 1);
-        mbar_init(bar(c.done[1]), 1);
         c.abort = c.bad_page = c.bad_v = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         prefetch_map(&p.kmap);
@@ -297,7 +301,7 @@ attn_tc_kernel(const __grid_constant__ Params p) {
         // divisions by the ring's length at every wait had made it 2400.) So stages and parities are
         // counted, and the waits' verdicts are looked at once a tile.
         const int slot = warp == 1 ? 0 : 1;
-        uint32_t kst = 0, kph = 0, vst = 0, vph = 0, seg = 0;
+        uint32_t kst = 0, kph = 0, vst = 0, vph = 0, qph = 0;
         uint32_t u0 = 0;  // tiles of the slot before the segment
         bool ok = true;
         auto wait = [&](uint64_t &b, uint32_t par) {
@@ -358,10 +362,13 @@ attn_tc_kernel(const __grid_constant__ Params p) {
                     mma_ts_elect(tO, pt + x * 8u, v + x * (2048u >> 4), id_o, !first || x != 0);
                 commit_elect(bar(c.pv_done[slot][u & 1u]));
             };
-            wait(c.q_full, seg++ & 1u);
-            __syncwarp();
-            tc_fence_after();
-            mma_issued = true;
+            if (two || n > slot) {  // the slot has tiles
+                wait(c.q_full[slot], qph);
+                qph ^= 1u;
+                __syncwarp();
+                tc_fence_after();
+                mma_issued = true;
+            }
             // with two row tiles each slot takes every key tile, else the slots take them in turn;
             // S runs two of the slot's tiles ahead of P V
             const int ahead = two ? 2 : 4, sh = two ? 0 : 1;
@@ -504,7 +511,10 @@ attn_tc_kernel(const __grid_constant__ Params p) {
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(c.q_full));
+                if (lane == 0) {
+                    mbar_arrive(bar(c.q_full[0]));
+                    if (two || n > 1) mbar_arrive(bar(c.q_full[1]));
+                }
             }
             const int row = two ? slot * 128 + trow : trow;  // row of the item
             const bool active = row - lane < g.rows;         // the warp has rows
