@@ -232,7 +232,9 @@ __global__ void __launch_bounds__(256) commit_kernel(const CommitArgs a) {
     for (int j = tid; j < n; j += blockDim.x) {
         const int m = path[j], prev = j > 0 ? path[j - 1] : -1;
         int f = 0;
-        if (m <= prev || m < 0 || m >= a.cap - len) {
+        // (m < j: behind a bad node the path may ascend again from a low one, and slot len + j
+        // need not lie in the table; an ascending path has m >= j)
+        if (m <= prev || m < j || m >= a.cap - len) {
             f = FLAG_BAD_SEQUENCE;
         } else {
             const int ps = table[(len + m) / a.page], pd = table[(len + j) / a.page];

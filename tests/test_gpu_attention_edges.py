@@ -32,3 +32,26 @@ def test_many_pieces_of_one_key_tile(B, dh, page):
     for _ in range(3):
         blk.attend()
     blk.check()
+
+
+@pytest.mark.parametrize("path,room", [([-5, -3, 0], 1), ([3, 0, 1, 2], 3), ([7, -1, 0, 1, 2], 2)])
+def test_a_bad_path_looks_up_no_slot_past_the_table(path, room):
+    """Behind its first bad node a path ascends again from a low one: node path[j] has a slot in the
+    table, slot len + j has none. The entry behind the row belongs to the next sequence, whose table
+    is not to be looked at (its entries are outside the pool: bit 2 would tell)."""
+    blk = Block(52, BF, lens=(40, 40), ns=(8, 8), H=4, Hkv=1, page=1).upload()
+    cap = blk.max_pages
+    blk.lend.copy_(torch.tensor([cap - room, 0], dtype=torch.int32))
+    blk.tabled[0] = torch.arange(cap, dtype=torch.int32) % blk.n_pages
+    blk.tabled[1] = -9
+    k, v = blk.kd.clone(), blk.vd.clone()
+    paths = torch.tensor([path, [0] * len(path)], dtype=torch.int32, device=DEV)
+    new = torch.zeros(2, dtype=torch.int32, device=DEV)
+    M.moe_kv_commit(blk.C, blk.kd, blk.vd, blk.tabled, blk.lend, paths,
+                    torch.tensor([len(path), 0], dtype=torch.int32, device=DEV), new, blk.ws)
+    assert M.moe_workspace_check(blk.ws) == 8
+    kept = 1 if 0 <= path[0] < room else 0
+    assert new.tolist() == [cap - room + kept, 0]
+    if not kept:
+        assert torch.equal(blk.kd.nan_to_num(9), k.nan_to_num(9))
+        assert torch.equal(blk.vd.nan_to_num(9), v.nan_to_num(9))
