@@ -662,7 +662,9 @@ attn_tc_kernel(const __grid_constant__ Params p) {
                 *reinterpret_cast<float2 *>(a.part_ml + part_row(a, blockIdx.x, g, row) * 2) =
                     make_float2(m2, l);
             }
-            if (c.bad_v) {
+            // one verdict for the warp, whose lanes also meet here: the keeper may set the flag for a
+            // later piece at any moment, and tensor memory is read by all lanes together
+            if (__any_sync(0xffffffffu, c.bad_v)) {
                 give_back(a, g, node, pos, n, 2 * DC, tO);
                 f0 = fmaxf(f0, 1e-37f);  // what was given back must not vanish in the merge
             }

@@ -55,3 +55,28 @@ def test_a_bad_path_looks_up_no_slot_past_the_table(path, room):
     if not kept:
         assert torch.equal(blk.kd.nan_to_num(9), k.nan_to_num(9))
         assert torch.equal(blk.vd.nan_to_num(9), v.nan_to_num(9))
+
+
+@pytest.mark.parametrize("dh,ns,ln", [(128, 10, 300), (64, 12, 60), (128, 70, 200)])
+def test_values_that_are_not_finite_in_many_pieces_in_a_row(dh, ns, ln):
+    """Every third sequence has a node of infinite values: while a piece's output is formed, the
+    warp that looks after V meets such values in a later one. Rows that do not see them are what they
+    were, rows that do are infinite."""
+    r = np.random.default_rng(dh + ns)
+    B = 400
+    lens = tuple(int(v) for v in r.integers(0, ln, B))
+    blk = Block(53, BF, lens=lens, ns=(ns,) * B, H=4, Hkv=2, dh=dh, kind="tree").upload().attend()
+    torch.cuda.synchronize()
+    want = blk.out.clone()
+    sees = torch.zeros(blk.R, dtype=torch.bool)
+    for b in range(0, B, 3):
+        m = ns // 2
+        j = lens[b] + m
+        blk.vd[int(blk.table[b, j // blk.page]), j % blk.page] = float("inf")
+        sees[blk.rows[b]:blk.rows[b + 1]] = torch.from_numpy(blk.visible(b)[:, j])
+    for _ in range(3):
+        blk.out.fill_(7.25)
+        blk.attend()
+        assert torch.equal(blk.out[~sees.to(DEV)], want[~sees.to(DEV)])
+        assert torch.isinf(blk.out[sees.to(DEV)]).all()
+    assert M.moe_workspace_check(blk.ws) == 0
