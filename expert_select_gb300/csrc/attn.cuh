@@ -383,6 +383,13 @@ __device__ __forceinline__ bool tile_masked(const Args &a, const Seq &s, int i0,
     return k0 < max_pos - a.window + 1 && k0 + BN > a.sinks;
 }
 
+// No row of the sequence sees slots a .. b: older than every window (nodes' positions are s.len or
+// later) and behind the first tokens. Their table entries may hold anything: a cache with a window
+// gives such pages back.
+__device__ __forceinline__ bool out_of_reach(const Args &a, const Seq &s, int from, int to) {
+    return a.window > 0 && from >= a.sinks && to <= s.len - a.window;
+}
+
 // The page of slot j, or -1 if the table's entry is outside the pool.
 __device__ __forceinline__ int page_of(const Args &a, int b, int j) {
     const int pg = a.table[(size_t)b * a.max_pages + j / a.page];

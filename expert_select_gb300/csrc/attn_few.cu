@@ -106,15 +106,14 @@ __global__ void __launch_bounds__(kThr, Shape<DC>::kCtas) attn_few_kernel(const 
     cp.start(a, range);
     int lstage = 0;
     // the page of the lane's row in the tile that is copied next, looked up a tile ahead
-    // (INT_MIN: the slot is past the sequence's end, or older than every row's window and not one
-    // of the first tokens: node positions are s.len or later)
+    // (INT_MIN: the slot is past the sequence's end or out of every row's reach)
     int page = INT_MIN, slot = 0;
     auto look_up = [&]() {
         page = INT_MIN;
         if (!ld.on) return;
         slot = ld.g.tl.at(ld.g.t + ld.t) * kBN + warp * 16 + (lane & 15);
-        const bool old = a.window > 0 && slot >= a.sinks && slot <= ld.g.s.len - a.window;
-        if (slot < ld.g.s.L && !old) page = a.table[(size_t)ld.g.b * a.max_pages + slot / a.page];
+        if (slot < ld.g.s.L && !out_of_reach(a, ld.g.s, slot, slot))
+            page = max(a.table[(size_t)ld.g.b * a.max_pages + slot / a.page], -1);
     };
     look_up();
     auto issue = [&]() {  // copies the warp's 16 slots of the next tile, if there is one

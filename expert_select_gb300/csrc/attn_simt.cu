@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(kThr) attn_simt_kernel(const Args a) {
             for (int i = tid; i < 32 * (D / 8); i += kThr) {
                 const int key = i / (D / 8), col = (i % (D / 8)) * 8;
                 const int j = k0 + key;
-                bool ok = j < g.s.L && col < a.dh;
+                bool ok = j < g.s.L && col < a.dh && !out_of_reach(a, g.s, j, j);
                 size_t off = 0;
                 if (ok) {
                     const int pi = j / a.page, pg = a.table[(size_t)g.b * a.max_pages + pi];
@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(kThr) attn_simt_kernel(const Args a) {
             {
                 const int j = k0 + (tid & 31);
                 bool ok = true;
-                if (j < g.s.L) {
+                if (j < g.s.L && !out_of_reach(a, g.s, j, j)) {
                     const int pg = a.table[(size_t)g.b * a.max_pages + j / a.page];
                     ok = pg >= 0 && pg < a.n_pages;
                 }

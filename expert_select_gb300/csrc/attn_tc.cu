@@ -204,17 +204,21 @@ attn_tc_kernel(const __grid_constant__ Params p) {
         while (ok && next_segment<kBN, kHeavy>(a, r, g)) {
             const int n = __shfl_sync(0xffffffffu, g.count, 0);
             // Pages of 64 boxes (one tile of single-slot boxes, 64 tiles of 64-slot ones), two a
-            // lane; the next 64 boxes' are on their way while these are used.
+            // lane; the next 64 boxes' are on their way while these are used. A box out of every
+            // row's reach is not copied (its stage keeps what it held: those scores are masked, and
+            // the keeper clears those rows of V).
             const int per_tile = kBN / p.box, in_use = (g.s.L + p.box - 1) / p.box;  // boxes
             int first = -1, in_page = 0;  // box of pg[0] of lane 0; slot in its page of the next box
+            constexpr int kNone = INT_MIN;  // no box, or one that is not needed
             int pg[2], next[2];
             uint32_t good[2], there[2];
             auto look_up = [&](int from, int (&out)[2]) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int bx = from + lane + 32 * i;
-                    out[i] = bx < in_use ? a.table[(size_t)g.b * a.max_pages + bx * p.box / a.page]
-                                         : -1;
+                    out[i] = bx < in_use && !out_of_reach(a, g.s, bx * p.box, (bx + 1) * p.box - 1)
+                                 ? max(a.table[(size_t)g.b * a.max_pages + bx * p.box / a.page], -1)
+                                 : kNone;
                 }
             };
             auto take = [&](int from) {  // makes `next` current and looks further ahead
@@ -223,7 +227,7 @@ attn_tc_kernel(const __grid_constant__ Params p) {
                 for (int i = 0; i < 2; ++i) {
                     pg[i] = next[i];
                     good[i] = __ballot_sync(0xffffffffu, pg[i] >= 0 && pg[i] < a.n_pages);
-                    there[i] = __ballot_sync(0xffffffffu, from + lane + 32 * i < in_use);
+                    there[i] = __ballot_sync(0xffffffffu, pg[i] != kNone);
                 }
                 look_up(from + 64, next);
                 if (good[0] != there[0] || good[1] != there[1]) {
@@ -410,13 +414,19 @@ attn_tc_kernel(const __grid_constant__ Params p) {
                 const int k0 = g.tl.at(g.t + t) * kBN;
                 if (c.bad_page || tile_masked<kBN>(a, g.s, i0, i1, k0)) {
                     // rows that no query of the item sees are cleared whole: with one node all
-                    // that it does not see, else what lies past the end or has no page
+                    // that it does not see, else what lies past the end, is out of every row's
+                    // reach or has no page
                     uint32_t bits[2];
                     if (i0 == i1) {
                         visible_bits<2>(a, g.s, i0, pos, k0, bits);
                     } else {
 #pragma unroll
-                        for (int w = 0; w < 2; ++w) bits[w] = range_bits(0, g.s.L, k0 + 32 * w);
+                        for (int w = 0; w < 2; ++w) {
+                            const int kw = k0 + 32 * w;
+                            bits[w] = range_bits(0, g.s.L, kw);
+                            if (a.window > 0)
+                                bits[w] &= ~range_bits(a.sinks, g.s.len - a.window + 1, kw);
+                        }
                     }
                     uint8_t *tile = gV + (size_t)st * kKv;
 #pragma unroll 1

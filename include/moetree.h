@@ -471,7 +471,9 @@ size_t moe_attention_workspace_bytes(const moe_cache_desc *C, int B, int N);
  * gives zeros. A slot that no row sees takes no part, whatever it holds (infinities, NaN).
  *   q           [R, H, dh] device, rows ldq elements apart (ldq a multiple of 8, >= H dh).
  *   k_pages, v_pages  the pools; the block's own k and v must be in them (moe_kv_append).
- *   page_table  [B, max_pages] device int32; entries past a sequence's last slot are not read.
+ *   page_table  [B, max_pages] device int32; entries of pages that no row can see may hold
+ *               anything: past a sequence's last slot, and, with a window, those whose slots are
+ *               all at or before cache_len - window and not among the first sink_tokens.
  *   cache_len   [B] device int32, committed tokens.
  *   row_start   [B + 1] device int32: sequence b has rows row_start[b] .. row_start[b+1] - 1, at
  *               most N of them (none is fine); rows past row_start[B] are left as they are.

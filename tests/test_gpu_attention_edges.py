@@ -80,3 +80,45 @@ def test_values_that_are_not_finite_in_many_pieces_in_a_row(dh, ns, ln):
         assert torch.equal(blk.out[~sees.to(DEV)], want[~sees.to(DEV)])
         assert torch.isinf(blk.out[sees.to(DEV)]).all()
     assert M.moe_workspace_check(blk.ws) == 0
+
+
+# shape, and which kernel it takes in bf16
+WINDOWED = [
+    dict(lens=(1000, 130, 77), ns=(1, 1, 1), H=16, Hkv=2, window=100, sinks=4),           # few rows
+    dict(lens=(1000, 5), ns=(12, 12), H=8, Hkv=2, dh=128, window=50, kind="tree", page=5),  # few rows
+    dict(lens=(900, 400), ns=(65, 65), H=16, Hkv=2, dh=128, window=128, sinks=4, kind="tree"),
+    dict(lens=(900, 1200), ns=(65, 1), H=16, Hkv=2, dh=128, window=130, sinks=70, page=1),
+    dict(lens=(3000,), ns=(300,), H=8, Hkv=1, window=200, page=32, layout="hnd"),
+    dict(lens=(2000, 0), ns=(200, 150), H=8, Hkv=1, dh=80, window=70, sinks=9, page=7),
+    dict(lens=(600, 64), ns=(30, 40), H=4, Hkv=2, dh=136, window=40, sinks=3, page=8),    # CUDA cores
+]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("case", WINDOWED, ids=range(len(WINDOWED)))
+@pytest.mark.parametrize("entry", [-1, 1 << 30])
+def test_pages_older_than_every_window_need_no_entry(case, dtype, entry):
+    """An engine with a window gives pages back that no row can see any more: their entries may hold
+    anything, what is left in the pages too, and nothing is flagged."""
+    blk = Block(54, dtype, **case).upload()
+    gone = 0
+    for b, ln in enumerate(blk.lens):
+        for p in range(ln // blk.page):
+            if p * blk.page >= blk.sinks and (p + 1) * blk.page - 1 <= ln - blk.window:
+                pg = int(blk.table[b, p])
+                blk.kd[pg] = float("nan")
+                blk.vd[pg] = float("nan")
+                blk.tabled[b, p] = entry
+                gone += 1
+    assert gone > 0
+    blk.attend().check()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("n", [1, 65])
+@pytest.mark.parametrize("entry", [-1, -(1 << 31), (1 << 31) - 1])
+def test_any_entry_outside_the_pool_is_flagged(dtype, n, entry):
+    blk = Block(58, dtype, lens=(200,), ns=(n,), H=4, Hkv=1, dh=128).upload()
+    blk.tabled[0, 3] = entry
+    blk.attend()
+    assert M.moe_workspace_check(blk.ws) == 4
