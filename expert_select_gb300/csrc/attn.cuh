@@ -102,7 +102,9 @@ __device__ __forceinline__ Tiles tiles_of(const Args &a, const Seq &s, int q0, i
     if (a.window > 0) {
         // the oldest slot a window can reach (tree nodes may all be at the root's depth)
         const int lo = max(0, s.len + (a.parent ? 0 : i0) - a.window + 1);
-        t.w0 = min(lo / BN, all);
+        // (one tile at least: where lengths are cut to the table, rows past its end may see nothing,
+        // and an item without tiles would not write their zeros)
+        t.w0 = min(lo / BN, all - 1);
         t.ns = min((int)(((long long)a.sinks + BN - 1) / BN), t.w0);
     }
     t.nt = t.ns + all - t.w0;

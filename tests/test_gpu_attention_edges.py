@@ -122,3 +122,27 @@ def test_any_entry_outside_the_pool_is_flagged(dtype, n, entry):
     blk.tabled[0, 3] = entry
     blk.attend()
     assert M.moe_workspace_check(blk.ws) == 4
+
+
+@pytest.mark.parametrize("dtype,dh", [(BF, 64), (BF, 128), (BF, 136), (F32, 64)])
+@pytest.mark.parametrize("N,over", [(1, 0), (40, 2), (300, 3), (300, 0)])
+def test_rows_past_the_table_that_see_nothing_give_zeros(dtype, dh, N, over):
+    """A sequence whose length leaves its block `over` slots of a table that ends with a key tile,
+    under a window of 2: node i sees slots len + i - 1 and len + i as far as there are any. Rows of
+    whole items see nothing."""
+    blk = Block(55, dtype, lens=(16,), ns=(N,), page=64, H=4, Hkv=1, dh=dh, window=2).upload()
+    blk.lend[0] = blk.max_pages * blk.page - over
+    blk.tabled[:] = blk.tabled[0, 0]
+    blk.kd[:] = 1
+    blk.vd[:] = 2
+    blk.attend()
+    torch.cuda.synchronize()
+    assert M.moe_workspace_check(blk.ws) == 8
+    assert (blk.out[:over + 1] == 2).all() and torch.isfinite(blk.lse[:over + 1]).all()
+    assert (blk.out[over + 1:] == 0).all() and (blk.lse[over + 1:] == -float("inf")).all()
+    one = Block(55, dtype, lens=(16,), ns=(N,), page=64, H=4, Hkv=1, dh=dh, window=1).upload()
+    one.lend[0] = one.max_pages * one.page
+    one.attend()
+    torch.cuda.synchronize()
+    assert M.moe_workspace_check(one.ws) == 8
+    assert (one.out == 0).all() and (one.lse == -float("inf")).all()
