@@ -64,6 +64,15 @@ bool few_rows(const attn::Args &a) {
     return blocks <= 32 && blocks * slots <= 1 << 17;
 }
 
+// Do n bytes at p and m bytes at q share any?
+bool overlap(const void *p, size_t n, const void *q, size_t m) {
+    return p && q && (uintptr_t)p < (uintptr_t)q + m && (uintptr_t)q < (uintptr_t)p + n;
+}
+// Bytes from the first to the last of R rows of `width` elements, ld apart.
+size_t span(int R, long long ld, int width, int dtype) {
+    return ((size_t)(R - 1) * ld + width) * elem_size(dtype);
+}
+
 bool rows_ok(const void *p, long long ld, int width) {
     return p && aligned16(p) && ld >= width && ld % 8 == 0;
 }
@@ -100,9 +109,8 @@ moe_status moe_tree_attention(const moe_cache_desc *C, const void *q, long long 
     if ((long long)B * (((long long)N * a.G + attn::kSimtRows - 1) / attn::kSimtRows) > (1 << 30))
         return MOE_ERR_UNSUPPORTED;
     // one CTA may still read q where another has written its rows
-    const size_t elt = C->dtype == MOE_DTYPE_F32 ? 4 : 2, row = (size_t)C->H * C->dh;
-    const uintptr_t q0 = (uintptr_t)q, o0 = (uintptr_t)out;
-    if (o0 < q0 + ((size_t)(R - 1) * ldq + row) * elt && q0 < o0 + (size_t)R * row * elt)
+    const int row = C->H * C->dh;
+    if (overlap(out, span(R, row, row, C->dtype), q, span(R, ldq, row, C->dtype)))
         return MOE_ERR_ARG;
     const attn::WsLayout w = attn::ws_layout(C->dh, (long long)N * a.G);
     a.q = q;
@@ -157,6 +165,13 @@ moe_status moe_kv_append(const moe_cache_desc *C, const moe_rope_params *P, cons
     if (q && q == q_out && ldq != (long long)C->H * C->dh) return MOE_ERR_ARG;
     if (!rows_ok(k, ldk, C->H_kv * C->dh) || !rows_ok(v, ldv, C->H_kv * C->dh) || !k_pages ||
         !v_pages || !aligned16(k_pages) || !aligned16(v_pages) || !page_table || !cache_len)
+        return MOE_ERR_ARG;
+    // rows are taken in no order: q_out may be q itself, row for row, and else nothing that is read
+    const int qw = C->H * C->dh, kw = C->H_kv * C->dh;
+    const size_t out_bytes = q ? span(R, qw, qw, C->dtype) : 0;
+    if ((q != q_out && overlap(q_out, out_bytes, q, span(R, ldq, qw, C->dtype))) ||
+        overlap(q_out, out_bytes, k, span(R, ldk, kw, C->dtype)) ||
+        overlap(q_out, out_bytes, v, span(R, ldv, kw, C->dtype)))
         return MOE_ERR_ARG;
     if (!aligned16(P->q_weight) || !aligned16(P->k_weight) || ((uintptr_t)workspace & 255u))
         return MOE_ERR_ARG;

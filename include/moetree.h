@@ -514,7 +514,8 @@ typedef struct {
  * n).
  *   q [R, H, dh], k, v [R, H_kv, dh] device, rows ldq, ldk, ldv elements apart (each may be
  *   part of one projection's output); q_out [R, H, dh] device, dense; it may be q itself where
- *   ldq = H dh. q and q_out may both be NULL (only the cache is written).
+ *   ldq = H dh, and must not overlap q otherwise, nor k or v (refused). q and q_out may both be
+ *   NULL (only the cache is written).
  *   workspace: only its check word is used (bits as for moe_tree_attention; rows whose slot has
  *   no valid page are not written to the cache); may be NULL.
  * Other arguments as moe_tree_attention. */
