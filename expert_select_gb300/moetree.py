@@ -432,7 +432,7 @@ def _rows(fn, name, t, dtype, shape, index) -> int:
         return heads * dh
     if one != 1 or (heads > 1 and head != dh):
         raise ValueError(f"{fn}: the heads of {name}'s rows must lie side by side")
-    return ld if n > 1 else max(ld, heads * dh)
+    return ld if n > 1 else heads * dh  # (a single row has no stride to speak of)
 
 
 def _at(t: Optional[torch.Tensor]):

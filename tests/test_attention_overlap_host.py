@@ -55,3 +55,11 @@ def test_append_refuses_queries_over_what_it_reads(kw):
 ], ids=range(8))
 def test_append_takes_queries_beside_what_it_reads(kw):
     assert _append(**kw) in OK_UNTIL_CUDA
+
+
+def test_a_single_row_has_no_stride():
+    """The row of one token in a projection's output: the binding gives its width as its stride."""
+    rows = torch.zeros(1, 40, 128, dtype=torch.bfloat16)
+    assert M._rows("f", "q", rows[:, :32], torch.bfloat16, (1, 32, 128), -1) == 32 * 128
+    assert M._rows("f", "q", torch.zeros(3, 40, 128)[:, :32], torch.float32, (3, 32, 128),
+                   -1) == 40 * 128

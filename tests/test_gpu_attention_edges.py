@@ -146,3 +146,16 @@ def test_rows_past_the_table_that_see_nothing_give_zeros(dtype, dh, N, over):
     torch.cuda.synchronize()
     assert M.moe_workspace_check(one.ws) == 8
     assert (one.out == 0).all() and (one.lse == -float("inf")).all()
+
+
+def test_a_single_row_of_a_projection_is_rotated_in_place():
+    """q as the first heads of one row of a projection's output, and q_out the same memory."""
+    blk = Block(59, BF, lens=(30,), ns=(1,), H=8, Hkv=2).upload()
+    freq = torch.tensor([1.0, 0.1, 0.01, 0.001], device=DEV)
+    qkv = torch.randn(1, 12, 64, device=DEV).to(BF)
+    want, kept = torch.empty(1, 8, 64, dtype=BF, device=DEV), qkv.clone()
+    for q_out in (want, qkv[:, :8]):
+        M.moe_kv_append(blk.C, qkv[:, :8], qkv[:, 8:10], qkv[:, 10:], blk.kd, blk.vd, blk.tabled,
+                        blk.lend, 1, 1, q_out, blk.ws, inv_freq=freq)
+    assert torch.equal(qkv[:, :8], want) and not torch.equal(want, kept[:, :8])
+    assert torch.equal(qkv[:, 8:], kept[:, 8:])
