@@ -257,6 +257,18 @@ moe_status moe_block_norm(const moe_layer_desc *L, const void *x, const void *br
     if ((h && h == hn) || (!branch && (w_post || gate))) return MOE_ERR_ARG;
     for (const void *p : {x, branch, w_post, gate, w_pre, (const void *)h, (const void *)hn})
         if (!aligned16(p)) return MOE_ERR_ARG;
+    // rows are taken in no order: an output may be an input row for row, else shares nothing
+    const size_t all = span(R, L->d, L->d, L->dtype), row = span(1, 0, L->d, L->dtype);
+    const size_t gates = gate ? row * (((size_t)R + gate_rows - 1) / gate_rows) : 0;
+    auto over = [&](const void *o, const void *in, size_t n, bool by_rows) {
+        return !(by_rows && o == in) && overlap(o, all, in, n);
+    };
+    for (const void *o : {(const void *)h, (const void *)hn})
+        if (over(o, x, all, o == h || h != x) || over(o, branch, all, true) ||
+            over(o, gate, gates, gate_rows == 1) || over(o, w_post, row, false) ||
+            over(o, w_pre, row, false))
+            return MOE_ERR_ARG;
+    if (overlap(h, all, hn, all)) return MOE_ERR_ARG;
     return cuda_status(launch_block_norm(*L, x, branch, w_post, gate, gate_rows, scale, w_pre, eps,
                                          R, h, hn, (cudaStream_t)stream));
 }

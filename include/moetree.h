@@ -544,7 +544,8 @@ moe_status moe_kv_commit(const moe_cache_desc *C, void *k_pages, void *v_pages,
  * Sums in fp32 (rows whose squares leave fp32's range are scaled first); hn is formed from h
  * before its rounding; each output is rounded once.
  *   x, branch, h, hn [R, d] device, layer dtype; h may be x or branch; hn may be NULL, or
- *   branch, or x where h is not x. branch NULL: h = x (h may be NULL then).
+ *   branch, or x where h is not x. branch NULL: h = x (h may be NULL then). Outputs that overlap
+ *   one another or an input in any other way are refused.
  *   gate [ceil(R / gate_rows), d] or NULL: rows r share gate row r / gate_rows (gate_rows = R: one
  *   row for all). w_post, w_pre [d]. eps >= 0. All 16-byte aligned. */
 moe_status moe_block_norm(const moe_layer_desc *L, const void *x, const void *branch,

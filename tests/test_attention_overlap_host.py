@@ -63,3 +63,37 @@ def test_a_single_row_has_no_stride():
     assert M._rows("f", "q", rows[:, :32], torch.bfloat16, (1, 32, 128), -1) == 32 * 128
     assert M._rows("f", "q", torch.zeros(3, 40, 128)[:, :32], torch.float32, (3, 32, 128),
                    -1) == 40 * 128
+
+
+def _norm(x=BASE, branch=BASE + (1 << 20), post=None, gate=None, rows=0, pre=None, R=4,
+          h=BASE + (2 << 20), hn=BASE + (3 << 20), dtype="bf16"):
+    at = lambda p: None if p is None else C.c_void_p(p)
+    L = M.layer_desc(2048, 8, 1, 64, dtype)
+    return M.lib().moe_block_norm(C.byref(L), at(x), at(branch), at(post), at(gate), rows, 1.0,
+                                  at(pre), 1e-6, R, at(h), at(hn), None)
+
+
+X, BR, HH, HN, D = BASE, BASE + (1 << 20), BASE + (2 << 20), BASE + (3 << 20), 4096  # D: a bf16 row
+
+
+@pytest.mark.parametrize("kw", [
+    dict(h=X + D), dict(h=X - D), dict(h=BR + 3 * D), dict(hn=X + D), dict(hn=BR - 3 * D),
+    dict(h=None, branch=None, hn=X + D), dict(hn=HH + D), dict(hn=HH - 3 * D), dict(h=X, hn=X),
+    dict(gate=HH, rows=4), dict(gate=HH + D, rows=1), dict(gate=HN + 3 * D, rows=4),
+    dict(gate=HH - D, rows=2), dict(post=HH), dict(pre=HN + 2 * D), dict(pre=HH + 3 * D),
+    dict(dtype="fp32", h=X + 7 * D),
+], ids=range(17))
+def test_block_norm_refuses_outputs_over_other_rows(kw):
+    assert _norm(**kw) == M.MOE_ERR_ARG
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the pointers are not a device's")
+@pytest.mark.parametrize("kw", [
+    dict(), dict(h=X), dict(h=BR), dict(h=X, hn=BR), dict(h=BR, hn=X), dict(hn=X), dict(hn=BR),
+    dict(hn=None), dict(branch=None, h=None, hn=X), dict(branch=None, h=X), dict(x=BR),
+    dict(h=X + 4 * D), dict(h=X - 4 * D), dict(hn=HH + 4 * D), dict(hn=HH - 4 * D),
+    dict(gate=HH, rows=1), dict(gate=HH - D, rows=4), dict(gate=HH - 2 * D, rows=3),
+    dict(post=HH - D, pre=HN + 4 * D), dict(post=X, pre=X),
+], ids=range(20))
+def test_block_norm_takes_outputs_beside_or_row_for_row(kw):
+    assert _norm(**kw) in OK_UNTIL_CUDA
