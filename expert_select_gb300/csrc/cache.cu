@@ -80,6 +80,43 @@ __device__ __forceinline__ float turns(int pos, float freq) {
     return t - rintf(t);
 }
 
+// A head's elements of one lane become x / sqrt(mean x^2 + eps), ss being the head's fp32 sum of
+// squares. It serves unless it overflows, or is so small that squares lost below fp32's range
+// count; then the head is scaled by a power of two first. group: the lanes of the head.
+template <int W, int LPH>
+__device__ __forceinline__ float head_scale(float (&vx)[W], float (&vy)[W], bool on, float ss, int dh,
+                                            float eps, uint32_t group) {
+    if ((ss < INFINITY && (ss > 1e-25f * (float)dh || eps > 1e-30f)) || ss != ss)
+        return 1.f / sqrtf(ss / (float)dh + eps);
+    float mx = 0.f;
+    if (on) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) mx = fmaxf(mx, fmaxf(fabsf(vx[j]), fabsf(vy[j])));
+    }
+#pragma unroll
+    for (int o = LPH / 2; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(group, mx, o, LPH));
+    if (mx == 0.f || mx == INFINITY) return mx == 0.f ? 1.f / sqrtf(eps) : 0.f;
+    int ex;
+    frexpf(mx, &ex);  // mx = f 2^ex, f in [0.5, 1)
+    ex = max(ex, -126);
+    // mean + eps = 2^(2 ex) (t / dh + eps 2^(-2 ex)), t of the head scaled by 2^-ex
+    const double e2 = ldexp((double)eps, -2 * ex);
+    if (e2 > 1e30) return 1.f / sqrtf(eps);  // the mean is far below eps
+    const float down = ldexpf(1.f, -ex);
+    float t = 0.f;
+    if (on) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+            vx[j] *= down;
+            vy[j] *= down;
+            t = fmaf(vx[j], vx[j], fmaf(vy[j], vy[j], t));
+        }
+    }
+#pragma unroll
+    for (int o = LPH / 2; o >= 1; o >>= 1) t += __shfl_xor_sync(group, t, o, LPH);
+    return 1.f / sqrtf(t / (float)dh + (float)e2);
+}
+
 // A CTA per row. The row's angles are formed once; LPH lanes take a head at a time, a lane
 // W elements and their rotary partners rot / 2 further on (behind rot: two runs that only pass
 // through). The next heads' elements are on their way while a pass is computed.
@@ -173,7 +210,7 @@ __global__ void __launch_bounds__(kThr) append_kernel(const AppendArgs a) {
                 LPH == 32 ? 0xffffffffu : ((1u << LPH) - 1u) << (tid & 31 & ~(LPH - 1));
 #pragma unroll
             for (int o = LPH / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(group, ss, o, LPH);
-            const float f = 1.f / sqrtf(ss / (float)a.dh + a.eps);
+            const float f = head_scale<W, LPH>(vx, vy, on, ss, a.dh, a.eps, group);
             if (on) {
                 Run<T, W> wx, wy;
                 float fx[W], fy[W];

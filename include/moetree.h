@@ -497,6 +497,7 @@ moe_status moe_tree_attention(const moe_cache_desc *C, const void *q, long long 
 
 /* What moe_kv_append does to the projected rows before it writes them. q_weight, k_weight [dh]
  * (layer dtype, device, or NULL): RMS norm of each head's q and k, x / sqrt(mean x^2 + eps) w.
+ * Heads whose squares leave fp32's range are scaled first.
  * inv_freq [rot_dim / 2] (device fp32, or NULL: no rotation): elements i and i + rot_dim / 2 of
  * a head, i < rot_dim / 2, turn by the angle position * inv_freq[i] (reduced to a
  * fraction of a turn in two fp32 parts, so far positions keep their angle), and are multiplied by

@@ -159,3 +159,36 @@ def test_a_single_row_of_a_projection_is_rotated_in_place():
                         blk.lend, 1, 1, q_out, blk.ws, inv_freq=freq)
     assert torch.equal(qkv[:, :8], want) and not torch.equal(want, kept[:, :8])
     assert torch.equal(qkv[:, 8:], kept[:, 8:])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("eps", [1e-6, 0.0])
+@pytest.mark.parametrize("dh,rot", [(64, 64), (40, 24), (256, 0)])
+def test_append_norms_at_the_ends_of_the_range(dtype, eps, dh, rot):
+    """Heads whose squares overflow or vanish in fp32, and a single large element: x / rms(x) as the
+    64-bit value within the roundings of a norm ((dh / 2 + 12) 2^-24) and of a turn by angle 0 (none:
+    cos 0 = 1, sin 0 = 0), then one to the type. Zero heads stay zero where eps is not."""
+    g = torch.Generator().manual_seed(dh)
+    scales = [1.0, 1e30, 1e-30, 1e-18, 3e37, 1e19]
+    x = torch.randn(1, 8, dh, generator=g)
+    for i, s in enumerate(scales):
+        x[0, i] *= s / x[0, i].abs().max()
+    x[0, 6] = 1e-20
+    x[0, 6, 3] = 1e25
+    x[0, 7] = 0 if eps else 1
+    x = x.to(dtype)
+    blk = Block(56, dtype, lens=(0,), ns=(1,), H=8, Hkv=8, dh=dh).upload()
+    w = torch.ones(dh, dtype=dtype, device=DEV)
+    q_out = torch.empty(1, 8, dh, dtype=dtype, device=DEV)
+    freq = torch.ones(rot // 2, device=DEV) if rot else None
+    M.moe_kv_append(blk.C, x.to(DEV), x.to(DEV), x.to(DEV), blk.kd, blk.vd, blk.tabled, blk.lend, 1,
+                    1, q_out, blk.ws, inv_freq=freq, q_weight=w, k_weight=w, eps=eps)
+    assert M.moe_workspace_check(blk.ws) == 0
+    d = x.double()
+    want = d / torch.sqrt((d * d).mean(2, keepdim=True) + eps)
+    u = 2.0 ** -8 if dtype == BF else 2.0 ** -24
+    tol = (u + (dh / 2 + 12) * 2.0 ** -24) * want.abs() + 1e-37
+    page = int(blk.table[0, 0])
+    for got in (q_out[0], blk.kd[page, 0]):
+        assert ((got.double().cpu() - want[0]).abs() <= tol[0]).all()
+    assert torch.equal(blk.vd[page, 0].cpu(), x[0])
