@@ -64,20 +64,30 @@ template <int W> struct Run<float, W> {
     }
 };
 
-// Fraction of a turn (within half a turn of 0) that pos * freq radians leave. 1 / (2 pi) is taken
-// as the sum of two fp32 values and the product with pos, cut into parts below 2^15 and 2^16 that
-// are exact in fp32, with its rounding error: at position 10^6 a plain fp32 product would be off
-// by up to 0.06 rad, this is within 10^-9 turns.
-__device__ __forceinline__ float turns(int pos, float freq) {
+// a + b (a in .x) with what the sum loses added to .y (two-sum: exact).
+__device__ __forceinline__ float2 add_kept(float2 a, float b) {
+    const float s = a.x + b, t = s - a.x;
+    return make_float2(s, a.y + ((a.x - (s - t)) + (b - t)));
+}
+
+// Fraction of a turn (.x, within half a turn of 0, and .y, some 2^-24 of one) that pos * freq
+// radians leave. 1 / (2 pi) is taken as the sum of two fp32 values and the product with pos, cut into
+// parts below 2^15 and 2^16 that are exact in fp32, with its rounding error; what the sum of the
+// parts' fractions loses is kept in .y. Of the turns pos freq / (2 pi) at most 2^-45 are lost in all
+// (emulated on the CPU: 1.5e-9 turns at positions up to 10^6, 3e-8 up to 2^24), where
+// a plain fp32 product is off by up to 0.06 rad at 10^6 and the fraction as one fp32 value by
+// 6e-8 turns.
+__device__ __forceinline__ float2 turns(int pos, float freq) {
     constexpr double kInv = 0.15915494309189533577;  // 1 / (2 pi)
     constexpr float hi = (float)kInv, lo = (float)(kInv - (double)hi);
     const float c = freq * hi, ce = fmaf(freq, hi, -c) + freq * lo;
     const float big = (float)(pos & ~0xffff), small = (float)(pos & 0xffff);
     const float b = big * c, s = small * c;
     const float be = fmaf(big, c, -b) + big * ce, se = fmaf(small, c, -s) + small * ce;
-    float t = (b - rintf(b)) + be;
-    t += (s - rintf(s)) + se;
-    return t - rintf(t);
+    float2 t = add_kept(make_float2(b - rintf(b), 0.f), s - rintf(s));
+    t = add_kept(add_kept(t, be), se);
+    t.x -= rintf(t.x);
+    return t;
 }
 
 // A head's elements of one lane become x / sqrt(mean x^2 + eps), ss being the head's fp32 sum of
@@ -184,10 +194,12 @@ __global__ void __launch_bounds__(kThr) append_kernel(const AppendArgs a) {
         }
     }
     for (int i = tid; i < half; i += kThr) {
+        const float2 t = turns(pos, a.inv_freq[i]);
         float s, c;
-        sincospif(2.f * turns(pos, a.inv_freq[i]), &s, &c);
-        s_cos[i] = c * a.rope_scale;
-        s_sin[i] = s * a.rope_scale;
+        sincospif(2.f * t.x, &s, &c);
+        const float d = 6.2831853071795865f * t.y;  // (its square is below 2^-40)
+        s_cos[i] = fmaf(-s, d, c) * a.rope_scale;
+        s_sin[i] = fmaf(c, d, s) * a.rope_scale;
     }
     __syncthreads();
 

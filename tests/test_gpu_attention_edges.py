@@ -192,3 +192,31 @@ def test_append_norms_at_the_ends_of_the_range(dtype, eps, dh, rot):
     for got in (q_out[0], blk.kd[page, 0]):
         assert ((got.double().cpu() - want[0]).abs() <= tol[0]).all()
     assert torch.equal(blk.vd[page, 0].cpu(), x[0])
+
+
+@pytest.mark.parametrize("top", [10 ** 6, 1 << 24])
+def test_angles_of_far_positions(top):
+    """Heads of ones and zeros, so that the written key is the angle's cosine and sine in fp32. They
+    are off by 2^-24 (a sine or cosine right to a unit in the last place), 2^-25 (one more rounding)
+    and by the angle's own error, 2^-45 of pos freq: 1 / (2 pi) as two fp32 values (2^-48) and its
+    product with freq as two more (2^-47 and 2^-48), the same of the product with pos (2^-46), all
+    of them at their worst."""
+    dh, n = 256, 512
+    r = np.random.default_rng(7)
+    blk = Block(57, F32, lens=(0,), ns=(n,), H=1, Hkv=1, dh=dh, page=64).upload()
+    pos = r.integers(0, top, n).astype(np.int32)
+    pos[:3] = (0, 1, top - 1)
+    freq = np.exp(-r.random(dh // 2) * np.log(1e6)).astype(np.float32)
+    freq[:2] = (1.0, 0.7)
+    k = torch.zeros(n, 1, dh, device=DEV)
+    k[..., :dh // 2] = 1
+    q = torch.empty(n, 1, dh, device=DEV)
+    M.moe_kv_append(blk.C, k, k, k, blk.kd, blk.vd, blk.tabled, blk.lend, 1, n, q, blk.ws,
+                    depth=torch.from_numpy(pos).to(DEV), inv_freq=torch.from_numpy(freq).to(DEV))
+    assert M.moe_workspace_check(blk.ws) == 0
+    # (pos has 24 bits and freq 24: their product is exact in 64 bits)
+    a = pos.astype(np.float64)[:, None] * freq.astype(np.float64)[None]
+    got = q[:, 0].double().cpu().numpy()
+    tol = 2.0 ** -24 + 2.0 ** -25 + 2.0 ** -45 * np.abs(a)
+    assert (np.abs(got[:, :dh // 2] - np.cos(a)) <= tol).all()
+    assert (np.abs(got[:, dh // 2:] - np.sin(a)) <= tol).all()
