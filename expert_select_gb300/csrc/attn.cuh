@@ -100,11 +100,11 @@ __device__ __forceinline__ Tiles tiles_of(const Args &a, const Seq &s, int q0, i
     t.ns = t.w0 = 0;
     const int all = (kend + BN - 1) / BN;
     if (a.window > 0) {
-        // the oldest slot a window can reach (tree nodes may all be at the root's depth)
-        const int lo = max(0, s.len + (a.parent ? 0 : i0) - a.window + 1);
-        // (one tile at least: where lengths are cut to the table, rows past its end may see nothing,
-        // and an item without tiles would not write their zeros)
-        t.w0 = min(lo / BN, all - 1);
+        // the oldest slot a window can reach (tree nodes may all be at the root's depth); at most the
+        // last one: where lengths are cut to the table, rows past its end may see nothing, and an
+        // item without tiles would not write their zeros
+        const int lo = min(max(0, s.len + (a.parent ? 0 : i0) - a.window + 1), kend - 1);
+        t.w0 = lo / BN;
         t.ns = min((int)(((long long)a.sinks + BN - 1) / BN), t.w0);
     }
     t.nt = t.ns + all - t.w0;

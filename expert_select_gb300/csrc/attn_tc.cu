@@ -209,16 +209,18 @@ attn_tc_kernel(const __grid_constant__ Params p) {
             // the keeper clears those rows of V).
             const int per_tile = kBN / p.box, in_use = (g.s.L + p.box - 1) / p.box;  // boxes
             int first = -1, in_page = 0;  // box of pg[0] of lane 0; slot in its page of the next box
-            constexpr int kNone = INT_MIN;  // no box, or one that is not needed
+            // boxes gone0 .. gone0 + gone - 1 are wholly out of reach (see out_of_reach)
+            const int shift = __ffs(p.box) - 1;
+            const int gone0 = (int)(((long long)a.sinks + p.box - 1) >> shift);
+            const unsigned gone = a.window > 0 ? max(0, ((g.s.len - a.window + 1) >> shift) - gone0) : 0;
+            auto needed = [&](int bx) { return bx < in_use && (unsigned)(bx - gone0) >= gone; };
             int pg[2], next[2];
             uint32_t good[2], there[2];
             auto look_up = [&](int from, int (&out)[2]) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int bx = from + lane + 32 * i;
-                    out[i] = bx < in_use && !out_of_reach(a, g.s, bx * p.box, (bx + 1) * p.box - 1)
-                                 ? max(a.table[(size_t)g.b * a.max_pages + bx * p.box / a.page], -1)
-                                 : kNone;
+                    out[i] = needed(bx) ? a.table[(size_t)g.b * a.max_pages + bx * p.box / a.page] : -1;
                 }
             };
             auto take = [&](int from) {  // makes `next` current and looks further ahead
@@ -227,7 +229,7 @@ attn_tc_kernel(const __grid_constant__ Params p) {
                 for (int i = 0; i < 2; ++i) {
                     pg[i] = next[i];
                     good[i] = __ballot_sync(0xffffffffu, pg[i] >= 0 && pg[i] < a.n_pages);
-                    there[i] = __ballot_sync(0xffffffffu, pg[i] != kNone);
+                    there[i] = __ballot_sync(0xffffffffu, needed(from + lane + 32 * i));
                 }
                 look_up(from + 64, next);
                 if (good[0] != there[0] || good[1] != there[1]) {
