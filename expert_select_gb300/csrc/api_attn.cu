@@ -52,9 +52,16 @@ bool block_ok(const moe_cache_desc *C, int B, int N, int R, const int *row_start
 // tcgen05 kernel takes 18-167 (1.0 to 1.7 times as long; 24 rows of 64 sequences: 108 against 72).
 // With more rows it reads the cache once for every 16, but starts and ends sooner: up to 32 such
 // blocks in all and 2^17 slots between them it is 1.03 to 1.6 times as fast (8 nodes of 8 heads,
-// 4 key/value heads of 128: 2003 slots 14.5 against 20.7 us, 8003 slots 20.2 against 23.1, 16003
-// slots 28.5 against 27.0; 4 sequences of 1003 slots, 64 blocks, 21.7 against 20.7). The lengths
-// are not known here: the page table's capacity stands for them.
+// 4 key/value heads of 128: 2003 slots 14.5 against 21.0 us, 8003 slots 21.0 against 23.9, 16003
+// slots 30.6 against 27.8; 4 sequences of 1003 slots, 64 blocks, 21.9 against 21.0). The lengths
+// are not known here: the page table's capacity stands for them, so 8 nodes over 2003 slots
+// with a table for 131072 take 20.7 us, not 14.4.
+// With either kernel forced on 226 shapes of 24 to 264 rows, this one is never slower where the rule
+// takes it, and the other is at least 5 % slower on 26 where the rule takes that: twelve without a
+// window (up to 1.25 times: one sequence of 16-30k slots, some short ones of 500-1000), fourteen
+// with a window of 128, where a limit of 32 blocks is too low (groups of 8 heads, 4 key/value
+// heads of 128: 128 trees of 3 nodes 88.8 us against 45.9, of 5 nodes 90.5 against 66.4, of 8 92.8
+// against 80.1; but of 16 nodes 97.9 against 155.8).
 bool few_rows(const attn::Args &a) {
     const long long rows = (long long)a.N * a.G;
     if (rows <= attn::kFewRows) return true;

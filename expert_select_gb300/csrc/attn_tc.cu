@@ -5,9 +5,9 @@
 // in one pass over the keys with a running maximum m and sum l per row (c = scale log2 e). An
 // item is 256 rows (node, head in group) of one key/value head: a prompt chunk or a large tree
 // fills both 128-row tiles, which then share every K and V tile ("two tiles"); where an item has
-// at most 128 rows (single tokens: 8 rows of a group of 8 heads) its one tile is computed over
-// even key tiles by one half of the CTA and over odd ones by the other, and the halves are
-// merged at the end ("one tile"). Either way two independent score tiles are in flight: while
+// at most 128 rows (16 nodes of a group of 8 heads; the last 8 rows of 65 such nodes) its one tile
+// is computed over even key tiles by one half of the CTA and over odd ones by the other, and the
+// halves are merged at the end ("one tile"). Either way two independent score tiles are in flight: while
 // the tensor cores work for one, the CUDA cores exponentiate the other.
 //
 // One CTA per SM, 416 threads:
@@ -17,6 +17,9 @@
 //   warps 1, 12  MMA issuers of slots 0 and 1 (warp 1 also allocates TMEM)
 //   warp 2       looks after V: clears what no row may see (see below)
 //   warps 4-7, 8-11  softmax of slot 0 and slot 1: a thread per row, its 64 scores in registers
+// (With 13 warps a thread has at most 128 registers; all are used, and 44-56 bytes spilled. Twelve
+// warps would allow 168. The 13th, an issuing warp for each slot, took the 64 trees below from 523 to
+// 502 us when it came and left the chunks as they were.)
 //
 // TMEM (512 columns): two buffers of S for each of slots 0 and 1 (64 columns each; P overwrites the
 // first 32 of its S), O of slots 0 and 1 (128 each). With two buffers S of the next tile is there
@@ -30,7 +33,9 @@
 // the nominal rate, and the SM clock falls from 2.0 to 1.66 GHz under the load (power). 64 trees of
 // 65 nodes over 0.2-8k tokens 0.42 ms: 65 nodes of 8 heads are 520 rows, three items that each read
 // the sequence's K and V (1.6 GB from HBM for 0.55 GB of cache), and a piece of an item costs
-// about 10 us beside its tiles (query rows, the pipeline's start and end, the output).
+// about 10 us beside its tiles (query rows, the pipeline's start and end, the output). That fixed
+// cost is most of what a window leaves: 4096 tokens over 4003 with a window of 128 (64/8 heads of
+// 64) 140 us for 11 us of bytes, 64 trees of 65 nodes so 223 us for 14.
 //
 // A masked score is -inf, so its P is 0; but 0 x V is NaN where V is infinite or NaN. In tiles
 // that hold masked slots (the last ones, and a window's first) warp 2 therefore clears the rows of

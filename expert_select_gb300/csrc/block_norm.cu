@@ -463,7 +463,10 @@ cudaError_t launch_t(int d, const void *x, const void *branch, const void *w_pos
     // A warp per row where there are several rows for each of the SM's warps, room for their rings,
     // and gate rows that many rows share: 8192 x 2880 bf16 takes 42 us so (4.5 TB/s) and 57 us with
     // 384 threads a row, whose two block reductions are a chain of 2000 cycles; a few rows are done
-    // sooner with up to 512 threads each (65 x 2048: 2.5 us).
+    // sooner with up to 512 threads each (65 x 2048: 2.5 us). The rings and weights bound the width:
+    // bf16 up to 3208 columns, fp32 up to 1696. 8192 rows with both norms and a gate, here: bf16 3200
+    // 44.5 us, fp32 1600 37.5; in the other kernel bf16 4096 86 us (3.1 TB/s), 5120 82 (4.1), 6144 145
+    // (2.8), fp32 2048 59 (4.6), 4096 128 (4.2).
     const size_t row_smem = (size_t)d * (8 + 4 * kRowWarps * sizeof(T));
     if (R >= 2 * kRowWarps * nsm && row_smem <= 226 * 1024 && (!gate || gate_rows >= 4 * kRowWarps)) {
         const int nv = (vecs + 31) / 32, thr = 32 * kRowWarps;

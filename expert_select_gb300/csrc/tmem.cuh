@@ -108,7 +108,7 @@ __device__ __forceinline__ void commit_elect(uint32_t bar) {
 }
 
 // The operand of a P V product is MN-major in V: rows of 64 elements of the head (128 B), one row
-// per key, 8-row groups 1024 B apart, blocks of 64 elements 16 KB apart (the leading offset).
+// per key, 8-row groups 1024 B apart, blocks of 64 elements 8 KB apart (64 keys; the leading offset).
 constexpr uint32_t kIdescBMn = 1u << 16;  // instruction descriptor: B is MN-major
 
 // A copy issued by one elected lane of a warp whose lanes hold the same operands.

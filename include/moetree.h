@@ -532,7 +532,9 @@ moe_status moe_kv_append(const moe_cache_desc *C, const moe_rope_params *P, cons
  *   path [B, P] device int32: ascending node indexes from the root down (rows of moe_draft_select's
  *   order, parents first); n_accept [B] device int32, 0 .. P; new_len [B] device int32, may be
  *   cache_len itself. A path that is not ascending, or leaves the page table or the pool, ends
- *   before its first bad node (bit 2 or 3 of the check word; workspace may be NULL). */
+ *   before its first bad node (bit 2 or 3 of the check word; workspace may be NULL). How many nodes
+ *   the block has is not known here: a path that ascends past the last of them, inside the table,
+ *   takes what those slots hold. */
 moe_status moe_kv_commit(const moe_cache_desc *C, void *k_pages, void *v_pages,
                          const int *page_table, const int *cache_len, const int *path,
                          const int *n_accept, int B, int P, int *new_len, void *workspace,
