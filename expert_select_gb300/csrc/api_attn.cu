@@ -26,8 +26,6 @@ WsLayout ws_layout(int dh, long long rows_per_seq) {
 
 }  // namespace attn
 
-namespace {
-
 bool cache_ok(const moe_cache_desc *C) {
     if (!C || C->H_kv < 1 || C->H < C->H_kv || C->H % C->H_kv || C->H > 65536) return false;
     if (C->dh < 8 || C->dh % 8 || C->dh > 256) return false;
@@ -39,6 +37,8 @@ bool cache_ok(const moe_cache_desc *C) {
     if (C->window < 0 || C->sink_tokens < 0) return false;
     return C->scale > 0.f && std::isfinite(C->scale);
 }
+
+namespace {
 
 // Rows of a ragged or uniform block. N nodes of G heads each must fit an int.
 bool block_ok(const moe_cache_desc *C, int B, int N, int R, const int *row_start) {

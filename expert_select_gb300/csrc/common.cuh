@@ -171,6 +171,7 @@ inline T *at(void *ws, size_t off) {
 }
 
 bool desc_ok(const moe_layer_desc *L);
+bool cache_ok(const moe_cache_desc *C);
 bool select_args(const moe_select_params *P, int k, SelectArgs *a);
 bool aligned16(const void *p);
 // The argument checks of moe_tree_forward other than those of the workspace.

@@ -1,0 +1,507 @@
+// Upkeep of a cache's pages: sequences that end, grow and fork, and a pool that is compacted. The
+// bookkeeping (which page belongs to whom) is apart from the copies of keys and values, as one table
+// serves all layers and each layer has pools of its own.
+//
+// A page is free where its count of holders is 0; new pages are the free ones of the lowest numbers,
+// in the order of the sequences, so results do not depend on the order of threads. Finding them is a
+// scan over the counts (4 bytes a page), and the bookkeeping of a call waits for it, so a call is
+// one cluster of CTAs: each scans its slice, the slices' sums meet in distributed shared memory, and
+// the call's phases are cluster barriers instead of launches.
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
+#include "pages.cuh"
+
+namespace moe {
+namespace pages {
+
+static size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+WsLayout ws_layout(const moe_page_book &K) {
+    WsLayout w{};
+    w.list = 4096;
+    w.map = align256(w.list + (size_t)K.n_pages * 4);
+    w.claim = align256(w.map + (size_t)K.n_pages * 4);
+    w.off = align256(w.claim + (size_t)K.B * 4);
+    w.total = align256(w.off + (size_t)K.B * 4);
+    return w;
+}
+
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kThr = 1024, kWarps = kThr / 32;
+constexpr int kCluster = 8;
+
+struct Book {
+    int *table, *held, *len, *ref;
+    int B, max_pages, n_pages, page;
+    int *flags, *list, *map, *claim, *off;
+};
+
+__device__ __forceinline__ void flag(const Book &k, int bit) {
+    if (k.flags) atomicOr(k.flags, bit);
+}
+
+// A sequence whose numbers fit the table: 0 <= held <= max_pages, 0 <= len <= held pages.
+__device__ __forceinline__ bool sane(const Book &k, int held, int len) {
+    return held >= 0 && held <= k.max_pages && len >= 0 && (long long)len <= (long long)held * k.page;
+}
+
+// Sums of the block's threads before this one (exclusive, in thread order) and of all.
+template <typename T> __device__ __forceinline__ T block_scan(T v, T *part, T *total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    T s = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const T t = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += t;
+    }
+    __syncthreads();  // (part may still be read from the scan before)
+    if (lane == 31) part[warp] = s;
+    __syncthreads();
+    if (warp == 0) {
+        T p = part[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const T t = __shfl_up_sync(0xffffffffu, p, o);
+            if (lane >= o) p += t;
+        }
+        part[lane] = p;
+    }
+    __syncthreads();
+    *total = part[kWarps - 1];
+    return s - v + (warp ? part[warp - 1] : 0);
+}
+
+// The cluster's warps share the pages [lo, hi) in contiguous runs, in order. Every warp gets the
+// number of pages before its run for which `pick` holds; total: of all. Called by all threads.
+struct Run {
+    int lo, hi, before, total;
+};
+template <class Pick>
+__device__ __forceinline__ Run cluster_count(const int *ref, int lo, int hi, int *part, int *mine,
+                                             Pick pick) {
+    cg::cluster_group cl = cg::this_cluster();
+    const int ctas = cl.num_blocks(), rank = cl.block_rank();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int n = max(0, hi - lo), warps = ctas * kWarps;
+    // runs of whole 128-byte lines
+    const int per = ((n + warps - 1) / warps + 31) / 32 * 32;
+    const long long first = lo + (long long)(rank * kWarps + warp) * per;
+    Run r;
+    r.lo = (int)min((long long)max(lo, hi), first);
+    r.hi = (int)min((long long)max(lo, hi), first + per);
+    int c = 0;
+#pragma unroll 8
+    for (int p = r.lo + lane; p < r.hi; p += 32) c += pick(p, ref[p]);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+    int sum;
+    const int at = block_scan(lane == 0 ? c : 0, part, &sum);  // warps in order
+    if (threadIdx.x == 0) *mine = sum;
+    cl.sync();
+    int base = 0, total = 0;
+    for (int i = 0; i < ctas; ++i) {
+        const int v = *cl.map_shared_rank(mine, i);
+        if (i < rank) base += v;
+        total += v;
+    }
+    cl.sync();  // (`mine` may be written again)
+    r.before = base + __shfl_sync(0xffffffffu, at, 0);
+    r.total = total;
+    return r;
+}
+
+// Calls put(page, how many picked ones are before it) for each picked page of the warp's run.
+template <class Pick, class Put>
+__device__ __forceinline__ void cluster_emit(const int *ref, const Run &r, Pick pick, Put put) {
+    const int lane = threadIdx.x & 31;
+    int at = r.before;
+    for (int p0 = r.lo; p0 < r.hi; p0 += 32) {
+        const int p = p0 + lane;
+        const bool on = p < r.hi && pick(p, ref[p]);
+        const uint32_t m = __ballot_sync(0xffffffffu, on);
+        if (on) put(p, at + __popc(m & ((1u << lane) - 1)));
+        at += __popc(m);
+    }
+}
+
+__device__ __forceinline__ bool is_free(int, int ref) { return ref <= 0; }
+
+// The first `want` free pages go to k.list, ascending. Returns how many free pages there are.
+__device__ __forceinline__ int list_free(const Book &k, int want, int *part, int *mine) {
+    const Run r = cluster_count(k.ref, 0, k.n_pages, part, mine, is_free);
+    if (r.before < want)
+        cluster_emit(k.ref, r, is_free, [&](int p, int i) {
+            if (i < want) k.list[i] = p;
+        });
+    return r.total;
+}
+
+// ------------------------------------------------------------------ free
+
+// A CTA for each entry of the list. Lowering `held` is what takes the pages: of two entries that
+// name one sequence each releases the pages between its own mark and the one it found.
+__global__ void __launch_bounds__(128) free_kernel(Book k, const int *seqs, const int *keep) {
+    __shared__ int s_old;
+    pdl_wait();
+    const int b = seqs[blockIdx.x], left = keep ? keep[blockIdx.x] : 0;
+    if (b < 0 || b >= k.B || left < 0) {
+        if (threadIdx.x == 0) flag(k, attn::FLAG_BAD_SEQUENCE);
+        return;
+    }
+    const long long want_ll = ((long long)left + k.page - 1) / k.page;
+    const int want = (int)min(want_ll, (long long)k.max_pages);
+    if (threadIdx.x == 0) {
+        s_old = atomicMin(&k.held[b], want);
+        atomicMin(&k.len[b], left);
+        if (s_old > k.max_pages) flag(k, attn::FLAG_BAD_SEQUENCE);
+    }
+    __syncthreads();
+    const int old = min(s_old, k.max_pages);
+    for (int j = want + threadIdx.x; j < old; j += blockDim.x) {
+        const int p = k.table[(size_t)b * k.max_pages + j];
+        if (p < 0 || p >= k.n_pages || atomicSub(&k.ref[p], 1) <= 0) {
+            if (p >= 0 && p < k.n_pages) atomicAdd(&k.ref[p], 1);  // nobody held it: stays free
+            flag(k, attn::FLAG_BAD_PAGE);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ reserve
+
+__global__ void __launch_bounds__(kThr) reserve_kernel(Book k, int N, const int *n_new) {
+    __shared__ int part[kWarps], mine;
+    __shared__ long long part2[kWarps];
+    pdl_wait();
+    const int rank = cg::this_cluster().block_rank(), ctas = cg::this_cluster().num_blocks();
+    // pages that each sequence lacks, and those that the sequences before it lack: every CTA counts
+    // for itself, the first one writes them down
+    auto lacks = [&](int b, bool tell) {
+        const int held = k.held[b], len = k.len[b], more = n_new ? n_new[b] : N;
+        if (!sane(k, held, len) || more < 0) {
+            if (tell) flag(k, attn::FLAG_BAD_SEQUENCE);
+            return 0;
+        }
+        const long long want = ((long long)len + more + k.page - 1) / k.page;
+        if (want > k.max_pages) {
+            if (tell) flag(k, attn::FLAG_BAD_SEQUENCE);
+            return 0;
+        }
+        return min(max(0, (int)want - held), k.n_pages + 1);
+    };
+    long long total = 0;
+    for (int b0 = 0; b0 < k.B; b0 += kThr) {
+        const int b = b0 + threadIdx.x;
+        const long long need = b < k.B ? lacks(b, rank == 0) : 0;
+        long long sum;
+        const long long at = block_scan(need, part2, &sum);
+        // (sums are cut at n_pages + 1: what lies behind is not served anyway)
+        if (rank == 0 && b < k.B) k.off[b] = (int)min(total + at, (long long)k.n_pages + 1);
+        total = min(total + sum, (long long)k.n_pages + 1);
+    }
+    const int want = (int)min(total, (long long)k.n_pages);
+    if (want == 0) return;
+    const int have = list_free(k, want, part, &mine);
+    cg::this_cluster().sync();
+    const int lane = threadIdx.x & 31;
+    for (int b = rank * kWarps + (threadIdx.x >> 5); b < k.B; b += ctas * kWarps) {
+        const int need = lacks(b, false), at = k.off[b], held = k.held[b];
+        __syncwarp();  // (held is written below)
+        if (need == 0) continue;
+        if (at + need > have) {
+            if (lane == 0) flag(k, FLAG_NO_PAGES);
+            continue;
+        }
+        for (int j = lane; j < need; j += 32) {
+            const int p = k.list[at + j];
+            k.table[(size_t)b * k.max_pages + held + j] = p;
+            k.ref[p] = 1;
+        }
+        if (lane == 0) k.held[b] = held + need;
+    }
+}
+
+// ------------------------------------------------------------------ fork
+
+constexpr int kForkCols = 256;  // table entries of a warp's piece
+
+__global__ void __launch_bounds__(kThr)
+fork_kernel(Book k, const int *src, const int *dst, int n, int *moves) {
+    __shared__ int part[kWarps], mine;
+    pdl_wait();
+    cg::cluster_group cl = cg::this_cluster();
+    const int rank = cl.block_rank(), ctas = cl.num_blocks();
+    const int lane = threadIdx.x & 31, gt = rank * kThr + threadIdx.x;
+    auto in = [&](int b) { return b >= 0 && b < k.B; };
+    // the first entry that names a sequence as its target has it
+    for (int i = gt; i < n; i += ctas * kThr) {
+        if (in(src[i])) k.claim[src[i]] = n;
+        if (in(dst[i])) k.claim[dst[i]] = n;
+    }
+    cl.sync();
+    for (int i = gt; i < n; i += ctas * kThr)
+        if (in(dst[i])) atomicMin(&k.claim[dst[i]], i);
+    cl.sync();
+    // Tokens behind the last full page, or -1: no fork. (A target is never a source, so what is read
+    // here of a source is not written by the call.)
+    auto tail_of = [&](int i) {
+        const int a = src[i], b = dst[i];
+        if (!in(a) || !in(b) || k.claim[b] != i || k.claim[a] != n) return -1;
+        if (!sane(k, k.held[a], k.len[a])) return -1;
+        return k.len[a] % k.page;
+    };
+    // entries that need a page, and how many do before each: every CTA counts for itself
+    int total = 0;
+    for (int i0 = 0; i0 < n; i0 += kThr) {
+        const int i = i0 + threadIdx.x;
+        int tail = -1;
+        if (i < n) {
+            tail = tail_of(i);
+            if (tail >= 0 && k.held[dst[i]] != 0) tail = -1;
+            if (tail < 0 && rank == 0) flag(k, attn::FLAG_BAD_SEQUENCE);
+        }
+        int sum;
+        const int at = block_scan((int)(tail > 0), part, &sum);
+        // (-1: no fork)
+        if (rank == 0 && i < n) k.off[i] = tail < 0 ? -1 : total + at;
+        total += sum;
+    }
+    const int have = list_free(k, min(total, k.n_pages), part, &mine);
+    cl.sync();
+    // pieces of table rows: full pages are shared, what is behind them gets a page of its own
+    const int pieces = (k.max_pages + kForkCols - 1) / kForkCols;
+    const long long items = (long long)n * pieces;
+    for (long long it = rank * kWarps + (threadIdx.x >> 5); it < items; it += ctas * kWarps) {
+        const int i = (int)(it / pieces), piece = (int)(it - (long long)i * pieces);
+        const int at = k.off[i];
+        int tail = at < 0 ? -1 : tail_of(i);
+        const bool short_of = tail > 0 && at >= have;
+        if (short_of) tail = -1;
+        if (tail < 0) {
+            if (piece == 0 && lane < 3) moves[3 * i + lane] = lane == 2 ? 0 : -1;
+            if (piece == 0 && lane == 0 && short_of) flag(k, FLAG_NO_PAGES);
+            continue;
+        }
+        const int a = src[i], b = dst[i], len = k.len[a], full = len / k.page;
+        const int *from = k.table + (size_t)a * k.max_pages;
+        int *to = k.table + (size_t)b * k.max_pages;
+        const int end = min(full, (piece + 1) * kForkCols);
+#pragma unroll 4
+        for (int j = piece * kForkCols + lane; j < end; j += 32) {
+            const int p = from[j];
+            to[j] = p;
+            if (p >= 0 && p < k.n_pages)
+                atomicAdd(&k.ref[p], 1);
+            else
+                flag(k, attn::FLAG_BAD_PAGE);
+        }
+        if (piece || lane) continue;
+        int old = -1, fresh = -1;
+        if (tail > 0) {
+            old = from[full];
+            fresh = k.list[at];
+            to[full] = fresh;
+            k.ref[fresh] = 1;
+        }
+        moves[3 * i] = old;
+        moves[3 * i + 1] = fresh;
+        moves[3 * i + 2] = tail;
+        k.held[b] = full + (tail > 0);
+        k.len[b] = len;
+    }
+}
+
+// ------------------------------------------------------------------ compact
+
+__global__ void __launch_bounds__(kThr)
+compact_kernel(Book k, int *ref_out, int *moves, int *counts) {
+    __shared__ int part[kWarps], mine;
+    pdl_wait();
+    cg::cluster_group cl = cg::this_cluster();
+    auto is_used = [](int, int ref) { return ref > 0; };
+    const int n = k.n_pages;
+    const int n_used = cluster_count(k.ref, 0, n, part, &mine, is_used).total;
+    // holes below n_used, in ascending order
+    const Run holes = cluster_count(k.ref, 0, n_used, part, &mine, is_free);
+    cluster_emit(k.ref, holes, is_free, [&](int p, int i) { k.list[i] = p; });
+    // pages that stay. (ref_out may be ref: nothing that is read here changes before the barriers of
+    // the next count.)
+    for (int p = cl.block_rank() * kThr + threadIdx.x; p < n; p += cl.num_blocks() * kThr) {
+        const int ref = k.ref[p];
+        if (ref > 0 && p >= n_used) continue;
+        k.map[p] = ref > 0 ? p : -1;
+        if (ref > 0 || p >= n_used) ref_out[p] = max(ref, 0);
+    }
+    // pages at n_used and above go to the holes, in order
+    const Run high = cluster_count(k.ref, n_used, n, part, &mine, is_used);
+    cluster_emit(k.ref, high, is_used, [&](int p, int i) {
+        const int to = k.list[i], ref = k.ref[p];
+        k.map[p] = to;
+        ref_out[to] = ref;
+        ref_out[p] = 0;
+        moves[3 * (size_t)i] = p;
+        moves[3 * (size_t)i + 1] = to;
+        moves[3 * (size_t)i + 2] = k.page;
+    });
+    if (cl.block_rank() == 0 && threadIdx.x == 0) {
+        counts[0] = high.total;
+        counts[1] = n_used;
+    }
+}
+
+// Table entries follow the pages. A row's entries behind what it holds stay as they are.
+__global__ void __launch_bounds__(256) remap_kernel(Book k, int *table_out) {
+    pdl_wait();
+    const long long all = (long long)k.B * k.max_pages;
+    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < all; i += gridDim.x * 256ll) {
+        const int b = (int)(i / k.max_pages), j = (int)(i - (long long)b * k.max_pages);
+        int p = k.table[i];
+        const int held = k.held[b];
+        if (j == 0 && (held < 0 || held > k.max_pages)) flag(k, attn::FLAG_BAD_SEQUENCE);
+        if (j < held) {
+            const int to = p >= 0 && p < k.n_pages ? k.map[p] : -1;
+            if (to >= 0)
+                p = to;
+            else
+                flag(k, attn::FLAG_BAD_PAGE);
+        }
+        table_out[i] = p;
+    }
+}
+
+// ------------------------------------------------------------------ copy
+
+constexpr int kCopyThr = 256, kCopyVecs = 4;  // 16-byte vectors a thread holds
+constexpr int kCopyPart = kCopyThr * kCopyVecs;
+
+// A page is `rows` runs of consecutive bytes: one, where heads and tokens lie densely token by
+// token; one a head, where a head's tokens do; else one a token and head. Work is cut into parts of
+// kCopyPart vectors of one page and pool.
+__global__ void __launch_bounds__(kCopyThr) copy_kernel(const CopyArgs a) {
+    pdl_wait();
+    const int n = a.count ? min(max(*a.count, 0), a.n) : a.n;
+    const int vecs = a.row_bytes / 16, page_vecs = a.page * a.heads * vecs;
+    const int parts = (page_vecs + kCopyPart - 1) / kCopyPart;
+    const long long items = 2ll * n * parts;
+    const bool by_token = a.st_head == a.row_bytes && a.st_tok == (long long)a.heads * a.row_bytes;
+    const bool by_head = a.st_tok == a.row_bytes;
+    for (long long it = blockIdx.x; it < items; it += gridDim.x) {
+        const int part = (int)(it % parts), m = (int)(it / parts / 2);
+        char *pool = (it / parts) & 1 ? a.vp : a.kp;
+        const int src = a.moves[3 * (size_t)m], dst = a.moves[3 * (size_t)m + 1];
+        const int tokens = a.moves[3 * (size_t)m + 2];
+        if (tokens <= 0 || src == dst) continue;
+        if (src < 0 || src >= a.n_pages || dst < 0 || dst >= a.n_pages || tokens > a.page) {
+            if (a.flags && threadIdx.x == 0) atomicOr(a.flags, attn::FLAG_BAD_PAGE);
+            continue;
+        }
+        const char *from = pool + src * a.st_page;
+        char *to = pool + dst * a.st_page;
+        const int all = tokens * a.heads * vecs;
+        uint4 v[kCopyVecs];
+        long long at[kCopyVecs];
+#pragma unroll
+        for (int q = 0; q < kCopyVecs; ++q) {
+            const int i = part * kCopyPart + q * kCopyThr + threadIdx.x;
+            at[q] = -1;
+            if (i >= all) continue;
+            if (by_token) {
+                at[q] = 16ll * i;
+            } else if (by_head) {
+                const int run = tokens * vecs, h = i / run;
+                at[q] = h * a.st_head + 16ll * (i - h * run);
+            } else {
+                const int row = i / vecs, t = row / a.heads;
+                at[q] = t * a.st_tok + (row - t * a.heads) * a.st_head + 16ll * (i - row * vecs);
+            }
+            v[q] = *reinterpret_cast<const uint4 *>(from + at[q]);
+        }
+#pragma unroll
+        for (int q = 0; q < kCopyVecs; ++q)
+            if (at[q] >= 0) *reinterpret_cast<uint4 *>(to + at[q]) = v[q];
+    }
+}
+
+Book book(const moe_page_book &K, void *ws) {
+    const WsLayout w = ws_layout(K);
+    Book k{};
+    k.table = K.page_table;
+    k.held = K.held;
+    k.len = K.cache_len;
+    k.ref = K.ref;
+    k.B = K.B;
+    k.max_pages = K.max_pages;
+    k.n_pages = K.n_pages;
+    k.page = K.page_size;
+    k.flags = at<int>(ws, 0);
+    k.list = at<int>(ws, w.list);
+    k.map = at<int>(ws, w.map);
+    k.claim = at<int>(ws, w.claim);
+    k.off = at<int>(ws, w.off);
+    return k;
+}
+
+// One cluster: of one CTA where the scan is short (its barriers are the CTA's own then).
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cluster(void (*kernel)(KArgs...), bool wide, cudaStream_t s, Args &&...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(wide ? kCluster : 1);
+    cfg.blockDim = dim3(kThr);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = wide ? kCluster : 1;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+constexpr int kWidePages = 8192;
+
+}  // namespace
+
+cudaError_t launch_free(const moe_page_book &K, const int *seqs, const int *keep, int n, void *ws,
+                        cudaStream_t s) {
+    return launch_pdl(free_kernel, dim3(n), dim3(128), 0, s, book(K, ws), seqs, keep);
+}
+
+cudaError_t launch_reserve(const moe_page_book &K, int N, const int *n_new, void *ws,
+                           cudaStream_t s) {
+    return launch_cluster(reserve_kernel, K.n_pages > kWidePages, s, book(K, ws), N, n_new);
+}
+
+cudaError_t launch_fork(const moe_page_book &K, const int *src, const int *dst, int n, int *moves,
+                        void *ws, cudaStream_t s) {
+    const bool wide = K.n_pages > kWidePages || (long long)n * K.max_pages > 4 * kWidePages;
+    return launch_cluster(fork_kernel, wide, s, book(K, ws), src, dst, n, moves);
+}
+
+cudaError_t launch_compact(const moe_page_book &K, int *table_out, int *ref_out, int *moves,
+                           int *counts, void *ws, cudaStream_t s) {
+    const Book k = book(K, ws);
+    cudaError_t err = launch_cluster(compact_kernel, K.n_pages > kWidePages, s, k, ref_out, moves,
+                                     counts);
+    if (err != cudaSuccess) return err;
+    const long long all = (long long)K.B * K.max_pages;
+    const int ctas = (int)std::min<long long>((all + 255) / 256, 8ll * std::max(1, device_sms()));
+    return launch_pdl(remap_kernel, dim3(ctas), dim3(256), 0, s, k, table_out);
+}
+
+cudaError_t launch_copy(const CopyArgs &a, cudaStream_t s) {
+    const long long parts =
+        ((long long)a.page * a.heads * (a.row_bytes / 16) + kCopyPart - 1) / kCopyPart;
+    const int ctas =
+        (int)std::min<long long>(2 * parts * a.n, 8ll * std::max(1, device_sms()));
+    return launch_pdl(copy_kernel, dim3(ctas), dim3(kCopyThr), 0, s, a);
+}
+
+}  // namespace pages
+}  // namespace moe

@@ -35,7 +35,9 @@ EXPORTS = (
     "moe_event_wait", "moe_tree_forward_noalloc", "moe_offload_forward", "moe_draft_select",
     "moe_tree_route", "moe_tree_block_stats", "moe_noalloc_check", "moe_offload_upload_wait",
     "moe_rms_norm", "moe_attention_workspace_bytes", "moe_tree_attention", "moe_kv_append",
-    "moe_kv_commit", "moe_block_norm",
+    "moe_kv_commit", "moe_block_norm", "moe_few_workspace_bytes", "moe_few_forward", "moe_sample",
+    "moe_tree_accept", "moe_pages_workspace_bytes", "moe_kv_reserve", "moe_kv_free", "moe_kv_fork",
+    "moe_kv_compact", "moe_kv_copy_pages",
 )
 
 
@@ -95,6 +97,18 @@ class RopeParams(C.Structure):
                 ("inv_freq", C.c_void_p), ("rot_dim", C.c_int), ("rope_scale", C.c_float)]
 
 
+class SampleParams(C.Structure):
+    _fields_ = [("V", C.c_int), ("dtype", C.c_int), ("param_rows", C.c_int),
+                ("temperature", C.c_void_p), ("top_k", C.c_void_p), ("top_p", C.c_void_p),
+                ("min_p", C.c_void_p)]
+
+
+class PageBook(C.Structure):
+    _fields_ = [("page_table", C.c_void_p), ("held", C.c_void_p), ("cache_len", C.c_void_p),
+                ("ref", C.c_void_p), ("B", C.c_int), ("max_pages", C.c_int), ("n_pages", C.c_int),
+                ("page_size", C.c_int)]
+
+
 _lib = None
 
 
@@ -139,6 +153,16 @@ def lib() -> C.CDLL:
                                P, P, I, I, I, P, P, P], I),
             "moe_kv_commit": ([P, P, P, P, P, P, P, I, I, P, P, P], I),
             "moe_block_norm": ([P, P, P, P, P, I, C.c_float, P, C.c_float, I, P, P, P], I),
+            "moe_few_workspace_bytes": ([P, I], S),
+            "moe_few_forward": ([P, P, P, P, P, P, P, I, P, P, P, P, P, P, P], I),
+            "moe_sample": ([P, P, C.c_longlong, P, I, P, P, P], I),
+            "moe_tree_accept": ([P, P, P, P, I, I, I, I, P, P, P, P], I),
+            "moe_pages_workspace_bytes": ([P], S),
+            "moe_kv_reserve": ([P, I, P, P, P], I),
+            "moe_kv_free": ([P, P, P, I, P, P], I),
+            "moe_kv_fork": ([P, P, P, I, P, P, P], I),
+            "moe_kv_compact": ([P, P, P, P, P, P, P], I),
+            "moe_kv_copy_pages": ([P, P, P, P, I, P, P, P], I),
         }
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
@@ -478,9 +502,8 @@ def cache_desc(pages: torch.Tensor, H: int, max_pages: int, window: int = 0, sin
                      dh ** -0.5 if scale is None else scale)
 
 
-def _pools(fn, C_, k_pages, v_pages, page_table, cache_len, B, row_start):
-    """Checks the cache's tensors against its description; the device index and type."""
-    index, dt = k_pages.get_device(), _TORCH[C_.dtype]
+def _like_cache(fn, C_, k_pages, v_pages, index, dt):
+    """Refuses pools that are not what the cache's description says."""
     shape = (C_.n_pages, C_.page_size, C_.H_kv, C_.dh)
     st = (C_.stride_page, C_.stride_tok, C_.stride_head, 1)
     if not (k_pages.dtype is dt and k_pages.shape == shape and k_pages.stride() == st and
@@ -491,6 +514,12 @@ def _pools(fn, C_, k_pages, v_pages, page_table, cache_len, B, row_start):
             # (a dimension of one element has no stride to speak of)
             if any(n > 1 and x != y for n, x, y in zip(shape, t.stride(), st)):
                 raise ValueError(f"{fn}: {name} has other strides than the cache description")
+
+
+def _pools(fn, C_, k_pages, v_pages, page_table, cache_len, B, row_start):
+    """Checks the cache's tensors against its description; the device index and type."""
+    index, dt = k_pages.get_device(), _TORCH[C_.dtype]
+    _like_cache(fn, C_, k_pages, v_pages, index, dt)
     i32 = torch.int32
     _dense(fn, "page_table", page_table, i32, (B, C_.max_pages), index)
     _dense(fn, "cache_len", cache_len, i32, (B,), index)
@@ -611,6 +640,190 @@ def moe_block_norm(L, x, branch=None, h=None, hn=None, w_post=None, gate=None, g
         _dense(fn, "gate", gate, dt, (-(-R // gate_rows), d), index)
     return _run(fn, index, stream, C.byref(L), x.data_ptr(), _at(branch), _at(w_post), _at(gate),
                 gate_rows, scale, _at(w_pre), eps, R, _at(h), _at(hn))
+
+
+# ------------------------------------------------------------- a decoding round's other calls
+
+def _zeroed(n: int, device) -> torch.Tensor:
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    ws[:4096].zero_()
+    return ws
+
+
+def moe_few_workspace_bytes(L: LayerDesc, R: int) -> int:
+    return int(lib().moe_few_workspace_bytes(C.byref(L), R))
+
+
+def few_workspace(L: LayerDesc, R: int, device="cuda") -> torch.Tensor:
+    """A device byte buffer of moe_few_workspace_bytes whose head is zeroed."""
+    n = moe_few_workspace_bytes(L, R)
+    if n == 0:
+        raise MoeError("moe_few_workspace_bytes", MOE_ERR_ARG)
+    return _zeroed(n, device)
+
+
+def moe_few_forward(L, x, W_r, W_gate, W_up, W_down, slot_of_expert, y, ws, logits=None,
+                    topk_idx=None, gates=None, opts: Optional[RunOpts] = None, stream=None):
+    """The whole layer for up to 16 tokens in one launch (see include/moetree.h). x, y [R, d]; ws
+    from few_workspace."""
+    fn, R, d, f, dt = "moe_few_forward", x.shape[0], L.d, L.f, _TORCH[L.dtype]
+    index, S = x.get_device(), L.slots if L.slots > 0 else L.E
+    _dense(fn, "x", x, dt, (R, d), index)
+    _dense(fn, "y", y, dt, (R, d), index)
+    _dense(fn, "W_r", W_r, dt, (L.E, d), index)
+    _dense(fn, "W_gate", W_gate, dt, (S, f, d), index)
+    _dense(fn, "W_up", W_up, dt, (S, f, d), index)
+    _dense(fn, "W_down", W_down, dt, (S, d, f), index)
+    _dense(fn, "slot_of_expert", slot_of_expert, torch.int32, (L.E,), index)
+    _dense(fn, "logits", logits, torch.float32, (R, L.E), index)
+    _dense(fn, "topk_idx", topk_idx, torch.int32, (R, L.k), index)
+    _dense(fn, "gates", gates, torch.float32, (R, L.k), index)
+    desc = C.byref(L)
+    if 0 < R <= 16:
+        if ws is None:
+            raise ValueError(f"{fn}: it needs a workspace")
+        _scratch(fn, ws, index, lib().moe_few_workspace_bytes(desc, R))
+    return _run(fn, index, stream, desc, x.data_ptr(), W_r.data_ptr(), W_gate.data_ptr(),
+                W_up.data_ptr(), W_down.data_ptr(), _at(slot_of_expert), R, y.data_ptr(),
+                _at(logits), _at(topk_idx), _at(gates), _at(ws),
+                None if opts is None else C.byref(opts))
+
+
+def moe_sample(logits, u, token, temperature=None, top_k=None, top_p=None, min_p=None,
+               param_rows: int = 1, logprob=None, stream=None):
+    """Samples a token from each row of logits [R, V] (rows may be a part of wider ones) at the
+    random numbers u [R] (see include/moetree.h). temperature, top_k (int32), top_p, min_p
+    [ceil(R / param_rows)] on the device, or None."""
+    fn, index = "moe_sample", logits.get_device()
+    R, V = logits.shape
+    code = _CODE.get(logits.dtype)
+    if code is None:
+        raise ValueError(f"{fn}: logits are {logits.dtype}, expected float32 or bfloat16")
+    if V > 1 and logits.stride(1) != 1:
+        raise ValueError(f"{fn}: a row's logits must lie side by side")
+    if param_rows < 1:
+        raise ValueError(f"{fn}: param_rows is {param_rows}, expected the rows of an entry")
+    ld = logits.stride(0) if R > 1 else V
+    f32, n = torch.float32, (-(-R // param_rows),)
+    _dense(fn, "u", u, f32, (R,), index)
+    _dense(fn, "token", token, torch.int32, (R,), index)
+    _dense(fn, "logprob", logprob, f32, (R,), index)
+    _dense(fn, "temperature", temperature, f32, n, index)
+    _dense(fn, "top_k", top_k, torch.int32, n, index)
+    _dense(fn, "top_p", top_p, f32, n, index)
+    _dense(fn, "min_p", min_p, f32, n, index)
+    P = SampleParams(V, code, param_rows, _at(temperature), _at(top_k), _at(top_p), _at(min_p))
+    return _run(fn, index, stream, C.byref(P), logits.data_ptr(), ld, u.data_ptr(), R,
+                token.data_ptr(), _at(logprob))
+
+
+def moe_tree_accept(token, parent, sampled, B, N, path, n_accept, emitted=None, row_start=None,
+                    stream=None):
+    """Follows the sampled tokens through B draft trees (see include/moetree.h). token, parent (or
+    None: chains), sampled [R]; path, emitted [B, P]; n_accept [B]; all int32."""
+    fn, i32, R, index = "moe_tree_accept", torch.int32, token.shape[0], path.get_device()
+    P = path.shape[1]
+    _dense(fn, "token", token, i32, (R,), index)
+    _dense(fn, "parent", parent, i32, (R,), index)
+    _dense(fn, "sampled", sampled, i32, (R,), index)
+    _dense(fn, "row_start", row_start, i32, (B + 1,), index)
+    _dense(fn, "path", path, i32, (B, P), index)
+    _dense(fn, "n_accept", n_accept, i32, (B,), index)
+    _dense(fn, "emitted", emitted, i32, (B, P), index)
+    return _run(fn, index, stream, token.data_ptr(), _at(parent), sampled.data_ptr(),
+                _at(row_start), B, N, R, P, path.data_ptr(), n_accept.data_ptr(), _at(emitted))
+
+
+def page_book(page_table, held, cache_len, ref, page_size: int) -> PageBook:
+    """The book of a cache's pages (see moe_page_book): page_table [B, max_pages], held [B],
+    cache_len [B], ref [n_pages], int32 on one device. It keeps the tensors alive."""
+    fn, i32, index = "page_book", torch.int32, page_table.get_device()
+    B, width = page_table.shape
+    _dense(fn, "page_table", page_table, i32, (B, width), index)
+    _dense(fn, "held", held, i32, (B,), index)
+    _dense(fn, "cache_len", cache_len, i32, (B,), index)
+    _dense(fn, "ref", ref, i32, (ref.numel(),), index)
+    K = PageBook(page_table.data_ptr(), held.data_ptr(), cache_len.data_ptr(), ref.data_ptr(), B,
+                 width, ref.numel(), page_size)
+    K.tensors, K.index = (page_table, held, cache_len, ref), index
+    return K
+
+
+def moe_pages_workspace_bytes(K: PageBook) -> int:
+    return int(lib().moe_pages_workspace_bytes(C.byref(K)))
+
+
+def pages_workspace(K: PageBook, device=None) -> torch.Tensor:
+    """A device byte buffer of moe_pages_workspace_bytes whose head is zeroed."""
+    n = moe_pages_workspace_bytes(K)
+    if n == 0:
+        raise MoeError("moe_pages_workspace_bytes", MOE_ERR_ARG)
+    return _zeroed(n, K.tensors[0].device if device is None else device)
+
+
+def _pages_scratch(fn, K, ws):
+    if ws is None:
+        raise ValueError(f"{fn}: it needs a workspace")
+    _scratch(fn, ws, K.index, lib().moe_pages_workspace_bytes(C.byref(K)))
+
+
+def moe_kv_reserve(K, N, ws, n_new=None, stream=None):
+    """Room for N (n_new [B]: for each sequence its own) more tokens (see include/moetree.h)."""
+    fn = "moe_kv_reserve"
+    _dense(fn, "n_new", n_new, torch.int32, (K.B,), K.index)
+    _pages_scratch(fn, K, ws)
+    return _run(fn, K.index, stream, C.byref(K), N, _at(n_new), ws.data_ptr())
+
+
+def moe_kv_free(K, seqs, ws, keep=None, stream=None):
+    """Gives back the pages of the sequences seqs [n] behind their first keep [n] tokens (None:
+    all)."""
+    fn, shape = "moe_kv_free", (seqs.numel(),)
+    _dense(fn, "seqs", seqs, torch.int32, shape, K.index)
+    _dense(fn, "keep", keep, torch.int32, shape, K.index)
+    _pages_scratch(fn, K, ws)
+    return _run(fn, K.index, stream, C.byref(K), seqs.data_ptr(), _at(keep), shape[0],
+                ws.data_ptr())
+
+
+def moe_kv_fork(K, src, dst, moves, ws, stream=None):
+    """Sequences dst [n] become forks of src [n]; moves [n, 3] is for moe_kv_copy_pages."""
+    fn, n = "moe_kv_fork", src.numel()
+    _dense(fn, "src", src, torch.int32, (n,), K.index)
+    _dense(fn, "dst", dst, torch.int32, (n,), K.index)
+    _dense(fn, "moves", moves, torch.int32, (n, 3), K.index)
+    _pages_scratch(fn, K, ws)
+    return _run(fn, K.index, stream, C.byref(K), src.data_ptr(), dst.data_ptr(), n,
+                moves.data_ptr(), ws.data_ptr())
+
+
+def moe_kv_compact(K, table_out, ref_out, moves, counts, ws, stream=None):
+    """Plans a dense pool: table_out, ref_out (may be the book's own), moves [n_pages // 2, 3],
+    counts [2] (moves, pages in use)."""
+    fn, i32 = "moe_kv_compact", torch.int32
+    _dense(fn, "table_out", table_out, i32, (K.B, K.max_pages), K.index)
+    _dense(fn, "ref_out", ref_out, i32, (K.n_pages,), K.index)
+    _dense(fn, "moves", moves, i32, (K.n_pages // 2, 3), K.index)
+    _dense(fn, "counts", counts, i32, (2,), K.index)
+    _pages_scratch(fn, K, ws)
+    return _run(fn, K.index, stream, C.byref(K), table_out.data_ptr(), ref_out.data_ptr(),
+                moves.data_ptr(), counts.data_ptr(), ws.data_ptr())
+
+
+def moe_kv_copy_pages(C_, k_pages, v_pages, moves, count=None, ws=None, stream=None):
+    """Copies the tokens of moves [n, 3] (page, new page, tokens) between a layer's pages; count: a
+    device int32 tensor whose first element says how many of them, None: all."""
+    fn, n = "moe_kv_copy_pages", moves.shape[0]
+    index, dt = k_pages.get_device(), _TORCH[C_.dtype]
+    _like_cache(fn, C_, k_pages, v_pages, index, dt)
+    _dense(fn, "moves", moves, torch.int32, (n, 3), index)
+    if count is not None:
+        _dense(fn, "count", count, torch.int32, count.shape, index)
+        if count.numel() < 1:
+            raise ValueError(f"{fn}: count has no element")
+    _scratch(fn, ws, index, 4096)
+    return _run(fn, index, stream, C.byref(C_), k_pages.data_ptr(), v_pages.data_ptr(),
+                moves.data_ptr(), n, _at(count), _at(ws))
 
 
 def moe_event_wait(event, timeout_s: float) -> None:

@@ -19,6 +19,8 @@
  *     a cost-aware choice of which drafted nodes to verify (moe_draft_select).
  *   - the attention half of the block for the same nodes: a paged cache, tree attention
  *     over it, the commit of the accepted path, and the norms between the halves.
+ *   - what a decoding round needs beside these: the layer for a few tokens, sampling, the
+ *     walk along a tree's samples, and the upkeep of the cache's pages.
  *
  * Conventions shared by every entry point:
  *   - All tensors are plain pointers, row-major, densely packed. "device" means
@@ -335,8 +337,8 @@ moe_status moe_draft_select(const moe_layer_desc *L, int C, const int *parent, c
 
 /* Reads and clears the kernel-side check word of a workspace. Waits for `stream`.
  * *flags = 0 when no kernel reported a problem since the last call; bit 0 = an
- * expert id outside [0, E) was skipped; bit 1 = a bounded device wait gave up; bits 2 and 3
- * are those of the attention calls. */
+ * expert id outside [0, E) was skipped; bit 1 = a bounded device wait gave up; bits 2 to 4
+ * are those of the attention and page calls. */
 moe_status moe_workspace_check(void *workspace, int *flags, moe_stream_t stream);
 
 /* ---------------------------------------------------------------- offload ----
@@ -555,6 +557,151 @@ moe_status moe_block_norm(const moe_layer_desc *L, const void *x, const void *br
                           const void *w_post, const void *gate, int gate_rows, float scale,
                           const void *w_pre, float eps, int R, void *h, void *hn,
                           moe_stream_t stream);
+
+/* ------------------------------------------------------------- decoding ----
+ * What a round needs beside the tree's layer and attention. */
+
+/* Bytes of workspace of moe_few_forward for up to R tokens (1 .. 16); 0 for a bad descriptor.
+ * Like the attention's workspace, its first 4096 bytes must be zero before the first call that
+ * gets it (check word and grid barrier), and again after a call whose check word has bit 1; the
+ * rest is scratch. Two calls that overlap in time must use different workspaces, captured graphs
+ * that may run at the same time too. */
+size_t moe_few_workspace_bytes(const moe_layer_desc *L, int R);
+
+/* The whole layer for a few tokens in one launch ("MoE and speculative decoding" blog, "starting
+ * from one MoE layer"): single tokens of a few users, or a short chain, routed naturally:
+ *   l = W_r x;  e_1 .. e_k the k largest (ties to the lower id);  g = softmax(l[e]);
+ *   y = sum_j g_j W_down[e_j] (silu(W_gate[e_j] x) * (W_up[e_j] x)),
+ * with opts->norm_input on the pre-norm of x, with opts->residual added to x (see moe_run_opts).
+ * R <= 16, else MOE_ERR_UNSUPPORTED (moe_tree_forward takes any number; its results differ by
+ * roundings). Sums are fp32; bf16 layers keep the gated activations as a bf16 value and its bf16
+ * rest (2^-17 relative). Tokens that do not fit a CTA's shared memory together (more than 138 KB
+ * of rows) take further launches.
+ *   x, y [R, d] device, layer dtype; y may be x itself, and must not overlap it otherwise.
+ *   W_r, W_gate, W_up, W_down, slot_of_expert as for moe_tree_forward.
+ *   logits [R, E], topk_idx [R, k], gates [R, k] device outputs, each may be NULL.
+ *   opts: norm_input, residual and ffn_max_ctas are used; events are refused.
+ * The launch is cooperative: it waits until the GPU has room for one CTA on each SM (or
+ * ffn_max_ctas of them), so two calls on two streams run at once only if both are capped.
+ * Check word: bit 0 = an expert's slot outside [0, slots) was skipped, bit 1 = a bounded wait
+ * gave up (y is not valid). */
+moe_status moe_few_forward(const moe_layer_desc *L, const void *x, const void *W_r,
+                           const void *W_gate, const void *W_up, const void *W_down,
+                           const int *slot_of_expert, int R, void *y, float *logits, int *topk_idx,
+                           float *gates, void *workspace, const moe_run_opts *opts,
+                           moe_stream_t stream);
+
+/* How rows of logits are sampled. Row r uses entry r / param_rows of each array (device, or NULL:
+ * not asked for): param_rows = N shares a sequence's settings among a tree's nodes.
+ *   temperature T  <= 0 (or NaN): the largest logit's token, ties to the lowest id. NULL: 1.
+ *   top_k          the k largest are kept (ties to the lower id); <= 0 or >= V: all.
+ *   top_p          of these, in descending order (ties to the lower id), those are kept before
+ *                  which less than p of their weight lies; the first always; >= 1 (or NaN): all.
+ *   min_p          of these, those of at least min_p times the largest's weight; <= 0: all. */
+typedef struct {
+    int V;      /* tokens, 1 .. 524288 */
+    int dtype;  /* moe_dtype of the logits */
+    int param_rows;
+    const float *temperature;
+    const int *top_k;
+    const float *top_p, *min_p;
+} moe_sample_params;
+
+/* Samples a token from each row of logits by inversion, in the order of the tokens:
+ *   w_i = exp((l_i - max l) / T) of the kept tokens, else 0;
+ *   token = the first i with w_0 + .. + w_i > u (w_0 + .. + w_(V-1)),
+ * u a given random number of [0, 1) (below 0 or NaN counts as 0, 1 and above as the largest below).
+ * Weights are carried to 2^-42 relative and summed as integers of 2^-43 of the largest, so the token
+ * is that of the definition except where u lies within some 2^-40 of a border, whatever the order of
+ * threads; weights below 2^-43 of the largest count as 0. NaN logits count as -inf
+ * (masked), +inf as the type's largest finite value; a row without a logit above -inf gives token -1
+ * and logprob -inf.
+ *   logits [R, V] device, rows ld elements apart (any ld >= V, any alignment of the type).
+ *   u [R] device fp32; token [R] device int32; logprob [R] device fp32 or NULL: log of the token's
+ *   share of the kept weight. Outputs must not overlap inputs. */
+moe_status moe_sample(const moe_sample_params *P, const void *logits, long long ld, const float *u,
+                      int R, int *token, float *logprob, moe_stream_t stream);
+
+/* Follows the tokens sampled at a draft tree's nodes ("MoE and speculative decoding" blog: the
+ * accepted prefix of a round): from node 0 on, the next node is the lowest child c of the present
+ * one with token[c] == sampled[present]; the walk ends where there is none, or after P nodes. As
+ * every node's token is drawn from the target's own distribution there, what is emitted is
+ * distributed as without a draft.
+ *   token [R] device int32: the drafted token of each node (node 0's is not looked at);
+ *   parent, row_start, B, N, R as for moe_tree_attention (parent NULL: chains); ranges that do not
+ *   fit are cut. sampled [R] device int32: moe_sample's tokens; a negative one ends the walk.
+ *   path [B, P] device int32: the nodes, ascending, as moe_kv_commit takes them (-1 past the end);
+ *   n_accept [B]: how many (0 for a sequence without nodes); emitted [B, P] or NULL: the tokens
+ *   sampled at them (-1 past the end): the accepted ones and the one behind them. P >= 1. */
+moe_status moe_tree_accept(const int *token, const int *parent, const int *sampled,
+                           const int *row_start, int B, int N, int R, int P, int *path,
+                           int *n_accept, int *emitted, moe_stream_t stream);
+
+/* ---------------------------------------------------------------- pages ----
+ * Upkeep of the pages that the attention's calls take for granted. The bookkeeping is done once for
+ * all layers; where keys and values have to move, it leaves a list of moves for moe_kv_copy_pages,
+ * which is called for each layer's pools.
+ *
+ * Sequence b holds the pages page_table[b][0 .. held[b] - 1], of which its cache_len[b] tokens fill
+ * the first ones; ref[p] counts the table entries that hold page p, and a page with ref[p] <= 0 is
+ * free. New pages are the free ones of the lowest numbers, in the order of the sequences (of a list's
+ * entries), so results repeat. All arrays are device int32. Calls on one book are ordered on one
+ * stream by the caller. A sequence whose numbers do not fit (held outside [0, max_pages], cache_len
+ * outside [0, held * page_size]) is left as it is.
+ * Limits: B <= 65536, n_pages <= 2^24, max_pages * page_size <= 2^30.
+ * Check word of the workspace: bit 2 = a page outside the pool, or one given back that nobody held;
+ * bit 3 = a sequence outside [0, B), one whose numbers do not fit, one that would need more than
+ * max_pages, or a fork that is refused; bit 4 = too few free pages. */
+typedef struct {
+    int *page_table; /* [B, max_pages] */
+    int *held;       /* [B] */
+    int *cache_len;  /* [B] */
+    int *ref;        /* [n_pages] */
+    int B, max_pages, n_pages, page_size;
+} moe_page_book;
+
+/* Bytes of workspace of the bookkeeping calls; 0 for a bad book. Its first 4096 bytes must be zero
+ * before the first call (the check word); calls that overlap in time need different ones. */
+size_t moe_pages_workspace_bytes(const moe_page_book *K);
+
+/* Gives every sequence room for n_new[b] tokens (NULL: N for all) behind its cache_len: pages are
+ * added until held[b] * page_size >= cache_len[b] + n_new[b]. A sequence gets all it lacks or
+ * nothing: the first whose need is not met, and those behind it that lack any, get none (bit 4). */
+moe_status moe_kv_reserve(const moe_page_book *K, int N, const int *n_new, void *workspace,
+                          moe_stream_t stream);
+
+/* Gives back pages of n listed sequences: keep[i] tokens of sequence seqs[i] stay (NULL: none; more
+ * than it has: all), and the pages behind them that it holds are released; cache_len becomes at most
+ * keep[i]. A sequence may be listed more than once (the smallest keep holds). seqs, keep [n]. */
+moe_status moe_kv_free(const moe_page_book *K, const int *seqs, const int *keep, int n,
+                       void *workspace, moe_stream_t stream);
+
+/* Forks sequences: dst[i] becomes a copy of src[i] as it is before the call. Pages full of src's
+ * tokens are shared; the tokens behind them get a page of their own, and moves[i] = (src's page, the new
+ * page, tokens to copy), or (-1, -1, 0) where there are none. Pages that src holds behind its tokens are
+ * not shared. A target holds no pages (moe_kv_free), is listed once (else the first entry has it)
+ * and is no entry's source; other entries are refused (bit 3), and one without a page for its last
+ * tokens too (bit 4): their targets stay empty. src, dst [n], moves [n, 3]; n <= B. */
+moe_status moe_kv_fork(const moe_page_book *K, const int *src, const int *dst, int n, int *moves,
+                       void *workspace, moe_stream_t stream);
+
+/* Plans a dense pool: the pages in use with numbers from n_used (how many are in use) on move to the
+ * free ones below it, each in ascending order. moves [n_pages / 2, 3]: (page, new page, page_size);
+ * rows past the moves are left as they are. counts [2]: number of moves, n_used. table_out, ref_out:
+ * the table and the counts afterwards; each may be the book's own, or other memory, so that the old
+ * table serves kernels in flight. Table entries behind held[b] are copied as they are. After the
+ * moves are made (moe_kv_copy_pages, all layers) only pages below n_used are in use. */
+moe_status moe_kv_compact(const moe_page_book *K, int *table_out, int *ref_out, int *moves,
+                          int *counts, void *workspace, moe_stream_t stream);
+
+/* Copies keys and values between pages of one layer's pools: for each i < n (count [1] device, or
+ * NULL: n; the smaller) the first moves[i][2] tokens of page moves[i][0] go to page moves[i][1].
+ * No page may be written by two moves, nor read by one and written by another (the lists of
+ * moe_kv_fork and moe_kv_compact are such). Moves of no tokens are skipped; those of more than
+ * page_size, or outside the pool, too (bit 2 of the check word; workspace may be NULL). */
+moe_status moe_kv_copy_pages(const moe_cache_desc *C, void *k_pages, void *v_pages,
+                             const int *moves, int n, const int *count, void *workspace,
+                             moe_stream_t stream);
 
 #ifdef __cplusplus
 }
