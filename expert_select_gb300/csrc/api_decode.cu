@@ -60,13 +60,16 @@ moe_status moe_few_forward(const moe_layer_desc *L, const void *x, const void *W
     a.slot = slot_of_expert;
     a.h = at<void>(workspace, w.h);
     a.flags = at<int>(workspace, 0);
-    a.barrier = at<int>(workspace, 1024);
+    a.barrier = at<unsigned long long>(workspace, few::kBarrier);
+    a.scores = at<unsigned long long>(workspace, few::kScores);
     a.d = L->d;
     a.E = L->E;
     a.k = L->k;
     a.f = L->f;
     a.slots = L->slots > 0 ? L->slots : L->E;
     a.norm = opts && opts->norm_input;
+    a.inv_d.hi = (float)(1.0 / L->d);
+    a.inv_d.lo = (float)(1.0 / L->d - (double)a.inv_d.hi);
     a.residual = opts && opts->residual;
     const int most = few::rows_at_once(*L);
     const size_t row = (size_t)L->d * elem_size(L->dtype);
@@ -74,7 +77,7 @@ moe_status moe_few_forward(const moe_layer_desc *L, const void *x, const void *W
         a.R = std::min(most, R - r0);
         a.x = (const char *)x + r0 * row;
         a.y = (char *)y + r0 * row;
-        a.logits = (logits ? logits : at<float>(workspace, w.logits)) + (size_t)r0 * L->E;
+        a.logits = logits ? logits + (size_t)r0 * L->E : nullptr;
         a.topk_idx = topk_idx ? topk_idx + (size_t)r0 * L->k : nullptr;
         a.gates = gates ? gates + (size_t)r0 * L->k : nullptr;
         const cudaError_t err = few::launch_few(a, L->dtype, opts ? opts->ffn_max_ctas : 0,

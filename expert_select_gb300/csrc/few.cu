@@ -19,7 +19,6 @@
 #include <algorithm>
 
 #include "few.cuh"
-#include "norm.cuh"
 
 namespace moe {
 namespace few {
@@ -28,8 +27,7 @@ static size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 WsLayout ws_layout(const moe_layer_desc &L, int R) {
     WsLayout w{};
-    w.logits = kHeadBytes;
-    w.h = align256(w.logits + (size_t)R * L.E * 4);
+    w.h = kHeadBytes;
     w.total = align256(w.h + (size_t)R * L.k * L.f * 4);
     return w;
 }
@@ -50,8 +48,11 @@ struct Plan {
     unsigned short tokens[kMaxE];     // by expert: a bit for each token
     unsigned char place[kMaxE][kMaxRows];  // by expert and token: the token's place of the expert
     float gate[kMaxRows][kMaxK];
-    double part[kWarps];
-    double scale[kMaxRows];
+    Pair part[kWarps], scale[kMaxRows];
+    double wide_scale[kMaxRows];
+    int wide[kMaxRows];
+    uint32_t word[kMaxE / 32];
+    unsigned long long launch;
     int alive;
 };
 
@@ -88,41 +89,51 @@ __device__ __forceinline__ void mma32(float (&c)[4], const uint4 &x, const uint4
     mma(c, x.z, y.z, x.w, y.w, b.z, b.w);
 }
 
-// Waits until all CTAs of the grid have come here; what they wrote before is visible then. bar: a
-// count and a generation; the last to come sets the count back. Gives up after 2 s.
-__device__ __forceinline__ bool grid_barrier(const Args &a, Plan &s) {
+// The head of the workspace holds a word that counts the CTAs that have ended step 2 (low 16 bits)
+// and the launches so far (the rest), and the scores of step 1, each beside the number of the launch that
+// wrote it: who reads a score waits for the word itself, not for a barrier and then for the word.
+__device__ __forceinline__ unsigned long long load_relaxed(const unsigned long long *p) {
+    unsigned long long v;
+    asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ unsigned long long load_acquire(const unsigned long long *p) {
+    unsigned long long v;
+    asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ unsigned long long now_ns() {
+    unsigned long long t;
+    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+    return t;
+}
+constexpr unsigned long long kPatience = 2000000000ull;  // a wait gives up after 2 s
+
+// Waits until all CTAs of the grid have come here; what they wrote before is visible then.
+__device__ __forceinline__ bool grid_barrier(const Args &a, Plan &s, unsigned long long launch) {
     __syncthreads();
     if (threadIdx.x == 0) {
-        unsigned *count = (unsigned *)a.barrier, *gen = count + 32;
-        unsigned was, got;
-        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(was) : "l"(gen) : "memory");
+        unsigned long long was;
         __threadfence();
-        asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;"
-                     : "=r"(got)
-                     : "l"(count)
+        asm volatile("atom.acq_rel.gpu.global.add.u64 %0, [%1], 1;"
+                     : "=l"(was)
+                     : "l"(a.barrier)
                      : "memory");
-        int alive = 1;
-        if (got == gridDim.x - 1) {
-            *count = 0;
-            asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(gen), "r"(was + 1) : "memory");
+        if ((was & 0xffff) == gridDim.x - 1) {
+            // the next launch's number; who still waits takes either as the sign
+            atomicAdd(a.barrier, 0x10000ull - gridDim.x);
         } else {
-            unsigned long long t0, t;
-            asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t0));
-            for (unsigned i = 0;; ++i) {
-                unsigned now;
-                asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(now) : "l"(gen) : "memory");
-                if (now != was) break;
-                if ((i & 255) == 255) {
-                    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-                    if (t - t0 > 2000000000ull) {
-                        atomicOr(a.flags, FLAG_WAIT_TIMEOUT);
-                        alive = 0;
-                        break;
-                    }
+            const unsigned long long t0 = now_ns();
+            for (unsigned i = 1;; ++i) {
+                const unsigned long long v = load_acquire(a.barrier);
+                if (v >> 16 != launch || (v & 0xffff) == gridDim.x) break;
+                if (i % 256 == 0 && now_ns() - t0 > kPatience) {
+                    atomicOr(a.flags, FLAG_WAIT_TIMEOUT);
+                    s.alive = 0;
+                    break;
                 }
             }
         }
-        s.alive = alive;
     }
     __syncthreads();
     return s.alive != 0;
@@ -147,102 +158,146 @@ template <> __device__ __forceinline__ void load8(const float *p, float v[8]) {
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 
-// Every token's scale 1 / sqrt(mean x^2 + eps). The squares' sum is carried as two fp32 values (bf16
-// squares are exact in fp32, fp32 ones are split), or in fp64 where it leaves fp32's range; the root
-// by two Newton steps in fp64, as a divide and a root there take dozens of its slow operations.
+// Every token's scale 1 / sqrt(mean x^2 + eps), from the tokens in shared memory. Sums and the scale
+// are carried as pairs (2^-45; bf16 squares are exact in fp32, fp32 ones have a rest), as fp64
+// operations take tens of cycles each here; a row whose squares leave fp32's range takes them.
 template <typename T>
-__device__ __forceinline__ void norm_scales(const Args &a, Plan &s) {
+__device__ __forceinline__ void norm_scales(const Args &a, Plan &s, const char *xs) {
+    const int stride = token_stride(a.d, sizeof(T));
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int per = kWarps;  // warps a token
     while (per > 1 && kWarps / per < a.R) per /= 2;
     const int r = warp / per, w = warp % per;
-    const T *x = reinterpret_cast<const T *>(a.x) + (size_t)r * a.d;
-    double sum = 0.0;
+    const T *x = reinterpret_cast<const T *>(xs + r * stride);
+    Pair sum{0.f, 0.f};
     if (r < a.R) {
-        float hi = 0.f, lo = 0.f;
         for (int c = (w * 32 + lane) * 8; c < a.d; c += per * 256) {
             float v[8];
             load8(x + c, v);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float p = v[i] * v[i];
-                if (sizeof(T) == 4) lo += fmaf(v[i], v[i], -p);
-                add_kept(hi, lo, p);
+                if (sizeof(T) == 4) sum.lo += fmaf(v[i], v[i], -p);
+                add_kept(sum.hi, sum.lo, p);
             }
-        }
-        // (squares below 2^-100 may have lost bits, infinite ones everything)
-        const bool fine = hi < 1e30f && (hi > 1e-25f || hi == 0.f);
-        if (!__all_sync(0xffffffffu, fine)) {
-            sum = 0.0;
-            for (int c = (w * 32 + lane) * 8; c < a.d; c += per * 256) {
-                float v[8];
-                load8(x + c, v);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) sum = fma((double)v[i], (double)v[i], sum);
-            }
-        } else {
-            sum = (double)hi + (double)lo;
         }
     }
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    for (int o = 16; o >= 1; o >>= 1) {
+        const float hi = __shfl_xor_sync(0xffffffffu, sum.hi, o), lo = __shfl_xor_sync(0xffffffffu, sum.lo, o);
+        add_kept(sum.hi, sum.lo, hi);
+        sum.lo += lo;
+    }
     if (lane == 0) s.part[warp] = sum;
     __syncthreads();
     if (threadIdx.x < a.R) {
-        double v = 0.0;
-        for (int i = 0; i < per; ++i) v += s.part[threadIdx.x * per + i];
-        v = v / (double)a.d + kNormEps;
-        double y;
-        if (v < 1e37) {
-            y = (double)rsqrtf((float)v);
-            y = y * fma(-0.5 * v * y, y, 1.5);
-            y = y * fma(-0.5 * v * y, y, 1.5);
-        } else {
-            y = 1.0 / sqrt(v);
+        Pair v{0.f, 0.f};
+        for (int i = 0; i < per; ++i) {
+            add_kept(v.hi, v.lo, s.part[threadIdx.x * per + i].hi);
+            v.lo += s.part[threadIdx.x * per + i].lo;
         }
-        s.scale[threadIdx.x] = y;
+        // (squares below 2^-100 may have lost bits, infinite ones everything)
+        const bool wide = !(v.hi < 1e30f && (v.hi > 1e-25f || v.hi == 0.f));
+        s.wide[threadIdx.x] = wide;
+        // mean + eps
+        Pair m;
+        m.hi = v.hi * a.inv_d.hi;
+        m.lo = fmaf(v.hi, a.inv_d.hi, -m.hi) + fmaf(v.hi, a.inv_d.lo, v.lo * a.inv_d.hi);
+        add_kept(m.hi, m.lo, (float)kNormEps);
+        m.lo += (float)(kNormEps - (double)(float)kNormEps);
+        // a Newton step from the fp32 root: y (1 + e / 2 + 3 e^2 / 8), e = 1 - m y^2
+        const float y = rsqrtf(m.hi), q = __fmul_rn(y, y), qe = fmaf(y, y, -q);
+        const float p = __fmul_rn(m.hi, q), pe = fmaf(m.hi, q, -p) + fmaf(m.hi, qe, m.lo * q);
+        const float e = (1.f - p) - pe;
+        s.scale[threadIdx.x] = Pair{y, y * e * fmaf(0.375f, e, 0.5f)};
+    }
+    __syncthreads();
+    if (r < a.R && w == 0 && s.wide[r]) {
+        double t = 0.0;
+        for (int c = lane * 8; c < a.d; c += 256) {
+            float v[8];
+            load8(x + c, v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) t = fma((double)v[i], (double)v[i], t);
+        }
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+        if (lane == 0) s.wide_scale[r] = 1.0 / sqrt(t / (double)a.d + kNormEps);
     }
     __syncthreads();
 }
 
-// The tokens (normed where asked) go to shared memory.
+// v times a scale in fp64, rounded once to bf16 (a call, so that no other element takes the fp64
+// instructions).
+__device__ __noinline__ uint32_t scaled_wide(float v, double sc) {
+    return __bfloat16_as_ushort(__double2bfloat16((double)v * sc));
+}
+// The same for an fp32 product that lies in the middle of two bf16 values: its rest, at most half a
+// step of fp32's, decides; elsewhere the product's own rounding is the answer.
+__device__ __noinline__ uint32_t scaled_middle(float v, Pair sc) {
+    const float p = v * sc.hi;
+    if (!(fabsf(p) > 1e-25f)) return scaled_wide(v, (double)sc.hi + (double)sc.lo);
+    const uint32_t b = __float_as_uint(p);
+    const float rest = fmaf(v, sc.hi, -p) + v * sc.lo;
+    if (rest == 0.f) return (b + 0x7fffu + (b >> 16 & 1u)) >> 16;
+    return (b >> 16) + ((rest > 0.f) == (p > 0.f) ? 1u : 0u);
+}
+__device__ __forceinline__ void scale16(uint4 *p, Pair sc, const double *wide) {
+    const uint4 w = *p;
+    float v[8];
+    load8(reinterpret_cast<const __nv_bfloat16 *>(&w), v);
+    uint32_t q[8];
+    bool middle = false;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t b = __float_as_uint(v[j] * sc.hi);
+        middle |= (b & 0xffffu) == 0x8000u;
+        q[j] = (b + 0x7fffu + (b >> 16 & 1u)) >> 16;
+    }
+    // (what is not a number would be rounded to something else)
+    if (middle || wide) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (wide)
+                q[j] = scaled_wide(v[j], *wide);
+            else if ((__float_as_uint(v[j] * sc.hi) & 0xffffu) == 0x8000u)
+                q[j] = scaled_middle(v[j], sc);
+        }
+    }
+    *p = make_uint4(q[0] | q[1] << 16, q[2] | q[3] << 16, q[4] | q[5] << 16, q[6] | q[7] << 16);
+}
+__device__ __noinline__ float scaled_wide_f32(float v, double sc) { return (float)((double)v * sc); }
+__device__ __forceinline__ float scaled(float v, Pair sc) {
+    const float p = v * sc.hi, ap = fabsf(p);
+    // (where the product's rest may lie below fp32's range)
+    if (!(ap > 1e-25f && ap < 1e37f)) return scaled_wide_f32(v, (double)sc.hi + (double)sc.lo);
+    return p + (fmaf(v, sc.hi, -p) + v * sc.lo);
+}
+
+// The tokens go to shared memory, normed where asked.
 template <typename T> __device__ __forceinline__ void stage_tokens(const Args &a, Plan &s, char *xs) {
-    const int stride = token_stride(a.d, sizeof(T)), per = a.d / 8;
-    if (a.norm) norm_scales<T>(a, s);
-    for (int i = threadIdx.x; i < a.R * per; i += kThr) {
-        const int r = i / per, c = (i - r * per) * 8;
-        const T *src = reinterpret_cast<const T *>(a.x) + (size_t)r * a.d + c;
-        T *dst = reinterpret_cast<T *>(xs + r * stride) + c;
-        float v[8];
-        load8(src, v);
-        if (sizeof(T) == 2) {
-            uint4 u = *reinterpret_cast<const uint4 *>(src);
-            if (a.norm) {
-                const double sc = s.scale[r];
-                const float scf = __double2float_rn(sc);
-                uint32_t q[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) q[j] = scaled_bf16(v[j], sc, scf);
-                u = make_uint4(q[0] | q[1] << 16, q[2] | q[3] << 16, q[4] | q[5] << 16,
-                               q[6] | q[7] << 16);
-            }
-            *reinterpret_cast<uint4 *>(dst) = u;
+    constexpr int kN = 16 / sizeof(T);
+    const int stride = token_stride(a.d, sizeof(T)), per = a.d / kN, all = a.R * per;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < all; i += kThr) {
+        const int r = i / per, c = i - r * per;
+        *reinterpret_cast<uint4 *>(xs + r * stride + 16 * c) =
+            *(reinterpret_cast<const uint4 *>(a.x) + i);
+    }
+    __syncthreads();
+    if (!a.norm) return;
+    norm_scales<T>(a, s, xs);
+    for (int i = threadIdx.x; i < all; i += kThr) {
+        const int r = i / per, c = i - r * per;
+        T *p = reinterpret_cast<T *>(xs + r * stride) + c * kN;
+        const Pair sc = s.scale[r];
+        const double *wide = s.wide[r] ? s.wide_scale + r : nullptr;
+        if constexpr (sizeof(T) == 2) {
+            scale16(reinterpret_cast<uint4 *>(p), sc, wide);
         } else {
-            if (a.norm) {
-                // the fp64 product, rounded once, from the scale as two fp32 values
-                const double sc = s.scale[r];
-                const float hi = __double2float_rn(sc), lo = (float)(sc - (double)hi);
-                const bool plain = hi < 1e18f;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float p = v[j] * hi, ap = fabsf(p);
-                    v[j] = plain && ap > 1e-25f && ap < 1e37f ? p + (fmaf(v[j], hi, -p) + v[j] * lo)
-                                                             : (float)((double)v[j] * sc);
-                }
-            }
-            float4 *o = reinterpret_cast<float4 *>(dst);
-            o[0] = make_float4(v[0], v[1], v[2], v[3]);
-            o[1] = make_float4(v[4], v[5], v[6], v[7]);
+            for (int j = 0; j < 4; ++j)
+                p[j] = wide ? scaled_wide_f32(p[j], *wide) : scaled(p[j], sc);
         }
     }
     __syncthreads();
@@ -274,82 +329,111 @@ template <> struct Eight<float> {
 // Scores of the CTA's experts, all tokens: the CTA's threads share an expert's row. first: the thread's
 // elements of the CTA's first row, on their way since the start.
 template <typename T>
-__device__ __forceinline__ void router(const Args &a, const char *xs, float *red, Eight<T> first) {
+__device__ __forceinline__ void router(const Args &a, const char *xs, float *red, Eight<T> first,
+                                       uint32_t tag) {
     const int stride = token_stride(a.d, sizeof(T));
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int e = blockIdx.x; e < a.E; e += gridDim.x) {
         const T *w = reinterpret_cast<const T *>(a.wr) + (size_t)e * a.d;
-        float acc[kMaxRows];
+        // four tokens at a time: code that runs once waits for its instructions
+#pragma unroll 1
+        for (int r0 = 0; r0 < a.R; r0 += 4) {
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+            for (int c = threadIdx.x * 8; c < a.d; c += kThr * 8) {
+                Eight<T> we = first;
+                if (e != blockIdx.x || c >= kThr * 8) we.load(w + c);
+                float wv[8];
+                we.get(wv);
 #pragma unroll
-        for (int r = 0; r < kMaxRows; ++r) acc[r] = 0.f;
-        for (int c = threadIdx.x * 8; c < a.d; c += kThr * 8) {
-            Eight<T> we = first;
-            if (e != blockIdx.x || c >= kThr * 8) we.load(w + c);
-            float wv[8];
-            we.get(wv);
+                for (int q = 0; q < 4; ++q) {
+                    if (r0 + q < a.R) {
+                        float xv[8];
+                        load8(reinterpret_cast<const T *>(xs + (r0 + q) * stride) + c, xv);
 #pragma unroll
-            for (int r = 0; r < kMaxRows; ++r) {
-                if (r < a.R) {
-                    float xv[8];
-                    load8(reinterpret_cast<const T *>(xs + r * stride) + c, xv);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) acc[r] = fmaf(wv[i], xv[i], acc[r]);
+                        for (int i = 0; i < 8; ++i) acc[q] = fmaf(wv[i], xv[i], acc[q]);
+                    }
                 }
             }
-        }
 #pragma unroll
-        for (int r = 0; r < kMaxRows; ++r) {
-            if (r < a.R) {
-                float v = acc[r];
+            for (int o = 16; o >= 1; o >>= 1)
 #pragma unroll
-                for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-                if (lane == 0) red[warp * kMaxRows + r] = v;
-            }
+                for (int q = 0; q < 4; ++q) acc[q] += __shfl_xor_sync(0xffffffffu, acc[q], o);
+            if (lane < 4 && r0 + lane < a.R)
+                red[warp * kMaxRows + r0 + lane] =
+                    lane == 0 ? acc[0] : lane == 1 ? acc[1] : lane == 2 ? acc[2] : acc[3];
         }
         __syncthreads();
         if (threadIdx.x < a.R) {
             float v = 0.f;
 #pragma unroll
             for (int i = 0; i < kWarps; ++i) v += red[i * kMaxRows + threadIdx.x];
-            a.logits[(size_t)threadIdx.x * a.E + e] = v;
+            const unsigned long long word = (unsigned long long)tag << 32 | __float_as_uint(v);
+            asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(a.scores + threadIdx.x * kMaxE + e),
+                         "l"(word)
+                         : "memory");
+            if (a.logits) a.logits[(size_t)threadIdx.x * a.E + e] = v;
         }
         __syncthreads();
     }
 }
 
 // Each token's k largest scores (ties to the lower expert), their softmax, and who chose whom.
-__device__ __forceinline__ void choose(const Args &a, Plan &s) {
+__device__ __forceinline__ void choose(const Args &a, Plan &s, uint32_t tag) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int e = threadIdx.x; e < kMaxE; e += kThr) s.tokens[e] = 0;
-    if (threadIdx.x == 0) s.n = 0;
-    __syncthreads();
     if (warp < a.R) {
-        const float *l = a.logits + (size_t)warp * a.E;
+        const unsigned long long *l = a.scores + warp * kMaxE, t0 = now_ns();
         uint32_t key[kMaxE / 32];
 #pragma unroll
-        for (int i = 0; i < kMaxE / 32; ++i) {
-            const int e = i * 32 + lane;
-            key[i] = 0;
-            if (e < a.E) {
-                const uint32_t b = __float_as_uint(__ldcg(l + e) + 0.f);
-                key[i] = max(1u, b ^ ((int)b < 0 ? 0xffffffffu : 0x80000000u));
+        for (int i = 0; i < kMaxE / 32; ++i) key[i] = 0;
+        for (unsigned tries = 1;; ++tries) {
+            bool here = true;
+#pragma unroll
+            for (int i = 0; i < kMaxE / 32; ++i) {
+                const int e = i * 32 + lane;
+                if (e < a.E && key[i] == 0) {
+                    const unsigned long long w = load_relaxed(l + e);
+                    if ((uint32_t)(w >> 32) == tag) {
+                        const uint32_t b = __float_as_uint(__uint_as_float((uint32_t)w) + 0.f);
+                        key[i] = max(1u, b ^ ((int)b < 0 ? 0xffffffffu : 0x80000000u));
+                    } else {
+                        here = false;
+                    }
+                }
+            }
+            if (__all_sync(0xffffffffu, here)) break;
+            if (tries % 256 == 0 && __any_sync(0xffffffffu, now_ns() - t0 > kPatience)) {
+                if (lane == 0) {
+                    atomicOr(a.flags, FLAG_WAIT_TIMEOUT);
+                    s.alive = 0;
+                }
+                break;
             }
         }
         float mine = -INFINITY, top = 0.f;  // lane j: the j-th chosen score
         int who = 0;
-        for (int j = 0; j < a.k; ++j) {
-            uint32_t best = 0;
-#pragma unroll
-            for (int i = 0; i < kMaxE / 32; ++i) best = max(best, key[i]);
-            best = __reduce_max_sync(0xffffffffu, best);
-            int e = kMaxE;
+        // the lane's largest, and its place; only the lane that loses it looks again
+        uint32_t own = 0;
+        int at = 0;
+        auto look = [&]() {
+            own = 0;
 #pragma unroll
             for (int i = kMaxE / 32 - 1; i >= 0; --i)
-                if (key[i] == best) e = i * 32 + lane;
-            e = (int)__reduce_min_sync(0xffffffffu, (unsigned)e);
+                if (key[i] >= own) {
+                    own = key[i];
+                    at = i;
+                }
+        };
+        look();
+        for (int j = 0; j < a.k; ++j) {
+            const uint32_t best = __reduce_max_sync(0xffffffffu, own);
+            const int e = (int)__reduce_min_sync(0xffffffffu, own == best ? (unsigned)(at * 32 + lane) : (unsigned)kMaxE);
+            if ((e & 31) == lane) {
 #pragma unroll
-            for (int i = 0; i < kMaxE / 32; ++i)
-                if (i * 32 + lane == e) key[i] = 0;
+                for (int i = 0; i < kMaxE / 32; ++i)
+                    if (i == at) key[i] = 0;
+                look();
+            }
             const float v = __uint_as_float(best ^ ((int)best < 0 ? 0x80000000u : 0xffffffffu));
             if (j == 0) top = v;
             if (lane == j) {
@@ -374,28 +458,31 @@ __device__ __forceinline__ void choose(const Args &a, Plan &s) {
         }
     }
     __syncthreads();
-    if (warp == 0) {
-        int n = 0;
-#pragma unroll
-        for (int i = 0; i < kMaxE / 32; ++i) {
-            const int e = i * 32 + lane;
-            bool on = e < a.E && s.tokens[e];
-            int slot = e;
-            if (on && a.slot) slot = a.slot[e];
-            if (on && (slot < 0 || slot >= a.slots)) {
-                on = false;
-                if (blockIdx.x == 0) atomicOr(a.flags, FLAG_BAD_EXPERT);
-            }
-            const uint32_t m = __ballot_sync(0xffffffffu, on);
-            if (on) {
-                const int at = n + __popc(m & ((1u << lane) - 1));
-                s.expert[at] = (short)e;
-                s.slot[at] = slot;
-            }
-            n += __popc(m);
-        }
-        if (lane == 0) s.n = n;
+    // a warp for 32 experts
+    const int e = threadIdx.x;
+    int slot = e;
+    bool on = e < a.E && s.tokens[e];
+    if (on && a.slot) slot = a.slot[e];
+    if (on && (slot < 0 || slot >= a.slots)) {
+        on = false;
+        if (blockIdx.x == 0) atomicOr(a.flags, FLAG_BAD_EXPERT);
     }
+    const uint32_t m = __ballot_sync(0xffffffffu, on);
+    if (warp < kMaxE / 32 && lane == 0) s.word[warp] = m;
+    __syncthreads();
+    int before = 0, n = 0;
+#pragma unroll
+    for (int i = 0; i < kMaxE / 32; ++i) {
+        const int c = __popc(s.word[i]);
+        if (i < warp) before += c;
+        n += c;
+    }
+    if (on) {
+        const int at = before + __popc(m & ((1u << lane) - 1));
+        s.expert[at] = (short)e;
+        s.slot[at] = slot;
+    }
+    if (threadIdx.x == 0) s.n = n;
     __syncthreads();
 }
 
@@ -454,8 +541,8 @@ __device__ __forceinline__ void store_y(const Args &a, int r, int col, float v) 
 // read itself, so a warp waits for no other thread. The copies of step 3's first entries, which do
 // not depend on step 2, are on their way while the CTA ends step 2 and waits at the grid's barrier.
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool on) {
-    const int n = on ? 16 : 0;  // (0: the 16 bytes become zeros, nothing is read)
+// n: 16, or 0: the 16 bytes become zeros and nothing is read.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, int n) {
     asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
                  : "memory");
 }
@@ -468,184 +555,225 @@ __device__ __forceinline__ uint4 shared16(uint32_t p) {
     return v;
 }
 
-// The entries of step 2: the CTA's share of the rows (pairs of a gate and an up row, over all chosen
-// experts), in runs of one expert, tiles of 8 pairs, and the warp's part of the inner dimension.
-struct GateUp {
-    long long p, p1;
-    int kc0, kc1, ui, j0, nj, tiles, tile, kc, m;
-    const __nv_bfloat16 *wg, *wu;
-    __device__ __forceinline__ void run(const Args &a, const Plan &s) {
-        if (p >= p1) return;
+// Step 2's work: the CTA's share of the pairs (a gate and an up row) over all chosen experts, in runs of
+// one expert whose partial sums fit a buffer, of tiles of 8 pairs.
+struct Run {
+    int ui, j0, nj, tiles, m;
+    unsigned mask;
+    __device__ __forceinline__ Run(const Args &a, const Plan &s, long long p, long long p1) {
         ui = (int)(p / a.f);
         j0 = (int)(p - (long long)ui * a.f);
-        m = __popc(s.tokens[s.expert[ui]]);
+        mask = s.tokens[s.expert[ui]];
+        m = __popc(mask);
         const int most = kRedBytes / (kWarps * 16 * 4 * m);
         nj = (int)min(min((long long)(a.f - j0), p1 - p), 8ll * most);
         tiles = (nj + 7) / 8;
-        const size_t at = ((size_t)s.slot[ui] * a.f + j0) * a.d;
-        wg = reinterpret_cast<const __nv_bfloat16 *>(a.wg) + at;
-        wu = reinterpret_cast<const __nv_bfloat16 *>(a.wu) + at;
-    }
-    __device__ __forceinline__ void start(const Args &a, const Plan &s, int warp) {
-        const long long pairs = (long long)s.n * a.f;
-        p = pairs * blockIdx.x / gridDim.x;
-        p1 = pairs * (blockIdx.x + 1) / gridDim.x;
-        // (a warp without a part has one entry of zeros a tile)
-        const int nk = (a.d + 31) / 32;
-        kc0 = warp * nk / kWarps;
-        kc1 = max(kc0 + 1, (warp + 1) * nk / kWarps);
-        kc = kc0;
-        tile = 0;
-        run(a, s);
-    }
-    __device__ __forceinline__ bool more() const { return p < p1; }
-    // (the inner elements behind a part of none belong to the next warp)
-    __device__ __forceinline__ bool mine(const Args &a, int warp) const {
-        return (warp + 1) * ((a.d + 31) / 32) / kWarps > kc0;
-    }
-    __device__ __forceinline__ bool last_of_tile() const { return kc + 1 == kc1; }
-    __device__ __forceinline__ bool last_of_run() const { return last_of_tile() && tile + 1 == tiles; }
-    __device__ __forceinline__ void next(const Args &a, const Plan &s) {
-        if (++kc < kc1) return;
-        kc = kc0;
-        if (++tile < tiles) return;
-        tile = 0;
-        p += nj;
-        run(a, s);
-    }
-    __device__ __forceinline__ void copy(const Args &a, uint32_t at, bool mine) const {
-        const int lane = threadIdx.x & 31, j = tile * 8 + (lane >> 2), c = kc * 32 + 8 * (lane & 3);
-        const bool on = mine && j < nj && c < a.d;
-        const size_t row = on ? (size_t)j * a.d + c : 0;
-        copy16(at, wg + row, on);
-        copy16(at + 512, wu + row, on);
     }
 };
-
-// The entries of step 3: tiles of up to 16 of the CTA's output columns, and the warp's part of the
-// inner dimension, which runs over all chosen experts.
-struct Down {
-    int c0, c1, tiles, tile, q0, q1, q, nk, ui, kc, first_ui, first_kc, b0, b1;
-    __device__ __forceinline__ void columns() {
-        b0 = c0 + (c1 - c0) * tile / tiles;
-        b1 = c0 + (c1 - c0) * (tile + 1) / tiles;
-    }
-    __device__ __forceinline__ void start(const Args &a, const Plan &s, int warp) {
+__device__ __forceinline__ long long first_pair(const Args &a, const Plan &s, int cta) {
+    return (long long)s.n * a.f * cta / gridDim.x;
+}
+// The warp's part of n groups of 32 inner elements.
+__device__ __forceinline__ int part(int n, int warp) { return (int)((long long)n * warp / kWarps); }
+__device__ __forceinline__ int groups(int n) { return (n + 31) / 32; }
+// Step 3's work: the CTA's output columns, in tiles of up to 16.
+struct Columns {
+    int c0, c1, tiles;
+    __device__ __forceinline__ Columns(const Args &a) {
         c0 = (int)((long long)a.d * blockIdx.x / gridDim.x);
         c1 = (int)((long long)a.d * (blockIdx.x + 1) / gridDim.x);
         tiles = (c1 - c0 + 15) / 16;
-        nk = (a.f + 31) / 32;
-        const int all = s.n * nk;
-        q0 = (int)((long long)all * warp / kWarps);
-        q1 = (int)((long long)all * (warp + 1) / kWarps);
-        first_ui = q0 / nk;
-        first_kc = q0 - first_ui * nk;
-        tile = 0;
-        back();
-        if (tiles) columns();
     }
-    __device__ __forceinline__ void back() {
-        q = q0;
-        ui = first_ui;
-        kc = first_kc;
+    __device__ __forceinline__ int at(int tile) const { return c0 + (c1 - c0) * tile / tiles; }
+};
+
+// What a warp copies, entry after entry: first step 2's, then step 3's. A segment is a run of entries
+// along the inner dimension of the same 16 rows; inside it a lane's addresses only advance. Step 3's
+// entries have the activations of the same inner elements in a second ring.
+template <int D> struct Feed {
+    const Args &a;
+    const Plan &s;
+    uint32_t base, put;  // the lane's bytes of entry 0, offset of the next entry
+    uint32_t acts;       // from the weights' ring to the activations'
+    // the segment, as the lane sees it
+    const __nv_bfloat16 *x, *y, *h;  // two rows of weights, and of activations
+    int c, end, left;                // inner element, where the rows end, entries left
+    int nx, ny, nh;                  // bytes of a copy, or 0
+    // where the segments come from
+    long long pair, pair1;
+    int tile, tiles, nj, ui, j0, q;
+    bool down, done;
+
+    __device__ __forceinline__ Feed(const Args &a_, const Plan &s_, const char *ring, const char *h_ring)
+        : a(a_), s(s_) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        base = (uint32_t)__cvta_generic_to_shared(ring) + warp * D * 1024 + lane * 16;
+        acts = (uint32_t)(h_ring - ring);
+        put = 0;
+        pair = first_pair(a, s, blockIdx.x);
+        pair1 = first_pair(a, s, blockIdx.x + 1);
+        nj = tiles = left = 0;
+        tile = -1;
+        down = done = false;
+        segment();
     }
-    __device__ __forceinline__ bool more() const { return q < q1 && tile < tiles; }
-    __device__ __forceinline__ void step() {
-        ++q;
-        if (++kc == nk) {
-            kc = 0;
-            ++ui;
+    // Activations of the lane's column of an expert, from element c on: the expert's g-th token's.
+    __device__ __forceinline__ const __nv_bfloat16 *activations(int ui, int col, int c) const {
+        const int e = s.expert[ui];
+        const unsigned mask = s.tokens[e];
+        const int r = nth_token(mask, col < __popc(mask) ? col : 0);
+        return reinterpret_cast<const __nv_bfloat16 *>(a.h) +
+               (size_t)(r * a.k + s.place[e][r]) * 2 * a.f + c;
+    }
+    __device__ __forceinline__ int columns(int ui) const { return __popc(s.tokens[s.expert[ui]]); }
+    // The next segment (left > 0), or done.
+    __device__ __forceinline__ void segment() {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+        if (!down) {
+            const int k0 = part(groups(a.d), warp), k1 = part(groups(a.d), warp + 1);
+            if (++tile >= tiles) {
+                pair += nj;
+                tile = 0;
+                if (pair >= pair1 || k0 == k1) {  // (a warp without a part has no entries)
+                    down = true;
+                    q = part(s.n * groups(a.f), warp);
+                    tiles = Columns(a).tiles;
+                } else {
+                    const Run r(a, s, pair, pair1);
+                    tiles = r.tiles;
+                    nj = r.nj;
+                    ui = r.ui;
+                    j0 = r.j0;
+                }
+            }
+            if (!down) {
+                const int j = tile * 8 + g;
+                const bool on = j < nj;
+                nx = ny = on ? 16 : 0;
+                c = k0 * 32 + 8 * t;
+                end = a.d;
+                left = k1 - k0;
+                const size_t at = ((size_t)s.slot[ui] * a.f + j0 + (on ? j : 0)) * a.d + c;
+                x = reinterpret_cast<const __nv_bfloat16 *>(a.wg) + at;
+                y = reinterpret_cast<const __nv_bfloat16 *>(a.wu) + at;
+                return;
+            }
         }
+        const int nk = groups(a.f), q0 = part(s.n * nk, warp), q1 = part(s.n * nk, warp + 1);
+        if (q >= q1) {
+            q = q0;
+            ++tile;
+        }
+        if (q0 == q1 || tile >= tiles) {
+            done = true;
+            return;
+        }
+        const Columns cols(a);
+        const int e = q / nk, k0 = q - e * nk, col = cols.at(tile) + g, last = cols.at(tile + 1);
+        left = min(nk - k0, q1 - q);
+        q += left;
+        nx = col < last ? 16 : 0;
+        ny = col + 8 < last ? 16 : 0;
+        c = k0 * 32 + 8 * t;
+        end = a.f;
+        x = reinterpret_cast<const __nv_bfloat16 *>(a.wd) +
+            ((size_t)s.slot[e] * a.d + (nx ? col : 0)) * a.f + c;
+        y = ny ? x + 8ll * a.f : x;
+        h = activations(e, g, c);
+        nh = g < columns(e) ? 16 : 0;
     }
-    __device__ __forceinline__ void next() {
-        step();
-        if (q < q1) return;
-        back();
-        if (++tile < tiles) columns();
+    template <bool H> __device__ __forceinline__ void fill() {
+        if (!done) {
+            const bool in = c < end;
+            copy16(base + put, x, in ? nx : 0);
+            copy16(base + put + 512, y, in ? ny : 0);
+            if (H && in && nh) {
+                copy16(base + put + acts, h, 16);
+                copy16(base + put + acts + 512, h + a.f, 16);
+            }
+            x += 32;
+            y += 32;
+            h += 32;
+            c += 32;
+            if (--left == 0) segment();
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        put = put + 1024 == D * 1024 ? 0 : put + 1024;
     }
-    __device__ __forceinline__ void copy(const Args &a, const Plan &s, uint32_t at) const {
-        const int lane = threadIdx.x & 31, col = b0 + (lane >> 2), c = kc * 32 + 8 * (lane & 3);
-        const __nv_bfloat16 *w = reinterpret_cast<const __nv_bfloat16 *>(a.wd) +
-                                 (size_t)s.slot[ui] * a.d * a.f;
-        const bool x = c < a.f && col < b1, y = c < a.f && col + 8 < b1;
-        copy16(at, x ? w + (size_t)col * a.f + c : w, x);
-        copy16(at + 512, y ? w + (size_t)(col + 8) * a.f + c : w, y);
+    // The activations of the entries of step 3 that were copied before there were any.
+    __device__ __forceinline__ void catch_up(uint32_t take) const {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+        const int nk = groups(a.f), q0 = part(s.n * nk, warp), q1 = part(s.n * nk, warp + 1);
+        const int entries = (q1 - q0) * Columns(a).tiles;
+#pragma unroll 1
+        for (int i = 0; i < D - 1; ++i) {
+            if (i < entries) {
+                const int q = q0 + i % (q1 - q0), e = q / nk, c = (q - e * nk) * 32 + 8 * t;
+                const __nv_bfloat16 *p = activations(e, g, c);
+                if (c < a.f && g < columns(e)) {
+                    copy16(base + take + acts, p, 16);
+                    copy16(base + take + acts + 512, p + a.f, 16);
+                }
+                take = take + 1024 == D * 1024 ? 0 : take + 1024;
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
     }
 };
 
-// NT: groups of 8 tokens; D: entries of a warp's ring.
-template <int NT, int D> struct Ring {
+// Steps 2 and 3. NT: groups of 8 tokens; D: entries of a warp's ring.
+template <int NT, int D> struct Experts {
     const Args &a;
     Plan &s;
-    GateUp load1, use1;
-    Down load2;
-    bool mine1;
-    uint32_t base;    // the lane's bytes of entry 0
-    int put, take;    // entries
+    Feed<D> feed;
+    uint32_t take;
 
-    __device__ __forceinline__ Ring(const Args &a_, Plan &s_, const char *ring) : a(a_), s(s_) {
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        base = (uint32_t)__cvta_generic_to_shared(ring) + warp * D * 1024 + lane * 16;
-        put = take = 0;
-        load1.start(a, s, warp);
-        use1 = load1;
-        mine1 = load1.mine(a, warp);
-        load2.start(a, s, warp);
+    __device__ __forceinline__ Experts(const Args &a_, Plan &s_, const char *ring, const char *h_ring)
+        : a(a_), s(s_), feed(a_, s_, ring, h_ring), take(0) {
 #pragma unroll 1
-        for (int i = 0; i < D - 1; ++i) fill();
+        for (int i = 0; i < D - 1; ++i) feed.template fill<false>();
     }
-    // The next entry's copies, of step 2 or, when they are all on their way, of step 3.
-    __device__ __forceinline__ void fill() {
-        const uint32_t at = base + put * 1024;
-        if (load1.more()) {
-            load1.copy(a, at, mine1);
-            load1.next(a, s);
-        } else if (load2.more()) {
-            load2.copy(a, s, at);
-            load2.next();
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        put = put + 1 == D ? 0 : put + 1;
-    }
-    // The oldest entry's operands; its place is filled again by the next fill().
-    __device__ __forceinline__ void get(uint4 &x, uint4 &y) {
+    // The oldest entry's address; its place is filled again by the next fill().
+    __device__ __forceinline__ uint32_t get() {
         asm volatile("cp.async.wait_group %0;" ::"n"(D - 2) : "memory");
-        const uint32_t at = base + take * 1024;
-        x = shared16(at);
-        y = shared16(at + 512);
-        take = take + 1 == D ? 0 : take + 1;
+        const uint32_t at = feed.base + take;
+        take = take + 1024 == D * 1024 ? 0 : take + 1024;
+        return at;
     }
 
     __device__ __forceinline__ void gate_up(const char *xs, float *red) {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
         const int stride = token_stride(a.d, 2);
-        int buf = 0, run = -1;
-        unsigned mask = 0;
-        const char *x0 = nullptr, *x1 = nullptr;
-        float c0[4] = {0.f, 0.f, 0.f, 0.f}, c1[4] = {0.f, 0.f, 0.f, 0.f};
-        while (use1.more()) {
-            const int m = use1.m;
-            if (use1.ui != run) {  // this lane's columns: tokens g and g + 8 of the expert's
-                run = use1.ui;
-                mask = s.tokens[s.expert[run]];
-                x0 = g < m ? xs + nth_token(mask, g) * stride : nullptr;
-                x1 = g + 8 < m ? xs + nth_token(mask, g + 8) * stride : nullptr;
-            }
-            uint4 x, y, b = make_uint4(0, 0, 0, 0);
-            const int c = use1.kc * 32 + 8 * t;
-            const bool in = c < a.d;
-            get(x, y);
-            fill();
-            if (in && x0) b = *reinterpret_cast<const uint4 *>(x0 + 2 * c);
-            mma32(c0, x, y, b);
-            if (NT > 1 && m > 8) {
-                b = make_uint4(0, 0, 0, 0);
-                if (in && x1) b = *reinterpret_cast<const uint4 *>(x1 + 2 * c);
-                mma32(c1, x, y, b);
-            }
-            if (use1.last_of_tile()) {
-                float *out = red + buf * (kRedBytes / 4);
-                float *o = out + ((size_t)(warp * use1.tiles + use1.tile) * 16 + g) * m;
+        const int k0 = part(groups(a.d), warp), k1 = part(groups(a.d), warp + 1);
+        const long long p1 = first_pair(a, s, blockIdx.x + 1);
+        int buf = 0;
+#pragma unroll 1
+        for (long long p = first_pair(a, s, blockIdx.x); p < p1;) {
+            const Run r(a, s, p, p1);
+            const int m = r.m;
+            float *out = red + buf * (kRedBytes / 4);
+            // this lane's columns: tokens g and g + 8 of the expert's
+            const char *x0 = g < m ? xs + nth_token(r.mask, g) * stride : nullptr;
+            const char *x1 = g + 8 < m ? xs + nth_token(r.mask, g + 8) * stride : nullptr;
+#pragma unroll 1
+            for (int tile = 0; tile < r.tiles; ++tile) {
+                float c0[4] = {0.f, 0.f, 0.f, 0.f}, c1[4] = {0.f, 0.f, 0.f, 0.f};
+                int c = k0 * 32 + 8 * t;
+#pragma unroll 1
+                for (int k = k0; k < k1; ++k, c += 32) {
+                    const uint32_t at = get();
+                    const uint4 x = shared16(at), y = shared16(at + 512);
+                    uint4 b = make_uint4(0, 0, 0, 0);
+                    if (x0 && c < a.d) b = *reinterpret_cast<const uint4 *>(x0 + 2 * c);
+                    feed.template fill<false>();
+                    mma32(c0, x, y, b);
+                    if (NT > 1 && m > 8) {
+                        b = make_uint4(0, 0, 0, 0);
+                        if (x1 && c < a.d) b = *reinterpret_cast<const uint4 *>(x1 + 2 * c);
+                        mma32(c1, x, y, b);
+                    }
+                }
+                float *o = out + ((size_t)(warp * r.tiles + tile) * 16 + g) * m;
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     const int col = 2 * t + q;
@@ -658,96 +786,76 @@ template <int NT, int D> struct Ring {
                         o[8 * m + col + 8] = c1[2 + q];
                     }
                 }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) c0[i] = c1[i] = 0.f;
-                if (use1.last_of_run()) {
-                    __syncthreads();
-                    finish_gate_up<__nv_bfloat16>(a, s, out, use1.tiles, s.expert[run], use1.j0,
-                                                  use1.nj, mask, m);
-                    buf ^= 1;  // (a buffer is written again after the CTA's next barrier)
-                }
             }
-            use1.next(a, s);
-        }
-    }
-
-    // The activations that an entry's columns are multiplied with.
-    __device__ __forceinline__ void activations(int ui, int kc, uint4 (&hi)[NT], uint4 (&lo)[NT]) const {
-        const int lane = threadIdx.x & 31, g = lane >> 2, c = kc * 32 + 8 * (lane & 3);
-        const int e = s.expert[ui];
-        const unsigned mask = s.tokens[e];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            hi[n] = lo[n] = make_uint4(0, 0, 0, 0);
-            const int r = g + 8 * n;
-            if (c < a.f && (mask >> r & 1)) {
-                const __nv_bfloat16 *p = reinterpret_cast<const __nv_bfloat16 *>(a.h) +
-                                         (size_t)(r * a.k + s.place[e][r]) * 2 * a.f + c;
-                hi[n] = l2_16(p);
-                lo[n] = l2_16(p + a.f);
-            }
+            __syncthreads();
+            finish_gate_up<__nv_bfloat16>(a, s, out, r.tiles, s.expert[r.ui], r.j0, r.nj, r.mask, m);
+            buf ^= 1;  // (a buffer is written again after the CTA's next barrier)
+            p += r.nj;
         }
     }
 
     __device__ __forceinline__ void down(float *red) {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-        Down use;
-        use.start(a, s, warp);
-        for (; use.tile < use.tiles;) {
-            float acc[NT][4], sum[NT][4];
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[n][i] = sum[n][i] = 0.f;
-            const int b0 = use.b0, b1 = use.b1;
-            // activations are asked for two entries ahead
-            Down ahead = use;
-            uint4 hi[2][NT], lo[2][NT];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                if (ahead.q < use.q1) activations(ahead.ui, ahead.kc, hi[i], lo[i]);
-                ahead.step();
-            }
-            while (use.q < use.q1) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    if (use.q < use.q1) {
-                        uint4 x, y;
-                        get(x, y);
-                        fill();
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            mma32(acc[n], x, y, hi[i][n]);
-                            mma32(acc[n], x, y, lo[i][n]);
+        float *mine = red + (size_t)warp * 16 * kMaxRows;
+        const Columns cols(a);
+        const int nk = groups(a.f), q0 = part(s.n * nk, warp), q1 = part(s.n * nk, warp + 1);
+        feed.catch_up(take);
+#pragma unroll 1
+        for (int tile = 0; tile < cols.tiles; ++tile) {
+            const int b0 = cols.at(tile), b1 = cols.at(tile + 1);
+            for (int i = lane; i < 16 * kMaxRows; i += 32) mine[i] = 0.f;
+            __syncwarp();
+            int ui = q0 / nk;
+#pragma unroll 1
+            for (int q = q0; q < q1; ++ui) {
+                const int last = min(q1, (ui + 1) * nk);
+                const unsigned mask = s.tokens[s.expert[ui]];
+                const int m = __popc(mask);
+                // products with the values and with their rests (two chains), and of tokens past the 8th
+                float hi[4] = {0.f, 0.f, 0.f, 0.f}, lo[4] = {0.f, 0.f, 0.f, 0.f};
+                float more[4] = {0.f, 0.f, 0.f, 0.f};
+                int c = (q - ui * nk) * 32 + 8 * t;
+#pragma unroll 1
+                for (; q < last; ++q, c += 32) {
+                    const uint32_t at = get();
+                    const uint4 x = shared16(at), y = shared16(at + 512);
+                    uint4 u = make_uint4(0, 0, 0, 0), v = u;
+                    if (g < m && c < a.f) {
+                        u = shared16(at + feed.acts);
+                        v = shared16(at + feed.acts + 512);
+                    }
+                    feed.template fill<true>();
+                    mma32(hi, x, y, u);
+                    mma32(lo, x, y, v);
+                    if (NT > 1 && m > 8) {
+                        // (an expert of more than 8 tokens: the others' are read here and now)
+                        const __nv_bfloat16 *p = feed.activations(ui, g + 8, c);
+                        u = v = make_uint4(0, 0, 0, 0);
+                        if (g + 8 < m && c < a.f) {
+                            u = l2_16(p);
+                            v = l2_16(p + a.f);
                         }
-                        if (ahead.q < use.q1) activations(ahead.ui, ahead.kc, hi[i], lo[i]);
-                        ahead.step();
-                        const int ui = use.ui;
-                        use.step();
-                        if (use.ui != ui || use.q == use.q1) {
-                            // the expert's sums count for the tokens that chose it only (its
-                            // weights may hold what times zero is not zero)
-                            const unsigned mask = s.tokens[s.expert[ui]];
-#pragma unroll
-                            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) {
-                                    if (mask >> (n * 8 + 2 * t + (j & 1)) & 1) sum[n][j] += acc[n][j];
-                                    acc[n][j] = 0.f;
-                                }
-                        }
+                        mma32(more, x, y, u);
+                        mma32(more, x, y, v);
                     }
                 }
+                // the warp's part of the expert is done: its columns are tokens
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int col = 2 * t + k;
+                    if (col < m) {
+                        float *o = mine + g * kMaxRows + nth_token(mask, col);
+                        o[0] += hi[k] + lo[k];
+                        o[8 * kMaxRows] += hi[2 + k] + lo[2 + k];
+                    }
+                    if (NT > 1 && col + 8 < m) {
+                        float *o = mine + g * kMaxRows + nth_token(mask, col + 8);
+                        o[0] += more[k];
+                        o[8 * kMaxRows] += more[2 + k];
+                    }
+                }
+                __syncwarp();
             }
-            use.back();
-            if (++use.tile < use.tiles) use.columns();
-            __syncthreads();  // (the tile before is read out)
-            float *o = red + (size_t)warp * 16 * kMaxRows;
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    o[(g + 8 * (i >> 1)) * kMaxRows + n * 8 + 2 * t + (i & 1)] = sum[n][i];
             __syncthreads();
             for (int i = threadIdx.x; i < (b1 - b0) * a.R; i += kThr) {
                 const int r = i / (b1 - b0), col = i - r * (b1 - b0);
@@ -756,6 +864,7 @@ template <int NT, int D> struct Ring {
                 for (int w = 0; w < kWarps; ++w) v += red[(size_t)(w * 16 + col) * kMaxRows + r];
                 store_y<__nv_bfloat16>(a, r, b0 + col, v);
             }
+            __syncthreads();  // (the sums are read before the next tile's)
         }
     }
 };
@@ -854,19 +963,27 @@ __global__ void __launch_bounds__(kThr, 1) few_kernel(const Args a) {
     Eight<T> first{};
     if (blockIdx.x < a.E && threadIdx.x * 8 < a.d)
         first.load(reinterpret_cast<const T *>(a.wr) + (size_t)blockIdx.x * a.d + threadIdx.x * 8);
+    if (threadIdx.x < kMaxE) s.tokens[threadIdx.x] = 0;
+    if (threadIdx.x == 0) {
+        // (no CTA counts this launch as ended before this one has come to the barrier)
+        s.launch = load_relaxed(a.barrier) >> 16;
+        s.alive = 1;
+    }
     stage_tokens<T>(a, s, xs);
-    router<T>(a, xs, red, first);
-    if (!grid_barrier(a, s)) return;
-    choose(a, s);
+    const unsigned long long launch = s.launch;
+    const uint32_t tag = (uint32_t)launch + 1;
+    router<T>(a, xs, red, first, tag);
+    choose(a, s, tag);
+    if (!s.alive) return;
     if constexpr (D > 0) {
-        Ring<NT, D> r(a, s, ring);
+        Experts<NT, D> r(a, s, ring, xs);
         r.gate_up(xs, red);
-        const bool alive = grid_barrier(a, s);
+        const bool alive = grid_barrier(a, s, launch);
         if (alive) r.down(red);
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
         gate_up(a, s, xs);
-        if (!grid_barrier(a, s)) return;
+        if (!grid_barrier(a, s, launch)) return;
         down(a, s);
     }
 }
@@ -879,7 +996,9 @@ template <typename T, int NT, int D> cudaError_t launch(const Args &a, int max_c
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(max_ctas > 0 ? std::min(max_ctas, sms) : sms);
     cfg.blockDim = dim3(kThr);
-    cfg.dynamicSmemBytes = (size_t)kFixed + ring_bytes(D) + (size_t)a.R * token_stride(a.d, sizeof(T));
+    // (step 3's activations take the tokens' place)
+    cfg.dynamicSmemBytes = (size_t)kFixed + ring_bytes(D) +
+                           std::max(ring_bytes(D), a.R * token_stride(a.d, sizeof(T)));
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeCooperative;
@@ -889,7 +1008,7 @@ template <typename T, int NT, int D> cudaError_t launch(const Args &a, int max_c
     return cudaLaunchKernelEx(&cfg, few_kernel<T, NT, D>, a);
 }
 
-constexpr int kShallow = 4, kDeep = 8;
+constexpr int kShallow = 4, kDeep = 5;
 
 }  // namespace
 
@@ -898,6 +1017,8 @@ int rows_at_once(const moe_layer_desc &L) {
     return std::min(kMaxRows, (kSmem - kFixed - (L.dtype == MOE_DTYPE_F32 ? 0 : ring_bytes(kShallow))) /
                                   token_stride(L.d, e));
 }
+
+static_assert(kHeadBytes == MOE_FEW_HEAD_BYTES, "the header says how much is zeroed");
 
 cudaError_t launch_few(const Args &a, int dtype, int max_ctas, cudaStream_t s) {
     using bf16 = __nv_bfloat16;

@@ -644,9 +644,12 @@ def moe_block_norm(L, x, branch=None, h=None, hn=None, w_post=None, gate=None, g
 
 # ------------------------------------------------------------- a decoding round's other calls
 
-def _zeroed(n: int, device) -> torch.Tensor:
+MOE_FEW_HEAD_BYTES = 36864
+
+
+def _zeroed(n: int, device, head: int = 4096) -> torch.Tensor:
     ws = torch.empty(n, dtype=torch.uint8, device=device)
-    ws[:4096].zero_()
+    ws[:head].zero_()
     return ws
 
 
@@ -659,7 +662,7 @@ def few_workspace(L: LayerDesc, R: int, device="cuda") -> torch.Tensor:
     n = moe_few_workspace_bytes(L, R)
     if n == 0:
         raise MoeError("moe_few_workspace_bytes", MOE_ERR_ARG)
-    return _zeroed(n, device)
+    return _zeroed(n, device, MOE_FEW_HEAD_BYTES)
 
 
 def moe_few_forward(L, x, W_r, W_gate, W_up, W_down, slot_of_expert, y, ws, logits=None,

@@ -562,10 +562,10 @@ moe_status moe_block_norm(const moe_layer_desc *L, const void *x, const void *br
  * What a round needs beside the tree's layer and attention. */
 
 /* Bytes of workspace of moe_few_forward for up to R tokens (1 .. 16); 0 for a bad descriptor.
- * Like the attention's workspace, its first 4096 bytes must be zero before the first call that
- * gets it (check word and grid barrier), and again after a call whose check word has bit 1; the
- * rest is scratch. Two calls that overlap in time must use different workspaces, captured graphs
+ * Its first MOE_FEW_HEAD_BYTES must be zero before the first call that gets it (check word, grid
+ * barrier, scores), and again after a call whose check word has bit 1; the rest is scratch. Two calls that overlap in time must use different workspaces, captured graphs
  * that may run at the same time too. */
+#define MOE_FEW_HEAD_BYTES 36864
 size_t moe_few_workspace_bytes(const moe_layer_desc *L, int R);
 
 /* The whole layer for a few tokens in one launch ("MoE and speculative decoding" blog, "starting
