@@ -11,7 +11,14 @@
 // polynomial carried as pairs of fp32 values; off by some 2^-42 relative, checked against 64 bits),
 // and sums are 64-bit integers: exact, and the same in any order.
 //
-// A cluster of CTAs holds a row in shared memory, which reads it once. Cuts are found by histograms of
+// A cluster of CTAs holds a row in shared memory, which reads it once.
+//
+// Every cut keeps the first tokens of the descending order, so what is kept lies among the largest
+// ones, of which there are few as a rule: a bound from below on the last of them (for top-k, the k-th
+// largest of the threads' own largest values, up to a bin; for min-p its own) lets a second pass collect
+// them, and one CTA sorts them and does the rest. top-p needs the whole weight too; a sum of fp32
+// exponentials, off by at most 2^-15, decides unless a cut lies within that.
+// Where more is kept than a list holds (flat distributions, no cuts), cuts are found by histograms of
 // the row's live values (weights that are not below 2^-43) over bins that descend with the value:
 // counts for top-k, weights for top-p; the bin that a cut falls in is divided by the bits of the
 // values until one value is left, and ties are taken in the order of the tokens.
@@ -93,6 +100,12 @@ __device__ __forceinline__ u64 weight(const Scale &s, float l, const float2 *pow
     return w > 0 ? (u64)w : 0;
 }
 
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // Values in the order of their keys (NaN and -0 do not occur).
 __device__ __forceinline__ uint32_t key_of(float l) {
     const uint32_t b = __float_as_uint(l);
@@ -165,9 +178,22 @@ template <> struct Block<__nv_bfloat16> {
     }
 };
 
+constexpr int kList = 512;           // tokens of a list
+constexpr int kListK = 384;          // of them asked for (the bins' last may hold more)
+constexpr int kGuess = 256;          // where only top-p cuts: as many of the largest are tried
+constexpr float kSumError = 0x1p-15f;
+
 struct Shared {
     float2 powers[256];
-    uint32_t lo[kBins], hi[kBins];
+    union {
+        struct {
+            uint32_t lo[kBins], hi[kBins];
+        };
+        struct {
+            uint32_t list_key[kList], list_index[kList];
+            u64 sorted[kList];  // ~key, index: ascending
+        };
+    };
     u64 part[kWarps];
     float red_f[kWarps];
     uint32_t red_a[kWarps], red_b[kWarps];
@@ -176,6 +202,9 @@ struct Shared {
     uint32_t kmin, kmax, index;
     u64 wsum[kWarps];
     uint32_t ties[kWarps];
+    uint32_t listed;
+    float sum;
+    int settled;
     // found by one thread
     int bin;
     u64 before;
@@ -207,6 +236,13 @@ __device__ __forceinline__ u64 block_scan(u64 v, u64 *part, u64 *total) {
     }
     *total = all;
     return before + s - v;
+}
+
+// log of the share that a token of logit l has of the sum z.
+__device__ __forceinline__ float log_share(float l, float top, float temp, u64 z) {
+    const float lz = z < 2 * kOne ? log1pf((float)(long long)(z - kOne) * 0x1p-43f)
+                                  : logf((float)z * 0x1p-43f);
+    return (l - top) / temp - lz;
 }
 
 // What is kept of a row: values of keys above `key`, and the first `ties` tokens of that key.
@@ -324,6 +360,138 @@ template <typename T> struct Sampler {
         }
         __syncthreads();
         return target <= total;
+    }
+
+    // Samples from a list of the row's largest tokens. own: the thread's largest value. False (for the
+    // whole cluster) where the list does not hold all that may be kept.
+    __device__ __forceinline__ bool from_list(const Args &a, int r, int k, float top_p,
+                                              uint32_t low_key, float own, float u, float temp) {
+        const int ctas = cl.num_blocks(), rank = cl.block_rank();
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        const bool by_p = top_p < 1.f, whole = by_p && !k;  // top-p of the whole row's weight
+        int last = kBins - 1;  // bins up to this one are listed
+        if (k || !low_key) {
+            clear();
+            if (is_live(sc, own))
+                atomicAdd(&sh.lo[min(kBins - 1, (int)(octaves(sc, own) * kBinScale))], 1u);
+            share();
+            if (find(k ? k : kGuess)) last = sh.bin;
+            __syncthreads();  // (the list takes the bins' place)
+        }
+        float sum = 0.f;
+        auto listed = [&](float l) {
+            return is_live(sc, l) && min(kBins - 1, (int)(octaves(sc, l) * kBinScale)) <= last &&
+                   (k || key_of(l) >= low_key);
+        };
+        for (int j0 = row.w0; j0 < row.w1; j0 += 32) {
+            const int j = j0 + lane;
+            if (j >= row.w1) continue;
+            const Block<T> b = row.block(j);
+            if (whole) {
+                float part = 0.f;
+#pragma unroll
+                for (int i = 0; i < Block<T>::kN; ++i) part += exp2_approx(-octaves(sc, b.get(i)));
+                sum += part;
+            }
+            if (listed(b.top())) {
+#pragma unroll 1
+                for (int i = 0; i < Block<T>::kN; ++i) {
+                    const float l = b.get(i);
+                    if (!listed(l)) continue;
+                    const uint32_t at = atomicAdd(&sh.listed, 1u);
+                    if (at < kList) {
+                        sh.list_key[at] = key_of(l);
+                        sh.list_index[at] = j * Block<T>::kN - row.shift + i;
+                    }
+                }
+            }
+        }
+        if (whole) {
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (lane == 0) sh.red_f[warp] = sum;
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                for (int i = 1; i < kWarps; ++i) sum += sh.red_f[i];
+                sh.sum = sum;
+            }
+        }
+        cl.sync();
+        int n = 0;
+        for (int c = 0; c < ctas; ++c) n += (int)min(cl.map_shared_rank(&sh, c)->listed, kList + 1u);
+        if (n > kList) {
+            cl.sync();
+            return false;
+        }
+        if (rank == 0) {
+            // the lists of all CTAs, sorted
+            u64 mine = ~0ull;
+            float z_all = 0.f;
+            int first = 0;
+            for (int c = 0; c < ctas; ++c) {
+                const Shared *o = cl.map_shared_rank(&sh, c);
+                const int count = (int)o->listed, i = (int)threadIdx.x - first;
+                if (i >= 0 && i < count) mine = (u64)~o->list_key[i] << 32 | o->list_index[i];
+                first += count;
+                if (whole) z_all += o->sum;
+            }
+            sh.sorted[threadIdx.x] = mine;
+            __syncthreads();
+            int at = 0;
+            if ((int)threadIdx.x < n) {
+#pragma unroll 4
+                for (int i = 0; i < n; ++i) at += sh.sorted[i] < mine;
+            }
+            __syncthreads();
+            if ((int)threadIdx.x < n) sh.sorted[at] = mine;
+            __syncthreads();
+            // token i of the order, its weight and that of those before it
+            const int i = threadIdx.x;
+            mine = i < n ? sh.sorted[i] : 0;
+            const float l = value_of(~(uint32_t)(mine >> 32));
+            const u64 w = i < n && (!k || i < k) ? weigh(l) : 0;
+            u64 all;
+            const u64 before = block_scan(w, sh.part, &all);
+            bool kept = w > 0 && ~(uint32_t)(mine >> 32) >= low_key, sure = true;
+            if (by_p) {
+                if (whole) {
+                    const double t = (double)top_p * (double)z_all * 0x1p43;
+                    const double lo = t * (1.0 - (double)kSumError), hi = t * (1.0 + (double)kSumError);
+                    // every border is on one side, and the last kept one is listed
+                    sure = i == 0 || !kept || (double)before < lo || (double)before >= hi;
+                    if (!low_key && (double)all < hi) sure = false;
+                    kept = kept && (i == 0 || (double)before < t);
+                } else {
+                    const double t = (double)top_p * (double)all;
+                    kept = kept && (i == 0 || before < (u64)ceil(t));
+                }
+            }
+            const int keep = __syncthreads_count(kept);
+            const bool fine = __syncthreads_and(sure);
+            if (threadIdx.x == 0) sh.settled = fine;
+            if (fine) {
+                // in the order of the tokens
+                u64 z, *weights = reinterpret_cast<u64 *>(sh.list_key);  // (the list has been read)
+                weights[i] = w;
+                block_scan(kept ? w : 0, sh.part, &z);
+                if (kept) {
+                    u64 at = 0;
+#pragma unroll 4
+                    for (int q = 0; q < keep; ++q)
+                        if ((uint32_t)sh.sorted[q] < (uint32_t)mine) at += weights[q];
+                    const double x = (double)u * (double)z;
+                    const u64 target = min(z - 1, x > 0.0 ? (u64)x : 0ull);
+                    if (at <= target && target < at + w) {
+                        a.token[r] = (int)(uint32_t)mine;
+                        if (a.logprob) a.logprob[r] = log_share(l, sc.top, temp, z);
+                    }
+                }
+            }
+        }
+        cl.sync();
+        const bool settled = cl.map_shared_rank(&sh, 0)->settled;
+        cl.sync();
+        return settled;
     }
 
     // The cut at which the running count (W: weight) of the values above cut.key reaches `target`
@@ -451,6 +619,7 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const Args a, int held_
         top = fmaxf(top, b.top());
     }
     if (keep) row.held = held;
+    const float own = top;  // the thread's largest
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     if (lane == 0) sh.red_f[warp] = top;
@@ -460,6 +629,7 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const Args a, int held_
         sh.top = top;
         sh.index = 0xffffffffu;
         sh.owner = -1;
+        sh.listed = 0;
     }
     cl.sync();
     for (int c = 0; c < ctas; ++c) top = fmaxf(top, cl.map_shared_rank(&sh, c)->top);
@@ -497,8 +667,19 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const Args a, int held_
     s.sc.top = top;
     s.sc.ch = (float)c;
     s.sc.cl = (float)(c - (double)s.sc.ch);
-    if (k > 0 && k < a.V) s.template search<false>([&](u64) { return (u64)k; });
-    if (top_p < 1.f) {
+    const bool by_k = k > 0 && k < a.V, by_p = top_p < 1.f, by_m = min_p > 0.f;
+    if (by_m) {
+        if (threadIdx.x == 0)
+            sh.low = __double2float_ru((double)top + (double)temp * log((double)fminf(min_p, 1.f)));
+        __syncthreads();
+    }
+    const uint32_t low_key = by_m ? key_of(sh.low + 0.f) : 0;
+    if ((by_k && k <= kListK) || (!by_k && (by_m || by_p))) {
+        const bool done = s.from_list(a, r, by_k ? k : 0, top_p, low_key, own, u, temp);
+        if (done) return;
+    }
+    if (by_k) s.template search<false>([&](u64) { return (u64)k; });
+    if (by_p) {
         const u64 w_tie = s.cut.ties ? s.weigh(value_of(s.cut.key)) : 0;
         u64 all = 0, target = 0;
         auto goal = [&](u64 above) {
@@ -513,13 +694,7 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const Args a, int held_
                 s.cut.ties = min(before.ties, (uint32_t)((target - all + w_tie - 1) / w_tie));
         }
     }
-    if (min_p > 0.f) {
-        if (threadIdx.x == 0)
-            sh.low = __double2float_ru((double)top + (double)temp * log((double)fminf(min_p, 1.f)));
-        __syncthreads();
-        const uint32_t low = key_of(sh.low + 0.f) - 1;
-        if (low >= s.cut.key) s.cut = Cut{low, 0};
-    }
+    if (by_m && low_key - 1 >= s.cut.key) s.cut = Cut{low_key - 1, 0};
 
     // weights and ties of every warp, in the order of the tokens
     const u64 w_tie = s.cut.ties ? s.weigh(value_of(s.cut.key)) : 0;
@@ -600,13 +775,7 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const Args a, int held_
                         one(l, w, t);
                         if (target < total(w, t)) {
                             a.token[r] = j * B::kN - row.shift + i;
-                            if (a.logprob) {
-                                const u64 z = sh.z;
-                                const float zf = (float)z * 0x1p-43f;
-                                const float lz = z < 2 * kOne ? log1pf((float)(long long)(z - kOne) * 0x1p-43f)
-                                                              : logf(zf);
-                                a.logprob[r] = (l - top) / temp - lz;
-                            }
+                            if (a.logprob) a.logprob[r] = log_share(l, top, temp, sh.z);
                             break;
                         }
                     }
