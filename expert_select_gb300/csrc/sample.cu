@@ -17,7 +17,7 @@
 // ones, of which there are few as a rule: a bound from below on the last of them (for top-k, the k-th
 // largest of the threads' own largest values, up to a bin; for min-p its own) lets a second pass collect
 // them, and one CTA sorts them and does the rest. top-p needs the whole weight too; a sum of fp32
-// exponentials, off by at most 2^-15, decides unless a cut lies within that.
+// exponentials, off by at most 2^-16, decides unless a cut lies within that.
 // Where more is kept than a list holds (flat distributions, no cuts), cuts are found by histograms of
 // the row's live values (weights that are not below 2^-43) over bins that descend with the value:
 // counts for top-k, weights for top-p; the bin that a cut falls in is divided by the bits of the
@@ -123,6 +123,14 @@ template <> struct Block<float> {
     __device__ __forceinline__ float get(int i) const {
         return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
     }
+    // the first value; the others move up
+    __device__ __forceinline__ float take() {
+        const float f = v.x;
+        v.x = v.y;
+        v.y = v.z;
+        v.z = v.w;
+        return f;
+    }
     // NaN becomes -inf, +inf the largest finite value, -0 becomes 0
     __device__ __forceinline__ static float clean(float x) {
         return fminf(fmaxf(x, -INFINITY), FLT_MAX) + 0.f;
@@ -136,11 +144,13 @@ template <> struct Block<float> {
     __device__ __forceinline__ float top() const {
         return fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
     }
-    __device__ __forceinline__ void edge(const float *p, int e, int V) {
+    // (by value: what a call gets the address of lives in memory)
+    __device__ __noinline__ static uint4 edge(const float *p, int e, int V) {
         float x[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[i] = e + i >= 0 && e + i < V ? p[e + i] : -INFINITY;
-        v = make_float4(x[0], x[1], x[2], x[3]);
+        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                          __float_as_uint(x[3]));
     }
 };
 template <> struct Block<__nv_bfloat16> {
@@ -149,6 +159,14 @@ template <> struct Block<__nv_bfloat16> {
     __device__ __forceinline__ float get(int i) const {
         const uint32_t w = i < 2 ? v.x : i < 4 ? v.y : i < 6 ? v.z : v.w;
         return i & 1 ? bf16_hi(w) : bf16_lo(w);
+    }
+    __device__ __forceinline__ float take() {
+        const float f = bf16_lo(v.x);
+        v.x = __funnelshift_r(v.x, v.y, 16);
+        v.y = __funnelshift_r(v.y, v.z, 16);
+        v.z = __funnelshift_r(v.z, v.w, 16);
+        v.w >>= 16;
+        return f;
     }
     __device__ __forceinline__ static uint32_t clean(uint32_t x) {
         const uint32_t low = 0xff80ff80u, big = 0x7f7f7f7fu, zero = 0;
@@ -169,591 +187,722 @@ template <> struct Block<__nv_bfloat16> {
         const __nv_bfloat162 m = __hmax2(__hmax2(p[0], p[1]), __hmax2(p[2], p[3]));
         return fmaxf(__low2float(m), __high2float(m));
     }
-    __device__ __forceinline__ void edge(const __nv_bfloat16 *p, int e, int V) {
+    __device__ __noinline__ static uint4 edge(const __nv_bfloat16 *p, int e, int V) {
         uint32_t x[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             x[i] = e + i >= 0 && e + i < V ? __bfloat16_as_ushort(p[e + i]) : 0xff80u;
-        v = make_uint4(x[0] | x[1] << 16, x[2] | x[3] << 16, x[4] | x[5] << 16, x[6] | x[7] << 16);
+        return make_uint4(x[0] | x[1] << 16, x[2] | x[3] << 16, x[4] | x[5] << 16, x[6] | x[7] << 16);
     }
 };
 
-constexpr int kList = 512;           // tokens of a list
-constexpr int kListK = 384;          // of them asked for (the bins' last may hold more)
-constexpr int kGuess = 256;          // where only top-p cuts: as many of the largest are tried
-constexpr float kSumError = 0x1p-15f;
+constexpr int kList = 2048;            // tokens of a list
+constexpr int kAsk = 1536;             // of them asked for (the last bin may hold more)
+constexpr int kGuess = 256;            // where only top-p cuts: as many are tried
+constexpr int kCount = 256;            // up to so many are ordered by counting, more by a network
+constexpr float kFar = 36.f;           // octaves from which values do not count in the fp32 sum
+constexpr float kSumError = 0x1p-16f;
 
-struct Shared {
-    float2 powers[256];
-    union {
-        struct {
-            uint32_t lo[kBins], hi[kBins];
-        };
-        struct {
-            uint32_t list_key[kList], list_index[kList];
-            u64 sorted[kList];  // ~key, index: ascending
-        };
-    };
-    u64 part[kWarps];
-    float red_f[kWarps];
-    uint32_t red_a[kWarps], red_b[kWarps];
-    // read by the other CTAs of the cluster
-    float top;
-    uint32_t kmin, kmax, index;
-    u64 wsum[kWarps];
-    uint32_t ties[kWarps];
-    uint32_t listed;
-    float sum;
-    int settled;
-    // found by one thread
-    int bin;
-    u64 before;
-    int owner;
-    u64 own_w;
-    uint32_t own_t;
-    u64 target, z;
-    float low;  // the least value that min-p keeps
+// A row, its settings, and where its results go.
+struct Task {
+    const void *inner, *low, *high;  // blocks (see Row)
+    int blocks, shift;               // block j holds the tokens j kN - shift ..
+    int b0, b1, per;                 // of this CTA's slice, and of a warp
+    bool raw;
+    float temp, top_p, u;
+    int k;                 // 0: all
+    uint32_t low_key;      // of min-p, or 0
+    int *token;
+    float *logprob;
 };
-
-// Sum of the block's threads before this one, in their order; the sum of all in *total.
-__device__ __forceinline__ u64 block_scan(u64 v, u64 *part, u64 *total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    u64 s = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const u64 t = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += t;
-    }
-    __syncthreads();
-    if (lane == 31) part[warp] = s;
-    __syncthreads();
-    u64 before = 0, all = 0;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-        const u64 p = part[i];
-        if (i < warp) before += p;
-        all += p;
-    }
-    *total = all;
-    return before + s - v;
-}
-
-// log of the share that a token of logit l has of the sum z.
-__device__ __forceinline__ float log_share(float l, float top, float temp, u64 z) {
-    const float lz = z < 2 * kOne ? log1pf((float)(long long)(z - kOne) * 0x1p-43f)
-                                  : logf((float)z * 0x1p-43f);
-    return (l - top) / temp - lz;
-}
 
 // What is kept of a row: values of keys above `key`, and the first `ties` tokens of that key.
 struct Cut {
     uint32_t key, ties;
 };
 
+struct Shared {
+    Task task;
+    Cut cut;
+    u64 goal;      // what a search looks for
+    double below;  // how far min-p's least value lies from the largest (-inf: not asked for)
+    u64 limit, limit_lo, limit_hi;
+    uint4 ends[2];
+    float2 powers[256];
+    uint32_t lo[kBins], hi[kBins];
+    u64 list[kList];  // ~key, index: ascending
+    u64 part[kWarps], scanned;
+    Scale sc;
+    // what a pass found, by warp
+    float sums[kWarps];
+    uint32_t kmin[kWarps], kmax[kWarps];
+    // read by the other CTAs of the cluster
+    u64 wsum[kWarps];
+    uint32_t ties[kWarps];
+    float top, sum;
+    uint32_t first, last, index;
+    int listed, settled;
+    // found by one thread
+    int bin, owner;
+    u64 before, own_w, target, z;
+    uint32_t own_t;
+};
+
+// Sum of the block's threads before this one, in their order; of all: sh.scanned. (What is used in
+// several places is called: code that a row runs through once waits for its instructions.)
+__device__ __noinline__ u64 block_scan(Shared &sh, u64 v) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    u64 s = v;
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+        const u64 t = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += t;
+    }
+    __syncthreads();
+    if (lane == 31) sh.part[warp] = s;
+    __syncthreads();
+    if (warp == 0) {
+        const u64 own = lane < kWarps ? sh.part[lane] : 0;
+        u64 t = own;
+#pragma unroll 1
+        for (int o = 1; o < kWarps; o <<= 1) {
+            const u64 x = __shfl_up_sync(0xffffffffu, t, o);
+            if (lane >= o) t += x;
+        }
+        if (lane < kWarps) sh.part[lane] = t - own;
+        if (lane == kWarps - 1) sh.scanned = t;
+    }
+    __syncthreads();
+    return sh.part[warp] + s - v;
+}
+
+__device__ __noinline__ u64 weigh(const Shared &sh, float l) { return weight(sh.sc, l, sh.powers); }
+
+__device__ __forceinline__ int bin_of(const Scale &sc, float l) {
+    return min(kBins - 1, (int)(octaves(sc, l) * kBinScale));
+}
+
+// log of the share that a token of logit l has of the sum z.
+__device__ __noinline__ float log_share(float l, float top, float temp, u64 z) {
+    const float lz = z < 2 * kOne ? log1pf((float)(long long)(z - kOne) * 0x1p-43f)
+                                  : logf((float)z * 0x1p-43f);
+    return (l - top) / temp - lz;
+}
+
 template <typename T> struct Row {
     using B = Block<T>;
-    const T *p;
-    const B *held;     // the slice in shared memory, or null
-    int V, shift;      // block j holds the tokens j kN - shift ..
-    int b0, b1;        // blocks of this CTA's slice
-    int w0, w1;        // of this warp
-    __device__ __forceinline__ B from_memory(int j) const {
-        B b;
-        const int e = j * B::kN - shift;
-        if (e >= 0 && e + B::kN <= V)
-            b = *reinterpret_cast<const B *>(p + e);
-        else
-            b.edge(p, e, V);
+    const B *inner;     // block j lies at inner + j, in memory or in shared memory
+    const B *low, *high;  // (the first and the last one elsewhere, as they reach past the row)
+    int high_j;
+    int shift;          // block j holds the tokens j kN - shift ..
+    int w0, w1;         // the warp's blocks
+    bool raw;           // not cleaned
+    __device__ __forceinline__ explicit Row(const Task &t) {
+        inner = reinterpret_cast<const B *>(t.inner);
+        low = reinterpret_cast<const B *>(t.low);
+        high = reinterpret_cast<const B *>(t.high);
+        high_j = t.blocks - 1;
+        shift = t.shift;
+        raw = t.raw;
+        w0 = min(t.b1, t.b0 + (int)(threadIdx.x >> 5) * t.per);
+        w1 = min(t.b1, w0 + t.per);
+    }
+    __device__ __forceinline__ const B *at(int j) const {
+        const B *p = inner + j;
+        p = j == 0 ? low : p;
+        return j == high_j ? high : p;
+    }
+    // f(block, its number) for the warp's blocks, kDeep of them on their way at a time (the loads are
+    // not conditional, so that none waits for another)
+    template <int kDeep, class F> __device__ __forceinline__ void blocks(F f) const {
+        const int lane = threadIdx.x & 31;
+#pragma unroll 1
+        for (int j0 = w0 + lane; j0 < w1; j0 += 32 * kDeep) {
+            B b[kDeep];
+#pragma unroll
+            for (int q = 0; q < kDeep; ++q) b[q] = *at(min(j0 + 32 * q, w1 - 1));
+            if (raw) {
+#pragma unroll
+                for (int q = 0; q < kDeep; ++q) b[q].clean();
+            }
+            f(b, j0, min(kDeep, (w1 - j0 + 31) / 32));
+        }
+    }
+    __device__ __forceinline__ B block(int j) const {
+        B b = *at(j);
         b.clean();
         return b;
     }
-    __device__ __forceinline__ B block(int j) const { return held ? held[j - b0] : from_memory(j); }
-    // f(value) for the warp's values of blocks that have one for which `any` of the largest holds;
-    // whole warps call it
-    template <class Any, class F> __device__ __forceinline__ void each(Any any, F f) const {
-        const int lane = threadIdx.x & 31;
-        for (int j0 = w0; j0 < w1; j0 += 32) {
-            const int j = j0 + lane;
-            const bool in = j < w1;
-            B b;
-            bool on = false;
-            if (in) {
-                b = block(j);
-                on = any(b.top());
-            }
-            if (on) {
-#pragma unroll
-                for (int i = 0; i < B::kN; ++i) f(b.get(i));
-            }
-        }
-    }
 };
 
-template <typename T> struct Sampler {
-    Shared &sh;
-    Row<T> row;
-    Scale sc;
-    Cut cut;
-    cg::cluster_group cl;
+// What a pass over a row's slice does with its live values whose keys lie in lo .. hi:
+enum : int {
+    kCounts,       // counts them in bins by octave
+    kCountKeys,    // counts them in bins (hi - key) >> arg
+    kWeights,      // adds their weights in bins by octave
+    kWeightKeys,   // adds their weights in bins (hi - key) >> arg
+    kRange,        // finds the least and the largest key of those in bin `arg`
+    kTake,         // appends those of bins up to `arg` to the list
+    kTakeAndSum,   // the same, and the fp32 sum of all weights
+    kFinal         // the weight of those above lo, and how many are lo's
+};
 
-    __device__ __forceinline__ u64 weigh(float l) const { return weight(sc, l, sh.powers); }
-    // Live and not cut off (ties apart).
-    __device__ __forceinline__ bool above(float l) const {
-        return is_live(sc, l) && key_of(l) > cut.key;
-    }
-
-    __device__ __forceinline__ void clear() {
-        for (int i = threadIdx.x; i < kBins; i += kThr) sh.lo[i] = sh.hi[i] = 0;
-        __syncthreads();
-    }
-    template <bool W> __device__ __forceinline__ void add(int bin, float l) {
-        if (!W) {
-            atomicAdd(&sh.lo[bin], 1u);
-            return;
-        }
-        const u64 w = weigh(l);
-        const uint32_t low = (uint32_t)w, old = atomicAdd(&sh.lo[bin], low);
-        const uint32_t high = (uint32_t)(w >> 32) + (old + low < old);
-        if (high) atomicAdd(&sh.hi[bin], high);
-    }
-    // The cluster's histograms become their sum.
-    __device__ __forceinline__ void share() {
-        const int ctas = cl.num_blocks(), rank = cl.block_rank();
-        __syncthreads();
-        if (ctas == 1) return;
-        cl.sync();
-        const int per = kBins / ctas;
-        for (int i = rank * per + threadIdx.x; i < (rank + 1) * per; i += kThr) {
-            u64 v = 0;
-            for (int c = 0; c < ctas; ++c) {
-                const Shared *o = cl.map_shared_rank(&sh, c);
-                v += (u64)o->hi[i] << 32 | o->lo[i];
-            }
-            for (int c = 0; c < ctas; ++c) {
-                Shared *o = cl.map_shared_rank(&sh, c);
-                o->lo[i] = (uint32_t)v;
-                o->hi[i] = (uint32_t)(v >> 32);
+template <typename T, int kMode>
+__device__ __noinline__ void pass(Shared &sh, uint32_t lo, uint32_t hi, int arg) {
+    using B = Block<T>;
+    const Row<T> row(sh.task);
+    const Scale sc = sh.sc;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    u64 wsum = 0;
+    uint32_t ties = 0, kmin = 0xffffffffu, kmax = 0;
+    float sum = 0.f;
+    auto value = [&](float l, int token) {
+        const uint32_t key = key_of(l);
+        if (key < lo || key > hi || !is_live(sc, l)) return;
+        if constexpr (kMode == kTake || kMode == kTakeAndSum) {
+            if (bin_of(sc, l) > arg) return;
+            const int at = atomicAdd(&sh.listed, 1);
+            if (at < kList) sh.list[at] = (u64)~key << 32 | (uint32_t)token;
+        } else if constexpr (kMode == kRange) {
+            if (bin_of(sc, l) != arg) return;
+            kmin = min(kmin, key);
+            kmax = max(kmax, key);
+        } else if constexpr (kMode == kCounts) {
+            atomicAdd(&sh.lo[bin_of(sc, l)], 1u);
+        } else if constexpr (kMode == kCountKeys) {
+            atomicAdd(&sh.lo[(hi - key) >> arg], 1u);
+        } else {
+            const u64 w = weight(sc, l, sh.powers);
+            if constexpr (kMode == kFinal) {
+                if (key > lo) wsum += w;
+                ties += key == lo;
+            } else {
+                const int bin = kMode == kWeightKeys ? (int)((hi - key) >> arg) : bin_of(sc, l);
+                const uint32_t low = (uint32_t)w, old = atomicAdd(&sh.lo[bin], low);
+                const uint32_t high = (uint32_t)(w >> 32) + (old + low < old);
+                if (high) atomicAdd(&sh.hi[bin], high);
             }
         }
-        cl.sync();
-    }
-    // The bin in which the running sum reaches `target` (> 0): sh.bin, and the sum before it in
-    // sh.before. False where it is not reached.
-    __device__ __forceinline__ bool find(u64 target) {
-        u64 v[kPer], own = 0, total;
+    };
+    constexpr int kDeep = kMode == kTake || kMode == kTakeAndSum ? 8 : 4;
+    row.template blocks<kDeep>([&](const auto &b, int j0, int n) {
+        uint32_t todo = 0;  // blocks that hold a value to look at
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int bin = threadIdx.x * kPer + i;
-            v[i] = (u64)sh.hi[bin] << 32 | sh.lo[bin];
-            own += v[i];
-        }
-        u64 at = block_scan(own, sh.part, &total);
-        if (at < target && target <= at + own) {
+        for (int q = 0; q < kDeep; ++q) {
+            const float m = b[q].top(), far = octaves(sc, m);
+            if (q >= n) continue;
+            if constexpr (kMode == kTakeAndSum) {
+                if (far < kFar) {
+                    float part = 0.f;
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                if (at < target && target <= at + v[i]) {
-                    sh.bin = threadIdx.x * kPer + i;
-                    sh.before = at;
+                    for (int i = 0; i < B::kN; ++i) part += exp2_approx(-octaves(sc, b[q].get(i)));
+                    sum += part;
                 }
-                at += v[i];
             }
-        }
-        __syncthreads();
-        return target <= total;
-    }
-
-    // Samples from a list of the row's largest tokens. own: the thread's largest value. False (for the
-    // whole cluster) where the list does not hold all that may be kept.
-    __device__ __forceinline__ bool from_list(const Args &a, int r, int k, float top_p,
-                                              uint32_t low_key, float own, float u, float temp) {
-        const int ctas = cl.num_blocks(), rank = cl.block_rank();
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        const bool by_p = top_p < 1.f, whole = by_p && !k;  // top-p of the whole row's weight
-        int last = kBins - 1;  // bins up to this one are listed
-        if (k || !low_key) {
-            clear();
-            if (is_live(sc, own))
-                atomicAdd(&sh.lo[min(kBins - 1, (int)(octaves(sc, own) * kBinScale))], 1u);
-            share();
-            if (find(k ? k : kGuess)) last = sh.bin;
-            __syncthreads();  // (the list takes the bins' place)
-        }
-        float sum = 0.f;
-        auto listed = [&](float l) {
-            return is_live(sc, l) && min(kBins - 1, (int)(octaves(sc, l) * kBinScale)) <= last &&
-                   (k || key_of(l) >= low_key);
-        };
-        for (int j0 = row.w0; j0 < row.w1; j0 += 32) {
-            const int j = j0 + lane;
-            if (j >= row.w1) continue;
-            const Block<T> b = row.block(j);
-            if (whole) {
-                float part = 0.f;
+            bool on = far < kLive && key_of(m) >= lo;
+            if constexpr (kMode == kTake || kMode == kTakeAndSum) on = on && bin_of(sc, m) <= arg;
+            if constexpr (kMode == kCounts) {
+                if (on) {
 #pragma unroll
-                for (int i = 0; i < Block<T>::kN; ++i) part += exp2_approx(-octaves(sc, b.get(i)));
-                sum += part;
+                    for (int i = 0; i < B::kN; ++i) value(b[q].get(i), 0);
+                }
+            } else {
+                todo |= on ? 1u << q : 0;
             }
-            if (listed(b.top())) {
+        }
 #pragma unroll 1
-                for (int i = 0; i < Block<T>::kN; ++i) {
-                    const float l = b.get(i);
-                    if (!listed(l)) continue;
-                    const uint32_t at = atomicAdd(&sh.listed, 1u);
-                    if (at < kList) {
-                        sh.list_key[at] = key_of(l);
-                        sh.list_index[at] = j * Block<T>::kN - row.shift + i;
-                    }
-                }
-            }
-        }
-        if (whole) {
+        while (todo) {
+            const int at_q = __ffs(todo) - 1;
+            todo &= todo - 1;
+            B one = b[0];
 #pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (lane == 0) sh.red_f[warp] = sum;
-            __syncthreads();
-            if (threadIdx.x == 0) {
-                for (int i = 1; i < kWarps; ++i) sum += sh.red_f[i];
-                sh.sum = sum;
-            }
+            for (int q = 1; q < kDeep; ++q)
+                if (at_q == q) one = b[q];
+            const int token = (j0 + 32 * at_q) * B::kN - row.shift;
+#pragma unroll 1
+            for (int i = 0; i < B::kN; ++i) value(one.take(), token + i);
         }
-        cl.sync();
-        int n = 0;
-        for (int c = 0; c < ctas; ++c) n += (int)min(cl.map_shared_rank(&sh, c)->listed, kList + 1u);
-        if (n > kList) {
-            cl.sync();
-            return false;
-        }
-        if (rank == 0) {
-            // the lists of all CTAs, sorted
-            u64 mine = ~0ull;
-            float z_all = 0.f;
-            int first = 0;
-            for (int c = 0; c < ctas; ++c) {
-                const Shared *o = cl.map_shared_rank(&sh, c);
-                const int count = (int)o->listed, i = (int)threadIdx.x - first;
-                if (i >= 0 && i < count) mine = (u64)~o->list_key[i] << 32 | o->list_index[i];
-                first += count;
-                if (whole) z_all += o->sum;
-            }
-            sh.sorted[threadIdx.x] = mine;
-            __syncthreads();
-            int at = 0;
-            if ((int)threadIdx.x < n) {
-#pragma unroll 4
-                for (int i = 0; i < n; ++i) at += sh.sorted[i] < mine;
-            }
-            __syncthreads();
-            if ((int)threadIdx.x < n) sh.sorted[at] = mine;
-            __syncthreads();
-            // token i of the order, its weight and that of those before it
-            const int i = threadIdx.x;
-            mine = i < n ? sh.sorted[i] : 0;
-            const float l = value_of(~(uint32_t)(mine >> 32));
-            const u64 w = i < n && (!k || i < k) ? weigh(l) : 0;
-            u64 all;
-            const u64 before = block_scan(w, sh.part, &all);
-            bool kept = w > 0 && ~(uint32_t)(mine >> 32) >= low_key, sure = true;
-            if (by_p) {
-                if (whole) {
-                    const double t = (double)top_p * (double)z_all * 0x1p43;
-                    const double lo = t * (1.0 - (double)kSumError), hi = t * (1.0 + (double)kSumError);
-                    // every border is on one side, and the last kept one is listed
-                    sure = i == 0 || !kept || (double)before < lo || (double)before >= hi;
-                    if (!low_key && (double)all < hi) sure = false;
-                    kept = kept && (i == 0 || (double)before < t);
-                } else {
-                    const double t = (double)top_p * (double)all;
-                    kept = kept && (i == 0 || before < (u64)ceil(t));
-                }
-            }
-            const int keep = __syncthreads_count(kept);
-            const bool fine = __syncthreads_and(sure);
-            if (threadIdx.x == 0) sh.settled = fine;
-            if (fine) {
-                // in the order of the tokens
-                u64 z, *weights = reinterpret_cast<u64 *>(sh.list_key);  // (the list has been read)
-                weights[i] = w;
-                block_scan(kept ? w : 0, sh.part, &z);
-                if (kept) {
-                    u64 at = 0;
-#pragma unroll 4
-                    for (int q = 0; q < keep; ++q)
-                        if ((uint32_t)sh.sorted[q] < (uint32_t)mine) at += weights[q];
-                    const double x = (double)u * (double)z;
-                    const u64 target = min(z - 1, x > 0.0 ? (u64)x : 0ull);
-                    if (at <= target && target < at + w) {
-                        a.token[r] = (int)(uint32_t)mine;
-                        if (a.logprob) a.logprob[r] = log_share(l, sc.top, temp, z);
-                    }
-                }
-            }
-        }
-        cl.sync();
-        const bool settled = cl.map_shared_rank(&sh, 0)->settled;
-        cl.sync();
-        return settled;
+    });
+    __syncwarp();
+    if (kMode == kTakeAndSum) {
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == 0) sh.sums[warp] = sum;
     }
-
-    // The cut at which the running count (W: weight) of the values above cut.key reaches `target`
-    // (> 0). False where it is not reached: nothing changes then. target_of gets the sum of all (W).
-    template <bool W, class Target>
-    __device__ __forceinline__ bool search(Target target_of) {
-        clear();
-        row.each([&](float m) { return above(m); }, [&](float l) {
-            if (above(l)) add<W>(min(kBins - 1, (int)(octaves(sc, l) * kBinScale)), l);
-        });
-        share();
-        u64 sum = 0;
-        if (W) {  // the target depends on the sum
-            u64 own = 0;
+    if (kMode == kFinal) {
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const int bin = threadIdx.x * kPer + i;
-                own += (u64)sh.hi[bin] << 32 | sh.lo[bin];
-            }
-            block_scan(own, sh.part, &sum);
+        for (int o = 16; o >= 1; o >>= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, o);
+        ties = __reduce_add_sync(0xffffffffu, ties);
+        if (lane == 0) {
+            sh.wsum[warp] = wsum;
+            sh.ties[warp] = ties;
         }
-        u64 target = target_of(sum);
-        if (!find(target)) return false;
-        const int first = sh.bin;
-        target -= sh.before;
-        // the keys that occur in the bin
-        uint32_t kmin = 0xffffffffu, kmax = 0;
-        row.each([&](float m) { return above(m); }, [&](float l) {
-            if (above(l) && min(kBins - 1, (int)(octaves(sc, l) * kBinScale)) == first) {
-                kmin = min(kmin, key_of(l));
-                kmax = max(kmax, key_of(l));
-            }
-        });
+    }
+    if (kMode == kRange) {
         kmin = __reduce_min_sync(0xffffffffu, kmin);
         kmax = __reduce_max_sync(0xffffffffu, kmax);
-        __syncthreads();
-        if ((threadIdx.x & 31) == 0) {
-            sh.red_a[threadIdx.x >> 5] = kmin;
-            sh.red_b[threadIdx.x >> 5] = kmax;
+        if (lane == 0) {
+            sh.kmin[warp] = kmin;
+            sh.kmax[warp] = kmax;
         }
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            for (int i = 0; i < kWarps; ++i) {
-                kmin = min(kmin, sh.red_a[i]);
-                kmax = max(kmax, sh.red_b[i]);
-            }
-            sh.kmin = kmin;
-            sh.kmax = kmax;
-        }
-        cl.sync();
-        for (int c = 0; c < (int)cl.num_blocks(); ++c) {
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ void clear_bins(Shared &sh) {
+    for (int i = threadIdx.x; i < kBins; i += kThr) sh.lo[i] = sh.hi[i] = 0;
+    __syncthreads();
+}
+
+// The cluster's histograms become their sum.
+__device__ __noinline__ void share_bins(Shared &sh) {
+    cg::cluster_group cl = cg::this_cluster();
+    const int ctas = cl.num_blocks(), rank = cl.block_rank();
+    __syncthreads();
+    if (ctas == 1) return;
+    cl.sync();
+    const int per = kBins / ctas;
+    for (int i = rank * per + threadIdx.x; i < (rank + 1) * per; i += kThr) {
+        u64 v = 0;
+#pragma unroll 4
+        for (int c = 0; c < ctas; ++c) {
             const Shared *o = cl.map_shared_rank(&sh, c);
-            kmin = min(kmin, o->kmin);
-            kmax = max(kmax, o->kmax);
+            v += (u64)o->hi[i] << 32 | o->lo[i];
         }
-        cl.sync();
-        while (kmin < kmax) {
-            const int shift = max(0, 32 - __clz(kmax - kmin) - 10);
-            clear();
-            row.each([&](float m) { return key_of(m) >= kmin; }, [&](float l) {
-                const uint32_t key = key_of(l);
-                if (key >= kmin && key <= kmax) add<W>((int)((kmax - key) >> shift), l);
-            });
-            share();
-            find(target);
-            target -= sh.before;
-            kmax -= (uint32_t)sh.bin << shift;
-            const uint32_t width = (1u << shift) - 1;
-            if (kmax - kmin > width) kmin = kmax - width;
-            if (shift == 0) break;
+#pragma unroll 4
+        for (int c = 0; c < ctas; ++c) {
+            Shared *o = cl.map_shared_rank(&sh, c);
+            o->lo[i] = (uint32_t)v;
+            o->hi[i] = (uint32_t)(v >> 32);
         }
-        cut.key = kmax;
-        // ties that are needed to reach the target
-        if (W) {
-            const u64 w = weigh(value_of(kmax));
-            cut.ties = w ? (uint32_t)((target + w - 1) / w) : 1u;
-        } else {
-            cut.ties = (uint32_t)target;
+    }
+    cl.sync();
+}
+
+// The bin in which the running sum reaches `target` (> 0): sh.bin, and the sum before it in sh.before;
+// sh.scanned: that of all. False where it is not reached.
+__device__ __noinline__ bool find_bin(Shared &sh, u64 target) {
+    u64 own = 0;
+    const int bin0 = threadIdx.x * kPer;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) own += (u64)sh.hi[bin0 + i] << 32 | sh.lo[bin0 + i];
+    u64 at = block_scan(sh, own);
+    if (at < target && target <= at + own) {
+        for (int i = 0; i < kPer; ++i) {
+            const u64 v = (u64)sh.hi[bin0 + i] << 32 | sh.lo[bin0 + i];
+            if (at < target && target <= at + v) {
+                sh.bin = bin0 + i;
+                sh.before = at;
+            }
+            at += v;
+        }
+    }
+    __syncthreads();
+    return target <= sh.scanned;
+}
+
+// Lowers sh.cut to where the running count of the values above it reaches sh.goal (> 0), or (W) their
+// running weight p times the weight of all of them and of the cut's ties. False where that is not
+// reached: the cut stays, and sh.goal is what is wanted of its ties.
+template <typename T, bool W> __device__ __noinline__ bool search(Shared &sh, double p) {
+    cg::cluster_group cl = cg::this_cluster();
+    u64 target = sh.goal;
+    const Cut cut = sh.cut;
+    clear_bins(sh);
+    pass<T, W ? kWeights : kCounts>(sh, cut.key + 1, 0xffffffffu, 0);
+    share_bins(sh);
+    if (W) {
+        u64 own = 0;
+        for (int i = threadIdx.x; i < kBins; i += kThr) own += (u64)sh.hi[i] << 32 | sh.lo[i];
+        block_scan(sh, own);
+        const u64 tie = cut.ties ? weigh(sh, value_of(cut.key)) : 0;
+        if (threadIdx.x == 0) {
+            const double t = p * (double)(sh.scanned + tie * cut.ties);
+            sh.goal = t >= 1.0 ? (u64)ceil(t) : 1;
+        }
+        __syncthreads();
+        target = sh.goal;
+        __syncthreads();
+    }
+    if (!find_bin(sh, target)) {
+        if (threadIdx.x == 0) sh.goal = target - sh.scanned;
+        __syncthreads();
+        return false;
+    }
+    target -= sh.before;
+    // the keys that occur in the bin
+    pass<T, kRange>(sh, cut.key + 1, 0xffffffffu, sh.bin);
+    uint32_t kmin = 0xffffffffu, kmax = 0;
+    for (int i = 0; i < kWarps; ++i) {
+        kmin = min(kmin, sh.kmin[i]);
+        kmax = max(kmax, sh.kmax[i]);
+    }
+    if (threadIdx.x == 0) {
+        sh.first = kmin;
+        sh.last = kmax;
+    }
+    cl.sync();
+    for (int c = 0; c < (int)cl.num_blocks(); ++c) {
+        const Shared *o = cl.map_shared_rank(&sh, c);
+        kmin = min(kmin, o->first);
+        kmax = max(kmax, o->last);
+    }
+    cl.sync();
+    while (kmin < kmax) {
+        const int shift = max(0, 32 - __clz(kmax - kmin) - 10);
+        clear_bins(sh);
+        pass<T, W ? kWeightKeys : kCountKeys>(sh, kmin, kmax, shift);
+        share_bins(sh);
+        find_bin(sh, target);
+        target -= sh.before;
+        kmax -= (uint32_t)sh.bin << shift;
+        const uint32_t width = (1u << shift) - 1;
+        if (kmax - kmin > width) kmin = kmax - width;
+        if (shift == 0) break;
+    }
+    // ties that are needed to reach the target
+    const u64 one = W ? weigh(sh, value_of(kmax)) : 1;
+    __syncthreads();
+    if (threadIdx.x == 0) sh.cut = Cut{kmax, one ? (uint32_t)((target + one - 1) / one) : 1u};
+    __syncthreads();
+    return true;
+}
+
+// Puts the first n of the list in ascending order.
+__device__ __noinline__ void sort_list(Shared &sh, int n) {
+    if (n <= kCount) {
+        u64 mine = 0;
+        int at = 0;
+        if ((int)threadIdx.x < n) {
+            mine = sh.list[threadIdx.x];
+#pragma unroll 4
+            for (int i = 0; i < n; ++i) at += sh.list[i] < mine;
+        }
+        __syncthreads();
+        if ((int)threadIdx.x < n) sh.list[at] = mine;
+        __syncthreads();
+        return;
+    }
+    int size = 2 * kCount;
+    while (size < n) size *= 2;
+    for (int i = n + threadIdx.x; i < size; i += kThr) sh.list[i] = ~0ull;
+    __syncthreads();
+    for (int k = 2; k <= size; k *= 2)
+        for (int j = k / 2; j > 0; j /= 2) {
+            for (int q = threadIdx.x; q < size / 2; q += kThr) {
+                const int i = 2 * q - (q & (j - 1)), o = i + j;
+                const u64 x = sh.list[i], y = sh.list[o];
+                if ((x > y) == ((i & k) == 0)) {
+                    sh.list[i] = y;
+                    sh.list[o] = x;
+                }
+            }
+            __syncthreads();
+        }
+}
+
+__device__ __noinline__ void emit(const Shared &sh, int token, float l, u64 z) {
+    *sh.task.token = token;
+    if (sh.task.logprob) *sh.task.logprob = log_share(l, sh.sc.top, sh.task.temp, z);
+}
+
+__device__ __forceinline__ u64 aim(float u, u64 z) {
+    const double x = (double)u * (double)z;
+    return min(z - 1, x > 0.0 ? (u64)x : 0ull);
+}
+
+// The weight of the list's first n.
+__device__ __noinline__ u64 list_weight(Shared &sh, int n) {
+    u64 all = 0;
+    for (int i = threadIdx.x; i < n; i += kThr) all += weigh(sh, value_of(~(uint32_t)(sh.list[i] >> 32)));
+    block_scan(sh, all);
+    all = sh.scanned;
+    __syncthreads();
+    return all;
+}
+
+// Borders (the weight before a token) below sh.limit are kept by top-p; in limit_lo .. limit_hi they
+// cannot be told from it. z: the weight that top-p cuts, up to a relative error. One thread's fp64: it
+// takes tens of cycles an instruction for every warp.
+__device__ __noinline__ void set_limit(Shared &sh, double z, double error) {
+    if (threadIdx.x == 0) {
+        const double t = (double)sh.task.top_p * z;
+        sh.limit = t >= 1.0 ? (u64)ceil(t) : 1;
+        sh.limit_lo = error > 0.0 ? (u64)(t * (1.0 - error)) : sh.limit;
+        sh.limit_hi = error > 0.0 ? (u64)(t * (1.0 + error)) + 1 : sh.limit;
+    }
+    __syncthreads();
+}
+
+// The cuts and the token from the sorted list of n tokens (top-k's at most); false where a border cannot
+// be told from top-p's limit.
+__device__ __noinline__ bool choose(Shared &sh, int n) {
+    const Task &ask = sh.task;
+    const bool by_p = ask.top_p < 1.f;
+    const u64 limit = sh.limit, limit_lo = sh.limit_lo, limit_hi = sh.limit_hi;
+    u64 *weights = reinterpret_cast<u64 *>(sh.lo);
+    bool sure = true;
+    if (n <= kCount / 2) {
+        // a thread for each token adds up what it needs itself
+        const int i = threadIdx.x;
+        const bool on = i < n;
+        const u64 e = on ? sh.list[i] : 0;
+        const uint32_t key = ~(uint32_t)(e >> 32);
+        const float l = value_of(key);
+        const u64 w = on ? weigh(sh, l) : 0;
+        if (on) weights[i] = w;
+        __syncthreads();
+        u64 before = 0;
+        if (on) {
+#pragma unroll 4
+            for (int q = 0; q < i; ++q) before += weights[q];
+        }
+        bool kept = w > 0 && key >= ask.low_key;
+        if (by_p && i > 0 && kept) {
+            sure = before < limit_lo || before >= limit_hi;
+            kept = before < limit;
+        }
+        const int keep = __syncthreads_count(kept);
+        if (!__syncthreads_and(sure)) return false;
+        if (i == keep - 1) {
+            sh.z = before + w;
+            sh.target = aim(ask.u, before + w);
+        }
+        __syncthreads();
+        if (kept) {
+            const u64 target = sh.target;
+            u64 at = 0;
+#pragma unroll 4
+            for (int q = 0; q < keep; ++q)
+                if ((uint32_t)sh.list[q] < (uint32_t)e) at += weights[q];
+            if (at <= target && target < at + w) emit(sh, (int)(uint32_t)e, l, sh.z);
         }
         return true;
     }
-};
+    u64 before = 0, z = 0;
+    int keep = 0;
+    for (int i0 = 0; i0 < n; i0 += kThr) {
+        const int i = i0 + threadIdx.x;
+        const uint32_t key = i < n ? ~(uint32_t)(sh.list[i] >> 32) : 0;
+        const u64 w = i < n ? weigh(sh, value_of(key)) : 0;
+        const u64 b = before + block_scan(sh, w);
+        before += sh.scanned;
+        bool kept = w > 0 && key >= ask.low_key;
+        if (by_p && i > 0 && kept) {
+            if (b >= limit_lo && b < limit_hi) sure = false;
+            kept = b < limit;
+        }
+        keep += __syncthreads_count(kept);
+        block_scan(sh, kept ? w : 0);
+        z += sh.scanned;
+        __syncthreads();
+    }
+    if (!__syncthreads_and(sure)) return false;
+    if (threadIdx.x == 0) sh.target = aim(ask.u, z);
+    // what is kept, in the order of the tokens
+    for (int i = threadIdx.x; i < keep; i += kThr) {
+        const u64 e = sh.list[i];
+        sh.list[i] = e << 32 | (uint32_t)~(uint32_t)(e >> 32);  // index, key
+    }
+    __syncthreads();
+    const u64 target = sh.target;
+    sort_list(sh, keep);
+    before = 0;
+    for (int i0 = 0; i0 < keep; i0 += kThr) {
+        const int i = i0 + threadIdx.x;
+        const u64 e = i < keep ? sh.list[i] : 0;
+        const float l = value_of((uint32_t)e);
+        const u64 w = i < keep ? weigh(sh, l) : 0;
+        const u64 b = before + block_scan(sh, w);
+        if (b <= target && target < b + w) emit(sh, (int)(e >> 32), l, z);
+        before += sh.scanned;
+        __syncthreads();
+    }
+    return true;
+}
 
-template <typename T>
-__global__ void __launch_bounds__(kThr, 2) sample_kernel(const Args a, int held_blocks) {
-    extern __shared__ __align__(16) unsigned char dyn[];
-    __shared__ __align__(16) Shared sh;
+// Samples from a list of the row's largest tokens: those that min-p leaves (want 0), or `want` of them
+// and a few more. own: the thread's largest value. False (for the whole cluster) where the list does
+// not hold all that may be kept.
+template <typename T> __device__ __noinline__ bool from_list(Shared &sh, int want, float own) {
+    const Task &ask = sh.task;
+    cg::cluster_group cl = cg::this_cluster();
+    const int ctas = cl.num_blocks(), rank = cl.block_rank();
+    const bool whole = ask.top_p < 1.f && !ask.k;  // top-p of the whole row's weight
+    int last = kBins - 1;                          // bins up to this one are listed
+    int listed = 0, undecided = 0;
+    if (threadIdx.x == 0) sh.listed = 0;
+    if (want) {
+        clear_bins(sh);
+        if (want <= kThr / 2 * ctas) {
+            // as many threads' largest values: at least as many values
+            if (is_live(sh.sc, own)) atomicAdd(&sh.lo[bin_of(sh.sc, own)], 1u);
+        } else {
+            pass<T, kCounts>(sh, 0, 0xffffffffu, 0);
+        }
+        share_bins(sh);
+        if (find_bin(sh, want)) last = sh.bin;
+    }
+    __syncthreads();
+    if (whole)
+        pass<T, kTakeAndSum>(sh, ask.low_key, 0xffffffffu, last);
+    else
+        pass<T, kTake>(sh, ask.k ? 0 : ask.low_key, 0xffffffffu, last);
+    if (whole && threadIdx.x == 0) {
+        float sum = 0.f;
+        for (int i = 0; i < kWarps; ++i) sum += sh.sums[i];
+        sh.sum = sum;
+    }
+    cl.sync();
+    if (rank == 0) {
+        // a lane for each CTA reads how much it has listed
+        const int lane = threadIdx.x & 31;
+        int mine = 0, before;
+        float z_all = 0.f;
+        if (lane < ctas) {
+            const Shared *o = cl.map_shared_rank(&sh, lane);
+            mine = min(o->listed, kList + 1);
+            z_all = whole ? o->sum : 0.f;
+        }
+        before = mine;
+#pragma unroll
+        for (int o = 1; o < kMaxCluster; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, before, o);
+            if (lane >= o) before += x;
+            z_all += __shfl_xor_sync(0xffffffffu, z_all, o);
+        }
+        int n = __shfl_sync(0xffffffffu, before, kMaxCluster - 1);
+        z_all = __shfl_sync(0xffffffffu, z_all, 0);
+        bool fine = n <= kList;
+        if (threadIdx.x < ctas) sh.kmin[lane] = before;  // (the list's ends)
+        __syncthreads();
+        if (fine) {
+            const int own = sh.listed;
+            for (int i = own + threadIdx.x; i < n; i += kThr) {
+                int c = 0, first = 0;
+                for (int o = 1; o < ctas; ++o) {
+                    const int x = (int)sh.kmin[o - 1];
+                    if (i >= x) {
+                        c = o;
+                        first = x;
+                    }
+                }
+                sh.list[i] = cl.map_shared_rank(&sh, c)->list[i - first];
+            }
+            __syncthreads();
+            if (whole) {
+                set_limit(sh, (double)z_all * 0x1p43, (double)kSumError);
+                // (what top-p keeps last is to be listed)
+                if (!ask.low_key) fine = list_weight(sh, n) >= sh.limit_hi;
+            }
+        }
+        if (fine) {
+            sort_list(sh, n);
+            if (ask.k) n = min(n, ask.k);
+            if (ask.k && ask.top_p < 1.f) set_limit(sh, (double)list_weight(sh, n), 0.0);
+            fine = choose(sh, n);
+            if (!fine) undecided = 1;
+        }
+        if (threadIdx.x == 0) sh.settled = fine ? 1 : undecided ? 2 : 0;
+        listed = n;
+    }
+    cl.sync();
+    int settled = cl.map_shared_rank(&sh, 0)->settled;
+    if (settled == 2) {
+        // a border lies within the error of the fp32 sum: the row's weight as it is
+        pass<T, kFinal>(sh, 0, 0xffffffffu, 0);
+        if (threadIdx.x < kWarps) {
+            u64 sum = sh.wsum[threadIdx.x];
+#pragma unroll
+            for (int o = kWarps / 2; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffu, sum, o);
+            if (threadIdx.x == 0) sh.wsum[0] = sum;
+        }
+        cl.sync();
+        if (rank == 0) {
+            u64 z = 0;
+            for (int c = 0; c < ctas; ++c) z += cl.map_shared_rank(&sh, c)->wsum[0];
+            set_limit(sh, (double)z, 0.0);
+            choose(sh, listed);
+        }
+        settled = 1;
+    }
+    cl.sync();
+    return settled != 0;
+}
+
+// Samples from the row itself.
+template <typename T> __device__ __noinline__ void from_row(Shared &sh) {
     using B = Block<T>;
+    const Task &ask = sh.task;
+    const Row<T> row(ask);
     cg::cluster_group cl = cg::this_cluster();
     const int ctas = cl.num_blocks(), rank = cl.block_rank();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int r = blockIdx.x / ctas;
-    for (int i = threadIdx.x; i < 256; i += kThr)
-        sh.powers[i] = make_float2(kPowers.hi[i], kPowers.lo[i]);
-    pdl_wait();
-    const int g = r / a.group;
-    // (beyond these the weights are those of the largest alone, or equal)
-    float temp = a.temperature ? a.temperature[g] : 1.f;
-    if (temp > 0.f) temp = fminf(fmaxf(temp, 1e-30f), 1e30f);
-    const int k = a.top_k ? a.top_k[g] : 0;
-    const float top_p = a.top_p ? a.top_p[g] : 1.f, min_p = a.min_p ? a.min_p[g] : 0.f;
-    const float u = a.u[r];
-
-    Sampler<T> s{sh, {}, {}, {0, 0}, cl};
-    Row<T> &row = s.row;
-    row.p = reinterpret_cast<const T *>(a.logits) + (size_t)r * a.ld;
-    row.V = a.V;
-    row.shift = (int)(((uintptr_t)row.p / sizeof(T)) % B::kN);
-    const int blocks = (a.V + row.shift + B::kN - 1) / B::kN, per = (blocks + ctas - 1) / ctas;
-    row.b0 = min(blocks, rank * per);
-    row.b1 = min(blocks, row.b0 + per);
-    row.held = nullptr;
-    const int wper = ((row.b1 - row.b0 + kWarps - 1) / kWarps + 31) / 32 * 32;
-    row.w0 = min(row.b1, row.b0 + warp * wper);
-    row.w1 = min(row.b1, row.w0 + wper);
-
-    // the row's slice, and the largest value
-    B *held = reinterpret_cast<B *>(dyn);
-    const bool keep = per <= held_blocks;
-    float top = -INFINITY;
-#pragma unroll 4
-    for (int j = row.w0 + lane; j < row.w1; j += 32) {
-        const B b = row.from_memory(j);
-        if (keep) held[j - row.b0] = b;
-        top = fmaxf(top, b.top());
-    }
-    if (keep) row.held = held;
-    const float own = top;  // the thread's largest
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (lane == 0) sh.red_f[warp] = top;
-    __syncthreads();
-    for (int i = 0; i < kWarps; ++i) top = fmaxf(top, sh.red_f[i]);
     if (threadIdx.x == 0) {
-        sh.top = top;
-        sh.index = 0xffffffffu;
-        sh.owner = -1;
-        sh.listed = 0;
+        sh.cut = Cut{0, 0};
+        sh.goal = ask.k;
     }
-    cl.sync();
-    for (int c = 0; c < ctas; ++c) top = fmaxf(top, cl.map_shared_rank(&sh, c)->top);
-
-    if (top == -INFINITY) {  // nothing to sample from
-        if (rank == 0 && threadIdx.x == 0) {
-            a.token[r] = -1;
-            if (a.logprob) a.logprob[r] = -INFINITY;
-        }
-        cl.sync();
-        return;
-    }
-    if (!(temp > 0.f)) {  // the first of the largest
-        for (int j = row.w0 + lane; j < row.w1; j += 32) {
-            const B b = row.block(j);
-            if (b.top() < top) continue;
-            int first = 0;
-            for (int i = B::kN - 1; i >= 0; --i)
-                if (b.get(i) == top) first = i;
-            atomicMin(&sh.index, (uint32_t)(j * B::kN - row.shift + first));
-            break;
-        }
-        cl.sync();
-        if (rank == 0 && threadIdx.x == 0) {
-            uint32_t first = 0xffffffffu;
-            for (int c = 0; c < ctas; ++c) first = min(first, cl.map_shared_rank(&sh, c)->index);
-            a.token[r] = (int)first;
-            if (a.logprob) a.logprob[r] = 0.f;
-        }
-        cl.sync();
-        return;
-    }
-
-    const double c = 1.4426950408889634074 / (double)temp;
-    s.sc.top = top;
-    s.sc.ch = (float)c;
-    s.sc.cl = (float)(c - (double)s.sc.ch);
-    const bool by_k = k > 0 && k < a.V, by_p = top_p < 1.f, by_m = min_p > 0.f;
-    if (by_m) {
-        if (threadIdx.x == 0)
-            sh.low = __double2float_ru((double)top + (double)temp * log((double)fminf(min_p, 1.f)));
-        __syncthreads();
-    }
-    const uint32_t low_key = by_m ? key_of(sh.low + 0.f) : 0;
-    if ((by_k && k <= kListK) || (!by_k && (by_m || by_p))) {
-        const bool done = s.from_list(a, r, by_k ? k : 0, top_p, low_key, own, u, temp);
-        if (done) return;
-    }
-    if (by_k) s.template search<false>([&](u64) { return (u64)k; });
-    if (by_p) {
-        const u64 w_tie = s.cut.ties ? s.weigh(value_of(s.cut.key)) : 0;
-        u64 all = 0, target = 0;
-        auto goal = [&](u64 above) {
-            all = above;
-            const double t = (double)top_p * (double)(above + w_tie * s.cut.ties);
-            target = t >= 1.0 ? (u64)ceil(t) : 1;
-            return target;
-        };
-        const Cut before = s.cut;
-        if (!s.template search<true>(goal)) {  // the cut lies among the ties of top-k's
-            if (before.ties && w_tie)
-                s.cut.ties = min(before.ties, (uint32_t)((target - all + w_tie - 1) / w_tie));
+    __syncthreads();
+    if (ask.k) search<T, false>(sh, 0.0);
+    if (ask.top_p < 1.f) {
+        const Cut before = sh.cut;
+        if (!search<T, true>(sh, (double)ask.top_p) && before.ties) {
+            // the cut lies among the ties of top-k's
+            const u64 tie = weigh(sh, value_of(before.key));
+            if (threadIdx.x == 0 && tie)
+                sh.cut.ties = min(before.ties, (uint32_t)((sh.goal + tie - 1) / tie));
+            __syncthreads();
         }
     }
-    if (by_m && low_key - 1 >= s.cut.key) s.cut = Cut{low_key - 1, 0};
+    Cut cut = sh.cut;
+    if (ask.low_key && ask.low_key - 1 >= cut.key) cut = Cut{ask.low_key - 1, 0};
 
     // weights and ties of every warp, in the order of the tokens
-    const u64 w_tie = s.cut.ties ? s.weigh(value_of(s.cut.key)) : 0;
-    const Cut cut = s.cut;
-    u64 sum = 0;
-    uint32_t ties = 0;
-    row.each([&](float m) { return is_live(s.sc, m) && key_of(m) >= cut.key; }, [&](float l) {
-        if (!is_live(s.sc, l)) return;
-        const uint32_t key = key_of(l);
-        if (key > cut.key) sum += s.weigh(l);
-        ties += key == cut.key;
-    });
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    ties = __reduce_add_sync(0xffffffffu, ties);
-    if (lane == 0) {
-        sh.wsum[warp] = sum;
-        sh.ties[warp] = ties;
-    }
+    pass<T, kFinal>(sh, cut.key, 0xffffffffu, 0);
     cl.sync();
+    const u64 w_tie = cut.ties ? weigh(sh, value_of(cut.key)) : 0;
+    auto total = [&](u64 w, u64 t) { return w + w_tie * min(t, (u64)cut.ties); };
     {
-        u64 w = 0, t = 0, all_w, all_t;
+        u64 w = 0, t = 0;
         if (threadIdx.x < kWarps * ctas) {
             const Shared *o = cl.map_shared_rank(&sh, threadIdx.x / kWarps);
             w = o->wsum[threadIdx.x % kWarps];
             t = o->ties[threadIdx.x % kWarps];
         }
-        const u64 w0 = block_scan(w, sh.part, &all_w), t0 = block_scan(t, sh.part, &all_t);
-        auto total = [&](u64 w, u64 t) { return w + w_tie * min(t, (u64)cut.ties); };
+        const u64 w0 = block_scan(sh, w), all_w = sh.scanned;
+        __syncthreads();
+        const u64 t0 = block_scan(sh, t), all_t = sh.scanned;
         const u64 z = total(all_w, all_t);
-        const double x = (double)u * (double)z;
-        const u64 target = min(z - 1, x > 0.0 ? (u64)x : 0ull);
-        if (threadIdx.x < kWarps * ctas && total(w0, t0) <= target && target < total(w0 + w, t0 + t)) {
+        if (threadIdx.x == 0) sh.target = aim(ask.u, z);
+        __syncthreads();
+        const u64 goal = sh.target;
+        if (total(w0, t0) <= goal && goal < total(w0 + w, t0 + t)) {
             sh.owner = threadIdx.x;
             sh.own_w = w0;
             sh.own_t = (uint32_t)t0;
-            sh.target = target;
             sh.z = z;
         }
         __syncthreads();
     }
     if (sh.owner == rank * kWarps + warp) {
-        const u64 target = sh.target;
+        const Scale sc = sh.sc;
+        const u64 goal = sh.target;
         u64 w_at = sh.own_w, t_at = sh.own_t;
-        auto total = [&](u64 w, u64 t) { return w + w_tie * min(t, (u64)cut.ties); };
+#pragma unroll 1
         for (int j0 = row.w0; j0 < row.w1; j0 += 32) {
             const int j = j0 + lane;
-            B b;
             u64 w = 0, t = 0;
-            auto one = [&](float l, u64 &w, u64 &t) {
-                if (!is_live(s.sc, l)) return;
-                const uint32_t key = key_of(l);
-                if (key > cut.key) w += s.weigh(l);
-                t += key == cut.key;
-            };
+            B b;
             if (j < row.w1) {
                 b = row.block(j);
-#pragma unroll
-                for (int i = 0; i < B::kN; ++i) one(b.get(i), w, t);
+                B c = b;
+#pragma unroll 1
+                for (int i = 0; i < B::kN; ++i) {
+                    const float l = c.take();
+                    if (!is_live(sc, l)) continue;
+                    if (key_of(l) > cut.key) w += weigh(sh, l);
+                    t += key_of(l) == cut.key;
+                }
             }
             u64 ws = w, ts = t;
 #pragma unroll
@@ -764,18 +913,20 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const Args a, int held_
                     ts += y;
                 }
             }
-            const bool here = target < total(w_at + ws, t_at + ts);
+            const bool here = goal < total(w_at + ws, t_at + ts);
             const uint32_t m = __ballot_sync(0xffffffffu, here);
             if (m) {
                 if (lane == __ffs(m) - 1) {
                     w = w_at + ws - w;
                     t = t_at + ts - t;
+#pragma unroll 1
                     for (int i = 0; i < B::kN; ++i) {
-                        const float l = b.get(i);
-                        one(l, w, t);
-                        if (target < total(w, t)) {
-                            a.token[r] = j * B::kN - row.shift + i;
-                            if (a.logprob) a.logprob[r] = log_share(l, top, temp, sh.z);
+                        const float l = b.take();
+                        if (!is_live(sc, l)) continue;
+                        if (key_of(l) > cut.key) w += weigh(sh, l);
+                        t += key_of(l) == cut.key;
+                        if (goal < total(w, t)) {
+                            emit(sh, j * B::kN - row.shift + i, l, sh.z);
                             break;
                         }
                     }
@@ -789,15 +940,155 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const Args a, int held_
     cl.sync();  // (shared memory of CTAs that have ended is not to be read)
 }
 
+template <typename T>
+__global__ void __launch_bounds__(kThr, 2) sample_kernel(const Args a, int held_blocks) {
+    extern __shared__ __align__(16) unsigned char dyn[];
+    __shared__ __align__(16) Shared sh;
+    using B = Block<T>;
+    cg::cluster_group cl = cg::this_cluster();
+    const int ctas = cl.num_blocks(), rank = cl.block_rank();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int r = blockIdx.x / ctas;
+    for (int i = threadIdx.x; i < 256; i += kThr)
+        sh.powers[i] = make_float2(kPowers.hi[i], kPowers.lo[i]);
+    pdl_wait();
+    Task &t = sh.task;
+    if (threadIdx.x == 0) {
+        const int g = r / a.group;
+        const T *p = reinterpret_cast<const T *>(a.logits) + (size_t)r * a.ld;
+        t.shift = (int)(((uintptr_t)p / sizeof(T)) % B::kN);
+        t.blocks = (a.V + t.shift + B::kN - 1) / B::kN;
+        const int per = (t.blocks + ctas - 1) / ctas;
+        t.b0 = min(t.blocks, rank * per);
+        t.b1 = min(t.blocks, t.b0 + per);
+        t.per = ((t.b1 - t.b0 + kWarps - 1) / kWarps + 31) / 32 * 32;
+        // the row's ends reach into other memory: their blocks are made up
+        const B *inner = reinterpret_cast<const B *>(p - t.shift);
+        t.inner = inner;
+        t.low = inner;
+        t.high = inner + t.blocks - 1;
+        if (t.shift) {
+            sh.ends[0] = B::edge(p, -t.shift, a.V);
+            t.low = sh.ends;
+        }
+        const int last = (t.blocks - 1) * B::kN - t.shift;
+        if (last + B::kN > a.V) {
+            sh.ends[1] = B::edge(p, last, a.V);
+            t.high = sh.ends + 1;
+        }
+        if (t.blocks == 1 && t.shift) t.high = t.low;
+        t.raw = true;
+        // (beyond these the weights are those of the largest alone, or equal)
+        t.temp = a.temperature ? a.temperature[g] : 1.f;
+        if (t.temp > 0.f) t.temp = fminf(fmaxf(t.temp, 1e-30f), 1e30f);
+        const int k = a.top_k ? a.top_k[g] : 0;
+        t.k = k < a.V ? max(k, 0) : 0;
+        const float p_ = a.top_p ? a.top_p[g] : 1.f;
+        t.top_p = p_ < 1.f ? p_ : 1.f;
+        t.u = a.u[r];
+        t.token = a.token + r;
+        t.logprob = a.logprob ? a.logprob + r : nullptr;
+        sh.index = 0xffffffffu;
+        sh.owner = -1;
+    } else if (threadIdx.x == 32) {
+        float temp = a.temperature ? a.temperature[r / a.group] : 1.f;
+        temp = fminf(fmaxf(temp, 1e-30f), 1e30f);
+        const double c = 1.4426950408889634074 / (double)temp;
+        sh.sc.ch = (float)c;
+        sh.sc.cl = (float)(c - (double)sh.sc.ch);
+    } else if (threadIdx.x == 64) {
+        const float min_p = a.min_p ? a.min_p[r / a.group] : 0.f;
+        float temp = a.temperature ? a.temperature[r / a.group] : 1.f;
+        temp = fminf(fmaxf(temp, 1e-30f), 1e30f);
+        sh.below = min_p > 0.f ? (double)temp * log((double)fminf(min_p, 1.f)) : -1.0 / 0.0;
+    }
+    __syncthreads();
+
+    // the row's slice, and the largest value
+    const Row<T> row(t);
+    B *held = t.b1 - t.b0 <= held_blocks ? reinterpret_cast<B *>(dyn) - t.b0 : nullptr;
+    float top = -INFINITY;
+    row.template blocks<8>([&](const auto &b, int j0, int n) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            if (q >= n) continue;
+            if (held) held[j0 + 32 * q] = b[q];
+            top = fmaxf(top, b[q].top());
+        }
+    });
+    const float own = top;  // the thread's largest
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) sh.sums[warp] = top;
+    __syncthreads();
+    for (int i = 0; i < kWarps; ++i) top = fmaxf(top, sh.sums[i]);
+    if (threadIdx.x == 0) {
+        sh.top = top;
+        if (held) {
+            t.inner = t.low = held;
+            t.high = held + t.blocks - 1;
+            t.raw = false;
+        }
+    }
+    cl.sync();
+    if (ctas > 1) {  // (a lane for each CTA: the reads do not wait for one another)
+        if (lane < ctas) top = fmaxf(top, cl.map_shared_rank(&sh, lane)->top);
+#pragma unroll
+        for (int o = kMaxCluster / 2; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        top = __shfl_sync(0xffffffffu, top, 0);
+    }
+
+    if (top == -INFINITY) {  // nothing to sample from
+        if (rank == 0 && threadIdx.x == 0) {
+            *t.token = -1;
+            if (t.logprob) *t.logprob = -INFINITY;
+        }
+        cl.sync();
+        return;
+    }
+    if (!(t.temp > 0.f)) {  // the first of the largest
+        if (own == top) {
+            for (int j = row.w0 + lane; j < row.w1; j += 32) {
+                B b = row.block(j);
+                if (b.top() < top) continue;
+                int i = 0;
+                while (b.take() != top) ++i;
+                atomicMin(&sh.index, (uint32_t)(j * B::kN - row.shift + i));
+                break;
+            }
+        }
+        cl.sync();
+        if (rank == 0 && threadIdx.x == 0) {
+            uint32_t first = 0xffffffffu;
+            for (int c = 0; c < ctas; ++c) first = min(first, cl.map_shared_rank(&sh, c)->index);
+            *t.token = (int)first;
+            if (t.logprob) *t.logprob = 0.f;
+        }
+        cl.sync();
+        return;
+    }
+
+    const bool by_m = sh.below > -1.0 / 0.0;
+    if (threadIdx.x == 0) {
+        sh.sc.top = top;
+        t.low_key = by_m ? key_of(__double2float_ru((double)top + sh.below) + 0.f) : 0;
+    }
+    __syncthreads();
+    // what is kept may fit a list: k tokens, or those that min-p leaves, or top-p's as a guess
+    if (t.k ? t.k <= kAsk : by_m || t.top_p < 1.f)
+        if (from_list<T>(sh, t.k ? t.k : by_m ? 0 : kGuess, own)) return;
+    from_row<T>(sh);
+}
+
 constexpr int kHeldBytes = 76 * 1024;  // of a row in a CTA: two CTAs share an SM
 
 template <typename T> cudaError_t launch(const Args &a, cudaStream_t s) {
     const int blocks = (a.V + 2 * Block<T>::kN - 2) / Block<T>::kN;
-    const int room = kHeldBytes / 16, sms = std::max(1, device_sms());
-    // the CTAs that hold a row; more of them for few rows
+    const int room = kHeldBytes / 16, slots = 2 * std::max(1, device_sms());
+    // more CTAs a row only where the GPU has room for them: barriers over a cluster cost more than what
+    // they save where rows wait
     int ctas = 1;
-    while (ctas < kMaxCluster && (blocks + ctas - 1) / ctas > room) ctas *= 2;
-    while (ctas < kMaxCluster && (long long)a.R * ctas * 2 <= sms && blocks / ctas > 2 * kThr) ctas *= 2;
+    while (ctas < kMaxCluster && (long long)a.R * ctas * 2 <= slots && blocks / ctas > 2 * kThr) ctas *= 2;
     const int per = (blocks + ctas - 1) / ctas;
     const int held = per <= room ? per : 0;
     cudaError_t err = allow_smem(sample_kernel<T>, kHeldBytes);
