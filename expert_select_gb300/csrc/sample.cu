@@ -106,6 +106,44 @@ __device__ __forceinline__ float exp2_approx(float x) {
     return y;
 }
 
+// The weights of two live values: the same steps, two to an instruction.
+__device__ __forceinline__ void weight2(const Scale &s, float l0, float l1, const float2 *powers, u64 &w0,
+                                        u64 &w1) {
+    constexpr float kBig = 12582912.f;
+    constexpr double kLn2 = 0.69314718055994530942;
+    constexpr float lh = (float)kLn2, ll = (float)(kLn2 - (double)lh);
+    auto both = [](float v) { return pack2(v, v); };
+    const uint64_t minus = both(-1.f), l = pack2(l0, l1), top = both(s.top), ch = both(s.ch);
+    const uint64_t d = fma2(l, minus, top), bb = add2(d, both(-s.top));
+    const uint64_t e = fma2(add2(l, bb), minus, fma2(fma2(bb, minus, d), minus, top));
+    const uint64_t p = mul2(d, ch);
+    const uint64_t pe = add2(fma2(d, ch, mul2(d, both(-s.ch))), fma2(d, both(s.cl), mul2(e, ch)));
+    const uint64_t kb = fma2(p, both(256.f), both(kBig));
+    const uint64_t r = fma2(add2(kb, both(-kBig)), both(-1.f / 256.f), p);
+    const uint64_t q = mul2(r, both(-lh));
+    const uint64_t ql = fma2(r, both(-ll), fma2(pe, both(-lh), fma2(r, both(-lh), mul2(r, both(lh)))));
+    const uint64_t poly = fma2(q, fma2(q, both(1.f / 24.f), both(1.f / 6.f)), both(0.5f));
+    const uint64_t more = fma2(mul2(q, q), poly, fma2(ql, q, ql));
+    const uint64_t eh = add2(q, more), el = fma2(fma2(q, minus, eh), minus, more);
+    const float2 kf = unpack2(kb);
+    const int k0 = __float_as_int(kf.x) - 0x4b400000, k1 = __float_as_int(kf.y) - 0x4b400000;
+    const float2 t0 = powers[k0 & 255], t1 = powers[k1 & 255];
+    const uint64_t sc = pack2(__int_as_float((127 + 22 - (k0 >> 8)) << 23),
+                              __int_as_float((127 + 22 - (k1 >> 8)) << 23));
+    const uint64_t a = mul2(pack2(t0.x, t1.x), sc), al = mul2(pack2(t0.y, t1.y), sc), b = mul2(a, eh);
+    const uint64_t c = add2(fma2(a, eh, mul2(a, mul2(eh, minus))), fma2(a, el, fma2(al, q, al)));
+    const uint64_t ai = add2(a, both(8388608.f)), bi = add2(b, both(kBig));
+    const uint64_t rest = add2(add2(fma2(add2(ai, both(-8388608.f)), minus, a),
+                                    fma2(add2(bi, both(-kBig)), minus, b)), c);
+    const float2 af = unpack2(ai), bf = unpack2(bi), lo = unpack2(fma2(rest, both(2097152.f), both(kBig)));
+    const int h0 = (__float_as_int(af.x) - 0x4b000000) + (__float_as_int(bf.x) - 0x4b400000);
+    const int h1 = (__float_as_int(af.y) - 0x4b000000) + (__float_as_int(bf.y) - 0x4b400000);
+    const long long x = ((long long)h0 << 21) + (__float_as_int(lo.x) - 0x4b400000);
+    const long long y = ((long long)h1 << 21) + (__float_as_int(lo.y) - 0x4b400000);
+    w0 = x > 0 ? (u64)x : 0;
+    w1 = y > 0 ? (u64)y : 0;
+}
+
 // Values in the order of their keys (NaN and -0 do not occur).
 __device__ __forceinline__ uint32_t key_of(float l) {
     const uint32_t b = __float_as_uint(l);
@@ -342,7 +380,7 @@ enum : int {
     kWeights,      // adds their weights in bins by octave
     kWeightKeys,   // adds their weights in bins (hi - key) >> arg
     kRange,        // finds the least and the largest key of those in bin `arg`
-    kTake,         // appends those of bins up to `arg` to the list
+    kTake,         // appends those from lo on to the list
     kTakeAndSum,   // the same, and the fp32 sum of all weights
     kFinal         // the weight of those above lo, and how many are lo's
 };
@@ -356,58 +394,56 @@ __device__ __noinline__ void pass(Shared &sh, uint32_t lo, uint32_t hi, int arg)
     u64 wsum = 0;
     uint32_t ties = 0, kmin = 0xffffffffu, kmax = 0;
     float sum = 0.f;
-    auto value = [&](float l, int token) {
+    auto look_at = [&](uint32_t key, float l) { return key >= lo && key <= hi && is_live(sc, l); };
+    auto value = [&](float l) {
         const uint32_t key = key_of(l);
-        if (key < lo || key > hi || !is_live(sc, l)) return;
-        if constexpr (kMode == kTake || kMode == kTakeAndSum) {
-            if (bin_of(sc, l) > arg) return;
-            const int at = atomicAdd(&sh.listed, 1);
-            if (at < kList) sh.list[at] = (u64)~key << 32 | (uint32_t)token;
-        } else if constexpr (kMode == kRange) {
+        if (!look_at(key, l)) return;
+        if constexpr (kMode == kRange) {
             if (bin_of(sc, l) != arg) return;
             kmin = min(kmin, key);
             kmax = max(kmax, key);
-        } else if constexpr (kMode == kCounts) {
-            atomicAdd(&sh.lo[bin_of(sc, l)], 1u);
-        } else if constexpr (kMode == kCountKeys) {
-            atomicAdd(&sh.lo[(hi - key) >> arg], 1u);
         } else {
-            const u64 w = weight(sc, l, sh.powers);
-            if constexpr (kMode == kFinal) {
-                if (key > lo) wsum += w;
-                ties += key == lo;
-            } else {
-                const int bin = kMode == kWeightKeys ? (int)((hi - key) >> arg) : bin_of(sc, l);
-                const uint32_t low = (uint32_t)w, old = atomicAdd(&sh.lo[bin], low);
-                const uint32_t high = (uint32_t)(w >> 32) + (old + low < old);
-                if (high) atomicAdd(&sh.hi[bin], high);
-            }
+            atomicAdd(&sh.lo[kMode == kCounts ? bin_of(sc, l) : (int)((hi - key) >> arg)], 1u);
         }
     };
-    constexpr int kDeep = kMode == kTake || kMode == kTakeAndSum ? 8 : 4;
+    auto weighed = [&](uint32_t key, float l, u64 w) {
+        if constexpr (kMode == kFinal) {
+            if (key > lo) wsum += w;
+            ties += key == lo;
+        } else {
+            const int bin = kMode == kWeightKeys ? (int)((hi - key) >> arg) : bin_of(sc, l);
+            const uint32_t low = (uint32_t)w, old = atomicAdd(&sh.lo[bin], low);
+            const uint32_t high = (uint32_t)(w >> 32) + (old + low < old);
+            if (high) atomicAdd(&sh.hi[bin], high);
+        }
+    };
+    constexpr bool kTakes = kMode == kTake || kMode == kTakeAndSum;
+    constexpr int kDeep = kTakes ? 8 : 4;
+    const float least = value_of(lo);
     row.template blocks<kDeep>([&](const auto &b, int j0, int n) {
         uint32_t todo = 0;  // blocks that hold a value to look at
 #pragma unroll
         for (int q = 0; q < kDeep; ++q) {
-            const float m = b[q].top(), far = octaves(sc, m);
+            const float m = b[q].top();
             if (q >= n) continue;
-            if constexpr (kMode == kTakeAndSum) {
-                if (far < kFar) {
+            if constexpr (kTakes) {
+                if (kMode == kTakeAndSum && octaves(sc, m) < kFar) {
                     float part = 0.f;
 #pragma unroll
                     for (int i = 0; i < B::kN; ++i) part += exp2_approx(-octaves(sc, b[q].get(i)));
                     sum += part;
                 }
-            }
-            bool on = far < kLive && key_of(m) >= lo;
-            if constexpr (kMode == kTake || kMode == kTakeAndSum) on = on && bin_of(sc, m) <= arg;
-            if constexpr (kMode == kCounts) {
-                if (on) {
-#pragma unroll
-                    for (int i = 0; i < B::kN; ++i) value(b[q].get(i), 0);
-                }
+                if (m >= least) todo |= 1u << q;
             } else {
-                todo |= on ? 1u << q : 0;
+                const bool on = is_live(sc, m) && key_of(m) >= lo;
+                if constexpr (kMode == kCounts) {
+                    if (on) {
+#pragma unroll
+                        for (int i = 0; i < B::kN; ++i) value(b[q].get(i));
+                    }
+                } else {
+                    todo |= on ? 1u << q : 0;
+                }
             }
         }
 #pragma unroll 1
@@ -418,9 +454,35 @@ __device__ __noinline__ void pass(Shared &sh, uint32_t lo, uint32_t hi, int arg)
 #pragma unroll
             for (int q = 1; q < kDeep; ++q)
                 if (at_q == q) one = b[q];
-            const int token = (j0 + 32 * at_q) * B::kN - row.shift;
+            if constexpr (kTakes) {
+                uint32_t hits = 0;
+#pragma unroll
+                for (int i = 0; i < B::kN; ++i) hits |= one.get(i) >= least ? 1u << i : 0;
+                int at = atomicAdd(&sh.listed, __popc(hits));
+                const int token = (j0 + 32 * at_q) * B::kN - row.shift;
 #pragma unroll 1
-            for (int i = 0; i < B::kN; ++i) value(one.take(), token + i);
+                for (int i = 0; hits; ++i, hits >>= 1) {
+                    const float l = one.take();
+                    if (!(hits & 1)) continue;
+                    if (at < kList) sh.list[at] = (u64)~key_of(l) << 32 | (uint32_t)(token + i);
+                    ++at;
+                }
+            } else if constexpr (kMode == kRange || kMode == kCounts || kMode == kCountKeys) {
+#pragma unroll 1
+                for (int i = 0; i < B::kN; ++i) value(one.take());
+            } else {
+#pragma unroll 1
+                for (int i = 0; i < B::kN; i += 2) {
+                    const float l0 = one.take(), l1 = one.take();
+                    const uint32_t k0 = key_of(l0), k1 = key_of(l1);
+                    const bool on0 = look_at(k0, l0), on1 = look_at(k1, l1);
+                    if (!on0 && !on1) continue;
+                    u64 x, y;
+                    weight2(sc, l0, l1, sh.powers, x, y);
+                    if (on0) weighed(k0, l0, x);
+                    if (on1) weighed(k1, l1, y);
+                }
+            }
         }
     });
     __syncwarp();
@@ -634,12 +696,13 @@ __device__ __noinline__ void set_limit(Shared &sh, double z, double error) {
     __syncthreads();
 }
 
-// The cuts and the token from the sorted list of n tokens (top-k's at most); false where a border cannot
-// be told from top-p's limit.
-__device__ __noinline__ bool choose(Shared &sh, int n) {
+// The cuts and the token from the sorted list of n tokens (top-k's at most); of_list: top-p is of their
+// weight. False where a border cannot be told from top-p's limit.
+__device__ __noinline__ bool choose(Shared &sh, int n, bool of_list) {
     const Task &ask = sh.task;
     const bool by_p = ask.top_p < 1.f;
-    const u64 limit = sh.limit, limit_lo = sh.limit_lo, limit_hi = sh.limit_hi;
+    if (of_list && n > kCount / 2) set_limit(sh, (double)list_weight(sh, n), 0.0);
+    u64 limit = sh.limit, limit_lo = sh.limit_lo, limit_hi = sh.limit_hi;
     u64 *weights = reinterpret_cast<u64 *>(sh.lo);
     bool sure = true;
     if (n <= kCount / 2) {
@@ -656,6 +719,12 @@ __device__ __noinline__ bool choose(Shared &sh, int n) {
         if (on) {
 #pragma unroll 4
             for (int q = 0; q < i; ++q) before += weights[q];
+        }
+        if (of_list) {
+            if (i == n - 1) sh.z = before + w;
+            __syncthreads();
+            set_limit(sh, (double)sh.z, 0.0);
+            limit = limit_lo = limit_hi = sh.limit;
         }
         bool kept = w > 0 && key >= ask.low_key;
         if (by_p && i > 0 && kept) {
@@ -744,10 +813,15 @@ template <typename T> __device__ __noinline__ bool from_list(Shared &sh, int wan
         if (find_bin(sh, want)) last = sh.bin;
     }
     __syncthreads();
+    // All values of those bins (and perhaps a few below them) are at least so large; min-p's least value
+    // is one itself.
+    float least = sh.sc.top - (float)(last + 1) * (1.0f + 0x1p-18f) / kBinScale / sh.sc.ch;
+    uint32_t least_key = key_of(fmaxf(least, -FLT_MAX) + 0.f);
+    if (!ask.k) least_key = max(least_key, ask.low_key);
     if (whole)
-        pass<T, kTakeAndSum>(sh, ask.low_key, 0xffffffffu, last);
+        pass<T, kTakeAndSum>(sh, least_key, 0xffffffffu, 0);
     else
-        pass<T, kTake>(sh, ask.k ? 0 : ask.low_key, 0xffffffffu, last);
+        pass<T, kTake>(sh, least_key, 0xffffffffu, 0);
     if (whole && threadIdx.x == 0) {
         float sum = 0.f;
         for (int i = 0; i < kWarps; ++i) sum += sh.sums[i];
@@ -799,8 +873,7 @@ template <typename T> __device__ __noinline__ bool from_list(Shared &sh, int wan
         if (fine) {
             sort_list(sh, n);
             if (ask.k) n = min(n, ask.k);
-            if (ask.k && ask.top_p < 1.f) set_limit(sh, (double)list_weight(sh, n), 0.0);
-            fine = choose(sh, n);
+            fine = choose(sh, n, ask.k && ask.top_p < 1.f);
             if (!fine) undecided = 1;
         }
         if (threadIdx.x == 0) sh.settled = fine ? 1 : undecided ? 2 : 0;
@@ -822,7 +895,7 @@ template <typename T> __device__ __noinline__ bool from_list(Shared &sh, int wan
             u64 z = 0;
             for (int c = 0; c < ctas; ++c) z += cl.map_shared_rank(&sh, c)->wsum[0];
             set_limit(sh, (double)z, 0.0);
-            choose(sh, listed);
+            choose(sh, listed, false);
         }
         settled = 1;
     }
