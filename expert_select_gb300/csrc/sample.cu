@@ -128,8 +128,9 @@ __device__ __forceinline__ void weight2(const Scale &s, float l0, float l1, cons
     const float2 kf = unpack2(kb);
     const int k0 = __float_as_int(kf.x) - 0x4b400000, k1 = __float_as_int(kf.y) - 0x4b400000;
     const float2 t0 = powers[k0 & 255], t1 = powers[k1 & 255];
-    const uint64_t sc = pack2(__int_as_float((127 + 22 - (k0 >> 8)) << 23),
-                              __int_as_float((127 + 22 - (k1 >> 8)) << 23));
+    // 2^(22 - (k >> 8))
+    const uint64_t sc = pack2(__int_as_float((k0 & ~255) * -32768 + (149 << 23)),
+                              __int_as_float((k1 & ~255) * -32768 + (149 << 23)));
     const uint64_t a = mul2(pack2(t0.x, t1.x), sc), al = mul2(pack2(t0.y, t1.y), sc), b = mul2(a, eh);
     const uint64_t c = add2(fma2(a, eh, mul2(a, mul2(eh, minus))), fma2(a, el, fma2(al, q, al)));
     const uint64_t ai = add2(a, both(8388608.f)), bi = add2(b, both(kBig));
@@ -138,10 +139,8 @@ __device__ __forceinline__ void weight2(const Scale &s, float l0, float l1, cons
     const float2 af = unpack2(ai), bf = unpack2(bi), lo = unpack2(fma2(rest, both(2097152.f), both(kBig)));
     const int h0 = (__float_as_int(af.x) - 0x4b000000) + (__float_as_int(bf.x) - 0x4b400000);
     const int h1 = (__float_as_int(af.y) - 0x4b000000) + (__float_as_int(bf.y) - 0x4b400000);
-    const long long x = ((long long)h0 << 21) + (__float_as_int(lo.x) - 0x4b400000);
-    const long long y = ((long long)h1 << 21) + (__float_as_int(lo.y) - 0x4b400000);
-    w0 = x > 0 ? (u64)x : 0;
-    w1 = y > 0 ? (u64)y : 0;
+    w0 = (u64)((long long)h0 * (1 << 21) + (__float_as_int(lo.x) - 0x4b400000));
+    w1 = (u64)((long long)h1 * (1 << 21) + (__float_as_int(lo.y) - 0x4b400000));
 }
 
 // Values in the order of their keys (NaN and -0 do not occur).
@@ -406,20 +405,33 @@ __device__ __noinline__ void pass(Shared &sh, uint32_t lo, uint32_t hi, int arg)
             atomicAdd(&sh.lo[kMode == kCounts ? bin_of(sc, l) : (int)((hi - key) >> arg)], 1u);
         }
     };
-    auto weighed = [&](uint32_t key, float l, u64 w) {
-        if constexpr (kMode == kFinal) {
-            if (key > lo) wsum += w;
-            ties += key == lo;
-        } else {
-            const int bin = kMode == kWeightKeys ? (int)((hi - key) >> arg) : bin_of(sc, l);
-            const uint32_t low = (uint32_t)w, old = atomicAdd(&sh.lo[bin], low);
-            const uint32_t high = (uint32_t)(w >> 32) + (old + low < old);
-            if (high) atomicAdd(&sh.hi[bin], high);
+    // (keys below the least value's and above the largest's stand for no value)
+    const float least = lo > key_of(-INFINITY) ? value_of(lo) : -INFINITY;
+    const float most = hi < key_of(INFINITY) ? value_of(hi) : INFINITY;
+    // two values' weights; comparisons of values instead of keys, which take more instructions
+    auto pair = [&](float l0, float l1) {
+        const bool on0 = l0 >= least && l0 <= most && is_live(sc, l0);
+        const bool on1 = l1 >= least && l1 <= most && is_live(sc, l1);
+        if (!on0 && !on1) return;
+        u64 w[2];
+        weight2(sc, l0, l1, sh.powers, w[0], w[1]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float l = i ? l1 : l0;
+            if (!(i ? on1 : on0)) continue;
+            if constexpr (kMode == kFinal) {
+                if (l > least) wsum += w[i];
+                ties += l == least;
+            } else {
+                const int bin = kMode == kWeightKeys ? (int)((hi - key_of(l)) >> arg) : bin_of(sc, l);
+                const uint32_t low = (uint32_t)w[i], old = atomicAdd(&sh.lo[bin], low);
+                const uint32_t high = (uint32_t)(w[i] >> 32) + (old + low < old);
+                if (high) atomicAdd(&sh.hi[bin], high);
+            }
         }
     };
     constexpr bool kTakes = kMode == kTake || kMode == kTakeAndSum;
     constexpr int kDeep = kTakes ? 8 : 4;
-    const float least = value_of(lo);
     row.template blocks<kDeep>([&](const auto &b, int j0, int n) {
         uint32_t todo = 0;  // blocks that hold a value to look at
 #pragma unroll
@@ -435,7 +447,7 @@ __device__ __noinline__ void pass(Shared &sh, uint32_t lo, uint32_t hi, int arg)
                 }
                 if (m >= least) todo |= 1u << q;
             } else {
-                const bool on = is_live(sc, m) && key_of(m) >= lo;
+                const bool on = is_live(sc, m) && m >= least;
                 if constexpr (kMode == kCounts) {
                     if (on) {
 #pragma unroll
@@ -471,17 +483,8 @@ __device__ __noinline__ void pass(Shared &sh, uint32_t lo, uint32_t hi, int arg)
 #pragma unroll 1
                 for (int i = 0; i < B::kN; ++i) value(one.take());
             } else {
-#pragma unroll 1
-                for (int i = 0; i < B::kN; i += 2) {
-                    const float l0 = one.take(), l1 = one.take();
-                    const uint32_t k0 = key_of(l0), k1 = key_of(l1);
-                    const bool on0 = look_at(k0, l0), on1 = look_at(k1, l1);
-                    if (!on0 && !on1) continue;
-                    u64 x, y;
-                    weight2(sc, l0, l1, sh.powers, x, y);
-                    if (on0) weighed(k0, l0, x);
-                    if (on1) weighed(k1, l1, y);
-                }
+#pragma unroll
+                for (int i = 0; i < B::kN; i += 2) pair(one.get(i), one.get(i + 1));
             }
         }
     });
@@ -645,22 +648,46 @@ __device__ __noinline__ void sort_list(Shared &sh, int n) {
         __syncthreads();
         return;
     }
+    // A bitonic network: a thread holds entries warp 128 + 32 q + lane, q < 4, so that steps of less
+    // than 32 are shuffles, of 32 and 64 registers, and only longer ones meet in shared memory.
+    static_assert(kList == 4 * kThr, "four entries a thread");
     int size = 2 * kCount;
     while (size < n) size *= 2;
-    for (int i = n + threadIdx.x; i < size; i += kThr) sh.list[i] = ~0ull;
-    __syncthreads();
-    for (int k = 2; k <= size; k *= 2)
+    const int lane = threadIdx.x & 31, base = (threadIdx.x >> 5) * 128 + lane;
+    u64 v[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = base + 32 * q < n ? sh.list[base + 32 * q] : ~0ull;
+#pragma unroll 1
+    for (int k = 2; k <= size; k *= 2) {
+#pragma unroll 1
         for (int j = k / 2; j > 0; j /= 2) {
-            for (int q = threadIdx.x; q < size / 2; q += kThr) {
-                const int i = 2 * q - (q & (j - 1)), o = i + j;
-                const u64 x = sh.list[i], y = sh.list[o];
-                if ((x > y) == ((i & k) == 0)) {
-                    sh.list[i] = y;
-                    sh.list[o] = x;
-                }
+            u64 o[4];
+            if (j >= 128) {
+                __syncthreads();
+#pragma unroll
+                for (int q = 0; q < 4; ++q) sh.list[base + 32 * q] = v[q];
+                __syncthreads();
+#pragma unroll
+                for (int q = 0; q < 4; ++q) o[q] = sh.list[(base + 32 * q) ^ j];
+            } else if (j >= 32) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) o[q] = j == 32 ? v[q ^ 1] : v[q ^ 2];
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) o[q] = __shfl_xor_sync(0xffffffffu, v[q], j);
             }
-            __syncthreads();
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int i = base + 32 * q;
+                const bool low = ((i & k) == 0) == ((i & j) == 0);  // this one keeps the lesser
+                if ((o[q] < v[q]) == low) v[q] = o[q];
+            }
         }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < 4; ++q) sh.list[base + 32 * q] = v[q];
+    __syncthreads();
 }
 
 __device__ __noinline__ void emit(const Shared &sh, int token, float l, u64 z) {
@@ -748,25 +775,34 @@ __device__ __noinline__ bool choose(Shared &sh, int n, bool of_list) {
         }
         return true;
     }
-    u64 before = 0, z = 0;
+    // four entries of the order a thread
+    const int i0 = 4 * threadIdx.x;
+    u64 w[4], own = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        w[q] = i0 + q < n ? weigh(sh, value_of(~(uint32_t)(sh.list[i0 + q] >> 32))) : 0;
+        own += w[q];
+    }
+    u64 before = block_scan(sh, own);
     int keep = 0;
-    for (int i0 = 0; i0 < n; i0 += kThr) {
-        const int i = i0 + threadIdx.x;
-        const uint32_t key = i < n ? ~(uint32_t)(sh.list[i] >> 32) : 0;
-        const u64 w = i < n ? weigh(sh, value_of(key)) : 0;
-        const u64 b = before + block_scan(sh, w);
-        before += sh.scanned;
-        bool kept = w > 0 && key >= ask.low_key;
-        if (by_p && i > 0 && kept) {
-            if (b >= limit_lo && b < limit_hi) sure = false;
-            kept = b < limit;
+    own = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        bool kept = w[q] > 0 && ~(uint32_t)(sh.list[i0 + q] >> 32) >= ask.low_key;
+        if (by_p && i0 + q > 0 && kept) {
+            if (before >= limit_lo && before < limit_hi) sure = false;
+            kept = before < limit;
         }
-        keep += __syncthreads_count(kept);
-        block_scan(sh, kept ? w : 0);
-        z += sh.scanned;
-        __syncthreads();
+        before += w[q];
+        keep += kept;
+        own += kept ? w[q] : 0;
     }
     if (!__syncthreads_and(sure)) return false;
+    block_scan(sh, own);
+    const u64 z = sh.scanned;
+    __syncthreads();
+    block_scan(sh, (u64)keep);
+    keep = (int)sh.scanned;
     if (threadIdx.x == 0) sh.target = aim(ask.u, z);
     // what is kept, in the order of the tokens
     for (int i = threadIdx.x; i < keep; i += kThr) {
@@ -776,16 +812,18 @@ __device__ __noinline__ bool choose(Shared &sh, int n, bool of_list) {
     __syncthreads();
     const u64 target = sh.target;
     sort_list(sh, keep);
-    before = 0;
-    for (int i0 = 0; i0 < keep; i0 += kThr) {
-        const int i = i0 + threadIdx.x;
-        const u64 e = i < keep ? sh.list[i] : 0;
-        const float l = value_of((uint32_t)e);
-        const u64 w = i < keep ? weigh(sh, l) : 0;
-        const u64 b = before + block_scan(sh, w);
-        if (b <= target && target < b + w) emit(sh, (int)(e >> 32), l, z);
-        before += sh.scanned;
-        __syncthreads();
+    own = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        w[q] = i0 + q < keep ? weigh(sh, value_of((uint32_t)sh.list[i0 + q])) : 0;
+        own += w[q];
+    }
+    before = block_scan(sh, own);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        if (before <= target && target < before + w[q])
+            emit(sh, (int)(sh.list[i0 + q] >> 32), value_of((uint32_t)sh.list[i0 + q]), z);
+        before += w[q];
     }
     return true;
 }
