@@ -11,7 +11,8 @@
 // polynomial carried as pairs of fp32 values; off by some 2^-42 relative, checked against 64 bits),
 // and sums are 64-bit integers: exact, and the same in any order.
 //
-// A cluster of CTAs holds a row in shared memory, which reads it once.
+// A row belongs to a CTA, or, where rows are few, to a cluster of CTAs that hold it in shared memory;
+// else it is read again from L2.
 //
 // Every cut keeps the first tokens of the descending order, so what is kept lies among the largest
 // ones, of which there are few as a rule: a bound from below on the last of them (for top-k, the k-th
@@ -233,10 +234,8 @@ template <> struct Block<__nv_bfloat16> {
     }
 };
 
-constexpr int kList = 2048;            // tokens of a list
-constexpr int kAsk = 1536;             // of them asked for (the last bin may hold more)
-constexpr int kGuess = 256;            // where only top-p cuts: as many are tried
-constexpr int kCount = 256;            // up to so many are ordered by counting, more by a network
+constexpr int kList = kThr;             // tokens of a list, a thread for each
+constexpr int kAsk = kList / 2;        // of them asked for (the last bin may hold more)
 constexpr float kFar = 36.f;           // octaves from which values do not count in the fp32 sum
 constexpr float kSumError = 0x1p-16f;
 
@@ -262,6 +261,7 @@ struct Shared {
     Task task;
     Cut cut;
     u64 goal;      // what a search looks for
+    float live;    // the least live value
     double below;  // how far min-p's least value lies from the largest (-inf: not asked for)
     u64 limit, limit_lo, limit_hi;
     uint4 ends[2];
@@ -272,17 +272,20 @@ struct Shared {
     Scale sc;
     // what a pass found, by warp
     float sums[kWarps];
-    uint32_t kmin[kWarps], kmax[kWarps];
+    int ends_of[kMaxCluster];  // the lists', one after the other
     // read by the other CTAs of the cluster
     u64 wsum[kWarps];
     uint32_t ties[kWarps];
     float top, sum;
-    uint32_t first, last, index;
+    uint32_t index;
     int listed, settled;
     // found by one thread
     int bin, owner;
+    uint32_t edges[2];
     u64 before, own_w, target, z;
     uint32_t own_t;
+    u64 part_w[kWarps], part_t[kWarps];
+    int part_owner;
 };
 
 // Sum of the block's threads before this one, in their order; of all: sh.scanned. (What is used in
@@ -378,7 +381,6 @@ enum : int {
     kCountKeys,    // counts them in bins (hi - key) >> arg
     kWeights,      // adds their weights in bins by octave
     kWeightKeys,   // adds their weights in bins (hi - key) >> arg
-    kRange,        // finds the least and the largest key of those in bin `arg`
     kTake,         // appends those from lo on to the list
     kTakeAndSum,   // the same, and the fp32 sum of all weights
     kFinal         // the weight of those above lo, and how many are lo's
@@ -391,72 +393,27 @@ __device__ __noinline__ void pass(Shared &sh, uint32_t lo, uint32_t hi, int arg)
     const Scale sc = sh.sc;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     u64 wsum = 0;
-    uint32_t ties = 0, kmin = 0xffffffffu, kmax = 0;
+    uint32_t ties = 0;
     float sum = 0.f;
-    auto look_at = [&](uint32_t key, float l) { return key >= lo && key <= hi && is_live(sc, l); };
-    auto value = [&](float l) {
-        const uint32_t key = key_of(l);
-        if (!look_at(key, l)) return;
-        if constexpr (kMode == kRange) {
-            if (bin_of(sc, l) != arg) return;
-            kmin = min(kmin, key);
-            kmax = max(kmax, key);
-        } else {
-            atomicAdd(&sh.lo[kMode == kCounts ? bin_of(sc, l) : (int)((hi - key) >> arg)], 1u);
-        }
-    };
-    // (keys below the least value's and above the largest's stand for no value)
-    const float least = lo > key_of(-INFINITY) ? value_of(lo) : -INFINITY;
-    const float most = hi < key_of(INFINITY) ? value_of(hi) : INFINITY;
-    // two values' weights; comparisons of values instead of keys, which take more instructions
-    auto pair = [&](float l0, float l1) {
-        const bool on0 = l0 >= least && l0 <= most && is_live(sc, l0);
-        const bool on1 = l1 >= least && l1 <= most && is_live(sc, l1);
-        if (!on0 && !on1) return;
-        u64 w[2];
-        weight2(sc, l0, l1, sh.powers, w[0], w[1]);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float l = i ? l1 : l0;
-            if (!(i ? on1 : on0)) continue;
-            if constexpr (kMode == kFinal) {
-                if (l > least) wsum += w[i];
-                ties += l == least;
-            } else {
-                const int bin = kMode == kWeightKeys ? (int)((hi - key_of(l)) >> arg) : bin_of(sc, l);
-                const uint32_t low = (uint32_t)w[i], old = atomicAdd(&sh.lo[bin], low);
-                const uint32_t high = (uint32_t)(w[i] >> 32) + (old + low < old);
-                if (high) atomicAdd(&sh.hi[bin], high);
-            }
-        }
-    };
     constexpr bool kTakes = kMode == kTake || kMode == kTakeAndSum;
     constexpr int kDeep = kTakes ? 8 : 4;
+    // (keys below the least value's and above the largest's stand for no value)
+    float least = lo > key_of(-INFINITY) ? value_of(lo) : -INFINITY;
+    const float most = hi < key_of(INFINITY) ? value_of(hi) : INFINITY, cut = least;
+    if (!kTakes) least = fmaxf(least, sh.live);
     row.template blocks<kDeep>([&](const auto &b, int j0, int n) {
         uint32_t todo = 0;  // blocks that hold a value to look at
 #pragma unroll
         for (int q = 0; q < kDeep; ++q) {
             const float m = b[q].top();
             if (q >= n) continue;
-            if constexpr (kTakes) {
-                if (kMode == kTakeAndSum && octaves(sc, m) < kFar) {
-                    float part = 0.f;
+            if (kMode == kTakeAndSum && octaves(sc, m) < kFar) {
+                float part = 0.f;
 #pragma unroll
-                    for (int i = 0; i < B::kN; ++i) part += exp2_approx(-octaves(sc, b[q].get(i)));
-                    sum += part;
-                }
-                if (m >= least) todo |= 1u << q;
-            } else {
-                const bool on = is_live(sc, m) && m >= least;
-                if constexpr (kMode == kCounts) {
-                    if (on) {
-#pragma unroll
-                        for (int i = 0; i < B::kN; ++i) value(b[q].get(i));
-                    }
-                } else {
-                    todo |= on ? 1u << q : 0;
-                }
+                for (int i = 0; i < B::kN; ++i) part += exp2_approx(-octaves(sc, b[q].get(i)));
+                sum += part;
             }
+            if (m >= least) todo |= 1u << q;
         }
 #pragma unroll 1
         while (todo) {
@@ -466,10 +423,10 @@ __device__ __noinline__ void pass(Shared &sh, uint32_t lo, uint32_t hi, int arg)
 #pragma unroll
             for (int q = 1; q < kDeep; ++q)
                 if (at_q == q) one = b[q];
-            if constexpr (kTakes) {
-                uint32_t hits = 0;
+            uint32_t hits = 0;
 #pragma unroll
-                for (int i = 0; i < B::kN; ++i) hits |= one.get(i) >= least ? 1u << i : 0;
+            for (int i = 0; i < B::kN; ++i) hits |= one.get(i) >= least && one.get(i) <= most ? 1u << i : 0;
+            if constexpr (kTakes) {
                 int at = atomicAdd(&sh.listed, __popc(hits));
                 const int token = (j0 + 32 * at_q) * B::kN - row.shift;
 #pragma unroll 1
@@ -479,12 +436,34 @@ __device__ __noinline__ void pass(Shared &sh, uint32_t lo, uint32_t hi, int arg)
                     if (at < kList) sh.list[at] = (u64)~key_of(l) << 32 | (uint32_t)(token + i);
                     ++at;
                 }
-            } else if constexpr (kMode == kRange || kMode == kCounts || kMode == kCountKeys) {
-#pragma unroll 1
-                for (int i = 0; i < B::kN; ++i) value(one.take());
+            } else if constexpr (kMode == kCounts || kMode == kCountKeys) {
+#pragma unroll
+                for (int i = 0; i < B::kN; ++i) {
+                    const float l = one.get(i);
+                    if (hits >> i & 1)
+                        atomicAdd(&sh.lo[kMode == kCounts ? bin_of(sc, l) : (int)((hi - key_of(l)) >> arg)], 1u);
+                }
             } else {
 #pragma unroll
-                for (int i = 0; i < B::kN; i += 2) pair(one.get(i), one.get(i + 1));
+                for (int i = 0; i < B::kN; i += 2) {
+                    if (!(hits >> i & 3)) continue;
+                    u64 w[2];
+                    weight2(sc, one.get(i), one.get(i + 1), sh.powers, w[0], w[1]);
+#pragma unroll
+                    for (int o = 0; o < 2; ++o) {
+                        const float l = one.get(i + o);
+                        if (!(hits >> (i + o) & 1)) continue;
+                        if constexpr (kMode == kFinal) {
+                            if (l > cut) wsum += w[o];
+                            ties += l == cut;
+                        } else {
+                            const int bin = kMode == kWeightKeys ? (int)((hi - key_of(l)) >> arg) : bin_of(sc, l);
+                            const uint32_t low = (uint32_t)w[o], old = atomicAdd(&sh.lo[bin], low);
+                            const uint32_t high = (uint32_t)(w[o] >> 32) + (old + low < old);
+                            if (high) atomicAdd(&sh.hi[bin], high);
+                        }
+                    }
+                }
             }
         }
     });
@@ -501,14 +480,6 @@ __device__ __noinline__ void pass(Shared &sh, uint32_t lo, uint32_t hi, int arg)
         if (lane == 0) {
             sh.wsum[warp] = wsum;
             sh.ties[warp] = ties;
-        }
-    }
-    if (kMode == kRange) {
-        kmin = __reduce_min_sync(0xffffffffu, kmin);
-        kmax = __reduce_max_sync(0xffffffffu, kmax);
-        if (lane == 0) {
-            sh.kmin[warp] = kmin;
-            sh.kmax[warp] = kmax;
         }
     }
     __syncthreads();
@@ -566,6 +537,41 @@ __device__ __noinline__ bool find_bin(Shared &sh, u64 target) {
     return target <= sh.scanned;
 }
 
+// The largest key of a bf16 value up to this one.
+__device__ __forceinline__ uint32_t bf16_key(uint32_t key) {
+    return key >= 0x80000000u ? key & 0xffff0000u : ((key + 1) & 0xffff0000u) - 1;
+}
+
+// The least key whose value is live and in bin b or one before it: bins descend with the value, so 32
+// lanes divide what is left by 33 at a time.
+__device__ __noinline__ uint32_t bin_edge(const Scale &sc, int b) {
+    const int lane = threadIdx.x & 31;
+    auto in = [&](uint32_t key) {
+        const float l = value_of(key);
+        return is_live(sc, l) && bin_of(sc, l) <= b;
+    };
+    uint32_t out = key_of(-FLT_MAX) - 1, at = key_of(sc.top);  // (out: not in)
+    while (at - out > 1) {
+        const uint32_t step = max(1u, (at - out) / 33);
+        const uint32_t key = min(at, out + step * (lane + 1));
+        const uint32_t m = __ballot_sync(0xffffffffu, in(key));
+        const int first = m ? __ffs(m) - 1 : 32;
+        const uint32_t from = out;
+        if (first < 32) at = min(at, from + step * (first + 1));
+        if (first > 0) out = min(at - 1, from + step * first);
+    }
+    return at;
+}
+
+// The least live value, for the passes that weigh or count.
+__device__ __forceinline__ void set_live(Shared &sh) {
+    if (threadIdx.x < 32) {
+        const uint32_t edge = bin_edge(sh.sc, kBins - 1);
+        if (threadIdx.x == 0) sh.live = value_of(edge);
+    }
+    __syncthreads();
+}
+
 // Lowers sh.cut to where the running count of the values above it reaches sh.goal (> 0), or (W) their
 // running weight p times the weight of all of them and of the cut's ties. False where that is not
 // reached: the cut stays, and sh.goal is what is wanted of its ties.
@@ -595,36 +601,32 @@ template <typename T, bool W> __device__ __noinline__ bool search(Shared &sh, do
         return false;
     }
     target -= sh.before;
-    // the keys that occur in the bin
-    pass<T, kRange>(sh, cut.key + 1, 0xffffffffu, sh.bin);
-    uint32_t kmin = 0xffffffffu, kmax = 0;
-    for (int i = 0; i < kWarps; ++i) {
-        kmin = min(kmin, sh.kmin[i]);
-        kmax = max(kmax, sh.kmax[i]);
+    // the bin's keys; bf16 values' are 2^16 apart
+    constexpr int kStep = sizeof(T) == 2 ? 16 : 0;
+    const int bin = sh.bin;
+    if (threadIdx.x < 64) {
+        const uint32_t edge = threadIdx.x < 32 ? bin_edge(sh.sc, bin)
+                              : bin            ? bin_edge(sh.sc, bin - 1) - 1
+                                               : key_of(sh.sc.top);
+        if ((threadIdx.x & 31) == 0) sh.edges[threadIdx.x / 32] = edge;
     }
-    if (threadIdx.x == 0) {
-        sh.first = kmin;
-        sh.last = kmax;
-    }
-    cl.sync();
-    for (int c = 0; c < (int)cl.num_blocks(); ++c) {
-        const Shared *o = cl.map_shared_rank(&sh, c);
-        kmin = min(kmin, o->first);
-        kmax = max(kmax, o->last);
-    }
-    cl.sync();
+    __syncthreads();
+    uint32_t kmin = max(sh.edges[0], cut.key + 1), kmax = sh.edges[1];
+    if (kStep) kmax = bf16_key(kmax);
     while (kmin < kmax) {
-        const int shift = max(0, 32 - __clz(kmax - kmin) - 10);
+        const int shift = max(kStep, 32 - __clz(kmax - kmin) - 10);
         clear_bins(sh);
         pass<T, W ? kWeightKeys : kCountKeys>(sh, kmin, kmax, shift);
         share_bins(sh);
         find_bin(sh, target);
         target -= sh.before;
         kmax -= (uint32_t)sh.bin << shift;
+        if (shift <= kStep) break;
         const uint32_t width = (1u << shift) - 1;
         if (kmax - kmin > width) kmin = kmax - width;
-        if (shift == 0) break;
+        if (kStep) kmax = bf16_key(kmax);
     }
+    if (kStep) kmax = bf16_key(kmax);
     // ties that are needed to reach the target
     const u64 one = W ? weigh(sh, value_of(kmax)) : 1;
     __syncthreads();
@@ -633,60 +635,17 @@ template <typename T, bool W> __device__ __noinline__ bool search(Shared &sh, do
     return true;
 }
 
-// Puts the first n of the list in ascending order.
+// Puts the first n of the list in ascending order: a thread counts what comes before its entry.
 __device__ __noinline__ void sort_list(Shared &sh, int n) {
-    if (n <= kCount) {
-        u64 mine = 0;
-        int at = 0;
-        if ((int)threadIdx.x < n) {
-            mine = sh.list[threadIdx.x];
+    const bool on = (int)threadIdx.x < n;
+    const u64 mine = on ? sh.list[threadIdx.x] : 0;
+    int at = 0;
+    if (on) {
 #pragma unroll 4
-            for (int i = 0; i < n; ++i) at += sh.list[i] < mine;
-        }
-        __syncthreads();
-        if ((int)threadIdx.x < n) sh.list[at] = mine;
-        __syncthreads();
-        return;
-    }
-    // A bitonic network: a thread holds entries warp 128 + 32 q + lane, q < 4, so that steps of less
-    // than 32 are shuffles, of 32 and 64 registers, and only longer ones meet in shared memory.
-    static_assert(kList == 4 * kThr, "four entries a thread");
-    int size = 2 * kCount;
-    while (size < n) size *= 2;
-    const int lane = threadIdx.x & 31, base = (threadIdx.x >> 5) * 128 + lane;
-    u64 v[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) v[q] = base + 32 * q < n ? sh.list[base + 32 * q] : ~0ull;
-#pragma unroll 1
-    for (int k = 2; k <= size; k *= 2) {
-#pragma unroll 1
-        for (int j = k / 2; j > 0; j /= 2) {
-            u64 o[4];
-            if (j >= 128) {
-                __syncthreads();
-#pragma unroll
-                for (int q = 0; q < 4; ++q) sh.list[base + 32 * q] = v[q];
-                __syncthreads();
-#pragma unroll
-                for (int q = 0; q < 4; ++q) o[q] = sh.list[(base + 32 * q) ^ j];
-            } else if (j >= 32) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) o[q] = j == 32 ? v[q ^ 1] : v[q ^ 2];
-            } else {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) o[q] = __shfl_xor_sync(0xffffffffu, v[q], j);
-            }
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int i = base + 32 * q;
-                const bool low = ((i & k) == 0) == ((i & j) == 0);  // this one keeps the lesser
-                if ((o[q] < v[q]) == low) v[q] = o[q];
-            }
-        }
+        for (int i = 0; i < n; ++i) at += sh.list[i] < mine;
     }
     __syncthreads();
-#pragma unroll
-    for (int q = 0; q < 4; ++q) sh.list[base + 32 * q] = v[q];
+    if (on) sh.list[at] = mine;
     __syncthreads();
 }
 
@@ -728,102 +687,48 @@ __device__ __noinline__ void set_limit(Shared &sh, double z, double error) {
 __device__ __noinline__ bool choose(Shared &sh, int n, bool of_list) {
     const Task &ask = sh.task;
     const bool by_p = ask.top_p < 1.f;
-    if (of_list && n > kCount / 2) set_limit(sh, (double)list_weight(sh, n), 0.0);
     u64 limit = sh.limit, limit_lo = sh.limit_lo, limit_hi = sh.limit_hi;
     u64 *weights = reinterpret_cast<u64 *>(sh.lo);
-    bool sure = true;
-    if (n <= kCount / 2) {
-        // a thread for each token adds up what it needs itself
-        const int i = threadIdx.x;
-        const bool on = i < n;
-        const u64 e = on ? sh.list[i] : 0;
-        const uint32_t key = ~(uint32_t)(e >> 32);
-        const float l = value_of(key);
-        const u64 w = on ? weigh(sh, l) : 0;
-        if (on) weights[i] = w;
-        __syncthreads();
-        u64 before = 0;
-        if (on) {
+    // a thread for each token adds up what it needs itself
+    const int i = threadIdx.x;
+    const bool on = i < n;
+    const u64 e = on ? sh.list[i] : 0;
+    const uint32_t key = ~(uint32_t)(e >> 32);
+    const float l = value_of(key);
+    const u64 w = on ? weigh(sh, l) : 0;
+    if (on) weights[i] = w;
+    __syncthreads();
+    u64 before = 0;
+    if (on) {
 #pragma unroll 4
-            for (int q = 0; q < i; ++q) before += weights[q];
-        }
-        if (of_list) {
-            if (i == n - 1) sh.z = before + w;
-            __syncthreads();
-            set_limit(sh, (double)sh.z, 0.0);
-            limit = limit_lo = limit_hi = sh.limit;
-        }
-        bool kept = w > 0 && key >= ask.low_key;
-        if (by_p && i > 0 && kept) {
-            sure = before < limit_lo || before >= limit_hi;
-            kept = before < limit;
-        }
-        const int keep = __syncthreads_count(kept);
-        if (!__syncthreads_and(sure)) return false;
-        if (i == keep - 1) {
-            sh.z = before + w;
-            sh.target = aim(ask.u, before + w);
-        }
+        for (int q = 0; q < i; ++q) before += weights[q];
+    }
+    if (of_list) {
+        if (i == n - 1) sh.z = before + w;
         __syncthreads();
-        if (kept) {
-            const u64 target = sh.target;
-            u64 at = 0;
-#pragma unroll 4
-            for (int q = 0; q < keep; ++q)
-                if ((uint32_t)sh.list[q] < (uint32_t)e) at += weights[q];
-            if (at <= target && target < at + w) emit(sh, (int)(uint32_t)e, l, sh.z);
-        }
-        return true;
+        set_limit(sh, (double)sh.z, 0.0);
+        limit = limit_lo = limit_hi = sh.limit;
     }
-    // four entries of the order a thread
-    const int i0 = 4 * threadIdx.x;
-    u64 w[4], own = 0;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        w[q] = i0 + q < n ? weigh(sh, value_of(~(uint32_t)(sh.list[i0 + q] >> 32))) : 0;
-        own += w[q];
+    bool kept = w > 0 && key >= ask.low_key, sure = true;
+    if (by_p && i > 0 && kept) {
+        sure = before < limit_lo || before >= limit_hi;
+        kept = before < limit;
     }
-    u64 before = block_scan(sh, own);
-    int keep = 0;
-    own = 0;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        bool kept = w[q] > 0 && ~(uint32_t)(sh.list[i0 + q] >> 32) >= ask.low_key;
-        if (by_p && i0 + q > 0 && kept) {
-            if (before >= limit_lo && before < limit_hi) sure = false;
-            kept = before < limit;
-        }
-        before += w[q];
-        keep += kept;
-        own += kept ? w[q] : 0;
-    }
+    const int keep = __syncthreads_count(kept);
     if (!__syncthreads_and(sure)) return false;
-    block_scan(sh, own);
-    const u64 z = sh.scanned;
-    __syncthreads();
-    block_scan(sh, (u64)keep);
-    keep = (int)sh.scanned;
-    if (threadIdx.x == 0) sh.target = aim(ask.u, z);
-    // what is kept, in the order of the tokens
-    for (int i = threadIdx.x; i < keep; i += kThr) {
-        const u64 e = sh.list[i];
-        sh.list[i] = e << 32 | (uint32_t)~(uint32_t)(e >> 32);  // index, key
+    if (i == keep - 1) {
+        sh.z = before + w;
+        sh.target = aim(ask.u, before + w);
     }
     __syncthreads();
-    const u64 target = sh.target;
-    sort_list(sh, keep);
-    own = 0;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        w[q] = i0 + q < keep ? weigh(sh, value_of((uint32_t)sh.list[i0 + q])) : 0;
-        own += w[q];
-    }
-    before = block_scan(sh, own);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        if (before <= target && target < before + w[q])
-            emit(sh, (int)(sh.list[i0 + q] >> 32), value_of((uint32_t)sh.list[i0 + q]), z);
-        before += w[q];
+    if (kept) {
+        // in the order of the tokens
+        const u64 target = sh.target;
+        u64 at = 0;
+#pragma unroll 4
+        for (int q = 0; q < keep; ++q)
+            if ((uint32_t)sh.list[q] < (uint32_t)e) at += weights[q];
+        if (at <= target && target < at + w) emit(sh, (int)(uint32_t)e, l, sh.z);
     }
     return true;
 }
@@ -841,12 +746,8 @@ template <typename T> __device__ __noinline__ bool from_list(Shared &sh, int wan
     if (threadIdx.x == 0) sh.listed = 0;
     if (want) {
         clear_bins(sh);
-        if (want <= kThr / 2 * ctas) {
-            // as many threads' largest values: at least as many values
-            if (is_live(sh.sc, own)) atomicAdd(&sh.lo[bin_of(sh.sc, own)], 1u);
-        } else {
-            pass<T, kCounts>(sh, 0, 0xffffffffu, 0);
-        }
+        // as many threads' largest values: at least as many values
+        if (is_live(sh.sc, own)) atomicAdd(&sh.lo[bin_of(sh.sc, own)], 1u);
         share_bins(sh);
         if (find_bin(sh, want)) last = sh.bin;
     }
@@ -886,14 +787,14 @@ template <typename T> __device__ __noinline__ bool from_list(Shared &sh, int wan
         int n = __shfl_sync(0xffffffffu, before, kMaxCluster - 1);
         z_all = __shfl_sync(0xffffffffu, z_all, 0);
         bool fine = n <= kList;
-        if (threadIdx.x < ctas) sh.kmin[lane] = before;  // (the list's ends)
+        if (threadIdx.x < ctas) sh.ends_of[lane] = before;
         __syncthreads();
         if (fine) {
             const int own = sh.listed;
             for (int i = own + threadIdx.x; i < n; i += kThr) {
                 int c = 0, first = 0;
                 for (int o = 1; o < ctas; ++o) {
-                    const int x = (int)sh.kmin[o - 1];
+                    const int x = sh.ends_of[o - 1];
                     if (i >= x) {
                         c = o;
                         first = x;
@@ -921,6 +822,7 @@ template <typename T> __device__ __noinline__ bool from_list(Shared &sh, int wan
     int settled = cl.map_shared_rank(&sh, 0)->settled;
     if (settled == 2) {
         // a border lies within the error of the fp32 sum: the row's weight as it is
+        set_live(sh);
         pass<T, kFinal>(sh, 0, 0xffffffffu, 0);
         if (threadIdx.x < kWarps) {
             u64 sum = sh.wsum[threadIdx.x];
@@ -953,7 +855,7 @@ template <typename T> __device__ __noinline__ void from_row(Shared &sh) {
         sh.cut = Cut{0, 0};
         sh.goal = ask.k;
     }
-    __syncthreads();
+    set_live(sh);
     if (ask.k) search<T, false>(sh, 0.0);
     if (ask.top_p < 1.f) {
         const Cut before = sh.cut;
@@ -995,57 +897,96 @@ template <typename T> __device__ __noinline__ void from_row(Shared &sh) {
         }
         __syncthreads();
     }
-    if (sh.owner == rank * kWarps + warp) {
+    // The CTA whose warp holds the token: all its warps share that warp's blocks and add up their parts,
+    // then the one that holds it adds up 32 blocks at a time.
+    if (sh.owner >= 0 && sh.owner / kWarps == rank) {
         const Scale sc = sh.sc;
+        const float least = cut.key > key_of(-INFINITY) ? value_of(cut.key) : -INFINITY;
         const u64 goal = sh.target;
-        u64 w_at = sh.own_w, t_at = sh.own_t;
-#pragma unroll 1
-        for (int j0 = row.w0; j0 < row.w1; j0 += 32) {
-            const int j = j0 + lane;
-            u64 w = 0, t = 0;
-            B b;
-            if (j < row.w1) {
-                b = row.block(j);
-                B c = b;
-#pragma unroll 1
-                for (int i = 0; i < B::kN; ++i) {
-                    const float l = c.take();
-                    if (!is_live(sc, l)) continue;
-                    if (key_of(l) > cut.key) w += weigh(sh, l);
-                    t += key_of(l) == cut.key;
+        const int from = min(ask.b1, ask.b0 + sh.owner % kWarps * ask.per), to = min(ask.b1, from + ask.per);
+        const int rounds = (to - from + 31) / 32, each = (rounds + kWarps - 1) / kWarps;
+        const int j_from = from + warp * each * 32, j_to = min(to, j_from + each * 32);
+        // a block's weight and ties
+        auto block_sums = [&](const B &b, u64 &w, u64 &t) {
+#pragma unroll 2
+            for (int i = 0; i < B::kN; i += 2) {
+                const float l0 = b.get(i), l1 = b.get(i + 1);
+                u64 x, y;
+                weight2(sc, l0, l1, sh.powers, x, y);
+                if (l0 >= sh.live) {
+                    if (l0 > least) w += x;
+                    t += l0 == least;
+                }
+                if (l1 >= sh.live) {
+                    if (l1 > least) w += y;
+                    t += l1 == least;
                 }
             }
-            u64 ws = w, ts = t;
+        };
+        u64 w_at = 0, t_at = 0;
+#pragma unroll 1
+        for (int turn = 0; turn < 2; ++turn) {
+            u64 w_all = 0, t_all = 0;
+            if (turn == 1 && sh.part_owner != warp) break;
+#pragma unroll 1
+            for (int j0 = j_from; j0 < j_to; j0 += 32) {
+                const int j = j0 + lane;
+                u64 w = 0, t = 0;
+                B b;
+                if (j < j_to) {
+                    b = row.block(j);
+                    block_sums(b, w, t);
+                }
+                u64 ws = w, ts = t;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const u64 x = __shfl_up_sync(0xffffffffu, ws, o), y = __shfl_up_sync(0xffffffffu, ts, o);
-                if (lane >= o) {
-                    ws += x;
-                    ts += y;
-                }
-            }
-            const bool here = goal < total(w_at + ws, t_at + ts);
-            const uint32_t m = __ballot_sync(0xffffffffu, here);
-            if (m) {
-                if (lane == __ffs(m) - 1) {
-                    w = w_at + ws - w;
-                    t = t_at + ts - t;
-#pragma unroll 1
-                    for (int i = 0; i < B::kN; ++i) {
-                        const float l = b.take();
-                        if (!is_live(sc, l)) continue;
-                        if (key_of(l) > cut.key) w += weigh(sh, l);
-                        t += key_of(l) == cut.key;
-                        if (goal < total(w, t)) {
-                            emit(sh, j * B::kN - row.shift + i, l, sh.z);
-                            break;
-                        }
+                for (int o = 1; o < 32; o <<= 1) {
+                    const u64 x = __shfl_up_sync(0xffffffffu, ws, o), y = __shfl_up_sync(0xffffffffu, ts, o);
+                    if (lane >= o) {
+                        ws += x;
+                        ts += y;
                     }
                 }
-                break;
+                const uint32_t m = __ballot_sync(0xffffffffu, turn == 1 && goal < total(w_at + ws, t_at + ts));
+                if (m) {
+                    if (lane == __ffs(m) - 1) {
+                        w = w_at + ws - w;
+                        t = t_at + ts - t;
+#pragma unroll 1
+                        for (int i = 0; i < B::kN; ++i) {
+                            const float l = b.take();
+                            if (!(l >= sh.live)) continue;
+                            if (l > least) w += weigh(sh, l);
+                            t += l == least;
+                            if (goal < total(w, t)) {
+                                emit(sh, j * B::kN - row.shift + i, l, sh.z);
+                                break;
+                            }
+                        }
+                    }
+                    break;
+                }
+                w_all += __shfl_sync(0xffffffffu, ws, 31);
+                t_all += __shfl_sync(0xffffffffu, ts, 31);
+                if (turn == 1) {
+                    w_at += __shfl_sync(0xffffffffu, ws, 31);
+                    t_at += __shfl_sync(0xffffffffu, ts, 31);
+                }
             }
-            w_at += __shfl_sync(0xffffffffu, ws, 31);
-            t_at += __shfl_sync(0xffffffffu, ts, 31);
+            if (turn == 1) break;
+            if (lane == 0) {
+                sh.part_w[warp] = w_all;
+                sh.part_t[warp] = t_all;
+            }
+            __syncthreads();
+            w_at = sh.own_w;
+            t_at = sh.own_t;
+            for (int i = 0; i < warp; ++i) {
+                w_at += sh.part_w[i];
+                t_at += sh.part_t[i];
+            }
+            if (lane == 0 && total(w_at, t_at) <= goal && goal < total(w_at + w_all, t_at + t_all))
+                sh.part_owner = warp;
+            __syncthreads();
         }
     }
     cl.sync();  // (shared memory of CTAs that have ended is not to be read)
@@ -1101,6 +1042,7 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const Args a, int held_
         t.logprob = a.logprob ? a.logprob + r : nullptr;
         sh.index = 0xffffffffu;
         sh.owner = -1;
+        sh.part_owner = -1;
     } else if (threadIdx.x == 32) {
         float temp = a.temperature ? a.temperature[r / a.group] : 1.f;
         temp = fminf(fmaxf(temp, 1e-30f), 1e30f);
@@ -1187,7 +1129,7 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const Args a, int held_
     __syncthreads();
     // what is kept may fit a list: k tokens, or those that min-p leaves, or top-p's as a guess
     if (t.k ? t.k <= kAsk : by_m || t.top_p < 1.f)
-        if (from_list<T>(sh, t.k ? t.k : by_m ? 0 : kGuess, own)) return;
+        if (from_list<T>(sh, t.k ? t.k : by_m ? 0 : kAsk, own)) return;
     from_row<T>(sh);
 }
 
@@ -1195,11 +1137,16 @@ constexpr int kHeldBytes = 76 * 1024;  // of a row in a CTA: two CTAs share an S
 
 template <typename T> cudaError_t launch(const Args &a, cudaStream_t s) {
     const int blocks = (a.V + 2 * Block<T>::kN - 2) / Block<T>::kN;
-    const int room = kHeldBytes / 16, slots = 2 * std::max(1, device_sms());
-    // more CTAs a row only where the GPU has room for them: barriers over a cluster cost more than what
-    // they save where rows wait
-    int ctas = 1;
-    while (ctas < kMaxCluster && (long long)a.R * ctas * 2 <= slots && blocks / ctas > 2 * kThr) ctas *= 2;
+    const int room = kHeldBytes / 16, sms = std::max(1, device_sms());
+    // CTAs of a row, for rows long enough. Few rows take several; with more rows the cluster's barriers
+    // cost more than what they save. Rows of bf16 151936, us by 1, 2, 4 and 8 CTAs a row: 16 rows with
+    // top-k 20: 19.5, 17.6, 14.9, 16.2; 65: 19.8, 18.1, 18.5, 31.9; 100: 19.7, 23.5, 29.9, 46; 1040: 105,
+    // 159, 248, 438. Rows that no list serves are bound by instructions, and gain from a second CTA up to
+    // where all of them run at once: without cuts 16 rows 78, 46, 30, 28; 65: 78, 47, 47, 61; 192: 138, 109,
+    // 122, 152; 304: 140, 142, 182, 236. That is to be expected where neither top-k nor min-p is asked for.
+    const bool open = !a.top_k && !a.min_p;
+    int ctas = a.R <= sms / 16 ? 8 : a.R <= sms / 2 ? 4 : a.R <= (open ? 3 * sms / 2 : 0) ? 2 : 1;
+    while (ctas > 1 && blocks / ctas < kThr) ctas /= 2;
     const int per = (blocks + ctas - 1) / ctas;
     const int held = per <= room ? per : 0;
     cudaError_t err = allow_smem(sample_kernel<T>, kHeldBytes);
