@@ -35,7 +35,8 @@ WsLayout ws_layout(const moe_layer_desc &L, int R) {
 namespace {
 
 constexpr int kThr = 512, kWarps = kThr / 32;
-constexpr int kRedBytes = 16 * 1024;  // one buffer of the warps' partial sums
+// One buffer of the warps' partial sums: 16 rows of a token of every warp take 1 KB.
+__host__ __device__ inline int red_bytes(int R) { return R <= 8 ? 8 * 1024 : 16 * 1024; }
 
 // Bytes between two tokens in shared memory: 64 bytes past whole lines, so that the 16-byte reads of
 // two tokens' quarters of a line do not meet in a bank.
@@ -412,27 +413,36 @@ __device__ __forceinline__ void choose(const Args &a, Plan &s, uint32_t tag) {
         }
         float mine = -INFINITY, top = 0.f;  // lane j: the j-th chosen score
         int who = 0;
-        // the lane's largest, and its place; only the lane that loses it looks again
-        uint32_t own = 0;
-        int at = 0;
-        auto look = [&]() {
-            own = 0;
+        // the lane's keys in descending order (ties to the lower expert), so that what is next is at hand
+        int id[kMaxE / 32];
 #pragma unroll
-            for (int i = kMaxE / 32 - 1; i >= 0; --i)
-                if (key[i] >= own) {
-                    own = key[i];
-                    at = i;
-                }
-        };
-        look();
+        for (int i = 0; i < kMaxE / 32; ++i) id[i] = i * 32 + lane;
+        const int held = (a.E + 31) / 32;
+#pragma unroll
+        for (int n = 1; n < kMaxE / 32; ++n) {
+            if (n >= held) break;
+#pragma unroll
+            for (int i = n; i > 0; --i) {
+                const bool up = key[i] > key[i - 1];
+                const uint32_t k0 = up ? key[i] : key[i - 1], k1 = up ? key[i - 1] : key[i];
+                const int i0 = up ? id[i] : id[i - 1], i1 = up ? id[i - 1] : id[i];
+                key[i - 1] = k0;
+                key[i] = k1;
+                id[i - 1] = i0;
+                id[i] = i1;
+            }
+        }
+#pragma unroll 1
         for (int j = 0; j < a.k; ++j) {
-            const uint32_t best = __reduce_max_sync(0xffffffffu, own);
-            const int e = (int)__reduce_min_sync(0xffffffffu, own == best ? (unsigned)(at * 32 + lane) : (unsigned)kMaxE);
-            if ((e & 31) == lane) {
+            const uint32_t best = __reduce_max_sync(0xffffffffu, key[0]);
+            const int e = (int)__reduce_min_sync(0xffffffffu, key[0] == best ? (unsigned)id[0] : (unsigned)kMaxE);
+            if (e == id[0]) {
 #pragma unroll
-                for (int i = 0; i < kMaxE / 32; ++i)
-                    if (i == at) key[i] = 0;
-                look();
+                for (int i = 0; i + 1 < kMaxE / 32; ++i) {
+                    key[i] = key[i + 1];
+                    id[i] = id[i + 1];
+                }
+                key[kMaxE / 32 - 1] = 0;
             }
             const float v = __uint_as_float(best ^ ((int)best < 0 ? 0x80000000u : 0xffffffffu));
             if (j == 0) top = v;
@@ -565,7 +575,7 @@ struct Run {
         j0 = (int)(p - (long long)ui * a.f);
         mask = s.tokens[s.expert[ui]];
         m = __popc(mask);
-        const int most = kRedBytes / (kWarps * 16 * 4 * m);
+        const int most = red_bytes(a.R) / (kWarps * 16 * 4 * m);
         nj = (int)min(min((long long)(a.f - j0), p1 - p), 8ll * most);
         tiles = (nj + 7) / 8;
     }
@@ -593,8 +603,10 @@ struct Columns {
 template <int D> struct Feed {
     const Args &a;
     const Plan &s;
-    uint32_t base, put;  // the lane's bytes of entry 0, offset of the next entry
-    uint32_t acts;       // from the weights' ring to the activations'
+    uint32_t base, put;      // the lane's bytes of entry 0, offset of the next entry
+    // The same of the activations' ring: an entry has the values and the rests of as many columns as
+    // there may be, 64 bytes each.
+    uint32_t h_base, h_put;
     // the segment, as the lane sees it
     const __nv_bfloat16 *x, *y, *h;  // two rows of weights, and of activations
     int c, end, left;                // inner element, where the rows end, entries left
@@ -608,8 +620,10 @@ template <int D> struct Feed {
         : a(a_), s(s_) {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         base = (uint32_t)__cvta_generic_to_shared(ring) + warp * D * 1024 + lane * 16;
-        acts = (uint32_t)(h_ring - ring);
         put = 0;
+        h_base = (uint32_t)__cvta_generic_to_shared(h_ring) + warp * D * slot() + (lane >> 2) * 128 +
+                 (lane & 3) * 16;
+        h_put = 0;
         pair = first_pair(a, s, blockIdx.x);
         pair1 = first_pair(a, s, blockIdx.x + 1);
         nj = tiles = left = 0;
@@ -617,6 +631,7 @@ template <int D> struct Feed {
         down = done = false;
         segment();
     }
+    __device__ __forceinline__ uint32_t slot() const { return min(a.R, 8) * 128; }
     // Activations of the lane's column of an expert, from element c on: the expert's g-th token's.
     __device__ __forceinline__ const __nv_bfloat16 *activations(int ui, int col, int c) const {
         const int e = s.expert[ui];
@@ -687,9 +702,12 @@ template <int D> struct Feed {
             const bool in = c < end;
             copy16(base + put, x, in ? nx : 0);
             copy16(base + put + 512, y, in ? ny : 0);
-            if (H && in && nh) {
-                copy16(base + put + acts, h, 16);
-                copy16(base + put + acts + 512, h + a.f, 16);
+            if (H) {
+                if (in && nh) {
+                    copy16(h_base + h_put, h, 16);
+                    copy16(h_base + h_put + 64, h + a.f, 16);
+                }
+                h_put = h_put + slot() == D * slot() ? 0 : h_put + slot();
             }
             x += 32;
             y += 32;
@@ -701,23 +719,35 @@ template <int D> struct Feed {
         put = put + 1024 == D * 1024 ? 0 : put + 1024;
     }
     // The activations of the entries of step 3 that were copied before there were any.
-    __device__ __forceinline__ void catch_up(uint32_t take) const {
+    __device__ __forceinline__ void catch_up() {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
         const int nk = groups(a.f), q0 = part(s.n * nk, warp), q1 = part(s.n * nk, warp + 1);
-        const int entries = (q1 - q0) * Columns(a).tiles;
+        int todo = min(D - 1, (q1 - q0) * Columns(a).tiles);
+        const int none = D - 1 - todo;
 #pragma unroll 1
-        for (int i = 0; i < D - 1; ++i) {
-            if (i < entries) {
-                const int q = q0 + i % (q1 - q0), e = q / nk, c = (q - e * nk) * 32 + 8 * t;
+        while (todo > 0) {  // (again from q0 where the warp's part is shorter than the ring)
+#pragma unroll 1
+            for (int q = q0; q < q1 && todo > 0;) {
+                const int e = q / nk, n = min(min(nk - (q - e * nk), q1 - q), todo);
+                const bool on = g < columns(e);
+                int c = (q - e * nk) * 32 + 8 * t;
                 const __nv_bfloat16 *p = activations(e, g, c);
-                if (c < a.f && g < columns(e)) {
-                    copy16(base + take + acts, p, 16);
-                    copy16(base + take + acts + 512, p + a.f, 16);
+#pragma unroll 1
+                for (int i = 0; i < n; ++i, c += 32, p += 32) {
+                    if (on && c < a.f) {
+                        copy16(h_base + h_put, p, 16);
+                        copy16(h_base + h_put + 64, p + a.f, 16);
+                    }
+                    h_put = h_put + slot() == D * slot() ? 0 : h_put + slot();
+                    asm volatile("cp.async.commit_group;" ::: "memory");
                 }
-                take = take + 1024 == D * 1024 ? 0 : take + 1024;
+                q += n;
+                todo -= n;
             }
-            asm volatile("cp.async.commit_group;" ::: "memory");
         }
+        // (as many groups as there are entries before an entry is waited for)
+#pragma unroll 1
+        for (int i = 0; i < none; ++i) asm volatile("cp.async.commit_group;" ::: "memory");
     }
 };
 
@@ -751,7 +781,7 @@ template <int NT, int D> struct Experts {
         for (long long p = first_pair(a, s, blockIdx.x); p < p1;) {
             const Run r(a, s, p, p1);
             const int m = r.m;
-            float *out = red + buf * (kRedBytes / 4);
+            float *out = red + buf * (red_bytes(a.R) / 4);
             // this lane's columns: tokens g and g + 8 of the expert's
             const char *x0 = g < m ? xs + nth_token(r.mask, g) * stride : nullptr;
             const char *x1 = g + 8 < m ? xs + nth_token(r.mask, g + 8) * stride : nullptr;
@@ -796,14 +826,15 @@ template <int NT, int D> struct Experts {
 
     __device__ __forceinline__ void down(float *red) {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-        float *mine = red + (size_t)warp * 16 * kMaxRows;
+        float *mine = red + (size_t)warp * 16 * a.R;
         const Columns cols(a);
         const int nk = groups(a.f), q0 = part(s.n * nk, warp), q1 = part(s.n * nk, warp + 1);
-        feed.catch_up(take);
+        feed.catch_up();
+        uint32_t h_take = 0;
 #pragma unroll 1
         for (int tile = 0; tile < cols.tiles; ++tile) {
             const int b0 = cols.at(tile), b1 = cols.at(tile + 1);
-            for (int i = lane; i < 16 * kMaxRows; i += 32) mine[i] = 0.f;
+            for (int i = lane; i < 16 * a.R; i += 32) mine[i] = 0.f;
             __syncwarp();
             int ui = q0 / nk;
 #pragma unroll 1
@@ -821,9 +852,10 @@ template <int NT, int D> struct Experts {
                     const uint4 x = shared16(at), y = shared16(at + 512);
                     uint4 u = make_uint4(0, 0, 0, 0), v = u;
                     if (g < m && c < a.f) {
-                        u = shared16(at + feed.acts);
-                        v = shared16(at + feed.acts + 512);
+                        u = shared16(feed.h_base + h_take);
+                        v = shared16(feed.h_base + h_take + 64);
                     }
+                    h_take = h_take + feed.slot() == D * feed.slot() ? 0 : h_take + feed.slot();
                     feed.template fill<true>();
                     mma32(hi, x, y, u);
                     mma32(lo, x, y, v);
@@ -844,14 +876,14 @@ template <int NT, int D> struct Experts {
                 for (int k = 0; k < 2; ++k) {
                     const int col = 2 * t + k;
                     if (col < m) {
-                        float *o = mine + g * kMaxRows + nth_token(mask, col);
+                        float *o = mine + g * a.R + nth_token(mask, col);
                         o[0] += hi[k] + lo[k];
-                        o[8 * kMaxRows] += hi[2 + k] + lo[2 + k];
+                        o[8 * a.R] += hi[2 + k] + lo[2 + k];
                     }
                     if (NT > 1 && col + 8 < m) {
-                        float *o = mine + g * kMaxRows + nth_token(mask, col + 8);
+                        float *o = mine + g * a.R + nth_token(mask, col + 8);
                         o[0] += more[k];
-                        o[8 * kMaxRows] += more[2 + k];
+                        o[8 * a.R] += more[2 + k];
                     }
                 }
                 __syncwarp();
@@ -861,7 +893,7 @@ template <int NT, int D> struct Experts {
                 const int r = i / (b1 - b0), col = i - r * (b1 - b0);
                 float v = 0.f;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) v += red[(size_t)(w * 16 + col) * kMaxRows + r];
+                for (int w = 0; w < kWarps; ++w) v += red[(size_t)(w * 16 + col) * a.R + r];
                 store_y<__nv_bfloat16>(a, r, b0 + col, v);
             }
             __syncthreads();  // (the sums are read before the next tile's)
@@ -949,8 +981,12 @@ __device__ __forceinline__ void down(const Args &a, const Plan &s) {
 
 constexpr int kPlanBytes = (sizeof(Plan) + 127) / 128 * 128;
 constexpr int kSmem = 227 * 1024;
-constexpr int kFixed = kPlanBytes + 2 * kRedBytes;
-constexpr int ring_bytes(int D) { return D * kWarps * 1024; }
+inline __host__ __device__ int fixed_bytes(int R) { return kPlanBytes + 2 * red_bytes(R); }
+__host__ __device__ constexpr int ring_bytes(int D) { return D * kWarps * 1024; }
+// Shared memory of a launch; step 3's activations take the tokens' place.
+inline int smem_bytes(int R, int d, int elem, int D) {
+    return fixed_bytes(R) + ring_bytes(D) + std::max(D * kWarps * std::min(R, 8) * 128, R * token_stride(d, elem));
+}
 
 // D = 0: fp32.
 template <typename T, int NT, int D>
@@ -958,8 +994,9 @@ __global__ void __launch_bounds__(kThr, 1) few_kernel(const Args a) {
     extern __shared__ __align__(128) char dyn[];
     Plan &s = *reinterpret_cast<Plan *>(dyn);
     float *red = reinterpret_cast<float *>(dyn + kPlanBytes);
-    const char *ring = dyn + kFixed;
-    char *xs = dyn + kFixed + ring_bytes(D);
+    const char *ring = dyn + fixed_bytes(a.R);
+    char *xs = dyn + fixed_bytes(a.R) + ring_bytes(D);
+    pdl_wait();
     Eight<T> first{};
     if (blockIdx.x < a.E && threadIdx.x * 8 < a.d)
         first.load(reinterpret_cast<const T *>(a.wr) + (size_t)blockIdx.x * a.d + threadIdx.x * 8);
@@ -996,37 +1033,43 @@ template <typename T, int NT, int D> cudaError_t launch(const Args &a, int max_c
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(max_ctas > 0 ? std::min(max_ctas, sms) : sms);
     cfg.blockDim = dim3(kThr);
-    // (step 3's activations take the tokens' place)
-    cfg.dynamicSmemBytes = (size_t)kFixed + ring_bytes(D) +
-                           std::max(ring_bytes(D), a.R * token_stride(a.d, sizeof(T)));
+    cfg.dynamicSmemBytes = smem_bytes(a.R, a.d, sizeof(T), D);
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeCooperative;
     attr[0].val.cooperative = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, few_kernel<T, NT, D>, a);
 }
 
-constexpr int kShallow = 4, kDeep = 5;
+// Rings as deep as shared memory holds: at one token 10 entries a warp (of the 12 that it has of step 3 in
+// the Qwen3-shaped layer, 9 are on their way before the grid's barrier), with 16 tokens 5.
+template <int NT, int D> cudaError_t launch_ring(const Args &a, int max_ctas, cudaStream_t s) {
+    return launch<__nv_bfloat16, NT, D>(a, max_ctas, s);
+}
 
 }  // namespace
 
 int rows_at_once(const moe_layer_desc &L) {
     const int e = (int)elem_size(L.dtype);
-    return std::min(kMaxRows, (kSmem - kFixed - (L.dtype == MOE_DTYPE_F32 ? 0 : ring_bytes(kShallow))) /
-                                  token_stride(L.d, e));
+    int R = kMaxRows;
+    while (R > 1 && smem_bytes(R, L.d, e, L.dtype == MOE_DTYPE_F32 ? 0 : 4) > kSmem) --R;
+    return R;
 }
 
 static_assert(kHeadBytes == MOE_FEW_HEAD_BYTES, "the header says how much is zeroed");
 
 cudaError_t launch_few(const Args &a, int dtype, int max_ctas, cudaStream_t s) {
-    using bf16 = __nv_bfloat16;
     if (dtype == MOE_DTYPE_F32) return launch<float, 1, 0>(a, max_ctas, s);
-    const bool deep = a.R * token_stride(a.d, 2) <= kSmem - kFixed - ring_bytes(kDeep);
+    auto fits = [&](int D) { return smem_bytes(a.R, a.d, 2, D) <= kSmem; };
     if (a.R <= 8)
-        return deep ? launch<bf16, 1, kDeep>(a, max_ctas, s) : launch<bf16, 1, kShallow>(a, max_ctas, s);
-    return deep ? launch<bf16, 2, kDeep>(a, max_ctas, s) : launch<bf16, 2, kShallow>(a, max_ctas, s);
+        return fits(10) ? launch_ring<1, 10>(a, max_ctas, s)
+               : fits(7) ? launch_ring<1, 7>(a, max_ctas, s)
+                         : fits(5) ? launch_ring<1, 5>(a, max_ctas, s) : launch_ring<1, 4>(a, max_ctas, s);
+    return fits(5) ? launch_ring<2, 5>(a, max_ctas, s) : launch_ring<2, 4>(a, max_ctas, s);
 }
 
 }  // namespace few
