@@ -52,6 +52,8 @@ struct Plan {
     Pair part[kWarps], scale[kMaxRows];
     double wide_scale[kMaxRows];
     int wide[kMaxRows];
+    int pair0, pair1;                 // the CTA's share of the pairs of rows of step 2
+    int col0, col1;                   // its output columns
     uint32_t word[kMaxE / 32];
     unsigned long long launch;
     int alive;
@@ -492,7 +494,16 @@ __device__ __forceinline__ void choose(const Args &a, Plan &s, uint32_t tag) {
         s.expert[at] = (short)e;
         s.slot[at] = slot;
     }
-    if (threadIdx.x == 0) s.n = n;
+    // (what needs divisions is computed once: 256 experts of 6144 pairs on a thousand CTAs fit 32 bits)
+    if (threadIdx.x == 0) {
+        s.n = n;
+        const unsigned pairs = n * a.f;
+        s.pair0 = (int)(pairs * blockIdx.x / gridDim.x);
+        s.pair1 = (int)(pairs * (blockIdx.x + 1) / gridDim.x);
+    } else if (threadIdx.x == 32) {
+        s.col0 = (int)((unsigned)a.d * blockIdx.x / gridDim.x);
+        s.col1 = (int)((unsigned)a.d * (blockIdx.x + 1) / gridDim.x);
+    }
     __syncthreads();
 }
 
@@ -570,31 +581,31 @@ __device__ __forceinline__ uint4 shared16(uint32_t p) {
 struct Run {
     int ui, j0, nj, tiles, m;
     unsigned mask;
-    __device__ __forceinline__ Run(const Args &a, const Plan &s, long long p, long long p1) {
-        ui = (int)(p / a.f);
-        j0 = (int)(p - (long long)ui * a.f);
+    __device__ __forceinline__ Run(const Args &a, const Plan &s, int p, int p1) {
+        ui = (int)((unsigned)p / (unsigned)a.f);
+        j0 = p - ui * a.f;
         mask = s.tokens[s.expert[ui]];
         m = __popc(mask);
-        const int most = red_bytes(a.R) / (kWarps * 16 * 4 * m);
-        nj = (int)min(min((long long)(a.f - j0), p1 - p), 8ll * most);
+        // tiles that fit a buffer: red_bytes() / (1 KB m)
+        const int most = (a.R <= 8 ? 8u : 16u) / (unsigned)m;
+        nj = min(min(a.f - j0, p1 - p), 8 * most);
         tiles = (nj + 7) / 8;
     }
 };
-__device__ __forceinline__ long long first_pair(const Args &a, const Plan &s, int cta) {
-    return (long long)s.n * a.f * cta / gridDim.x;
-}
 // The warp's part of n groups of 32 inner elements.
-__device__ __forceinline__ int part(int n, int warp) { return (int)((long long)n * warp / kWarps); }
+__device__ __forceinline__ int part(int n, int warp) { return (int)((unsigned)(n * warp) / kWarps); }
 __device__ __forceinline__ int groups(int n) { return (n + 31) / 32; }
 // Step 3's work: the CTA's output columns, in tiles of up to 16.
 struct Columns {
     int c0, c1, tiles;
-    __device__ __forceinline__ Columns(const Args &a) {
-        c0 = (int)((long long)a.d * blockIdx.x / gridDim.x);
-        c1 = (int)((long long)a.d * (blockIdx.x + 1) / gridDim.x);
+    __device__ __forceinline__ explicit Columns(const Plan &s) {
+        c0 = s.col0;
+        c1 = s.col1;
         tiles = (c1 - c0 + 15) / 16;
     }
-    __device__ __forceinline__ int at(int tile) const { return c0 + (c1 - c0) * tile / tiles; }
+    __device__ __forceinline__ int at(int tile) const {
+        return tiles == 1 ? (tile ? c1 : c0) : c0 + (int)((unsigned)((c1 - c0) * tile) / (unsigned)tiles);
+    }
 };
 
 // What a warp copies, entry after entry: first step 2's, then step 3's. A segment is a run of entries
@@ -612,8 +623,7 @@ template <int D> struct Feed {
     int c, end, left;                // inner element, where the rows end, entries left
     int nx, ny, nh;                  // bytes of a copy, or 0
     // where the segments come from
-    long long pair, pair1;
-    int tile, tiles, nj, ui, j0, q;
+    int pair, pair1, tile, tiles, nj, ui, j0, q;
     bool down, done;
 
     __device__ __forceinline__ Feed(const Args &a_, const Plan &s_, const char *ring, const char *h_ring)
@@ -624,8 +634,8 @@ template <int D> struct Feed {
         h_base = (uint32_t)__cvta_generic_to_shared(h_ring) + warp * D * slot() + (lane >> 2) * 128 +
                  (lane & 3) * 16;
         h_put = 0;
-        pair = first_pair(a, s, blockIdx.x);
-        pair1 = first_pair(a, s, blockIdx.x + 1);
+        pair = s.pair0;
+        pair1 = s.pair1;
         nj = tiles = left = 0;
         tile = -1;
         down = done = false;
@@ -652,7 +662,7 @@ template <int D> struct Feed {
                 if (pair >= pair1 || k0 == k1) {  // (a warp without a part has no entries)
                     down = true;
                     q = part(s.n * groups(a.f), warp);
-                    tiles = Columns(a).tiles;
+                    tiles = Columns(s).tiles;
                 } else {
                     const Run r(a, s, pair, pair1);
                     tiles = r.tiles;
@@ -683,7 +693,7 @@ template <int D> struct Feed {
             done = true;
             return;
         }
-        const Columns cols(a);
+        const Columns cols(s);
         const int e = q / nk, k0 = q - e * nk, col = cols.at(tile) + g, last = cols.at(tile + 1);
         left = min(nk - k0, q1 - q);
         q += left;
@@ -722,7 +732,7 @@ template <int D> struct Feed {
     __device__ __forceinline__ void catch_up() {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
         const int nk = groups(a.f), q0 = part(s.n * nk, warp), q1 = part(s.n * nk, warp + 1);
-        int todo = min(D - 1, (q1 - q0) * Columns(a).tiles);
+        int todo = min(D - 1, (q1 - q0) * Columns(s).tiles);
         const int none = D - 1 - todo;
 #pragma unroll 1
         while (todo > 0) {  // (again from q0 where the warp's part is shorter than the ring)
@@ -775,10 +785,10 @@ template <int NT, int D> struct Experts {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
         const int stride = token_stride(a.d, 2);
         const int k0 = part(groups(a.d), warp), k1 = part(groups(a.d), warp + 1);
-        const long long p1 = first_pair(a, s, blockIdx.x + 1);
+        const int p1 = s.pair1;
         int buf = 0;
 #pragma unroll 1
-        for (long long p = first_pair(a, s, blockIdx.x); p < p1;) {
+        for (int p = s.pair0; p < p1;) {
             const Run r(a, s, p, p1);
             const int m = r.m;
             float *out = red + buf * (red_bytes(a.R) / 4);
@@ -827,7 +837,7 @@ template <int NT, int D> struct Experts {
     __device__ __forceinline__ void down(float *red) {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
         float *mine = red + (size_t)warp * 16 * a.R;
-        const Columns cols(a);
+        const Columns cols(s);
         const int nk = groups(a.f), q0 = part(s.n * nk, warp), q1 = part(s.n * nk, warp + 1);
         feed.catch_up();
         uint32_t h_take = 0;
@@ -905,10 +915,8 @@ template <int NT, int D> struct Experts {
 __device__ __forceinline__ void gate_up(const Args &a, const Plan &s, const char *xs) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int stride = token_stride(a.d, 4);
-    const long long pairs = (long long)s.n * a.f;
-    const long long p0 = pairs * blockIdx.x / gridDim.x, p1 = pairs * (blockIdx.x + 1) / gridDim.x;
-    for (long long p = p0 + warp; p < p1; p += kWarps) {
-        const int ui = (int)(p / a.f), j = (int)(p - (long long)ui * a.f), e = s.expert[ui];
+    for (int p = s.pair0 + warp; p < s.pair1; p += kWarps) {
+        const int ui = (int)((unsigned)p / (unsigned)a.f), j = p - ui * a.f, e = s.expert[ui];
         const size_t at = ((size_t)s.slot[ui] * a.f + j) * a.d;
         const float *wg = reinterpret_cast<const float *>(a.wg) + at;
         const float *wu = reinterpret_cast<const float *>(a.wu) + at;
@@ -955,8 +963,7 @@ __device__ __forceinline__ void gate_up(const Args &a, const Plan &s, const char
 // fp32: a warp takes a column and a token at a time (the weights are in L1 after the first).
 __device__ __forceinline__ void down(const Args &a, const Plan &s) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int c0 = (int)((long long)a.d * blockIdx.x / gridDim.x);
-    const int c1 = (int)((long long)a.d * (blockIdx.x + 1) / gridDim.x);
+    const int c0 = s.col0, c1 = s.col1;
     const float *h = reinterpret_cast<const float *>(a.h);
     for (int i = warp; i < (c1 - c0) * a.R; i += kWarps) {
         const int col = c0 + i / a.R, r = i % a.R;
