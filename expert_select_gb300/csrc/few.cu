@@ -174,16 +174,26 @@ __device__ __forceinline__ void norm_scales(const Args &a, Plan &s, const char *
     const T *x = reinterpret_cast<const T *>(xs + r * stride);
     Pair sum{0.f, 0.f};
     if (r < a.R) {
+        // two sums side by side, two to an instruction
+        const uint64_t minus = pack2(-1.f, -1.f);
+        uint64_t hi = 0, lo = 0;
+#pragma unroll 1
         for (int c = (w * 32 + lane) * 8; c < a.d; c += per * 256) {
             float v[8];
             load8(x + c, v);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float p = v[i] * v[i];
-                if (sizeof(T) == 4) sum.lo += fmaf(v[i], v[i], -p);
-                add_kept(sum.hi, sum.lo, p);
+            for (int i = 0; i < 8; i += 2) {
+                const uint64_t q = pack2(v[i], v[i + 1]), p = mul2(q, q);
+                if (sizeof(T) == 4) lo = add2(lo, fma2(q, q, mul2(p, minus)));
+                // s = hi + p, and what it loses (exact)
+                const uint64_t s2 = add2(hi, p), t2 = fma2(hi, minus, s2);
+                lo = add2(lo, add2(fma2(fma2(t2, minus, s2), minus, hi), fma2(t2, minus, p)));
+                hi = s2;
             }
         }
+        const float2 h2 = unpack2(hi), l2 = unpack2(lo);
+        sum = Pair{h2.x, l2.x + l2.y};
+        add_kept(sum.hi, sum.lo, h2.y);
     }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) {
@@ -249,25 +259,28 @@ __device__ __forceinline__ void scale16(uint4 *p, Pair sc, const double *wide) {
     const uint4 w = *p;
     float v[8];
     load8(reinterpret_cast<const __nv_bfloat16 *>(&w), v);
-    uint32_t q[8];
+    uint32_t q[4];
     bool middle = false;
+    const uint64_t by = pack2(sc.hi, sc.hi);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const uint32_t b = __float_as_uint(v[j] * sc.hi);
-        middle |= (b & 0xffffu) == 0x8000u;
-        q[j] = (b + 0x7fffu + (b >> 16 & 1u)) >> 16;
+    for (int j = 0; j < 4; ++j) {
+        const float2 x = unpack2(mul2(pack2(v[2 * j], v[2 * j + 1]), by));
+        middle |= (__float_as_uint(x.x) & 0xffffu) == 0x8000u || (__float_as_uint(x.y) & 0xffffu) == 0x8000u;
+        const __nv_bfloat162 b = __floats2bfloat162_rn(x.x, x.y);
+        q[j] = reinterpret_cast<const uint32_t &>(b);
     }
-    // (what is not a number would be rounded to something else)
     if (middle || wide) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
+            uint32_t one = j & 1 ? q[j / 2] >> 16 : q[j / 2] & 0xffffu;
             if (wide)
-                q[j] = scaled_wide(v[j], *wide);
+                one = scaled_wide(v[j], *wide);
             else if ((__float_as_uint(v[j] * sc.hi) & 0xffffu) == 0x8000u)
-                q[j] = scaled_middle(v[j], sc);
+                one = scaled_middle(v[j], sc);
+            q[j / 2] = j & 1 ? (q[j / 2] & 0xffffu) | one << 16 : (q[j / 2] & 0xffff0000u) | one;
         }
     }
-    *p = make_uint4(q[0] | q[1] << 16, q[2] | q[3] << 16, q[4] | q[5] << 16, q[6] | q[7] << 16);
+    *p = make_uint4(q[0], q[1], q[2], q[3]);
 }
 __device__ __noinline__ float scaled_wide_f32(float v, double sc) { return (float)((double)v * sc); }
 __device__ __forceinline__ float scaled(float v, Pair sc) {
