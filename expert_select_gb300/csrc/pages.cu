@@ -103,12 +103,10 @@ __device__ __forceinline__ Run cluster_count(const int *ref, int lo, int hi, int
     const int at = block_scan(lane == 0 ? c : 0, part, &sum);  // warps in order
     if (threadIdx.x == 0) *mine = sum;
     cl.sync();
-    int base = 0, total = 0;
-    for (int i = 0; i < ctas; ++i) {
-        const int v = *cl.map_shared_rank(mine, i);
-        if (i < rank) base += v;
-        total += v;
-    }
+    // (a lane for each CTA: the reads do not wait for one another)
+    const int count = lane < ctas ? *cl.map_shared_rank(mine, lane) : 0;
+    const int base = __reduce_add_sync(0xffffffffu, lane < rank ? count : 0);
+    const int total = __reduce_add_sync(0xffffffffu, count);
     cl.sync();  // (`mine` may be written again)
     r.before = base + __shfl_sync(0xffffffffu, at, 0);
     r.total = total;

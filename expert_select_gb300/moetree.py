@@ -748,7 +748,7 @@ def page_book(page_table, held, cache_len, ref, page_size: int) -> PageBook:
     _dense(fn, "ref", ref, i32, (ref.numel(),), index)
     K = PageBook(page_table.data_ptr(), held.data_ptr(), cache_len.data_ptr(), ref.data_ptr(), B,
                  width, ref.numel(), page_size)
-    K.tensors, K.index = (page_table, held, cache_len, ref), index
+    K.tensors, K.index, K.desc = (page_table, held, cache_len, ref), index, C.byref(K)
     return K
 
 
@@ -767,15 +767,17 @@ def pages_workspace(K: PageBook, device=None) -> torch.Tensor:
 def _pages_scratch(fn, K, ws):
     if ws is None:
         raise ValueError(f"{fn}: it needs a workspace")
-    _scratch(fn, ws, K.index, lib().moe_pages_workspace_bytes(C.byref(K)))
+    _scratch(fn, ws, K.index, _lib.moe_pages_workspace_bytes(K.desc) if _lib else
+             moe_pages_workspace_bytes(K))
+    return K.desc, ws.data_ptr()
 
 
 def moe_kv_reserve(K, N, ws, n_new=None, stream=None):
     """Room for N (n_new [B]: for each sequence its own) more tokens (see include/moetree.h)."""
     fn = "moe_kv_reserve"
     _dense(fn, "n_new", n_new, torch.int32, (K.B,), K.index)
-    _pages_scratch(fn, K, ws)
-    return _run(fn, K.index, stream, C.byref(K), N, _at(n_new), ws.data_ptr())
+    desc, at = _pages_scratch(fn, K, ws)
+    return _run(fn, K.index, stream, desc, N, _at(n_new), at)
 
 
 def moe_kv_free(K, seqs, ws, keep=None, stream=None):
@@ -784,9 +786,8 @@ def moe_kv_free(K, seqs, ws, keep=None, stream=None):
     fn, shape = "moe_kv_free", (seqs.numel(),)
     _dense(fn, "seqs", seqs, torch.int32, shape, K.index)
     _dense(fn, "keep", keep, torch.int32, shape, K.index)
-    _pages_scratch(fn, K, ws)
-    return _run(fn, K.index, stream, C.byref(K), seqs.data_ptr(), _at(keep), shape[0],
-                ws.data_ptr())
+    desc, at = _pages_scratch(fn, K, ws)
+    return _run(fn, K.index, stream, desc, seqs.data_ptr(), _at(keep), shape[0], at)
 
 
 def moe_kv_fork(K, src, dst, moves, ws, stream=None):
@@ -795,9 +796,8 @@ def moe_kv_fork(K, src, dst, moves, ws, stream=None):
     _dense(fn, "src", src, torch.int32, (n,), K.index)
     _dense(fn, "dst", dst, torch.int32, (n,), K.index)
     _dense(fn, "moves", moves, torch.int32, (n, 3), K.index)
-    _pages_scratch(fn, K, ws)
-    return _run(fn, K.index, stream, C.byref(K), src.data_ptr(), dst.data_ptr(), n,
-                moves.data_ptr(), ws.data_ptr())
+    desc, at = _pages_scratch(fn, K, ws)
+    return _run(fn, K.index, stream, desc, src.data_ptr(), dst.data_ptr(), n, moves.data_ptr(), at)
 
 
 def moe_kv_compact(K, table_out, ref_out, moves, counts, ws, stream=None):
@@ -808,9 +808,9 @@ def moe_kv_compact(K, table_out, ref_out, moves, counts, ws, stream=None):
     _dense(fn, "ref_out", ref_out, i32, (K.n_pages,), K.index)
     _dense(fn, "moves", moves, i32, (K.n_pages // 2, 3), K.index)
     _dense(fn, "counts", counts, i32, (2,), K.index)
-    _pages_scratch(fn, K, ws)
-    return _run(fn, K.index, stream, C.byref(K), table_out.data_ptr(), ref_out.data_ptr(),
-                moves.data_ptr(), counts.data_ptr(), ws.data_ptr())
+    desc, at = _pages_scratch(fn, K, ws)
+    return _run(fn, K.index, stream, desc, table_out.data_ptr(), ref_out.data_ptr(),
+                moves.data_ptr(), counts.data_ptr(), at)
 
 
 def moe_kv_copy_pages(C_, k_pages, v_pages, moves, count=None, ws=None, stream=None):
