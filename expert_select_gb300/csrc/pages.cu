@@ -113,17 +113,26 @@ __device__ __forceinline__ Run cluster_count(const int *ref, int lo, int hi, int
     return r;
 }
 
-// Calls put(page, how many picked ones are before it) for each picked page of the warp's run.
+// Calls put(page, how many picked ones are before it) for the picked pages of the warp's run that have
+// fewer than `want` before them.
 template <class Pick, class Put>
-__device__ __forceinline__ void cluster_emit(const int *ref, const Run &r, Pick pick, Put put) {
+__device__ __forceinline__ void cluster_emit(const int *ref, const Run &r, int want, Pick pick, Put put) {
+    constexpr int kDeep = 8;  // loads on their way
     const int lane = threadIdx.x & 31;
     int at = r.before;
-    for (int p0 = r.lo; p0 < r.hi; p0 += 32) {
-        const int p = p0 + lane;
-        const bool on = p < r.hi && pick(p, ref[p]);
-        const uint32_t m = __ballot_sync(0xffffffffu, on);
-        if (on) put(p, at + __popc(m & ((1u << lane) - 1)));
-        at += __popc(m);
+    for (int p0 = r.lo; p0 < r.hi && at < want; p0 += 32 * kDeep) {
+        int v[kDeep];
+#pragma unroll
+        for (int q = 0; q < kDeep; ++q) v[q] = ref[min(p0 + 32 * q + lane, r.hi - 1)];
+#pragma unroll
+        for (int q = 0; q < kDeep; ++q) {
+            const int p = p0 + 32 * q + lane;
+            const bool on = p < r.hi && pick(p, v[q]);
+            const uint32_t m = __ballot_sync(0xffffffffu, on);
+            const int i = at + __popc(m & ((1u << lane) - 1));
+            if (on && i < want) put(p, i, v[q]);
+            at += __popc(m);
+        }
     }
 }
 
@@ -132,10 +141,7 @@ __device__ __forceinline__ bool is_free(int, int ref) { return ref <= 0; }
 // The first `want` free pages go to k.list, ascending. Returns how many free pages there are.
 __device__ __forceinline__ int list_free(const Book &k, int want, int *part, int *mine) {
     const Run r = cluster_count(k.ref, 0, k.n_pages, part, mine, is_free);
-    if (r.before < want)
-        cluster_emit(k.ref, r, is_free, [&](int p, int i) {
-            if (i < want) k.list[i] = p;
-        });
+    cluster_emit(k.ref, r, want, is_free, [&](int p, int i, int) { k.list[i] = p; });
     return r.total;
 }
 
@@ -325,7 +331,7 @@ compact_kernel(Book k, int *ref_out, int *moves, int *counts) {
     const int n_used = cluster_count(k.ref, 0, n, part, &mine, is_used).total;
     // holes below n_used, in ascending order
     const Run holes = cluster_count(k.ref, 0, n_used, part, &mine, is_free);
-    cluster_emit(k.ref, holes, is_free, [&](int p, int i) { k.list[i] = p; });
+    cluster_emit(k.ref, holes, n, is_free, [&](int p, int i, int) { k.list[i] = p; });
     // pages that stay. (ref_out may be ref: nothing that is read here changes before the barriers of
     // the next count.)
     for (int p = cl.block_rank() * kThr + threadIdx.x; p < n; p += cl.num_blocks() * kThr) {
@@ -336,8 +342,8 @@ compact_kernel(Book k, int *ref_out, int *moves, int *counts) {
     }
     // pages at n_used and above go to the holes, in order
     const Run high = cluster_count(k.ref, n_used, n, part, &mine, is_used);
-    cluster_emit(k.ref, high, is_used, [&](int p, int i) {
-        const int to = k.list[i], ref = k.ref[p];
+    cluster_emit(k.ref, high, n, is_used, [&](int p, int i, int ref) {
+        const int to = k.list[i];
         k.map[p] = to;
         ref_out[to] = ref;
         ref_out[p] = 0;
