@@ -18,7 +18,7 @@
 // ones, of which there are few as a rule: a bound from below on the last of them (for top-k, the k-th
 // largest of the threads' own largest values, up to a bin; for min-p its own) lets a second pass collect
 // them, and one CTA sorts them and does the rest. top-p needs the whole weight too; a sum of fp32
-// exponentials, off by at most 2^-16, decides unless a cut lies within that.
+// exponentials, off by at most 2^-15, decides unless a cut lies within that.
 // Where more is kept than a list holds (flat distributions, no cuts), cuts are found by histograms of
 // the row's live values (weights that are not below 2^-43) over bins that descend with the value:
 // counts for top-k, weights for top-p; the bin that a cut falls in is divided by the bits of the
@@ -153,6 +153,10 @@ __device__ __forceinline__ float value_of(uint32_t key) {
     return __uint_as_float(key ^ ((int)key < 0 ? 0x80000000u : 0xffffffffu));
 }
 
+template <typename T> __device__ __forceinline__ T from_value(float v);
+template <> __device__ __forceinline__ float from_value(float v) { return v; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_value(float v) { return __float2bfloat16(v); }
+
 // A 16-byte block of a row.
 template <typename T> struct Block;
 template <> struct Block<float> {
@@ -237,13 +241,14 @@ template <> struct Block<__nv_bfloat16> {
 constexpr int kList = kThr;             // tokens of a list, a thread for each
 constexpr int kAsk = kList / 2;        // of them asked for (the last bin may hold more)
 constexpr float kFar = 36.f;           // octaves from which values do not count in the fp32 sum
-constexpr float kSumError = 0x1p-16f;
+constexpr float kSumError = 0x1p-15f;
 
 // A row, its settings, and where its results go.
 struct Task {
     const void *inner, *low, *high;  // blocks (see Row)
     int blocks, shift;               // block j holds the tokens j kN - shift ..
     int b0, b1, per;                 // of this CTA's slice, and of a warp
+    const void *tops;                // the blocks' largest values in shared memory, or null
     bool raw;
     float temp, top_p, u;
     int k;                 // 0: all
@@ -266,7 +271,8 @@ struct Shared {
     u64 limit, limit_lo, limit_hi;
     uint4 ends[2];
     float2 powers[256];
-    uint32_t lo[kBins], hi[kBins];
+    alignas(16) uint32_t lo[kBins];
+    uint32_t hi[kBins];
     u64 list[kList];  // ~key, index: ascending
     u64 part[kWarps], scanned;
     Scale sc;
@@ -480,6 +486,40 @@ __device__ __noinline__ void pass(Shared &sh, uint32_t lo, uint32_t hi, int arg)
         if (lane == 0) {
             sh.wsum[warp] = wsum;
             sh.ties[warp] = ties;
+        }
+    }
+    __syncthreads();
+}
+
+// Appends the values from lo on to the list: the blocks that have one are found by their largest values.
+template <typename T> __device__ __noinline__ void take(Shared &sh, uint32_t lo) {
+    using B = Block<T>;
+    const Row<T> row(sh.task);
+    const B *tops = reinterpret_cast<const B *>(sh.task.tops);
+    const int b0 = sh.task.b0, n = (sh.task.b1 - b0 + B::kN - 1) / B::kN;
+    const float least = value_of(lo);
+#pragma unroll 1
+    for (int i = threadIdx.x; i < n; i += kThr) {
+        const B v = tops[i];
+        uint32_t todo = 0;
+#pragma unroll
+        for (int q = 0; q < B::kN; ++q) todo |= v.get(q) >= least ? 1u << q : 0;
+#pragma unroll 1
+        for (; todo; todo &= todo - 1) {
+            const int j = b0 + i * B::kN + __ffs(todo) - 1;
+            B b = row.block(j);
+            uint32_t hits = 0;
+#pragma unroll
+            for (int q = 0; q < B::kN; ++q) hits |= b.get(q) >= least ? 1u << q : 0;
+            int at = atomicAdd(&sh.listed, __popc(hits));
+            const int token = j * B::kN - row.shift;
+#pragma unroll 1
+            for (int q = 0; hits; ++q, hits >>= 1) {
+                const float l = b.take();
+                if (!(hits & 1)) continue;
+                if (at < kList) sh.list[at] = (u64)~key_of(l) << 32 | (uint32_t)(token + q);
+                ++at;
+            }
         }
     }
     __syncthreads();
@@ -733,10 +773,44 @@ __device__ __noinline__ bool choose(Shared &sh, int n, bool of_list) {
     return true;
 }
 
+// By one warp: the bin in which the running count reaches `want`, or the last: sh.bin. It looks at 128
+// bins at a time and is done early where little is wanted.
+__device__ __noinline__ void first_bin(Shared &sh, int want) {
+    const int lane = threadIdx.x;
+    uint32_t before = 0;
+    int bin = kBins - 1;
+#pragma unroll 1
+    for (int b0 = 4 * lane; b0 < kBins; b0 += 128) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(sh.lo + b0);
+        uint32_t s = v.x + v.y + v.z + v.w;
+        const uint32_t own = s;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t x = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += x;
+        }
+        s += before;
+        const uint32_t m = __ballot_sync(0xffffffffu, s >= (uint32_t)want);
+        if (m) {
+            if (lane == __ffs(m) - 1) {
+                uint32_t at = s - own;
+                bin = b0;
+                if ((at += v.x) < (uint32_t)want) ++bin;
+                if (bin == b0 + 1 && (at += v.y) < (uint32_t)want) ++bin;
+                if (bin == b0 + 2 && (at += v.z) < (uint32_t)want) ++bin;
+            }
+            bin = __shfl_sync(0xffffffffu, bin, __ffs(m) - 1);
+            break;
+        }
+        before = __shfl_sync(0xffffffffu, s, 31);
+    }
+    if (lane == 0) sh.bin = bin;
+}
+
 // Samples from a list of the row's largest tokens: those that min-p leaves (want 0), or `want` of them
 // and a few more. own: the thread's largest value. False (for the whole cluster) where the list does
 // not hold all that may be kept.
-template <typename T> __device__ __noinline__ bool from_list(Shared &sh, int want, float own) {
+template <typename T> __device__ __noinline__ bool from_list(Shared &sh, int want, float own, float sum) {
     const Task &ask = sh.task;
     cg::cluster_group cl = cg::this_cluster();
     const int ctas = cl.num_blocks(), rank = cl.block_rank();
@@ -748,23 +822,36 @@ template <typename T> __device__ __noinline__ bool from_list(Shared &sh, int wan
         clear_bins(sh);
         // as many threads' largest values: at least as many values
         if (is_live(sh.sc, own)) atomicAdd(&sh.lo[bin_of(sh.sc, own)], 1u);
-        share_bins(sh);
-        if (find_bin(sh, want)) last = sh.bin;
+        // (each CTA's own as long as all their lists together are short)
+        if (want * ctas > kAsk)
+            share_bins(sh);
+        else
+            __syncthreads();
+        if (threadIdx.x < 32) first_bin(sh, want);
     }
     __syncthreads();
+    if (want) last = sh.bin;
     // All values of those bins (and perhaps a few below them) are at least so large; min-p's least value
     // is one itself.
     float least = sh.sc.top - (float)(last + 1) * (1.0f + 0x1p-18f) / kBinScale / sh.sc.ch;
     uint32_t least_key = key_of(fmaxf(least, -FLT_MAX) + 0.f);
     if (!ask.k) least_key = max(least_key, ask.low_key);
-    if (whole)
+    if (ask.tops) {
+        if (whole) {
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if ((threadIdx.x & 31) == 0) sh.sums[threadIdx.x >> 5] = sum;
+        }
+        take<T>(sh, least_key);
+    } else if (whole) {
         pass<T, kTakeAndSum>(sh, least_key, 0xffffffffu, 0);
-    else
+    } else {
         pass<T, kTake>(sh, least_key, 0xffffffffu, 0);
+    }
     if (whole && threadIdx.x == 0) {
-        float sum = 0.f;
-        for (int i = 0; i < kWarps; ++i) sum += sh.sums[i];
-        sh.sum = sum;
+        float all = 0.f;
+        for (int i = 0; i < kWarps; ++i) all += sh.sums[i];
+        sh.sum = all;
     }
     cl.sync();
     if (rank == 0) {
@@ -993,7 +1080,7 @@ template <typename T> __device__ __noinline__ void from_row(Shared &sh) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThr, 2) sample_kernel(const Args a, int held_blocks) {
+__global__ void __launch_bounds__(kThr, 2) sample_kernel(const Args a, int held_blocks, int tops_blocks) {
     extern __shared__ __align__(16) unsigned char dyn[];
     __shared__ __align__(16) Shared sh;
     using B = Block<T>;
@@ -1060,23 +1147,43 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const Args a, int held_
     // the row's slice, and the largest value
     const Row<T> row(t);
     B *held = t.b1 - t.b0 <= held_blocks ? reinterpret_cast<B *>(dyn) - t.b0 : nullptr;
-    float top = -INFINITY;
+    T *tops = t.b1 - t.b0 <= tops_blocks
+                  ? reinterpret_cast<T *>(dyn + (size_t)held_blocks * 16) - t.b0 : nullptr;
+    // Beside it, where top-p is of the row's weight, the fp32 sum of the weights relative to the largest
+    // value that the thread has seen.
+    const bool whole = tops && t.top_p < 1.f && !t.k && t.temp > 0.f;
+    const float ch = sh.sc.ch;
+    float top = -INFINITY, sum = 0.f;
     row.template blocks<8>([&](const auto &b, int j0, int n) {
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
             if (q >= n) continue;
+            const float m = b[q].top();
             if (held) held[j0 + 32 * q] = b[q];
-            top = fmaxf(top, b[q].top());
+            if (tops) tops[j0 + 32 * q] = from_value<T>(m);
+            if (whole && m > -INFINITY) {
+                if (m > top) sum *= exp2_approx((top - m) * ch);
+                const float at = fmaxf(top, m);
+                if ((at - m) * ch < kFar) {
+                    float part = 0.f;
+#pragma unroll
+                    for (int i = 0; i < B::kN; ++i) part += exp2_approx((b[q].get(i) - at) * ch);
+                    sum += part;
+                }
+            }
+            top = fmaxf(top, m);
         }
     });
     const float own = top;  // the thread's largest
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     if (lane == 0) sh.sums[warp] = top;
+    if (tops && threadIdx.x < B::kN) tops[t.b1 + threadIdx.x] = from_value<T>(-INFINITY);
     __syncthreads();
     for (int i = 0; i < kWarps; ++i) top = fmaxf(top, sh.sums[i]);
     if (threadIdx.x == 0) {
         sh.top = top;
+        t.tops = tops ? tops + t.b0 : nullptr;
         if (held) {
             t.inner = t.low = held;
             t.high = held + t.blocks - 1;
@@ -1129,7 +1236,8 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const Args a, int held_
     __syncthreads();
     // what is kept may fit a list: k tokens, or those that min-p leaves, or top-p's as a guess
     if (t.k ? t.k <= kAsk : by_m || t.top_p < 1.f)
-        if (from_list<T>(sh, t.k ? t.k : by_m ? 0 : kAsk, own)) return;
+        if (from_list<T>(sh, t.k ? t.k : by_m ? 0 : kAsk, own, whole ? sum * exp2_approx((own - top) * ch) : 0.f))
+            return;
     from_row<T>(sh);
 }
 
@@ -1149,12 +1257,15 @@ template <typename T> cudaError_t launch(const Args &a, cudaStream_t s) {
     while (ctas > 1 && blocks / ctas < kThr) ctas /= 2;
     const int per = (blocks + ctas - 1) / ctas;
     const int held = per <= room ? per : 0;
-    cudaError_t err = allow_smem(sample_kernel<T>, kHeldBytes);
+    // the blocks' largest values, and a block of padding
+    const int tops_bytes = (per + 2 * Block<T>::kN) * (int)sizeof(T) / 16 * 16;
+    const bool tops = held || tops_bytes <= kHeldBytes;
+    cudaError_t err = allow_smem(sample_kernel<T>, 2 * kHeldBytes);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)a.R * ctas);
     cfg.blockDim = dim3(kThr);
-    cfg.dynamicSmemBytes = (size_t)held * 16;
+    cfg.dynamicSmemBytes = (size_t)held * 16 + (tops ? tops_bytes : 0);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1165,7 +1276,7 @@ template <typename T> cudaError_t launch(const Args &a, cudaStream_t s) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, sample_kernel<T>, a, held);
+    return cudaLaunchKernelEx(&cfg, sample_kernel<T>, a, held, tops ? per : 0);
 }
 
 }  // namespace
