@@ -18,7 +18,7 @@
 // ones, of which there are few as a rule: a bound from below on the last of them (for top-k, the k-th
 // largest of the threads' own largest values, up to a bin; for min-p its own) lets a second pass collect
 // them, and one CTA sorts them and does the rest. top-p needs the whole weight too; a sum of fp32
-// exponentials, off by at most 2^-15, decides unless a cut lies within that.
+// exponentials, off by at most 2^-16, decides unless a cut lies within that.
 // Where more is kept than a list holds (flat distributions, no cuts), cuts are found by histograms of
 // the row's live values (weights that are not below 2^-43) over bins that descend with the value:
 // counts for top-k, weights for top-p; the bin that a cut falls in is divided by the bits of the
@@ -241,7 +241,7 @@ template <> struct Block<__nv_bfloat16> {
 constexpr int kList = kThr;             // tokens of a list, a thread for each
 constexpr int kAsk = kList / 2;        // of them asked for (the last bin may hold more)
 constexpr float kFar = 36.f;           // octaves from which values do not count in the fp32 sum
-constexpr float kSumError = 0x1p-15f;
+constexpr float kSumError = 0x1p-16f;
 
 // A row, its settings, and where its results go.
 struct Task {
@@ -823,7 +823,7 @@ template <typename T> __device__ __noinline__ bool from_list(Shared &sh, int wan
         // as many threads' largest values: at least as many values
         if (is_live(sh.sc, own)) atomicAdd(&sh.lo[bin_of(sh.sc, own)], 1u);
         // (each CTA's own as long as all their lists together are short)
-        if (want * ctas > kAsk)
+        if (want * ctas > kAsk / 2)
             share_bins(sh);
         else
             __syncthreads();
@@ -1149,11 +1149,15 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const Args a, int held_
     B *held = t.b1 - t.b0 <= held_blocks ? reinterpret_cast<B *>(dyn) - t.b0 : nullptr;
     T *tops = t.b1 - t.b0 <= tops_blocks
                   ? reinterpret_cast<T *>(dyn + (size_t)held_blocks * 16) - t.b0 : nullptr;
-    // Beside it, where top-p is of the row's weight, the fp32 sum of the weights relative to the largest
-    // value that the thread has seen.
+    // Beside it, where top-p is of the row's weight, the fp32 sum of the weights relative to a value that
+    // the thread has seen; a larger one takes its place from 8 octaves on, so that what was added up
+    // before hardly counts when it has been scaled down twice.
+    // Its error, relative: 2.5 roundings of up to 17 octaves (what lies further down is too little), twice with
+    // the last scaling, 4 10^-6; exp2's 2^-22 three times; a thread's up to 82 additions, 4.9 10^-6, and 24 of
+    // threads, warps and CTAs, 1.4 10^-6: 1.1 10^-5 < 2^-16.
     const bool whole = tops && t.top_p < 1.f && !t.k && t.temp > 0.f;
     const float ch = sh.sc.ch;
-    float top = -INFINITY, sum = 0.f;
+    float top = -INFINITY, at = -INFINITY, sum = 0.f;
     row.template blocks<8>([&](const auto &b, int j0, int n) {
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
@@ -1162,8 +1166,10 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const Args a, int held_
             if (held) held[j0 + 32 * q] = b[q];
             if (tops) tops[j0 + 32 * q] = from_value<T>(m);
             if (whole && m > -INFINITY) {
-                if (m > top) sum *= exp2_approx((top - m) * ch);
-                const float at = fmaxf(top, m);
+                if (!((m - at) * ch < 8.f)) {
+                    sum *= exp2_approx((at - m) * ch);
+                    at = m;
+                }
                 if ((at - m) * ch < kFar) {
                     float part = 0.f;
 #pragma unroll
@@ -1236,7 +1242,7 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const Args a, int held_
     __syncthreads();
     // what is kept may fit a list: k tokens, or those that min-p leaves, or top-p's as a guess
     if (t.k ? t.k <= kAsk : by_m || t.top_p < 1.f)
-        if (from_list<T>(sh, t.k ? t.k : by_m ? 0 : kAsk, own, whole ? sum * exp2_approx((own - top) * ch) : 0.f))
+        if (from_list<T>(sh, t.k ? t.k : by_m ? 0 : kAsk, own, whole && sum > 0.f ? sum * exp2_approx((at - top) * ch) : 0.f))
             return;
     from_row<T>(sh);
 }
