@@ -16,6 +16,11 @@
 // 16 x 8 x 16 products (the order of the inner index is free, so a lane's 16 bytes are two operands);
 // tokens are the 8 columns. The activations times their gates are kept as a bf16 value and the bf16
 // rest, which is fp32's accuracy to 2^-17. fp32 layers take fp32 products.
+//
+// Measured, calls in a row with other weights each: one token of the Qwen3-shaped layer 26.6 us (6 until
+// the first weights are asked for, 3 between the last of step 2 and the first of step 3), 16 tokens
+// 149 (0.77 of the HBM's measured rate; CTAs end step 2 over 13 us), 4 tokens of d = f = 2880, 32
+// experts, top-4 123 (0.79), 3 tokens of an fp32 layer of d 520 13.9.
 #include <algorithm>
 
 #include "few.cuh"

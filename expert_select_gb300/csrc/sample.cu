@@ -23,6 +23,11 @@
 // the row's live values (weights that are not below 2^-43) over bins that descend with the value:
 // counts for top-k, weights for top-p; the bin that a cut falls in is divided by the bits of the
 // values until one value is left, and ties are taken in the order of the tokens.
+//
+// Measured for bf16 rows of 151936 with top-k 20 and top-p 0.9: one row 13.8 us (bound by the cluster's
+// barriers), 1040 rows 95-97 (48 of it the HBM's; two CTAs an SM, and a row's list keeps one warp of its CTA
+// busy for 11); 192 rows of fp32 50257, a third of them without top-k, 112 (bound by the instructions of
+// exact weights).
 #include <cooperative_groups.h>
 
 #include <cfloat>

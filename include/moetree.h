@@ -575,8 +575,8 @@ size_t moe_few_workspace_bytes(const moe_layer_desc *L, int R);
  * with opts->norm_input on the pre-norm of x, with opts->residual added to x (see moe_run_opts).
  * R <= 16, else MOE_ERR_UNSUPPORTED (moe_tree_forward takes any number; its results differ by
  * roundings). Sums are fp32; bf16 layers keep the gated activations as a bf16 value and its bf16
- * rest (2^-17 relative). Tokens that do not fit a CTA's shared memory together (more than 138 KB
- * of rows) take further launches.
+ * rest (2^-17 relative). Tokens that do not fit a CTA's shared memory together (16 of them above
+ * some 3900 bf16 or 2900 fp32 elements) take further launches.
  *   x, y [R, d] device, layer dtype; y may be x itself, and must not overlap it otherwise.
  *   W_r, W_gate, W_up, W_down, slot_of_expert as for moe_tree_forward.
  *   logits [R, E], topk_idx [R, k], gates [R, k] device outputs, each may be NULL.
