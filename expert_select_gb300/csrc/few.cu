@@ -536,9 +536,15 @@ __device__ __forceinline__ int nth_token(unsigned mask, int i) {
 // A gated activation of assignment (token, place), element j.
 __device__ __forceinline__ void store_h(const Args &a, __nv_bfloat16 *, int row, int j, float v) {
     __nv_bfloat16 *h = reinterpret_cast<__nv_bfloat16 *>(a.h) + (size_t)row * 2 * a.f;
-    const __nv_bfloat16 hi = __float2bfloat16(v);
+    __nv_bfloat16 hi = __float2bfloat16(v);
+    float rest = v - __bfloat162float(hi);
+    if (fabsf(rest) == INFINITY || fabsf(v) == INFINITY) {
+        // beyond bf16's largest: that and the rest; an infinity has none
+        hi = __float2bfloat16_rz(v);
+        rest = fabsf(v) == INFINITY ? 0.f : v - __bfloat162float(hi);
+    }
     h[j] = hi;
-    h[a.f + j] = __float2bfloat16(v - __bfloat162float(hi));
+    h[a.f + j] = __float2bfloat16(rest);
 }
 __device__ __forceinline__ void store_h(const Args &a, float *, int row, int j, float v) {
     reinterpret_cast<float *>(a.h)[(size_t)row * a.f + j] = v;

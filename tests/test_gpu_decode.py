@@ -643,3 +643,58 @@ def test_copy_pages(layout, page, heads, dh, dt):
     count.fill_(-3)
     M.moe_kv_copy_pages(C, kp, vp, torch.from_numpy(moves).to(DEV), count=count)
     assert torch.equal(kp, want[0])
+
+
+# ---------------------------------------------- where numbers do not fit, and sizes at the ends
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("size", [1e20, 1.8422e19])
+def test_few_activations_at_the_end_of_the_range(dt, size):
+    """An activation beyond fp32 gives infinities of the signs of W_down's rows; one between bf16's and
+    fp32's largest is held by its value and rest (both signs of it, so that y is finite)."""
+    R, d, E, k, f = 3, 64, 4, 1, 32
+    t = Few(19, R, d, E, k, f, dt)
+    t.x = torch.ones(R, d, dtype=dt)
+    t.wg[:, 3], t.wu[:, 3] = 0, 0
+    t.wg[:, 3, 5] = t.wu[:, 3, 7] = size
+    t.wd[t.wd == 0] = 1
+    big = float(t.wg[0, 3, 5]) * float(t.wu[0, 3, 7])
+    if size < 1e20:
+        # the product at row 3 lies above bf16's largest value's upper half step, below fp32's
+        t.wu[:, 3, 7] = 1.8446744073709552e19
+        t.wg[:, 3, 5], t.wg[:, 3, 6] = 1.8374686479671624e19, 4e16  # 255 2^56, and a little
+        big = (float(t.wg[0, 3, 5]) + float(t.wg[0, 3, 6])) * 2.0 ** 64
+        assert 3.3961775e38 < big < 3.4028e38
+        t.wd[:, :, 3] = t.wd[:, :, 3].sign() * 2.0 ** -20
+    t.upload().run()
+    y = t.y.cpu().double()
+    for r in range(R):
+        e = int(t.idx[r, 0])
+        if size < 1e20:
+            want = big * t.wd[e, :, 3].double()
+            tol = (U[dt] + 2.0 ** -16) * want.abs()  # (what the other activations add is far below)
+            assert ((y[r] - want).abs() <= tol).all()
+        else:
+            assert torch.equal(y[r], t.wd[e, :, 3].double().sign() * math.inf)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("ctas", [1, 2, 151])
+def test_few_on_any_number_of_ctas(dt, ctas):
+    t = Few(23, 11, 2888, 9, 3, 200, dt).upload().run(True, True, max_ctas=ctas)
+    t.check(True, True)
+
+
+def test_copy_pages_past_4_gb():
+    n, page, heads, dh = 40000, 64, 8, 128  # 5.2 GB a pool
+    kp = torch.empty(n, page, heads, dh, dtype=torch.bfloat16, device=DEV)
+    vp = torch.empty(n, heads, page, dh, dtype=torch.bfloat16, device=DEV).permute(0, 2, 1, 3)
+    for p in (kp, vp):
+        C = M.cache_desc(p, heads, 4)
+        p[n - 1].normal_()
+        p[3].fill_(7)
+        p[n - 2].fill_(5)
+        want = p[n - 1].clone()
+        M.moe_kv_copy_pages(C, p, p, torch.tensor([[n - 1, 3, 64], [n - 1, n - 2, 9]], dtype=torch.int32, device=DEV))
+        assert torch.equal(p[3], want) and torch.equal(p[n - 1], want)
+        assert torch.equal(p[n - 2, :9], want[:9]) and bool((p[n - 2, 9:] == 5).all())
