@@ -152,7 +152,8 @@ __device__ __forceinline__ int list_free(const Book &k, int want, int *part, int
 // ------------------------------------------------------------------ free
 
 // A CTA for each entry of the list. Lowering `held` is what takes the pages: of two entries that
-// name one sequence each releases the pages between its own mark and the one it found.
+// name one sequence each releases the pages between its own mark and the one it found. The tokens are
+// cut before, so that the numbers fit at any time, for who reads them in the other order.
 __global__ void __launch_bounds__(128) free_kernel(Book k, const int *seqs, const int *keep) {
     __shared__ int s_old;
     pdl_wait();
@@ -164,12 +165,25 @@ __global__ void __launch_bounds__(128) free_kernel(Book k, const int *seqs, cons
     const long long want_ll = ((long long)left + k.page - 1) / k.page;
     const int want = (int)min(want_ll, (long long)k.max_pages);
     if (threadIdx.x == 0) {
-        s_old = atomicMin(&k.held[b], want);
-        atomicMin(&k.len[b], left);
-        if (s_old > k.max_pages) flag(k, attn::FLAG_BAD_SEQUENCE);
+        const volatile int *held = k.held + b, *len = k.len + b;
+        // (side by side first; what looks wrong then may be another entry's work)
+        int h = *held, l = *len;
+        if (!sane(k, h, l)) {
+            h = *held;
+            __threadfence();
+            l = *len;
+        }
+        s_old = 0;
+        if (sane(k, h, l)) {
+            if (l > left) atomicMin(&k.len[b], left);
+            __threadfence();
+            s_old = atomicMin(&k.held[b], want);
+        } else {
+            flag(k, attn::FLAG_BAD_SEQUENCE);
+        }
     }
     __syncthreads();
-    const int old = min(s_old, k.max_pages);
+    const int old = s_old;
     for (int j = want + threadIdx.x; j < old; j += blockDim.x) {
         const int p = k.table[(size_t)b * k.max_pages + j];
         if (p < 0 || p >= k.n_pages || atomicSub(&k.ref[p], 1) <= 0) {

@@ -647,7 +647,7 @@ moe_status moe_tree_accept(const int *token, const int *parent, const int *sampl
  * free. New pages are the free ones of the lowest numbers, in the order of the sequences (of a list's
  * entries), so results repeat. All arrays are device int32. Calls on one book are ordered on one
  * stream by the caller. A sequence whose numbers do not fit (held outside [0, max_pages], cache_len
- * outside [0, held * page_size]) is left as it is.
+ * outside [0, held * page_size]) is left as it is (moe_kv_compact moves what its entries hold).
  * Limits: B <= 65536, n_pages <= 2^24, max_pages * page_size <= 2^30.
  * Check word of the workspace: bit 2 = a page outside the pool, or one given back that nobody held;
  * bit 3 = a sequence outside [0, B), one whose numbers do not fit, one that would need more than

@@ -685,6 +685,31 @@ def test_few_on_any_number_of_ctas(dt, ctas):
     t.check(True, True)
 
 
+def test_pages_of_sequences_whose_numbers_do_not_fit():
+    """They are left as they are and told, whichever call meets them, also beside others of the list."""
+    k = Book(31, 12, 5, 90, 8)
+    k.free(list(range(12)))
+    k.reserve(20)
+    k.same()
+    k.held[1], k.held[2], k.len[3], k.len[4] = -3, 6, 25, -1  # (three pages of 8 each)
+    k.len[5:] = [24, 17, 16, 9, 1, 0, 8]
+    for i, a in ((1, k.held), (2, k.len)):
+        k.dev[i].copy_(torch.from_numpy(a))
+    odd = [1, 2, 3, 4]
+    saved = k.held[odd].copy(), k.len[odd].copy(), k.ref.copy()
+    put = lambda v: torch.tensor(v, dtype=torch.int32, device=DEV)  # noqa: E731
+    M.moe_kv_free(k.K, put(odd), k.ws)
+    M.moe_kv_free(k.K, put(odd + odd), k.ws, keep=put([8, 8, 8, 8, 0, 30, 0, 5]))
+    k.flags = 8
+    k.same()
+    # the same sequence many times, in any order: the smallest keep holds
+    lists = [5, 6] * 40
+    keeps = [int(v) for v in np.random.default_rng(3).integers(3, 25, 80)]
+    k.free(lists, keeps)
+    k.same()
+    assert np.array_equal(saved[0], k.held[odd]) and np.array_equal(saved[1], k.len[odd])
+
+
 def test_copy_pages_past_4_gb():
     n, page, heads, dh = 40000, 64, 8, 128  # 5.2 GB a pool
     kp = torch.empty(n, page, heads, dh, dtype=torch.bfloat16, device=DEV)
