@@ -24,10 +24,10 @@
 // counts for top-k, weights for top-p; the bin that a cut falls in is divided by the bits of the
 // values until one value is left, and ties are taken in the order of the tokens.
 //
-// Measured for bf16 rows of 151936 with top-k 20 and top-p 0.9: one row 13.8 us (bound by the cluster's
-// barriers), 1040 rows 95-97 (48 of it the HBM's; two CTAs an SM, and a row's list keeps one warp of its CTA
-// busy for 11); 192 rows of fp32 50257, a third of them without top-k, 112 (bound by the instructions of
-// exact weights).
+// Measured for bf16 rows of 151936 with top-k 20 and top-p 0.9: one row 13.3 us (bound by the cluster's
+// barriers), 1040 rows 85 (48 of it the HBM's; two CTAs an SM, and a row's list keeps one warp of its CTA
+// busy for 11); 192 rows of fp32 50257, a third of them without top-k, 70 (bound by the instructions of
+// exact weights, and by the slowest rows).
 #include <cooperative_groups.h>
 
 #include <cfloat>
@@ -79,55 +79,25 @@ struct Scale {
 __device__ __forceinline__ float octaves(const Scale &s, float l) { return (s.top - l) * s.ch; }
 __device__ __forceinline__ bool is_live(const Scale &s, float l) { return octaves(s, l) < kLive; }
 
-// The weight of a live value in units of 2^-43. The difference and its product with log2(e) / T are
-// carried as two fp32 values; 2^-x is a table's 2^(-k/256) times e^q, |q| <= 2^-9 ln 2 and a
-// little; the parts are turned into integers at 2^22 and 2^43.
-__device__ __forceinline__ u64 weight(const Scale &s, float l, const float2 *powers) {
-    constexpr float kBig = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer
-    constexpr double kLn2 = 0.69314718055994530942;
-    constexpr float lh = (float)kLn2, ll = (float)(kLn2 - (double)lh);
-    const float d = s.top - l, bb = d - s.top, e = (s.top - (d - bb)) - (l + bb);
-    const float p = __fmul_rn(d, s.ch), pe = fmaf(d, s.ch, -p) + fmaf(d, s.cl, e * s.ch);
-    const float kb = fmaf(p, 256.f, kBig);
-    const int k = __float_as_int(kb) - 0x4b400000;
-    const float r = fmaf(kb - kBig, -1.f / 256.f, p);  // exact
-    const float q = __fmul_rn(-r, lh), ql = fmaf(-r, lh, -q) - fmaf(r, ll, pe * lh);
-    const float more = fmaf(ql, q, ql) + q * q * fmaf(q, fmaf(q, 1.f / 24.f, 1.f / 6.f), 0.5f);
-    const float eh = q + more, el = more - (eh - q);
-    const float2 t = powers[k & 255];
-    const float sc = __int_as_float((127 + 22 - (k >> 8)) << 23);
-    const float a = t.x * sc, b = __fmul_rn(a, eh), al = t.y * sc;
-    const float c = fmaf(a, eh, -b) + fmaf(a, el, fmaf(al, q, al));
-    const float ai = a + 8388608.f, bi = b + kBig;
-    const float rest = (a - (ai - 8388608.f)) + (b - (bi - kBig)) + c;
-    const int hi = (__float_as_int(ai) - 0x4b000000) + (__float_as_int(bi) - 0x4b400000);
-    const int lo = __float_as_int(fmaf(rest, 2097152.f, kBig)) - 0x4b400000;
-    const long long w = ((long long)hi << 21) + lo;
-    return w > 0 ? (u64)w : 0;
-}
-
-__device__ __forceinline__ float exp2_approx(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// The weights of two live values: the same steps, two to an instruction.
+// The weights of two live values in units of 2^-43, two to an instruction. The difference and its product
+// with log2(e) / T are carried as two fp32 values; 2^-x is a table's 2^(-k/256) times e^q, |q| <= 2^-9 ln 2
+// and a little; the parts are turned into integers at 2^22 and 2^43. Bound by the fp32 pipe (40
+// instructions), so what can be had negated or with an addend in one step is.
 __device__ __forceinline__ void weight2(const Scale &s, float l0, float l1, const float2 *powers, u64 &w0,
                                         u64 &w1) {
-    constexpr float kBig = 12582912.f;
+    constexpr float kBig = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer
     constexpr double kLn2 = 0.69314718055994530942;
     constexpr float lh = (float)kLn2, ll = (float)(kLn2 - (double)lh);
     auto both = [](float v) { return pack2(v, v); };
     const uint64_t minus = both(-1.f), l = pack2(l0, l1), top = both(s.top), ch = both(s.ch);
     const uint64_t d = fma2(l, minus, top), bb = add2(d, both(-s.top));
     const uint64_t e = fma2(add2(l, bb), minus, fma2(fma2(bb, minus, d), minus, top));
-    const uint64_t p = mul2(d, ch);
-    const uint64_t pe = add2(fma2(d, ch, mul2(d, both(-s.ch))), fma2(d, both(s.cl), mul2(e, ch)));
-    const uint64_t kb = fma2(p, both(256.f), both(kBig));
-    const uint64_t r = fma2(add2(kb, both(-kBig)), both(-1.f / 256.f), p);
-    const uint64_t q = mul2(r, both(-lh));
-    const uint64_t ql = fma2(r, both(-ll), fma2(pe, both(-lh), fma2(r, both(-lh), mul2(r, both(lh)))));
+    const uint64_t p = mul2(d, both(-s.ch));  // -x
+    const uint64_t pe = add2(fma2(d, ch, p), fma2(d, both(s.cl), mul2(e, ch)));
+    const uint64_t kb = fma2(p, both(-256.f), both(kBig));
+    const uint64_t r = fma2(add2(kb, both(-kBig)), both(1.f / 256.f), p);  // exact
+    const uint64_t q = mul2(r, both(lh));
+    const uint64_t ql = fma2(r, both(ll), fma2(pe, both(-lh), fma2(r, both(lh), mul2(r, both(-lh)))));
     const uint64_t poly = fma2(q, fma2(q, both(1.f / 24.f), both(1.f / 6.f)), both(0.5f));
     const uint64_t more = fma2(mul2(q, q), poly, fma2(ql, q, ql));
     const uint64_t eh = add2(q, more), el = fma2(fma2(q, minus, eh), minus, more);
@@ -137,16 +107,28 @@ __device__ __forceinline__ void weight2(const Scale &s, float l0, float l1, cons
     // 2^(22 - (k >> 8))
     const uint64_t sc = pack2(__int_as_float((k0 & ~255) * -32768 + (149 << 23)),
                               __int_as_float((k1 & ~255) * -32768 + (149 << 23)));
-    const uint64_t a = mul2(pack2(t0.x, t1.x), sc), al = mul2(pack2(t0.y, t1.y), sc), b = mul2(a, eh);
-    const uint64_t c = add2(fma2(a, eh, mul2(a, mul2(eh, minus))), fma2(a, el, fma2(al, q, al)));
-    const uint64_t ai = add2(a, both(8388608.f)), bi = add2(b, both(kBig));
-    const uint64_t rest = add2(add2(fma2(add2(ai, both(-8388608.f)), minus, a),
-                                    fma2(add2(bi, both(-kBig)), minus, b)), c);
+    const uint64_t a = mul2(pack2(t0.x, t1.x), sc), al = mul2(pack2(t0.y, t1.y), sc);
+    // a and a eh: their integers, and what is left of them (of a eh up to 2^-26)
+    const uint64_t ai = add2(a, both(8388608.f)), bi = fma2(a, eh, both(kBig));
+    const uint64_t ra = add2(a, fma2(ai, minus, both(8388608.f))), rb = fma2(a, eh, fma2(bi, minus, both(kBig)));
+    const uint64_t rest = add2(add2(ra, rb), fma2(a, el, fma2(al, q, al)));
     const float2 af = unpack2(ai), bf = unpack2(bi), lo = unpack2(fma2(rest, both(2097152.f), both(kBig)));
     const int h0 = (__float_as_int(af.x) - 0x4b000000) + (__float_as_int(bf.x) - 0x4b400000);
     const int h1 = (__float_as_int(af.y) - 0x4b000000) + (__float_as_int(bf.y) - 0x4b400000);
     w0 = (u64)((long long)h0 * (1 << 21) + (__float_as_int(lo.x) - 0x4b400000));
     w1 = (u64)((long long)h1 * (1 << 21) + (__float_as_int(lo.y) - 0x4b400000));
+}
+// One of them: the same steps, so the same weight (0 where the value is not live).
+__device__ __forceinline__ u64 weight(const Scale &s, float l, const float2 *powers) {
+    u64 w, other;
+    weight2(s, l, s.top, powers, w, other);
+    return (long long)w > 0 ? w : 0;
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 // Values in the order of their keys (NaN and -0 do not occur).
@@ -299,6 +281,15 @@ struct Shared {
     int part_owner;
 };
 
+// A barrier of the row's CTAs. (A cluster's costs more than a CTA's even where it has one CTA.)
+__device__ __forceinline__ void row_sync() {
+    cg::cluster_group cl = cg::this_cluster();
+    if (cl.num_blocks() > 1)
+        cl.sync();
+    else
+        __syncthreads();
+}
+
 // Sum of the block's threads before this one, in their order; of all: sh.scanned. (What is used in
 // several places is called: code that a row runs through once waits for its instructions.)
 __device__ __noinline__ u64 block_scan(Shared &sh, u64 v) {
@@ -407,37 +398,37 @@ __device__ __noinline__ void pass(Shared &sh, uint32_t lo, uint32_t hi, int arg)
     uint32_t ties = 0;
     float sum = 0.f;
     constexpr bool kTakes = kMode == kTake || kMode == kTakeAndSum;
-    constexpr int kDeep = kTakes ? 8 : 4;
+    constexpr int kDeep = 8;
     // (keys below the least value's and above the largest's stand for no value)
     float least = lo > key_of(-INFINITY) ? value_of(lo) : -INFINITY;
     const float most = hi < key_of(INFINITY) ? value_of(hi) : INFINITY, cut = least;
     if (!kTakes) least = fmaxf(least, sh.live);
-    row.template blocks<kDeep>([&](const auto &b, int j0, int n) {
-        uint32_t todo = 0;  // blocks that hold a value to look at
+    if constexpr (kTakes) {
+        row.template blocks<kDeep>([&](const auto &b, int j0, int n) {
+            uint32_t todo = 0;  // blocks that hold a value to look at
 #pragma unroll
-        for (int q = 0; q < kDeep; ++q) {
-            const float m = b[q].top();
-            if (q >= n) continue;
-            if (kMode == kTakeAndSum && octaves(sc, m) < kFar) {
-                float part = 0.f;
+            for (int q = 0; q < kDeep; ++q) {
+                const float m = b[q].top();
+                if (q >= n) continue;
+                if (kMode == kTakeAndSum && octaves(sc, m) < kFar) {
+                    float part = 0.f;
 #pragma unroll
-                for (int i = 0; i < B::kN; ++i) part += exp2_approx(-octaves(sc, b[q].get(i)));
-                sum += part;
+                    for (int i = 0; i < B::kN; ++i) part += exp2_approx(-octaves(sc, b[q].get(i)));
+                    sum += part;
+                }
+                if (m >= least) todo |= 1u << q;
             }
-            if (m >= least) todo |= 1u << q;
-        }
 #pragma unroll 1
-        while (todo) {
-            const int at_q = __ffs(todo) - 1;
-            todo &= todo - 1;
-            B one = b[0];
+            while (todo) {
+                const int at_q = __ffs(todo) - 1;
+                todo &= todo - 1;
+                B one = b[0];
 #pragma unroll
-            for (int q = 1; q < kDeep; ++q)
-                if (at_q == q) one = b[q];
-            uint32_t hits = 0;
+                for (int q = 1; q < kDeep; ++q)
+                    if (at_q == q) one = b[q];
+                uint32_t hits = 0;
 #pragma unroll
-            for (int i = 0; i < B::kN; ++i) hits |= one.get(i) >= least && one.get(i) <= most ? 1u << i : 0;
-            if constexpr (kTakes) {
+                for (int i = 0; i < B::kN; ++i) hits |= one.get(i) >= least && one.get(i) <= most ? 1u << i : 0;
                 int at = atomicAdd(&sh.listed, __popc(hits));
                 const int token = (j0 + 32 * at_q) * B::kN - row.shift;
 #pragma unroll 1
@@ -447,37 +438,67 @@ __device__ __noinline__ void pass(Shared &sh, uint32_t lo, uint32_t hi, int arg)
                     if (at < kList) sh.list[at] = (u64)~key_of(l) << 32 | (uint32_t)(token + i);
                     ++at;
                 }
-            } else if constexpr (kMode == kCounts || kMode == kCountKeys) {
+            }
+        });
+    } else {
+        // blocks by their largest values, where these are at hand; the next one is on its way meanwhile
+        constexpr int kMany = 16;
+        const T *tops = reinterpret_cast<const T *>(sh.task.tops);
+        const int b0 = sh.task.b0;
+#pragma unroll 1
+        for (int j0 = row.w0 + lane; j0 < row.w1; j0 += 32 * kMany) {
+            uint32_t todo = 0;
+#pragma unroll 4
+            for (int q = 0; q < kMany; ++q) {
+                const int j = j0 + 32 * q;
+                if (j < row.w1 && (!tops || (float)tops[j - b0] >= least)) todo |= 1u << q;
+            }
+            B next;
+            if (todo) next = *row.at(j0 + 32 * (__ffs(todo) - 1));
+#pragma unroll 1
+            while (todo) {
+                B one = next;
+                todo &= todo - 1;
+                if (todo) next = *row.at(j0 + 32 * (__ffs(todo) - 1));
+                if (row.raw) one.clean();
+                uint32_t hits = 0;
 #pragma unroll
-                for (int i = 0; i < B::kN; ++i) {
-                    const float l = one.get(i);
-                    if (hits >> i & 1)
-                        atomicAdd(&sh.lo[kMode == kCounts ? bin_of(sc, l) : (int)((hi - key_of(l)) >> arg)], 1u);
-                }
-            } else {
+                for (int i = 0; i < B::kN; ++i) hits |= one.get(i) >= least && one.get(i) <= most ? 1u << i : 0;
+                if constexpr (kMode == kCounts || kMode == kCountKeys) {
 #pragma unroll
-                for (int i = 0; i < B::kN; i += 2) {
-                    if (!(hits >> i & 3)) continue;
-                    u64 w[2];
-                    weight2(sc, one.get(i), one.get(i + 1), sh.powers, w[0], w[1]);
+                    for (int i = 0; i < B::kN; ++i) {
+                        const float l = one.get(i);
+                        if (hits >> i & 1)
+                            atomicAdd(&sh.lo[kMode == kCounts ? bin_of(sc, l) : (int)((hi - key_of(l)) >> arg)], 1u);
+                    }
+                } else {
+                    // (four at a time without a branch: each weight is a chain of some 25 steps)
 #pragma unroll
-                    for (int o = 0; o < 2; ++o) {
-                        const float l = one.get(i + o);
-                        if (!(hits >> (i + o) & 1)) continue;
-                        if constexpr (kMode == kFinal) {
-                            if (l > cut) wsum += w[o];
-                            ties += l == cut;
-                        } else {
-                            const int bin = kMode == kWeightKeys ? (int)((hi - key_of(l)) >> arg) : bin_of(sc, l);
-                            const uint32_t low = (uint32_t)w[o], old = atomicAdd(&sh.lo[bin], low);
-                            const uint32_t high = (uint32_t)(w[o] >> 32) + (old + low < old);
-                            if (high) atomicAdd(&sh.hi[bin], high);
+                    for (int i = 0; i < B::kN; i += 4) {
+                        if (!(hits >> i & 15)) continue;
+                        u64 w[4];
+                        weight2(sc, one.get(i), one.get(i + 1), sh.powers, w[0], w[1]);
+                        weight2(sc, one.get(i + 2), one.get(i + 3), sh.powers, w[2], w[3]);
+#pragma unroll
+                        for (int o = 0; o < 4; ++o) {
+                            const float l = one.get(i + o);
+                            const bool on = hits >> (i + o) & 1;
+                            if constexpr (kMode == kFinal) {
+                                wsum += on && l > cut ? w[o] : 0;
+                                ties += on && l == cut;
+                            } else {
+                                if (!on) continue;
+                                const int bin = kMode == kWeightKeys ? (int)((hi - key_of(l)) >> arg) : bin_of(sc, l);
+                                const uint32_t low = (uint32_t)w[o], old = atomicAdd(&sh.lo[bin], low);
+                                const uint32_t high = (uint32_t)(w[o] >> 32) + (old + low < old);
+                                if (high) atomicAdd(&sh.hi[bin], high);
+                            }
                         }
                     }
                 }
             }
         }
-    });
+    }
     __syncwarp();
     if (kMode == kTakeAndSum) {
 #pragma unroll
@@ -541,7 +562,7 @@ __device__ __noinline__ void share_bins(Shared &sh) {
     const int ctas = cl.num_blocks(), rank = cl.block_rank();
     __syncthreads();
     if (ctas == 1) return;
-    cl.sync();
+    row_sync();
     const int per = kBins / ctas;
     for (int i = rank * per + threadIdx.x; i < (rank + 1) * per; i += kThr) {
         u64 v = 0;
@@ -557,7 +578,7 @@ __device__ __noinline__ void share_bins(Shared &sh) {
             o->hi[i] = (uint32_t)(v >> 32);
         }
     }
-    cl.sync();
+    row_sync();
 }
 
 // The bin in which the running sum reaches `target` (> 0): sh.bin, and the sum before it in sh.before;
@@ -624,8 +645,19 @@ template <typename T, bool W> __device__ __noinline__ bool search(Shared &sh, do
     cg::cluster_group cl = cg::this_cluster();
     u64 target = sh.goal;
     const Cut cut = sh.cut;
+    uint32_t from = cut.key + 1;
     clear_bins(sh);
-    pass<T, W ? kWeights : kCounts>(sh, cut.key + 1, 0xffffffffu, 0);
+    if (!W && sh.task.tops) {
+        // the goal-th of the blocks' largest values is a bound of what is looked for, up to a bin
+        const T *tops = reinterpret_cast<const T *>(sh.task.tops);
+        for (int i = threadIdx.x; i < sh.task.b1 - sh.task.b0; i += kThr)
+            if ((float)tops[i] >= sh.live) atomicAdd(&sh.lo[bin_of(sh.sc, tops[i])], 1u);
+        share_bins(sh);
+        if (find_bin(sh, target)) from = max(from, bin_edge(sh.sc, sh.bin));
+        __syncthreads();
+        clear_bins(sh);
+    }
+    pass<T, W ? kWeights : kCounts>(sh, from, 0xffffffffu, 0);
     share_bins(sh);
     if (W) {
         u64 own = 0;
@@ -858,7 +890,7 @@ template <typename T> __device__ __noinline__ bool from_list(Shared &sh, int wan
         for (int i = 0; i < kWarps; ++i) all += sh.sums[i];
         sh.sum = all;
     }
-    cl.sync();
+    row_sync();
     if (rank == 0) {
         // a lane for each CTA reads how much it has listed
         const int lane = threadIdx.x & 31;
@@ -910,7 +942,7 @@ template <typename T> __device__ __noinline__ bool from_list(Shared &sh, int wan
         if (threadIdx.x == 0) sh.settled = fine ? 1 : undecided ? 2 : 0;
         listed = n;
     }
-    cl.sync();
+    row_sync();
     int settled = cl.map_shared_rank(&sh, 0)->settled;
     if (settled == 2) {
         // a border lies within the error of the fp32 sum: the row's weight as it is
@@ -922,7 +954,7 @@ template <typename T> __device__ __noinline__ bool from_list(Shared &sh, int wan
             for (int o = kWarps / 2; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffu, sum, o);
             if (threadIdx.x == 0) sh.wsum[0] = sum;
         }
-        cl.sync();
+        row_sync();
         if (rank == 0) {
             u64 z = 0;
             for (int c = 0; c < ctas; ++c) z += cl.map_shared_rank(&sh, c)->wsum[0];
@@ -931,7 +963,7 @@ template <typename T> __device__ __noinline__ bool from_list(Shared &sh, int wan
         }
         settled = 1;
     }
-    cl.sync();
+    row_sync();
     return settled != 0;
 }
 
@@ -964,7 +996,7 @@ template <typename T> __device__ __noinline__ void from_row(Shared &sh) {
 
     // weights and ties of every warp, in the order of the tokens
     pass<T, kFinal>(sh, cut.key, 0xffffffffu, 0);
-    cl.sync();
+    row_sync();
     const u64 w_tie = cut.ties ? weigh(sh, value_of(cut.key)) : 0;
     auto total = [&](u64 w, u64 t) { return w + w_tie * min(t, (u64)cut.ties); };
     {
@@ -1081,7 +1113,7 @@ template <typename T> __device__ __noinline__ void from_row(Shared &sh) {
             __syncthreads();
         }
     }
-    cl.sync();  // (shared memory of CTAs that have ended is not to be read)
+    row_sync();  // (shared memory of CTAs that have ended is not to be read)
 }
 
 template <typename T>
@@ -1201,7 +1233,7 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const Args a, int held_
             t.raw = false;
         }
     }
-    cl.sync();
+    row_sync();
     if (ctas > 1) {  // (a lane for each CTA: the reads do not wait for one another)
         if (lane < ctas) top = fmaxf(top, cl.map_shared_rank(&sh, lane)->top);
 #pragma unroll
@@ -1214,7 +1246,7 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const Args a, int held_
             *t.token = -1;
             if (t.logprob) *t.logprob = -INFINITY;
         }
-        cl.sync();
+        row_sync();
         return;
     }
     if (!(t.temp > 0.f)) {  // the first of the largest
@@ -1228,14 +1260,14 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const Args a, int held_
                 break;
             }
         }
-        cl.sync();
+        row_sync();
         if (rank == 0 && threadIdx.x == 0) {
             uint32_t first = 0xffffffffu;
             for (int c = 0; c < ctas; ++c) first = min(first, cl.map_shared_rank(&sh, c)->index);
             *t.token = (int)first;
             if (t.logprob) *t.logprob = 0.f;
         }
-        cl.sync();
+        row_sync();
         return;
     }
 
@@ -1259,12 +1291,14 @@ template <typename T> cudaError_t launch(const Args &a, cudaStream_t s) {
     const int room = kHeldBytes / 16, sms = std::max(1, device_sms());
     // CTAs of a row, for rows long enough. Few rows take several; with more rows the cluster's barriers
     // cost more than what they save. Rows of bf16 151936, us by 1, 2, 4 and 8 CTAs a row: 16 rows with
-    // top-k 20: 19.5, 17.6, 14.9, 16.2; 65: 19.8, 18.1, 18.5, 31.9; 100: 19.7, 23.5, 29.9, 46; 1040: 105,
-    // 159, 248, 438. Rows that no list serves are bound by instructions, and gain from a second CTA up to
-    // where all of them run at once: without cuts 16 rows 78, 46, 30, 28; 65: 78, 47, 47, 61; 192: 138, 109,
-    // 122, 152; 304: 140, 142, 182, 236. That is to be expected where neither top-k nor min-p is asked for.
-    const bool open = !a.top_k && !a.min_p;
-    int ctas = a.R <= sms / 16 ? 8 : a.R <= sms / 2 ? 4 : a.R <= (open ? 3 * sms / 2 : 0) ? 2 : 1;
+    // top-k 20: 16.2, 15.9, 14.3, 14.5; 65: 16.6, 16.2, 16.9, 29; 152: 16.5, 19.1, 42; 192: 22, 32, 46; 1040:
+    // 85, 132, 243. Rows that no list serves gain from more CTAs up to where all of them run at once: without
+    // cuts 16 rows 73, 45, 29, 27; 65: 74, 47, 45, 58; 152: 74, 74, 102; 192: 127, 106, 122; 304: 128, 138, 184;
+    // and rows of all kinds, where the slow ones are waited for, more: 152: 196, 130, 111; 192: 208, 131, 112.
+    // So with up to a row an SM two are taken, and up to one and a half where a list is not to be expected
+    // (neither top-k nor min-p is asked for) or each row has settings of its own.
+    const bool slow = a.group == 1 || (!a.top_k && !a.min_p);
+    int ctas = a.R <= sms / 16 ? 8 : a.R <= sms / 2 ? 4 : a.R <= (slow ? 3 * sms / 2 : sms) ? 2 : 1;
     while (ctas > 1 && blocks / ctas < kThr) ctas /= 2;
     const int per = (blocks + ctas - 1) / ctas;
     const int held = per <= room ? per : 0;
