@@ -8,9 +8,9 @@
 // one cluster of CTAs: each scans its slice, the slices' sums meet in distributed shared memory, and
 // the call's phases are cluster barriers instead of launches.
 //
-// Measured: the end, fork, growth and copies of 4 of 16 sequences 21 us, of 128 of 512 sequences 24.5 (four
-// launches, where the host's side of each is 5); compaction 15 at 1k pages and 12 at 16k, where its copies
-// take another 160, at the HBM's rate.
+// Measured: the end, fork, growth and copies of 4 of 16 sequences 19 us (the host's: four calls of 3.5 to 5;
+// 11.5 replayed from a graph), of 128 of 512 sequences 21.5; compaction 14 at 1k pages (9 from a graph) and
+// 13 at 16k, where its copies take another 154, at the HBM's rate.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -54,6 +54,15 @@ __device__ __forceinline__ bool sane(const Book &k, int held, int len) {
     return held >= 0 && held <= k.max_pages && len >= 0 && (long long)len <= (long long)held * k.page;
 }
 
+// A barrier of the call's CTAs. (A cluster's costs more than a CTA's even where it has one CTA.)
+__device__ __forceinline__ void call_sync() {
+    cg::cluster_group cl = cg::this_cluster();
+    if (cl.num_blocks() > 1)
+        cl.sync();
+    else
+        __syncthreads();
+}
+
 // Sums of the block's threads before this one (exclusive, in thread order) and of all.
 template <typename T> __device__ __forceinline__ T block_scan(T v, T *part, T *total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -80,10 +89,37 @@ template <typename T> __device__ __forceinline__ T block_scan(T v, T *part, T *t
     return s - v + (warp ? part[warp - 1] : 0);
 }
 
+// The same of values up to `cap`, sums cut at it: the value before a thread is then at least what makes
+// the sum with its own exceed cap - 1.
+__device__ __forceinline__ int capped_scan(int v, int cap, int *part, int *total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int s = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s = min(s + t, cap);
+    }
+    __syncthreads();
+    if (lane == 31) part[warp] = s;
+    __syncthreads();
+    int p = part[lane], all = 0;  // (every warp scans the warps' sums itself)
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, p, o);
+        if (lane >= o) p = min(p + t, cap);
+    }
+    all = __shfl_sync(0xffffffffu, p, 31);
+    const int before = __shfl_sync(0xffffffffu, p, max(warp - 1, 0));
+    *total = all;
+    return min((warp ? before : 0) + s, cap) - v;
+}
+
 // The cluster's warps share the pages [lo, hi) in contiguous runs, in order. Every warp gets the
 // number of pages before its run for which `pick` holds; total: of all. Called by all threads.
+constexpr int kDeep = 8;  // loads on their way
 struct Run {
     int lo, hi, before, total;
+    int v[kDeep];  // a lane's first pages
 };
 template <class Pick>
 __device__ __forceinline__ Run cluster_count(const int *ref, int lo, int hi, int *part, int *mine,
@@ -99,12 +135,23 @@ __device__ __forceinline__ Run cluster_count(const int *ref, int lo, int hi, int
     r.lo = (int)min((long long)max(lo, hi), first);
     r.hi = (int)min((long long)max(lo, hi), first + per);
     int c = 0;
-#pragma unroll 8
-    for (int p = r.lo + lane; p < r.hi; p += 32) c += pick(p, ref[p]);
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+    for (int q = 0; q < kDeep; ++q) r.v[q] = ref[max(0, min(r.lo + 32 * q + lane, r.hi - 1))];
+#pragma unroll
+    for (int q = 0; q < kDeep; ++q) {
+        const int p = r.lo + 32 * q + lane;
+        c += p < r.hi && pick(p, r.v[q]);
+    }
+#pragma unroll 8
+    for (int p = r.lo + 32 * kDeep + lane; p < r.hi; p += 32) c += pick(p, ref[p]);
+    c = __reduce_add_sync(0xffffffffu, c);
     int sum;
     const int at = block_scan(lane == 0 ? c : 0, part, &sum);  // warps in order
+    if (ctas == 1) {
+        r.before = __shfl_sync(0xffffffffu, at, 0);
+        r.total = sum;
+        return r;
+    }
     if (threadIdx.x == 0) *mine = sum;
     cl.sync();
     // (a lane for each CTA: the reads do not wait for one another)
@@ -121,13 +168,17 @@ __device__ __forceinline__ Run cluster_count(const int *ref, int lo, int hi, int
 // fewer than `want` before them.
 template <class Pick, class Put>
 __device__ __forceinline__ void cluster_emit(const int *ref, const Run &r, int want, Pick pick, Put put) {
-    constexpr int kDeep = 8;  // loads on their way
     const int lane = threadIdx.x & 31;
     int at = r.before;
-    for (int p0 = r.lo; p0 < r.hi && at < want; p0 += 32 * kDeep) {
-        int v[kDeep];
+    int v[kDeep];
 #pragma unroll
-        for (int q = 0; q < kDeep; ++q) v[q] = ref[min(p0 + 32 * q + lane, r.hi - 1)];
+    for (int q = 0; q < kDeep; ++q) v[q] = r.v[q];
+#pragma unroll 1
+    for (int p0 = r.lo; p0 < r.hi && at < want; p0 += 32 * kDeep) {
+        if (p0 > r.lo) {
+#pragma unroll
+            for (int q = 0; q < kDeep; ++q) v[q] = ref[min(p0 + 32 * q + lane, r.hi - 1)];
+        }
 #pragma unroll
         for (int q = 0; q < kDeep; ++q) {
             const int p = p0 + 32 * q + lane;
@@ -142,11 +193,16 @@ __device__ __forceinline__ void cluster_emit(const int *ref, const Run &r, int w
 
 __device__ __forceinline__ bool is_free(int, int ref) { return ref <= 0; }
 
-// The first `want` free pages go to k.list, ascending. Returns how many free pages there are.
-__device__ __forceinline__ int list_free(const Book &k, int want, int *part, int *mine) {
-    const Run r = cluster_count(k.ref, 0, k.n_pages, part, mine, is_free);
-    cluster_emit(k.ref, r, want, is_free, [&](int p, int i, int) { k.list[i] = p; });
-    return r.total;
+__device__ __forceinline__ Run count_free(const Book &k, int *part, int *mine) {
+    return cluster_count(k.ref, 0, k.n_pages, part, mine, is_free);
+}
+// The first `want` free pages, ascending: in `here` (of kSmall), where one CTA makes the call and
+// wants no more, else in k.list. To be read after a call_sync.
+constexpr int kSmall = 1024;
+__device__ __forceinline__ const int *list_free(const Book &k, const Run &r, int want, int *here) {
+    int *list = cg::this_cluster().num_blocks() == 1 && want <= kSmall ? here : k.list;
+    cluster_emit(k.ref, r, want, is_free, [&](int p, int i, int) { list[i] = p; });
+    return list;
 }
 
 // ------------------------------------------------------------------ free
@@ -196,144 +252,234 @@ __global__ void __launch_bounds__(128) free_kernel(Book k, const int *seqs, cons
 // ------------------------------------------------------------------ reserve
 
 __global__ void __launch_bounds__(kThr) reserve_kernel(Book k, int N, const int *n_new) {
-    __shared__ int part[kWarps], mine;
-    __shared__ long long part2[kWarps];
+    __shared__ int part[kWarps], mine, here[kSmall];
     pdl_wait();
     const int rank = cg::this_cluster().block_rank(), ctas = cg::this_cluster().num_blocks();
-    // pages that each sequence lacks, and those that the sequences before it lack: every CTA counts
-    // for itself, the first one writes them down
-    auto lacks = [&](int b, bool tell) {
-        const int held = k.held[b], len = k.len[b], more = n_new ? n_new[b] : N;
-        if (!sane(k, held, len) || more < 0) {
-            if (tell) flag(k, attn::FLAG_BAD_SEQUENCE);
-            return 0;
-        }
-        const long long want = ((long long)len + more + k.page - 1) / k.page;
-        if (want > k.max_pages) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // pages that a sequence lacks, up to one more than there are
+    auto lacks = [&](int held, int len, int more, bool tell) {
+        // (len and page_size are 2^30 at most)
+        const unsigned want = ((unsigned)len + (unsigned)more + (unsigned)k.page - 1) / (unsigned)k.page;
+        if (!sane(k, held, len) || more < 0 || want > (unsigned)k.max_pages) {
             if (tell) flag(k, attn::FLAG_BAD_SEQUENCE);
             return 0;
         }
         return min(max(0, (int)want - held), k.n_pages + 1);
     };
-    long long total = 0;
-    for (int b0 = 0; b0 < k.B; b0 += kThr) {
+    // How many the sequences before it lack (sums are cut at n_pages + 1: what lies behind is not served
+    // anyway): every CTA counts for itself. The loads of the last sequences are on their way beside those
+    // of the free pages.
+    const int cap = k.n_pages + 1;
+    int total = 0, b0 = 0;
+    for (; b0 + kThr < k.B; b0 += kThr) {
         const int b = b0 + threadIdx.x;
-        const long long need = b < k.B ? lacks(b, rank == 0) : 0;
-        long long sum;
-        const long long at = block_scan(need, part2, &sum);
-        // (sums are cut at n_pages + 1: what lies behind is not served anyway)
-        if (rank == 0 && b < k.B) k.off[b] = (int)min(total + at, (long long)k.n_pages + 1);
-        total = min(total + sum, (long long)k.n_pages + 1);
+        const int need = lacks(k.held[b], k.len[b], n_new ? n_new[b] : N, rank == 0);
+        int sum;
+        const int at = capped_scan(need, cap, part, &sum);
+        if (rank == 0) k.off[b] = min(total + at, cap);
+        total = min(total + sum, cap);
     }
-    const int want = (int)min(total, (long long)k.n_pages);
+    const int b = b0 + threadIdx.x, held = b < k.B ? k.held[b] : 0, len = b < k.B ? k.len[b] : 0;
+    const int more = n_new ? b < k.B ? n_new[b] : 0 : N;
+    const Run r = count_free(k, part, &mine);
+    const int need = b < k.B ? lacks(held, len, more, rank == 0) : 0;
+    int sum;
+    const int at = min(total + capped_scan(need, cap, part, &sum), cap);
+    total = min(total + sum, cap);
+    const int have = r.total, want = min(total, k.n_pages);
     if (want == 0) return;
-    const int have = list_free(k, want, part, &mine);
-    cg::this_cluster().sync();
-    const int lane = threadIdx.x & 31;
-    for (int b = rank * kWarps + (threadIdx.x >> 5); b < k.B; b += ctas * kWarps) {
-        const int need = lacks(b, false), at = k.off[b], held = k.held[b];
+    const int *list = list_free(k, r, want, here);
+    call_sync();
+    auto serve = [&](int seq, int first, int held_, int need_, int from, int step) {
+        for (int j = from; j < need_; j += step) {
+            const int p = list[first + j];
+            k.table[(size_t)seq * k.max_pages + held_ + j] = p;
+            k.ref[p] = 1;
+        }
+    };
+    // The last sequences: a thread for each, and a warp for what it lacks where that is more than a few.
+    // The CTAs take turns by warps.
+    const bool mine_to_do = warp % ctas == rank;
+    const bool met = at + need <= have;
+    if (mine_to_do && need > 0) {
+        if (!met) flag(k, FLAG_NO_PAGES);
+        if (met) {
+            if (need <= 8) serve(b, at, held, need, 0, 1);
+            k.held[b] = held + need;
+        }
+    }
+    if (mine_to_do) {
+        uint32_t many = __ballot_sync(0xffffffffu, met && need > 8);
+        for (; many; many &= many - 1) {
+            const int l = __ffs(many) - 1;
+            serve(b0 + warp * 32 + l, __shfl_sync(0xffffffffu, at, l), __shfl_sync(0xffffffffu, held, l),
+                  __shfl_sync(0xffffffffu, need, l), lane, 32);
+        }
+    }
+    // those before them, a warp for each
+    for (int q = rank * kWarps + warp; q < b0; q += ctas * kWarps) {
+        const int held_q = k.held[q], first = k.off[q];
+        const int need_q = lacks(held_q, k.len[q], n_new ? n_new[q] : N, false);
         __syncwarp();  // (held is written below)
-        if (need == 0) continue;
-        if (at + need > have) {
+        if (need_q == 0) continue;
+        if (first + need_q > have) {
             if (lane == 0) flag(k, FLAG_NO_PAGES);
             continue;
         }
-        for (int j = lane; j < need; j += 32) {
-            const int p = k.list[at + j];
-            k.table[(size_t)b * k.max_pages + held + j] = p;
-            k.ref[p] = 1;
-        }
-        if (lane == 0) k.held[b] = held + need;
+        serve(q, first, held_q, need_q, lane, 32);
+        if (lane == 0) k.held[q] = held_q + need_q;
     }
 }
 
 // ------------------------------------------------------------------ fork
 
 constexpr int kForkCols = 256;  // table entries of a warp's piece
+constexpr int kFewForks = 256;  // entries that every CTA keeps in shared memory
 
+struct Fork {
+    int src, dst, len;
+    int at;  // number of its page among those that the call takes; -1: no fork
+};
+
+// One entry's piece of a table row: full pages are shared, what is behind them gets a page of its own.
+__device__ __forceinline__ void fork_piece(const Book &k, const Fork &f, int i, int piece, int have,
+                                           const int *list, int *moves) {
+    const int lane = threadIdx.x & 31;
+    const int full = f.at < 0 ? 0 : f.len / k.page, tail = f.at < 0 ? -1 : f.len - full * k.page;
+    const bool short_of = tail > 0 && f.at >= have;
+    if (tail < 0 || short_of) {
+        if (piece == 0 && lane < 3) moves[3 * i + lane] = lane == 2 ? 0 : -1;
+        if (piece == 0 && lane == 0 && short_of) flag(k, FLAG_NO_PAGES);
+        return;
+    }
+    const int *from = k.table + (size_t)f.src * k.max_pages;
+    int *to = k.table + (size_t)f.dst * k.max_pages;
+    const int end = min(full, (piece + 1) * kForkCols);
+    const int old = piece == 0 && lane == 0 && tail > 0 ? from[full] : -1;
+#pragma unroll 4
+    for (int j = piece * kForkCols + lane; j < end; j += 32) {
+        const int p = from[j];
+        to[j] = p;
+        if (p >= 0 && p < k.n_pages)
+            atomicAdd(&k.ref[p], 1);
+        else
+            flag(k, attn::FLAG_BAD_PAGE);
+    }
+    if (piece || lane) return;
+    int fresh = -1;
+    if (tail > 0) {
+        fresh = list[f.at];
+        to[full] = fresh;
+        k.ref[fresh] = 1;
+    }
+    moves[3 * i] = old;
+    moves[3 * i + 1] = fresh;
+    moves[3 * i + 2] = tail;
+    k.held[f.dst] = full + (tail > 0);
+    k.len[f.dst] = f.len;
+}
+
+// FEW: up to kFewForks entries. Every CTA works all of them out for itself, a thread for each, from three
+// loads that wait for one another (the entry, its sequences, the table), beside which the counts are read.
+template <bool FEW>
 __global__ void __launch_bounds__(kThr)
 fork_kernel(Book k, const int *src, const int *dst, int n, int *moves) {
     __shared__ int part[kWarps], mine;
+    __shared__ Fork forks[FEW ? kFewForks : 1];
+    __shared__ int here[FEW ? kSmall : 1], counts[kWarps];
     pdl_wait();
     cg::cluster_group cl = cg::this_cluster();
     const int rank = cl.block_rank(), ctas = cl.num_blocks();
-    const int lane = threadIdx.x & 31, gt = rank * kThr + threadIdx.x;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gt = rank * kThr + threadIdx.x;
     auto in = [&](int b) { return b >= 0 && b < k.B; };
-    // the first entry that names a sequence as its target has it
-    for (int i = gt; i < n; i += ctas * kThr) {
-        if (in(src[i])) k.claim[src[i]] = n;
-        if (in(dst[i])) k.claim[dst[i]] = n;
-    }
-    cl.sync();
-    for (int i = gt; i < n; i += ctas * kThr)
-        if (in(dst[i])) atomicMin(&k.claim[dst[i]], i);
-    cl.sync();
-    // Tokens behind the last full page, or -1: no fork. (A target is never a source, so what is read
-    // here of a source is not written by the call.)
-    auto tail_of = [&](int i) {
-        const int a = src[i], b = dst[i];
-        if (!in(a) || !in(b) || k.claim[b] != i || k.claim[a] != n) return -1;
-        if (!sane(k, k.held[a], k.len[a])) return -1;
-        return k.len[a] % k.page;
-    };
-    // entries that need a page, and how many do before each: every CTA counts for itself
-    int total = 0;
-    for (int i0 = 0; i0 < n; i0 += kThr) {
-        const int i = i0 + threadIdx.x;
-        int tail = -1;
-        if (i < n) {
-            tail = tail_of(i);
-            if (tail >= 0 && k.held[dst[i]] != 0) tail = -1;
-            if (tail < 0 && rank == 0) flag(k, attn::FLAG_BAD_SEQUENCE);
-        }
-        int sum;
-        const int at = block_scan((int)(tail > 0), part, &sum);
-        // (-1: no fork)
-        if (rank == 0 && i < n) k.off[i] = tail < 0 ? -1 : total + at;
-        total += sum;
-    }
-    const int have = list_free(k, min(total, k.n_pages), part, &mine);
-    cl.sync();
-    // pieces of table rows: full pages are shared, what is behind them gets a page of its own
     const int pieces = (k.max_pages + kForkCols - 1) / kForkCols;
     const long long items = (long long)n * pieces;
-    for (long long it = rank * kWarps + (threadIdx.x >> 5); it < items; it += ctas * kWarps) {
-        const int i = (int)(it / pieces), piece = (int)(it - (long long)i * pieces);
-        const int at = k.off[i];
-        int tail = at < 0 ? -1 : tail_of(i);
-        const bool short_of = tail > 0 && at >= have;
-        if (short_of) tail = -1;
-        if (tail < 0) {
-            if (piece == 0 && lane < 3) moves[3 * i + lane] = lane == 2 ? 0 : -1;
-            if (piece == 0 && lane == 0 && short_of) flag(k, FLAG_NO_PAGES);
-            continue;
+    if constexpr (FEW) {
+        const int t = threadIdx.x;
+        int a = -1, b = -1;
+        if (t < n) {
+            a = src[t];
+            b = dst[t];
+            forks[t].src = a;
+            forks[t].dst = b;
         }
-        const int a = src[i], b = dst[i], len = k.len[a], full = len / k.page;
-        const int *from = k.table + (size_t)a * k.max_pages;
-        int *to = k.table + (size_t)b * k.max_pages;
-        const int end = min(full, (piece + 1) * kForkCols);
-#pragma unroll 4
-        for (int j = piece * kForkCols + lane; j < end; j += 32) {
-            const int p = from[j];
-            to[j] = p;
-            if (p >= 0 && p < k.n_pages)
-                atomicAdd(&k.ref[p], 1);
-            else
-                flag(k, attn::FLAG_BAD_PAGE);
+        const Run r = count_free(k, part, &mine);
+        int tail = -1;
+        if (t < n && in(a) && in(b)) {
+            const int held = k.held[a], len = k.len[a], empty = k.held[b];
+            // the first entry that names a sequence as its target has it; a target is no source
+            bool ok = true;
+#pragma unroll 8
+            for (int j = 0; j < n; ++j) {
+                const int other = forks[j].dst;
+                ok = ok && other != a && (j >= t || other != b);
+            }
+            if (ok && empty == 0 && sane(k, held, len)) {
+                tail = len % k.page;
+                forks[t].len = len;
+            }
         }
-        if (piece || lane) continue;
-        int old = -1, fresh = -1;
-        if (tail > 0) {
-            old = from[full];
-            fresh = k.list[at];
-            to[full] = fresh;
-            k.ref[fresh] = 1;
+        if (t < n && tail < 0 && rank == 0) flag(k, attn::FLAG_BAD_SEQUENCE);
+        // entries that need a page, and how many do before each
+        const uint32_t needs = __ballot_sync(0xffffffffu, tail > 0);
+        if (lane == 0) counts[warp] = __popc(needs);
+        __syncthreads();
+        const int c = counts[lane];
+        const int total = __reduce_add_sync(0xffffffffu, c);
+        const int before = __reduce_add_sync(0xffffffffu, lane < warp ? c : 0);
+        if (t < n) forks[t].at = tail < 0 ? -1 : before + __popc(needs & ((1u << lane) - 1));
+        const int *list = list_free(k, r, min(total, k.n_pages), here);
+        call_sync();
+        for (long long it = rank * kWarps + warp; it < items; it += ctas * kWarps) {
+            const int i = (int)(it / pieces), piece = (int)(it - (long long)i * pieces);
+            fork_piece(k, forks[i], i, piece, r.total, list, moves);
         }
-        moves[3 * i] = old;
-        moves[3 * i + 1] = fresh;
-        moves[3 * i + 2] = tail;
-        k.held[b] = full + (tail > 0);
-        k.len[b] = len;
+    } else {
+        for (int i = gt; i < n; i += ctas * kThr) {
+            if (in(src[i])) k.claim[src[i]] = n;
+            if (in(dst[i])) k.claim[dst[i]] = n;
+        }
+        call_sync();
+        for (int i = gt; i < n; i += ctas * kThr)
+            if (in(dst[i])) atomicMin(&k.claim[dst[i]], i);
+        call_sync();
+        // An entry without its `at`. (A target is never a source, so what is read here of a source is not
+        // written by the call.)
+        auto entry = [&](int i) {
+            Fork f{src[i], dst[i], 0, -1};
+            if (!in(f.src) || !in(f.dst) || k.claim[f.dst] != i || k.claim[f.src] != n) return f;
+            if (!sane(k, k.held[f.src], k.len[f.src])) return f;
+            f.len = k.len[f.src];
+            f.at = 0;
+            return f;
+        };
+        int total = 0;
+        for (int i0 = 0; i0 < n; i0 += kThr) {
+            const int i = i0 + threadIdx.x;
+            int tail = -1;
+            if (i < n) {
+                const Fork f = entry(i);
+                if (f.at == 0 && k.held[f.dst] == 0) tail = f.len % k.page;
+                if (tail < 0 && rank == 0) flag(k, attn::FLAG_BAD_SEQUENCE);
+            }
+            int sum;
+            const int at = block_scan((int)(tail > 0), part, &sum);
+            if (rank == 0 && i < n) k.off[i] = tail < 0 ? -1 : total + at;
+            total += sum;
+        }
+        const Run r = count_free(k, part, &mine);
+        cluster_emit(k.ref, r, min(total, k.n_pages), is_free, [&](int p, int i, int) { k.list[i] = p; });
+        call_sync();
+        for (long long it = rank * kWarps + warp; it < items; it += ctas * kWarps) {
+            const int i = (int)(it / pieces), piece = (int)(it - (long long)i * pieces);
+            const int at = k.off[i];
+            Fork f{-1, -1, 0, -1};
+            if (at >= 0) {
+                f = entry(i);
+                f.at = at;
+            }
+            fork_piece(k, f, i, piece, r.total, k.list, moves);
+        }
     }
 }
 
@@ -486,7 +632,11 @@ cudaError_t launch_cluster(void (*kernel)(KArgs...), bool wide, cudaStream_t s, 
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
-constexpr int kWidePages = 8192;
+// us by one CTA and by eight: reserving 2000 pages 3.7, 5.3; 8000: 4.1, 5.4; 12000: 5.5, 5.5; 16000: 5.3, 5.4;
+// 25000: 7.3, 5.3; 65000: 12.3, 5.6; plans of compaction 6.8, 11.6; 8.9, 12.0; 11.0, 12.2; 12.7, 12.3; 17.7, 13.3;
+// 40, 15.5.
+constexpr int kWidePages = 14000;
+constexpr int kWideEntries = 32768;  // of a fork's tables
 
 }  // namespace
 
@@ -502,8 +652,9 @@ cudaError_t launch_reserve(const moe_page_book &K, int N, const int *n_new, void
 
 cudaError_t launch_fork(const moe_page_book &K, const int *src, const int *dst, int n, int *moves,
                         void *ws, cudaStream_t s) {
-    const bool wide = K.n_pages > kWidePages || (long long)n * K.max_pages > 4 * kWidePages;
-    return launch_cluster(fork_kernel, wide, s, book(K, ws), src, dst, n, moves);
+    const bool wide = K.n_pages > kWidePages || (long long)n * K.max_pages > kWideEntries;
+    return launch_cluster(n <= kFewForks ? fork_kernel<true> : fork_kernel<false>, wide, s, book(K, ws), src,
+                          dst, n, moves);
 }
 
 cudaError_t launch_compact(const moe_page_book &K, int *table_out, int *ref_out, int *moves,

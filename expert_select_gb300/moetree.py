@@ -749,6 +749,7 @@ def page_book(page_table, held, cache_len, ref, page_size: int) -> PageBook:
     K = PageBook(page_table.data_ptr(), held.data_ptr(), cache_len.data_ptr(), ref.data_ptr(), B,
                  width, ref.numel(), page_size)
     K.tensors, K.index, K.desc = (page_table, held, cache_len, ref), index, C.byref(K)
+    K.need = None  # bytes of workspace, asked for once
     return K
 
 
@@ -767,8 +768,9 @@ def pages_workspace(K: PageBook, device=None) -> torch.Tensor:
 def _pages_scratch(fn, K, ws):
     if ws is None:
         raise ValueError(f"{fn}: it needs a workspace")
-    _scratch(fn, ws, K.index, _lib.moe_pages_workspace_bytes(K.desc) if _lib else
-             moe_pages_workspace_bytes(K))
+    if K.need is None:
+        K.need = moe_pages_workspace_bytes(K)
+    _scratch(fn, ws, K.index, K.need)
     return K.desc, ws.data_ptr()
 
 

@@ -723,3 +723,26 @@ def test_copy_pages_past_4_gb():
         M.moe_kv_copy_pages(C, p, p, torch.tensor([[n - 1, 3, 64], [n - 1, n - 2, 9]], dtype=torch.int32, device=DEV))
         assert torch.equal(p[3], want) and torch.equal(p[n - 1], want)
         assert torch.equal(p[n - 2, :9], want[:9]) and bool((p[n - 2, 9:] == 5).all())
+
+
+@pytest.mark.parametrize("B,n,page", [(1500, 700, 5), (2300, 900, 16), (700, 256, 4), (700, 257, 4)])
+def test_pages_of_many_sequences(B, n, page):
+    """More forks than a thread block keeps, more sequences than it has threads, entries that are refused
+    among them, and too few pages for the last."""
+    k = Book(B, B, 30, 9 * B, page, used=0.2)
+    r = k.r
+    k.free(list(range(0, B, 2)))
+    k.same()
+    empty = [b for b in range(B) if k.held[b] == 0]
+    full = [b for b in range(B) if k.held[b]]
+    dst = [int(v) for v in r.choice(empty, n)]  # with repeats
+    src = [int(v) for v in r.choice(full, n)]
+    for i in r.integers(0, n, 12):
+        src[i] = int(r.choice([-1, B, dst[0], 1 << 30]))
+        dst[(i + 5) % n] = int(r.choice([-7, B, full[0]]))
+    k.fork(src, dst)
+    k.same()
+    k.reserve(r.integers(0, 25 * page, B).astype(np.int32))  # more than there are
+    k.same()
+    k.reserve(1)
+    k.same()
