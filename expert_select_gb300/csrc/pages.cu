@@ -114,6 +114,31 @@ __device__ __forceinline__ int capped_scan(int v, int cap, int *part, int *total
     return min((warp ? before : 0) + s, cap) - v;
 }
 
+// The same of a value of each warp, over the cluster's. `mine` is read by the other CTAs.
+template <typename T>
+__device__ __forceinline__ T cluster_scan(T v, T *part, T *mine, T *total) {
+    cg::cluster_group cl = cg::this_cluster();
+    const int ctas = cl.num_blocks(), rank = cl.block_rank(), lane = threadIdx.x & 31;
+    T sum;
+    const T at = __shfl_sync(0xffffffffu, block_scan(lane == 0 ? v : T(0), part, &sum), 0);
+    if (ctas == 1) {
+        *total = sum;
+        return at;
+    }
+    if (threadIdx.x == 0) *mine = sum;
+    cl.sync();
+    // (a lane for each CTA: the reads do not wait for one another)
+    T all = lane < ctas ? *cl.map_shared_rank(mine, lane) : T(0), base = lane < rank ? all : T(0);
+#pragma unroll
+    for (int o = kCluster / 2; o >= 1; o >>= 1) {
+        all += __shfl_xor_sync(0xffffffffu, all, o);
+        base += __shfl_xor_sync(0xffffffffu, base, o);
+    }
+    cl.sync();  // (`mine` may be written again)
+    *total = __shfl_sync(0xffffffffu, all, 0);
+    return __shfl_sync(0xffffffffu, base, 0) + at;
+}
+
 // The cluster's warps share the pages [lo, hi) in contiguous runs, in order. Every warp gets the
 // number of pages before its run for which `pick` holds; total: of all. Called by all threads.
 constexpr int kDeep = 8;  // loads on their way
@@ -144,23 +169,7 @@ __device__ __forceinline__ Run cluster_count(const int *ref, int lo, int hi, int
     }
 #pragma unroll 8
     for (int p = r.lo + 32 * kDeep + lane; p < r.hi; p += 32) c += pick(p, ref[p]);
-    c = __reduce_add_sync(0xffffffffu, c);
-    int sum;
-    const int at = block_scan(lane == 0 ? c : 0, part, &sum);  // warps in order
-    if (ctas == 1) {
-        r.before = __shfl_sync(0xffffffffu, at, 0);
-        r.total = sum;
-        return r;
-    }
-    if (threadIdx.x == 0) *mine = sum;
-    cl.sync();
-    // (a lane for each CTA: the reads do not wait for one another)
-    const int count = lane < ctas ? *cl.map_shared_rank(mine, lane) : 0;
-    const int base = __reduce_add_sync(0xffffffffu, lane < rank ? count : 0);
-    const int total = __reduce_add_sync(0xffffffffu, count);
-    cl.sync();  // (`mine` may be written again)
-    r.before = base + __shfl_sync(0xffffffffu, at, 0);
-    r.total = total;
+    r.before = cluster_scan(__reduce_add_sync(0xffffffffu, c), part, mine, &r.total);
     return r;
 }
 
@@ -485,48 +494,11 @@ fork_kernel(Book k, const int *src, const int *dst, int n, int *moves) {
 
 // ------------------------------------------------------------------ compact
 
-__global__ void __launch_bounds__(kThr)
-compact_kernel(Book k, int *ref_out, int *moves, int *counts) {
-    __shared__ int part[kWarps], mine;
-    pdl_wait();
-    cg::cluster_group cl = cg::this_cluster();
-    auto is_used = [](int, int ref) { return ref > 0; };
-    const int n = k.n_pages;
-    const int n_used = cluster_count(k.ref, 0, n, part, &mine, is_used).total;
-    // holes below n_used, in ascending order
-    const Run holes = cluster_count(k.ref, 0, n_used, part, &mine, is_free);
-    cluster_emit(k.ref, holes, n, is_free, [&](int p, int i, int) { k.list[i] = p; });
-    // pages that stay. (ref_out may be ref: nothing that is read here changes before the barriers of
-    // the next count.)
-    for (int p = cl.block_rank() * kThr + threadIdx.x; p < n; p += cl.num_blocks() * kThr) {
-        const int ref = k.ref[p];
-        if (ref > 0 && p >= n_used) continue;
-        k.map[p] = ref > 0 ? p : -1;
-        if (ref > 0 || p >= n_used) ref_out[p] = max(ref, 0);
-    }
-    // pages at n_used and above go to the holes, in order
-    const Run high = cluster_count(k.ref, n_used, n, part, &mine, is_used);
-    cluster_emit(k.ref, high, n, is_used, [&](int p, int i, int ref) {
-        const int to = k.list[i];
-        k.map[p] = to;
-        ref_out[to] = ref;
-        ref_out[p] = 0;
-        moves[3 * (size_t)i] = p;
-        moves[3 * (size_t)i + 1] = to;
-        moves[3 * (size_t)i + 2] = k.page;
-    });
-    if (cl.block_rank() == 0 && threadIdx.x == 0) {
-        counts[0] = high.total;
-        counts[1] = n_used;
-    }
-}
-
-// Table entries follow the pages. A row's entries behind what it holds stay as they are.
-__global__ void __launch_bounds__(256) remap_kernel(Book k, int *table_out) {
-    pdl_wait();
-    const long long all = (long long)k.B * k.max_pages;
-    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < all; i += gridDim.x * 256ll) {
-        const int b = (int)(i / k.max_pages), j = (int)(i - (long long)b * k.max_pages);
+// The table with its pages' new numbers: entries `first`, `first` + `step`, ..
+template <typename I>
+__device__ __forceinline__ void remap(const Book &k, int *table_out, I all, I first, I step) {
+    for (I i = first; i < all; i += step) {
+        const int b = (int)(i / (I)k.max_pages), j = (int)(i - (I)b * (I)k.max_pages);
         int p = k.table[i];
         const int held = k.held[b];
         if (j == 0 && (held < 0 || held > k.max_pages)) flag(k, attn::FLAG_BAD_SEQUENCE);
@@ -539,6 +511,70 @@ __global__ void __launch_bounds__(256) remap_kernel(Book k, int *table_out) {
         }
         table_out[i] = p;
     }
+}
+
+// entries: of the table, where the cluster renames them itself; else 0, and remap_kernel does.
+__global__ void __launch_bounds__(kThr)
+compact_kernel(Book k, int *table_out, int *ref_out, int *moves, int *counts, unsigned entries) {
+    __shared__ int part[kWarps], mine;
+    __shared__ long long pairs[kWarps], my_pair;
+    pdl_wait();
+    cg::cluster_group cl = cg::this_cluster();
+    const int lane = threadIdx.x & 31, n = k.n_pages;
+    auto is_used = [](int, int ref) { return ref > 0; };
+    Run r = cluster_count(k.ref, 0, n, part, &mine, is_used);
+    const int n_used = r.total;
+    auto is_hole = [&](int p, int ref) { return p < n_used && ref <= 0; };
+    auto is_high = [&](int p, int ref) { return p >= n_used && ref > 0; };
+    // The run's holes below n_used and pages in use above it; what stays or is free is written at once.
+    // (ref_out may be ref: a free page's count becomes 0, others' change behind the next barrier)
+    int holes = 0, high = 0;
+    auto look = [&](int p, int ref) {
+        holes += is_hole(p, ref);
+        high += is_high(p, ref);
+        if (is_high(p, ref)) return;
+        k.map[p] = ref > 0 ? p : -1;
+        if (ref > 0 || p >= n_used) ref_out[p] = max(ref, 0);
+    };
+#pragma unroll
+    for (int q = 0; q < kDeep; ++q) {
+        const int p = r.lo + 32 * q + lane;
+        if (p < r.hi) look(p, r.v[q]);
+    }
+#pragma unroll 4
+    for (int p = r.lo + 32 * kDeep + lane; p < r.hi; p += 32) look(p, k.ref[p]);
+    long long total;
+    const long long before = cluster_scan((long long)__reduce_add_sync(0xffffffffu, high) << 32 |
+                                              __reduce_add_sync(0xffffffffu, holes),
+                                          pairs, &my_pair, &total);
+    r.before = (int)(before & 0xffffffff);
+    cluster_emit(k.ref, r, n, is_hole, [&](int p, int i, int) { k.list[i] = p; });
+    call_sync();
+    // pages at n_used and above go to the holes, in order
+    r.before = (int)(before >> 32);
+    cluster_emit(k.ref, r, n, is_high, [&](int p, int i, int ref) {
+        const int to = k.list[i];
+        k.map[p] = to;
+        ref_out[to] = ref;
+        ref_out[p] = 0;
+        moves[3 * (size_t)i] = p;
+        moves[3 * (size_t)i + 1] = to;
+        moves[3 * (size_t)i + 2] = k.page;
+    });
+    if (cl.block_rank() == 0 && threadIdx.x == 0) {
+        counts[0] = (int)(total >> 32);
+        counts[1] = n_used;
+    }
+    if (entries) {
+        call_sync();
+        remap<unsigned>(k, table_out, entries, cl.block_rank() * kThr + threadIdx.x, cl.num_blocks() * kThr);
+    }
+}
+
+__global__ void __launch_bounds__(256) remap_kernel(Book k, int *table_out) {
+    pdl_wait();
+    remap<long long>(k, table_out, (long long)k.B * k.max_pages, blockIdx.x * 256ll + threadIdx.x,
+                     gridDim.x * 256ll);
 }
 
 // ------------------------------------------------------------------ copy
@@ -660,10 +696,13 @@ cudaError_t launch_fork(const moe_page_book &K, const int *src, const int *dst, 
 cudaError_t launch_compact(const moe_page_book &K, int *table_out, int *ref_out, int *moves,
                            int *counts, void *ws, cudaStream_t s) {
     const Book k = book(K, ws);
-    cudaError_t err = launch_cluster(compact_kernel, K.n_pages > kWidePages, s, k, ref_out, moves,
-                                     counts);
-    if (err != cudaSuccess) return err;
+    const bool wide = K.n_pages > kWidePages;
     const long long all = (long long)K.B * K.max_pages;
+    // A few entries a thread cost less than a launch.
+    const bool here = all <= 8ll * kThr * (wide ? kCluster : 1);
+    const cudaError_t err = launch_cluster(compact_kernel, wide, s, k, table_out, ref_out, moves, counts,
+                                           here ? (unsigned)all : 0u);
+    if (err != cudaSuccess || here) return err;
     const int ctas = (int)std::min<long long>((all + 255) / 256, 8ll * std::max(1, device_sms()));
     return launch_pdl(remap_kernel, dim3(ctas), dim3(256), 0, s, k, table_out);
 }

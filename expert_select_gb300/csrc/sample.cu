@@ -8,7 +8,7 @@
 // A token of thousands follows from comparisons of sums of up to V weights, so sums that depend on the
 // order of threads, or that are off by fp32's roundings, give another token every few thousand
 // rows. Weights are therefore integers of 2^-43 (exp2 from a difference, a product and a
-// polynomial carried as pairs of fp32 values; off by some 2^-42 relative, checked against 64 bits),
+// polynomial carried as pairs of fp32 values; off by 1.4 units at most, checked against 64 bits),
 // and sums are 64-bit integers: exact, and the same in any order.
 //
 // A row belongs to a CTA, or, where rows are few, to a cluster of CTAs that hold it in shared memory;

@@ -611,9 +611,10 @@ typedef struct {
  *   w_i = exp((l_i - max l) / T) of the kept tokens, else 0;
  *   token = the first i with w_0 + .. + w_i > u (w_0 + .. + w_(V-1)),
  * u a given random number of [0, 1) (below 0 or NaN counts as 0, 1 and above as the largest below).
- * Weights are carried to 2^-42 relative and summed as integers of 2^-43 of the largest, so the token
- * is that of the definition except where u lies within some 2^-40 of a border, whatever the order of
- * threads; weights below 2^-43 of the largest count as 0. NaN logits count as -inf
+ * Weights are rounded to integers of 2^-43 of the largest (off by less than 2^-42 of it) and summed
+ * exactly, so results do not depend on the order of threads, and the token is that of the definition
+ * except where u or a cut of top-p lies within n 2^-42 of a border, n the tokens that are summed (some
+ * sqrt(n) 2^-43 where their roundings differ); weights below 2^-43 of the largest count as 0. NaN logits count as -inf
  * (masked), +inf as the type's largest finite value; a row without a logit above -inf gives token -1
  * and logprob -inf.
  *   logits [R, V] device, rows ld elements apart (any ld >= V, any alignment of the type).
