@@ -9,8 +9,8 @@
 // the call's phases are cluster barriers instead of launches.
 //
 // Measured: the end, fork, growth and copies of 4 of 16 sequences 19 us (the host's: four calls of 3.5 to 5;
-// 11.5 replayed from a graph), of 128 of 512 sequences 21.5; compaction 14 at 1k pages (9 from a graph) and
-// 13 at 16k, where its copies take another 154, at the HBM's rate.
+// 12 replayed from a graph), of 128 of 512 sequences 21; compaction 12.6 at 1k pages (8.4 from a graph) and
+// 172 at 16k, of which the copies take 154, at the HBM's rate.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -668,10 +668,10 @@ cudaError_t launch_cluster(void (*kernel)(KArgs...), bool wide, cudaStream_t s, 
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
-// us by one CTA and by eight: reserving 2000 pages 3.7, 5.3; 8000: 4.1, 5.4; 12000: 5.5, 5.5; 16000: 5.3, 5.4;
-// 25000: 7.3, 5.3; 65000: 12.3, 5.6; plans of compaction 6.8, 11.6; 8.9, 12.0; 11.0, 12.2; 12.7, 12.3; 17.7, 13.3;
-// 40, 15.5.
-constexpr int kWidePages = 14000;
+// us by one CTA and by eight: reserving 2000 pages 3.4, 4.9; 8000: 3.6, 5.0; 16000: 4.8, 4.9; 25000: 6.7, 4.9; 65000:
+// 11, 5.1; 32 forks 4.7, 6.1; 4.7, 6.1; 5.8, 6.4; 6.9, 6.6; 8.9, 6.6; plans of compaction 6.3, 8.9; 7.1, 9.1; 11, 10;
+// 19, 11; 47, 14 (12000: 10.7, 9.6; from 8192 on a warp's pages are more than its registers hold).
+constexpr int kWidePages = 16384, kWidePlan = 8192;
 constexpr int kWideEntries = 32768;  // of a fork's tables
 
 }  // namespace
@@ -696,7 +696,7 @@ cudaError_t launch_fork(const moe_page_book &K, const int *src, const int *dst, 
 cudaError_t launch_compact(const moe_page_book &K, int *table_out, int *ref_out, int *moves,
                            int *counts, void *ws, cudaStream_t s) {
     const Book k = book(K, ws);
-    const bool wide = K.n_pages > kWidePages;
+    const bool wide = K.n_pages > kWidePlan;
     const long long all = (long long)K.B * K.max_pages;
     // A few entries a thread cost less than a launch.
     const bool here = all <= 8ll * kThr * (wide ? kCluster : 1);
