@@ -1208,10 +1208,15 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const Args a, int held_
                     at = m;
                 }
                 if ((at - m) * ch < kFar) {
-                    float part = 0.f;
+                    const uint64_t less = pack2(-at, -at), by = pack2(ch, ch);
+                    uint64_t part = 0;
 #pragma unroll
-                    for (int i = 0; i < B::kN; ++i) part += exp2_approx((b[q].get(i) - at) * ch);
-                    sum += part;
+                    for (int i = 0; i < B::kN; i += 2) {
+                        const float2 x = unpack2(mul2(add2(pack2(b[q].get(i), b[q].get(i + 1)), less), by));
+                        part = add2(part, pack2(exp2_approx(x.x), exp2_approx(x.y)));
+                    }
+                    const float2 p2 = unpack2(part);
+                    sum += p2.x + p2.y;
                 }
             }
             top = fmaxf(top, m);
