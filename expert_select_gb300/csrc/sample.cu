@@ -25,8 +25,8 @@
 // values until one value is left, and ties are taken in the order of the tokens.
 //
 // Measured for bf16 rows of 151936 with top-k 20 and top-p 0.9: one row 13.3 us (bound by the cluster's
-// barriers), 1040 rows 85 (48 of it the HBM's; two CTAs an SM, and a row's list keeps one warp of its CTA
-// busy for 11); 192 rows of fp32 50257, a third of them without top-k, 70 (bound by the instructions of
+// barriers), 1040 rows 85 (48 of it the HBM's; two CTAs an SM, and a row takes 8 to read and then 9 for its
+// list); 192 rows of fp32 50257, a third of them without top-k, 70 (bound by the instructions of
 // exact weights, and by the slowest rows).
 #include <cooperative_groups.h>
 

@@ -619,7 +619,7 @@ typedef struct {
  * and logprob -inf.
  *   logits [R, V] device, rows ld elements apart (any ld >= V, any alignment of the type).
  *   u [R] device fp32; token [R] device int32; logprob [R] device fp32 or NULL: log of the token's
- *   share of the kept weight. Outputs must not overlap inputs. */
+ *   share of the kept weight, to a few steps of fp32 and n 2^-42. Outputs must not overlap inputs. */
 moe_status moe_sample(const moe_sample_params *P, const void *logits, long long ld, const float *u,
                       int R, int *token, float *logprob, moe_stream_t stream);
 
@@ -673,7 +673,8 @@ moe_status moe_kv_reserve(const moe_page_book *K, int N, const int *n_new, void 
 
 /* Gives back pages of n listed sequences: keep[i] tokens of sequence seqs[i] stay (NULL: none; more
  * than it has: all), and the pages behind them that it holds are released; cache_len becomes at most
- * keep[i]. A sequence may be listed more than once (the smallest keep holds). seqs, keep [n]. */
+ * keep[i]. A sequence may be listed more than once (the smallest keep holds). seqs, keep [n]; keep may
+ * be cache_len itself where entry i is sequence i, and is no other part of the book. */
 moe_status moe_kv_free(const moe_page_book *K, const int *seqs, const int *keep, int n,
                        void *workspace, moe_stream_t stream);
 
