@@ -935,78 +935,188 @@ template <int NT, int D> struct Experts {
     }
 };
 
-// fp32: a warp takes a pair of rows at a time.
-__device__ __forceinline__ void gate_up(const Args &a, const Plan &s, const char *xs) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int stride = token_stride(a.d, 4);
-    for (int p = s.pair0 + warp; p < s.pair1; p += kWarps) {
-        const int ui = (int)((unsigned)p / (unsigned)a.f), j = p - ui * a.f, e = s.expert[ui];
-        const size_t at = ((size_t)s.slot[ui] * a.f + j) * a.d;
-        const float *wg = reinterpret_cast<const float *>(a.wg) + at;
-        const float *wu = reinterpret_cast<const float *>(a.wu) + at;
-        // four tokens at a time (the weights are in L1 after the first)
-        for (unsigned mask = s.tokens[e]; mask;) {
-            int tok[4], n = 0;
-            float ga[4] = {0.f, 0.f, 0.f, 0.f}, ua[4] = {0.f, 0.f, 0.f, 0.f};
+// ---- fp32 steps 2 and 3: rows times tokens in registers, 32 sums a lane ----
+// A weight is read once for up to 4, 8 or 16 tokens, a token once for 8, 4 or 2 rows. Measured: 13 tokens,
+// 7 experts of 1104 x 1088, top-6 76 us (floor 15; a warp and a row for each token 111), 14 tokens, 83
+// experts of 904 x 336, top-8 74 (34; 161), one token, 68 of 1504 x 2608, top-4 52 (28; 56). Bound by the
+// loads' latency: 16 warps with 8 loads each on their way. Asking L2 for the next rows ahead: 82 to 100.
+// A lane's 32 sums are summed over the warp and shared out: lane i gets the i-th (31 shuffles).
+__device__ __forceinline__ float sum_out(float (&v)[32]) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                tok[i] = mask ? __ffs(mask) - 1 : 0;
-                n += mask != 0;
-                mask &= mask - 1;
-            }
-#pragma unroll 4
-            for (int c = lane * 4; c < a.d; c += 128) {
-                const float4 gv = __ldg(reinterpret_cast<const float4 *>(wg + c));
-                const float4 uv = __ldg(reinterpret_cast<const float4 *>(wu + c));
+    for (int o = 16; o >= 1; o >>= 1)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (i < n) {
-                        const float4 x = *reinterpret_cast<const float4 *>(xs + tok[i] * stride + 4 * c);
-                        ga[i] += gv.x * x.x + gv.y * x.y + gv.z * x.z + gv.w * x.w;
-                        ua[i] += uv.x * x.x + uv.y * x.y + uv.z * x.z + uv.w * x.w;
-                    }
+        for (int i = 0; i < o; ++i) {
+            const float keep = lane & o ? v[i + o] : v[i], give = lane & o ? v[i] : v[i + o];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+        }
+    return v[0];
+}
+__device__ __forceinline__ void add_product(float &s, const float4 &a, const float4 &b) {
+    s = fmaf(a.x, b.x, s);
+    s = fmaf(a.y, b.y, s);
+    s = fmaf(a.z, b.z, s);
+    s = fmaf(a.w, b.w, s);
+}
+
+// P pairs of rows (np of them are there) times T tokens at a time.
+template <int P, int T>
+__device__ __forceinline__ void gate_up_pairs(const Args &a, const Plan &s, const char *xs, int ui, int j0,
+                                              int np) {
+    static_assert(P * T == 16, "32 sums, gate's in the lower half of the warp");
+    const int lane = threadIdx.x & 31, e = s.expert[ui], stride = token_stride(a.d, 4);
+    const size_t at = ((size_t)s.slot[ui] * a.f + j0) * a.d;
+    const float *wg = reinterpret_cast<const float *>(a.wg) + at;
+    const float *wu = reinterpret_cast<const float *>(a.wu) + at;
+    for (unsigned mask = s.tokens[e]; mask;) {
+        const unsigned group = mask;
+        const int n = min(T, __popc(mask));
+        int x[T];
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+            x[t] = mask ? (__ffs(mask) - 1) * stride : 0;
+            mask &= mask - 1;
+        }
+        float v[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = 0.f;
+        // (8 loads of weights on their way)
+        constexpr int U = 4 / P;
+#pragma unroll 1
+        for (int c = lane * 4; c < a.d; c += 128 * U) {
+            float4 w[U][2 * P];
+#pragma unroll
+            for (int k = 0; k < U; ++k)
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    const size_t row = (size_t)(i < np ? i : 0) * a.d + (c + 128 * k < a.d ? c + 128 * k : c);
+                    w[k][i] = __ldg(reinterpret_cast<const float4 *>(wg + row));
+                    w[k][P + i] = __ldg(reinterpret_cast<const float4 *>(wu + row));
+                }
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                if (c + 128 * k >= a.d) break;
+#pragma unroll
+                for (int t = 0; t < T; ++t) {
+                    if (t >= n) break;
+                    const float4 q = *reinterpret_cast<const float4 *>(xs + x[t] + 4 * (c + 128 * k));
+#pragma unroll
+                    for (int i = 0; i < 2 * P; ++i) add_product(v[i * T + t], w[k][i], q);
                 }
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (i >= n) continue;
-#pragma unroll
-                for (int o = 16; o >= 1; o >>= 1) {
-                    ga[i] += __shfl_xor_sync(0xffffffffu, ga[i], o);
-                    ua[i] += __shfl_xor_sync(0xffffffffu, ua[i], o);
-                }
-                const int place = s.place[e][tok[i]];
-                if (lane == 0)
-                    store_h(a, (float *)nullptr, tok[i] * a.k + place, j,
-                            silu(ga[i]) * ua[i] * s.gate[tok[i]][place]);
-            }
+        }
+        const float g = sum_out(v), u = __shfl_down_sync(0xffffffffu, g, 16);
+        const int i = lane / T, t = lane % T;
+        if (i < np && t < n) {
+            const int r = nth_token(group, t), place = s.place[e][r];
+            store_h(a, (float *)nullptr, r * a.k + place, j0 + i, silu(g) * u * s.gate[r][place]);
         }
     }
 }
 
-// fp32: a warp takes a column and a token at a time (the weights are in L1 after the first).
-__device__ __forceinline__ void down(const Args &a, const Plan &s) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int c0 = s.col0, c1 = s.col1;
-    const float *h = reinterpret_cast<const float *>(a.h);
-    for (int i = warp; i < (c1 - c0) * a.R; i += kWarps) {
-        const int col = c0 + i / a.R, r = i % a.R;
-        float v = 0.f;
-        for (int ui = 0; ui < s.n; ++ui) {
-            const int e = s.expert[ui];
-            if (!(s.tokens[e] >> r & 1)) continue;
-            const float *w = reinterpret_cast<const float *>(a.wd) + ((size_t)s.slot[ui] * a.d + col) * a.f;
-            const float *p = h + (size_t)(r * a.k + s.place[e][r]) * a.f;
-#pragma unroll 4
-            for (int c = lane * 4; c < a.f; c += 128) {
-                const float4 wv = __ldg(reinterpret_cast<const float4 *>(w + c));
-                const float4 hv = __ldcg(reinterpret_cast<const float4 *>(p + c));
-                v += wv.x * hv.x + wv.y * hv.y + wv.z * hv.z + wv.w * hv.w;
+// The warps take groups of up to 4 pairs of an expert in turn: weights are read once for 4 tokens, and
+// tokens once for 8 rows. More tokens take fewer rows, and so do short shares.
+__device__ __forceinline__ void gate_up(const Args &a, const Plan &s, const char *xs) {
+    const int warp = threadIdx.x >> 5, p1 = s.pair1;
+    const int each = (p1 - s.pair0 + kWarps - 1) / kWarps;  // pairs a warp
+    int turn = 0;
+#pragma unroll 1
+    for (int p = s.pair0; p < p1;) {
+        const int ui = (int)((unsigned)p / (unsigned)a.f), end = min(p1, (ui + 1) * a.f);
+        const int m = __popc((unsigned)s.tokens[s.expert[ui]]);
+        const int size = each == 1 ? 1 : m <= 4 && each > 2 ? 4 : 2;
+        const int n = (end - p + size - 1) / size;
+#pragma unroll 1
+        for (int g = (warp - turn) & (kWarps - 1); g < n; g += kWarps) {
+            const int at = p + g * size, j0 = at - ui * a.f, np = min(size, end - at);
+            if (size == 4)
+                gate_up_pairs<4, 4>(a, s, xs, ui, j0, np);
+            else if (size == 2)
+                gate_up_pairs<2, 8>(a, s, xs, ui, j0, np);
+            else
+                gate_up_pairs<1, 16>(a, s, xs, ui, j0, np);
+        }
+        turn += n;
+        p = end;
+    }
+}
+
+// C columns times T tokens: the warps share the inner dimension over all chosen experts, in chunks of 128.
+template <int C, int T>
+__device__ __forceinline__ void down_columns(const Args &a, const Plan &s, int c0, int nc, int ui, int k0,
+                                             int k1, float *mine) {
+    static_assert(C * T == 32, "32 sums");
+    const int lane = threadIdx.x & 31, e = s.expert[ui];
+    const float *w0 = reinterpret_cast<const float *>(a.wd) + ((size_t)s.slot[ui] * a.d + c0) * a.f;
+    for (unsigned mask = s.tokens[e]; mask;) {
+        const unsigned group = mask;
+        const int n = min(T, __popc(mask));
+        int row[T];
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+            const int r = mask ? __ffs(mask) - 1 : __ffs(group) - 1;
+            row[t] = (r * a.k + s.place[e][r]) * a.f;
+            mask &= mask - 1;
+        }
+        float v[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = 0.f;
+#pragma unroll 1
+        for (int c = k0 * 128 + lane * 4; c < min(a.f, k1 * 128); c += 128) {
+            // (all loads before the first branch, as it would part them: places without a token read the
+            // first one's activations)
+            float4 w[C], q[T];
+#pragma unroll
+            for (int i = 0; i < C; ++i)
+                w[i] = __ldg(reinterpret_cast<const float4 *>(w0 + (size_t)(i < nc ? i : 0) * a.f + c));
+#pragma unroll
+            for (int t = 0; t < T; ++t)
+                q[t] = __ldcg(reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(a.h) + row[t] + c));
+#pragma unroll
+            for (int t = 0; t < T; ++t) {
+                if (t >= n) break;
+#pragma unroll
+                for (int i = 0; i < C; ++i) add_product(v[i * T + t], w[i], q[t]);
             }
         }
+        const float sum = sum_out(v);
+        const int i = lane / T, t = lane % T;
+        if (i < nc && t < n) mine[i * a.R + nth_token(group, t)] += sum;
+        __syncwarp();
+    }
+}
+
+__device__ __forceinline__ void down(const Args &a, const Plan &s, float *red) {
+    constexpr int kCols = 8;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int nk = (a.f + 127) / 128, q0 = part(s.n * nk, warp), q1 = part(s.n * nk, warp + 1);
+    float *mine = red + warp * kCols * a.R;
+#pragma unroll 1
+    for (int c0 = s.col0; c0 < s.col1; c0 += kCols) {
+        const int nc = min(kCols, s.col1 - c0);
+        for (int i = lane; i < kCols * a.R; i += 32) mine[i] = 0.f;
+        __syncwarp();
+#pragma unroll 1
+        for (int q = q0; q < q1;) {
+            const int ui = q / nk, last = min(q1, (ui + 1) * nk), k0 = q - ui * nk, k1 = last - ui * nk;
+            if (__popc((unsigned)s.tokens[s.expert[ui]]) <= 4) {
+                down_columns<8, 4>(a, s, c0, nc, ui, k0, k1, mine);
+            } else {
+#pragma unroll 1
+                for (int h = 0; h < nc; h += 4)
+                    down_columns<4, 8>(a, s, c0 + h, min(4, nc - h), ui, k0, k1, mine + h * a.R);
+            }
+            q = last;
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < nc * a.R; i += kThr) {
+            const int col = i / a.R, r = i - col * a.R;
+            float v = 0.f;
 #pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (lane == 0) store_y<float>(a, r, col, v);
+            for (int w = 0; w < kWarps; ++w) v += red[(w * kCols + col) * a.R + r];
+            store_y<float>(a, r, c0 + col, v);
+        }
+        __syncthreads();  // (the sums are read before the next columns')
     }
 }
 
@@ -1052,7 +1162,7 @@ __global__ void __launch_bounds__(kThr, 1) few_kernel(const Args a) {
     } else {
         gate_up(a, s, xs);
         if (!grid_barrier(a, s, launch)) return;
-        down(a, s);
+        down(a, s, red);
     }
 }
 
