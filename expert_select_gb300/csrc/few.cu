@@ -20,7 +20,7 @@
 // Measured, calls in a row with other weights each: one token of the Qwen3-shaped layer 26.6 us (6 until
 // the first weights are asked for, 3 between the last of step 2 and the first of step 3), 16 tokens
 // 148 (0.77 of the HBM's measured rate; CTAs end step 2 over 13 us), 4 tokens of d = f = 2880, 32
-// experts, top-4 124 (0.78), 3 tokens of an fp32 layer of d 520 13.2.
+// experts, top-4 124 (0.78), 3 tokens of an fp32 layer of d 520 14.5.
 #include <algorithm>
 
 #include "few.cuh"
