@@ -33,6 +33,7 @@
 #include <cfloat>
 
 #include "sample.cuh"
+#include "sample_keys.cuh"
 
 namespace moe {
 namespace sample {
@@ -42,7 +43,7 @@ namespace cg = cooperative_groups;
 using u64 = unsigned long long;
 
 constexpr int kThr = 512, kWarps = kThr / 32;
-constexpr int kBins = 1024, kPer = kBins / kThr;
+constexpr int kBins = kRangeBins, kPer = kBins / kThr;
 constexpr int kMaxCluster = 8;
 constexpr float kLive = 43.f;                   // octaves below the largest
 constexpr float kBinScale = (kBins - 1) / kLive;
@@ -129,15 +130,6 @@ __device__ __forceinline__ float exp2_approx(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
-}
-
-// Values in the order of their keys (NaN and -0 do not occur).
-__device__ __forceinline__ uint32_t key_of(float l) {
-    const uint32_t b = __float_as_uint(l);
-    return b ^ ((int)b < 0 ? 0xffffffffu : 0x80000000u);
-}
-__device__ __forceinline__ float value_of(uint32_t key) {
-    return __uint_as_float(key ^ ((int)key < 0 ? 0x80000000u : 0xffffffffu));
 }
 
 template <typename T> __device__ __forceinline__ T from_value(float v);
@@ -603,11 +595,6 @@ __device__ __noinline__ bool find_bin(Shared &sh, u64 target) {
     return target <= sh.scanned;
 }
 
-// The largest key of a bf16 value up to this one.
-__device__ __forceinline__ uint32_t bf16_key(uint32_t key) {
-    return key >= 0x80000000u ? key & 0xffff0000u : ((key + 1) & 0xffff0000u) - 1;
-}
-
 // The least key whose value is live and in bin b or one before it: bins descend with the value, so 32
 // lanes divide what is left by 33 at a time.
 __device__ __noinline__ uint32_t bin_edge(const Scale &sc, int b) {
@@ -688,26 +675,20 @@ template <typename T, bool W> __device__ __noinline__ bool search(Shared &sh, do
         if ((threadIdx.x & 31) == 0) sh.edges[threadIdx.x / 32] = edge;
     }
     __syncthreads();
-    uint32_t kmin = max(sh.edges[0], cut.key + 1), kmax = sh.edges[1];
-    if (kStep) kmax = bf16_key(kmax);
-    while (kmin < kmax) {
-        const int shift = max(kStep, 32 - __clz(kmax - kmin) - 10);
+    KeyRange<kStep> keys(max(sh.edges[0], cut.key + 1), sh.edges[1]);
+    for (bool more = keys.open(); more;) {
+        const int shift = keys.shift();
         clear_bins(sh);
-        pass<T, W ? kWeightKeys : kCountKeys>(sh, kmin, kmax, shift);
+        pass<T, W ? kWeightKeys : kCountKeys>(sh, keys.min, keys.max, shift);
         share_bins(sh);
         find_bin(sh, target);
         target -= sh.before;
-        kmax -= (uint32_t)sh.bin << shift;
-        if (shift <= kStep) break;
-        const uint32_t width = (1u << shift) - 1;
-        if (kmax - kmin > width) kmin = kmax - width;
-        if (kStep) kmax = bf16_key(kmax);
+        more = keys.narrow(sh.bin, shift);
     }
-    if (kStep) kmax = bf16_key(kmax);
     // ties that are needed to reach the target
-    const u64 one = W ? weigh(sh, value_of(kmax)) : 1;
+    const u64 one = W ? weigh(sh, value_of(keys.max)) : 1;
     __syncthreads();
-    if (threadIdx.x == 0) sh.cut = Cut{kmax, one ? (uint32_t)((target + one - 1) / one) : 1u};
+    if (threadIdx.x == 0) sh.cut = Cut{keys.max, one ? (uint32_t)((target + one - 1) / one) : 1u};
     __syncthreads();
     return true;
 }

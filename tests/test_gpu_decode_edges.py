@@ -1,0 +1,60 @@
+"""GPU tests of the decoding calls at values, sizes and paths where they can go wrong, against the same plain
+64-bit computations as test_gpu_decode.py (its tolerances hold here too)."""
+import pytest
+import torch
+
+from expert_select_gb300 import moetree as M
+from test_gpu_decode import sample_check
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    from expert_select_gb300 import build
+    build.build()
+    M.lib()
+
+
+# --------------------------------------------------------------------- sampling
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V", [600, 4099, 70001])
+def test_sample_min_p_at_zero(V, dt):
+    """min-p's least value is 0.0 itself, in lists and where more is kept than a list holds."""
+    g = torch.Generator().manual_seed(V)
+    r = torch.rand(V, generator=g)
+    n = torch.randn(V, generator=g)
+    rows = [torch.zeros(V), torch.where(r < 0.5, 0.0, -0.0), torch.where(r < 0.9, 0.0, -n.abs()),
+            torch.where(r < 0.9, -n.abs(), 0.0), torch.where(r < 0.95, 0.0, -1e-38),
+            torch.where(torch.arange(V) == V // 3, 0.0, -n.abs() - 0.1)]
+    x = torch.stack(rows).to(dt)
+    for kw in (dict(m=1.0), dict(m=2.0), dict(m=1.0, k=300), dict(m=1.0, p=0.6), dict(m=1.0, k=550, p=0.7),
+               dict(m=1.0, T=0.3), dict(m=0.999, p=0.8)):
+        for u in (torch.rand(len(rows), generator=g), torch.zeros(len(rows))):
+            sample_check(x, u, **kw)
+
+
+@pytest.mark.parametrize("V", [700, 4099, 70001])
+def test_sample_between_zero_and_the_smallest_values(V):
+    """Zeros of both signs among denormals, cuts among them: keys beside zero's."""
+    g = torch.Generator().manual_seed(V)
+    tiny = lambda most: torch.randint(1, most, (V,), generator=g).int().view(torch.float32)  # noqa: E731
+    r = torch.rand(V, generator=g)
+    zero = torch.where(torch.rand(V, generator=g) < 0.5, 0.0, -0.0)
+    rows = []
+    for most in (8, 4096, 0x400000):
+        rows += [torch.where(r < 0.3, zero, -tiny(most)), torch.where(r < 0.3, zero, tiny(most)),
+                 torch.where(r < 0.2, zero, torch.where(r < 0.6, tiny(most), -tiny(most)))]
+    # the largest 2^n - 1 steps above zero
+    for n in (1, 3, 10, 13, 20):
+        row = torch.where(r < 0.3, zero, -tiny(0x400000))
+        row[V // 2] = torch.tensor((1 << n) - 1, dtype=torch.int32).view(torch.float32)
+        rows.append(row)
+    x = torch.stack(rows)
+    for kw in (dict(k=V // 4 + 300), dict(k=V * 3 // 5 + 200), dict(k=V - 2), dict(p=0.55), dict(p=0.9),
+               dict(p=0.7, k=V * 4 // 5), dict(T=1e-30, p=0.6), dict(T=1e-30, k=V * 2 // 3 + 90)):
+        sample_check(x, torch.rand(len(rows), generator=g), **kw)
