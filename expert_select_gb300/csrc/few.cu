@@ -227,7 +227,9 @@ __device__ __forceinline__ void norm_scales(const Args &a, Plan &s, const char *
         const float y = rsqrtf(m.hi), q = __fmul_rn(y, y), qe = fmaf(y, y, -q);
         const float p = __fmul_rn(m.hi, q), pe = fmaf(m.hi, q, -p) + fmaf(m.hi, qe, m.lo * q);
         const float e = (1.f - p) - pe;
-        s.scale[threadIdx.x] = Pair{y, y * e * fmaf(0.375f, e, 0.5f)};
+        // (the pair's first is the scale rounded to fp32)
+        const float more = y * e * fmaf(0.375f, e, 0.5f), hi = y + more;
+        s.scale[threadIdx.x] = Pair{hi, more - (hi - y)};
     }
     __syncthreads();
     if (r < a.R && w == 0 && s.wide[r]) {
@@ -250,15 +252,19 @@ __device__ __forceinline__ void norm_scales(const Args &a, Plan &s, const char *
 __device__ __noinline__ uint32_t scaled_wide(float v, double sc) {
     return __bfloat16_as_ushort(__double2bfloat16((double)v * sc));
 }
-// The same for an fp32 product that lies in the middle of two bf16 values: its rest, at most half a
-// step of fp32's, decides; elsewhere the product's own rounding is the answer.
+// An fp32 product with the scale's first part is off by a step and a half at most: half a step for its own
+// rounding, and v times the second part, which is half a step of the first's or less. So where it lies two
+// steps or more from the middle of two bf16 values its rounding is the answer.
+__device__ __forceinline__ bool near_middle(float p) { return ((__float_as_uint(p) + 0x8001u) & 0xffffu) <= 2u; }
+// Elsewhere what the product lacks decides (good to 2^-45 of the product, as the scale is).
 __device__ __noinline__ uint32_t scaled_middle(float v, Pair sc) {
     const float p = v * sc.hi;
     if (!(fabsf(p) > 1e-25f)) return scaled_wide(v, (double)sc.hi + (double)sc.lo);
     const uint32_t b = __float_as_uint(p);
-    const float rest = fmaf(v, sc.hi, -p) + v * sc.lo;
-    if (rest == 0.f) return (b + 0x7fffu + (b >> 16 & 1u)) >> 16;
-    return (b >> 16) + ((rest > 0.f) == (p > 0.f) ? 1u : 0u);
+    const float past = p - __uint_as_float((b & 0xffff0000u) | 0x8000u);  // exact
+    const float t = past + (fmaf(v, sc.hi, -p) + v * sc.lo);
+    if (t == 0.f) return (b >> 16) + (b >> 16 & 1u);
+    return (b >> 16) + ((t > 0.f) == (p > 0.f) ? 1u : 0u);
 }
 __device__ __forceinline__ void scale16(uint4 *p, Pair sc, const double *wide) {
     const uint4 w = *p;
@@ -270,7 +276,7 @@ __device__ __forceinline__ void scale16(uint4 *p, Pair sc, const double *wide) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const float2 x = unpack2(mul2(pack2(v[2 * j], v[2 * j + 1]), by));
-        middle |= (__float_as_uint(x.x) & 0xffffu) == 0x8000u || (__float_as_uint(x.y) & 0xffffu) == 0x8000u;
+        middle |= near_middle(x.x) || near_middle(x.y);
         const __nv_bfloat162 b = __floats2bfloat162_rn(x.x, x.y);
         q[j] = reinterpret_cast<const uint32_t &>(b);
     }
@@ -280,7 +286,7 @@ __device__ __forceinline__ void scale16(uint4 *p, Pair sc, const double *wide) {
             uint32_t one = j & 1 ? q[j / 2] >> 16 : q[j / 2] & 0xffffu;
             if (wide)
                 one = scaled_wide(v[j], *wide);
-            else if ((__float_as_uint(v[j] * sc.hi) & 0xffffu) == 0x8000u)
+            else if (near_middle(v[j] * sc.hi))
                 one = scaled_middle(v[j], sc);
             q[j / 2] = j & 1 ? (q[j / 2] & 0xffffu) | one << 16 : (q[j / 2] & 0xffff0000u) | one;
         }

@@ -58,3 +58,51 @@ def test_sample_between_zero_and_the_smallest_values(V):
     for kw in (dict(k=V // 4 + 300), dict(k=V * 3 // 5 + 200), dict(k=V - 2), dict(p=0.55), dict(p=0.9),
                dict(p=0.7, k=V * 4 // 5), dict(T=1e-30, p=0.6), dict(T=1e-30, k=V * 2 // 3 + 90)):
         sample_check(x, torch.rand(len(rows), generator=g), **kw)
+
+
+# --------------------------------------------------------------------- a few tokens
+
+def _few(d, E, k, f, R, dt, wr, wg, wu, wd):
+    up = lambda t: t.to(dt).to(DEV).contiguous()  # noqa: E731
+    L = M.layer_desc(d, E, k, f, dt)
+    return L, [up(t) for t in (wr, wg, wu, wd)], M.few_workspace(L, R)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_few_norm_rounds_each_element_once(dt):
+    """The router is the identity, so the logits are the normed elements: each is the 64-bit one rounded once.
+    Rows are those of many that have elements beside the middle of two values of the type. (The scale is good
+    to 2^-45, so an element within 2^-44 of a middle may go either way.)"""
+    d, R = 256, 16
+    g = torch.Generator().manual_seed(12)
+    x = (torch.randn(60000, d, generator=g) * (0.1 + 10 * torch.rand(60000, 1, generator=g))).to(dt)
+    step = 2.0 ** (-8 if dt == torch.bfloat16 else -24)
+
+    def normed(x):
+        t = x.double()
+        return t / torch.sqrt((t * t).mean(1, keepdim=True) + 1e-6)
+
+    def off_middle(y):  # relative distance from the nearest middle
+        m, e = torch.frexp(y)
+        q = m.abs() / step  # in steps of the type, in [1 / 2, 1) / step
+        return (q - torch.floor(q) - 0.5).abs() * step
+
+    def rounded(y):  # (torch's conversion to bf16 rounds to fp32 first)
+        m, e = torch.frexp(y)
+        return torch.ldexp(torch.round(m / step) * step, e)
+    near = (off_middle(normed(x)) < 2.0 ** (-22 if dt == torch.bfloat16 else -38)).any(1)
+    x = x[near][:960]
+    assert len(x) >= 320
+    x = x[:len(x) // R * R]
+    zero = torch.zeros(d, 8, d)
+    L, w, ws = _few(d, d, 1, 8, R, dt, torch.eye(d), zero, zero, zero.transpose(1, 2))
+    y, logits = torch.empty(R, d, dtype=dt, device=DEV), torch.empty(len(x), d, device=DEV)
+    for r in range(0, len(x), R):
+        M.moe_few_forward(L, x[r:r + R].to(DEV), *w, None, y, ws, logits=logits[r:r + R],
+                          opts=M.run_opts(norm_input=True))
+    want = normed(x)
+    got = logits.cpu()
+    bad = (got.double() != rounded(want)) & (off_middle(want) > 2.0 ** -44)
+    assert not bad.any(), (int(bad.sum()), int(bad.any(1).sum()), len(x))
+    # where it may go either way, one of the two
+    assert ((got.double() - want).abs() <= (step / 2 + 2.0 ** -44) * 2 * want.abs()).all()
