@@ -18,7 +18,7 @@
 // ones, of which there are few as a rule: a bound from below on the last of them (for top-k, the k-th
 // largest of the threads' own largest values, up to a bin; for min-p its own) lets a second pass collect
 // them, and one CTA sorts them and does the rest. top-p needs the whole weight too; a sum of fp32
-// exponentials, off by at most 2^-16, decides unless a cut lies within that.
+// exponentials, off by at most 2^-15, decides unless a cut lies within that.
 // Where more is kept than a list holds (flat distributions, no cuts), cuts are found by histograms of
 // the row's live values (weights that are not below 2^-43) over bins that descend with the value:
 // counts for top-k, weights for top-p; the bin that a cut falls in is divided by the bits of the
@@ -220,7 +220,14 @@ template <> struct Block<__nv_bfloat16> {
 constexpr int kList = kThr;             // tokens of a list, a thread for each
 constexpr int kAsk = kList / 2;        // of them asked for (the last bin may hold more)
 constexpr float kFar = 36.f;           // octaves from which values do not count in the fp32 sum
-constexpr float kSumError = 0x1p-16f;
+// The fp32 sum's relative error, whichever pass forms it. A term meets at most 282 additions (256 blocks of a
+// thread that has 2^19 values alone with its CTA, a block's values, 24 of threads, warps and CTAs), 2^-24 each:
+// 1.7 10^-5. Blocks of kFar octaves and more are left out: kMaxV 2^-36, 7.6 10^-6. Octaves have three roundings,
+// and their mean over the weights is below 15 (V values x octaves down beside the largest: x V 2^-x / (1 + V 2^-x)):
+// 1.9 10^-6, exp2 2.4 10^-7. 2.7 10^-5 < 2^-15. The sum made while a row is read has 106 additions at most (76 KB
+// of blocks' largest values), but scales its terms three times more (what is scaled more often is too little), over
+// 16 octaves more: 6.5 + 7.6 + 3.8 + 1 = 18.9 10^-6.
+constexpr float kSumError = 0x1p-15f;
 
 // A row, its settings, and where its results go.
 struct Task {
@@ -1169,10 +1176,7 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const Args a, int held_
                   ? reinterpret_cast<T *>(dyn + (size_t)held_blocks * 16) - t.b0 : nullptr;
     // Beside it, where top-p is of the row's weight, the fp32 sum of the weights relative to a value that
     // the thread has seen; a larger one takes its place from 8 octaves on, so that what was added up
-    // before hardly counts when it has been scaled down twice.
-    // Its error, relative: 2.5 roundings of up to 17 octaves (what lies further down is too little), twice with
-    // the last scaling, 4 10^-6; exp2's 2^-22 three times; a thread's up to 82 additions, 4.9 10^-6, and 24 of
-    // threads, warps and CTAs, 1.4 10^-6: 1.1 10^-5 < 2^-16.
+    // before hardly counts when it has been scaled down twice (its error: kSumError).
     const bool whole = tops && t.top_p < 1.f && !t.k && t.temp > 0.f;
     const float ch = sh.sc.ch;
     float top = -INFINITY, at = -INFINITY, sum = 0.f;

@@ -106,3 +106,38 @@ def test_few_norm_rounds_each_element_once(dt):
     assert not bad.any(), (int(bad.sum()), int(bad.any(1).sum()), len(x))
     # where it may go either way, one of the two
     assert ((got.double() - want).abs() <= (step / 2 + 2.0 ** -44) * 2 * want.abs()).all()
+
+
+# --------------------------------------------------------------------- rows too long for shared memory
+
+def _many(row, R, u, **kw):
+    """Tokens of R equal rows, row r at u[r]."""
+    V = row.numel()
+    x = row.to(DEV).expand(R, V).contiguous()
+    token = torch.full((R,), -9, dtype=torch.int32, device=DEV)
+    put = lambda n, dt: torch.full((R,), kw[n], dtype=dt, device=DEV) if n in kw else None  # noqa: E731
+    M.moe_sample(x, u.to(DEV), token, temperature=put("T", torch.float32), top_k=put("k", torch.int32),
+                 top_p=put("p", torch.float32))
+    return token.cpu()
+
+
+def test_sample_border_beside_a_sum_that_rounds_away():
+    """Rows of one CTA each, summed block after block: 512 threads begin with a weight of 1 and three of 2^-24,
+    and what follows, 2^-24 a block, is lost in fp32 (each a tie that goes to even), 258 2^-24 in all. top-p's
+    limit is put so that the 257th of the equal tokens is kept only if the weight is known better than to that."""
+    V, threads, blocks = 1 << 19, 512, 256
+    octaves = torch.full((16, blocks, 32, 4), 26.0)  # by warp, turn, lane: a block of four
+    octaves[:, 0, :, 1:] = 24.0
+    octaves[:, 0, :, 0] = 0.0
+    row = -octaves.reshape(V)
+    T = torch.tensor(1.4426950408889634).item()  # an octave is a step of one in the logits
+    heavy = torch.nonzero(row == 0).flatten()
+    assert len(heavy) == threads
+    z = threads * (1 + 258 * 2.0 ** -24)
+    # the border of the 257th token (256 before it) lies between p z and p times what is left of z with an error of 2^-16
+    p = torch.tensor(256 / z * (1 + 0.9 * 2.0 ** -24)).item()
+    assert p * z > 256 * (1 + 2.0 ** -26) and p * threads * (1 + 2.0 ** -16) < 256 * (1 - 2.0 ** -26)
+    R = 240
+    u = (torch.arange(R) + 0.5) / R
+    got = _many(row, R, u, T=T, p=p)
+    assert torch.equal(got.long(), heavy[(u.double() * 257).long()])
