@@ -41,11 +41,11 @@ namespace {
 
 constexpr int kThr = 512, kWarps = kThr / 32;
 // One buffer of the warps' partial sums: 16 rows of a token of every warp take 1 KB.
-__host__ __device__ inline int red_bytes(int R) { return R <= 8 ? 8 * 1024 : 16 * 1024; }
+__host__ __device__ constexpr int red_bytes(int R) { return R <= 8 ? 8 * 1024 : 16 * 1024; }
 
 // Bytes between two tokens in shared memory: 64 bytes past whole lines, so that the 16-byte reads of
 // two tokens' quarters of a line do not meet in a bank.
-__host__ __device__ inline int token_stride(int d, int elem) { return (d * elem + 127) / 128 * 128 + 64; }
+__host__ __device__ constexpr int token_stride(int d, int elem) { return (d * elem + 127) / 128 * 128 + 64; }
 
 struct Plan {
     int n;                            // experts that some token chose
@@ -1128,10 +1128,10 @@ __device__ __forceinline__ void down(const Args &a, const Plan &s, float *red) {
 
 constexpr int kPlanBytes = (sizeof(Plan) + 127) / 128 * 128;
 constexpr int kSmem = 227 * 1024;
-inline __host__ __device__ int fixed_bytes(int R) { return kPlanBytes + 2 * red_bytes(R); }
+constexpr __host__ __device__ int fixed_bytes(int R) { return kPlanBytes + 2 * red_bytes(R); }
 __host__ __device__ constexpr int ring_bytes(int D) { return D * kWarps * 1024; }
 // Shared memory of a launch; step 3's activations take the tokens' place.
-inline int smem_bytes(int R, int d, int elem, int D) {
+constexpr int smem_bytes(int R, int d, int elem, int D) {
     return fixed_bytes(R) + ring_bytes(D) + std::max(D * kWarps * std::min(R, 8) * 128, R * token_stride(d, elem));
 }
 
@@ -1192,8 +1192,11 @@ template <typename T, int NT, int D> cudaError_t launch(const Args &a, int max_c
     return cudaLaunchKernelEx(&cfg, few_kernel<T, NT, D>, a);
 }
 
-// Rings as deep as shared memory holds: at one token 10 entries a warp (of the 12 that it has of step 3 in
-// the Qwen3-shaped layer, 9 are on their way before the grid's barrier), with 16 tokens 5.
+// Rings as deep as shared memory holds: at one or two tokens 10 entries a warp (of the 12 that it has of step 3
+// in the Qwen3-shaped layer, 9 are on their way before the grid's barrier), up to 6 tokens 7, with more 5, and 4 from 9
+// long tokens on (16 of more than 3392 elements).
+static_assert(smem_bytes(2, kMaxD, 2, 10) <= kSmem && smem_bytes(6, kMaxD, 2, 7) <= kSmem &&
+              smem_bytes(8, kMaxD, 2, 5) <= kSmem && smem_bytes(9, kMaxD, 2, 4) <= kSmem);
 template <int NT, int D> cudaError_t launch_ring(const Args &a, int max_ctas, cudaStream_t s) {
     return launch<__nv_bfloat16, NT, D>(a, max_ctas, s);
 }
@@ -1213,9 +1216,9 @@ cudaError_t launch_few(const Args &a, int dtype, int max_ctas, cudaStream_t s) {
     if (dtype == MOE_DTYPE_F32) return launch<float, 1, 0>(a, max_ctas, s);
     auto fits = [&](int D) { return smem_bytes(a.R, a.d, 2, D) <= kSmem; };
     if (a.R <= 8)
-        return fits(10) ? launch_ring<1, 10>(a, max_ctas, s)
+        return fits(10)  ? launch_ring<1, 10>(a, max_ctas, s)
                : fits(7) ? launch_ring<1, 7>(a, max_ctas, s)
-                         : fits(5) ? launch_ring<1, 5>(a, max_ctas, s) : launch_ring<1, 4>(a, max_ctas, s);
+                         : launch_ring<1, 5>(a, max_ctas, s);
     return fits(5) ? launch_ring<2, 5>(a, max_ctas, s) : launch_ring<2, 4>(a, max_ctas, s);
 }
 
