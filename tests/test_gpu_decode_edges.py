@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from expert_select_gb300 import moetree as M
-from test_gpu_decode import sample_check
+from test_gpu_decode import Few, peaked, sample_check
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -108,6 +108,37 @@ def test_few_norm_rounds_each_element_once(dt):
     assert ((got.double() - want).abs() <= (step / 2 + 2.0 ** -44) * 2 * want.abs()).all()
 
 
+@pytest.mark.parametrize("R,d,E,k,f", [(16, 136, 3, 3, 72), (13, 520, 7, 7, 264), (9, 64, 2, 2, 24), (16, 8, 1, 1, 8),
+                                       (12, 328, 5, 4, 1000), (10, 2048, 4, 4, 16)])
+@pytest.mark.parametrize("ctas", [0, 3])
+def test_few_fp32_experts_of_many_tokens(R, d, E, k, f, ctas):
+    """9 to 16 tokens of an expert: more than a lane's sums take at a time, in both halves of the call."""
+    t = Few(R + d, R, d, E, k, f, torch.float32).upload().run(True, True, max_ctas=ctas)
+    counts = torch.bincount(t.idx.cpu().flatten().long(), minlength=E)
+    assert counts.max() >= 9
+    t.check(True, True)
+
+
+@pytest.mark.parametrize("depth,R,d", [(10, 1, 512), (10, 2, 6144), (7, 3, 512), (7, 6, 6144), (5, 7, 512), (5, 8, 6144),
+                                       (5, 16, 512), (5, 16, 3392), (4, 16, 3400), (5, 9, 6016), (4, 9, 6024)])
+@pytest.mark.parametrize("f", [8, 264])
+def test_few_rings_of_every_depth(depth, R, d, f):
+    """bf16 layers on both sides of the sizes at which a warp's ring gets fewer entries: parts of a row that are
+    shorter than the ring, and longer ones."""
+    Few(R + d, R, d, 4, 2, f, torch.bfloat16).upload().run().check()
+
+
+@pytest.mark.parametrize("dt,R,d", [(torch.bfloat16, 16, 3912), (torch.bfloat16, 13, 4808), (torch.float32, 16, 2984),
+                                    (torch.float32, 9, 5320)])
+def test_few_tokens_of_several_launches(dt, R, d):
+    """One token more than fit a CTA's shared memory together."""
+    t = Few(R + d, R, d, 4, 2, 16, dt).upload().run(True, True)
+    t.check(True, True)
+    x = t.dev[0].clone()
+    t.dev[0] = x
+    t.run(True, True, y=x).check(True, True, y=x)
+
+
 # --------------------------------------------------------------------- rows too long for shared memory
 
 def _many(row, R, u, **kw):
@@ -141,3 +172,19 @@ def test_sample_border_beside_a_sum_that_rounds_away():
     u = (torch.arange(R) + 0.5) / R
     got = _many(row, R, u, T=T, p=p)
     assert torch.equal(got.long(), heavy[(u.double() * 257).long()])
+
+
+@pytest.mark.parametrize("dt,V", [(torch.float32, 79000), (torch.float32, 151936), (torch.bfloat16, 330007)])
+def test_sample_many_long_rows(dt, V):
+    """Rows of one CTA each whose blocks' largest values do not fit shared memory, every row with settings of its
+    own: lists of top-k, of min-p, of top-p of the whole row, and what no list holds."""
+    g = torch.Generator().manual_seed(V)
+    R = 232
+    pick = lambda vals: torch.tensor(vals)[torch.randint(0, len(vals), (R,), generator=g)]  # noqa: E731
+    x = peaked(g, R, V, dt)
+    sample_check(x, torch.rand(R, generator=g), T=pick([0.0, 0.3, 0.7, 0.7, 1.0]), k=pick([0, 0, 1, 20, 250, 1000]),
+                 p=pick([1.0, 0.95, 0.9, 0.5]), m=pick([0.0, 0.0, 0.02, 0.3]), shift=3, pad=1)
+    # settings shared among rows: fewer rows take one CTA each
+    R = 160
+    sample_check(x[:R], torch.rand(R, generator=g), T=0.8, k=40, p=0.9, group=R)
+    sample_check(x[:R], torch.rand(R, generator=g), T=0.6, p=0.9, m=0.001, group=R)
