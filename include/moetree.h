@@ -563,8 +563,9 @@ moe_status moe_block_norm(const moe_layer_desc *L, const void *x, const void *br
 
 /* Bytes of workspace of moe_few_forward for up to R tokens (1 .. 16); 0 for a bad descriptor.
  * Its first MOE_FEW_HEAD_BYTES must be zero before the first call that gets it (check word, grid
- * barrier, scores), and again after a call whose check word has bit 1; the rest is scratch. Two calls that overlap in time must use different workspaces, captured graphs
- * that may run at the same time too. */
+ * barrier, scores), and again after a call whose check word has bit 1; the rest is scratch. Two calls
+ * that overlap in time must use different workspaces, captured graphs that may run at the same time
+ * too. */
 #define MOE_FEW_HEAD_BYTES 36864
 size_t moe_few_workspace_bytes(const moe_layer_desc *L, int R);
 
@@ -575,7 +576,7 @@ size_t moe_few_workspace_bytes(const moe_layer_desc *L, int R);
  * with opts->norm_input on the pre-norm of x, with opts->residual added to x (see moe_run_opts).
  * R <= 16, else MOE_ERR_UNSUPPORTED (moe_tree_forward takes any number; its results differ by
  * roundings). Sums are fp32; bf16 layers keep the gated activations as a bf16 value and its bf16
- * rest (2^-17 relative). Tokens that do not fit a CTA's shared memory together (16 of them above
+ * rest (2^-17 relative), so a weight that is infinite gives NaN or an infinity. Tokens that do not fit a CTA's shared memory together (16 of them above
  * some 3900 bf16 or 2900 fp32 elements) take further launches.
  *   x, y [R, d] device, layer dtype; y may be x itself, and must not overlap it otherwise.
  *   W_r, W_gate, W_up, W_down, slot_of_expert as for moe_tree_forward.
@@ -648,7 +649,8 @@ moe_status moe_tree_accept(const int *token, const int *parent, const int *sampl
  * free. New pages are the free ones of the lowest numbers, in the order of the sequences (of a list's
  * entries), so results repeat. All arrays are device int32. Calls on one book are ordered on one
  * stream by the caller. A sequence whose numbers do not fit (held outside [0, max_pages], cache_len
- * outside [0, held * page_size]) is left as it is (moe_kv_compact moves what its entries hold).
+ * outside [0, held * page_size]) is left as it is (moe_kv_compact, which does not read cache_len, moves
+ * what its entries hold).
  * Limits: B <= 65536, n_pages <= 2^24, max_pages * page_size <= 2^30.
  * Check word of the workspace: bit 2 = a page outside the pool, or one given back that nobody held;
  * bit 3 = a sequence outside [0, B), one whose numbers do not fit, one that would need more than
@@ -671,19 +673,22 @@ size_t moe_pages_workspace_bytes(const moe_page_book *K);
 moe_status moe_kv_reserve(const moe_page_book *K, int N, const int *n_new, void *workspace,
                           moe_stream_t stream);
 
-/* Gives back pages of n listed sequences: keep[i] tokens of sequence seqs[i] stay (NULL: none; more
- * than it has: all), and the pages behind them that it holds are released; cache_len becomes at most
- * keep[i]. A sequence may be listed more than once (the smallest keep holds). seqs, keep [n]; keep may
- * be cache_len itself where entry i is sequence i, and is no other part of the book. */
+/* Gives back pages of n listed sequences: of sequence seqs[i] the first ceil(keep[i] / page_size) pages stay
+ * (NULL: none), as far as it holds them and also where its tokens need fewer, and those behind are
+ * released; cache_len becomes at most keep[i]. A sequence may be listed more than once (the smallest keep
+ * holds). seqs, keep [n]; keep may be cache_len itself where entry i is sequence i, and is no other part
+ * of the book. */
 moe_status moe_kv_free(const moe_page_book *K, const int *seqs, const int *keep, int n,
                        void *workspace, moe_stream_t stream);
 
 /* Forks sequences: dst[i] becomes a copy of src[i] as it is before the call. Pages full of src's
  * tokens are shared; the tokens behind them get a page of their own, and moves[i] = (src's page, the new
  * page, tokens to copy), or (-1, -1, 0) where there are none. Pages that src holds behind its tokens are
- * not shared. A target holds no pages (moe_kv_free), is listed once (else the first entry has it)
- * and is no entry's source; other entries are refused (bit 3), and one without a page for its last
- * tokens too (bit 4): their targets stay empty. src, dst [n], moves [n, 3]; n <= B. */
+ * not shared. An entry is refused (bit 3) where its target holds pages (moe_kv_free) or is the target
+ * of an entry before it, or where its source is the target of any entry; and one without a page for
+ * its last tokens too (bit 4). The targets of refused entries are left as they are. (Of
+ * (a, b) and (b, c) the first is carried out and the second refused.) src, dst [n], moves [n, 3];
+ * n <= B. */
 moe_status moe_kv_fork(const moe_page_book *K, const int *src, const int *dst, int n, int *moves,
                        void *workspace, moe_stream_t stream);
 

@@ -1,10 +1,11 @@
 """GPU tests of the decoding calls at values, sizes and paths where they can go wrong, against the same plain
 64-bit computations as test_gpu_decode.py (its tolerances hold here too)."""
+import numpy as np
 import pytest
 import torch
 
 from expert_select_gb300 import moetree as M
-from test_gpu_decode import Few, peaked, sample_check
+from test_gpu_decode import Book, Few, peaked, sample_check
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -188,3 +189,31 @@ def test_sample_many_long_rows(dt, V):
     R = 160
     sample_check(x[:R], torch.rand(R, generator=g), T=0.8, k=40, p=0.9, group=R)
     sample_check(x[:R], torch.rand(R, generator=g), T=0.6, p=0.9, m=0.001, group=R)
+
+
+# --------------------------------------------------------------------- pages
+
+@pytest.mark.parametrize("n", [2, 300])
+def test_fork_of_a_target(n):
+    """Of the entries (a, b), (b, c) the first is carried out and the second refused, in lists of both kinds."""
+    k = Book(3, 900, 4, 5000, 8, used=0.0)
+    k.reserve(np.array([11, 9] + [0] * 898, np.int32))
+    k.len[:2] = 11, 9
+    k.dev[2].copy_(torch.from_numpy(k.len))
+    dst = list(range(2, 2 + n))
+    k.fork([0, 2] + [0] * (n - 2), [2, 3] + dst[2:])
+    assert k.flags & 8
+    k.same()
+    assert k.held[2] > 0 and k.held[3] == 0
+
+
+def test_free_keeps_the_pages_of_keep():
+    """Pages of ceil(keep / page_size) stay although the tokens need fewer; those behind go."""
+    k = Book(4, 6, 12, 90, 16, used=0.0)
+    k.reserve(np.array([5, 100, 16, 17, 0, 190], np.int32))
+    k.len[:] = [5, 20, 16, 17, 0, 3]
+    k.dev[2].copy_(torch.from_numpy(k.len))
+    k.same()
+    k.free([0, 1, 2, 3, 4, 5], [16, 33, 1000, 16, 7, 32])
+    k.same()
+    assert k.held.tolist() == [1, 3, 1, 1, 0, 2] and k.len.tolist() == [5, 20, 16, 16, 0, 3]
