@@ -8,7 +8,7 @@
 // A token of thousands follows from comparisons of sums of up to V weights, so sums that depend on the
 // order of threads, or that are off by fp32's roundings, give another token every few thousand
 // rows. Weights are therefore integers of 2^-43 (exp2 from a difference, a product and a
-// polynomial carried as pairs of fp32 values; off by 1.4 units at most, checked against 64 bits),
+// polynomial carried as pairs of fp32 values; off by 1.3 units at most, checked against 64 bits),
 // and sums are 64-bit integers: exact, and the same in any order.
 //
 // A row belongs to a CTA, or, where rows are few, to a cluster of CTAs that hold it in shared memory;
@@ -323,7 +323,9 @@ __device__ __forceinline__ int bin_of(const Scale &sc, float l) {
     return min(kBins - 1, (int)(octaves(sc, l) * kBinScale));
 }
 
-// log of the share that a token of logit l has of the sum z.
+// log of the share that a token of logit l has of the sum z, in fp32: off by a few steps (measured over mixed rows:
+// 1.25 times the error of rounding the exact one). In fp64 one row's call took 13.4 -> 14.8 us and 16 trees of 65
+// 96 -> 101; with what each step loses carried along 13.4 -> 13.75 for 1.1 times that error.
 __device__ __noinline__ float log_share(float l, float top, float temp, u64 z) {
     const float lz = z < 2 * kOne ? log1pf((float)(long long)(z - kOne) * 0x1p-43f)
                                   : logf((float)z * 0x1p-43f);
@@ -1281,12 +1283,14 @@ template <typename T> cudaError_t launch(const Args &a, cudaStream_t s) {
     const int room = kHeldBytes / 16, sms = std::max(1, device_sms());
     // CTAs of a row, for rows long enough. Few rows take several; with more rows the cluster's barriers
     // cost more than what they save. Rows of bf16 151936, us by 1, 2, 4 and 8 CTAs a row: 16 rows with
-    // top-k 20: 16.2, 15.9, 14.3, 14.5; 65: 16.6, 16.2, 16.9, 29; 152: 16.5, 19.1, 42; 192: 22, 32, 46; 1040:
-    // 85, 132, 243. Rows that no list serves gain from more CTAs up to where all of them run at once: without
-    // cuts 16 rows 73, 45, 29, 27; 65: 74, 47, 45, 58; 152: 74, 74, 102; 192: 127, 106, 122; 304: 128, 138, 184;
-    // and rows of all kinds, where the slow ones are waited for, more: 152: 196, 130, 111; 192: 208, 131, 112.
-    // So with up to a row an SM two are taken, and up to one and a half where a list is not to be expected
-    // (neither top-k nor min-p is asked for) or each row has settings of its own.
+    // top-k 20: 16.2, 15.9, 14.3, 14.5; 65: 18.3, 18.3, 18.4; 152: 19.8, 21.6, 46; 192: 24, 38, 51; 1040: 85, 132, 243.
+    // Rows that no list serves gain from more CTAs up to where all of them run at once: without cuts 16 rows 73,
+    // 45, 29, 27; 65: 74, 47, 47, 58; 152: 76, 76, 103; 192: 128, 108, 123; 304: 132, 139, 180. In batches of all
+    // kinds they are waited for: 152: 194, 121, 95; 192: 195, 139, 111; 228: 292, 154, 132.
+    // So with up to a row an SM two are taken, and up to one and a half where no list is to be expected (neither
+    // top-k nor min-p is asked for) or a row's settings may be its own. What these are is on the device, so between one
+    // and one and a half rows an SM with param_rows 1 a batch whose rows all have a list pays 14 us (top-k 20: 24 to
+    // 38) for what a mixed one saves (40 to 137).
     const bool slow = a.group == 1 || (!a.top_k && !a.min_p);
     int ctas = a.R <= sms / 16 ? 8 : a.R <= sms / 2 ? 4 : a.R <= (slow ? 3 * sms / 2 : sms) ? 2 : 1;
     while (ctas > 1 && blocks / ctas < kThr) ctas /= 2;
