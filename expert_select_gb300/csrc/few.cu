@@ -15,12 +15,15 @@
 // rows, and add up in shared memory. bf16 weights go from global memory straight into the operands of
 // 16 x 8 x 16 products (the order of the inner index is free, so a lane's 16 bytes are two operands);
 // tokens are the 8 columns. The activations times their gates are kept as a bf16 value and the bf16
-// rest, which is fp32's accuracy to 2^-17. fp32 layers take fp32 products.
+// rest, which is fp32's accuracy to 2^-17. (With a third part, all 24 bits: one token 26.4 -> 27.0 us, 16 tokens
+// 142 -> 158, the wide experts below 123 -> 137, and 1.8 of a thousand outputs there round to another
+// bf16 neighbour than in 64 bits instead of 3.0; what is left are the tensor unit's fp32 sums.) fp32 layers take
+// fp32 products.
 //
-// Measured, calls in a row with other weights each: one token of the Qwen3-shaped layer 26.6 us (6 until
+// Measured, calls in a row with other weights each: one token of the Qwen3-shaped layer 26.5 us (6 until
 // the first weights are asked for, 3 between the last of step 2 and the first of step 3), 16 tokens
-// 148 (0.77 of the HBM's measured rate; CTAs end step 2 over 13 us), 4 tokens of d = f = 2880, 32
-// experts, top-4 124 (0.78), 3 tokens of an fp32 layer of d 520 14.5.
+// 134 to 146 by the experts they choose (0.8 of the HBM's measured rate; CTAs end step 2 over 13 us), 4 tokens of
+// d = f = 2880, 32 experts, top-4 114 to 134 (0.78), 3 tokens of an fp32 layer of d 520 15.
 #include <algorithm>
 
 #include "few.cuh"

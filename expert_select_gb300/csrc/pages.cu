@@ -8,9 +8,9 @@
 // one cluster of CTAs: each scans its slice, the slices' sums meet in distributed shared memory, and
 // the call's phases are cluster barriers instead of launches.
 //
-// Measured: the end, fork, growth and copies of 4 of 16 sequences 19 us (the host's: four calls of 3.5 to 5;
-// 12 replayed from a graph), of 128 of 512 sequences 21; compaction 12.6 at 1k pages (8.4 from a graph) and
-// 172 at 16k, of which the copies take 154, at the HBM's rate.
+// Measured: the end, fork, growth and copies of 4 of 16 sequences 19.4 to 21 us (the host's: four calls of 3.5 to
+// 5; 12 replayed from a graph), of 128 of 512 sequences 22.5; compaction 13 to 15 at 1k pages (8.4 from a graph)
+// and 173 at 16k, of which the copies take 154, at the HBM's rate.
 #include <cooperative_groups.h>
 
 #include <algorithm>

@@ -24,9 +24,9 @@
 // counts for top-k, weights for top-p; the bin that a cut falls in is divided by the bits of the
 // values until one value is left, and ties are taken in the order of the tokens.
 //
-// Measured for bf16 rows of 151936 with top-k 20 and top-p 0.9: one row 13.3 us (bound by the cluster's
+// Measured for bf16 rows of 151936 with top-k 20 and top-p 0.9: one row 13.4 us (bound by the cluster's
 // barriers), 1040 rows 85 (48 of it the HBM's; two CTAs an SM, and a row takes 8 to read and then 9 for its
-// list); 192 rows of fp32 50257, a third of them without top-k, 70 (bound by the instructions of
+// list); 192 rows of fp32 50257, a third of them without top-k, 75 to 80 (bound by the instructions of
 // exact weights, and by the slowest rows).
 #include <cooperative_groups.h>
 
@@ -324,7 +324,7 @@ __device__ __forceinline__ int bin_of(const Scale &sc, float l) {
 }
 
 // log of the share that a token of logit l has of the sum z, in fp32: off by a few steps (measured over mixed rows:
-// 1.25 times the error of rounding the exact one). In fp64 one row's call took 13.4 -> 14.8 us and 16 trees of 65
+// 1.25 to 2 times the error of rounding the exact one). In fp64 one row's call took 13.4 -> 14.8 us and 16 trees of 65
 // 96 -> 101; with what each step loses carried along 13.4 -> 13.75 for 1.1 times that error.
 __device__ __noinline__ float log_share(float l, float top, float temp, u64 z) {
     const float lz = z < 2 * kOne ? log1pf((float)(long long)(z - kOne) * 0x1p-43f)
